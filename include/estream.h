@@ -408,6 +408,131 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
                                                 const void* A, float* Y, float* logits_out,
                                                 void* cuda_stream);
 
+/* Largest T of a few-token layer call (one bit a token in an expert's mask). */
+#define ESTREAM_DECODE_MAX_T 32
+
+/*
+ * The layer for the few tokens of a generation step, in one launch: Eq. 2 as
+ * in estream_moe_layer_prefill, over the same resident arena. The prompt
+ * calls are built for hundreds of rows an expert; this one reads the weights
+ * of the experts that the T tokens chose once each, at HBM speed, with the
+ * routing, both projections and the sum over experts in one cooperative
+ * kernel (each token's contributions are added in a fixed order: Y does not
+ * depend on timing).
+ * X       device, [T][H] of the context's type (bf16; fp32 for ESTREAM_F32),
+ *         16-byte aligned.
+ * logits  device, [T][E] fp32.
+ * T, k    1 <= T <= min(T_max, ESTREAM_DECODE_MAX_T), 1 <= k <= min(k_max, E);
+ *         beyond: ESTREAM_ERR_CAPACITY.
+ * A       device, [T][H] in X's type, 16-byte aligned (A == X allowed): Y = A +
+ *         MoE(X), Y written; or NULL: Y += MoE(X).
+ * Y       device, [T][H] fp32, 16-byte aligned.
+ * Every group of the layer must be in the arena (estream_arena_preload, or an
+ * earlier call that loaded it with B*G >= E), else ESTREAM_ERR_CAPACITY.
+ * The h intermediate is kept in fp32 and split exactly for the tensor cores,
+ * so no activation overflows here and Y has fp32 accuracy; NaNs and infinities
+ * in a token's X reach that token's Y alone. A grid barrier that gives up (1 s)
+ * leaves Y as it was and is reported by estream_get_device_error. Nothing is
+ * synchronised; a call can be captured into a CUDA graph, whose replays the
+ * caller orders against calls that refill the arena.
+ */
+estream_status estream_moe_layer_decode(estream_ctx* c, int layer, const void* X,
+                                        const float* logits, int T, int k, int renorm,
+                                        const void* A, float* Y, void* cuda_stream);
+
+/*
+ * The same with the router in front (the whole layer from its input, still one
+ * launch): logits = X W_r^T in fp32 accumulation, then as above.
+ * W_r        device, [E][H] bf16, 16-byte aligned.
+ * logits_out device, [T][E] fp32, or NULL: receives the router logits.
+ * Contexts of type ESTREAM_F32 are refused (ESTREAM_ERR_INVALID_ARG).
+ */
+estream_status estream_moe_layer_decode_from_x(estream_ctx* c, int layer, const void* X,
+                                               const void* W_r, int T, int k, int renorm,
+                                               const void* A, float* Y, float* logits_out,
+                                               void* cuda_stream);
+
+/* ---------------------------------------------------------------------- */
+/* Microscaled 4-bit floating point                                        */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * Rows of E2M1 codes ({0, .5, 1, 1.5, 2, 3, 4, 6} and a sign) with a scale per
+ * block of consecutive values; a value is q * s * g with the block's s and the
+ * tensor's g. No counterpart in the paper, whose 4-bit experts are integers.
+ *   E4M3X16: 16 values share an E4M3 scale, s = e4m3(amax / (6 g)) (nearest,
+ *            ties to even, at most 448).
+ *   E8M0X32: 32 values share a power of two, s = 2^max(floor(log2(amax / g)) - 2,
+ *            -126) (E8M0).
+ * q is the E2M1 value nearest to fl(x / d), d = fl(s g), ties to the even code,
+ * at most 6; d = 0 gives zeros. The steps are single fp32 operations in this
+ * order, so the codes are reproducible bit for bit; with g a power of two they
+ * are those of exact arithmetic. A block that holds a NaN or an infinity reads
+ * back as NaN.
+ * A row of K values is padded with zeros to Kp = the next multiple of 32:
+ * codes [rows][Kp / 2] (two to a byte, the first in the low half; 16-byte
+ * aligned), scales [rows][Kp / 16 or Kp / 32] (one byte each). K and N are at
+ * most 2^24, g is positive and finite.
+ */
+enum { ESTREAM_MX4_E4M3X16 = 0, ESTREAM_MX4_E8M0X32 = 1 };
+/* Element types of the unquantised side. */
+enum { ESTREAM_MX4_BF16 = 0, ESTREAM_MX4_F16 = 1, ESTREAM_MX4_F32 = 2 };
+
+/* Bytes of `rows` quantised rows (codes, scales), and of a weight's scale
+ * tiles; 0 for invalid sizes. */
+size_t estream_mx4_code_bytes(long long rows, int K);
+size_t estream_mx4_scale_bytes(long long rows, int K, int fmt);
+size_t estream_mx4_weight_scale_bytes(int P, int N, int K);
+
+/*
+ * Quantise R rows.
+ * x        device, rows of `elem` values, ld elements apart, aligned to their
+ *          type; [n_src][K], or with swiglu [n_src][2 K]: gate then up, and the
+ *          value quantised is fl(fl(gate / fl(1 + exp(-gate))) * up) in fp32.
+ * rows     device, [R] int32, or NULL: output row i is source row rows[i] (a
+ *          route map's rec_tok gathers each record's token); an index outside
+ *          [0, n_src) gives a row of NaNs. NULL needs n_src >= R.
+ * codes, scales  device, estream_mx4_code_bytes(R, K) and
+ *          estream_mx4_scale_bytes(R, K, fmt) bytes out.
+ */
+estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n_src, int R, int K,
+                                    const int32_t* rows, int swiglu, int fmt, float scale,
+                                    void* codes, void* scales, void* cuda_stream);
+
+/* out[r][i] = fl(q * fl(s g)), rounded once to `elem` (exact in bf16 and fp32
+ * when g is a power of two); out rows are ld elements apart. */
+estream_status estream_mx4_dequantize(const void* codes, const void* scales, int fmt, float scale,
+                                      int R, int K, void* out, int elem, long long ld,
+                                      void* cuda_stream);
+
+/* Lay out the scales of a product's weights [P][N][K] once:
+ * scales [P][N][Kp / block] -> tiles [P][ceil(N / 128)][ceil(K / 64)][512]
+ * (estream_mx4_weight_scale_bytes, 128-byte aligned): row r of 128 and 16-value
+ * group j of 64 at byte (r % 32) * 16 + (r / 32) * 4 + j, zeros past the matrix;
+ * a 32-value scale fills both of its groups. The codes are used as they are. */
+estream_status estream_mx4_weight_scales(const void* scales, int P, int N, int K, int fmt,
+                                         void* tiles, void* cuda_stream);
+
+/*
+ * Product of quantised rows with quantised weights of the same format:
+ * out[r][n] = scale * sum over blocks of s_x s_w * sum of q_x q_w, where scale
+ * is the product of the two tensor scales. Sums in fp32, rounded once.
+ * x_codes, x_scales  device, R quantised rows of K.
+ * w_codes  device, P matrices of N quantised rows of K; w_tiles their scales as
+ *          laid out by estream_mx4_weight_scales.
+ * offsets  device, [P + 1] int32, or NULL (needs P == 1): row r of x meets the
+ *          weights of the slot p with offsets[p] <= r < offsets[p + 1] (a route
+ *          map's offsets: the records of each slot); rows before offsets[0] or
+ *          from offsets[P] on give zeros. Offsets are ascending and inside
+ *          [0, R]; others are clamped and leave unspecified values in out.
+ * out      device, [R][N] of ESTREAM_MX4_BF16 or ESTREAM_MX4_F32, rows ld
+ *          elements apart.
+ */
+estream_status estream_mx4_product(const void* x_codes, const void* x_scales, int R,
+                                   const void* w_codes, const void* w_tiles, int P, int N, int K,
+                                   int fmt, float scale, const int32_t* offsets, void* out,
+                                   int elem, long long ld, void* cuda_stream);
+
 /* Timings and counters accumulated since the last estream_reset_stats. The
  * per-kernel times are CUDA-event times on the launching stream, recorded
  * only while timing is on (estream_set_timing); reading them synchronises. */

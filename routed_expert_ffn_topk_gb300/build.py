@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libestream.so")
 SOURCES = ["route.cu", "route_static.cu", "expert_gemm.cu", "expert_f32.cu", "runtime.cu",
-           "pipeline_model.cu", "router.cu"]
+           "pipeline_model.cu", "router.cu", "decode.cu", "mx4.cu", "mx4_product.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

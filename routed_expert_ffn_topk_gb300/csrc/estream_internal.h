@@ -27,6 +27,9 @@ constexpr int kDevErrLaunch = 4;     // a cluster kernel launched without its cl
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Whether the library's kernels run on device `dev` (built for sm_103a alone).
+bool device_supported(int dev);
+
 // Layout of the route-build workspace (all offsets 256-byte aligned).
 struct RouteWorkspace {
     size_t err_off;      // int32 device error word
@@ -198,6 +201,75 @@ cudaError_t launch_router_logits(const void* X, int T, int H, const void* W_r, i
                                  const RouterPlan& p, int* dev_err, cudaStream_t stream);
 
 cudaError_t launch_cast_f32_bf16(const float* src, void* dst, size_t n, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// One MoE layer for a few tokens (generation steps)
+// ---------------------------------------------------------------------------
+
+constexpr int kDecodeMaxT = ESTREAM_DECODE_MAX_T;  // tokens of a call: one bit each in an expert's mask
+
+struct DecodeCall {
+    const void* X;         // [T][H] bf16 (fp32 for fp32 planes)
+    const float* logits;   // [T][E], or null: from W_r
+    const void* W_r;       // [E][H] bf16, or null
+    float* logits_out;     // [T][E] (with W_r)
+    const void* A;         // residual rows in X's type, or null: Y += ...
+    float* Y;              // [T][H]
+    int T, E, k, renorm, H, F, n_shared, F_shared;
+    const char *plane_g, *plane_u, *plane_d;  // arena planes; expert e sits in slot phi[e]
+    size_t S_gu, S_d;
+    const int32_t* phi;    // [E]
+    const float* scale;    // [E] by slot: 2^-s of the down weights
+    const char *sh_g, *sh_u, *sh_d;           // shared experts' planes
+    size_t S_sh;
+    const float* sh_scale;
+    float* h;              // [T k][F]: alpha * scale * SiLU(gate) * up of each (expert, token)
+    float* h_shared;       // [n_shared T][F_shared]
+    int* sync;             // two words, zero between launches
+    int* err;
+    int withhold;          // test: bit 0 / 1, CTA 0 does not arrive at the router's / the h barrier
+};
+cudaError_t launch_layer_decode(const DecodeCall& d, int wdtype, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Microscaled 4-bit floating point
+// ---------------------------------------------------------------------------
+
+// Values a row is padded to (with zeros): whole 32-value groups, which also
+// makes a row of codes a multiple of 16 bytes.
+__host__ __device__ constexpr int mx4_padded(int K) { return (K + 31) / 32 * 32; }
+__host__ __device__ constexpr int mx4_block(int fmt) { return fmt == ESTREAM_MX4_E4M3X16 ? 16 : 32; }
+
+struct Mx4Quantize {
+    const void* x;         // [n_src][ld] rows of `elem` (ESTREAM_MX4_BF16 / F16 / F32)
+    int elem;
+    long long ld;          // elements between rows
+    int n_src, R, K;
+    const int32_t* rows;   // [R] source row of each output row, or null
+    int swiglu;            // rows hold gate [K] then up [K]
+    int fmt;
+    float scale;
+    uint8_t *codes, *scales;
+};
+cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream);
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, float scale,
+                                  int R, int K, void* out, int elem, long long ld,
+                                  cudaStream_t stream);
+// Scales [P][N][Kp / block] to the product's tiles [P][ceil(N / 128)][ceil(K / 64)][512].
+cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int P, int N, int K, int fmt,
+                                     uint8_t* tiles, cudaStream_t stream);
+
+struct Mx4Product {
+    const uint8_t *xc, *xs;      // [R][Kp/2], [R][Kp/block]
+    const uint8_t *wc, *wt;      // [P][N][Kp/2], scale tiles
+    const int32_t* offsets;      // [P + 1], or null (P == 1: every row)
+    int R, P, N, K, fmt;
+    float scale;
+    void* out;
+    int elem;
+    long long ld;
+};
+cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t stream);
 
 // Tensor-map helper (driver entry point resolved at run time).
 CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base,

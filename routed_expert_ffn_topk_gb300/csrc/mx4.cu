@@ -1,0 +1,366 @@
+// Microscaled 4-bit floating point: rows to E2M1 codes with a scale per block,
+// back to values, and the layout of a weight's scales for the product
+// (mx4_product.cu).
+//
+// A value is q * s * g with q in {0, .5, 1, 1.5, 2, 3, 4, 6} and a sign (E2M1,
+// two codes to a byte, the first in the low half), s the scale of its block
+// and g the tensor's:
+//   ESTREAM_MX4_E4M3X16  16 values share an E4M3 s = e4m3(amax / (6 g));
+//   ESTREAM_MX4_E8M0X32  32 values share s = 2^max(floor(log2(amax / g)) - 2, -126)
+//                        (E8M0; the OCP microscaling rule, which lets the top
+//                        binade's upper quarter saturate at 6 s).
+// With d = fl(s g), q = E2M1 value nearest to fl(x / d), ties to the even code,
+// at most 6; d = 0 (an E4M3 block of zeros, or one whose s rounds to 0) gives
+// zeros. A block holding a NaN or an infinity gets a NaN scale and zero codes,
+// and reads back as NaN.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "estream_internal.h"
+
+namespace es {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int kElem>
+struct Elem;
+template <>
+struct Elem<ESTREAM_MX4_BF16> {
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float up(T v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ T down(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<ESTREAM_MX4_F16> {
+    using T = __half;
+    static __device__ __forceinline__ float up(T v) { return __half2float(v); }
+    static __device__ __forceinline__ T down(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elem<ESTREAM_MX4_F32> {
+    using T = float;
+    static __device__ __forceinline__ float up(T v) { return v; }
+    static __device__ __forceinline__ T down(float v) { return v; }
+};
+
+// Eight consecutive values from p (n of them inside the row, the rest zero);
+// wide loads when the row's values are 16-byte aligned.
+template <int kElem>
+__device__ __forceinline__ void load8(const typename Elem<kElem>::T* p, int n, bool wide, float (&v)[8]) {
+    using T = typename Elem<kElem>::T;
+    if (wide && n >= 8) {
+        alignas(16) T t[8];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = Elem<kElem>::up(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<kElem>::up(p[i]) : 0.0f;
+    }
+}
+
+// SiLU(g) * u in the written order g / (1 + exp(-g)) * u, each step rounded to
+// fp32 (no contraction).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
+}
+
+__device__ __forceinline__ float e4m3_value(uint8_t s) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3)));
+}
+__device__ __forceinline__ float e8m0_value(uint8_t s) {
+    return s == 0xff ? __int_as_float(0x7fc00000)
+                     : __uint_as_float(s == 0 ? 0x00400000u : static_cast<uint32_t>(s) << 23);
+}
+
+// Eight values a lane; two (16-value blocks) or four (32-value blocks)
+// neighbouring lanes form a block's maximum by shuffles. A row is a whole
+// number of 32-value groups, so a block never spans rows.
+template <int kElem, bool kSwiglu, int kFmt>
+__global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, int groups, bool wide) {
+    using T = typename Elem<kElem>::T;
+    constexpr int kLanes = kFmt == ESTREAM_MX4_E4M3X16 ? 2 : 4;
+    const size_t total = static_cast<size_t>(q.R) * groups;
+    const size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
+    // a warp's lanes past the end stay for the shuffles
+    const bool in = i < total;
+    const int row = in ? static_cast<int>(i / groups) : 0;
+    const int c = in ? static_cast<int>(i % groups) * 8 : 0;
+    const int src = in && q.rows ? q.rows[row] : row;
+    const bool have = in && src >= 0 && src < q.n_src;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = in && !have ? __int_as_float(0x7fc00000) : 0.0f;
+    if (have) {
+        const T* p = static_cast<const T*>(q.x) + static_cast<size_t>(src) * q.ld + c;
+        const int n = q.K - c;
+        if (n > 0) {
+            load8<kElem>(p, n, wide, v);
+            if (kSwiglu) {
+                float u[8];
+                load8<kElem>(p + q.K, n, wide, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = silu_mul(v[j], u[j]);
+            }
+        }
+    }
+    // largest magnitude, as bits: a NaN or infinity is at least 0x7f800000
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if (kLanes == 4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const bool finite = m < 0x7f800000u;
+    const float amax = __uint_as_float(m);
+    uint8_t s;
+    float d;
+    if (kFmt == ESTREAM_MX4_E4M3X16) {
+        s = finite ? __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.0f, q.scale)), __NV_SATFINITE, __NV_E4M3)
+                   : 0x7f;
+        d = __fmul_rn(e4m3_value(s), q.scale);
+    } else {
+        const uint32_t top = __float_as_uint(__fdiv_rn(amax, q.scale));
+        s = !finite ? 0xff : static_cast<uint8_t>(min(max(static_cast<int>(top >> 23) - 2, 1), 0xfe));
+        d = __fmul_rn(e8m0_value(s), q.scale);
+    }
+    uint32_t codes = 0;
+    if (finite && d > 0.0f) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float2 f = make_float2(__fdiv_rn(v[j], d), __fdiv_rn(v[j + 1], d));
+            codes |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (4 * j);
+        }
+    }
+    if (!in) return;
+    reinterpret_cast<uint32_t*>(q.codes)[i] = codes;
+    if ((threadIdx.x & (kLanes - 1)) == 0) q.scales[i / kLanes] = s;
+}
+
+template <int kElem, int kFmt>
+__global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const uint32_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, float g,
+                                                             int R, int K, int groups, void* out,
+                                                             long long ld, bool wide) {
+    using T = typename Elem<kElem>::T;
+    constexpr int kLanes = kFmt == ESTREAM_MX4_E4M3X16 ? 2 : 4;
+    const size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= static_cast<size_t>(R) * groups) return;
+    const int row = static_cast<int>(i / groups);
+    const int c = static_cast<int>(i % groups) * 8;
+    const uint32_t w = codes[i];
+    const uint8_t s = scales[i / kLanes];
+    const float d = __fmul_rn(kFmt == ESTREAM_MX4_E4M3X16 ? e4m3_value(s) : e8m0_value(s), g);
+    alignas(16) T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const __half2 h(__nv_cvt_fp4x2_to_halfraw2(static_cast<uint8_t>(w >> (4 * j)), __NV_E2M1));
+        v[j] = Elem<kElem>::down(__fmul_rn(__low2float(h), d));
+        v[j + 1] = Elem<kElem>::down(__fmul_rn(__high2float(h), d));
+    }
+    T* p = static_cast<T*>(out) + static_cast<size_t>(row) * ld + c;
+    if (wide && c + 8 <= K) {
+#pragma unroll
+        for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j)
+            reinterpret_cast<uint4*>(p)[j] = reinterpret_cast<const uint4*>(v)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < K) p[j] = v[j];
+    }
+}
+
+// One thread a tile byte: tile [n / 128][k / 64] holds, for row r of its 128
+// and 16-value group j of its 64, byte (r % 32) * 16 + (r / 32) * 4 + j; rows
+// and groups past the matrix are zero. A 32-value block's scale fills two.
+__global__ void __launch_bounds__(kThreads) k_mx4_weight_scales(const uint8_t* __restrict__ scales, int P,
+                                                                int N, int nb, int fmt, int nt, int kt,
+                                                                uint8_t* __restrict__ tiles) {
+    const size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= static_cast<size_t>(P) * nt * kt * 512) return;
+    const int in = static_cast<int>(i % 512);
+    const size_t tile = i / 512;
+    const int k = static_cast<int>(tile % kt);
+    const int n = static_cast<int>(tile / kt % nt) * 128 + in / 16 + in % 16 / 4 * 32;
+    const size_t p = tile / kt / nt;
+    const int b = fmt == ESTREAM_MX4_E4M3X16 ? k * 4 + in % 4 : (k * 4 + in % 4) / 2;
+    tiles[i] = n < N && b < nb ? scales[(p * N + n) * nb + b] : 0;
+}
+
+template <int kElem, bool kSwiglu>
+cudaError_t quantize_fmt(const Mx4Quantize& q, int groups, bool wide, unsigned grid, cudaStream_t s) {
+    if (q.fmt == ESTREAM_MX4_E4M3X16)
+        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(q, groups, wide);
+    else
+        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(q, groups, wide);
+    return cudaGetLastError();
+}
+template <int kElem>
+cudaError_t quantize_elem(const Mx4Quantize& q, int groups, bool wide, unsigned grid, cudaStream_t s) {
+    return q.swiglu ? quantize_fmt<kElem, true>(q, groups, wide, grid, s)
+                    : quantize_fmt<kElem, false>(q, groups, wide, grid, s);
+}
+template <int kElem>
+cudaError_t dequantize_elem(const uint8_t* codes, const uint8_t* scales, int fmt, float g, int R, int K,
+                            int groups, void* out, long long ld, bool wide, unsigned grid, cudaStream_t s) {
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
+    if (fmt == ESTREAM_MX4_E4M3X16)
+        k_mx4_dequantize<kElem, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, groups, out, ld, wide);
+    else
+        k_mx4_dequantize<kElem, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, groups, out, ld, wide);
+    return cudaGetLastError();
+}
+
+size_t elem_bytes(int elem) { return elem == ESTREAM_MX4_F32 ? 4 : 2; }
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+
+cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream) {
+    const int groups = mx4_padded(q.K) / 8;
+    const size_t total = static_cast<size_t>(q.R) * groups;
+    if (total == 0) return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>((total + kThreads - 1) / kThreads);
+    // 16-byte loads need every row (and the up half of it) on a 16-byte boundary
+    const size_t b = elem_bytes(q.elem);
+    const bool wide = on16(q.x) && q.ld * b % 16 == 0 && (!q.swiglu || q.K * b % 16 == 0);
+    if (q.elem == ESTREAM_MX4_BF16) return quantize_elem<ESTREAM_MX4_BF16>(q, groups, wide, grid, stream);
+    if (q.elem == ESTREAM_MX4_F16) return quantize_elem<ESTREAM_MX4_F16>(q, groups, wide, grid, stream);
+    return quantize_elem<ESTREAM_MX4_F32>(q, groups, wide, grid, stream);
+}
+
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, float scale,
+                                  int R, int K, void* out, int elem, long long ld,
+                                  cudaStream_t stream) {
+    const int groups = mx4_padded(K) / 8;
+    const size_t total = static_cast<size_t>(R) * groups;
+    if (total == 0) return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>((total + kThreads - 1) / kThreads);
+    const bool wide = on16(out) && ld * elem_bytes(elem) % 16 == 0;
+    if (elem == ESTREAM_MX4_BF16)
+        return dequantize_elem<ESTREAM_MX4_BF16>(codes, scales, fmt, scale, R, K, groups, out, ld, wide, grid, stream);
+    if (elem == ESTREAM_MX4_F16)
+        return dequantize_elem<ESTREAM_MX4_F16>(codes, scales, fmt, scale, R, K, groups, out, ld, wide, grid, stream);
+    return dequantize_elem<ESTREAM_MX4_F32>(codes, scales, fmt, scale, R, K, groups, out, ld, wide, grid, stream);
+}
+
+cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int P, int N, int K, int fmt,
+                                     uint8_t* tiles, cudaStream_t stream) {
+    const int nt = (N + 127) / 128, kt = (K + 63) / 64;
+    const size_t total = static_cast<size_t>(P) * nt * kt * 512;
+    if (total == 0) return cudaSuccess;
+    k_mx4_weight_scales<<<static_cast<unsigned>((total + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+        scales, P, N, mx4_padded(K) / mx4_block(fmt), fmt, nt, kt, tiles);
+    return cudaGetLastError();
+}
+
+}  // namespace es
+
+using namespace es;
+
+namespace {
+bool mx4_fmt_ok(int fmt) { return fmt == ESTREAM_MX4_E4M3X16 || fmt == ESTREAM_MX4_E8M0X32; }
+bool mx4_elem_ok(int e) { return e == ESTREAM_MX4_BF16 || e == ESTREAM_MX4_F16 || e == ESTREAM_MX4_F32; }
+bool mx4_scale_ok(float s) { return s > 0.0f && s <= 3.402823466e38f; }
+bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
+constexpr int kMaxWidth = 1 << 24;   // K and N: keeps a row's offsets in 32 bits
+
+// ESTREAM_OK when the current device runs this library's kernels.
+estream_status on_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    return device_supported(dev) ? ESTREAM_OK : ESTREAM_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+extern "C" {
+
+size_t estream_mx4_code_bytes(long long rows, int K) {
+    if (rows < 0 || K < 1 || K > kMaxWidth) return 0;
+    return static_cast<size_t>(rows) * (mx4_padded(K) / 2);
+}
+
+size_t estream_mx4_scale_bytes(long long rows, int K, int fmt) {
+    if (rows < 0 || K < 1 || K > kMaxWidth || !mx4_fmt_ok(fmt)) return 0;
+    return static_cast<size_t>(rows) * (mx4_padded(K) / mx4_block(fmt));
+}
+
+size_t estream_mx4_weight_scale_bytes(int P, int N, int K) {
+    if (P < 1 || N < 1 || K < 1 || K > kMaxWidth || N > kMaxWidth) return 0;
+    return static_cast<size_t>(P) * ((N + 127) / 128) * ((K + 63) / 64) * 512;
+}
+
+estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n_src, int R, int K,
+                                    const int32_t* rows, int swiglu, int fmt, float scale,
+                                    void* codes, void* scales, void* cuda_stream) {
+    if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || n_src < 0 || K < 1 ||
+        K > kMaxWidth || ld < (swiglu ? 2ll : 1ll) * K || (!rows && n_src < R))
+        return ESTREAM_ERR_INVALID_ARG;
+    if (R == 0) return ESTREAM_OK;
+    const size_t b = elem == ESTREAM_MX4_F32 ? 4 : 2;
+    if (!at(x, b) || !at(codes, 16) || !scales || (rows && !at(rows, 4))) return ESTREAM_ERR_INVALID_ARG;
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    const Mx4Quantize q{x, elem, ld, n_src, R, K, rows, swiglu != 0, fmt, scale,
+                        static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales)};
+    return launch_mx4_quantize(q, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? ESTREAM_OK
+                                                                                         : ESTREAM_ERR_CUDA;
+}
+
+estream_status estream_mx4_dequantize(const void* codes, const void* scales, int fmt, float scale, int R,
+                                      int K, void* out, int elem, long long ld, void* cuda_stream) {
+    if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || K < 1 || K > kMaxWidth ||
+        ld < K)
+        return ESTREAM_ERR_INVALID_ARG;
+    if (R == 0) return ESTREAM_OK;
+    if (!at(codes, 16) || !scales || !at(out, elem == ESTREAM_MX4_F32 ? 4 : 2)) return ESTREAM_ERR_INVALID_ARG;
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    return launch_mx4_dequantize(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), fmt,
+                                 scale, R, K, out, elem, ld, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+               ? ESTREAM_OK
+               : ESTREAM_ERR_CUDA;
+}
+
+estream_status estream_mx4_weight_scales(const void* scales, int P, int N, int K, int fmt, void* tiles,
+                                         void* cuda_stream) {
+    if (!mx4_fmt_ok(fmt) || estream_mx4_weight_scale_bytes(P, N, K) == 0 || P > kMaxP || !scales ||
+        !at(tiles, 128))
+        return ESTREAM_ERR_INVALID_ARG;
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    return launch_mx4_weight_scales(static_cast<const uint8_t*>(scales), P, N, K, fmt,
+                                    static_cast<uint8_t*>(tiles), static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+               ? ESTREAM_OK
+               : ESTREAM_ERR_CUDA;
+}
+
+estream_status estream_mx4_product(const void* x_codes, const void* x_scales, int R, const void* w_codes,
+                                   const void* w_tiles, int P, int N, int K, int fmt, float scale,
+                                   const int32_t* offsets, void* out, int elem, long long ld,
+                                   void* cuda_stream) {
+    if (!mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > (1 << 30) || P < 1 || P > kMaxP || N < 1 ||
+        N > kMaxWidth || K < 1 || K > kMaxWidth || (!offsets && P != 1) || ld < N ||
+        (elem != ESTREAM_MX4_BF16 && elem != ESTREAM_MX4_F32))
+        return ESTREAM_ERR_INVALID_ARG;
+    if (R == 0) return ESTREAM_OK;
+    if (!at(x_codes, 16) || !at(x_scales, 2) || !at(w_codes, 16) || !at(w_tiles, 128) ||
+        (offsets && !at(offsets, 4)) || !at(out, elem == ESTREAM_MX4_F32 ? 4 : 2))
+        return ESTREAM_ERR_INVALID_ARG;
+    if (static_cast<long long>(P) * N >= (1ll << 31)) return ESTREAM_ERR_CAPACITY;  // weight rows: 32-bit
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    const Mx4Product p{static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales),
+                       static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_tiles),
+                       offsets, R, P, N, K, fmt, scale, out, elem, ld};
+    return launch_mx4_product(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? ESTREAM_OK
+                                                                                        : ESTREAM_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -35,6 +35,17 @@
 
 #include "estream_internal.h"
 
+namespace es {
+bool device_supported(int dev) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+        return false;
+    if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return false;
+    return major == 10 && minor == 3;
+}
+}  // namespace es
+
 using namespace es;
 
 namespace {
@@ -170,6 +181,11 @@ struct estream_ctx {
     float* resid_Y = nullptr;
     int resid_T = 0;
     bool ffn_down_only_next = false;   // test: the next call runs the down tiles alone
+    // few-token calls (estream_moe_layer_decode)
+    float *dec_h = nullptr, *dec_hs = nullptr;  // fp32 h rows, routed and shared
+    int* dec_sync = nullptr;                    // [2] grid-barrier words, zero between launches
+    cudaEvent_t dec_done = nullptr;             // after the latest few-token call
+    bool dec_recorded = false;
 };
 
 namespace {
@@ -225,15 +241,6 @@ void trace_state(estream_ctx* c, int bank, int layer, int group, int state) {
     c->trace.push_back(layer);
     c->trace.push_back(group);
     c->trace.push_back(state);
-}
-
-bool device_supported(int dev) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return false;
-    if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return false;
-    return major == 10 && minor == 3;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -466,7 +473,7 @@ const char* estream_status_string(estream_status s) {
     return "unknown status";
 }
 
-int estream_version(void) { return 10200; }
+int estream_version(void) { return 10300; }
 
 size_t estream_route_workspace_bytes(int T, int E, int k, int P) {
     if (T < 0 || E < 1 || k < 1 || P < 0 || P > kMaxP) return 0;
@@ -724,6 +731,7 @@ estream_status estream_bind_arena(estream_ctx** out, const estream_arena_desc* d
         return o;
     };
     const size_t o_err = take(sizeof(int));
+    const size_t o_dsync = take(2 * sizeof(int));   // zeroed below with the error word
     const size_t o_perm = take(sizeof(int32_t) * c->perm.size());
     const size_t o_scale = take(sizeof(float) * c->perm.size());
     const size_t o_ids = take(sizeof(int32_t) * R_cap);
@@ -751,11 +759,17 @@ estream_status estream_bind_arena(estream_ctx** out, const estream_arena_desc* d
         o_out = take(static_cast<size_t>(R_cap) * d->H * sizeof(float));
         if (d->n_shared > 0) o_outs = take(static_cast<size_t>(RS_cap) * d->H * sizeof(float));
     }
+    const size_t T_dec = std::min(d->T_max, kDecodeMaxT);
+    const size_t o_dh = take(sizeof(float) * T_dec * d->k_max * d->F);
+    const size_t o_dhs = take(sizeof(float) * T_dec * d->n_shared * d->F_shared);
     c->ws_bytes = off;
     st = ESTREAM_ERR_CUDA;
     do {
         if (cudaMalloc(&c->ws, c->ws_bytes) != cudaSuccess) break;
         c->dev_err = reinterpret_cast<int*>(c->ws + o_err);
+        c->dec_sync = reinterpret_cast<int*>(c->ws + o_dsync);
+        c->dec_h = reinterpret_cast<float*>(c->ws + o_dh);
+        c->dec_hs = reinterpret_cast<float*>(c->ws + o_dhs);
         c->d_perm = reinterpret_cast<int32_t*>(c->ws + o_perm);
         c->d_scale = reinterpret_cast<float*>(c->ws + o_scale);
         c->topk_ids = reinterpret_cast<int32_t*>(c->ws + o_ids);
@@ -807,6 +821,7 @@ estream_status estream_bind_arena(estream_ctx** out, const estream_arena_desc* d
         c->copy_stream = c->copy_streams[0];
         if (cudaEventCreateWithFlags(&c->copy_done, cudaEventDisableTiming) != cudaSuccess) break;
         if (cudaEventCreateWithFlags(&c->preload_done, cudaEventDisableTiming) != cudaSuccess) break;
+        if (cudaEventCreateWithFlags(&c->dec_done, cudaEventDisableTiming) != cudaSuccess) break;
         c->banks.resize(d->B);
         bool ev_ok = true;
         for (auto& b : c->banks) {
@@ -905,6 +920,8 @@ estream_status fill_bank(estream_ctx* c, int layer, int q, int b, size_t* bytes,
     const size_t gbytes = static_cast<size_t>(n_q) * c->S_gu;
     const size_t dbytes = static_cast<size_t>(n_q) * c->S_d;
     Bank& bk = c->banks[b];
+    // a few-token call reads every bank: the refill waits for the latest one
+    if (c->dec_recorded && cudaStreamWaitEvent(cs, c->dec_done, 0) != cudaSuccess) return ESTREAM_ERR_CUDA;
     if (bk.release_pending) {
         if (cudaStreamWaitEvent(cs, bk.released, 0) != cudaSuccess) return ESTREAM_ERR_CUDA;
         bk.release_pending = false;
@@ -1409,6 +1426,95 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
     return prefill_impl(c, layer, X, nullptr, W_r, logits_out, T, k, renorm, A, Y, cuda_stream);
 }
 
+// The few-token layer call: `logits`, or (logits null) the router weights W_r.
+static estream_status decode_impl(estream_ctx* c, int layer, const void* X, const float* logits,
+                                  const void* W_r, float* logits_out, int T, int k, int renorm,
+                                  const void* A, float* Y, void* cuda_stream) {
+    if (!c) return ESTREAM_ERR_NOT_BOUND;
+    if (layer < 0 || layer >= c->d.L || !X || (!logits && !W_r) || !Y || T < 1 || k < 1 || k > c->d.E)
+        return ESTREAM_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(Y, 16) || (A && !aligned(A, 16)) || !aligned(logits, 4))
+        return ESTREAM_ERR_INVALID_ARG;
+    if (W_r && (c->d.wdtype == ESTREAM_F32 || !aligned(W_r, 16) || !aligned(logits_out, 4)))
+        return ESTREAM_ERR_INVALID_ARG;
+    if (!on_bound_device(c)) return ESTREAM_ERR_INVALID_ARG;
+    if (T > c->d.T_max || T > kDecodeMaxT || k > c->d.k_max) return ESTREAM_ERR_CAPACITY;
+    if (!layer_resident(c, layer)) return ESTREAM_ERR_CAPACITY;
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    c->trace.clear();
+    c->stats.calls += 1;
+    TimedScope total(c, s, kTTotal, layer);
+    if (c->preload_pending) {
+        if (cudaStreamWaitEvent(s, c->preload_done, 0) != cudaSuccess) return ESTREAM_ERR_CUDA;
+        c->preload_pending = false;
+    }
+    DecodeCall d{};
+    d.X = X;
+    d.logits = logits;
+    d.W_r = W_r;
+    d.logits_out = logits_out ? logits_out : c->logits_buf;
+    d.A = A;
+    d.Y = Y;
+    d.T = T;
+    d.E = c->d.E;
+    d.k = k;
+    d.renorm = renorm;
+    d.H = c->d.H;
+    d.F = c->d.F;
+    d.n_shared = c->d.n_shared;
+    d.F_shared = c->d.F_shared;
+    d.plane_g = c->plane_g;
+    d.plane_u = c->plane_u;
+    d.plane_d = c->plane_d;
+    d.S_gu = c->S_gu;
+    d.S_d = c->S_d;
+    d.phi = c->d_perm + static_cast<size_t>(layer) * c->d.E;
+    d.scale = c->d_scale + static_cast<size_t>(layer) * c->d.E;
+    if (c->d.n_shared > 0) {
+        d.S_sh = plane_slot_bytes(c->d.wdtype, c->d.F_shared, c->d.H);
+        d.sh_g = static_cast<const char*>(c->shared_dev[layer]);
+        d.sh_u = d.sh_g + c->d.n_shared * d.S_sh;
+        d.sh_d = d.sh_u + c->d.n_shared * d.S_sh;
+        d.sh_scale = c->shared_scale[layer];
+    }
+    d.h = c->dec_h;
+    d.h_shared = c->dec_hs;
+    d.sync = c->dec_sync;
+    d.err = c->dev_err;
+    // tests of the bounded barriers: one CTA does not arrive
+    d.withhold = (c->route_withhold_next && W_r ? 1 : 0) | (c->ffn_down_only_next ? 2 : 0);
+    c->route_withhold_next = c->ffn_down_only_next = false;
+    TimedScope ts(c, s, kTFfn, layer);
+    if (launch_layer_decode(d, c->d.wdtype, c->num_sms, s) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    ts.end();
+    c->stats.launches += 1;
+    c->stats.n_ffn += c->timing ? 1 : 0;
+    c->stats.groups_hit += c->n_groups;
+    // a captured call has no place in the order of later refills: its replays are the caller's to order
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    if (cap == cudaStreamCaptureStatusNone) {
+        if (cudaEventRecord(c->dec_done, s) != cudaSuccess) return ESTREAM_ERR_CUDA;
+        c->dec_recorded = true;
+    }
+    return ESTREAM_OK;
+}
+
+estream_status estream_moe_layer_decode(estream_ctx* c, int layer, const void* X, const float* logits,
+                                        int T, int k, int renorm, const void* A, float* Y,
+                                        void* cuda_stream) {
+    if (!logits) return c ? ESTREAM_ERR_INVALID_ARG : ESTREAM_ERR_NOT_BOUND;
+    return decode_impl(c, layer, X, logits, nullptr, nullptr, T, k, renorm, A, Y, cuda_stream);
+}
+
+estream_status estream_moe_layer_decode_from_x(estream_ctx* c, int layer, const void* X, const void* W_r,
+                                               int T, int k, int renorm, const void* A, float* Y,
+                                               float* logits_out, void* cuda_stream) {
+    if (!c) return ESTREAM_ERR_NOT_BOUND;
+    if (!W_r) return ESTREAM_ERR_INVALID_ARG;
+    return decode_impl(c, layer, X, nullptr, W_r, logits_out, T, k, renorm, A, Y, cuda_stream);
+}
+
 estream_status estream_set_timing(estream_ctx* c, int on) {
     if (!c) return ESTREAM_ERR_NOT_BOUND;
     c->timing = on != 0;
@@ -1467,6 +1573,10 @@ estream_status estream_poison_workspace(estream_ctx* c, void* cuda_stream) {
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     char* call = c->ws + c->ws_call_off;
     if (cudaMemsetAsync(call, 0xff, c->ws_bytes - c->ws_call_off, s) != cudaSuccess)
+        return ESTREAM_ERR_CUDA;
+    // the route build's error word holds an error only after a routing call wrote it (each clears it first)
+    if (cudaMemsetAsync(static_cast<char*>(c->route_ws) + route_workspace_layout(0, 1, 0).err_off, 0,
+                        sizeof(int), s) != cudaSuccess)
         return ESTREAM_ERR_CUDA;
     struct { int32_t* p; size_t n; } counters[3] = {
         {c->done, c->n_done}, {c->sh_done, c->n_sh_done}, {c->tickets, c->n_tickets}};
@@ -1568,6 +1678,7 @@ void estream_unbind(estream_ctx* c) {
     }
     if (c->copy_done) cudaEventDestroy(c->copy_done);
     if (c->preload_done) cudaEventDestroy(c->preload_done);
+    if (c->dec_done) cudaEventSynchronize(c->dec_done), cudaEventDestroy(c->dec_done);
     for (cudaStream_t cs : c->copy_streams)
         if (cs) cudaStreamDestroy(cs);
     if (c->h_offsets) cudaFreeHost(c->h_offsets);

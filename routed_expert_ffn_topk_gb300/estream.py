@@ -9,6 +9,7 @@ module refuses to load when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -22,6 +23,9 @@ F32, BF16, Q4 = 0, 1, 2
 SCHED_AFTER_ROUTING, SCHED_PREFETCH = 0, 1
 FFN_AUTO, FFN_SINGLE, FFN_PAIR = 0, 1, 2
 PAIR_MIN_ROWS = 160
+DECODE_MAX_T = 32
+FP4_E4M3X16, FP4_E8M0X32 = 0, 1
+_MX4_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 STATE_NAMES = {0: "Available", 1: "Filling", 2: "Ready", 3: "InUse"}
 
 
@@ -66,6 +70,7 @@ _lib = None
 
 # name -> (restype, argtypes)
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "estream_status_string": (ctypes.c_char_p, [_I]),
     "estream_version": (_I, []),
@@ -91,6 +96,15 @@ SIGNATURES = {
     "estream_arena_invalidate": (_I, [_P]),
     "estream_moe_layer_prefill": (_I, [_P, _I, _P, _P, _I, _I, _I, _P, _P]),
     "estream_moe_layer_prefill_residual": (_I, [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "estream_moe_layer_decode": (_I, [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "estream_moe_layer_decode_from_x": (_I, [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "estream_mx4_code_bytes": (_SZ, [_L, _I]),
+    "estream_mx4_scale_bytes": (_SZ, [_L, _I, _I]),
+    "estream_mx4_weight_scale_bytes": (_SZ, [_I, _I, _I]),
+    "estream_mx4_quantize": (_I, [_P, _I, _L, _I, _I, _I, _P, _I, _I, _F, _P, _P, _P]),
+    "estream_mx4_dequantize": (_I, [_P, _P, _I, _F, _I, _I, _P, _I, _L, _P]),
+    "estream_mx4_weight_scales": (_I, [_P, _I, _I, _I, _I, _P, _P]),
+    "estream_mx4_product": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _P, _I, _L, _P]),
     "estream_set_timing": (_I, [_P, _I]),
     "estream_reset_stats": (_I, [_P]),
     "estream_last_stats": (_I, [_P, ctypes.POINTER(Stats)]),
@@ -489,6 +503,200 @@ def moe_layer_prefill_from_x(ctx, layer: int, X: torch.Tensor, W_r: torch.Tensor
                                                       int(bool(renorm)), _dptr(A), _dptr(Y),
                                                       _dptr(logits_out), _stream(stream, X.device)),
                "estream_moe_layer_prefill_from_x")
+
+
+def moe_layer_decode(ctx, layer: int, X: torch.Tensor, logits: torch.Tensor, k: int, renorm: bool,
+                     Y: torch.Tensor, A: torch.Tensor | None = None, stream=None) -> None:
+    """The layer for at most DECODE_MAX_T tokens, in one launch: Y += MoE(X), or
+    Y = A + MoE(X). The layer must be resident in the arena."""
+    _check_layer_args(X, logits, Y, A)
+    T = X.shape[0]
+    with _on(X):
+        _check(lib().estream_moe_layer_decode(ctx, layer, _dptr(X), _dptr(logits), T, k,
+                                              int(bool(renorm)), _dptr(A), _dptr(Y),
+                                              _stream(stream, X.device)), "estream_moe_layer_decode")
+
+
+def moe_layer_decode_from_x(ctx, layer: int, X: torch.Tensor, W_r: torch.Tensor, k: int, renorm: bool,
+                            Y: torch.Tensor, A: torch.Tensor | None = None,
+                            logits_out: torch.Tensor | None = None, stream=None) -> None:
+    """moe_layer_decode with the router logits X W_r^T formed in the same launch."""
+    if W_r.dim() != 2 or W_r.dtype != torch.bfloat16 or W_r.shape[1] != X.shape[1] \
+            or W_r.device != X.device:
+        raise ValueError("W_r must be [E, H] bf16 on X's device")
+    T = X.shape[0]
+    if logits_out is not None and tuple(logits_out.shape) != (T, W_r.shape[0]):
+        raise ValueError(f"logits_out must be [{T}, {W_r.shape[0]}]")
+    _check_layer_args(X, logits_out, Y, A)
+    with _on(X):
+        _check(lib().estream_moe_layer_decode_from_x(ctx, layer, _dptr(X), _dptr(W_r), T, k,
+                                                     int(bool(renorm)), _dptr(A), _dptr(Y),
+                                                     _dptr(logits_out), _stream(stream, X.device)),
+               "estream_moe_layer_decode_from_x")
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit floating point
+# ---------------------------------------------------------------------------
+
+def mx4_padded(K: int) -> int:
+    """Values a quantised row of K is padded to."""
+    return -(-K // 32) * 32
+
+
+def mx4_block(fmt: int) -> int:
+    """Values that share a scale."""
+    if fmt not in (FP4_E4M3X16, FP4_E8M0X32):
+        raise ValueError(f"unknown 4-bit format {fmt}")
+    return 16 if fmt == FP4_E4M3X16 else 32
+
+
+def mx4_tensor_scale(amax: float, fmt: int) -> float:
+    """A tensor scale for data whose largest magnitude is amax: for E4M3 block
+    scales the power of two that puts the largest of them in (224, 448] (exact
+    to divide by, and every value exact in bf16), 1 for E8M0 ones."""
+    if mx4_block(fmt) == 32 or not amax > 0.0 or math.isinf(amax):
+        return 1.0
+    return 2.0 ** max(-100, min(100, math.ceil(math.log2(amax / (6.0 * 448.0)))))
+
+
+class Mx4:
+    """Quantised rows: codes [R, Kp/2] and scales [R, Kp/block] (uint8, contiguous,
+    on one CUDA device), the width K, the format and the tensor scale."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int, fmt: int, scale: float = 1.0):
+        Kp, b = mx4_padded(K), mx4_block(fmt)
+        if K < 1 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2:
+            raise ValueError("codes and scales must be 2-d uint8 tensors of K >= 1 values a row")
+        R = codes.shape[0]
+        if tuple(codes.shape) != (R, Kp // 2) or tuple(scales.shape) != (R, Kp // b):
+            raise ValueError(f"codes must be [R, {Kp // 2}] and scales [R, {Kp // b}] for K = {K}")
+        if not codes.is_cuda or scales.device != codes.device:
+            raise ValueError("codes and scales must be on one CUDA device")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        self.codes, self.scales, self.K, self.fmt, self.scale = codes, scales, K, fmt, float(scale)
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.K
+
+
+class Mx4Weights:
+    """Weights [P, N, K] of mx4_product: quantised codes [P, N, Kp/2] and the scale
+    tiles made by mx4_weights."""
+
+    def __init__(self, codes, tiles, K, fmt, scale):
+        self.codes, self.tiles, self.K, self.fmt, self.scale = codes, tiles, K, fmt, float(scale)
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.codes.shape[1], self.K
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a 2-d tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-d with contiguous rows")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return ld
+
+
+def mx4_quantize(x: torch.Tensor, fmt: int, scale: float = 1.0, rows: torch.Tensor | None = None,
+                 swiglu: bool = False, out: Mx4 | None = None, stream=None) -> Mx4:
+    """Rows of x [n, K] (bf16, fp16 or fp32; rows may be strided) to 4-bit codes
+    with a scale per block. rows [R] int32 gathers source rows (a route map's
+    rec_tok); swiglu takes x [n, 2K] as gate | up and quantises SiLU(gate) * up."""
+    if x.dtype not in _MX4_ELEM or not x.is_cuda:
+        raise ValueError("x must be a bf16, fp16 or fp32 CUDA tensor")
+    ld = _row_stride(x, "x")
+    if swiglu and x.shape[1] % 2:
+        raise ValueError("swiglu needs an even number of columns (gate | up)")
+    K = x.shape[1] // 2 if swiglu else x.shape[1]
+    b = mx4_block(fmt)
+    if K < 1:
+        raise ValueError("x must have at least one column")
+    dev = x.device
+    if rows is not None and (rows.dim() != 1 or rows.dtype != torch.int32 or rows.device != dev):
+        raise ValueError("rows must be a 1-d int32 tensor on x's device")
+    R = x.shape[0] if rows is None else rows.numel()
+    if out is None:
+        out = Mx4(torch.empty(R, mx4_padded(K) // 2, dtype=torch.uint8, device=dev),
+                  torch.empty(R, mx4_padded(K) // b, dtype=torch.uint8, device=dev), K, fmt, scale)
+    elif out.shape != (R, K) or out.fmt != fmt or out.codes.device != dev:
+        raise ValueError(f"out must hold {R} rows of {K} in this format on x's device")
+    out.scale = float(scale)
+    with _on(x):
+        _check(lib().estream_mx4_quantize(x.data_ptr(), _MX4_ELEM[x.dtype], ld, x.shape[0], R, K, _dptr(rows),
+                                          int(bool(swiglu)), fmt, out.scale, _dptr(out.codes),
+                                          _dptr(out.scales), _stream(stream, dev)), "estream_mx4_quantize")
+    return out
+
+
+def mx4_dequantize(q: Mx4, dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [R, K] that quantised rows stand for (bf16, fp16 or fp32)."""
+    R, K = q.shape
+    dev = q.codes.device
+    if out is None:
+        out = torch.empty(R, K, dtype=dtype, device=dev)
+    if out.dtype not in _MX4_ELEM or tuple(out.shape) != (R, K) or out.device != dev:
+        raise ValueError(f"out must be [{R}, {K}] bf16, fp16 or fp32 on the codes' device")
+    with _on(q.codes):
+        _check(lib().estream_mx4_dequantize(_dptr(q.codes), _dptr(q.scales), q.fmt, q.scale, R, K, out.data_ptr(),
+                                            _MX4_ELEM[out.dtype], _row_stride(out, "out"),
+                                            _stream(stream, dev)), "estream_mx4_dequantize")
+    return out
+
+
+def mx4_weights(codes: torch.Tensor, scales: torch.Tensor, K: int, fmt: int, scale: float = 1.0,
+                stream=None) -> Mx4Weights:
+    """Weights of mx4_product from quantised rows: codes [N, Kp/2] or [P, N, Kp/2]
+    with their scales (the codes are kept, the scales laid out once)."""
+    if codes.dim() == 2:
+        codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
+    Kp, b = mx4_padded(K), mx4_block(fmt)
+    if codes.dim() != 3 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or K < 1:
+        raise ValueError("codes and scales must be uint8 [P, N, ...]")
+    P, N = codes.shape[:2]
+    if P < 1 or N < 1 or tuple(codes.shape) != (P, N, Kp // 2) or tuple(scales.shape) != (P, N, Kp // b):
+        raise ValueError(f"codes must be [P, N, {Kp // 2}] and scales [P, N, {Kp // b}] for K = {K}")
+    if not codes.is_cuda or scales.device != codes.device:
+        raise ValueError("codes and scales must be on one CUDA device")
+    tiles = torch.empty(lib().estream_mx4_weight_scale_bytes(P, N, K), dtype=torch.uint8, device=codes.device)
+    with _on(codes):
+        _check(lib().estream_mx4_weight_scales(_dptr(scales), P, N, K, fmt, _dptr(tiles),
+                                               _stream(stream, codes.device)), "estream_mx4_weight_scales")
+    if not codes.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return Mx4Weights(codes, tiles, K, fmt, scale)
+
+
+def mx4_product(x: Mx4, w: Mx4Weights, offsets: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """x [R, K] times w [P, N, K] transposed, both quantised in one format:
+    [R, N] in bf16 or fp32. With offsets [P + 1] int32 (a route map's), rows
+    [offsets[p], offsets[p + 1]) meet w[p], and rows outside every slot are zero."""
+    R, K = x.shape
+    P, N, Kw = w.shape
+    dev = x.codes.device
+    if K != Kw or x.fmt != w.fmt or w.codes.device != dev:
+        raise ValueError("x and w must have one width and format, on one device")
+    if offsets is None and P != 1:
+        raise ValueError("weights of several slots need offsets")
+    if offsets is not None:
+        _need(offsets, P + 1, torch.int32, "offsets", dev)
+    if out is None:
+        out = torch.empty(R, N, dtype=out_dtype, device=dev)
+    if out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != (R, N) or out.device != dev:
+        raise ValueError(f"out must be [{R}, {N}] bf16 or fp32 on x's device")
+    with _on(x.codes):
+        _check(lib().estream_mx4_product(_dptr(x.codes), _dptr(x.scales), R, _dptr(w.codes), _dptr(w.tiles),
+                                         P, N, K, x.fmt, x.scale * w.scale, _dptr(offsets), out.data_ptr(),
+                                         _MX4_ELEM[out.dtype], _row_stride(out, "out"),
+                                         _stream(stream, dev)), "estream_mx4_product")
+    return out
 
 
 def set_timing(ctx, on: bool) -> None:

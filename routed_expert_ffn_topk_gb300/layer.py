@@ -131,6 +131,32 @@ class BoundLayerStack:
         es.moe_layer_prefill_from_x(self.ctx, layer, X, W_r, k, renorm, Y, A=residual,
                                     logits_out=logits_out, stream=stream)
 
+    def decode(self, layer: int, X: torch.Tensor, logits: torch.Tensor, Y: torch.Tensor, k=None,
+               renorm=None, stream=None, residual: torch.Tensor | None = None) -> None:
+        """prefill's layer for at most DECODE_MAX_T tokens, in one launch (the layer
+        must be resident): Y += MoE(X), or Y = residual + MoE(X)."""
+        self._check_decode(X)
+        if logits.dim() != 2 or logits.shape[1] != self.cfg.E:
+            raise ValueError(f"logits must be [T, {self.cfg.E}]")
+        es.moe_layer_decode(self.ctx, layer, X, logits, self.cfg.k if k is None else k,
+                            self.cfg.renorm if renorm is None else renorm, Y, A=residual, stream=stream)
+
+    def decode_from_x(self, layer: int, X: torch.Tensor, W_r: torch.Tensor, Y: torch.Tensor, k=None,
+                      renorm=None, stream=None, residual: torch.Tensor | None = None,
+                      logits_out: torch.Tensor | None = None) -> None:
+        """decode with the router logits X W_r^T formed in the same launch."""
+        self._check_decode(X)
+        if W_r.shape[0] != self.cfg.E:
+            raise ValueError(f"W_r must have {self.cfg.E} rows")
+        es.moe_layer_decode_from_x(self.ctx, layer, X, W_r, self.cfg.k if k is None else k,
+                                   self.cfg.renorm if renorm is None else renorm, Y, A=residual,
+                                   logits_out=logits_out, stream=stream)
+
+    def _check_decode(self, X: torch.Tensor) -> None:
+        want = torch.float32 if self.dtype == es.F32 else torch.bfloat16
+        if X.dim() != 2 or X.shape[1] != self.cfg.H or X.dtype != want or X.device != self.device:
+            raise ValueError(f"X must be [T, {self.cfg.H}] {want} on {self.device}")
+
     def close(self) -> None:
         if getattr(self, "ctx", None):
             with torch.cuda.device(self.device):
