@@ -223,8 +223,10 @@ struct DecodeCall {
     const char *sh_g, *sh_u, *sh_d;           // shared experts' planes
     size_t S_sh;
     const float* sh_scale;
-    float* h;              // [T k][F]: alpha * scale * SiLU(gate) * up of each (expert, token)
-    float* h_shared;       // [n_shared T][F_shared]
+    // alpha * scale * SiLU(gate) * up of each (expert, token), fp32 planes: [T k][F]
+    // floats; else [T k][3][F] bf16, the value's three leading 8-bit parts
+    void* h;
+    void* h_shared;        // [n_shared T] rows of F_shared
     int* sync;             // two words, zero between launches
     int* err;
     int withhold;          // test: bit 0 / 1, CTA 0 does not arrive at the router's / the h barrier

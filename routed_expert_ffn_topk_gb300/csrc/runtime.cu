@@ -182,7 +182,7 @@ struct estream_ctx {
     int resid_T = 0;
     bool ffn_down_only_next = false;   // test: the next call runs the down tiles alone
     // few-token calls (estream_moe_layer_decode)
-    float *dec_h = nullptr, *dec_hs = nullptr;  // fp32 h rows, routed and shared
+    void *dec_h = nullptr, *dec_hs = nullptr;  // h rows, routed and shared (see DecodeCall)
     int* dec_sync = nullptr;                    // [2] grid-barrier words, zero between launches
     cudaEvent_t dec_done = nullptr;             // after the latest few-token call
     bool dec_recorded = false;
@@ -760,16 +760,17 @@ estream_status estream_bind_arena(estream_ctx** out, const estream_arena_desc* d
         if (d->n_shared > 0) o_outs = take(static_cast<size_t>(RS_cap) * d->H * sizeof(float));
     }
     const size_t T_dec = std::min(d->T_max, kDecodeMaxT);
-    const size_t o_dh = take(sizeof(float) * T_dec * d->k_max * d->F);
-    const size_t o_dhs = take(sizeof(float) * T_dec * d->n_shared * d->F_shared);
+    const size_t dh_bytes = f32 ? 4 : 6;  // an fp32 value, or three bf16 parts of it
+    const size_t o_dh = take(dh_bytes * T_dec * d->k_max * d->F);
+    const size_t o_dhs = take(dh_bytes * T_dec * d->n_shared * d->F_shared);
     c->ws_bytes = off;
     st = ESTREAM_ERR_CUDA;
     do {
         if (cudaMalloc(&c->ws, c->ws_bytes) != cudaSuccess) break;
         c->dev_err = reinterpret_cast<int*>(c->ws + o_err);
         c->dec_sync = reinterpret_cast<int*>(c->ws + o_dsync);
-        c->dec_h = reinterpret_cast<float*>(c->ws + o_dh);
-        c->dec_hs = reinterpret_cast<float*>(c->ws + o_dhs);
+        c->dec_h = c->ws + o_dh;
+        c->dec_hs = c->ws + o_dhs;
         c->d_perm = reinterpret_cast<int32_t*>(c->ws + o_perm);
         c->d_scale = reinterpret_cast<float*>(c->ws + o_scale);
         c->topk_ids = reinterpret_cast<int32_t*>(c->ws + o_ids);
