@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "estream_internal.h"
 
@@ -27,12 +28,21 @@ namespace {
 namespace {
 
 constexpr uint64_t kDecodeWaitNs = 1000000000ull;  // 1 s: bound of a grid barrier
+constexpr uint32_t kSpins = 64;  // polls between two looks at the clock, whose read takes about a microsecond
 constexpr int kSimpleThreads = 512;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
+}
+
+// mbar_wait that polls for a while before it looks at the clock: a weight copy
+// is nearly always a short wait away.
+__device__ __forceinline__ bool copy_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    for (uint32_t i = 0; i < kSpins; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, abort_flag, err);
 }
 
 // Barrier of the whole (cooperative) grid, bounded in time: returns false
@@ -44,12 +54,14 @@ __device__ bool decode_barrier(int* sync, int generation, int* err, int* ok_flag
         __threadfence();
         if (!withhold) atomicAdd(sync, 1);
         const int target = generation * static_cast<int>(gridDim.x);
-        const uint64_t t0 = global_ns();
+        uint64_t t0 = 0;
         bool ok = true;
-        while (true) {
+        for (uint32_t spins = 1;; ++spins) {
             int seen;
             asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(sync) : "memory");
             if (seen >= target) break;
+            if (spins % kSpins != 0) continue;  // the clock is slow to read
+            if (t0 == 0) t0 = global_ns();
             if (global_ns() - t0 > kDecodeWaitNs) {
                 record_error(err, kDevErrTimeout);
                 ok = false;
@@ -76,95 +88,181 @@ __device__ __forceinline__ void decode_leave(int* sync) {
     }
 }
 
+// One chosen expert, or a shared one after them.
+struct Act {
+    uint32_t mask;  // bit t: token t goes to it
+    int row0;       // its first h row (one row a token, ascending t)
+    int slot;       // arena slot, or index among the shared experts
+    float scale;    // 2^-s of its down weights
+};
+
 // The call's routes in shared memory, formed by every CTA for itself.
 struct Routes {
-    int* ids;        // [T k] expert of each route
-    float* alpha;    // [T k]
-    int* counts;     // [E + 1]
-    uint32_t* mask;  // [E] bit t: token t goes to the expert
-    int* act;        // [n_act] experts with a token, ascending
-    int* row0;       // [n_act] first h row of the expert (one row a token, ascending t)
-    int* row_tok;    // [T k] token of each h row
-    float* row_alpha;  // [T k] its weight
+    Act* act;          // [E + n_shared] experts with a token, ascending, then the shared ones
+    Act* expert;       // [E] every expert's entry
+    float* row_alpha;  // [T k] weight of each h row
+    int* row_tok;      // [T k] its token
+    int* ids;          // [T k] expert of each route; then, a token's h rows in ascending order
+    float* alpha;      // [T k] weight of each route
+    uint32_t* key;     // [T E] logits as ordered keys (E <= kKeysE)
+    int* counts;       // [E + 1] (E > kKeysE)
     int* n_act;
 };
 
-__host__ __device__ inline size_t routes_bytes(int R, int E) {
-    return (sizeof(int) * (4 * static_cast<size_t>(R) + 4 * static_cast<size_t>(E) + 2) + 15) / 16 * 16;
+constexpr int kKeysE = 128;
+
+__host__ __device__ inline size_t routes_bytes(int T, int k, int E, int n_shared) {
+    const size_t R = static_cast<size_t>(T) * k;
+    return (sizeof(Act) * (2 * static_cast<size_t>(E) + n_shared) +
+            sizeof(int) * (4 * R + (E <= kKeysE ? static_cast<size_t>(T) * E : static_cast<size_t>(E) + 1) + 1) + 15) /
+           16 * 16;
 }
 
-__device__ Routes routes_at(void* smem, int R, int E) {
+__device__ Routes routes_at(void* smem, int T, int k, int E, int n_shared) {
+    const int R = T * k;
     Routes r;
-    r.ids = static_cast<int*>(smem);
+    r.act = static_cast<Act*>(smem);
+    r.expert = r.act + E + n_shared;
+    r.row_alpha = reinterpret_cast<float*>(r.expert + E);
+    r.row_tok = reinterpret_cast<int*>(r.row_alpha + R);
+    r.ids = r.row_tok + R;
     r.alpha = reinterpret_cast<float*>(r.ids + R);
-    r.counts = r.ids + 2 * R;
-    r.mask = reinterpret_cast<uint32_t*>(r.counts + E + 1);
-    r.act = reinterpret_cast<int*>(r.mask + E);
-    r.row0 = r.act + E;
-    r.row_tok = r.row0 + E;
-    r.row_alpha = reinterpret_cast<float*>(r.row_tok + R);
-    r.n_act = r.row_tok + 2 * R;
+    r.n_act = reinterpret_cast<int*>(r.alpha + R);
+    r.key = reinterpret_cast<uint32_t*>(r.n_act + 1);
+    r.counts = r.n_act + 1;
     return r;
 }
 
-// Top-k of every token (a warp per token), then the experts' token masks and
-// the list of experts in use. T <= 32 is what lets one word hold a mask, and
-// a token's row among its expert's rows be a count of the lower bits.
-__device__ void build_routes(const Routes& r, const float* logits, int T, int E, int k, int renorm,
-                             int* err) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        r.counts[e] = 0;
-        r.mask[e] = 0u;
+__device__ __forceinline__ uint32_t logit_key(float v) {
+    const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 -> +0
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// What does not depend on the routing: the experts' slots and scales, fetched
+// while the logits are on their way.
+__device__ void prepare_routes(const Routes& r, const DecodeCall& d) {
+    for (int e = threadIdx.x; e < d.E; e += blockDim.x) {
+        const int slot = d.phi[e];
+        r.expert[e] = {0u, 0, slot, d.scale[slot]};
+        if (d.E > kKeysE) r.counts[e] = 0;
     }
-    __syncthreads();
+    if (threadIdx.x == 0 && d.E > kKeysE) r.counts[d.E] = 0;
+}
+
+// Which experts each token takes: the experts' token masks, the list of experts
+// in use and, with T <= 32, a token's row among its expert's rows as a count of
+// the mask's lower bits. A warp a token; up to kKeysE experts its keys stay in
+// four registers a lane, a round being the largest key and the lowest expert
+// that holds it. The weights of that form are left to route_weights, off the path
+// to the first weight copy; more experts take the route build's own selection.
+__device__ void build_routes(const Routes& r, const DecodeCall& d, const float* logits) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const int T = d.T, E = d.E, k = d.k;
+    __syncthreads();  // prepare_routes
     for (int t = warp; t < T; t += nw) {
-        const float* l = logits + static_cast<size_t>(t) * E;
-        if (E <= 64)
-            topk_token<2>(t, l, E, k, renorm, nullptr, E, r.ids, r.alpha, r.counts, err);
-        else if (E <= 256)
-            topk_token<8>(t, l, E, k, renorm, nullptr, E, r.ids, r.alpha, r.counts, err);
-        else
-            topk_token<kMaxPerLane>(t, l, E, k, renorm, nullptr, E, r.ids, r.alpha, r.counts, err);
-        __syncwarp();
-        if (lane < k && r.ids[t * k + lane] >= 0) atomicOr(&r.mask[r.ids[t * k + lane]], 1u << t);
+        if (E <= kKeysE) {
+            uint32_t key[kKeysE / 32];
+#pragma unroll
+            for (int j = 0; j < kKeysE / 32; ++j) {
+                const int e = lane + 32 * j;
+                key[j] = e < E ? logit_key(__ldcg(logits + t * E + e)) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < kKeysE / 32; ++j)
+                if (lane + 32 * j < E) r.key[t * E + lane + 32 * j] = key[j];
+            for (int i = 0; i < k; ++i) {
+                uint32_t top = 0u, at = 0xffffffffu;
+#pragma unroll
+                for (int j = 0; j < kKeysE / 32; ++j)
+                    if (key[j] > top) {
+                        top = key[j];
+                        at = lane + 32 * j;
+                    }
+                const uint32_t m = __reduce_max_sync(0xffffffffu, top);
+                const uint32_t e = __reduce_min_sync(0xffffffffu, top == m ? at : 0xffffffffu);
+#pragma unroll
+                for (int j = 0; j < kKeysE / 32; ++j)
+                    if (static_cast<uint32_t>(lane + 32 * j) == e) key[j] = 0u;
+                if (lane == 0) {
+                    // (no key is left only where a row of NaNs has every bit set)
+                    r.ids[t * k + i] = static_cast<int>(e);
+                    if (e < static_cast<uint32_t>(E)) atomicOr(&r.expert[e].mask, 1u << t);
+                }
+            }
+        } else {
+            topk_token<kMaxPerLane>(t, logits + static_cast<size_t>(t) * E, E, k, d.renorm, nullptr, E, r.ids,
+                                    r.alpha, r.counts, d.err);
+            __syncwarp();
+            if (lane < k && r.ids[t * k + lane] >= 0) atomicOr(&r.expert[r.ids[t * k + lane]].mask, 1u << t);
+        }
     }
     __syncthreads();
     if (warp == 0) {
         int n = 0, rows = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            const int c = e < E ? __popc(r.mask[e]) : 0;
+            const uint32_t mask = e < E ? r.expert[e].mask : 0u;
+            const int c = __popc(mask);
             const unsigned has = __ballot_sync(0xffffffffu, c > 0);
             int incl = c;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += o;
+            for (int s = 1; s < 32; s <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, s);
+                if (lane >= s) incl += o;
             }
             if (c > 0) {
-                const int at = n + __popc(has & ((1u << lane) - 1u));
-                r.act[at] = e;
-                r.row0[at] = rows + incl - c;
+                r.expert[e].row0 = rows + incl - c;
+                r.act[n + __popc(has & ((1u << lane) - 1u))] = r.expert[e];
             }
             n += __popc(has);
             rows += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) *r.n_act = n;
+        for (int j = lane; j < d.n_shared; j += 32)
+            r.act[n + j] = {T == 32 ? 0xffffffffu : (1u << T) - 1u, j * T, j, d.sh_scale[j]};
     }
-    __syncthreads();
-    // each route's h row: its expert's first row and the earlier tokens there
-    // (counts, now free, holds the experts' first rows)
-    for (int a = threadIdx.x; a < *r.n_act; a += blockDim.x) r.counts[r.act[a]] = r.row0[a];
     __syncthreads();
     for (int i = threadIdx.x; i < T * k; i += blockDim.x) {
         const int e = r.ids[i], t = i / k;
-        if (e < 0) continue;
-        const int row = r.counts[e] + __popc(r.mask[e] & ((1u << t) - 1u));
-        r.row_tok[row] = t;
-        r.row_alpha[row] = r.alpha[i];
+        if (e >= 0) r.row_tok[r.expert[e].row0 + __popc(r.expert[e].mask & ((1u << t) - 1u))] = t;
     }
     __syncthreads();
+}
+
+// The routes' weights at their h rows, and each token's rows in ascending order
+// in place of its experts; by one warp, lane t for token t. Up to kKeysE experts
+// the softmax weights are formed here, by topk_token's operations in its order
+// (denominator summed in ascending expert order, one division a weight).
+__device__ void route_weights(const Routes& r, const DecodeCall& d) {
+    const int t = threadIdx.x & 31, E = d.E, k = d.k;
+    if (t >= d.T) return;
+    float* a = r.alpha + t * k;
+    int* id = r.ids + t * k;
+    if (E <= kKeysE && id[0] >= 0) {
+        const uint32_t* row = r.key + t * E;
+        const float m = key_logit(row[id[0]]);
+        float s = 0.0f;
+#pragma unroll 4
+        for (int e = 0; e < E; ++e) s = __fadd_rn(s, route_exp(__fsub_rn(key_logit(row[e]), m)));
+        for (int j = 0; j < k; ++j)
+            a[j] = id[j] < 0 ? 0.0f : __fdiv_rn(route_exp(__fsub_rn(key_logit(row[id[j]]), m)), s);
+        if (d.renorm) {
+            float z = 0.0f;  // summed in rank order
+            for (int j = 0; j < k; ++j) z = __fadd_rn(z, a[j]);
+            for (int j = 0; j < k; ++j) a[j] = __fdiv_rn(a[j], z);
+        }
+    }
+    for (int j = 0; j < k; ++j) {
+        const int e = id[j];
+        const int row = e < 0 ? -1 : r.expert[e].row0 + __popc(r.expert[e].mask & ((1u << t) - 1u));
+        if (e >= 0) r.row_alpha[row] = a[j];
+        int x = j;  // insertion by row
+        for (; x > 0 && id[x - 1] > row; --x) id[x] = id[x - 1];
+        id[x] = row;
+    }
 }
 
 template <int kType>
@@ -206,36 +304,37 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int gw = blockIdx.x * nw + warp, gn = gridDim.x * nw;
     const int H = d.H, F = d.F, Fs = d.F_shared, T = d.T, k = d.k;
-    const Routes r = routes_at(smem, T * k, d.E);
+    const Routes r = routes_at(smem, T, k, d.E, d.n_shared);
     int gen = 0;
     bool ok = true;
     {
-        build_routes(r, d.logits, T, d.E, k, d.renorm, d.err);
+        prepare_routes(r, d);
+        build_routes(r, d, d.logits);
+        if (warp == 0) route_weights(r, d);
+        __syncthreads();
         const int n_act = *r.n_act;
         const int routed = n_act * F;
         for (int u = gw; u < routed + d.n_shared * Fs; u += gn) {
             const bool sh = u >= routed;
-            const int a = sh ? (u - routed) / Fs : u / F;
+            const int at = sh ? n_act + (u - routed) / Fs : u / F;
             const int f = sh ? (u - routed) % Fs : u % F;
-            const int e = sh ? a : r.act[a];
-            const size_t slot = sh ? static_cast<size_t>(a) : static_cast<size_t>(d.phi[e]);
-            const char* pg = sh ? d.sh_g + slot * d.S_sh : d.plane_g + slot * d.S_gu;
-            const char* pu = sh ? d.sh_u + slot * d.S_sh : d.plane_u + slot * d.S_gu;
-            const float scale = sh ? d.sh_scale[slot] : d.scale[slot];
-            uint32_t m = sh ? (T == 32 ? 0xffffffffu : (1u << T) - 1u) : r.mask[e];
-            int row = sh ? a * T : r.row0[a];
-            for (; m; m &= m - 1, ++row) {
+            const Act a = r.act[at];
+            const size_t slot = static_cast<size_t>(a.slot);
+            const float* pg = reinterpret_cast<const float*>(sh ? d.sh_g + slot * d.S_sh : d.plane_g + slot * d.S_gu);
+            const float* pu = reinterpret_cast<const float*>(sh ? d.sh_u + slot * d.S_sh : d.plane_u + slot * d.S_gu);
+            int row = a.row0;
+            for (uint32_t m = a.mask; m; m &= m - 1, ++row) {
                 const int t = __ffs(m) - 1;
                 float g = 0.0f, up = 0.0f;
                 for (int c = lane; c < H; c += 32) {
                     const float x = x_at<ESTREAM_F32>(d.X, static_cast<size_t>(t) * H + c);
-                    g = fmaf(reinterpret_cast<const float*>(pg)[static_cast<size_t>(f) * H + c], x, g);
-                    up = fmaf(reinterpret_cast<const float*>(pu)[static_cast<size_t>(f) * H + c], x, up);
+                    g = fmaf(pg[static_cast<size_t>(f) * H + c], x, g);
+                    up = fmaf(pu[static_cast<size_t>(f) * H + c], x, up);
                 }
                 g = warp_sum(g);
                 up = warp_sum(up);
                 if (lane == 0) {
-                    const float v = scale * (g / (1.0f + expf(-g)) * up);
+                    const float v = a.scale * (g / (1.0f + expf(-g)) * up);
                     if (sh)
                         static_cast<float*>(d.h_shared)[static_cast<size_t>(row) * Fs + f] = v;
                     else
@@ -250,19 +349,18 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
         for (int o = gw; o < H; o += gn)
             for (int t = 0; t < T; ++t) {
                 float y = 0.0f;
-                for (int a = 0; a < n_act + d.n_shared; ++a) {
-                    const bool sh = a >= n_act;
-                    const int e = sh ? a - n_act : r.act[a];
-                    if (!sh && !((r.mask[e] >> t) & 1u)) continue;
-                    const size_t slot = sh ? static_cast<size_t>(e) : static_cast<size_t>(d.phi[e]);
-                    const char* pd = sh ? d.sh_d + slot * d.S_sh : d.plane_d + slot * d.S_d;
+                for (int at = 0; at < n_act + d.n_shared; ++at) {
+                    const Act a = r.act[at];
+                    if (!((a.mask >> t) & 1u)) continue;
+                    const bool sh = at >= n_act;
+                    const size_t slot = static_cast<size_t>(a.slot);
+                    const float* pd =
+                        reinterpret_cast<const float*>(sh ? d.sh_d + slot * d.S_sh : d.plane_d + slot * d.S_d);
                     const int n = sh ? Fs : F;
-                    const float* h =
-                        sh ? static_cast<const float*>(d.h_shared) + (static_cast<size_t>(e) * T + t) * Fs
-                           : static_cast<const float*>(d.h) +
-                                 static_cast<size_t>(r.row0[a] + __popc(r.mask[e] & ((1u << t) - 1u))) * F;
+                    const float* h = static_cast<const float*>(sh ? d.h_shared : d.h) +
+                                     static_cast<size_t>(a.row0 + __popc(a.mask & ((1u << t) - 1u))) * n;
                     for (int c = lane; c < n; c += 32)
-                        y = fmaf(reinterpret_cast<const float*>(pd)[static_cast<size_t>(o) * n + c], __ldcg(h + c), y);
+                        y = fmaf(pd[static_cast<size_t>(o) * n + c], __ldcg(h + c), y);
                 }
                 y = warp_sum(y);
                 if (lane == 0) {
@@ -275,20 +373,24 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
 }
 
 // ---------------------------------------------------------------------------
-// Streaming form (bf16 and 4-bit planes): one persistent CTA per SM, 16
-// consumer warps and one producer warp.
+// Streaming form (bf16 and 4-bit planes): one persistent CTA of 16 warps per SM.
 //
-// The grid splits the h rows of all chosen experts (then the rows of Y) into
-// one contiguous range a CTA, to a single row (4-bit: 8 and 4 rows, whose
-// scales fill 16 bytes), so every SM streams the same number of weight bytes.
-// The producer copies the range's rows, box by box as the arena stores them,
-// into a shared-memory ring with cp.async.bulk; it needs the routes but not h,
-// so it runs into the down weights while the consumers still wait at the grid
-// barrier between the projections, and HBM does not idle there.
+// The h rows of all chosen experts are split into one contiguous range for each
+// group of four warps (to a single row; 4-bit: 4, whose scales fill 16 bytes),
+// so every SM streams the same number of weight bytes. A unit is 64 (down: 128)
+// reduction values of a row tile; a group's warps take a tile's units in turn, each through
+// a shared-memory ring of its own that it fills with cp.async.bulk. A copy costs
+// its issuing thread about 100 ns and its warp about 30 ns, so one producer warp
+// with 1 KB copies would stop at 3.7 TB/s (measured); sixteen issuers reach 6.7.
+// Groups of four rather than the whole CTA on a tile: the work per tile that is
+// not per unit (pointers, the sum over warps and its barrier) is then paid for 8
+// units a warp instead of 2 (H = 2048), and no barrier stops all warps.
+// A warp's copies need the routes but not h, so they run into the down weights
+// while it still waits at the grid barrier between the projections, and HBM does
+// not idle there.
 //
-// A stage holds 16 units, one a consumer warp: 64 reduction values of a row
-// tile. The products are mma.sync m16n8k16 with the weights as the 16 rows and
-// the tokens as the 8 columns: at 8 columns an instruction covers 512 bytes of
+// The products are mma.sync m16n8k16 with the weights as the 16 rows and the
+// tokens as the 8 columns: at 8 columns an instruction covers 512 bytes of
 // weights, far above what HBM delivers, so a tcgen05 tile of at least 64 rows
 // by 8 columns through tensor memory would add latency and no speed. A tile of
 // h is 8 gate rows over 8 up rows, which puts gate and up of one h value in one
@@ -298,30 +400,42 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
 // h leaves as three bf16 parts (8 leading bits, the next 8, the next 8), which
 // together hold the fp32 value; the down weights, fp16 in the arena, are bf16
 // numbers times a power of two and convert to bf16 exactly. So every product of
-// both projections is exact and only fp32 sums round. In the down projection
-// column t is token t whatever the expert, so the accumulators run on over the
-// experts in ascending order and Y needs no atomics.
+// both projections is exact and only fp32 sums round.
+//
+// Down projection, up to 8 tokens (kNT = 1): column t is token t whatever the
+// expert, so a CTA's Y rows run through all experts in ascending order in one
+// accumulator, and Y needs no partial sums. With more tokens that would read
+// every token's h in every CTA (T = 32, OLMoE shape: 240 MB through L2, 210 us
+// of down projection against 47 us of streaming); there the CTAs split the
+// (expert, row) pairs as they do for h, leave a row of Y per route, and sum a
+// token's routes in ascending expert order after a second grid barrier.
 // ---------------------------------------------------------------------------
 
-constexpr int kConsumers = 16;
-constexpr int kStreamThreads = 32 * (kConsumers + 1);
+constexpr int kWarps = 16;
+constexpr int kGroup = 4;  // warps that share a tile
+constexpr int kGroups = kWarps / kGroup;
+constexpr int kStreamThreads = 32 * kWarps;
 constexpr int kMaxStages = 6;
 
-template <bool kQ4>
+// (4-bit rows are short, so a tile takes more of them where the accumulators
+// leave room)
+template <bool kQ4, int kNT>
 struct Stream {
-    static constexpr int kHRows = kQ4 ? 32 : 8;    // h rows of a gate/up tile
-    static constexpr int kYRows = kQ4 ? 32 : 16;   // Y rows of a down tile
-    static constexpr int kHStep = kQ4 ? 8 : 1;     // granularity of a CTA's range
-    static constexpr int kYStep = kQ4 ? 4 : 1;
+    static constexpr int kHRows = kQ4 && kNT == 1 ? 32 : 16;  // h rows of a gate/up tile
+    static constexpr int kYRows = kQ4 && kNT == 1 ? 32 : 16;  // Y rows of a down tile
+    static constexpr int kStep = kQ4 ? 4 : 1;      // granularity of a range
     static constexpr int kHTiles = kHRows / 8;     // m16 tiles (8 gate + 8 up rows)
     static constexpr int kYTiles = kYRows / 16;
-    // one plane's part of a unit: rows x 64 weights. 4-bit: two column blocks
-    // of 16 bytes a row, then 4 bytes of scales a row.
+    // one plane's rows x 64 weights. 4-bit: two column blocks of 16 bytes a row,
+    // then 4 bytes of scales a row.
     static constexpr int kRowBytes = kQ4 ? 36 : 128;
-    static constexpr int kHUnit = 2 * kHRows * kRowBytes;
-    static constexpr int kYUnit = kYRows * kRowBytes;
-    static constexpr int kStage = kConsumers * (kHUnit > kYUnit ? kHUnit : kYUnit);
-    static constexpr int kRed = kConsumers * (kHTiles > kYTiles ? kHTiles : kYTiles) * 128;  // floats
+    static constexpr int kHPart = kHRows * kRowBytes;  // a unit of h: gate, up
+    static constexpr int kYPart = kYRows * kRowBytes;  // a unit of Y: two k-blocks
+    static constexpr int kUnit = 2 * (kHPart > kYPart ? kHPart : kYPart);
+    // the warps' partial sums of a tile, twice: a tile's are written while the last one's are read
+    static constexpr int kTiles = kHTiles > kYTiles ? kHTiles : kYTiles;
+    static constexpr int kRedTile = kWarps * kTiles * 128;  // floats
+    static constexpr int kRed = 2 * kRedTile;
 };
 
 __device__ __forceinline__ void bulk_row_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -332,16 +446,14 @@ __device__ __forceinline__ void bulk_row_load(uint32_t dst, const void* src, uin
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
+template <typename T>
+__device__ __forceinline__ T as(const uint8_t* p) {
+    return *reinterpret_cast<const T*>(p);
 }
 // Two fp16 weights of the down plane as bf16 (exact: see above).
 __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t w) {
@@ -349,73 +461,90 @@ __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t w) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
-// Codes p (low half) and p + 1 (high half) of a 4-bit word as bf16 weights: the
-// code placed in 128 + q, then - 136 and * d, both exact (d has 5 bits).
-__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int p, __nv_bfloat162 d) {
-    const uint32_t u = ((word >> (4 * p)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 q = __hsub2_rn(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                        __floats2bfloat162_rn(136.0f, 136.0f));
-    const __nv_bfloat162 v = __hmul2_rn(q, d);
+// Codes 2 i (low half) and 2 i + 1 (high half) of a 4-bit word as bf16 weights
+// (q - 8) d: the code in bits 3-6 of bf16 16 makes 16 + q, and one fma with
+// -24 d gives the weight. Exact: d has 5 significant bits, so 24 d has 7 and
+// (q - 8) d at most 8.
+__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i, __nv_bfloat162 d, __nv_bfloat162 d24) {
+    const uint32_t at = i == 0 ? word << 3 : word >> (4 * i - 3);
+    const uint32_t u = (at & 0x00780078u) | 0x41804180u;
+    const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), d, d24);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// The scale of column block b (the low or high 16 bits) twice, and - 24 of it.
+__device__ __forceinline__ void q4_scale(uint32_t bits, int b, bool half, __nv_bfloat162& d, __nv_bfloat162& d24) {
+    uint32_t v = __byte_perm(bits, 0, b ? 0x3232 : 0x1010);
+    if (half) v = half2_to_bf162(v);
+    d = *reinterpret_cast<const __nv_bfloat162*>(&v);
+    d24 = __hmul2(d, __floats2bfloat162_rn(-24.0f, -24.0f));
+}
 
-// A run of rows of one expert's plane: rows [r, r + n) of slot-plane p.
-struct Rows {
-    int at;       // index among the chosen experts, then the shared ones
-    int row, n;
+// The tiles of a range of rows of the chosen experts (len rows each, `routed`
+// in all), then of the shared ones (len_sh each): up to kRows rows of one expert.
+template <int kRows>
+struct Walk {
+    int at;         // index among the chosen experts, then the shared ones
+    int row, n;     // the tile's rows [row, row + n) of that expert
+    int left;       // rows of the range from the tile's first on
+    int len, len_sh, n_act;
+    __device__ __forceinline__ void start(int pos, int end, int routed, int n_act_, int len_, int len_sh_) {
+        len = len_;
+        len_sh = len_sh_;
+        n_act = n_act_;
+        left = end - pos;
+        const bool sh = pos >= routed;
+        const int p = sh ? pos - routed : pos;
+        at = left > 0 ? p / (sh ? len_sh : len) : 0;
+        row = p - at * (sh ? len_sh : len);
+        if (sh) at += n_act;
+        size();
+    }
+    __device__ __forceinline__ bool shared() const { return at >= n_act; }
+    __device__ __forceinline__ void size() { n = min(min((shared() ? len_sh : len) - row, left), kRows); }
+    __device__ __forceinline__ void next() {
+        left -= n;
+        row += n;
+        if (row == (shared() ? len_sh : len)) {
+            row = 0;
+            ++at;
+        }
+        size();
+    }
 };
-
-// The tile of a CTA's h range that starts at `pos` (rows of the chosen experts,
-// then of the shared ones): the rest of the expert, of the range, or of the
-// aligned tile, whichever ends first.
-template <int kRows>
-__device__ __forceinline__ Rows h_tile(int pos, int end, int routed, int n_act, int F, int Fs) {
-    Rows t;
-    const int base = pos < routed ? 0 : routed, len = pos < routed ? F : Fs;
-    t.at = (pos - base) / len;
-    t.row = (pos - base) % len;
-    t.n = min(min(len - t.row, end - pos), kRows - t.row % kRows);
-    if (pos >= routed) t.at += n_act;
-    return t;
-}
-// The tile of a CTA's Y range that starts at row o; a down box has 256 rows.
-template <int kRows>
-__device__ __forceinline__ int y_tile(int o, int end) {
-    return min(min(kRows, end - o), 256 - o % 256);
-}
-__device__ __forceinline__ int share(int total, int step, int part) {
+// First row of part `part` of `parts` of a range of `total` rows.
+__device__ __forceinline__ int share(int total, int step, int part, int parts) {
     const long long units = total / step;
-    return static_cast<int>(units * part / gridDim.x) * step;
+    return static_cast<int>(units * part / parts) * step;
 }
-
-// k-blocks of a stage of the gate/up pass: K split evenly into stages of at most 16
-__host__ __device__ __forceinline__ int h_chunks(int KB) { return (KB + kConsumers - 1) / kConsumers; }
 
 // kNT: token tiles of 8 that the accumulators have room for (T <= 8 kNT).
 template <bool kQ4, int kNT>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const DecodeCall d, int stages) {
-    using S = Stream<kQ4>;
+    using S = Stream<kQ4, kNT>;
+    constexpr bool kByToken = kNT == 1;  // down projection: columns are the call's tokens
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
+    __shared__ __align__(8) uint64_t bars[kWarps * kMaxStages + 1];  // the last: the routes' weights are there
     __shared__ int ok_flag;
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = d.H, F = d.F, Fs = d.F_shared, T = d.T, k = d.k;
     const int KB = H / 64, FB = F / 64, FsB = Fs / 64;
-    const uint32_t ring = smem_addr(smem_raw);
-    float* red = reinterpret_cast<float*>(smem_raw + static_cast<size_t>(stages) * S::kStage);
-    const Routes r = routes_at(red + S::kRed, T * k, d.E);
-    auto full = [&](int s) { return smem_addr(&bars[s]); };
-    auto empty = [&](int s) { return smem_addr(&bars[kMaxStages + s]); };
+    const uint8_t* ring_p = smem_raw + warp * stages * S::kUnit;
+    const uint32_t ring = smem_addr(ring_p);
+    float* red = reinterpret_cast<float*>(smem_raw + static_cast<size_t>(kWarps) * stages * S::kUnit);
+    const Routes r = routes_at(red + S::kRed, T, k, d.E, d.n_shared);
+    const uint32_t bar0 = smem_addr(&bars[warp * kMaxStages]);
+    const uint32_t weights_bar = smem_addr(&bars[kWarps * kMaxStages]);
     if (threadIdx.x == 0) {
         abort_word = 0;
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), kConsumers);
-        }
+        mbar_init(weights_bar, 1);
+    }
+    if (lane == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    prepare_routes(r, d);
     int gen = 0;
     bool ok = true;
     if (d.W_r) {
@@ -426,340 +555,475 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         decode_leave(d.sync);
         return;
     }
-    build_routes(r, d.W_r ? d.logits_out : d.logits, T, d.E, k, d.renorm, d.err);
+    build_routes(r, d, d.W_r ? d.logits_out : d.logits);
     const int n_act = *r.n_act;
-    const int routed = n_act * F, h_total = routed + d.n_shared * Fs;
-    const int h0 = share(h_total, S::kHStep, blockIdx.x), h1 = share(h_total, S::kHStep, blockIdx.x + 1);
-    const int y0 = share(H, S::kYStep, blockIdx.x), y1 = share(H, S::kYStep, blockIdx.x + 1);
-    const int chunks = h_chunks(KB), per = (KB + chunks - 1) / chunks;
-    const int YB = n_act * FB + d.n_shared * FsB;  // k-blocks of a Y row
+    const int routed_h = n_act * F, total_h = routed_h + d.n_shared * Fs;
+    const int wg = warp % kGroup, group = blockIdx.x * kGroups + warp / kGroup;
+    const int groups = gridDim.x * kGroups;
+    const int h0 = share(total_h, S::kStep, group, groups), h1 = share(total_h, S::kStep, group + 1, groups);
+    // Y rows: of Y itself, a range a CTA, or of every (expert, Y) pair, a range a group
+    const int routed_y = kByToken ? 0 : n_act * H;
+    const int total_y = kByToken ? H : routed_y + d.n_shared * H;
+    const int y_part = kByToken ? blockIdx.x : group, y_parts = kByToken ? gridDim.x : groups;
+    const int y0 = share(total_y, S::kStep, y_part, y_parts), y1 = share(total_y, S::kStep, y_part + 1, y_parts);
+    constexpr int kYWarps = kByToken ? kWarps : kGroup;  // warps that share a Y tile
+    const int wy = kByToken ? warp : wg;
+    const int YB = n_act * FB + d.n_shared * FsB;  // k-blocks of a Y row over all experts
+    // Tiles of Y: one expert's rows, or (kByToken, at = 0) Y's own rows.
+    auto start_y = [&](Walk<S::kYRows>& t) {
+        if (kByToken) {
+            t.at = 0;
+            t.row = y0;
+            t.left = y1 - y0;
+            t.n = min(S::kYRows, t.left);
+        } else {
+            t.start(y0, y1, routed_y, n_act, H, H);
+        }
+    };
+    auto next_y = [&](Walk<S::kYRows>& t) {
+        if (kByToken) {
+            t.row += t.n;
+            t.left -= t.n;
+            t.n = min(S::kYRows, t.left);
+        } else {
+            t.next();
+        }
+    };
 
-    if (warp == kConsumers) {
-        // ---- producer: the whole warp issues, a lane a copy ----
-        int s = 0;
-        uint32_t ph = 0;
-        int issued = 0;  // stages filled so far
-        bool live = true;
-        auto wait_empty = [&]() {
-            const bool w = mbar_wait(empty(s), ph ^ 1u, abort_flag, d.err);
-            return __all_sync(0xffffffffu, w);
-        };
-        auto next = [&]() {
-            ++issued;
-            if (++s == stages) {
-                s = 0;
-                ph ^= 1u;
+    // ---- the warp's copies, `stages` units ahead of its products ----
+    // Kept small: a unit's bookkeeping is the larger part of its instructions.
+    constexpr int kParts = kQ4 ? 3 : 1;  // copies of a plane's rows: codes, codes, scales
+    Walk<S::kHRows> ih;
+    Walk<S::kYRows> iy;
+    ih.start(h0, h1, routed_h, n_act, F, Fs);
+    start_y(iy);
+    int i_stage = 0, issued = 0;
+    int i_kb = 0, i_end = 0;   // next unit of the tile, units of the tile
+    int i_a = 0, i_akb = 0;    // kByToken: its expert and k-block there
+    bool i_down = false, i_fresh = true;  // in the down projection; the tile is yet to be entered
+    const char* i_src = nullptr;          // this lane's copy of that unit
+    uint32_t i_off = 0, i_bytes = 0, i_tx = 0;
+    size_t i_step = 0;
+    // this lane's copy of rows [row, row + n) of a box whose rows go to smem rows from `to` on
+    auto lane_rows = [&](int part, int box_rows, int smem_rows, int row, int to, int n, size_t& src_off) {
+        if (!kQ4) {
+            src_off = row * 128;
+            i_off = to * 128;
+            i_bytes = n * 128;
+        } else if (part < 2) {
+            src_off = part * (box_rows * 16) + row * 16;
+            i_off = part * (smem_rows * 16) + to * 16;
+            i_bytes = n * 16;
+        } else {
+            src_off = box_rows * 32 + row * 4;
+            i_off = smem_rows * 32 + to * 4;
+            i_bytes = n * 4;
+        }
+    };
+    auto down_src = [&](int at) {
+        const size_t slot = static_cast<size_t>(r.act[at].slot);
+        return at >= n_act ? d.sh_d + slot * d.S_sh : d.plane_d + slot * d.S_d;
+    };
+    size_t y_off = 0;  // kByToken: this lane's rows inside a k-block's box, and the box of its Y rows
+    int y_box = 0;
+    auto issue_next = [&]() {
+        while (i_kb >= i_end) {
+            if (!i_fresh) {
+                if (i_down) next_y(iy); else ih.next();
             }
-        };
-        for (int pos = h0; pos < h1 && live;) {
-            const Rows t = h_tile<S::kHRows>(pos, h1, routed, n_act, F, Fs);
-            pos += t.n;
-            const bool sh = t.at >= n_act;
-            const size_t slot = sh ? static_cast<size_t>(t.at - n_act) : static_cast<size_t>(d.phi[r.act[t.at]]);
-            const char* base = lane & 1 ? (sh ? d.sh_u + slot * d.S_sh : d.plane_u + slot * d.S_gu)
-                                        : (sh ? d.sh_g + slot * d.S_sh : d.plane_g + slot * d.S_gu);
-            base += static_cast<size_t>(t.row / 128) * KB * (128 * S::kRowBytes);
-            const int br = t.row % 128, tr = t.row % S::kHRows;
-            for (int c = 0; c < chunks && live; ++c) {
-                const int kb = c * per + (lane >> 1), nk = min(per, KB - c * per);
-                if (!(live = wait_empty())) break;
-                if (lane == 0) mbar_arrive_expect_tx(full(s), 2u * nk * t.n * S::kRowBytes);
-                __syncwarp();
-                if ((lane >> 1) < nk) {
-                    const uint32_t dst = ring + s * S::kStage + (lane >> 1) * S::kHUnit +
-                                         (lane & 1) * (S::kHRows * S::kRowBytes);
-                    const char* src = base + static_cast<size_t>(kb) * (128 * S::kRowBytes);
-                    if (kQ4) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            bulk_row_load(dst + j * (S::kHRows * 16) + tr * 16, src + j * 2048 + br * 16, t.n * 16,
-                                          full(s));
-                        bulk_row_load(dst + S::kHRows * 32 + tr * 4, src + 4096 + br * 4, t.n * 4, full(s));
-                    } else {
-                        bulk_row_load(dst + tr * 128, src + br * 128, t.n * 128, full(s));
-                    }
+            i_fresh = false;
+            if (!i_down && ih.left <= 0) {
+                i_down = true;
+                i_fresh = true;
+                i_kb = i_end = 0;
+                continue;
+            }
+            if (i_down && iy.left <= 0) {
+                i_kb = i_end = 0;
+                i_fresh = true;
+                return;
+            }
+            size_t off = 0;
+            // a lane a copy: the rows in the first box, then (over) those in the next one
+            if (!i_down) {
+                i_kb = wg;
+                const int here = min(ih.n, 128 - ih.row % 128);
+                const bool sh = ih.shared(), up = (lane / kParts) & 1, over = lane >= 2 * kParts;
+                const size_t slot = static_cast<size_t>(r.act[ih.at].slot);
+                lane_rows(lane % kParts, 128, S::kHRows, over ? 0 : ih.row % 128, over ? here : 0,
+                          over ? ih.n - here : here, off);
+                if (up) i_off += S::kHPart;
+                if (lane >= 4 * kParts) i_bytes = 0;
+                i_tx = 2u * ih.n * S::kRowBytes;
+                i_step = static_cast<size_t>(kGroup) * (128 * S::kRowBytes);
+                i_src = (sh ? (up ? d.sh_u : d.sh_g) + slot * d.S_sh : (up ? d.plane_u : d.plane_g) + slot * d.S_gu) +
+                        (static_cast<size_t>(ih.row / 128 + over) * KB + i_kb) * (128 * S::kRowBytes) + off;
+                i_end = KB;
+            } else {
+                i_kb = wy;
+                const int here = min(iy.n, 256 - iy.row % 256);
+                const bool second = (lane / kParts) & 1, over = lane >= 2 * kParts;
+                lane_rows(lane % kParts, 256, S::kYRows, over ? 0 : iy.row % 256, over ? here : 0,
+                          over ? iy.n - here : here, off);
+                if (second) {
+                    i_off += S::kYPart;
+                    off += 256 * S::kRowBytes;
                 }
-                next();
+                if (lane >= 4 * kParts) i_bytes = 0;
+                i_tx = 2u * iy.n * S::kRowBytes;
+                i_step = static_cast<size_t>(2 * kYWarps) * (256 * S::kRowBytes);
+                y_box = iy.row / 256 + over;
+                if (kByToken) {
+                    y_off = off;
+                    i_a = 0;
+                    i_akb = 2 * wy;
+                    i_end = YB / 2;
+                } else {
+                    const int len = iy.shared() ? FsB : FB;
+                    i_end = len / 2;
+                    i_src = down_src(iy.at) + (static_cast<size_t>(y_box) * len + 2 * i_kb) * (256 * S::kRowBytes) + off;
+                }
             }
         }
-        for (int o = y0; o < y1 && live;) {
-            const int n = y_tile<S::kYRows>(o, y1);
-            for (int q0 = 0; q0 < YB && live; q0 += kConsumers) {
-                const int nk = min(kConsumers, YB - q0);
-                if (!(live = wait_empty())) break;
-                if (lane == 0) mbar_arrive_expect_tx(full(s), 1u * nk * n * S::kRowBytes);
-                __syncwarp();
-                if (lane < nk) {
-                    const int q = q0 + lane;
-                    const bool sh = q >= n_act * FB;
-                    const int len = sh ? FsB : FB, p = sh ? q - n_act * FB : q;
-                    const int a = p / len, kb = p % len;
-                    const size_t slot = sh ? static_cast<size_t>(a) : static_cast<size_t>(d.phi[r.act[a]]);
-                    const char* src = (sh ? d.sh_d + slot * d.S_sh : d.plane_d + slot * d.S_d) +
-                                      (static_cast<size_t>(o / 256) * len + kb) * (256 * S::kRowBytes);
-                    const uint32_t dst = ring + s * S::kStage + lane * S::kYUnit;
-                    const int br = o % 256;
-                    if (kQ4) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            bulk_row_load(dst + j * (S::kYRows * 16), src + j * 4096 + br * 16, n * 16, full(s));
-                        bulk_row_load(dst + S::kYRows * 32, src + 8192 + br * 4, n * 4, full(s));
-                    } else {
-                        bulk_row_load(dst, src + br * 128, n * 128, full(s));
-                    }
-                }
-                next();
+        if (kByToken && i_down) {
+            for (int len = i_a >= n_act ? FsB : FB; i_akb >= len; len = i_a >= n_act ? FsB : FB) {
+                i_akb -= len;
+                ++i_a;
             }
-            o += n;
+            i_src = down_src(i_a) +
+                    (static_cast<size_t>(y_box) * (i_a >= n_act ? FsB : FB) + i_akb) * (256 * S::kRowBytes) + y_off;
+            i_akb += 2 * kYWarps;
         }
-        // after an abort the copies still in flight must land before the CTA ends
-        if (!live)
-            for (int i = max(0, issued - stages); i < issued; ++i)
-                mbar_wait_drain(full(i % stages), static_cast<uint32_t>(i / stages) & 1u);
-    } else {
-        // ---- consumers ----
-        const int g = lane >> 2, tq = lane & 3;
-        int s = 0;
-        uint32_t ph = 0;
-        bool live = true;
-        // A wait that gives up raises the abort flag, with which every other wait
-        // ends at once; the warp then passes the remaining stages without work,
-        // so that all consumers meet at every named barrier.
-        auto wait_full = [&]() {
-            live = __all_sync(0xffffffffu, live && mbar_wait(full(s), ph, abort_flag, d.err));
-            return live;
-        };
-        auto release = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty(s));
-            if (++s == stages) {
-                s = 0;
-                ph ^= 1u;
-            }
-        };
-        auto sync_consumers = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); };
-        // sum of the 16 warps' partial tiles, value i of m16 tile m
-        auto reduced = [&](int m, int i) {
-            float v = 0.0f;
+        const uint32_t bar = bar0 + 8 * i_stage;
+        if (lane == 0) mbar_arrive_expect_tx(bar, i_tx);
+        __syncwarp();
+        if (i_bytes) bulk_row_load(ring + i_stage * S::kUnit + i_off, i_src, i_bytes, bar);
+        i_src += i_step;
+        i_kb += i_down ? kYWarps : kGroup;
+        ++issued;
+        if (++i_stage == stages) i_stage = 0;
+    };
+    for (int s = 0; s < stages; ++s) issue_next();
+    if (warp == kWarps - 1) {
+        route_weights(r, d);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(weights_bar);
+    }
+
+    // ---- products ----
+    const int g = lane >> 2, tq = lane & 3;
+    int stage = 0, used = 0;
+    uint32_t ph = 0;
+    bool live = true;
+    // A wait that gives up raises the abort flag, with which every other wait
+    // ends at once; the warp then passes its remaining units without work, so
+    // that all warps meet at every barrier.
+    auto wait_full = [&]() {
+        live = __all_sync(0xffffffffu, live && used < issued && copy_wait(bar0 + 8 * stage, ph, abort_flag, d.err));
+        return live;
+    };
+    auto release = [&]() {
+        __syncwarp();
+        if (!live) return;
+        ++used;
+        if (++stage == stages) {
+            stage = 0;
+            ph ^= 1u;
+        }
+        issue_next();
+    };
+    // The partial tiles of the warps that share one meet in one of two buffers in
+    // turn: a warp can write to a buffer again only after the barrier of the other
+    // one, which every reader of this one has passed by then.
+    int turn = 0;
+    auto gather = [&](const float (&acc)[4], int m) {
+        *reinterpret_cast<float4*>(&red[turn * S::kRedTile + (warp * S::kTiles + m) * 128 + lane * 4]) =
+            make_float4(acc[0], acc[1], acc[2], acc[3]);
+    };
+    // sum over `n` warps from `w0` on, value i of m16 tile m
+    auto reduced = [&](int w0, auto n, int m, int i) {
+        float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) v += red[(w * S::kHTiles + m) * 128 + i];
-            return v;
-        };
-        for (int pos = h0; pos < h1;) {
-            const Rows t = h_tile<S::kHRows>(pos, h1, routed, n_act, F, Fs);
-            pos += t.n;
-            const bool sh = t.at >= n_act;
-            const int e = sh ? t.at - n_act : r.act[t.at];
-            const int cnt = sh ? T : __popc(r.mask[e]);
-            const int row0 = sh ? e * T : r.row0[t.at];
-            const int nt = (cnt + 7) / 8;
-            const __nv_bfloat16* xp[kNT];
+        for (int w = 0; w < decltype(n)::value; ++w) v += red[turn * S::kRedTile + ((w0 + w) * S::kTiles + m) * 128 + i];
+        return v;
+    };
+    auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / kGroup), "n"(32 * kGroup) : "memory"); };
+    const int tid_g = threadIdx.x % (32 * kGroup), w_g = warp / kGroup * kGroup;
+    Walk<S::kHRows> t;
+    t.start(h0, h1, routed_h, n_act, F, Fs);
+    for (; t.left > 0; t.next()) {
+        const bool sh = t.shared();
+        const Act act = r.act[t.at];
+        const int cnt = __popc(act.mask), row0 = act.row0;
+        const int nt = (cnt + 7) / 8;
+        // the lane's token of each column tile; columns past the last token repeat
+        // it, and what they sum is not read
+        const uint4* xp[kNT];
 #pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-                const int c = j * 8 + g;
-                xp[j] = c < cnt ? static_cast<const __nv_bfloat16*>(d.X) +
-                                      static_cast<size_t>(sh ? c : r.row_tok[row0 + c]) * H + tq * 8
-                                : nullptr;
-            }
-            float acc[S::kHTiles][kNT][4];
+        for (int j = 0; j < kNT; ++j) {
+            const int c = min(j * 8 + g, cnt - 1);
+            xp[j] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.X) +
+                                                   static_cast<size_t>(sh ? c : r.row_tok[row0 + c]) * H) + tq + wg * 8;
+        }
+        float acc[S::kHTiles][kNT][4];
 #pragma unroll
-            for (int m = 0; m < S::kHTiles; ++m)
+        for (int m = 0; m < S::kHTiles; ++m)
 #pragma unroll
-                for (int j = 0; j < kNT; ++j)
+            for (int j = 0; j < kNT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-            for (int c = 0; c < chunks; ++c) {
-                const int kb = c * per + warp;
-                const bool mine = warp < min(per, KB - c * per);
-                uint4 x[kNT][2];
+                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+        uint4 x[2], more[2];
+        x[0] = __ldg(xp[0]);
+        x[1] = __ldg(xp[0] + 4);
+        for (int kb = wg, at = 0; kb < KB; kb += kGroup, at += kGroup * 8) {
+            if (wait_full()) {
+                const uint8_t* u = ring_p + stage * S::kUnit;
 #pragma unroll
-                for (int j = 0; j < kNT; ++j)
+                for (int j = 0; j < kNT; ++j) {
+                    if (j >= nt) continue;
+                    // the next token tile's X, or the next unit's, is fetched ahead
+                    const uint4* np = xp[0] + (kb + kGroup < KB ? at + kGroup * 8 : at);
+                    if (j + 1 < kNT && j + 1 < nt) np = xp[(j + 1) % kNT] + at;
+                    more[0] = __ldg(np);
+                    more[1] = __ldg(np + 4);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        x[j][b] = mine && xp[j] ? __ldg(reinterpret_cast<const uint4*>(xp[j] + kb * 64 + b * 32))
-                                                : make_uint4(0, 0, 0, 0);
-                if (wait_full() && mine) {
-                    const uint32_t u = ring + s * S::kStage + warp * S::kHUnit;
-#pragma unroll
-                    for (int m = 0; m < S::kHTiles; ++m)
+                    for (int m = 0; m < S::kHTiles; ++m) {
+                        if (m > 0 && m * 8 >= t.n) continue;
+                        // a unit's sums join the running ones by rounded additions: the tensor
+                        // cores truncate, which over a long chain would bias the sum
+                        float part[2][4] = {};  // a chain for each column block
+                        uint32_t scg = 0, scu = 0;  // 4-bit: the rows' scales of both column blocks
+                        if (kQ4) {
+                            scg = as<uint32_t>(u + S::kHRows * 32 + (m * 8 + g) * 4);
+                            scu = as<uint32_t>(u + S::kHRows * 32 + (m * 8 + g) * 4 + S::kHPart);
+                        }
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             uint32_t wg[4], wu[4];
                             if (kQ4) {
-                                const uint32_t p = u + b * (S::kHRows * 16) + (m * 8 + g) * 16 + tq * 4;
-                                const uint32_t sc = u + S::kHRows * 32 + (m * 8 + g) * 4;
-                                constexpr uint32_t kUp = S::kHRows * S::kRowBytes;
-                                const uint32_t qg = ld_shared_u32(p), qu = ld_shared_u32(p + kUp);
-                                const uint32_t dg = ld_shared_u32(sc), du = ld_shared_u32(sc + kUp);
-                                const uint32_t sg = __byte_perm(dg, 0, b ? 0x3232 : 0x1010);
-                                const uint32_t su = __byte_perm(du, 0, b ? 0x3232 : 0x1010);
+                                const uint8_t* p = u + b * (S::kHRows * 16) + (m * 8 + g) * 16 + tq * 4;
+                                const uint32_t qg = as<uint32_t>(p), qu = as<uint32_t>(p + S::kHPart);
+                                __nv_bfloat162 sg, sg24, su, su24;
+                                q4_scale(scg, b, false, sg, sg24);
+                                q4_scale(scu, b, false, su, su24);
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    wg[i] = q4_pair(qg, i, *reinterpret_cast<const __nv_bfloat162*>(&sg));
-                                    wu[i] = q4_pair(qu, i, *reinterpret_cast<const __nv_bfloat162*>(&su));
+                                    wg[i] = q4_pair(qg, i, sg, sg24);
+                                    wu[i] = q4_pair(qu, i, su, su24);
                                 }
                             } else {
-                                const uint32_t p = u + (m * 8 + g) * 128 + b * 64 + tq * 16;
-                                const uint4 vg = ld_shared_v4(p), vu = ld_shared_v4(p + S::kHRows * 128);
+                                const uint8_t* p = u + (m * 8 + g) * 128 + b * 64 + tq * 16;
+                                const uint4 vg = as<uint4>(p), vu = as<uint4>(p + S::kHPart);
                                 wg[0] = vg.x, wg[1] = vg.y, wg[2] = vg.z, wg[3] = vg.w;
                                 wu[0] = vu.x, wu[1] = vu.y, wu[2] = vu.z, wu[3] = vu.w;
                             }
+                            mma_bf16(part[b], wg[0], wu[0], wg[1], wu[1], x[b].x, x[b].y);
+                            mma_bf16(part[b], wg[2], wu[2], wg[3], wu[3], x[b].z, x[b].w);
+                        }
 #pragma unroll
-                            for (int j = 0; j < kNT; ++j) {
-                                if (j >= nt) continue;
-                                mma_bf16(acc[m][j], wg[0], wu[0], wg[1], wu[1], x[j][b].x, x[j][b].y);
-                                mma_bf16(acc[m][j], wg[2], wu[2], wg[3], wu[3], x[j][b].z, x[j][b].w);
+                        for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][i] + part[1][i];
+                    }
+                    x[0] = more[0];
+                    x[1] = more[1];
+                }
+            }
+            release();
+        }
+        // the warps' partial sums, SwiGLU and the weights of the routes
+        const int len = sh ? Fs : F;
+        __nv_bfloat16* hp = static_cast<__nv_bfloat16*>(sh ? d.h_shared : d.h);
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+            if (j >= nt) continue;
+#pragma unroll
+            for (int m = 0; m < S::kHTiles; ++m) gather(acc[m][j], m);
+            sync_group();
+            copy_wait(weights_bar, 0, abort_flag, d.err);
+            // lane l's values 0, 1 are gate and 2, 3 up of columns 2 (l % 4), + 1
+            for (int i = tid_g; i < S::kHTiles * 64; i += 32 * kGroup) {
+                const int m = i >> 6, l = (i & 63) >> 1, hi = i & 1;
+                const int row = m * 8 + (l >> 2), f = t.row + row, c = j * 8 + (l & 3) * 2 + hi;
+                if (row >= t.n || c >= cnt) continue;
+                const std::integral_constant<int, kGroup> n{};
+                const float gate = reduced(w_g, n, m, l * 4 + hi), up = reduced(w_g, n, m, l * 4 + 2 + hi);
+                const float a = sh ? 1.0f : r.row_alpha[row0 + c];
+                const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
+                __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
+                const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
+                const float r1 = v - __bfloat162float(p0);
+                const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+                o[0] = p0;
+                o[len] = p1;
+                o[2 * len] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+            }
+            turn ^= 1;
+        }
+    }
+    // every h row of the call is written
+    turn = 0;
+    live = decode_barrier(d.sync, ++gen, d.err, &ok_flag,
+                          *abort_flag || ((d.withhold & 2) && blockIdx.x == 0));
+    Walk<S::kYRows> ty;
+    start_y(ty);
+    for (; live && ty.left > 0; next_y(ty)) {
+        const bool sh_t = !kByToken && ty.shared();
+        const int cnt = kByToken ? T : __popc(r.act[ty.at].mask);
+        const int row_t = kByToken ? 0 : r.act[ty.at].row0;
+        const int units = (kByToken ? YB : sh_t ? FsB : FB) / 2;
+        float acc[S::kYTiles][kNT][4];
+#pragma unroll
+        for (int m = 0; m < S::kYTiles; ++m)
+#pragma unroll
+            for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+        // Where the lane finds the h values of unit q for its column of token tile
+        // j: null for a token without the expert (kByToken); columns past the last
+        // token repeat it and are not read. l_len: 16-byte words of an h part.
+        int l_a = 0, l_kb = 2 * wy;  // kByToken: expert and k-block of the next unit
+        size_t l_len = (sh_t ? Fs : F) / 8;
+        auto h_at = [&](int q, int j) -> const uint4* {
+            if (!kByToken)
+                return static_cast<const uint4*>(sh_t ? d.h_shared : d.h) +
+                       static_cast<size_t>(row_t + min(j * 8 + g, cnt - 1)) * 3 * l_len + q * 16 + tq;
+            if (q >= units) return nullptr;
+            for (int n = l_a >= n_act ? FsB : FB; l_kb >= n; n = l_a >= n_act ? FsB : FB) {
+                l_kb -= n;
+                ++l_a;
+            }
+            const Act act = r.act[l_a];
+            const bool sh = l_a >= n_act;
+            l_len = (sh ? Fs : F) / 8;
+            const uint4* p = static_cast<const uint4*>(sh ? d.h_shared : d.h) +
+                             static_cast<size_t>(act.row0 + __popc(act.mask & ((1u << g) - 1u))) * 3 * l_len + l_kb * 8 + tq;
+            l_kb += 2 * kYWarps;
+            return (act.mask >> g) & 1u ? p : nullptr;
+        };
+        auto load_h = [&](const uint4* p, size_t len, uint4 (&x)[3][2]) {
+#pragma unroll
+            for (int q3 = 0; q3 < 3; ++q3)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) x[q3][b] = p ? __ldcg(p + q3 * len + b * 4) : make_uint4(0, 0, 0, 0);
+        };
+        uint4 xa[3][2], xb[3][2];  // h values of a unit's first and second k-block, loaded one ahead
+        const uint4* hp = wy < units ? h_at(wy, 0) : nullptr;
+        load_h(hp, l_len, xa);
+        for (int q = wy; q < units; q += kYWarps) {
+            const bool full = wait_full();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint4 (&x)[3][2] = half ? xb : xa;
+                if (half == 0) {
+                    load_h(hp ? hp + 8 : nullptr, l_len, xb);
+                } else {
+                    hp = q + kYWarps < units ? h_at(q + kYWarps, 0) : nullptr;
+                    load_h(hp, l_len, xa);
+                }
+                if (!full) continue;
+                const uint8_t* u = ring_p + stage * S::kUnit + half * S::kYPart;
+                uint32_t w[S::kYTiles][2][8];  // [.][column block][rows g, g + 8 alternating]
+#pragma unroll
+                for (int m = 0; m < S::kYTiles; ++m)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi) {
+                            const int row = m * 16 + hi * 8 + g;
+                            if (kQ4) {
+                                const uint32_t word = as<uint32_t>(u + b * (S::kYRows * 16) + row * 16 + tq * 4);
+                                __nv_bfloat162 sc, sc24;
+                                q4_scale(as<uint32_t>(u + S::kYRows * 32 + row * 4), b, true, sc, sc24);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[m][b][2 * i + hi] = q4_pair(word, i, sc, sc24);
+                            } else {
+                                const uint4 v = as<uint4>(u + row * 128 + b * 64 + tq * 16);
+                                w[m][b][hi] = half2_to_bf162(v.x);
+                                w[m][b][2 + hi] = half2_to_bf162(v.y);
+                                w[m][b][4 + hi] = half2_to_bf162(v.z);
+                                w[m][b][6 + hi] = half2_to_bf162(v.w);
                             }
                         }
-                }
-                release();
-            }
-            // the warps' partial sums, SwiGLU and the weights of the routes
-            const size_t slot = sh ? static_cast<size_t>(e) : static_cast<size_t>(d.phi[e]);
-            const float scale = sh ? d.sh_scale[slot] : d.scale[slot];
-            const int len = sh ? Fs : F;
-            __nv_bfloat16* hp = static_cast<__nv_bfloat16*>(sh ? d.h_shared : d.h);
 #pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-                if (j >= nt) continue;
-                sync_consumers();  // the previous sums have been read
+                for (int j = 0; j < kNT; ++j) {
+                    if (8 * j >= cnt) continue;
+                    if (j > 0) load_h(h_at(q, j) + half * 8, l_len, x);
+                    float part[2][S::kYTiles][4] = {};  // a chain for each column block
 #pragma unroll
-                for (int m = 0; m < S::kHTiles; ++m)
-                    *reinterpret_cast<float4*>(&red[(warp * S::kHTiles + m) * 128 + lane * 4]) =
-                        make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
-                sync_consumers();
-                // lane l's values 0, 1 are gate and 2, 3 up of columns 2 (l % 4), + 1
-                for (int i = threadIdx.x; i < S::kHTiles * 64; i += 32 * kConsumers) {
-                    const int m = i >> 6, l = (i & 63) >> 1, hi = i & 1;
-                    const int f = (t.row / S::kHRows) * S::kHRows + m * 8 + (l >> 2);
-                    const int c = j * 8 + (l & 3) * 2 + hi;
-                    if (f < t.row || f >= t.row + t.n || c >= cnt) continue;
-                    const float gate = reduced(m, l * 4 + hi), up = reduced(m, l * 4 + 2 + hi);
-                    const float a = sh ? 1.0f : r.row_alpha[row0 + c];
-                    const float v = a * scale * (gate / (1.0f + expf(-gate)) * up);
-                    __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
-                    const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
-                    const float r1 = v - __bfloat162float(p0);
-                    const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-                    o[0] = p0;
-                    o[len] = p1;
-                    o[2 * len] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
-                }
-            }
-        }
-        // every h row of the call is written: barrier over the consumers of the grid
-        {
-            sync_consumers();
-            if (threadIdx.x == 0) {
-                __threadfence();
-                if (!*abort_flag && !((d.withhold & 2) && blockIdx.x == 0)) atomicAdd(d.sync, 1);
-                const int target = (gen + 1) * static_cast<int>(gridDim.x);
-                const uint64_t t0 = global_ns();
-                int all = 1;
-                while (true) {
-                    int seen;
-                    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(d.sync) : "memory");
-                    if (seen >= target) break;
-                    if (*abort_flag || global_ns() - t0 > kDecodeWaitNs) {
-                        record_error(d.err, kDevErrTimeout);
-                        *abort_flag = 1;
-                        all = 0;
-                        break;
-                    }
-                }
-                __threadfence();
-                ok_flag = all;
-            }
-            sync_consumers();
-            live = ok_flag != 0;
-        }
-        for (int o = live ? y0 : y1; o < y1;) {
-            const int n = y_tile<S::kYRows>(o, y1);
-            float acc[S::kYTiles][kNT][4];
+                    for (int q3 = 0; q3 < 3; ++q3)
 #pragma unroll
-            for (int m = 0; m < S::kYTiles; ++m)
+                        for (int m = 0; m < S::kYTiles; ++m)
 #pragma unroll
-                for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-            for (int q0 = 0; q0 < YB; q0 += kConsumers) {
-                const int q = q0 + warp;
-                const bool mine = q < YB;
-                const bool sh = q >= n_act * FB;
-                const int len = sh ? FsB : FB, p = sh ? q - n_act * FB : q;
-                const int a = mine ? p / len : 0, kb = mine ? p % len : 0;
-                const uint32_t mask = !mine ? 0u
-                                      : sh  ? (T == 32 ? 0xffffffffu : (1u << T) - 1u)
-                                            : r.mask[r.act[a]];
-                const int row0 = !mine ? 0 : sh ? a * T : r.row0[a];
-                const __nv_bfloat16* hp = static_cast<const __nv_bfloat16*>(sh ? d.h_shared : d.h) + kb * 64 + tq * 8;
-                if (wait_full() && mine) {
-                    const uint32_t u = ring + s * S::kStage + warp * S::kYUnit;
-                    uint32_t w[S::kYTiles][2][8];  // [.][column block][rows g, g + 8 alternating]
+                            for (int b = 0; b < 2; ++b) {
+                                mma_bf16(part[b][m], w[m][b][0], w[m][b][1], w[m][b][2], w[m][b][3], x[q3][b].x, x[q3][b].y);
+                                mma_bf16(part[b][m], w[m][b][4], w[m][b][5], w[m][b][6], w[m][b][7], x[q3][b].z, x[q3][b].w);
+                            }
 #pragma unroll
                     for (int m = 0; m < S::kYTiles; ++m)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int row = m * 16 + half * 8 + g;
-                                if (kQ4) {
-                                    const uint32_t word = ld_shared_u32(u + b * (S::kYRows * 16) + row * 16 + tq * 4);
-                                    const uint32_t sc = ld_shared_u32(u + S::kYRows * 32 + row * 4);
-                                    const uint32_t s2 = half2_to_bf162(__byte_perm(sc, 0, b ? 0x3232 : 0x1010));
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        w[m][b][2 * i + half] =
-                                            q4_pair(word, i, *reinterpret_cast<const __nv_bfloat162*>(&s2));
-                                } else {
-                                    const uint4 v = ld_shared_v4(u + row * 128 + b * 64 + tq * 16);
-                                    w[m][b][half] = half2_to_bf162(v.x);
-                                    w[m][b][2 + half] = half2_to_bf162(v.y);
-                                    w[m][b][4 + half] = half2_to_bf162(v.z);
-                                    w[m][b][6 + half] = half2_to_bf162(v.w);
-                                }
-                            }
-#pragma unroll
-                    for (int j = 0; j < kNT; ++j) {
-                        if (((mask >> (8 * j)) & 0xffu) == 0u) continue;
-                        const int t = 8 * j + g;
-                        const bool has = (mask >> t) & 1u;
-                        const __nv_bfloat16* hr =
-                            hp + static_cast<size_t>(row0 + __popc(mask & ((1u << t) - 1u))) * 3 * (len * 64);
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const uint4 x = has ? __ldcg(reinterpret_cast<const uint4*>(hr + part * (len * 64) + b * 32))
-                                                    : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                                for (int m = 0; m < S::kYTiles; ++m) {
-                                    mma_bf16(acc[m][j], w[m][b][0], w[m][b][1], w[m][b][2], w[m][b][3], x.x, x.y);
-                                    mma_bf16(acc[m][j], w[m][b][4], w[m][b][5], w[m][b][6], w[m][b][7], x.z, x.w);
-                                }
-                            }
-                    }
-                }
-                release();
-            }
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-                if (8 * j >= T) continue;
-                sync_consumers();
-#pragma unroll
-                for (int m = 0; m < S::kYTiles; ++m)
-                    *reinterpret_cast<float4*>(&red[(warp * S::kHTiles + m) * 128 + lane * 4]) =
-                        make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
-                sync_consumers();
-                for (int i = threadIdx.x; i < S::kYTiles * 128; i += 32 * kConsumers) {
-                    const int m = i >> 7, l = (i & 127) >> 2, v = i & 3;
-                    const int row = m * 16 + (l >> 2) + (v >> 1) * 8, t = j * 8 + (l & 3) * 2 + (v & 1);
-                    if (row >= n || t >= T || *abort_flag) continue;
-                    const size_t at = static_cast<size_t>(t) * H + o + row;
-                    d.Y[at] = (d.A ? x_at<ESTREAM_BF16>(d.A, at) : d.Y[at]) + reduced(m, i & 127);
+                        for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][m][i] + part[1][m][i];
                 }
             }
-            o += n;
+            release();
+        }
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+            if (8 * j >= cnt) continue;
+#pragma unroll
+            for (int m = 0; m < S::kYTiles; ++m) gather(acc[m][j], m);
+            if (kByToken)
+                __syncthreads();
+            else
+                sync_group();
+            for (int i = kByToken ? threadIdx.x : tid_g; i < S::kYTiles * 128; i += 32 * kYWarps) {
+                const int m = i >> 7, l = (i & 127) >> 2, v = i & 3;
+                const int row = m * 16 + (l >> 2) + (v >> 1) * 8, c = j * 8 + (l & 3) * 2 + (v & 1);
+                if (row >= ty.n || c >= cnt || *abort_flag) continue;
+                const float y = reduced(kByToken ? 0 : w_g, std::integral_constant<int, kYWarps>{}, m, i & 127);
+                if (kByToken) {
+                    const size_t at = static_cast<size_t>(c) * H + ty.row + row;
+                    d.Y[at] = (d.A ? x_at<ESTREAM_BF16>(d.A, at) : d.Y[at]) + y;
+                } else {
+                    (sh_t ? d.y_shared : d.y_rows)[static_cast<size_t>(row_t + c) * H + ty.row + row] = y;
+                }
+            }
+            turn ^= 1;
+        }
+    }
+    if (!kByToken) {
+        if (live) live = decode_barrier(d.sync, ++gen, d.err, &ok_flag, *abort_flag != 0);
+        // Y[t] = A[t] (or Y[t]) + the token's routes in ascending expert order + the shared experts
+        const int n4 = T * (H / 4);
+        for (int i = blockIdx.x * kStreamThreads + threadIdx.x; live && i < n4; i += gridDim.x * kStreamThreads) {
+            const int t = i / (H / 4), c = (i - t * (H / 4)) * 4;
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            auto add = [&](const float* rows, size_t row) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(rows + row * H + c));
+                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+            };
+            for (int j = 0; j < k; ++j) {
+                const int row = r.ids[t * k + j];
+                if (row >= 0) add(d.y_rows, row);
+            }
+            for (int e = 0; e < d.n_shared; ++e) add(d.y_shared, static_cast<size_t>(e) * T + t);
+            const size_t at = static_cast<size_t>(t) * H + c;
+            float4* out = reinterpret_cast<float4*>(d.Y + at);
+            float4 a;
+            if (d.A) {
+                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(d.A) + at);
+                a = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                                __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+            } else {
+                a = *out;
+            }
+            *out = make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w);
+        }
+    }
+    // after an abort the copies still in flight must land before the CTA ends
+    for (; used < issued; ++used) {
+        mbar_wait_drain(bar0 + 8 * stage, ph);
+        if (++stage == stages) {
+            stage = 0;
+            ph ^= 1u;
         }
     }
     decode_leave(d.sync);
@@ -769,12 +1033,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
 
 template <bool kQ4, int kNT>
 static cudaError_t launch_stream(const DecodeCall& d, int num_sms, cudaStream_t stream) {
-    using S = Stream<kQ4>;
+    using S = Stream<kQ4, kNT>;
     // the ring takes what the sums and the routes leave of 227 KB (static part: 1 KB)
-    const size_t fixed = sizeof(float) * S::kRed + routes_bytes(d.T * d.k, d.E);
-    const int stages = static_cast<int>(std::min<size_t>(kMaxStages, (226 * 1024 - fixed) / S::kStage));
+    const size_t fixed = sizeof(float) * S::kRed + routes_bytes(d.T, d.k, d.E, d.n_shared);
+    const int stages = static_cast<int>(std::min<size_t>(kMaxStages, (226 * 1024 - fixed) / (kWarps * S::kUnit)));
     if (stages < 2) return cudaErrorInvalidConfiguration;
-    const size_t smem = static_cast<size_t>(stages) * S::kStage + fixed;
+    const size_t smem = static_cast<size_t>(stages) * kWarps * S::kUnit + fixed;
     const void* fn = reinterpret_cast<const void*>(k_layer_decode<kQ4, kNT>);
     cudaError_t rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
@@ -791,11 +1055,16 @@ cudaError_t launch_layer_decode(const DecodeCall& d, int wdtype, int num_sms, cu
         return few ? launch_stream<false, 1>(d, num_sms, stream) : launch_stream<false, 4>(d, num_sms, stream);
     if (wdtype == ESTREAM_Q4)
         return few ? launch_stream<true, 1>(d, num_sms, stream) : launch_stream<true, 4>(d, num_sms, stream);
-    const size_t smem = routes_bytes(d.T * d.k, d.E);
+    const size_t smem = routes_bytes(d.T, d.k, d.E, d.n_shared);
+    const void* fn = reinterpret_cast<const void*>(k_layer_decode_simple);
+    if (smem > 47 * 1024) {
+        const cudaError_t rc =
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (rc != cudaSuccess) return rc;
+    }
     DecodeCall call = d;
     void* args[] = {&call};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(k_layer_decode_simple), dim3(num_sms),
-                                       dim3(kSimpleThreads), args, smem, stream);
+    return cudaLaunchCooperativeKernel(fn, dim3(num_sms), dim3(kSimpleThreads), args, smem, stream);
 }
 
 }  // namespace es

@@ -227,6 +227,7 @@ struct DecodeCall {
     // floats; else [T k][3][F] bf16, the value's three leading 8-bit parts
     void* h;
     void* h_shared;        // [n_shared T] rows of F_shared
+    float *y_rows, *y_shared;  // [T k][H], [n_shared T][H]: Y's terms (T > 8)
     int* sync;             // two words, zero between launches
     int* err;
     int withhold;          // test: bit 0 / 1, CTA 0 does not arrive at the router's / the h barrier

@@ -183,6 +183,7 @@ struct estream_ctx {
     bool ffn_down_only_next = false;   // test: the next call runs the down tiles alone
     // few-token calls (estream_moe_layer_decode)
     void *dec_h = nullptr, *dec_hs = nullptr;  // h rows, routed and shared (see DecodeCall)
+    float *dec_y = nullptr, *dec_ys = nullptr; // Y's terms, routed and shared
     int* dec_sync = nullptr;                    // [2] grid-barrier words, zero between launches
     cudaEvent_t dec_done = nullptr;             // after the latest few-token call
     bool dec_recorded = false;
@@ -763,6 +764,8 @@ estream_status estream_bind_arena(estream_ctx** out, const estream_arena_desc* d
     const size_t dh_bytes = f32 ? 4 : 6;  // an fp32 value, or three bf16 parts of it
     const size_t o_dh = take(dh_bytes * T_dec * d->k_max * d->F);
     const size_t o_dhs = take(dh_bytes * T_dec * d->n_shared * d->F_shared);
+    const size_t o_dy = take(f32 ? 0 : sizeof(float) * T_dec * d->k_max * d->H);
+    const size_t o_dys = take(f32 ? 0 : sizeof(float) * T_dec * d->n_shared * d->H);
     c->ws_bytes = off;
     st = ESTREAM_ERR_CUDA;
     do {
@@ -771,6 +774,8 @@ estream_status estream_bind_arena(estream_ctx** out, const estream_arena_desc* d
         c->dec_sync = reinterpret_cast<int*>(c->ws + o_dsync);
         c->dec_h = c->ws + o_dh;
         c->dec_hs = c->ws + o_dhs;
+        c->dec_y = reinterpret_cast<float*>(c->ws + o_dy);
+        c->dec_ys = reinterpret_cast<float*>(c->ws + o_dys);
         c->d_perm = reinterpret_cast<int32_t*>(c->ws + o_perm);
         c->d_scale = reinterpret_cast<float*>(c->ws + o_scale);
         c->topk_ids = reinterpret_cast<int32_t*>(c->ws + o_ids);
@@ -1480,6 +1485,8 @@ static estream_status decode_impl(estream_ctx* c, int layer, const void* X, cons
     }
     d.h = c->dec_h;
     d.h_shared = c->dec_hs;
+    d.y_rows = c->dec_y;
+    d.y_shared = c->dec_ys;
     d.sync = c->dec_sync;
     d.err = c->dev_err;
     // tests of the bounded barriers: one CTA does not arrive
