@@ -533,6 +533,12 @@ estream_status estream_mx4_product(const void* x_codes, const void* x_scales, in
                                    int fmt, float scale, const int32_t* offsets, void* out,
                                    int elem, long long ld, void* cuda_stream);
 
+/* Synchronises `cuda_stream`, then returns and clears the first error that
+ * product kernels recorded on the current device: ESTREAM_OK, or
+ * ESTREAM_ERR_TIMEOUT when a bounded wait inside one ran out (its output is then
+ * incomplete). */
+estream_status estream_mx4_error(void* cuda_stream);
+
 /* Timings and counters accumulated since the last estream_reset_stats. The
  * per-kernel times are CUDA-event times on the launching stream, recorded
  * only while timing is on (estream_set_timing); reading them synchronises. */

@@ -273,6 +273,8 @@ struct Mx4Product {
     long long ld;
 };
 cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t stream);
+// Reads and clears the current device's product error word (kDevErr*), after the stream's work.
+cudaError_t read_mx4_error(int* code, cudaStream_t stream);
 
 // Tensor-map helper (driver entry point resolved at run time).
 CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base,

@@ -363,4 +363,13 @@ estream_status estream_mx4_product(const void* x_codes, const void* x_scales, in
                                                                                         : ESTREAM_ERR_CUDA;
 }
 
+estream_status estream_mx4_error(void* cuda_stream) {
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    int code = 0;
+    if (read_mx4_error(&code, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    if (code == kDevErrNone) return ESTREAM_OK;
+    return code == kDevErrTimeout ? ESTREAM_ERR_TIMEOUT : ESTREAM_ERR_DEVICE;
+}
+
 }  // extern "C"

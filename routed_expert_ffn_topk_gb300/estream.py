@@ -105,6 +105,7 @@ SIGNATURES = {
     "estream_mx4_dequantize": (_I, [_P, _P, _I, _F, _I, _I, _P, _I, _L, _P]),
     "estream_mx4_weight_scales": (_I, [_P, _I, _I, _I, _I, _P, _P]),
     "estream_mx4_product": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _P, _I, _L, _P]),
+    "estream_mx4_error": (_I, [_P]),
     "estream_set_timing": (_I, [_P, _I]),
     "estream_reset_stats": (_I, [_P]),
     "estream_last_stats": (_I, [_P, ctypes.POINTER(Stats)]),
@@ -697,6 +698,14 @@ def mx4_product(x: Mx4, w: Mx4Weights, offsets: torch.Tensor | None = None, out:
                                          _MX4_ELEM[out.dtype], _row_stride(out, "out"),
                                          _stream(stream, dev)), "estream_mx4_product")
     return out
+
+
+def mx4_error(device=None, stream=None) -> int:
+    """estream_mx4_error on `device` (default: the current one): the first error
+    that product kernels recorded there since the last call."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        return lib().estream_mx4_error(_stream(stream, device))
 
 
 def set_timing(ctx, on: bool) -> None:
