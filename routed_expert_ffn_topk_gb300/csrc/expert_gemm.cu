@@ -87,6 +87,7 @@ size_t gemm_smem_bytes(int seg_count) {
 }
 
 #include "tc_ptx.cuh"
+#include "tc_pair_ptx.cuh"
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fdividef(g, 1.0f + __expf(-g)) * u;
@@ -1265,120 +1266,6 @@ size_t pair_smem_bytes(int seg_count, bool q4 = false) {
     const size_t n = static_cast<size_t>(seg_count + 1);
     return 1024 + pair_layout(q4).off_table + sizeof(int) * n +
            (pair_offsets_cached(seg_count, q4) ? sizeof(int) * n : 0);
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// Address of the same shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cl(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// mbar_wait with cluster-scope acquire (arrivals come from the peer CTA).
-// The cluster-scope form of mbar_wait_drain (ignores the abort flag).
-__device__ bool mbar_wait_cl_drain(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait_cl(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait_cl(bar, parity))
-        if (global_ns() - t0 > kDrainLimitNs) return false;
-    return true;
-}
-
-__device__ bool mbar_wait_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* dev_err) {
-    if (mbar_try_wait_cl(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    uint32_t spins = 0;
-    while (true) {
-        if (mbar_try_wait_cl(bar, parity)) return true;
-        if ((++spins & 63u) == 0) {
-            if (*abort_flag) return false;
-            if (global_ns() - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                record_error(dev_err, kDevErrTimeout);
-                return false;
-            }
-        }
-    }
-}
-// Release of this thread's shared-memory writes at cluster scope, restricted
-// to shared::cta memory (lighter than a full cluster-scope release, which
-// also waits for the thread's global-memory traffic), followed by a relaxed
-// arrival on a barrier of the peer CTA: the hand-off of a shared-memory
-// payload to the other CTA of the pair.
-__device__ __forceinline__ void mbar_arrive_remote_smem_release(uint32_t cl_addr) {
-    asm volatile(
-        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
-        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr)
-        : "memory");
-}
-// Arrive on a barrier given by its shared::cluster address (either CTA).
-__device__ __forceinline__ void mbar_arrive_cl(uint32_t cl_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* tm, int x, int y,
-                                                 uint32_t cl_bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(cl_bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair_hint(uint32_t dst, const CUtensorMap* tm, int x,
-                                                      int y, uint32_t cl_bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(cl_bar), "l"(policy)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-                 "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive once on the barrier at offset `bar` in both CTAs of the pair when
-// the MMAs issued so far have completed.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
 }
 
 // A pair tile covers 256 records (M = 256: 128 per CTA), except the last one

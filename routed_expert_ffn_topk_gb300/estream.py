@@ -8,6 +8,7 @@ module refuses to load when the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -164,6 +165,8 @@ def _stream(stream=None, device=None):
     handle), else the current stream of `device`. A torch stream of another
     device than `device` is refused."""
     if stream is None:
+        if isinstance(device, torch.device) and device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)  # current_stream without its object
         stream = torch.cuda.current_stream(device)
     if hasattr(stream, "cuda_stream"):
         if device is not None and stream.device != torch.device(device):
@@ -172,12 +175,15 @@ def _stream(stream=None, device=None):
     return stream
 
 
-class _on(torch.cuda.device):
-    """Makes the tensors' device current for the duration of one library
-    call: the library launches on the current device, with these pointers."""
+_SAME_DEVICE = contextlib.nullcontext()
 
-    def __init__(self, t: torch.Tensor):
-        super().__init__(t.device)
+
+def _on(t: torch.Tensor):
+    """Makes the tensors' device current for the duration of one library call
+    (the library launches on the current device, with these pointers); costs
+    nothing where it is already."""
+    d = t.get_device()
+    return _SAME_DEVICE if d == torch.cuda.current_device() else torch.cuda.device(d)
 
 
 def version() -> int:
@@ -450,17 +456,17 @@ def _check_layer_args(X: torch.Tensor, logits: torch.Tensor | None, Y: torch.Ten
     [T, H] fp32 and the residual A like X, all on one CUDA device."""
     if X.dim() != 2 or Y.dim() != 2 or (logits is not None and logits.dim() != 2):
         raise ValueError("X, logits and Y must be 2-d")
-    T, H = X.shape
-    if (logits is not None and logits.shape[0] != T) or tuple(Y.shape) != (T, H):
+    shape, dtype, dev = X.shape, X.dtype, X.device
+    T, H = shape
+    if (logits is not None and logits.shape[0] != T) or Y.shape != shape:
         raise ValueError(f"logits must be [T, E] and Y [T, H] with T={T}, H={H}")
-    if X.dtype not in (torch.bfloat16, torch.float32):
+    if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("X must be bf16 or fp32")
     if (logits is not None and logits.dtype != torch.float32) or Y.dtype != torch.float32:
         raise ValueError("logits and Y must be fp32")
-    if A is not None and (tuple(A.shape) != (T, H) or A.dtype != X.dtype):
-        raise ValueError("the residual must have X's shape and type")
-    tensors = [X, Y] + [t for t in (logits, A) if t is not None]
-    if any(not t.is_cuda for t in tensors) or len({t.device for t in tensors}) != 1:
+    if A is not None and A is not X and (A.shape != shape or A.dtype != dtype or A.device != dev):
+        raise ValueError("the residual must have X's shape and type, on its device")
+    if dev.type != "cuda" or Y.device != dev or (logits is not None and logits.device != dev):
         raise ValueError("X, logits, Y (and the residual) must be on one CUDA device")
 
 
@@ -578,6 +584,15 @@ class Mx4:
             raise ValueError("codes and scales must be contiguous")
         self.codes, self.scales, self.K, self.fmt, self.scale = codes, scales, K, fmt, float(scale)
 
+    @classmethod
+    def _empty(cls, R, K, Kp, b, fmt, scale, device):
+        """Uninitialised rows, of sizes already checked."""
+        q = cls.__new__(cls)
+        q.codes = torch.empty((R, Kp // 2), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((R, Kp // b), dtype=torch.uint8, device=device)
+        q.K, q.fmt, q.scale = K, fmt, float(scale)
+        return q
+
     @property
     def shape(self):
         return self.codes.shape[0], self.K
@@ -597,10 +612,11 @@ class Mx4Weights:
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a 2-d tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and st[1] != 1):
         raise ValueError(f"{name} must be 2-d with contiguous rows")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if ld < t.shape[1]:
+    ld = st[0] if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
         raise ValueError(f"{name} must not have overlapping rows")
     return ld
 
@@ -610,44 +626,56 @@ def mx4_quantize(x: torch.Tensor, fmt: int, scale: float = 1.0, rows: torch.Tens
     """Rows of x [n, K] (bf16, fp16 or fp32; rows may be strided) to 4-bit codes
     with a scale per block. rows [R] int32 gathers source rows (a route map's
     rec_tok); swiglu takes x [n, 2K] as gate | up and quantises SiLU(gate) * up."""
-    if x.dtype not in _MX4_ELEM or not x.is_cuda:
+    elem = _MX4_ELEM.get(x.dtype)
+    if elem is None or not x.is_cuda:
         raise ValueError("x must be a bf16, fp16 or fp32 CUDA tensor")
     ld = _row_stride(x, "x")
-    if swiglu and x.shape[1] % 2:
-        raise ValueError("swiglu needs an even number of columns (gate | up)")
-    K = x.shape[1] // 2 if swiglu else x.shape[1]
+    n, K = x.shape
+    if swiglu:
+        if K % 2:
+            raise ValueError("swiglu needs an even number of columns (gate | up)")
+        K //= 2
     b = mx4_block(fmt)
     if K < 1:
         raise ValueError("x must have at least one column")
     dev = x.device
-    if rows is not None and (rows.dim() != 1 or rows.dtype != torch.int32 or rows.device != dev):
-        raise ValueError("rows must be a 1-d int32 tensor on x's device")
-    R = x.shape[0] if rows is None else rows.numel()
+    R, rp = n, None
+    if rows is not None:
+        if rows.dim() != 1 or rows.dtype != torch.int32 or rows.device != dev:
+            raise ValueError("rows must be a 1-d int32 tensor on x's device")
+        R, rp = rows.numel(), _dptr(rows)
     if out is None:
-        out = Mx4(torch.empty(R, mx4_padded(K) // 2, dtype=torch.uint8, device=dev),
-                  torch.empty(R, mx4_padded(K) // b, dtype=torch.uint8, device=dev), K, fmt, scale)
+        out = Mx4._empty(R, K, mx4_padded(K), b, fmt, scale, dev)
     elif out.shape != (R, K) or out.fmt != fmt or out.codes.device != dev:
         raise ValueError(f"out must hold {R} rows of {K} in this format on x's device")
-    out.scale = float(scale)
+    else:
+        out.scale = float(scale)
     with _on(x):
-        _check(lib().estream_mx4_quantize(x.data_ptr(), _MX4_ELEM[x.dtype], ld, x.shape[0], R, K, _dptr(rows),
-                                          int(bool(swiglu)), fmt, out.scale, _dptr(out.codes),
-                                          _dptr(out.scales), _stream(stream, dev)), "estream_mx4_quantize")
+        st = lib().estream_mx4_quantize(x.data_ptr(), elem, ld, n, R, K, rp, 1 if swiglu else 0, fmt, out.scale,
+                                        out.codes.data_ptr(), out.scales.data_ptr(), _stream(stream, dev))
+    if st:
+        _check(st, "estream_mx4_quantize")
     return out
 
 
 def mx4_dequantize(q: Mx4, dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [R, K] that quantised rows stand for (bf16, fp16 or fp32)."""
-    R, K = q.shape
-    dev = q.codes.device
+    codes = q.codes
+    R, K, dev = codes.shape[0], q.K, codes.device
     if out is None:
-        out = torch.empty(R, K, dtype=dtype, device=dev)
-    if out.dtype not in _MX4_ELEM or tuple(out.shape) != (R, K) or out.device != dev:
-        raise ValueError(f"out must be [{R}, {K}] bf16, fp16 or fp32 on the codes' device")
-    with _on(q.codes):
-        _check(lib().estream_mx4_dequantize(_dptr(q.codes), _dptr(q.scales), q.fmt, q.scale, R, K, out.data_ptr(),
-                                            _MX4_ELEM[out.dtype], _row_stride(out, "out"),
-                                            _stream(stream, dev)), "estream_mx4_dequantize")
+        out, ld = torch.empty((R, K), dtype=dtype, device=dev), K
+    else:
+        if tuple(out.shape) != (R, K) or out.device != dev:
+            raise ValueError(f"out must be [{R}, {K}] on the codes' device")
+        ld = _row_stride(out, "out")
+    elem = _MX4_ELEM.get(out.dtype)
+    if elem is None:
+        raise ValueError("out must be bf16, fp16 or fp32")
+    with _on(codes):
+        st = lib().estream_mx4_dequantize(codes.data_ptr(), q.scales.data_ptr(), q.fmt, q.scale, R, K,
+                                          out.data_ptr(), elem, ld, _stream(stream, dev))
+    if st:
+        _check(st, "estream_mx4_dequantize")
     return out
 
 
@@ -679,24 +707,31 @@ def mx4_product(x: Mx4, w: Mx4Weights, offsets: torch.Tensor | None = None, out:
     """x [R, K] times w [P, N, K] transposed, both quantised in one format:
     [R, N] in bf16 or fp32. With offsets [P + 1] int32 (a route map's), rows
     [offsets[p], offsets[p + 1]) meet w[p], and rows outside every slot are zero."""
-    R, K = x.shape
-    P, N, Kw = w.shape
-    dev = x.codes.device
-    if K != Kw or x.fmt != w.fmt or w.codes.device != dev:
+    codes, K = x.codes, x.K
+    R, dev = codes.shape[0], codes.device
+    P, N = w.codes.shape[:2]
+    if K != w.K or x.fmt != w.fmt or w.codes.device != dev:
         raise ValueError("x and w must have one width and format, on one device")
-    if offsets is None and P != 1:
-        raise ValueError("weights of several slots need offsets")
+    op = None
     if offsets is not None:
         _need(offsets, P + 1, torch.int32, "offsets", dev)
+        op = _dptr(offsets)
+    elif P != 1:
+        raise ValueError("weights of several slots need offsets")
     if out is None:
-        out = torch.empty(R, N, dtype=out_dtype, device=dev)
-    if out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != (R, N) or out.device != dev:
-        raise ValueError(f"out must be [{R}, {N}] bf16 or fp32 on x's device")
-    with _on(x.codes):
-        _check(lib().estream_mx4_product(_dptr(x.codes), _dptr(x.scales), R, _dptr(w.codes), _dptr(w.tiles),
-                                         P, N, K, x.fmt, x.scale * w.scale, _dptr(offsets), out.data_ptr(),
-                                         _MX4_ELEM[out.dtype], _row_stride(out, "out"),
-                                         _stream(stream, dev)), "estream_mx4_product")
+        out, ld = torch.empty((R, N), dtype=out_dtype, device=dev), N
+    else:
+        if tuple(out.shape) != (R, N) or out.device != dev:
+            raise ValueError(f"out must be [{R}, {N}] on x's device")
+        ld = _row_stride(out, "out")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be bf16 or fp32")
+    with _on(codes):
+        st = lib().estream_mx4_product(codes.data_ptr(), x.scales.data_ptr(), R, w.codes.data_ptr(),
+                                       w.tiles.data_ptr(), P, N, K, x.fmt, x.scale * w.scale, op, out.data_ptr(),
+                                       _MX4_ELEM[out.dtype], ld, _stream(stream, dev))
+    if st:
+        _check(st, "estream_mx4_product")
     return out
 
 
