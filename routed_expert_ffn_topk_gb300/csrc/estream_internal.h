@@ -276,9 +276,9 @@ cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t stream);
 // Reads and clears the current device's product error word (kDevErr*), after the stream's work.
 cudaError_t read_mx4_error(int* code, cudaStream_t stream);
 
-// Tensor-map helper (driver entry point resolved at run time).
+// Tensor-map helper (driver entry point resolved at run time); 128-byte swizzle or none.
 CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base,
                         uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                        uint32_t box_inner, uint32_t box_outer);
+                        uint32_t box_inner, uint32_t box_outer, bool swizzle = true);
 
 }  // namespace es

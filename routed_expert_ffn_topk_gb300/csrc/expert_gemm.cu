@@ -2177,7 +2177,7 @@ EncodeTiledFn encode_fn() {
 
 CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base, uint64_t inner,
                         uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
-                        uint32_t box_outer) {
+                        uint32_t box_outer, bool swizzle) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return CUDA_ERROR_NOT_FOUND;
     const cuuint64_t dims[2] = {inner, outer};
@@ -2186,7 +2186,8 @@ CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* 
     const cuuint32_t estr[2] = {1, 1};
     return fn(tm, dtype, 2,
               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

@@ -17,6 +17,15 @@ namespace {
 #include "tc_ptx.cuh"
 #include "tc_pair_ptx.cuh"
 
+// One thread of the warp (all 32 call it). The compiler knows what follows to run
+// in a single thread, so it need not serialise the tensor-core and copy
+// instructions there over possible lanes: 75 clocks an instruction under
+// lane == 0.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // First error of a product kernel on this device (estream_mx4_error).
 __device__ int g_mx4_err;
 
@@ -28,56 +37,36 @@ __device__ int g_mx4_err;
 //
 // Weights are the M side (128 rows a tile) and x the N side (NT rows), so a
 // route map's short segments cost no more than their own rows rounded up to NT.
-// A stage is 256 values of K, both operands' codes loaded by TMA (128-byte rows,
-// 128-byte swizzle). The scales go to tensor memory by another way than
-// tcgen05.cp, which runs in line with the products (73 clocks for each of a
-// stage's twelve 512-byte pieces of a 256 x 256 tile, against 526 for its
-// products: 220 us for 4096 x 14336 x 4096, measured): four warps, one for each
-// lane quarter, write them with tcgen05.st, beside the running products, into
-// columns that belong to the stage's ring slot (row r of 128: lane r % 32, column
-// r / 32; each quarter holds a copy). That also takes the scales of x from where they lie: a
-// route map's segments start anywhere, so no layout in advance would fit.
+// A stage is 256 values of K: both operands' codes by TMA (128-byte rows, 128-byte
+// swizzle), the weights' scale tiles by one bulk copy. The scales of x come row
+// by row (a segment starts anywhere, so no tile layout fits in advance): four
+// warps fetch them a stage ahead and place them as the tensor core wants them
+// (row r of 128: lane r % 32, byte group r / 32). The issuing thread copies
+// scales to tensor memory with tcgen05.cp ahead of the products that use them;
+// both run in its issue order, and two column sets alternate.
 // ---------------------------------------------------------------------------
 
 constexpr int kMmaThreads = 320;  // producer, MMA, 4 epilogue and 4 scale warps
 
-constexpr int kScaleRing = 6;
-template <int kGroups>
-struct Scales {
-    static constexpr int kX = kGroups * 2048, kSlot = kX + 2048;  // x rows of 16 bytes, 4 weight tiles
-    static constexpr int kBytes = kScaleRing * kSlot;
-};
-
 template <int NT>
 struct Tile {
     static constexpr int kGroups = (NT + 127) / 128;   // 128-row groups of x scales
-    static constexpr int kA = 128 * 128, kB = NT * 128;
-    static constexpr int kStage = kA + kB;
-    static constexpr int kStages = (224 * 1024 - Scales<kGroups>::kBytes) / kStage < 8
-                                       ? (224 * 1024 - Scales<kGroups>::kBytes) / kStage : 8;
-    static constexpr int kAccs = 2;                    // accumulators of NT columns
-    static constexpr int kSfCols = 16 + 16 * kGroups;  // a slot's scales in tensor memory
-    static_assert(kAccs * NT + kStages * kSfCols <= 512, "tensor memory");
+    static constexpr int kA = 128 * 128, kB = NT * 128, kSfA = 2048, kSfB = 2048 * kGroups;
+    static constexpr int kStage = kA + kB + kSfA + kSfB;
+    static constexpr int kStages = 220 * 1024 / kStage < 8 ? 220 * 1024 / kStage : 8;
+    static constexpr int kAccs = NT <= 128 ? 2 : 1;    // accumulators of NT columns
+    static constexpr int kSfCols = 16 + 16 * kGroups;  // a stage's scales in tensor memory
 };
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10,"
-        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-        "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
-        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-                 : "memory");
+// Descriptor of a 32-row x 16-byte block of scales (rows of 16 bytes, 8-row
+// groups 128 bytes apart, no swizzle).
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8) << 16) |
+           (static_cast<uint64_t>(8) << 32) | (static_cast<uint64_t>(1) << 46);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10,"
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29,"
-        "%30, %31, %32};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-        "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
-        "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-        "r"(v[30]), "r"(v[31])
-                 : "memory");
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                         uint32_t sfb, uint32_t accumulate) {
     asm volatile(
@@ -93,6 +82,13 @@ __device__ __forceinline__ uint32_t mx4_idesc(int M, int N, bool e8m0) {
     return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (e8m0 ? 1u << 23 : 0u) |
            (static_cast<uint32_t>(M >> 4) << 24);
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 // Slot's rows, kept inside [0, R] whatever the offsets hold.
 __device__ __forceinline__ void slot_rows(const Mx4Product& p, int slot, int& lo, int& hi) {
     lo = p.offsets ? min(max(p.offsets[slot], 0), p.R) : 0;
@@ -169,118 +165,99 @@ __device__ __forceinline__ Work work_at(const Mx4Product& p, const int* base, in
     return w;
 }
 
-// ---- scales ----
-// The four scale warps bring a stage's scales into a shared-memory ring of their
-// own, five stages ahead of the tensor core and across tiles (a row of x at a
-// time: a thread per row, so that each line is looked up once; all four lane
-// quarters then read all rows), and write them to tensor memory from there.
-__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void* src, int bytes, bool have) {
-    const int n = have ? bytes : 0;
-    if (bytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// The scales of one row of x for a stage: four words, one for each 64 values.
+struct RowScales {
+    uint32_t w[4];
+};
+__device__ __forceinline__ RowScales row_scales(const uint8_t* row, int stage, int nb, int fmt, bool wide) {
+    RowScales r;
+    if (fmt == ESTREAM_MX4_E4M3X16) {
+        const int b0 = stage * 16;
+        if (wide && b0 + 16 <= nb) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + b0));
+            r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int b = b0 + 4 * j;
+                const uint32_t lo = b < nb ? __ldg(reinterpret_cast<const uint16_t*>(row + b)) : 0u;
+                const uint32_t hi = b + 2 < nb ? __ldg(reinterpret_cast<const uint16_t*>(row + b + 2)) : 0u;
+                r.w[j] = lo | (hi << 16);
+            }
+        }
+    } else {
+        const int b0 = stage * 8;
+        uint32_t v[2] = {0u, 0u};
+        if (wide && b0 + 8 <= nb) {
+            const uint2 t = __ldg(reinterpret_cast<const uint2*>(row + b0));
+            v[0] = t.x, v[1] = t.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (b0 + j < nb) v[j / 4] |= static_cast<uint32_t>(__ldg(row + b0 + j)) << (8 * (j % 4));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.w[j] = __byte_perm(v[j / 2], 0, j % 2 ? 0x3322 : 0x1100);
+    }
+    return r;
 }
 
-// All tiles of one CTA (tiles first, first + step, ...), stage after stage, by
-// threads tid = 0 .. 127: `slot_free(cols)` waits for the stage's ring slot and
-// gives the warp's tensor-memory columns, `publish()` hands them over.
-// After a failed wait the warps pass the remaining stages without work, so that
-// they meet at the barriers.
+// The scale warps of one CTA over all its tiles (first, first + step, ...): warp
+// lw places rows lw * 32 + lane of each 128-row group of a stage. A row's scales
+// are fetched kAhead stages before their place in the ring is free, across tiles.
+// `slot_free()` waits for the next ring slot and gives its place for x scales (or
+// null: stop), `publish()` hands it over.
+constexpr int kAhead = 4;
 template <int kGroups, int kRows, typename WorkAt, typename Wait, typename Publish>
-__device__ __forceinline__ void write_scales(const Mx4Product& p, int first, int step, int tiles, int n_blocks,
-                                             int kt, uint8_t* ring, int tid, WorkAt work, Wait slot_free,
-                                             Publish publish) {
-    using S = Scales<kGroups>;
-    const int lane = tid & 31, n_st = (kt + 3) / 4;
-    const bool e4m3 = p.fmt == ESTREAM_MX4_E4M3X16;
-    const int nb = mx4_padded(p.K) / mx4_block(p.fmt), per = e4m3 ? 16 : 8;  // scale bytes of a row, of a stage
-    const bool wide = nb % per == 0 && reinterpret_cast<uintptr_t>(p.xs) % per == 0;
-    // what is fetched next
-    int f_tile = first, f_st = 0, f_slot = 0;
-    const uint8_t *f_x = p.xs, *f_w = p.wt;
-    int f_rows = 0;  // rows of the tile from this thread's first on
+__device__ __forceinline__ void feed_scales(const Mx4Product& p, int first, int step, int tiles, int n_st, int lw,
+                                            int lane, WorkAt work, Wait slot_free, Publish publish) {
+    if (first >= tiles) return;
+    const int nb = mx4_padded(p.K) / mx4_block(p.fmt);
+    const int align = p.fmt == ESTREAM_MX4_E4M3X16 ? 16 : 8;
+    const bool wide = nb % align == 0 && reinterpret_cast<uintptr_t>(p.xs) % align == 0;
+    const int r0 = lw * 32 + lane;
+    int f_tile = first, f_st = 0, f_rows = 0;
+    const uint8_t* f_x = p.xs;
     auto enter = [&] {
         if (f_tile >= tiles) return;
         const Work w = work(f_tile);
-        f_x = p.xs + static_cast<size_t>(w.row + tid) * nb;
-        f_rows = min(kRows, w.end - w.row) - tid;
-        // (a pair's second half may lie past the matrix: it reads the last tile, its rows are not stored)
-        f_w = p.wt + (static_cast<size_t>(w.slot) * n_blocks + min(w.n0 / 128, n_blocks - 1)) * kt * 512 + tid * 16;
+        f_x = p.xs + static_cast<size_t>(w.row + r0) * nb;
+        f_rows = min(kRows, w.end - w.row) - r0;
     };
-    auto fetch = [&] {
-        if (f_tile < tiles) {
-            uint8_t* at = ring + f_slot * S::kSlot + tid * 16;
+    RowScales next[kAhead][kGroups];
+    auto fetch = [&](RowScales (&to)[kGroups]) {
+        if (f_tile >= tiles) return;
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                const uint8_t* src = f_x + static_cast<size_t>(q * 128) * nb + f_st * per;
-                const bool have = q * 128 < f_rows;
-                if (wide) {
-                    const bool in = have && (f_st + 1) * per <= nb;
-                    copy_or_zero(smem_addr(at + q * 2048), in ? src : p.xs, per, in);
-                } else {
-                    uint32_t v[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < per && have && f_st * per + i < nb)
-                            v[i / 4] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i % 4));
-                    *reinterpret_cast<uint4*>(at + q * 2048) = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            const bool in = 4 * f_st + tid / 32 < kt;
-            copy_or_zero(smem_addr(at + S::kX), in ? f_w + static_cast<size_t>(f_st) * 2048 : p.wt, 16, in);
-            if (++f_st == n_st) {
-                f_st = 0;
-                f_tile += step;
-                enter();
-            }
+        for (int q = 0; q < kGroups; ++q)
+            to[q] = q * 128 < f_rows ? row_scales(f_x + static_cast<size_t>(q * 128) * nb, f_st, nb, p.fmt, wide)
+                                     : RowScales{{0u, 0u, 0u, 0u}};
+        if (++f_st == n_st) {
+            f_st = 0;
+            f_tile += step;
+            enter();
         }
-        if (++f_slot == kScaleRing) f_slot = 0;
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     enter();
-    for (int i = 0; i < kScaleRing - 1; ++i) fetch();
-    int slot = 0;
-    bool ok = true;
-    for (int i = first; i < tiles; i += step)
-        for (int st = 0; st < n_st; ++st) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kScaleRing - 2) : "memory");
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            fetch();  // into the slot that every warp has read by this barrier
-            const uint8_t* at = ring + slot * S::kSlot + lane * 16;
-            if (++slot == kScaleRing) slot = 0;
-            uint32_t va[16], vb[16 * kGroups];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 v = *reinterpret_cast<const uint4*>(at + S::kX + j * 512);
-                va[4 * j] = v.x, va[4 * j + 1] = v.y, va[4 * j + 2] = v.z, va[4 * j + 3] = v.w;
-            }
-            // row i * 32 + lane is column i of each 64 values
+    for (int d = 0; d < kAhead; ++d) fetch(next[d]);
+    const int total = ((tiles - first + step - 1) / step) * n_st;
+    for (int n = 0; n < total; n += kAhead) {
 #pragma unroll
-            for (int r = 0; r < 4 * kGroups; ++r) {
-                uint4 v;
-                if (e4m3) {
-                    v = *reinterpret_cast<const uint4*>(at + r * 512);
-                } else {
-                    const uint2 t = *reinterpret_cast<const uint2*>(at + r * 512);
-                    v = make_uint4(__byte_perm(t.x, 0, 0x1100), __byte_perm(t.x, 0, 0x3322),
-                                   __byte_perm(t.y, 0, 0x1100), __byte_perm(t.y, 0, 0x3322));
-                }
-                vb[r] = v.x, vb[4 * kGroups + r] = v.y, vb[8 * kGroups + r] = v.z, vb[12 * kGroups + r] = v.w;
-            }
-            uint32_t cols = 0;
-            ok = ok && slot_free(cols);
-            if (!ok) continue;
-            tmem_st16(cols, va);
-            if constexpr (kGroups == 2)
-                tmem_st32(cols + 16, vb);
-            else
-                tmem_st16(cols + 16, vb);
-            tmem_st_wait();
-            tc_fence_before();
+        for (int d = 0; d < kAhead; ++d) {
+            if (n + d >= total) break;
+            uint8_t* sf = slot_free();
+            if (!sf) return;
+            sf += lane * 16 + lw * 4;
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(sf + q * 2048 + j * 512) = next[d][q].w[j];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
             publish();
+            fetch(next[d]);
         }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
 }
 
 template <int NT>
@@ -297,8 +274,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     volatile int* abort_flag = &abort_word;
-    int* base = p.P <= 64 ? base_small : reinterpret_cast<int*>(smem + stages * S::kStage + Scales<S::kGroups>::kBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* base = p.P <= 64 ? base_small : reinterpret_cast<int*>(smem + stages * S::kStage);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t sbase = smem_addr(smem);
     auto full = [&](int s) { return smem_addr(&bars[s]); };
     auto empty = [&](int s) { return smem_addr(&bars[S::kStages + s]); };
@@ -331,18 +308,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
     int* err = &g_mx4_err;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
                 const Work w = work_at(p, base, NT, i);
+                const uint8_t* sf = p.wt + (static_cast<size_t>(w.slot) * n_blocks + w.n0 / 128) * kt * 512;
                 for (int st = 0; st < n_st; ++st) {
                     if (!(ok = mbar_wait(empty(s), ph ^ 1u, abort_flag, err))) break;
+                    const int nk = min(4, kt - 4 * st);
                     const uint32_t at = sbase + s * S::kStage;
-                    mbar_arrive_expect_tx(full(s), S::kA + S::kB);
+                    mbar_arrive_expect_tx(full(s), S::kA + S::kB + nk * 512);
                     tma_load_2d(at, &tm_w, st * 128, w.slot * p.N + w.n0, full(s));
                     tma_load_2d(at + S::kA, &tm_x, st * 128, w.row, full(s));
+                    bulk_load(at + S::kA + S::kB, sf + static_cast<size_t>(st) * 2048, nk * 512, full(s));
                     ++issued;
                     if (++s == stages) {
                         s = 0;
@@ -356,21 +336,28 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
                     mbar_wait_drain(full(i % stages), static_cast<uint32_t>(i / stages) & 1u);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc = mx4_idesc(128, NT, p.fmt == ESTREAM_MX4_E8M0X32);
-            int s = 0, a = 0;
+            int s = 0, a = 0, it = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
             for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
                 if (!(ok = mbar_wait(acc_empty(a), aph ^ 1u, abort_flag, err))) break;
                 const uint32_t acc = tmem + a * NT;
-                for (int st = 0; st < n_st; ++st) {
+                for (int st = 0; st < n_st; ++st, ++it) {
                     if (!(ok = mbar_wait(full(s), ph, abort_flag, err))) break;
                     tc_fence_after();
                     const int nk = min(4, kt - 4 * st);
                     const uint32_t at = sbase + s * S::kStage;
-                    const uint32_t sfa = sf_col + s * S::kSfCols, sfb = sfa + 16;
+                    const uint32_t sfa = sf_col + (it & 1) * S::kSfCols, sfb = sfa + 16;
                     const uint64_t da = sw128_desc(at), db = sw128_desc(at + S::kA);
+                    const uint64_t dsa = scale_desc(at + S::kA + S::kB), dsb = scale_desc(at + S::kA + S::kB + S::kSfA);
+                    for (int j = 0; j < nk; ++j) {
+                        scales_to_tmem(sfa + 4 * j, dsa + 32 * j);
+#pragma unroll
+                        for (int q = 0; q < S::kGroups; ++q)
+                            scales_to_tmem(sfb + 4 * (j * S::kGroups + q), dsb + 32 * j + 128 * q);
+                    }
                     for (int j = 0; j < nk; ++j)
                         mma_mx4(acc, da + 2 * j, db + 2 * j, idesc, sfa + 4 * j, sfb + 4 * j * S::kGroups,
                                 st > 0 || j > 0);
@@ -427,20 +414,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
             }
         }
     } else {
-        const uint32_t quarter = static_cast<uint32_t>(warp % 4 * 32) << 16;
         int s = 0;
         uint32_t ph = 0;
-        write_scales<S::kGroups, NT>(
-            p, blockIdx.x, gridDim.x, tiles, n_blocks, kt, smem + stages * S::kStage, threadIdx.x - 192,
-            [&](int i) { return work_at(p, base, NT, i); },
-            [&](uint32_t& cols) {
-                if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ph ^ 1u, abort_flag, err))) return false;
-                tc_fence_after();
-                cols = sf_col + quarter + s * S::kSfCols;
-                return true;
+        feed_scales<S::kGroups, NT>(
+            p, blockIdx.x, gridDim.x, tiles, n_st, warp - 6, lane, [&](int i) { return work_at(p, base, NT, i); },
+            [&]() -> uint8_t* {
+                if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ph ^ 1u, abort_flag, err))) return nullptr;
+                return smem + s * S::kStage + S::kA + S::kB + S::kSfA;
             },
             [&] {
-                __syncwarp();
                 if (lane == 0) mbar_arrive(full(s));
                 if (++s == stages) {
                     s = 0;
@@ -455,25 +437,49 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
 }
 
 // ---------------------------------------------------------------------------
-// Pair form: clusters of two CTAs on 256 weight rows x 256 rows of x with
-// cta_group::2 (M = 256, N = 256). Each CTA holds its 128 weight rows and half of
-// the x rows of a stage, 32 KB for the 128 x 256 x 256 products that it does,
-// against 48 KB in the form above: that one reads and fills shared memory at more
-// than its 128 bytes a clock, and L2 at more than it delivers. The leader (rank 0)
-// issues the products of both; the scales of x of all 256 rows are written in both
-// CTAs. One 256-column accumulator and the scales fill tensor
-// memory, so the epilogue is not hidden behind the next tile; its eight warps
-// first drain the accumulator into registers (bf16 packed) and store afterwards.
+// Pair form: clusters of two CTAs on 256 rows of x x 256 weight rows with
+// cta_group::2 (M = 256, N = 256). Each CTA holds half of both operands of a stage,
+// 32 KB for the 128 x 256 x 256 products that it does, against 48 KB for a CTA
+// alone, which would read and fill shared memory at more than its 128 bytes a
+// clock and L2 at more than it delivers. The leader (rank 0) issues the products and
+// scale copies of both. Here x is the M side: a CTA then places only its own 128
+// rows' scales (the weights' come as tiles by TMA), and a thread of the epilogue
+// holds a row's neighbouring columns, which leave in whole 128-byte pieces.
+// What kept the products waiting, for 4096 x 14336 x 4096 (68 us with neither
+// loads, scale fetches nor stores): scale copies issued by the MMA thread, half
+// of its time, now from a thread of their own into columns that belong to the
+// stage's ring slot; and everything in the load/store unit -- scales fetched by
+// loads, whose latency each fence of the placing thread waited for (22 us), and
+// the epilogue's stores (27 us). Both go through TMA where the alignment allows.
+// One 256-column accumulator and the scales fill tensor memory, so the epilogue
+// is not hidden behind the next tile; its eight warps first drain the accumulator
+// into registers, 128 columns a thread (the roles' registers are split for that),
+// and scale and store afterwards.
 // ---------------------------------------------------------------------------
 
-constexpr int kPairThreads = 448;  // producer, MMA, 8 epilogue and 4 scale warps
+// Warpgroups: producer and MMA warps; two of epilogue warps; scale warps. At 128
+// registers a thread the launch holds 512 x 128; the split 80 + 168 + 168 + 88
+// comes to 504.
+constexpr int kPairThreads = 512;
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 struct Pair {
-    static constexpr int kA = 128 * 128, kB = 128 * 128;
-    static constexpr int kStage = kA + kB;
-    static constexpr int kStages = 5;  // 256 accumulator and 5 x 48 scale columns of 512
+    static constexpr int kA = 128 * 128, kB = 128 * 128, kSfA = 2048, kSfB = 4096;
+    static constexpr int kStage = kA + kB + kSfA + kSfB;
+    static constexpr int kStages = 5;
     static constexpr int kSfCols = 48;
+    static constexpr int kOutBytes = 8 * 4096;  // epilogue stage, 4 KB a warp
 };
 
+__device__ __forceinline__ void scales_to_tmem_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
 __device__ __forceinline__ void mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                              uint32_t sfb, uint32_t accumulate) {
     asm volatile(
@@ -483,12 +489,60 @@ __device__ __forceinline__ void mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b,
         : "memory");
 }
 
+// 128 bytes of one row a lane (bf16: 64 columns, fp32: 32; the lane's row is
+// row0 + lane) through the warp's 4 KB stage (128-byte swizzle) to out columns
+// from n on: by TMA, or, where the rows end inside (another slot's follow) or out
+// is not aligned for it, by plain stores. Rows from `rows` on and columns from p.N
+// on are left out.
+template <typename T>
+__device__ __forceinline__ void write_rows(const Mx4Product& p, const CUtensorMap* tm, uint8_t* stage,
+                                           const uint32_t (&v)[32], int lane, int row0, int rows, int n, bool tma) {
+    constexpr int kCols = 128 / sizeof(T), kPiece = 16 / sizeof(T);
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();  // the stage's last use is over
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) =
+            make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    if (tma && (rows >= 32 || row0 + rows == p.R)) {  // (the map ends with the last row and column)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tm)),
+                "r"(n), "r"(row0), "r"(smem_addr(stage))
+                : "memory");
+        return;
+    }
+    __syncwarp();
+    const int c = lane & 7;
+    if (tma && n + kCols <= p.N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16));
+            if (r < rows)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<size_t>(row0 + r) * p.ld + n + c * kPiece) = x;
+        }
+    } else {
+        for (int r = 0; r < min(32, rows); ++r)
+            for (int x = lane; x < kCols && n + x < p.N; x += 32)
+                static_cast<T*>(p.out)[static_cast<size_t>(row0 + r) * p.ld + n + x] = *reinterpret_cast<const T*>(
+                    stage + r * 128 + (((x / kPiece) ^ (r & 7)) * 16) + x % kPiece * sizeof(T));
+    }
+}
+
 __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __grid_constant__ CUtensorMap tm_w,
                                                                      const __grid_constant__ CUtensorMap tm_x,
-                                                                     const Mx4Product p, int stages) {
+                                                                     const __grid_constant__ CUtensorMap tm_s,
+                                                                     const __grid_constant__ CUtensorMap tm_xs,
+                                                                     const __grid_constant__ CUtensorMap tm_out,
+                                                                     const Mx4Product p, int stages, bool tma_xs,
+                                                                     bool tma_out) {
     using S = Pair;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * S::kStages + 3];
+    __shared__ __align__(8) uint64_t bars[4 * S::kStages + 4];
     __shared__ int base_small[65];
     __shared__ int sums[32];
     __shared__ uint32_t tmem_slot;
@@ -501,24 +555,30 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __gr
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     volatile int* abort_flag = &abort_word;
-    int* base = p.P <= 64 ? base_small : reinterpret_cast<int*>(smem + stages * S::kStage + Scales<2>::kBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* out_stage = smem + stages * S::kStage;
+    int* base = p.P <= 64 ? base_small : reinterpret_cast<int*>(out_stage + S::kOutBytes);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
     const uint32_t sbase = smem_addr(smem);
     auto full = [&](int s) { return smem_addr(&bars[s]); };            // the leader's
     auto empty = [&](int s) { return smem_addr(&bars[S::kStages + s]); };
     const uint32_t acc_full = smem_addr(&bars[2 * S::kStages]);
     const uint32_t acc_empty = smem_addr(&bars[2 * S::kStages + 1]);   // the leader's
-    const uint32_t drained = smem_addr(&bars[2 * S::kStages + 2]);
+    const uint32_t drained = smem_addr(&bars[2 * S::kStages + 2]), sf_drained = drained + 8;
+    auto raw = [&](int s) { return smem_addr(&bars[3 * S::kStages + 4 + s]); };     // x scales as they lie
+    auto scaled = [&](int s) { return smem_addr(&bars[2 * S::kStages + 4 + s]); };  // scales in tensor memory
     if (threadIdx.x == 0) {
         abort_word = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(full(s), 1 + 4 + 4);  // the leader's expect_tx and both CTAs' scale warps
             mbar_init(empty(s), 1);
+            mbar_init(scaled(s), 1);
+            mbar_init(raw(s), 1);
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 8 + 8);
         mbar_init(drained, 1);
+        mbar_init(sf_drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -530,32 +590,43 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __gr
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_slot, sf_col = tmem + 256;
-    const int n_pairs_blocks = (p.N + 255) / 256;
-    const int tiles = base[p.P] * n_pairs_blocks;
+    const int tiles = base[p.P] * ((p.N + 255) / 256);
     const int kt = (p.K + 63) / 64, n_st = (kt + 3) / 4;
     const int n_blocks = (p.N + 127) / 128;
     const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
     int* err = &g_mx4_err;
+    const bool e4m3 = p.fmt == ESTREAM_MX4_E4M3X16;
+    // this CTA's rows of a tile, and the tile's first weight row
     auto work = [&](int i) {
         Work w = work_at(p, base, 256, i);
-        w.n0 = w.n0 * 2 + 128 * rank;
+        w.n0 *= 2;
+        w.row += 128 * rank;
         return w;
     };
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        fewer_registers<80>();
+        if (warp == 0 && elect_one()) {
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int i = pair; i < tiles && ok; i += pairs) {
                 const Work w = work(i);
+                const int sf = (w.slot * n_blocks + w.n0 / 128) * kt;
                 for (int st = 0; st < n_st; ++st) {
                     if (!(ok = mbar_wait_cl(empty(s), ph ^ 1u, abort_flag, err))) break;
                     const uint32_t at = sbase + s * S::kStage;
                     const uint32_t bar = map_rank(full(s), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * (S::kA + S::kB));
-                    tma_load_2d_pair(at, &tm_w, st * 128, w.slot * p.N + w.n0, bar);
-                    tma_load_2d_pair(at + S::kA, &tm_x, st * 128, w.row + 128 * rank, bar);
+                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * (S::kA + S::kB + S::kSfB));
+                    if (tma_xs) {  // 16 bytes of each row (32-value blocks: two stages' worth)
+                        mbar_arrive_expect_tx(raw(s), S::kSfA);
+                        tma_load_2d(at + S::kA + S::kB, &tm_xs, e4m3 ? st * 16 : st / 2 * 16, w.row, raw(s));
+                    }
+                    tma_load_2d_pair(at, &tm_x, st * 128, w.row, bar);
+                    tma_load_2d_pair(at + S::kA, &tm_w, st * 128, w.slot * p.N + w.n0 + 128 * rank, bar);
+                    // weight scales of all 256 rows (past the matrix: of rows that are not stored)
+                    tma_load_2d_pair(at + S::kA + S::kB + S::kSfA, &tm_s, 0, sf + 4 * st, bar);
+                    tma_load_2d_pair(at + S::kA + S::kB + S::kSfA + 2048, &tm_s, 0, sf + kt + 4 * st, bar);
                     ++issued;
                     if (++s == stages) {
                         s = 0;
@@ -564,28 +635,64 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __gr
                 }
             }
             // after an abort the copies in flight land (on the leader's barriers) before the pair ends
-            if (!ok && rank == 0)
-                for (int i = max(0, issued - stages); i < issued; ++i)
-                    mbar_wait_cl_drain(full(i % stages), static_cast<uint32_t>(i / stages) & 1u);
+            if (!ok)
+                for (int i = max(0, issued - stages); i < issued; ++i) {
+                    const uint32_t par = static_cast<uint32_t>(i / stages) & 1u;
+                    if (rank == 0) mbar_wait_cl_drain(full(i % stages), par);
+                    if (tma_xs) mbar_wait_drain(raw(i % stages), par);
+                }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (warp == 2 && rank == 0 && elect_one()) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i = pair; i < tiles && ok; i += pairs)
+                for (int st = 0; st < n_st; ++st) {
+                    if (!(ok = mbar_wait_cl(full(s), ph, abort_flag, err))) break;
+                    tc_fence_after();
+                    const uint32_t at = sbase + s * S::kStage + S::kA + S::kB;
+                    const uint32_t sfa = sf_col + s * S::kSfCols, sfb = sfa + 16;
+                    const uint64_t da = scale_desc(at), db = scale_desc(at + S::kSfA);
+                    // (a ragged last stage's pieces past K hold what the slot held before: no product reads them)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        scales_to_tmem_pair(sfa + 4 * j, da + 32 * j);
+                        scales_to_tmem_pair(sfb + 8 * j, db + 32 * j);
+                        scales_to_tmem_pair(sfb + 8 * j + 4, db + 32 * j + 128);
+                    }
+                    umma_commit_pair(scaled(s));
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            if (!ok) {
+                umma_commit_pair(sf_drained);
+                mbar_wait_cl_drain(sf_drained, 0);
+            }
+        }
+        if (warp == 1 && rank == 0 && elect_one()) {
             const uint32_t idesc = mx4_idesc(256, 256, p.fmt == ESTREAM_MX4_E8M0X32);
             int s = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
             for (int i = pair; i < tiles && ok; i += pairs) {
                 if (!(ok = mbar_wait_cl(acc_empty, aph ^ 1u, abort_flag, err))) break;
-                tc_fence_after();
                 for (int st = 0; st < n_st; ++st) {
-                    if (!(ok = mbar_wait_cl(full(s), ph, abort_flag, err))) break;
+                    if (!(ok = mbar_wait_cl(scaled(s), ph, abort_flag, err))) break;  // after full(s)
                     tc_fence_after();
                     const int nk = min(4, kt - 4 * st);
                     const uint32_t at = sbase + s * S::kStage;
                     const uint32_t sfa = sf_col + s * S::kSfCols, sfb = sfa + 16;
                     const uint64_t da = sw128_desc(at), db = sw128_desc(at + S::kA);
-                    for (int j = 0; j < nk; ++j)
-                        mma_mx4_pair(tmem, da + 2 * j, db + 2 * j, idesc, sfa + 4 * j, sfb + 8 * j, st > 0 || j > 0);
+                    if (nk == 4) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_mx4_pair(tmem, da + 2 * j, db + 2 * j, idesc, sfa + 4 * j, sfb + 8 * j, st > 0 || j > 0);
+                    } else {
+                        for (int j = 0; j < nk; ++j)
+                            mma_mx4_pair(tmem, da + 2 * j, db + 2 * j, idesc, sfa + 4 * j, sfb + 8 * j, st > 0 || j > 0);
+                    }
                     umma_commit_pair(empty(s));
                     if (++s == stages) {
                         s = 0;
@@ -601,91 +708,101 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __gr
                 mbar_wait_cl_drain(drained, 0);
             }
         }
-    } else if (warp < 10) {
-        zero_outside(p, blockIdx.x, gridDim.x, threadIdx.x - 64, 256);
-        const int quad = warp % 4, half = (warp - 2) / 4;  // TMEM lanes; columns [128 half, + 128)
+    } else if (warp < 12) {
+        more_registers<168>();
+        zero_outside(p, blockIdx.x, gridDim.x, threadIdx.x - 128, 256);
+        const int quad = warp % 4, half = (warp - 4) / 4;  // TMEM lanes; columns [128 half, + 128)
         const uint32_t acc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
         const uint32_t release = map_rank(acc_empty, 0);
+        uint8_t* stage = out_stage + (warp - 4) * 4096;
+        const bool f32 = p.elem == ESTREAM_MX4_F32;
         uint32_t aph = 0;
         for (int i = pair; i < tiles; i += pairs) {
             const Work w = work(i);
             if (!__all_sync(0xffffffffu, mbar_wait_cl(acc_full, aph, abort_flag, err))) break;
             aph ^= 1u;
             tc_fence_after();
-            const int n = w.n0 + quad * 32 + lane;
-            const int rows = min(128, w.end - w.row - half * 128);  // may be <= 0
-            const size_t row0 = static_cast<size_t>(w.row + half * 128) * p.ld + n;
-            auto done = [&] {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cl(release);
-            };
-            if (p.elem == ESTREAM_MX4_BF16) {
-                uint32_t v[64];  // two rows a word
+            const int row0 = w.row + quad * 32, rows = w.end - row0, n = w.n0 + half * 128;
+            uint32_t v[4][32];
+            if (rows > 0) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t t[32];
-                    if (c * 32 < rows) {
-                        tmem_ld32(acc + c * 32, t);
-                        tmem_ld_wait();
-                    }
+                for (int c = 0; c < 4; ++c) tmem_ld32(acc + c * 32, v[c]);
+                tmem_ld_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_smem_release(release);
+            if (rows <= 0) continue;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(t[2 * x]) * p.scale,
-                                                                       __uint_as_float(t[2 * x + 1]) * p.scale);
-                        v[c * 16 + x] = *reinterpret_cast<const uint32_t*>(&b);
-                    }
-                }
-                done();
-                if (n < p.N) {
-                    uint16_t* out = static_cast<uint16_t*>(p.out) + row0;
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        if (2 * x < rows) out[2 * x * p.ld] = static_cast<uint16_t>(v[x]);
-                        if (2 * x + 1 < rows) out[(2 * x + 1) * p.ld] = static_cast<uint16_t>(v[x] >> 16);
-                    }
-                }
+                for (int x = 0; x < 32; ++x) v[c][x] = __float_as_uint(__uint_as_float(v[c][x]) * p.scale);
+            if (f32) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n + c * 32 < p.N) write_rows<float>(p, &tm_out, stage, v[c], lane, row0, rows, n + c * 32, tma_out);
             } else {
-                float* out = static_cast<float*>(p.out) + row0;
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t t[32];
-                    if (c * 32 < rows) {
-                        tmem_ld32(acc + c * 32, t);
-                        tmem_ld_wait();
-                    }
-                    if (c == 3) done();
-                    if (n < p.N)
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (c * 32 + x < rows) out[(c * 32 + x) * p.ld] = __uint_as_float(t[x]) * p.scale;
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t t[32];  // 64 columns
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const __nv_bfloat162 q = __floats2bfloat162_rn(
+                            __uint_as_float(v[2 * c + x / 16][x % 16 * 2]), __uint_as_float(v[2 * c + x / 16][x % 16 * 2 + 1]));
+                        t[x] = *reinterpret_cast<const uint32_t*>(&q);
+                    }
+                    if (n + c * 64 < p.N) write_rows<__nv_bfloat16>(p, &tm_out, stage, t, lane, row0, rows, n + c * 64, tma_out);
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stage outlives its stores
     } else {
-        const uint32_t quarter = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        fewer_registers<88>();
+        const int lw = warp - 12;
         int s = 0;
         uint32_t ph = 0;
-        write_scales<2, 256>(
-            p, pair, pairs, tiles, n_blocks, kt, smem + stages * S::kStage, threadIdx.x - 320, work,
-            [&](uint32_t& cols) {
-                if (!__all_sync(0xffffffffu, mbar_wait_cl(empty(s), ph ^ 1u, abort_flag, err))) return false;
-                tc_fence_after();
-                cols = sf_col + quarter + s * S::kSfCols;
-                return true;
-            },
-            [&] {
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0)
-                        mbar_arrive(full(s));
-                    else
-                        mbar_arrive_remote_smem_release(map_rank(full(s), 0));
+        auto publish = [&] {
+            if (lane == 0) {
+                if (rank == 0)
+                    mbar_arrive(full(s));
+                else
+                    mbar_arrive_remote_smem_release(map_rank(full(s), 0));
+            }
+            if (++s == stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        };
+        if (tma_xs) {
+            // a row's 16 bytes are four 64-value words: from rows as they lie to the tensor
+            // core's order, in place
+            bool ok = true;
+            for (int i = pair; i < tiles; i += pairs)
+                for (int st = 0; st < n_st; ++st) {
+                    ok = __all_sync(0xffffffffu, ok && mbar_wait(raw(s), ph, abort_flag, err));
+                    uint8_t* sf = smem + s * S::kStage + S::kA + S::kB;
+                    uint4 v = *reinterpret_cast<const uint4*>(sf + (lw * 32 + lane) * 16);
+                    if (!e4m3) {
+                        const uint32_t x = st & 1 ? v.z : v.x, y = st & 1 ? v.w : v.y;
+                        v = make_uint4(__byte_perm(x, 0, 0x1100), __byte_perm(x, 0, 0x3322), __byte_perm(y, 0, 0x1100),
+                                       __byte_perm(y, 0, 0x3322));
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");  // every row is in a register
+                    uint32_t* to = reinterpret_cast<uint32_t*>(sf + lane * 16 + lw * 4);
+                    to[0] = v.x, to[128] = v.y, to[256] = v.z, to[384] = v.w;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (ok) publish();
                 }
-                if (++s == stages) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            });
+        } else {
+            feed_scales<1, 128>(
+                p, pair, pairs, tiles, n_st, lw, lane, work,
+                [&]() -> uint8_t* {
+                    if (!__all_sync(0xffffffffu, mbar_wait_cl(empty(s), ph ^ 1u, abort_flag, err))) return nullptr;
+                    return smem + s * S::kStage + S::kA + S::kB;
+                },
+                publish);
+        }
     }
     tc_fence_before();
     __syncwarp();
@@ -721,13 +838,29 @@ int max_pairs(size_t smem) {
 }
 
 cudaError_t launch_pair(const Mx4Product& p, cudaStream_t stream) {
-    CUtensorMap tm_w, tm_x;
+    CUtensorMap tm_w, tm_x, tm_s, tm_xs, tm_out;
+    const uint64_t tiles_s = static_cast<uint64_t>(p.P) * ((p.N + 127) / 128) * ((p.K + 63) / 64);
     if (codes_map(&tm_w, p.wc, p.K, static_cast<size_t>(p.P) * p.N, 128) != CUDA_SUCCESS ||
-        codes_map(&tm_x, p.xc, p.K, static_cast<size_t>(p.R), 128) != CUDA_SUCCESS)
+        codes_map(&tm_x, p.xc, p.K, static_cast<size_t>(p.R), 128) != CUDA_SUCCESS ||
+        encode_tmap_2d(&tm_s, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.wt, 128, tiles_s, 512, 128, 4, false) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    // x scales and out by TMA where rows start on 16-byte boundaries
+    const int nb = mx4_padded(p.K) / mx4_block(p.fmt);
+    const bool f32 = p.elem == ESTREAM_MX4_F32;
+    const bool tma_xs = nb % 16 == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0;
+    const bool tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld * (f32 ? 4 : 2) % 16 == 0;
+    tm_xs = tm_out = tm_x;
+    if (tma_xs && encode_tmap_2d(&tm_xs, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.xs, nb, static_cast<uint64_t>(p.R), nb, 16, 128,
+                                 false) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    if (tma_out &&
+        encode_tmap_2d(&tm_out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, p.N,
+                       static_cast<uint64_t>(p.R), p.ld * (f32 ? 4 : 2), f32 ? 32 : 64, 32) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     const size_t prefix = p.P > 64 ? sizeof(int) * (p.P + 1) : 0;
-    const int stages = static_cast<int>(std::min<size_t>(Pair::kStages, (225 * 1024 - Scales<2>::kBytes - prefix) / Pair::kStage));
-    const size_t smem = 1024 + static_cast<size_t>(stages) * Pair::kStage + Scales<2>::kBytes + prefix;
+    const int stages = static_cast<int>(
+        std::min<size_t>(Pair::kStages, (225 * 1024 - Pair::kOutBytes - prefix) / Pair::kStage));
+    const size_t smem = 1024 + static_cast<size_t>(stages) * Pair::kStage + Pair::kOutBytes + prefix;
     cudaError_t rc = cudaFuncSetAttribute(k_mx4_product_pair, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
@@ -746,7 +879,7 @@ cudaError_t launch_pair(const Mx4Product& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_mx4_product_pair, tm_w, tm_x, p, stages);
+    return cudaLaunchKernelEx(&cfg, k_mx4_product_pair, tm_w, tm_x, tm_s, tm_xs, tm_out, p, stages, tma_xs, tma_out);
 }
 
 template <int NT>
@@ -762,8 +895,8 @@ cudaError_t launch_mma(const Mx4Product& p, cudaStream_t stream) {
     if (rc != cudaSuccess) return rc;
     // the prefix of more than 64 slots' tiles takes the place of ring stages
     const size_t prefix = p.P > 64 ? sizeof(int) * (p.P + 1) : 0;
-    const int stages = static_cast<int>(std::min<size_t>(S::kStages, (225 * 1024 - Scales<S::kGroups>::kBytes - prefix) / S::kStage));
-    const size_t smem = 1024 + static_cast<size_t>(stages) * S::kStage + Scales<S::kGroups>::kBytes + prefix;
+    const int stages = static_cast<int>(std::min<size_t>(S::kStages, (225 * 1024 - prefix) / S::kStage));
+    const size_t smem = 1024 + static_cast<size_t>(stages) * S::kStage + prefix;
     rc = cudaFuncSetAttribute(k_mx4_product<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
     // at most one ragged row tile a slot
