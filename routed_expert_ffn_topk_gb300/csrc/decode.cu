@@ -107,6 +107,7 @@ struct Routes {
     uint32_t* key;     // [T E] logits as ordered keys (E <= kKeysE)
     int* counts;       // [E + 1] (E > kKeysE)
     int* n_act;
+    int* cum;          // [n_act + n_shared + 1] weights of the experts before this one (split_at)
 };
 
 constexpr int kKeysE = 128;
@@ -114,7 +115,7 @@ constexpr int kKeysE = 128;
 __host__ __device__ inline size_t routes_bytes(int T, int k, int E, int n_shared) {
     const size_t R = static_cast<size_t>(T) * k;
     return (sizeof(Act) * (2 * static_cast<size_t>(E) + n_shared) +
-            sizeof(int) * (4 * R + (E <= kKeysE ? static_cast<size_t>(T) * E : static_cast<size_t>(E) + 1) + 1) + 15) /
+            sizeof(int) * (4 * R + (E <= kKeysE ? static_cast<size_t>(T) * E : static_cast<size_t>(E) + 1) + E + n_shared + 2) + 15) /
            16 * 16;
 }
 
@@ -128,8 +129,9 @@ __device__ Routes routes_at(void* smem, int T, int k, int E, int n_shared) {
     r.ids = r.row_tok + R;
     r.alpha = reinterpret_cast<float*>(r.ids + R);
     r.n_act = reinterpret_cast<int*>(r.alpha + R);
-    r.key = reinterpret_cast<uint32_t*>(r.n_act + 1);
-    r.counts = r.n_act + 1;
+    r.cum = r.n_act + 1;
+    r.counts = r.cum + E + n_shared + 1;
+    r.key = reinterpret_cast<uint32_t*>(r.counts);
     return r;
 }
 
@@ -150,6 +152,32 @@ __device__ void prepare_routes(const Routes& r, const DecodeCall& d) {
         if (d.E > kKeysE) r.counts[e] = 0;
     }
     if (threadIdx.x == 0 && d.E > kKeysE) r.counts[d.E] = 0;
+}
+
+// What a weight row of an expert with c tokens costs: 1 for streaming it, 1 for its
+// products with each tile of 8 tokens.
+__device__ __forceinline__ int row_weight(int c) { return c > 0 ? 1 + (c + 7) / 8 : 0; }
+
+// Where part b of g of the chosen and shared experts' rows (len, len_sh each)
+// begins: parts of equal weight (OLMoE shape, 32 tokens: with parts of equal rows
+// the groups on experts of more than 8 tokens ended 40 us after the median one).
+__device__ __forceinline__ int split_at(const Routes& r, int n_sh, int len, int len_sh, int step, int b, int g) {
+    const int n_act = *r.n_act, n = n_act + n_sh;
+    if (n == 0) return 0;
+    const unsigned own = r.cum[n_act];
+    auto before = [&](int e) {
+        const unsigned c = r.cum[e];
+        return min(c, own) * len + (max(c, own) - own) * len_sh;
+    };
+    const unsigned target = static_cast<unsigned>(static_cast<unsigned long long>(before(n)) * b / g);
+    int lo = 0, hi = n;  // before(lo) <= target; before(hi) > target or hi = n
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (before(mid) <= target) lo = mid; else hi = mid;
+    }
+    const int rows = lo < n_act ? len : len_sh;
+    const int in = static_cast<int>((target - before(lo)) / static_cast<unsigned>(r.cum[lo + 1] - r.cum[lo]));
+    return min(lo, n_act) * len + max(lo - n_act, 0) * len_sh + min(in, rows) / step * step;
 }
 
 // Which experts each token takes: the experts' token masks, the list of experts
@@ -201,26 +229,32 @@ __device__ void build_routes(const Routes& r, const DecodeCall& d, const float* 
     }
     __syncthreads();
     if (warp == 0) {
-        int n = 0, rows = 0;
+        int n = 0, rows = 0, weights = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
             const uint32_t mask = e < E ? r.expert[e].mask : 0u;
             const int c = __popc(mask);
             const unsigned has = __ballot_sync(0xffffffffu, c > 0);
-            int incl = c;
+            const int w = row_weight(c);
+            int incl = c + (w << 16);  // (at most 1024 rows and 5 x 32 weights in a round)
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, incl, s);
                 if (lane >= s) incl += o;
             }
             if (c > 0) {
-                r.expert[e].row0 = rows + incl - c;
-                r.act[n + __popc(has & ((1u << lane) - 1u))] = r.expert[e];
+                const int at = n + __popc(has & ((1u << lane) - 1u));
+                r.expert[e].row0 = rows + (incl & 0xffff) - c;
+                r.act[at] = r.expert[e];
+                r.cum[at] = weights + (incl >> 16) - w;
             }
             n += __popc(has);
-            rows += __shfl_sync(0xffffffffu, incl, 31);
+            const int all = __shfl_sync(0xffffffffu, incl, 31);
+            rows += all & 0xffff;
+            weights += all >> 16;
         }
         if (lane == 0) *r.n_act = n;
+        for (int j = lane; j <= d.n_shared; j += 32) r.cum[n + j] = weights + j * row_weight(T);
         for (int j = lane; j < d.n_shared; j += 32)
             r.act[n + j] = {T == 32 ? 0xffffffffu : (1u << T) - 1u, j * T, j, d.sh_scale[j]};
     }
@@ -276,12 +310,13 @@ __device__ void router_rows(const DecodeCall& d) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const __nv_bfloat16* X = static_cast<const __nv_bfloat16*>(d.X);
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(d.W_r);
-    for (int p = blockIdx.x * nw + warp; p < d.T * d.E; p += gridDim.x * nw) {
+    // neighbouring pairs on different SMs: few pairs then are few on each
+    for (int p = warp * gridDim.x + blockIdx.x; p < d.T * d.E; p += gridDim.x * nw) {
         const int t = p / d.E, e = p % d.E;
         const uint4* x = reinterpret_cast<const uint4*>(X + static_cast<size_t>(t) * d.H);
         const uint4* w = reinterpret_cast<const uint4*>(W + static_cast<size_t>(e) * d.H);
         float s = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = lane; c < d.H / 8; c += 32) {
             const uint4 a = __ldg(x + c), b = __ldg(w + c);
             const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -461,22 +496,18 @@ __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t w) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
-// Codes 2 i (low half) and 2 i + 1 (high half) of a 4-bit word as bf16 weights
-// (q - 8) d: the code in bits 3-6 of bf16 16 makes 16 + q, and one fma with
-// -24 d gives the weight. Exact: d has 5 significant bits, so 24 d has 7 and
-// (q - 8) d at most 8.
-__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i, __nv_bfloat162 d, __nv_bfloat162 d24) {
-    const uint32_t at = i == 0 ? word << 3 : word >> (4 * i - 3);
-    const uint32_t u = (at & 0x00780078u) | 0x41804180u;
-    const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), d, d24);
+// Codes 2 i (low half) and 2 i + 1 (high half) of a 4-bit word as bf16 q - 8: the
+// code in bits 0-3 of bf16 128 makes 128 + q.
+__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i) {
+    const uint32_t u = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&u), __floats2bfloat162_rn(-136.0f, -136.0f));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// The scale of column block b (the low or high 16 bits) twice, and - 24 of it.
-__device__ __forceinline__ void q4_scale(uint32_t bits, int b, bool half, __nv_bfloat162& d, __nv_bfloat162& d24) {
-    uint32_t v = __byte_perm(bits, 0, b ? 0x3232 : 0x1010);
-    if (half) v = half2_to_bf162(v);
-    d = *reinterpret_cast<const __nv_bfloat162*>(&v);
-    d24 = __hmul2(d, __floats2bfloat162_rn(-24.0f, -24.0f));
+// The scales of a row's two column blocks (gate and up: bf16; down: fp16).
+__device__ __forceinline__ float2 q4_scales(uint32_t bits, bool half) {
+    if (half) return __half22float2(*reinterpret_cast<const __half2*>(&bits));
+    return make_float2(__uint_as_float(bits << 16), __uint_as_float(bits & 0xffff0000u));
 }
 
 // The tiles of a range of rows of the chosen experts (len rows each, `routed`
@@ -557,15 +588,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
     }
     build_routes(r, d, d.W_r ? d.logits_out : d.logits);
     const int n_act = *r.n_act;
-    const int routed_h = n_act * F, total_h = routed_h + d.n_shared * Fs;
+    const int routed_h = n_act * F, routed_y = kByToken ? 0 : n_act * H;
     const int wg = warp % kGroup, group = blockIdx.x * kGroups + warp / kGroup;
     const int groups = gridDim.x * kGroups;
-    const int h0 = share(total_h, S::kStep, group, groups), h1 = share(total_h, S::kStep, group + 1, groups);
-    // Y rows: of Y itself, a range a CTA, or of every (expert, Y) pair, a range a group
-    const int routed_y = kByToken ? 0 : n_act * H;
-    const int total_y = kByToken ? H : routed_y + d.n_shared * H;
-    const int y_part = kByToken ? blockIdx.x : group, y_parts = kByToken ? gridDim.x : groups;
-    const int y0 = share(total_y, S::kStep, y_part, y_parts), y1 = share(total_y, S::kStep, y_part + 1, y_parts);
+    // h rows [h0, h1) of a group; Y rows [y0, y1): of Y itself, a CTA's, or of every
+    // (expert, Y) pair, a group's
+    int h0, h1, y0, y1;
+    if (kByToken) {
+        const int total = routed_h + d.n_shared * Fs;
+        h0 = share(total, S::kStep, group, groups);
+        h1 = share(total, S::kStep, group + 1, groups);
+        y0 = share(H, S::kStep, blockIdx.x, gridDim.x);
+        y1 = share(H, S::kStep, blockIdx.x + 1, gridDim.x);
+    } else {
+        // four bounds, a lane each
+        const bool y = lane & 2;
+        const int at = split_at(r, d.n_shared, y ? H : F, y ? H : Fs, S::kStep, group + (lane & 1), groups);
+        h0 = __shfl_sync(0xffffffffu, at, 0);
+        h1 = __shfl_sync(0xffffffffu, at, 1);
+        y0 = __shfl_sync(0xffffffffu, at, 2);
+        y1 = __shfl_sync(0xffffffffu, at, 3);
+    }
     constexpr int kYWarps = kByToken ? kWarps : kGroup;  // warps that share a Y tile
     const int wy = kByToken ? warp : wg;
     const int YB = n_act * FB + d.n_shared * FsB;  // k-blocks of a Y row over all experts
@@ -792,24 +835,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                         // a unit's sums join the running ones by rounded additions: the tensor
                         // cores truncate, which over a long chain would bias the sum
                         float part[2][4] = {};  // a chain for each column block
-                        uint32_t scg = 0, scu = 0;  // 4-bit: the rows' scales of both column blocks
-                        if (kQ4) {
-                            scg = as<uint32_t>(u + S::kHRows * 32 + (m * 8 + g) * 4);
-                            scu = as<uint32_t>(u + S::kHRows * 32 + (m * 8 + g) * 4 + S::kHPart);
-                        }
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             uint32_t wg[4], wu[4];
                             if (kQ4) {
                                 const uint8_t* p = u + b * (S::kHRows * 16) + (m * 8 + g) * 16 + tq * 4;
                                 const uint32_t qg = as<uint32_t>(p), qu = as<uint32_t>(p + S::kHPart);
-                                __nv_bfloat162 sg, sg24, su, su24;
-                                q4_scale(scg, b, false, sg, sg24);
-                                q4_scale(scu, b, false, su, su24);
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    wg[i] = q4_pair(qg, i, sg, sg24);
-                                    wu[i] = q4_pair(qu, i, su, su24);
+                                    wg[i] = q4_pair(qg, i);
+                                    wu[i] = q4_pair(qu, i);
                                 }
                             } else {
                                 const uint8_t* p = u + (m * 8 + g) * 128 + b * 64 + tq * 16;
@@ -820,8 +855,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                             mma_bf16(part[b], wg[0], wu[0], wg[1], wu[1], x[b].x, x[b].y);
                             mma_bf16(part[b], wg[2], wu[2], wg[3], wu[3], x[b].z, x[b].w);
                         }
+                        if (kQ4) {
+                            const uint8_t* p = u + S::kHRows * 32 + (m * 8 + g) * 4;
+                            const float2 sg = q4_scales(as<uint32_t>(p), false);
+                            const float2 su = q4_scales(as<uint32_t>(p + S::kHPart), false);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][i] + part[1][i];
+                            for (int i = 0; i < 4; ++i)
+                                acc[m][j][i] = fmaf(part[0][i], i < 2 ? sg.x : su.x,
+                                                    fmaf(part[1][i], i < 2 ? sg.y : su.y, acc[m][j][i]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][i] + part[1][i];
+                        }
                     }
                     x[0] = more[0];
                     x[1] = more[1];
@@ -931,10 +976,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                             const int row = m * 16 + hi * 8 + g;
                             if (kQ4) {
                                 const uint32_t word = as<uint32_t>(u + b * (S::kYRows * 16) + row * 16 + tq * 4);
-                                __nv_bfloat162 sc, sc24;
-                                q4_scale(as<uint32_t>(u + S::kYRows * 32 + row * 4), b, true, sc, sc24);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) w[m][b][2 * i + hi] = q4_pair(word, i, sc, sc24);
+                                for (int i = 0; i < 4; ++i) w[m][b][2 * i + hi] = q4_pair(word, i);
                             } else {
                                 const uint4 v = as<uint4>(u + row * 128 + b * 64 + tq * 16);
                                 w[m][b][hi] = half2_to_bf162(v.x);
@@ -958,9 +1001,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                                 mma_bf16(part[b][m], w[m][b][4], w[m][b][5], w[m][b][6], w[m][b][7], x[q3][b].z, x[q3][b].w);
                             }
 #pragma unroll
-                    for (int m = 0; m < S::kYTiles; ++m)
+                    for (int m = 0; m < S::kYTiles; ++m) {
+                        if (kQ4) {
+                            const uint8_t* p = u + S::kYRows * 32 + (m * 16 + g) * 4;
+                            const float2 lo = q4_scales(as<uint32_t>(p), true), hi = q4_scales(as<uint32_t>(p + 32), true);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][m][i] + part[1][m][i];
+                            for (int i = 0; i < 4; ++i)
+                                acc[m][j][i] = fmaf(part[0][m][i], i < 2 ? lo.x : hi.x,
+                                                    fmaf(part[1][m][i], i < 2 ? lo.y : hi.y, acc[m][j][i]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][m][i] + part[1][m][i];
+                        }
+                    }
                 }
             }
             release();
