@@ -66,10 +66,29 @@ __device__ __forceinline__ void load8(const typename Elem<kElem>::T* p, int n, b
     }
 }
 
+// x / d from r = 1 / d: a quotient, its exact remainder and one correction
+// (Markstein 1990). For finite operands away from the ends of the exponent range.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+
 // SiLU(g) * u in the written order g / (1 + exp(-g)) * u, each step rounded to
-// fp32 (no contraction).
+// fp32 (no contraction). The reciprocal is the hardware's, refined by one Newton
+// step: two instructions for the range check and branch that a general division
+// carries for each value.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
+    const float y = __fadd_rn(1.0f, expf(-g));
+    float h;
+    if (y < 1e30f) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+        r = __fmaf_rn(__fmaf_rn(-y, r, 1.0f), r, r);
+        h = quotient(g, y, r);
+    } else {  // g below about -69, or not a number
+        h = __fdiv_rn(g, y);
+    }
+    return __fmul_rn(h, u);
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t s) {
@@ -80,20 +99,33 @@ __device__ __forceinline__ float e8m0_value(uint8_t s) {
                      : __uint_as_float(s == 0 ? 0x00400000u : static_cast<uint32_t>(s) << 23);
 }
 
+// How a block's warps lie over a matrix: 2^along of them beside each other on a
+// row (256 values each), the rest on the rows below, so that a lane's row and
+// column need no division.
+struct Tiling {
+    int groups;  // 8-value groups of a padded row
+    int along;
+    __device__ __forceinline__ int row() const {
+        return blockIdx.x * (kThreads / 32 >> along) + (threadIdx.x >> 5 >> along);
+    }
+    __device__ __forceinline__ int group() const {
+        return ((blockIdx.y << along) + (threadIdx.x >> 5 & ((1 << along) - 1))) * 32 + (threadIdx.x & 31);
+    }
+};
+
 // Eight values a lane; two (16-value blocks) or four (32-value blocks)
 // neighbouring lanes form a block's maximum by shuffles. A row is a whole
 // number of 32-value groups, so a block never spans rows.
 template <int kElem, bool kSwiglu, int kFmt>
-__global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, int groups, bool wide) {
+__global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, Tiling tiling, bool wide) {
     using T = typename Elem<kElem>::T;
     constexpr int kLanes = kFmt == ESTREAM_MX4_E4M3X16 ? 2 : 4;
-    const size_t total = static_cast<size_t>(q.R) * groups;
-    const size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
-    // a warp's lanes past the end stay for the shuffles
-    const bool in = i < total;
-    const int row = in ? static_cast<int>(i / groups) : 0;
-    const int c = in ? static_cast<int>(i % groups) * 8 : 0;
-    const int src = in && q.rows ? q.rows[row] : row;
+    const int row = tiling.row(), group = tiling.group(), c = group * 8;
+    if (row >= q.R || group - (threadIdx.x & 31) >= tiling.groups) return;  // the whole warp
+    // a warp's lanes past the row's end stay for the shuffles
+    const bool in = group < tiling.groups;
+    const size_t i = static_cast<size_t>(row) * tiling.groups + group;
+    const int src = q.rows ? q.rows[row] : row;
     const bool have = in && src >= 0 && src < q.n_src;
     float v[8];
 #pragma unroll
@@ -132,28 +164,37 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, 
     }
     uint32_t codes = 0;
     if (finite && d > 0.0f) {
+        // One reciprocal for the block. With d's and the block's exponents well inside
+        // the range, the corrected quotient gives the division's code for every d and
+        // every x next to a rounding boundary of E2M1; its sign is x's, also for -0.
+        if (amax < 1e18f && d > 1e-18f && d < 1e18f) {
+            const float r = __frcp_rn(d);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float2 f = make_float2(__fdiv_rn(v[j], d), __fdiv_rn(v[j + 1], d));
-            codes |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (4 * j);
+            for (int j = 0; j < 8; ++j) v[j] = copysignf(quotient(v[j], d, r), v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], d);
         }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+            codes |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(v[j], v[j + 1]), __NV_E2M1, cudaRoundNearest))
+                     << (4 * j);
     }
     if (!in) return;
     reinterpret_cast<uint32_t*>(q.codes)[i] = codes;
-    if ((threadIdx.x & (kLanes - 1)) == 0) q.scales[i / kLanes] = s;
+    if (group % kLanes == 0) q.scales[i / kLanes] = s;
 }
 
 template <int kElem, int kFmt>
 __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const uint32_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, float g,
-                                                             int R, int K, int groups, void* out,
+                                                             int R, int K, Tiling tiling, void* out,
                                                              long long ld, bool wide) {
     using T = typename Elem<kElem>::T;
     constexpr int kLanes = kFmt == ESTREAM_MX4_E4M3X16 ? 2 : 4;
-    const size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= static_cast<size_t>(R) * groups) return;
-    const int row = static_cast<int>(i / groups);
-    const int c = static_cast<int>(i % groups) * 8;
+    const int row = tiling.row(), group = tiling.group(), c = group * 8;
+    if (row >= R || group >= tiling.groups) return;
+    const size_t i = static_cast<size_t>(row) * tiling.groups + group;
     const uint32_t w = codes[i];
     const uint8_t s = scales[i / kLanes];
     const float d = __fmul_rn(kFmt == ESTREAM_MX4_E4M3X16 ? e4m3_value(s) : e8m0_value(s), g);
@@ -193,27 +234,36 @@ __global__ void __launch_bounds__(kThreads) k_mx4_weight_scales(const uint8_t* _
     tiles[i] = n < N && b < nb ? scales[(p * N + n) * nb + b] : 0;
 }
 
+Tiling tile_rows(int R, int K, dim3& grid) {
+    Tiling t{mx4_padded(K) / 8, 0};
+    const int warps = (t.groups + 31) / 32;
+    while (t.along < 3 && (2 << t.along) <= warps) ++t.along;
+    const int down = kThreads / 32 >> t.along;
+    grid = dim3((R + down - 1) / down, (warps + (1 << t.along) - 1) >> t.along);
+    return t;
+}
+
 template <int kElem, bool kSwiglu>
-cudaError_t quantize_fmt(const Mx4Quantize& q, int groups, bool wide, unsigned grid, cudaStream_t s) {
+cudaError_t quantize_fmt(const Mx4Quantize& q, const Tiling& t, bool wide, dim3 grid, cudaStream_t s) {
     if (q.fmt == ESTREAM_MX4_E4M3X16)
-        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(q, groups, wide);
+        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(q, t, wide);
     else
-        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(q, groups, wide);
+        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(q, t, wide);
     return cudaGetLastError();
 }
 template <int kElem>
-cudaError_t quantize_elem(const Mx4Quantize& q, int groups, bool wide, unsigned grid, cudaStream_t s) {
-    return q.swiglu ? quantize_fmt<kElem, true>(q, groups, wide, grid, s)
-                    : quantize_fmt<kElem, false>(q, groups, wide, grid, s);
+cudaError_t quantize_elem(const Mx4Quantize& q, const Tiling& t, bool wide, dim3 grid, cudaStream_t s) {
+    return q.swiglu ? quantize_fmt<kElem, true>(q, t, wide, grid, s)
+                    : quantize_fmt<kElem, false>(q, t, wide, grid, s);
 }
 template <int kElem>
 cudaError_t dequantize_elem(const uint8_t* codes, const uint8_t* scales, int fmt, float g, int R, int K,
-                            int groups, void* out, long long ld, bool wide, unsigned grid, cudaStream_t s) {
+                            const Tiling& t, void* out, long long ld, bool wide, dim3 grid, cudaStream_t s) {
     const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
     if (fmt == ESTREAM_MX4_E4M3X16)
-        k_mx4_dequantize<kElem, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, groups, out, ld, wide);
+        k_mx4_dequantize<kElem, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, t, out, ld, wide);
     else
-        k_mx4_dequantize<kElem, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, groups, out, ld, wide);
+        k_mx4_dequantize<kElem, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, t, out, ld, wide);
     return cudaGetLastError();
 }
 
@@ -223,31 +273,29 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream) {
-    const int groups = mx4_padded(q.K) / 8;
-    const size_t total = static_cast<size_t>(q.R) * groups;
-    if (total == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>((total + kThreads - 1) / kThreads);
+    if (q.R == 0) return cudaSuccess;
+    dim3 grid;
+    const Tiling t = tile_rows(q.R, q.K, grid);
     // 16-byte loads need every row (and the up half of it) on a 16-byte boundary
     const size_t b = elem_bytes(q.elem);
     const bool wide = on16(q.x) && q.ld * b % 16 == 0 && (!q.swiglu || q.K * b % 16 == 0);
-    if (q.elem == ESTREAM_MX4_BF16) return quantize_elem<ESTREAM_MX4_BF16>(q, groups, wide, grid, stream);
-    if (q.elem == ESTREAM_MX4_F16) return quantize_elem<ESTREAM_MX4_F16>(q, groups, wide, grid, stream);
-    return quantize_elem<ESTREAM_MX4_F32>(q, groups, wide, grid, stream);
+    if (q.elem == ESTREAM_MX4_BF16) return quantize_elem<ESTREAM_MX4_BF16>(q, t, wide, grid, stream);
+    if (q.elem == ESTREAM_MX4_F16) return quantize_elem<ESTREAM_MX4_F16>(q, t, wide, grid, stream);
+    return quantize_elem<ESTREAM_MX4_F32>(q, t, wide, grid, stream);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, float scale,
                                   int R, int K, void* out, int elem, long long ld,
                                   cudaStream_t stream) {
-    const int groups = mx4_padded(K) / 8;
-    const size_t total = static_cast<size_t>(R) * groups;
-    if (total == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>((total + kThreads - 1) / kThreads);
+    if (R == 0) return cudaSuccess;
+    dim3 grid;
+    const Tiling t = tile_rows(R, K, grid);
     const bool wide = on16(out) && ld * elem_bytes(elem) % 16 == 0;
     if (elem == ESTREAM_MX4_BF16)
-        return dequantize_elem<ESTREAM_MX4_BF16>(codes, scales, fmt, scale, R, K, groups, out, ld, wide, grid, stream);
+        return dequantize_elem<ESTREAM_MX4_BF16>(codes, scales, fmt, scale, R, K, t, out, ld, wide, grid, stream);
     if (elem == ESTREAM_MX4_F16)
-        return dequantize_elem<ESTREAM_MX4_F16>(codes, scales, fmt, scale, R, K, groups, out, ld, wide, grid, stream);
-    return dequantize_elem<ESTREAM_MX4_F32>(codes, scales, fmt, scale, R, K, groups, out, ld, wide, grid, stream);
+        return dequantize_elem<ESTREAM_MX4_F16>(codes, scales, fmt, scale, R, K, t, out, ld, wide, grid, stream);
+    return dequantize_elem<ESTREAM_MX4_F32>(codes, scales, fmt, scale, R, K, t, out, ld, wide, grid, stream);
 }
 
 cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int P, int N, int K, int fmt,
