@@ -51,7 +51,7 @@ struct Elem<ESTREAM_MX4_F32> {
 // Eight consecutive values from p (n of them inside the row, the rest zero);
 // wide loads when the row's values are 16-byte aligned.
 template <int kElem>
-__device__ __forceinline__ void load8(const typename Elem<kElem>::T* p, int n, bool wide, float (&v)[8]) {
+__device__ __forceinline__ void load8(const typename Elem<kElem>::T* p, int n, bool wide, float* v) {
     using T = typename Elem<kElem>::T;
     if (wide && n >= 8) {
         alignas(16) T t[8];
@@ -66,29 +66,65 @@ __device__ __forceinline__ void load8(const typename Elem<kElem>::T* p, int n, b
     }
 }
 
-// x / d from r = 1 / d: a quotient, its exact remainder and one correction
+// - x / d from nr = - 1 / d: a quotient, its exact remainder and one correction
 // (Markstein 1990). For finite operands away from the ends of the exponent range.
-__device__ __forceinline__ float quotient(float x, float d, float r) {
-    const float q = __fmul_rn(x, r);
-    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+// Two values an instruction, and negated throughout because a packed multiply-add
+// takes no signs; a zero's sign comes out opposite to x's as well.
+__device__ __forceinline__ float2 neg_quotient(float2 x, float2 d, float2 nr) {
+    const float2 q = __fmul2_rn(x, nr);
+    return __ffma2_rn(__ffma2_rn(q, d, x), nr, q);
+}
+// Eight values as E2M1 codes, the first in the lowest bits: nearest, ties to the
+// even code, at most 6.
+__device__ __forceinline__ uint32_t e2m1_codes(const float* v) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
+}
+// The largest magnitude, NaN if one is NaN.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
 }
 
-// SiLU(g) * u in the written order g / (1 + exp(-g)) * u, each step rounded to
-// fp32 (no contraction). The reciprocal is the hardware's, refined by one Newton
-// step: two instructions for the range check and branch that a general division
-// carries for each value.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    const float y = __fadd_rn(1.0f, expf(-g));
-    float h;
-    if (y < 1e30f) {
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-        r = __fmaf_rn(__fmaf_rn(-y, r, 1.0f), r, r);
-        h = quotient(g, y, r);
-    } else {  // g below about -69, or not a number
-        h = __fdiv_rn(g, y);
+// v = - SiLU(v) * u in the written order g / (1 + exp(-g)) * u, each step rounded
+// to fp32 (no contraction). The reciprocal is the hardware's, refined by one
+// Newton step; one range check and branch for the values instead of the one
+// that a general division carries for each. (Over every finite fp32 g with
+// 1 + exp(-g) < 1e30 the quotient equals the division's.)
+template <int kN>
+__device__ __forceinline__ void neg_silu_mul(float (&v)[kN], const float (&u)[kN]) {
+    float y[kN];
+    uint32_t top = 0;  // as bits: y >= 1, or a NaN, which is larger
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        y[j] = __fadd_rn(1.0f, expf(-v[j]));
+        top = max(top, __float_as_uint(y[j]));
     }
-    return __fmul_rn(h, u);
+    if (top < __float_as_uint(1e30f)) {
+#pragma unroll
+        for (int j = 0; j < kN; j += 2) {
+            float2 r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-y[j]));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-y[j + 1]));
+            const float2 d = make_float2(y[j], y[j + 1]);
+            r = __ffma2_rn(__ffma2_rn(d, r, make_float2(1.0f, 1.0f)), r, r);
+            const float2 h = __fmul2_rn(neg_quotient(make_float2(v[j], v[j + 1]), d, r), make_float2(u[j], u[j + 1]));
+            v[j] = h.x;
+            v[j + 1] = h.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] = -__fmul_rn(__fdiv_rn(v[j], y[j]), u[j]);
+    }
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t s) {
@@ -100,10 +136,10 @@ __device__ __forceinline__ float e8m0_value(uint8_t s) {
 }
 
 // How a block's warps lie over a matrix: 2^along of them beside each other on a
-// row (256 values each), the rest on the rows below, so that a lane's row and
-// column need no division.
+// row (32 groups of values each), the rest on the rows below, so that a lane's row
+// and column need no division.
 struct Tiling {
-    int groups;  // 8-value groups of a padded row
+    int groups;  // of a padded row
     int along;
     __device__ __forceinline__ int row() const {
         return blockIdx.x * (kThreads / 32 >> along) + (threadIdx.x >> 5 >> along);
@@ -113,44 +149,43 @@ struct Tiling {
     }
 };
 
-// Eight values a lane; two (16-value blocks) or four (32-value blocks)
-// neighbouring lanes form a block's maximum by shuffles. A row is a whole
-// number of 32-value groups, so a block never spans rows.
+// Sixteen values a lane: a block of 16, or with its neighbour one of 32, so what
+// is done once a block (scale, reciprocal, addresses) is shared by as many values
+// as a lane's registers hold at full occupancy. A row is a whole number of
+// 32-value groups, so a block never spans rows.
+// Bound by issue slots with SwiGLU.
+constexpr int kVals = 16;
 template <int kElem, bool kSwiglu, int kFmt>
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, Tiling tiling, bool wide) {
     using T = typename Elem<kElem>::T;
-    constexpr int kLanes = kFmt == ESTREAM_MX4_E4M3X16 ? 2 : 4;
-    const int row = tiling.row(), group = tiling.group(), c = group * 8;
-    if (row >= q.R || group - (threadIdx.x & 31) >= tiling.groups) return;  // the whole warp
-    // a warp's lanes past the row's end stay for the shuffles
+    const int row = tiling.row(), group = tiling.group(), c = group * kVals;
+    if (row >= q.R || group - static_cast<int>(threadIdx.x & 31) >= tiling.groups) return;  // the whole warp
+    // a warp's lanes past the row's end stay for the shuffle
     const bool in = group < tiling.groups;
     const size_t i = static_cast<size_t>(row) * tiling.groups + group;
     const int src = q.rows ? q.rows[row] : row;
     const bool have = in && src >= 0 && src < q.n_src;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = in && !have ? __int_as_float(0x7fc00000) : 0.0f;
+    float v[kVals];
     if (have) {
         const T* p = static_cast<const T*>(q.x) + static_cast<size_t>(src) * q.ld + c;
         const int n = q.K - c;
-        if (n > 0) {
-            load8<kElem>(p, n, wide, v);
-            if (kSwiglu) {
-                float u[8];
-                load8<kElem>(p + q.K, n, wide, u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = silu_mul(v[j], u[j]);
-            }
+        for (int j = 0; j < kVals; j += 8) load8<kElem>(p + j, n - j, wide, v + j);
+        if (kSwiglu) {
+            float u[kVals];
+#pragma unroll
+            for (int j = 0; j < kVals; j += 8) load8<kElem>(p + q.K + j, n - j, wide, u + j);
+            neg_silu_mul(v, u);
         }
-    }
-    // largest magnitude, as bits: a NaN or infinity is at least 0x7f800000
-    uint32_t m = 0;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    if (kLanes == 4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const bool finite = m < 0x7f800000u;
-    const float amax = __uint_as_float(m);
+        for (int j = 0; j < kVals; ++j) v[j] = in ? __int_as_float(0x7fc00000) : 0.0f;
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVals; j += 2) amax = max_abs(v[j], v[j + 1], amax);
+    if (kFmt == ESTREAM_MX4_E8M0X32) amax = max_abs(__shfl_xor_sync(0xffffffffu, amax, 1), amax, 0.0f);
+    const bool finite = amax < __int_as_float(0x7f800000);
     uint8_t s;
     float d;
     if (kFmt == ESTREAM_MX4_E4M3X16) {
@@ -162,27 +197,33 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, 
         s = !finite ? 0xff : static_cast<uint8_t>(min(max(static_cast<int>(top >> 23) - 2, 1), 0xfe));
         d = __fmul_rn(e8m0_value(s), q.scale);
     }
-    uint32_t codes = 0;
+    uint2 codes = make_uint2(0, 0);
     if (finite && d > 0.0f) {
         // One reciprocal for the block. With d's and the block's exponents well inside
         // the range, the corrected quotient gives the division's code for every d and
-        // every x next to a rounding boundary of E2M1; its sign is x's, also for -0.
+        // every x next to a rounding boundary of E2M1.
         if (amax < 1e18f && d > 1e-18f && d < 1e18f) {
-            const float r = __frcp_rn(d);
+            const float nr = -__frcp_rn(d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = copysignf(quotient(v[j], d, r), v[j]);
+            for (int j = 0; j < kVals; j += 2) {
+                const float2 f = neg_quotient(make_float2(v[j], v[j + 1]), make_float2(d, d), make_float2(nr, nr));
+                v[j] = f.x;
+                v[j + 1] = f.y;
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], d);
+            for (int j = 0; j < kVals; ++j) v[j] = __fdiv_rn(-v[j], d);
         }
-#pragma unroll
-        for (int j = 0; j < 8; j += 2)
-            codes |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(v[j], v[j + 1]), __NV_E2M1, cudaRoundNearest))
-                     << (4 * j);
+        // the values are negated here, with SwiGLU twice
+        const uint32_t sign = kSwiglu ? 0u : 0x88888888u;
+        codes = make_uint2(e2m1_codes(v) ^ sign, e2m1_codes(v + 8) ^ sign);
     }
     if (!in) return;
-    reinterpret_cast<uint32_t*>(q.codes)[i] = codes;
-    if (group % kLanes == 0) q.scales[i / kLanes] = s;
+    reinterpret_cast<uint2*>(q.codes)[i] = codes;
+    if (kFmt == ESTREAM_MX4_E4M3X16)
+        q.scales[i] = s;
+    else if (group % 2 == 0)
+        q.scales[i / 2] = s;
 }
 
 template <int kElem, int kFmt>
@@ -234,8 +275,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_weight_scales(const uint8_t* _
     tiles[i] = n < N && b < nb ? scales[(p * N + n) * nb + b] : 0;
 }
 
-Tiling tile_rows(int R, int K, dim3& grid) {
-    Tiling t{mx4_padded(K) / 8, 0};
+Tiling tile_rows(int R, int K, int vals, dim3& grid) {
+    Tiling t{mx4_padded(K) / vals, 0};
     const int warps = (t.groups + 31) / 32;
     while (t.along < 3 && (2 << t.along) <= warps) ++t.along;
     const int down = kThreads / 32 >> t.along;
@@ -275,7 +316,7 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream) {
     if (q.R == 0) return cudaSuccess;
     dim3 grid;
-    const Tiling t = tile_rows(q.R, q.K, grid);
+    const Tiling t = tile_rows(q.R, q.K, kVals, grid);
     // 16-byte loads need every row (and the up half of it) on a 16-byte boundary
     const size_t b = elem_bytes(q.elem);
     const bool wide = on16(q.x) && q.ld * b % 16 == 0 && (!q.swiglu || q.K * b % 16 == 0);
@@ -289,7 +330,7 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
                                   cudaStream_t stream) {
     if (R == 0) return cudaSuccess;
     dim3 grid;
-    const Tiling t = tile_rows(R, K, grid);
+    const Tiling t = tile_rows(R, K, 8, grid);
     const bool wide = on16(out) && ld * elem_bytes(elem) % 16 == 0;
     if (elem == ESTREAM_MX4_BF16)
         return dequantize_elem<ESTREAM_MX4_BF16>(codes, scales, fmt, scale, R, K, t, out, ld, wide, grid, stream);
