@@ -48,24 +48,6 @@ struct Elem<ESTREAM_MX4_F32> {
     static __device__ __forceinline__ T down(float v) { return v; }
 };
 
-// Eight consecutive values from p (n of them inside the row, the rest zero);
-// wide loads when the row's values are 16-byte aligned.
-template <int kElem>
-__device__ __forceinline__ void load8(const typename Elem<kElem>::T* p, int n, bool wide, float* v) {
-    using T = typename Elem<kElem>::T;
-    if (wide && n >= 8) {
-        alignas(16) T t[8];
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-            reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = Elem<kElem>::up(t[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? Elem<kElem>::up(p[i]) : 0.0f;
-    }
-}
-
 // - x / d from nr = - 1 / d: a quotient, its exact remainder and one correction
 // (Markstein 1990). For finite operands away from the ends of the exponent range.
 // Two values an instruction, and negated throughout because a packed multiply-add
@@ -141,6 +123,7 @@ __device__ __forceinline__ float e8m0_value(uint8_t s) {
 struct Tiling {
     int groups;  // of a padded row
     int along;
+    __host__ __device__ __forceinline__ int rows() const { return kThreads / 32 >> along; }  // of a block
     __device__ __forceinline__ int row() const {
         return blockIdx.x * (kThreads / 32 >> along) + (threadIdx.x >> 5 >> along);
     }
@@ -151,79 +134,116 @@ struct Tiling {
 
 // Sixteen values a lane: a block of 16, or with its neighbour one of 32, so what
 // is done once a block (scale, reciprocal, addresses) is shared by as many values
-// as a lane's registers hold at full occupancy. A row is a whole number of
-// 32-value groups, so a block never spans rows.
-// Bound by issue slots with SwiGLU.
+// as fit a lane's registers. A row is a whole number of 32-value groups, so a block
+// never spans rows. A warp goes down its columns, the next row's values on their
+// way while it converts a row's.
 constexpr int kVals = 16;
+constexpr int kResident = 3;  // blocks an SM
 template <int kElem, bool kSwiglu, int kFmt>
-__global__ void __launch_bounds__(kThreads) k_mx4_quantize(const Mx4Quantize q, Tiling tiling, bool wide) {
+__global__ void __launch_bounds__(kThreads, kResident) k_mx4_quantize(const Mx4Quantize q, Tiling tiling, bool wide) {
     using T = typename Elem<kElem>::T;
-    const int row = tiling.row(), group = tiling.group(), c = group * kVals;
-    if (row >= q.R || group - static_cast<int>(threadIdx.x & 31) >= tiling.groups) return;  // the whole warp
+    constexpr int kRaw = kVals * sizeof(T) / 16;  // 16-byte words
+    const int group = tiling.group(), c = group * kVals, n = q.K - c;
+    if (group - static_cast<int>(threadIdx.x & 31) >= tiling.groups) return;  // the whole warp
     // a warp's lanes past the row's end stay for the shuffle
     const bool in = group < tiling.groups;
-    const size_t i = static_cast<size_t>(row) * tiling.groups + group;
-    const int src = q.rows ? q.rows[row] : row;
-    const bool have = in && src >= 0 && src < q.n_src;
-    float v[kVals];
-    if (have) {
-        const T* p = static_cast<const T*>(q.x) + static_cast<size_t>(src) * q.ld + c;
-        const int n = q.K - c;
+    const bool whole = wide && n >= kVals;
+    const int stride = tiling.rows() * gridDim.x;
+    // source row, or -1 past the end and for an index out of range
+    auto source = [&](int row) {
+        if (row >= q.R) return -1;
+        const int src = q.rows ? __ldg(q.rows + row) : row;
+        return src < q.n_src ? src : -1;
+    };
+    auto at = [&](int src) { return static_cast<const T*>(q.x) + static_cast<size_t>(src) * q.ld + c; };
+    uint4 raw[kSwiglu ? 2 : 1][kRaw];
+    auto fetch = [&](int src) {
+        if (!whole || src < 0) return;
 #pragma unroll
-        for (int j = 0; j < kVals; j += 8) load8<kElem>(p + j, n - j, wide, v + j);
-        if (kSwiglu) {
-            float u[kVals];
+        for (int h = 0; h < (kSwiglu ? 2 : 1); ++h)
 #pragma unroll
-            for (int j = 0; j < kVals; j += 8) load8<kElem>(p + q.K + j, n - j, wide, u + j);
-            neg_silu_mul(v, u);
+            for (int j = 0; j < kRaw; ++j)
+                raw[h][j] = __ldg(reinterpret_cast<const uint4*>(at(src) + (h ? q.K : 0)) + j);
+    };
+    // half h (gate, up) of the row fetched last
+    auto values = [&](int src, int h, float (&v)[kVals]) {
+        if (whole) {
+            const T* t = reinterpret_cast<const T*>(raw[h]);
+#pragma unroll
+            for (int j = 0; j < kVals; ++j) v[j] = Elem<kElem>::up(t[j]);
+        } else {
+            const T* p = at(src) + (h ? q.K : 0);
+#pragma unroll
+            for (int j = 0; j < kVals; ++j) v[j] = j < n ? Elem<kElem>::up(p[j]) : 0.0f;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVals; ++j) v[j] = in ? __int_as_float(0x7fc00000) : 0.0f;
-    }
-    float amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kVals; j += 2) amax = max_abs(v[j], v[j + 1], amax);
-    if (kFmt == ESTREAM_MX4_E8M0X32) amax = max_abs(__shfl_xor_sync(0xffffffffu, amax, 1), amax, 0.0f);
-    const bool finite = amax < __int_as_float(0x7f800000);
-    uint8_t s;
-    float d;
-    if (kFmt == ESTREAM_MX4_E4M3X16) {
-        s = finite ? __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.0f, q.scale)), __NV_SATFINITE, __NV_E4M3)
-                   : 0x7f;
-        d = __fmul_rn(e4m3_value(s), q.scale);
-    } else {
-        const uint32_t top = __float_as_uint(__fdiv_rn(amax, q.scale));
-        s = !finite ? 0xff : static_cast<uint8_t>(min(max(static_cast<int>(top >> 23) - 2, 1), 0xfe));
-        d = __fmul_rn(e8m0_value(s), q.scale);
-    }
-    uint2 codes = make_uint2(0, 0);
-    if (finite && d > 0.0f) {
-        // One reciprocal for the block. With d's and the block's exponents well inside
-        // the range, the corrected quotient gives the division's code for every d and
-        // every x next to a rounding boundary of E2M1.
-        if (amax < 1e18f && d > 1e-18f && d < 1e18f) {
-            const float nr = -__frcp_rn(d);
-#pragma unroll
-            for (int j = 0; j < kVals; j += 2) {
-                const float2 f = neg_quotient(make_float2(v[j], v[j + 1]), make_float2(d, d), make_float2(nr, nr));
-                v[j] = f.x;
-                v[j + 1] = f.y;
+    };
+    int row = tiling.row();
+    int src = source(row), next = source(row + stride);
+    fetch(src);
+    for (; row < q.R; row += stride) {
+        const size_t i = static_cast<size_t>(row) * tiling.groups + group;
+        float v[kVals];
+        if (in && src >= 0) {
+            values(src, 0, v);
+            if (kSwiglu) {
+                float u[kVals];
+                values(src, 1, u);
+                fetch(next);
+                neg_silu_mul(v, u);
+            } else {
+                fetch(next);
             }
         } else {
+            fetch(next);
 #pragma unroll
-            for (int j = 0; j < kVals; ++j) v[j] = __fdiv_rn(-v[j], d);
+            for (int j = 0; j < kVals; ++j) v[j] = in ? __int_as_float(0x7fc00000) : 0.0f;
         }
-        // the values are negated here, with SwiGLU twice
-        const uint32_t sign = kSwiglu ? 0u : 0x88888888u;
-        codes = make_uint2(e2m1_codes(v) ^ sign, e2m1_codes(v + 8) ^ sign);
+        src = next;
+        next = source(row + 2 * stride);
+        float amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVals; j += 2) amax = max_abs(v[j], v[j + 1], amax);
+        if (kFmt == ESTREAM_MX4_E8M0X32) amax = max_abs(__shfl_xor_sync(0xffffffffu, amax, 1), amax, 0.0f);
+        const bool finite = amax < __int_as_float(0x7f800000);
+        uint8_t s;
+        float d;
+        if (kFmt == ESTREAM_MX4_E4M3X16) {
+            s = finite ? __nv_cvt_float_to_fp8(__fdiv_rn(amax, __fmul_rn(6.0f, q.scale)), __NV_SATFINITE, __NV_E4M3)
+                       : 0x7f;
+            d = __fmul_rn(e4m3_value(s), q.scale);
+        } else {
+            const uint32_t top = __float_as_uint(__fdiv_rn(amax, q.scale));
+            s = !finite ? 0xff : static_cast<uint8_t>(min(max(static_cast<int>(top >> 23) - 2, 1), 0xfe));
+            d = __fmul_rn(e8m0_value(s), q.scale);
+        }
+        uint2 codes = make_uint2(0, 0);
+        if (finite && d > 0.0f) {
+            // One reciprocal for the block. With d's and the block's exponents well inside
+            // the range, the corrected quotient gives the division's code for every d and
+            // every x next to a rounding boundary of E2M1.
+            if (amax < 1e18f && d > 1e-18f && d < 1e18f) {
+                const float nr = -__frcp_rn(d);
+#pragma unroll
+                for (int j = 0; j < kVals; j += 2) {
+                    const float2 f = neg_quotient(make_float2(v[j], v[j + 1]), make_float2(d, d), make_float2(nr, nr));
+                    v[j] = f.x;
+                    v[j + 1] = f.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVals; ++j) v[j] = __fdiv_rn(-v[j], d);
+            }
+            // the values are negated here, with SwiGLU twice
+            const uint32_t sign = kSwiglu ? 0u : 0x88888888u;
+            codes = make_uint2(e2m1_codes(v) ^ sign, e2m1_codes(v + 8) ^ sign);
+        }
+        if (!in) continue;
+        reinterpret_cast<uint2*>(q.codes)[i] = codes;
+        if (kFmt == ESTREAM_MX4_E4M3X16)
+            q.scales[i] = s;
+        else if (group % 2 == 0)
+            q.scales[i / 2] = s;
     }
-    if (!in) return;
-    reinterpret_cast<uint2*>(q.codes)[i] = codes;
-    if (kFmt == ESTREAM_MX4_E4M3X16)
-        q.scales[i] = s;
-    else if (group % 2 == 0)
-        q.scales[i / 2] = s;
 }
 
 template <int kElem, int kFmt>
@@ -278,9 +298,12 @@ __global__ void __launch_bounds__(kThreads) k_mx4_weight_scales(const uint8_t* _
 Tiling tile_rows(int R, int K, int vals, dim3& grid) {
     Tiling t{mx4_padded(K) / vals, 0};
     const int warps = (t.groups + 31) / 32;
-    while (t.along < 3 && (2 << t.along) <= warps) ++t.along;
-    const int down = kThreads / 32 >> t.along;
-    grid = dim3((R + down - 1) / down, (warps + (1 << t.along) - 1) >> t.along);
+    // the widest block that leaves at most a sixteenth of its warps without columns
+    for (int a = 3; a > 0 && t.along == 0; --a) {
+        const int used = (warps + (1 << a) - 1) >> a << a;
+        if ((used - warps) * 16 <= used) t.along = a;
+    }
+    grid = dim3((R + t.rows() - 1) / t.rows(), (warps + (1 << t.along) - 1) >> t.along);
     return t;
 }
 
@@ -317,6 +340,11 @@ cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream) {
     if (q.R == 0) return cudaSuccess;
     dim3 grid;
     const Tiling t = tile_rows(q.R, q.K, kVals, grid);
+    int dev = 0, sms = 0;
+    cudaError_t rc = cudaGetDevice(&dev);
+    if (rc == cudaSuccess) rc = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (rc != cudaSuccess) return rc;
+    grid.x = std::min(grid.x, std::max(1u, sms * kResident / grid.y));  // what is resident at once
     // 16-byte loads need every row (and the up half of it) on a 16-byte boundary
     const size_t b = elem_bytes(q.elem);
     const bool wide = on16(q.x) && q.ld * b % 16 == 0 && (!q.swiglu || q.K * b % 16 == 0);
