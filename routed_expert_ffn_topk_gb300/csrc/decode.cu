@@ -154,9 +154,9 @@ __device__ void prepare_routes(const Routes& r, const DecodeCall& d) {
     if (threadIdx.x == 0 && d.E > kKeysE) r.counts[d.E] = 0;
 }
 
-// What a weight row of an expert with c tokens costs: 1 for streaming it, 1 for its
-// products with each tile of 8 tokens.
-__device__ __forceinline__ int row_weight(int c) { return c > 0 ? 1 + (c + 7) / 8 : 0; }
+// What a weight row of an expert with c tokens costs: its products with each tile
+// of 8 tokens, which take longer than streaming it (two tiles: 1.9 times one).
+__device__ __forceinline__ int row_weight(int c) { return (c + 7) / 8; }
 
 // Where part b of g of the chosen and shared experts' rows (len, len_sh each)
 // begins: parts of equal weight (OLMoE shape, 32 tokens: with parts of equal rows
@@ -236,7 +236,7 @@ __device__ void build_routes(const Routes& r, const DecodeCall& d, const float* 
             const int c = __popc(mask);
             const unsigned has = __ballot_sync(0xffffffffu, c > 0);
             const int w = row_weight(c);
-            int incl = c + (w << 16);  // (at most 1024 rows and 5 x 32 weights in a round)
+            int incl = c + (w << 16);  // (at most 1024 rows and 4 x 32 weights in a round)
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, incl, s);
