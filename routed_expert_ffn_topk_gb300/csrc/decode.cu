@@ -88,18 +88,18 @@ __device__ __forceinline__ void decode_leave(int* sync) {
     }
 }
 
-// One chosen expert, or a shared one after them.
+// Up to 8 tokens of a chosen expert, or of a shared one after them.
 struct Act {
-    uint32_t mask;  // bit t: token t goes to it
-    int row0;       // its first h row (one row a token, ascending t)
+    uint32_t mask;  // bit t: token t is one of them
+    int row0;       // the first one's h row (one row a token, ascending t)
     int slot;       // arena slot, or index among the shared experts
     float scale;    // 2^-s of its down weights
 };
 
 // The call's routes in shared memory, formed by every CTA for itself.
 struct Routes {
-    Act* act;          // [E + n_shared] experts with a token, ascending, then the shared ones
-    Act* expert;       // [E] every expert's entry
+    Act* act;          // [act_max] tiles of experts with a token, ascending, then of the shared ones
+    Act* expert;       // [E] every expert's entry, with all its tokens
     float* row_alpha;  // [T k] weight of each h row
     int* row_tok;      // [T k] its token
     int* ids;          // [T k] expert of each route; then, a token's h rows in ascending order
@@ -107,15 +107,18 @@ struct Routes {
     uint32_t* key;     // [T E] logits as ordered keys (E <= kKeysE)
     int* counts;       // [E + 1] (E > kKeysE)
     int* n_act;
-    int* cum;          // [n_act + n_shared + 1] weights of the experts before this one (split_at)
 };
 
 constexpr int kKeysE = 128;
 
+__host__ __device__ inline int shared_tiles(int T, int n_shared) { return n_shared * ((T + 7) / 8); }
+__host__ __device__ inline int act_max(int T, int k, int E, int n_shared) {
+    return E + T * k / 8 + shared_tiles(T, n_shared);
+}
 __host__ __device__ inline size_t routes_bytes(int T, int k, int E, int n_shared) {
     const size_t R = static_cast<size_t>(T) * k;
-    return (sizeof(Act) * (2 * static_cast<size_t>(E) + n_shared) +
-            sizeof(int) * (4 * R + (E <= kKeysE ? static_cast<size_t>(T) * E : static_cast<size_t>(E) + 1) + E + n_shared + 2) + 15) /
+    return (sizeof(Act) * (static_cast<size_t>(E) + act_max(T, k, E, n_shared)) +
+            sizeof(int) * (4 * R + (E <= kKeysE ? static_cast<size_t>(T) * E : static_cast<size_t>(E) + 1) + 1) + 15) /
            16 * 16;
 }
 
@@ -123,14 +126,13 @@ __device__ Routes routes_at(void* smem, int T, int k, int E, int n_shared) {
     const int R = T * k;
     Routes r;
     r.act = static_cast<Act*>(smem);
-    r.expert = r.act + E + n_shared;
+    r.expert = r.act + act_max(T, k, E, n_shared);
     r.row_alpha = reinterpret_cast<float*>(r.expert + E);
     r.row_tok = reinterpret_cast<int*>(r.row_alpha + R);
     r.ids = r.row_tok + R;
     r.alpha = reinterpret_cast<float*>(r.ids + R);
     r.n_act = reinterpret_cast<int*>(r.alpha + R);
-    r.cum = r.n_act + 1;
-    r.counts = r.cum + E + n_shared + 1;
+    r.counts = r.n_act + 1;
     r.key = reinterpret_cast<uint32_t*>(r.counts);
     return r;
 }
@@ -154,34 +156,20 @@ __device__ void prepare_routes(const Routes& r, const DecodeCall& d) {
     if (threadIdx.x == 0 && d.E > kKeysE) r.counts[d.E] = 0;
 }
 
-// What a weight row of an expert with c tokens costs: its products with each tile
-// of 8 tokens, which take longer than streaming it (two tiles: 1.9 times one).
-__device__ __forceinline__ int row_weight(int c) { return (c + 7) / 8; }
-
-// Where part b of g of the chosen and shared experts' rows (len, len_sh each)
-// begins: parts of equal weight (OLMoE shape, 32 tokens: with parts of equal rows
-// the groups on experts of more than 8 tokens ended 40 us after the median one).
-__device__ __forceinline__ int split_at(const Routes& r, int n_sh, int len, int len_sh, int step, int b, int g) {
-    const int n_act = *r.n_act, n = n_act + n_sh;
-    if (n == 0) return 0;
-    const unsigned own = r.cum[n_act];
-    auto before = [&](int e) {
-        const unsigned c = r.cum[e];
-        return min(c, own) * len + (max(c, own) - own) * len_sh;
-    };
-    const unsigned target = static_cast<unsigned>(static_cast<unsigned long long>(before(n)) * b / g);
-    int lo = 0, hi = n;  // before(lo) <= target; before(hi) > target or hi = n
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (before(mid) <= target) lo = mid; else hi = mid;
+// An expert's entry as tiles of up to 8 tokens.
+__device__ __forceinline__ void list_tiles(Act* act, Act a) {
+    for (uint32_t left = a.mask; left; ++act) {
+        uint32_t rest = left;
+        for (int i = 0; i < 8; ++i) rest &= rest - 1;
+        a.mask = left & ~rest;
+        *act = a;
+        a.row0 += 8;
+        left = rest;
     }
-    const int rows = lo < n_act ? len : len_sh;
-    const int in = static_cast<int>((target - before(lo)) / static_cast<unsigned>(r.cum[lo + 1] - r.cum[lo]));
-    return min(lo, n_act) * len + max(lo - n_act, 0) * len_sh + min(in, rows) / step * step;
 }
 
-// Which experts each token takes: the experts' token masks, the list of experts
-// in use and, with T <= 32, a token's row among its expert's rows as a count of
+// Which experts each token takes: the experts' token masks, the list of tiles of up
+// to 8 tokens of the experts in use and, with T <= 32, a token's row among its expert's rows as a count of
 // the mask's lower bits. A warp a token; up to kKeysE experts its keys stay in
 // four registers a lane, a round being the largest key and the lowest expert
 // that holds it. The weights of that form are left to route_weights, off the path
@@ -229,34 +217,30 @@ __device__ void build_routes(const Routes& r, const DecodeCall& d, const float* 
     }
     __syncthreads();
     if (warp == 0) {
-        int n = 0, rows = 0, weights = 0;
+        int n = 0, rows = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
             const uint32_t mask = e < E ? r.expert[e].mask : 0u;
             const int c = __popc(mask);
-            const unsigned has = __ballot_sync(0xffffffffu, c > 0);
-            const int w = row_weight(c);
-            int incl = c + (w << 16);  // (at most 1024 rows and 4 x 32 weights in a round)
+            int incl = c + (((c + 7) / 8) << 16);  // rows and tiles
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, incl, s);
                 if (lane >= s) incl += o;
             }
             if (c > 0) {
-                const int at = n + __popc(has & ((1u << lane) - 1u));
-                r.expert[e].row0 = rows + (incl & 0xffff) - c;
-                r.act[at] = r.expert[e];
-                r.cum[at] = weights + (incl >> 16) - w;
+                Act a = r.expert[e];
+                a.row0 = rows + (incl & 0xffff) - c;
+                r.expert[e].row0 = a.row0;
+                list_tiles(r.act + n + (incl >> 16) - (c + 7) / 8, a);
             }
-            n += __popc(has);
             const int all = __shfl_sync(0xffffffffu, incl, 31);
+            n += all >> 16;
             rows += all & 0xffff;
-            weights += all >> 16;
         }
         if (lane == 0) *r.n_act = n;
-        for (int j = lane; j <= d.n_shared; j += 32) r.cum[n + j] = weights + j * row_weight(T);
         for (int j = lane; j < d.n_shared; j += 32)
-            r.act[n + j] = {T == 32 ? 0xffffffffu : (1u << T) - 1u, j * T, j, d.sh_scale[j]};
+            list_tiles(r.act + n + shared_tiles(T, j), {T == 32 ? 0xffffffffu : (1u << T) - 1u, j * T, j, d.sh_scale[j]});
     }
     __syncthreads();
     for (int i = threadIdx.x; i < T * k; i += blockDim.x) {
@@ -338,7 +322,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
     __shared__ int ok_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int gw = blockIdx.x * nw + warp, gn = gridDim.x * nw;
-    const int H = d.H, F = d.F, Fs = d.F_shared, T = d.T, k = d.k;
+    const int H = d.H, F = d.F, Fs = d.F_shared, T = d.T, k = d.k, n_sh = shared_tiles(T, d.n_shared);
     const Routes r = routes_at(smem, T, k, d.E, d.n_shared);
     int gen = 0;
     bool ok = true;
@@ -349,7 +333,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
         __syncthreads();
         const int n_act = *r.n_act;
         const int routed = n_act * F;
-        for (int u = gw; u < routed + d.n_shared * Fs; u += gn) {
+        for (int u = gw; u < routed + n_sh * Fs; u += gn) {
             const bool sh = u >= routed;
             const int at = sh ? n_act + (u - routed) / Fs : u / F;
             const int f = sh ? (u - routed) % Fs : u % F;
@@ -384,7 +368,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
         for (int o = gw; o < H; o += gn)
             for (int t = 0; t < T; ++t) {
                 float y = 0.0f;
-                for (int at = 0; at < n_act + d.n_shared; ++at) {
+                for (int at = 0; at < n_act + n_sh; ++at) {
                     const Act a = r.act[at];
                     if (!((a.mask >> t) & 1u)) continue;
                     const bool sh = at >= n_act;
@@ -452,12 +436,11 @@ constexpr int kGroups = kWarps / kGroup;
 constexpr int kStreamThreads = 32 * kWarps;
 constexpr int kMaxStages = 6;
 
-// (4-bit rows are short, so a tile takes more of them where the accumulators
-// leave room)
-template <bool kQ4, int kNT>
+// (4-bit rows are short, so a tile takes more of them)
+template <bool kQ4>
 struct Stream {
-    static constexpr int kHRows = kQ4 && kNT == 1 ? 32 : 16;  // h rows of a gate/up tile
-    static constexpr int kYRows = kQ4 && kNT == 1 ? 32 : 16;  // Y rows of a down tile
+    static constexpr int kHRows = kQ4 ? 32 : 16;  // h rows of a gate/up tile
+    static constexpr int kYRows = kQ4 ? 32 : 16;  // Y rows of a down tile
     static constexpr int kStep = kQ4 ? 4 : 1;      // granularity of a range
     static constexpr int kHTiles = kHRows / 8;     // m16 tiles (8 gate + 8 up rows)
     static constexpr int kYTiles = kYRows / 16;
@@ -548,18 +531,17 @@ __device__ __forceinline__ int share(int total, int step, int part, int parts) {
     return static_cast<int>(units * part / parts) * step;
 }
 
-// kNT: token tiles of 8 that the accumulators have room for (T <= 8 kNT).
-template <bool kQ4, int kNT>
+// kByToken (T <= 8): the down projection's columns are the call's tokens.
+template <bool kQ4, bool kByToken>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const DecodeCall d, int stages) {
-    using S = Stream<kQ4, kNT>;
-    constexpr bool kByToken = kNT == 1;  // down projection: columns are the call's tokens
+    using S = Stream<kQ4>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kWarps * kMaxStages + 1];  // the last: the routes' weights are there
     __shared__ int ok_flag;
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int H = d.H, F = d.F, Fs = d.F_shared, T = d.T, k = d.k;
+    const int H = d.H, F = d.F, Fs = d.F_shared, T = d.T, k = d.k, n_sh = shared_tiles(T, d.n_shared);
     const int KB = H / 64, FB = F / 64, FsB = Fs / 64;
     const uint8_t* ring_p = smem_raw + warp * stages * S::kUnit;
     const uint32_t ring = smem_addr(ring_p);
@@ -588,30 +570,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
     }
     build_routes(r, d, d.W_r ? d.logits_out : d.logits);
     const int n_act = *r.n_act;
-    const int routed_h = n_act * F, routed_y = kByToken ? 0 : n_act * H;
+    const int routed_h = n_act * F, total_h = routed_h + n_sh * Fs;
     const int wg = warp % kGroup, group = blockIdx.x * kGroups + warp / kGroup;
     const int groups = gridDim.x * kGroups;
-    // h rows [h0, h1) of a group; Y rows [y0, y1): of Y itself, a CTA's, or of every
-    // (expert, Y) pair, a group's
-    int h0, h1, y0, y1;
-    if (kByToken) {
-        const int total = routed_h + d.n_shared * Fs;
-        h0 = share(total, S::kStep, group, groups);
-        h1 = share(total, S::kStep, group + 1, groups);
-        y0 = share(H, S::kStep, blockIdx.x, gridDim.x);
-        y1 = share(H, S::kStep, blockIdx.x + 1, gridDim.x);
-    } else {
-        // four bounds, a lane each
-        const bool y = lane & 2;
-        const int at = split_at(r, d.n_shared, y ? H : F, y ? H : Fs, S::kStep, group + (lane & 1), groups);
-        h0 = __shfl_sync(0xffffffffu, at, 0);
-        h1 = __shfl_sync(0xffffffffu, at, 1);
-        y0 = __shfl_sync(0xffffffffu, at, 2);
-        y1 = __shfl_sync(0xffffffffu, at, 3);
-    }
+    const int h0 = share(total_h, S::kStep, group, groups), h1 = share(total_h, S::kStep, group + 1, groups);
+    // Y rows: of Y itself, a range a CTA, or of every (tile, Y) pair, a range a group
+    const int routed_y = kByToken ? 0 : n_act * H;
+    const int total_y = kByToken ? H : routed_y + n_sh * H;
+    const int y_part = kByToken ? blockIdx.x : group, y_parts = kByToken ? gridDim.x : groups;
+    const int y0 = share(total_y, S::kStep, y_part, y_parts), y1 = share(total_y, S::kStep, y_part + 1, y_parts);
     constexpr int kYWarps = kByToken ? kWarps : kGroup;  // warps that share a Y tile
     const int wy = kByToken ? warp : wg;
-    const int YB = n_act * FB + d.n_shared * FsB;  // k-blocks of a Y row over all experts
+    const int YB = n_act * FB + n_sh * FsB;  // k-blocks of a Y row over all experts
     // Tiles of Y: one expert's rows, or (kByToken, at = 0) Y's own rows.
     auto start_y = [&](Walk<S::kYRows>& t) {
         if (kByToken) {
@@ -798,79 +768,64 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         const bool sh = t.shared();
         const Act act = r.act[t.at];
         const int cnt = __popc(act.mask), row0 = act.row0;
-        const int nt = (cnt + 7) / 8;
-        // the lane's token of each column tile; columns past the last token repeat
-        // it, and what they sum is not read
-        const uint4* xp[kNT];
-#pragma unroll
-        for (int j = 0; j < kNT; ++j) {
-            const int c = min(j * 8 + g, cnt - 1);
-            xp[j] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.X) +
-                                                   static_cast<size_t>(sh ? c : r.row_tok[row0 + c]) * H) + tq + wg * 8;
-        }
-        float acc[S::kHTiles][kNT][4];
-#pragma unroll
-        for (int m = 0; m < S::kHTiles; ++m)
-#pragma unroll
-            for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+        // the lane's token; columns past the last one repeat it, and what they sum is
+        // not read
+        const int col = min(g, cnt - 1);
+        const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(d.X) +
+                                                         static_cast<size_t>(sh ? __ffs(act.mask) - 1 + col : r.row_tok[row0 + col]) * H) +
+                          tq + wg * 8;
+        float acc[S::kHTiles][4] = {};
         uint4 x[2], more[2];
-        x[0] = __ldg(xp[0]);
-        x[1] = __ldg(xp[0] + 4);
+        x[0] = __ldg(xp);
+        x[1] = __ldg(xp + 4);
         for (int kb = wg, at = 0; kb < KB; kb += kGroup, at += kGroup * 8) {
             if (wait_full()) {
                 const uint8_t* u = ring_p + stage * S::kUnit;
+                // the next unit's X is fetched ahead
+                const uint4* np = xp + (kb + kGroup < KB ? at + kGroup * 8 : at);
+                more[0] = __ldg(np);
+                more[1] = __ldg(np + 4);
 #pragma unroll
-                for (int j = 0; j < kNT; ++j) {
-                    if (j >= nt) continue;
-                    // the next token tile's X, or the next unit's, is fetched ahead
-                    const uint4* np = xp[0] + (kb + kGroup < KB ? at + kGroup * 8 : at);
-                    if (j + 1 < kNT && j + 1 < nt) np = xp[(j + 1) % kNT] + at;
-                    more[0] = __ldg(np);
-                    more[1] = __ldg(np + 4);
+                for (int m = 0; m < S::kHTiles; ++m) {
+                    if (m > 0 && m * 8 >= t.n) continue;
+                    // a unit's sums join the running ones by rounded additions: the tensor
+                    // cores truncate, which over a long chain would bias the sum
+                    float part[2][4] = {};  // a chain for each column block
 #pragma unroll
-                    for (int m = 0; m < S::kHTiles; ++m) {
-                        if (m > 0 && m * 8 >= t.n) continue;
-                        // a unit's sums join the running ones by rounded additions: the tensor
-                        // cores truncate, which over a long chain would bias the sum
-                        float part[2][4] = {};  // a chain for each column block
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            uint32_t wg[4], wu[4];
-                            if (kQ4) {
-                                const uint8_t* p = u + b * (S::kHRows * 16) + (m * 8 + g) * 16 + tq * 4;
-                                const uint32_t qg = as<uint32_t>(p), qu = as<uint32_t>(p + S::kHPart);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    wg[i] = q4_pair(qg, i);
-                                    wu[i] = q4_pair(qu, i);
-                                }
-                            } else {
-                                const uint8_t* p = u + (m * 8 + g) * 128 + b * 64 + tq * 16;
-                                const uint4 vg = as<uint4>(p), vu = as<uint4>(p + S::kHPart);
-                                wg[0] = vg.x, wg[1] = vg.y, wg[2] = vg.z, wg[3] = vg.w;
-                                wu[0] = vu.x, wu[1] = vu.y, wu[2] = vu.z, wu[3] = vu.w;
-                            }
-                            mma_bf16(part[b], wg[0], wu[0], wg[1], wu[1], x[b].x, x[b].y);
-                            mma_bf16(part[b], wg[2], wu[2], wg[3], wu[3], x[b].z, x[b].w);
-                        }
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t wg[4], wu[4];
                         if (kQ4) {
-                            const uint8_t* p = u + S::kHRows * 32 + (m * 8 + g) * 4;
-                            const float2 sg = q4_scales(as<uint32_t>(p), false);
-                            const float2 su = q4_scales(as<uint32_t>(p + S::kHPart), false);
+                            const uint8_t* p = u + b * (S::kHRows * 16) + (m * 8 + g) * 16 + tq * 4;
+                            const uint32_t qg = as<uint32_t>(p), qu = as<uint32_t>(p + S::kHPart);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[m][j][i] = fmaf(part[0][i], i < 2 ? sg.x : su.x,
-                                                    fmaf(part[1][i], i < 2 ? sg.y : su.y, acc[m][j][i]));
+                            for (int i = 0; i < 4; ++i) {
+                                wg[i] = q4_pair(qg, i);
+                                wu[i] = q4_pair(qu, i);
+                            }
                         } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][i] + part[1][i];
+                            const uint8_t* p = u + (m * 8 + g) * 128 + b * 64 + tq * 16;
+                            const uint4 vg = as<uint4>(p), vu = as<uint4>(p + S::kHPart);
+                            wg[0] = vg.x, wg[1] = vg.y, wg[2] = vg.z, wg[3] = vg.w;
+                            wu[0] = vu.x, wu[1] = vu.y, wu[2] = vu.z, wu[3] = vu.w;
                         }
+                        mma_bf16(part[b], wg[0], wu[0], wg[1], wu[1], x[b].x, x[b].y);
+                        mma_bf16(part[b], wg[2], wu[2], wg[3], wu[3], x[b].z, x[b].w);
                     }
-                    x[0] = more[0];
-                    x[1] = more[1];
+                    if (kQ4) {
+                        const uint8_t* p = u + S::kHRows * 32 + (m * 8 + g) * 4;
+                        const float2 sg = q4_scales(as<uint32_t>(p), false);
+                        const float2 su = q4_scales(as<uint32_t>(p + S::kHPart), false);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[m][i] = fmaf(part[0][i], i < 2 ? sg.x : su.x,
+                                             fmaf(part[1][i], i < 2 ? sg.y : su.y, acc[m][i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][i] += part[0][i] + part[1][i];
+                    }
                 }
+                x[0] = more[0];
+                x[1] = more[1];
             }
             release();
         }
@@ -878,31 +833,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         const int len = sh ? Fs : F;
         __nv_bfloat16* hp = static_cast<__nv_bfloat16*>(sh ? d.h_shared : d.h);
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) {
-            if (j >= nt) continue;
-#pragma unroll
-            for (int m = 0; m < S::kHTiles; ++m) gather(acc[m][j], m);
-            sync_group();
-            copy_wait(weights_bar, 0, abort_flag, d.err);
-            // lane l's values 0, 1 are gate and 2, 3 up of columns 2 (l % 4), + 1
-            for (int i = tid_g; i < S::kHTiles * 64; i += 32 * kGroup) {
-                const int m = i >> 6, l = (i & 63) >> 1, hi = i & 1;
-                const int row = m * 8 + (l >> 2), f = t.row + row, c = j * 8 + (l & 3) * 2 + hi;
-                if (row >= t.n || c >= cnt) continue;
-                const std::integral_constant<int, kGroup> n{};
-                const float gate = reduced(w_g, n, m, l * 4 + hi), up = reduced(w_g, n, m, l * 4 + 2 + hi);
-                const float a = sh ? 1.0f : r.row_alpha[row0 + c];
-                const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
-                __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
-                const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
-                const float r1 = v - __bfloat162float(p0);
-                const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-                o[0] = p0;
-                o[len] = p1;
-                o[2 * len] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
-            }
-            turn ^= 1;
+        for (int m = 0; m < S::kHTiles; ++m) gather(acc[m], m);
+        sync_group();
+        copy_wait(weights_bar, 0, abort_flag, d.err);
+        // lane l's values 0, 1 are gate and 2, 3 up of columns 2 (l % 4), + 1
+        for (int i = tid_g; i < S::kHTiles * 64; i += 32 * kGroup) {
+            const int m = i >> 6, l = (i & 63) >> 1, hi = i & 1;
+            const int row = m * 8 + (l >> 2), f = t.row + row, c = (l & 3) * 2 + hi;
+            if (row >= t.n || c >= cnt) continue;
+            const std::integral_constant<int, kGroup> n{};
+            const float gate = reduced(w_g, n, m, l * 4 + hi), up = reduced(w_g, n, m, l * 4 + 2 + hi);
+            const float a = sh ? 1.0f : r.row_alpha[row0 + c];
+            const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
+            __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
+            const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
+            const float r1 = v - __bfloat162float(p0);
+            const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+            o[0] = p0;
+            o[len] = p1;
+            o[2 * len] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
         }
+        turn ^= 1;
     }
     // every h row of the call is written
     turn = 0;
@@ -915,22 +866,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         const int cnt = kByToken ? T : __popc(r.act[ty.at].mask);
         const int row_t = kByToken ? 0 : r.act[ty.at].row0;
         const int units = (kByToken ? YB : sh_t ? FsB : FB) / 2;
-        float acc[S::kYTiles][kNT][4];
-#pragma unroll
-        for (int m = 0; m < S::kYTiles; ++m)
-#pragma unroll
-            for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-        // Where the lane finds the h values of unit q for its column of token tile
-        // j: null for a token without the expert (kByToken); columns past the last
-        // token repeat it and are not read. l_len: 16-byte words of an h part.
+        float acc[S::kYTiles][4] = {};
+        // Where the lane finds the h values of unit q for its column: null for a token
+        // without the expert (kByToken); columns past the last token repeat it and are
+        // not read. l_len: 16-byte words of an h part.
         int l_a = 0, l_kb = 2 * wy;  // kByToken: expert and k-block of the next unit
         size_t l_len = (sh_t ? Fs : F) / 8;
-        auto h_at = [&](int q, int j) -> const uint4* {
+        auto h_at = [&](int q) -> const uint4* {
             if (!kByToken)
                 return static_cast<const uint4*>(sh_t ? d.h_shared : d.h) +
-                       static_cast<size_t>(row_t + min(j * 8 + g, cnt - 1)) * 3 * l_len + q * 16 + tq;
+                       static_cast<size_t>(row_t + min(g, cnt - 1)) * 3 * l_len + q * 16 + tq;
             if (q >= units) return nullptr;
             for (int n = l_a >= n_act ? FsB : FB; l_kb >= n; n = l_a >= n_act ? FsB : FB) {
                 l_kb -= n;
@@ -951,7 +896,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                 for (int b = 0; b < 2; ++b) x[q3][b] = p ? __ldcg(p + q3 * len + b * 4) : make_uint4(0, 0, 0, 0);
         };
         uint4 xa[3][2], xb[3][2];  // h values of a unit's first and second k-block, loaded one ahead
-        const uint4* hp = wy < units ? h_at(wy, 0) : nullptr;
+        const uint4* hp = wy < units ? h_at(wy) : nullptr;
         load_h(hp, l_len, xa);
         for (int q = wy; q < units; q += kYWarps) {
             const bool full = wait_full();
@@ -961,7 +906,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                 if (half == 0) {
                     load_h(hp ? hp + 8 : nullptr, l_len, xb);
                 } else {
-                    hp = q + kYWarps < units ? h_at(q + kYWarps, 0) : nullptr;
+                    hp = q + kYWarps < units ? h_at(q + kYWarps) : nullptr;
                     load_h(hp, l_len, xa);
                 }
                 if (!full) continue;
@@ -986,61 +931,52 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                                 w[m][b][6 + hi] = half2_to_bf162(v.w);
                             }
                         }
+                float part[2][S::kYTiles][4] = {};  // a chain for each column block
 #pragma unroll
-                for (int j = 0; j < kNT; ++j) {
-                    if (8 * j >= cnt) continue;
-                    if (j > 0) load_h(h_at(q, j) + half * 8, l_len, x);
-                    float part[2][S::kYTiles][4] = {};  // a chain for each column block
+                for (int q3 = 0; q3 < 3; ++q3)
 #pragma unroll
-                    for (int q3 = 0; q3 < 3; ++q3)
+                    for (int m = 0; m < S::kYTiles; ++m)
 #pragma unroll
-                        for (int m = 0; m < S::kYTiles; ++m)
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                mma_bf16(part[b][m], w[m][b][0], w[m][b][1], w[m][b][2], w[m][b][3], x[q3][b].x, x[q3][b].y);
-                                mma_bf16(part[b][m], w[m][b][4], w[m][b][5], w[m][b][6], w[m][b][7], x[q3][b].z, x[q3][b].w);
-                            }
-#pragma unroll
-                    for (int m = 0; m < S::kYTiles; ++m) {
-                        if (kQ4) {
-                            const uint8_t* p = u + S::kYRows * 32 + (m * 16 + g) * 4;
-                            const float2 lo = q4_scales(as<uint32_t>(p), true), hi = q4_scales(as<uint32_t>(p + 32), true);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[m][j][i] = fmaf(part[0][m][i], i < 2 ? lo.x : hi.x,
-                                                    fmaf(part[1][m][i], i < 2 ? lo.y : hi.y, acc[m][j][i]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[m][j][i] += part[0][m][i] + part[1][m][i];
+                        for (int b = 0; b < 2; ++b) {
+                            mma_bf16(part[b][m], w[m][b][0], w[m][b][1], w[m][b][2], w[m][b][3], x[q3][b].x, x[q3][b].y);
+                            mma_bf16(part[b][m], w[m][b][4], w[m][b][5], w[m][b][6], w[m][b][7], x[q3][b].z, x[q3][b].w);
                         }
+#pragma unroll
+                for (int m = 0; m < S::kYTiles; ++m) {
+                    if (kQ4) {
+                        const uint8_t* p = u + S::kYRows * 32 + (m * 16 + g) * 4;
+                        const float2 lo = q4_scales(as<uint32_t>(p), true), hi = q4_scales(as<uint32_t>(p + 32), true);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[m][i] = fmaf(part[0][m][i], i < 2 ? lo.x : hi.x,
+                                             fmaf(part[1][m][i], i < 2 ? lo.y : hi.y, acc[m][i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][i] += part[0][m][i] + part[1][m][i];
                     }
                 }
             }
             release();
         }
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) {
-            if (8 * j >= cnt) continue;
-#pragma unroll
-            for (int m = 0; m < S::kYTiles; ++m) gather(acc[m][j], m);
-            if (kByToken)
-                __syncthreads();
-            else
-                sync_group();
-            for (int i = kByToken ? threadIdx.x : tid_g; i < S::kYTiles * 128; i += 32 * kYWarps) {
-                const int m = i >> 7, l = (i & 127) >> 2, v = i & 3;
-                const int row = m * 16 + (l >> 2) + (v >> 1) * 8, c = j * 8 + (l & 3) * 2 + (v & 1);
-                if (row >= ty.n || c >= cnt || *abort_flag) continue;
-                const float y = reduced(kByToken ? 0 : w_g, std::integral_constant<int, kYWarps>{}, m, i & 127);
-                if (kByToken) {
-                    const size_t at = static_cast<size_t>(c) * H + ty.row + row;
-                    d.Y[at] = (d.A ? x_at<ESTREAM_BF16>(d.A, at) : d.Y[at]) + y;
-                } else {
-                    (sh_t ? d.y_shared : d.y_rows)[static_cast<size_t>(row_t + c) * H + ty.row + row] = y;
-                }
+        for (int m = 0; m < S::kYTiles; ++m) gather(acc[m], m);
+        if (kByToken)
+            __syncthreads();
+        else
+            sync_group();
+        for (int i = kByToken ? threadIdx.x : tid_g; i < S::kYTiles * 128; i += 32 * kYWarps) {
+            const int m = i >> 7, l = (i & 127) >> 2, v = i & 3;
+            const int row = m * 16 + (l >> 2) + (v >> 1) * 8, c = (l & 3) * 2 + (v & 1);
+            if (row >= ty.n || c >= cnt || *abort_flag) continue;
+            const float y = reduced(kByToken ? 0 : w_g, std::integral_constant<int, kYWarps>{}, m, i & 127);
+            if (kByToken) {
+                const size_t at = static_cast<size_t>(c) * H + ty.row + row;
+                d.Y[at] = (d.A ? x_at<ESTREAM_BF16>(d.A, at) : d.Y[at]) + y;
+            } else {
+                (sh_t ? d.y_shared : d.y_rows)[static_cast<size_t>(row_t + c) * H + ty.row + row] = y;
             }
-            turn ^= 1;
         }
+        turn ^= 1;
     }
     if (!kByToken) {
         if (live) live = decode_barrier(d.sync, ++gen, d.err, &ok_flag, *abort_flag != 0);
@@ -1084,15 +1020,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
 
 }  // namespace
 
-template <bool kQ4, int kNT>
+template <bool kQ4, bool kByToken>
 static cudaError_t launch_stream(const DecodeCall& d, int num_sms, cudaStream_t stream) {
-    using S = Stream<kQ4, kNT>;
+    using S = Stream<kQ4>;
     // the ring takes what the sums and the routes leave of 227 KB (static part: 1 KB)
     const size_t fixed = sizeof(float) * S::kRed + routes_bytes(d.T, d.k, d.E, d.n_shared);
     const int stages = static_cast<int>(std::min<size_t>(kMaxStages, (226 * 1024 - fixed) / (kWarps * S::kUnit)));
     if (stages < 2) return cudaErrorInvalidConfiguration;
     const size_t smem = static_cast<size_t>(stages) * kWarps * S::kUnit + fixed;
-    const void* fn = reinterpret_cast<const void*>(k_layer_decode<kQ4, kNT>);
+    const void* fn = reinterpret_cast<const void*>(k_layer_decode<kQ4, kByToken>);
     cudaError_t rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
     DecodeCall call = d;
@@ -1102,12 +1038,12 @@ static cudaError_t launch_stream(const DecodeCall& d, int num_sms, cudaStream_t 
 }
 
 cudaError_t launch_layer_decode(const DecodeCall& d, int wdtype, int num_sms, cudaStream_t stream) {
-    // up to 8 tokens the accumulators of one token tile suffice
+    // up to 8 tokens fill the 8 columns of a product
     const bool few = d.T <= 8;
     if (wdtype == ESTREAM_BF16)
-        return few ? launch_stream<false, 1>(d, num_sms, stream) : launch_stream<false, 4>(d, num_sms, stream);
+        return few ? launch_stream<false, true>(d, num_sms, stream) : launch_stream<false, false>(d, num_sms, stream);
     if (wdtype == ESTREAM_Q4)
-        return few ? launch_stream<true, 1>(d, num_sms, stream) : launch_stream<true, 4>(d, num_sms, stream);
+        return few ? launch_stream<true, true>(d, num_sms, stream) : launch_stream<true, false>(d, num_sms, stream);
     const size_t smem = routes_bytes(d.T, d.k, d.E, d.n_shared);
     const void* fn = reinterpret_cast<const void*>(k_layer_decode_simple);
     if (smem > 47 * 1024) {
