@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_mx4_quantize(const Mx4Q
         } else {
             fetch(next);
 #pragma unroll
-            for (int j = 0; j < kVals; ++j) v[j] = in ? __int_as_float(0x7fc00000) : 0.0f;
+            for (int j = 0; j < kVals; ++j) v[j] = in && n > 0 ? __int_as_float(0x7fc00000) : 0.0f;
         }
         src = next;
         next = source(row + 2 * stride);

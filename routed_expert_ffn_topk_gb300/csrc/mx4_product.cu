@@ -9,6 +9,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "estream_internal.h"
 
@@ -844,11 +845,13 @@ cudaError_t launch_pair(const Mx4Product& p, cudaStream_t stream) {
         codes_map(&tm_x, p.xc, p.K, static_cast<size_t>(p.R), 128) != CUDA_SUCCESS ||
         encode_tmap_2d(&tm_s, CU_TENSOR_MAP_DATA_TYPE_UINT32, p.wt, 128, tiles_s, 512, 128, 4, false) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    // x scales and out by TMA where rows start on 16-byte boundaries
+    // x scales and out by TMA where rows start on 16-byte boundaries; out's also have
+    // to end on one (a store fills the 16 bytes that its last column begins)
     const int nb = mx4_padded(p.K) / mx4_block(p.fmt);
     const bool f32 = p.elem == ESTREAM_MX4_F32;
     const bool tma_xs = nb % 16 == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0;
-    const bool tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld * (f32 ? 4 : 2) % 16 == 0;
+    const bool tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld * (f32 ? 4 : 2) % 16 == 0 &&
+                         p.N * (f32 ? 4 : 2) % 16 == 0;
     tm_xs = tm_out = tm_x;
     if (tma_xs && encode_tmap_2d(&tm_xs, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.xs, nb, static_cast<uint64_t>(p.R), nb, 16, 128,
                                  false) != CUDA_SUCCESS)
@@ -864,7 +867,16 @@ cudaError_t launch_pair(const Mx4Product& p, cudaStream_t stream) {
     cudaError_t rc = cudaFuncSetAttribute(k_mx4_product_pair, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
-    const int most = max_pairs(smem);
+    int dev = 0;
+    rc = cudaGetDevice(&dev);
+    if (rc != cudaSuccess) return rc;
+    // the query takes as long as a small launch, so a device's answer is kept
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    const bool keep = prefix == 0 && dev < kDevices;
+    int most = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (most == 0) most = max_pairs(smem);
+    if (keep && most > 0) known[dev].store(most, std::memory_order_relaxed);
     if (most < 1) return cudaErrorInvalidConfiguration;
     const long long tiles = (static_cast<long long>(p.R) / 256 + p.P) * ((p.N + 255) / 256);
     const int pairs = static_cast<int>(std::min<long long>(most, tiles));
