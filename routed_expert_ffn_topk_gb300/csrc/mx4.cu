@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "estream_internal.h"
+#include "overlap.cuh"
 
 namespace es {
 namespace {
@@ -143,6 +144,7 @@ template <int kElem, bool kSwiglu, int kFmt>
 __global__ void __launch_bounds__(kThreads, kResident) k_mx4_quantize(const Mx4Quantize q, Tiling tiling, bool wide) {
     using T = typename Elem<kElem>::T;
     constexpr int kRaw = kVals * sizeof(T) / 16;  // 16-byte words
+    after_previous();
     const int group = tiling.group(), c = group * kVals, n = q.K - c;
     if (group - static_cast<int>(threadIdx.x & 31) >= tiling.groups) return;  // the whole warp
     // a warp's lanes past the row's end stay for the shuffle
@@ -253,6 +255,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const uint32_t* __r
                                                              long long ld, bool wide) {
     using T = typename Elem<kElem>::T;
     constexpr int kLanes = kFmt == ESTREAM_MX4_E4M3X16 ? 2 : 4;
+    after_previous();
     const int row = tiling.row(), group = tiling.group(), c = group * 8;
     if (row >= R || group >= tiling.groups) return;
     const size_t i = static_cast<size_t>(row) * tiling.groups + group;
@@ -310,10 +313,8 @@ Tiling tile_rows(int R, int K, int vals, dim3& grid) {
 template <int kElem, bool kSwiglu>
 cudaError_t quantize_fmt(const Mx4Quantize& q, const Tiling& t, bool wide, dim3 grid, cudaStream_t s) {
     if (q.fmt == ESTREAM_MX4_E4M3X16)
-        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(q, t, wide);
-    else
-        k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(q, t, wide);
-    return cudaGetLastError();
+        return launch_overlapped(k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E4M3X16>, grid, kThreads, 0, s, q, t, wide);
+    return launch_overlapped(k_mx4_quantize<kElem, kSwiglu, ESTREAM_MX4_E8M0X32>, grid, kThreads, 0, s, q, t, wide);
 }
 template <int kElem>
 cudaError_t quantize_elem(const Mx4Quantize& q, const Tiling& t, bool wide, dim3 grid, cudaStream_t s) {
@@ -325,10 +326,8 @@ cudaError_t dequantize_elem(const uint8_t* codes, const uint8_t* scales, int fmt
                             const Tiling& t, void* out, long long ld, bool wide, dim3 grid, cudaStream_t s) {
     const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
     if (fmt == ESTREAM_MX4_E4M3X16)
-        k_mx4_dequantize<kElem, ESTREAM_MX4_E4M3X16><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, t, out, ld, wide);
-    else
-        k_mx4_dequantize<kElem, ESTREAM_MX4_E8M0X32><<<grid, kThreads, 0, s>>>(c, scales, g, R, K, t, out, ld, wide);
-    return cudaGetLastError();
+        return launch_overlapped(k_mx4_dequantize<kElem, ESTREAM_MX4_E4M3X16>, grid, kThreads, 0, s, c, scales, g, R, K, t, out, ld, wide);
+    return launch_overlapped(k_mx4_dequantize<kElem, ESTREAM_MX4_E8M0X32>, grid, kThreads, 0, s, c, scales, g, R, K, t, out, ld, wide);
 }
 
 size_t elem_bytes(int elem) { return elem == ESTREAM_MX4_F32 ? 4 : 2; }

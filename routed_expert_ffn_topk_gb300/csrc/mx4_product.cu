@@ -12,6 +12,7 @@
 #include <atomic>
 
 #include "estream_internal.h"
+#include "overlap.cuh"
 
 namespace es {
 namespace {
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
         tmem_relinquish();
     }
     tc_fence_before();
+    after_previous();
     tile_prefix(p, NT, base, sums);  // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
@@ -432,6 +434,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
             });
     }
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
@@ -587,6 +590,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __gr
         tmem_relinquish_pair();
     }
     tc_fence_before();
+    after_previous();
     tile_prefix(p, 256, base, sums);
     cluster_sync();
     tc_fence_after();
@@ -881,16 +885,17 @@ cudaError_t launch_pair(const Mx4Product& p, cudaStream_t stream) {
     const long long tiles = (static_cast<long long>(p.R) / 256 + p.P) * ((p.N + 255) / 256);
     const int pairs = static_cast<int>(std::min<long long>(most, tiles));
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 2;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1] = overlapped();
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_mx4_product_pair, tm_w, tm_x, tm_s, tm_xs, tm_out, p, stages, tma_xs, tma_out);
 }
 
@@ -914,8 +919,7 @@ cudaError_t launch_mma(const Mx4Product& p, cudaStream_t stream) {
     // at most one ragged row tile a slot
     const long long tiles = (static_cast<long long>(p.R) / NT + p.P) * ((p.N + 127) / 128);
     const int grid = static_cast<int>(std::min<long long>(sms, std::max(1ll, tiles)));
-    k_mx4_product<NT><<<grid, kMmaThreads, smem, stream>>>(tm_w, tm_x, p, stages);
-    return cudaGetLastError();
+    return launch_overlapped(k_mx4_product<NT>, dim3(grid), kMmaThreads, smem, stream, tm_w, tm_x, p, stages);
 }
 
 }  // namespace
