@@ -46,6 +46,11 @@ __device__ int g_mx4_err;
 // (row r of 128: lane r % 32, byte group r / 32). The issuing thread copies
 // scales to tensor memory with tcgen05.cp ahead of the products that use them;
 // both run in its issue order, and two column sets alternate.
+// Bound by HBM (the weights) and by latency: 1 x 14336 x 4096 streams its 33 MB at
+// 6 TB/s for 5.5 us, after 2.5 us until the first stage is there (12 us a call back
+// to back, of 4.9 at HBM's rate); 64 slots of 128 rows, 2048 x 2048, take 43 us of 29,
+// the tensor pipe 22% busy, with 6 us of it the epilogue's 2-byte stores down a column
+// (weights are M, so a thread holds a column of D).
 // ---------------------------------------------------------------------------
 
 constexpr int kMmaThreads = 320;  // producer, MMA, 4 epilogue and 4 scale warps
@@ -458,7 +463,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
 // One 256-column accumulator and the scales fill tensor memory, so the epilogue
 // is not hidden behind the next tile; its eight warps first drain the accumulator
 // into registers, 128 columns a thread (the roles' registers are split for that),
-// and scale and store afterwards.
+// and scale and store afterwards. 4096 x 14336 x 4096: 100 us back to back,
+// 4.8 PFLOP/s, of 61 at the rate of 256 x 256 x 64 products back to back (128 clocks).
 // ---------------------------------------------------------------------------
 
 // Warpgroups: producer and MMA warps; two of epilogue warps; scale warps. At 128
@@ -926,9 +932,19 @@ cudaError_t launch_mma(const Mx4Product& p, cudaStream_t stream) {
 
 cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t stream) {
     if (p.R == 0 || p.N == 0) return cudaSuccess;
+    // Rows a slot decide (K = 2048, N = 2048 with 64 slots of uneven rows, us a call):
+    //   rows   pairs  128  64        one slot, 14336 x 4096:  pairs  128   64
+    //   256      63    68             192                      14.9  18.4
+    //   192      56.5  56.7           160                      16.6  20.4
+    //   160      54    50             128                      16.5  14.4
+    //   128      52    45             64                             11.3  11.2
+    //   64       -     35   39        32                             13.4  11.0
+    //   32       -     31   33
+    // With several slots some hold more than the mean, and a tile of 64 rows then
+    // reads their weights twice.
     const long long per = p.R / p.P;
     if (per >= 192) return launch_pair(p, stream);
-    if (per > 64) return launch_mma<128>(p, stream);
+    if (per > (p.P == 1 ? 64 : 31)) return launch_mma<128>(p, stream);
     return launch_mma<64>(p, stream);
 }
 
