@@ -872,11 +872,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
     }
     // every h row of the call is written
     turn = 0;
-    live = decode_barrier(d.sync, ++gen, d.err, &ok_flag,
-                          *abort_flag || ((d.withhold & 2) && blockIdx.x == 0));
+    const bool met = decode_barrier(d.sync, ++gen, d.err, &ok_flag,
+                                    *abort_flag || ((d.withhold & 2) && blockIdx.x == 0));
+    live = live && met;
     Walk<S::kYRows> ty;
     start_y(ty);
-    for (; live && ty.left > 0; next_y(ty)) {
+    // (met is the CTA's, live the warp's own: every warp passes every barrier below)
+    for (; met && ty.left > 0; next_y(ty)) {
         const bool sh_t = !kByToken && ty.shared();
         const int cnt = kByToken ? T : __popc(r.act[ty.at].mask);
         const int row_t = kByToken ? 0 : r.act[ty.at].row0;
@@ -994,10 +996,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         turn ^= 1;
     }
     if (!kByToken) {
-        if (live) live = decode_barrier(d.sync, ++gen, d.err, &ok_flag, *abort_flag != 0);
+        const bool summed = met && decode_barrier(d.sync, ++gen, d.err, &ok_flag, *abort_flag != 0);
         // Y[t] = A[t] (or Y[t]) + the token's routes in ascending expert order + the shared experts
         const int n4 = T * (H / 4);
-        for (int i = blockIdx.x * kStreamThreads + threadIdx.x; live && i < n4; i += gridDim.x * kStreamThreads) {
+        for (int i = blockIdx.x * kStreamThreads + threadIdx.x; summed && i < n4; i += gridDim.x * kStreamThreads) {
             const int t = i / (H / 4), c = (i - t * (H / 4)) * 4;
             float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             auto add = [&](const float* rows, size_t row) {
