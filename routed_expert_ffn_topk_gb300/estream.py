@@ -582,20 +582,44 @@ class Mx4:
             raise ValueError("codes and scales must be on one CUDA device")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes and scales must be contiguous")
-        self.codes, self.scales, self.K, self.fmt, self.scale = codes, scales, K, fmt, float(scale)
+        self.K, self.fmt, self.scale, self.device = K, fmt, float(scale), codes.device
+        self._codes, self._scales, self._buf, self._R = codes, scales, None, R
 
     @classmethod
     def _empty(cls, R, K, Kp, b, fmt, scale, device):
-        """Uninitialised rows, of sizes already checked."""
+        """Uninitialised rows, of sizes already checked: one allocation, the codes and
+        then the scales, which become tensors when they are asked for (an operation
+        of PyTorch costs the host as long as a launch)."""
         q = cls.__new__(cls)
-        q.codes = torch.empty((R, Kp // 2), dtype=torch.uint8, device=device)
-        q.scales = torch.empty((R, Kp // b), dtype=torch.uint8, device=device)
-        q.K, q.fmt, q.scale = K, fmt, float(scale)
+        q._buf = torch.empty(R * (Kp // 2 + Kp // b), dtype=torch.uint8, device=device)
+        q._codes = q._scales = None
+        q.K, q.fmt, q.scale, q.device, q._R = K, fmt, float(scale), device, R
         return q
 
     @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            row = mx4_padded(self.K) // 2
+            self._codes = self._buf[:self._R * row].view(self._R, row)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            Kp = mx4_padded(self.K)
+            self._scales = self._buf[self._R * (Kp // 2):].view(self._R, Kp // mx4_block(self.fmt))
+        return self._scales
+
+    def _ptrs(self):
+        """Addresses of the codes and the scales."""
+        if self._buf is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        p = self._buf.data_ptr()
+        return p, p + self._R * (mx4_padded(self.K) // 2)
+
+    @property
     def shape(self):
-        return self.codes.shape[0], self.K
+        return self._R, self.K
 
 
 class Mx4Weights:
@@ -646,13 +670,14 @@ def mx4_quantize(x: torch.Tensor, fmt: int, scale: float = 1.0, rows: torch.Tens
         R, rp = rows.numel(), _dptr(rows)
     if out is None:
         out = Mx4._empty(R, K, mx4_padded(K), b, fmt, scale, dev)
-    elif out.shape != (R, K) or out.fmt != fmt or out.codes.device != dev:
+    elif out.shape != (R, K) or out.fmt != fmt or out.device != dev:
         raise ValueError(f"out must hold {R} rows of {K} in this format on x's device")
     else:
         out.scale = float(scale)
+    cp, sp = out._ptrs()
     with _on(x):
         st = lib().estream_mx4_quantize(x.data_ptr(), elem, ld, n, R, K, rp, 1 if swiglu else 0, fmt, out.scale,
-                                        out.codes.data_ptr(), out.scales.data_ptr(), _stream(stream, dev))
+                                        cp, sp, _stream(stream, dev))
     if st:
         _check(st, "estream_mx4_quantize")
     return out
@@ -660,8 +685,7 @@ def mx4_quantize(x: torch.Tensor, fmt: int, scale: float = 1.0, rows: torch.Tens
 
 def mx4_dequantize(q: Mx4, dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [R, K] that quantised rows stand for (bf16, fp16 or fp32)."""
-    codes = q.codes
-    R, K, dev = codes.shape[0], q.K, codes.device
+    R, K, dev = q._R, q.K, q.device
     if out is None:
         out, ld = torch.empty((R, K), dtype=dtype, device=dev), K
     else:
@@ -671,8 +695,9 @@ def mx4_dequantize(q: Mx4, dtype=torch.float32, out: torch.Tensor | None = None,
     elem = _MX4_ELEM.get(out.dtype)
     if elem is None:
         raise ValueError("out must be bf16, fp16 or fp32")
-    with _on(codes):
-        st = lib().estream_mx4_dequantize(codes.data_ptr(), q.scales.data_ptr(), q.fmt, q.scale, R, K,
+    cp, sp = q._ptrs()
+    with _on(out):
+        st = lib().estream_mx4_dequantize(cp, sp, q.fmt, q.scale, R, K,
                                           out.data_ptr(), elem, ld, _stream(stream, dev))
     if st:
         _check(st, "estream_mx4_dequantize")
@@ -707,8 +732,7 @@ def mx4_product(x: Mx4, w: Mx4Weights, offsets: torch.Tensor | None = None, out:
     """x [R, K] times w [P, N, K] transposed, both quantised in one format:
     [R, N] in bf16 or fp32. With offsets [P + 1] int32 (a route map's), rows
     [offsets[p], offsets[p + 1]) meet w[p], and rows outside every slot are zero."""
-    codes, K = x.codes, x.K
-    R, dev = codes.shape[0], codes.device
+    R, K, dev = x._R, x.K, x.device
     P, N = w.codes.shape[:2]
     if K != w.K or x.fmt != w.fmt or w.codes.device != dev:
         raise ValueError("x and w must have one width and format, on one device")
@@ -726,8 +750,9 @@ def mx4_product(x: Mx4, w: Mx4Weights, offsets: torch.Tensor | None = None, out:
         ld = _row_stride(out, "out")
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out must be bf16 or fp32")
-    with _on(codes):
-        st = lib().estream_mx4_product(codes.data_ptr(), x.scales.data_ptr(), R, w.codes.data_ptr(),
+    cp, sp = x._ptrs()
+    with _on(out):
+        st = lib().estream_mx4_product(cp, sp, R, w.codes.data_ptr(),
                                        w.tiles.data_ptr(), P, N, K, x.fmt, x.scale * w.scale, op, out.data_ptr(),
                                        _MX4_ELEM[out.dtype], ld, _stream(stream, dev))
     if st:
