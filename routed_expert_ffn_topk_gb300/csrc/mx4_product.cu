@@ -734,36 +734,48 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx4_product_pair(const __gr
             aph ^= 1u;
             tc_fence_after();
             const int row0 = w.row + quad * 32, rows = w.end - row0, n = w.n0 + half * 128;
-            uint32_t v[4][32];
-            if (rows > 0) {
+            auto drained = [&] {  // the accumulator is read: the next tile may have it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_smem_release(release);
+            };
+            if (rows <= 0) {
+                drained();
+                continue;
+            }
+            if (f32) {
+                uint32_t v[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(acc + c * 32, v[c]);
                 tmem_ld_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote_smem_release(release);
-            if (rows <= 0) continue;
+                drained();
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) v[c][x] = __float_as_uint(__uint_as_float(v[c][x]) * p.scale);
-            if (f32) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int x = 0; x < 32; ++x) v[c][x] = __float_as_uint(__uint_as_float(v[c][x]) * p.scale);
                     if (n + c * 32 < p.N) write_rows<float>(p, &tm_out, stage, v[c], lane, row0, rows, n + c * 32, tma_out);
+                }
             } else {
+                uint32_t t[2][32];  // 64 columns each
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t t[32];  // 64 columns
+                    uint32_t v[2][32];
+                    tmem_ld32(acc + c * 64, v[0]);
+                    tmem_ld32(acc + c * 64 + 32, v[1]);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
-                        const __nv_bfloat162 q = __floats2bfloat162_rn(
-                            __uint_as_float(v[2 * c + x / 16][x % 16 * 2]), __uint_as_float(v[2 * c + x / 16][x % 16 * 2 + 1]));
-                        t[x] = *reinterpret_cast<const uint32_t*>(&q);
+                        const __nv_bfloat162 q =
+                            __floats2bfloat162_rn(__uint_as_float(v[x / 16][x % 16 * 2]) * p.scale,
+                                                  __uint_as_float(v[x / 16][x % 16 * 2 + 1]) * p.scale);
+                        t[c][x] = *reinterpret_cast<const uint32_t*>(&q);
                     }
-                    if (n + c * 64 < p.N) write_rows<__nv_bfloat16>(p, &tm_out, stage, t, lane, row0, rows, n + c * 64, tma_out);
                 }
+                drained();
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (n + c * 64 < p.N)
+                        write_rows<__nv_bfloat16>(p, &tm_out, stage, t[c], lane, row0, rows, n + c * 64, tma_out);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stage outlives its stores
