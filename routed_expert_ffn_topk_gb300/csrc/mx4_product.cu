@@ -462,9 +462,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
 // the epilogue's stores (27 us). Both go through TMA where the alignment allows.
 // One 256-column accumulator and the scales fill tensor memory, so the epilogue
 // is not hidden behind the next tile; its eight warps first drain the accumulator
-// into registers, 128 columns a thread (the roles' registers are split for that),
-// and scale and store afterwards. 4096 x 14336 x 4096: 100 us back to back,
-// 4.8 PFLOP/s, of 61 at the rate of 256 x 256 x 64 products back to back (128 clocks).
+// into registers, 128 columns a thread (the roles' registers are split for that;
+// bf16 results are packed on the way, without which they spill: 99 against 94 us),
+// and store afterwards.
+// 4096 x 14336 x 4096: 94 us back to back, 5.1 PFLOP/s. Bound by what L2 delivers to an
+// SM: a stage's 38 KB take 750 clocks (51 bytes a clock; plain TMA loads out of L2
+// into every SM reach 40 to 47, with multicast in clusters of 2 or 4 no more), its
+// products 512. Another 1570 clocks of a tile's 13500 pass between its last commit and
+// the next tile's first product.
 // ---------------------------------------------------------------------------
 
 // Warpgroups: producer and MMA warps; two of epilogue warps; scale warps. At 128
