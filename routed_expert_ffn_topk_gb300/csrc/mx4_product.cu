@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
     } else if (warp < 6) {
         zero_outside(p, blockIdx.x, gridDim.x, threadIdx.x - 64, 128);
         const int quad = warp % 4;
+        const bool pairs_out = p.elem == ESTREAM_MX4_BF16 && p.ld % 2 == 0 && p.N % 2 == 0 &&
+                               reinterpret_cast<uintptr_t>(p.out) % 4 == 0;
         int a = 0;
         uint32_t aph = 0;
         for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
@@ -409,7 +411,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_empty(a));
                 }
-                if (n < p.N) {
+                if (pairs_out) {
+                    // neighbouring lanes exchange: the even one stores both columns of row x,
+                    // the odd one of row x + 1
+                    const bool odd = lane & 1;
+                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(w.row + c + odd) * p.ld + (n & ~1);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2, o += 2 * p.ld) {
+                        const __nv_bfloat162 q = __floats2bfloat162_rn(__uint_as_float(v[x]) * p.scale,
+                                                                       __uint_as_float(v[x + 1]) * p.scale);
+                        const uint32_t own = *reinterpret_cast<const uint32_t*>(&q);
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                        if (n < p.N && c + x + odd < rows)
+                            *reinterpret_cast<uint32_t*>(o) = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                    }
+                } else if (n < p.N) {
                     size_t at = static_cast<size_t>(w.row + c) * p.ld + n;
 #pragma unroll
                     for (int x = 0; x < 32; ++x, at += p.ld)
