@@ -48,8 +48,8 @@ __device__ int g_mx4_err;
 // both run in its issue order, and two column sets alternate.
 // Bound by HBM (the weights) and by latency: 1 x 14336 x 4096 streams its 33 MB at
 // 6 TB/s for 5.5 us, after 2.5 us until the first stage is there (12 us a call back
-// to back, of 4.9 at HBM's rate); 64 slots of 128 rows, 2048 x 2048, take 43 us of 29,
-// the tensor pipe 22% busy, with 6 us of it the epilogue's 2-byte stores down a column
+// to back, of 4.9 at HBM's rate); 64 slots of 128 rows, 2048 x 2048, take 42 us of 29,
+// the tensor pipe 22% busy, with about 5 us of it the epilogue's small stores
 // (weights are M, so a thread holds a column of D).
 // ---------------------------------------------------------------------------
 
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
                 }
                 if (pairs_out) {
                     // neighbouring lanes exchange: the even one stores both columns of row x,
-                    // the odd one of row x + 1
+                    // the odd one of row x + 1 (half the stores: 42.1 against 43.4 us, 64 slots)
                     const bool odd = lane & 1;
                     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(w.row + c + odd) * p.ld + (n & ~1);
 #pragma unroll
