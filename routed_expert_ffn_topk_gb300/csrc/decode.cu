@@ -437,12 +437,12 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
 // Measured, L2 cold, of the time that the chosen experts' bytes take at 6.7 TB/s:
 //   OLMoE shape (2048 x 1024, 8 of 64), 1 token, router included     36 us of 15
 //   DeepSeek shape (2048 x 1408, 6 of 64 and 2), 4 tokens            74-83 us of 59
-//   Mixtral shape (4096 x 14336, 2 of 8) in 4 bits, 2 tokens         127-160 us of 52
+//   Mixtral shape (4096 x 14336, 2 of 8) in 4 bits, 2 tokens         115-150 us of 52
 //   OLMoE shape, 32 tokens                                           168 us of 119
 // At one token, latency: 8 us until the routes are known in every CTA and the first
 // weights are there, and 7 us of down projection after the grid barrier, though its
 // weights wait in shared memory by then (every SM reads the same h rows out of L2).
-// In 4 bits, issue slots: 32 instructions for 8 weights, of which 11 decode them.
+// In 4 bits, issue slots: 27 instructions for 8 weights, of which 9 decode them.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 16;
@@ -494,12 +494,17 @@ __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t w) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
-// Codes 2 i (low half) and 2 i + 1 (high half) of a 4-bit word as bf16 q - 8: the
-// code in bits 0-3 of bf16 128 makes 128 + q.
+// Codes 2 i (low half) and 2 i + 1 (high half) of a 4-bit word as bf16 (q - 8) / 64.
+// A half word's low eight bits alone are bf16 numbers below 2^-125, where the format
+// is linear: a code in bits 0-3 is q 2^-133, one in bits 4-7 q 2^-129. One
+// multiply-add, exact, takes either to its place, so only two of the four pairs of
+// a word share a shift. (A code set into the mantissa of 128 needs a shift each.)
+constexpr float kQ4Unit = 64.0f;  // what the sums of such products are short of
 __device__ __forceinline__ uint32_t q4_pair(uint32_t word, int i) {
-    const uint32_t u = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 v =
-        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&u), __floats2bfloat162_rn(-136.0f, -136.0f));
+    const uint32_t u = (i < 2 ? word : word >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+    const uint32_t to = i & 1 ? 0x7d007d00u : 0x7f007f00u;  // 2^123, 2^127
+    const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&to),
+                                     __floats2bfloat162_rn(-0.125f, -0.125f));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 // The scales of a row's two column blocks (gate and up: bf16; down: fp16).
@@ -857,7 +862,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
             const int row = m * 8 + (l >> 2), f = t.row + row, c = (l & 3) * 2 + hi;
             if (row >= t.n || c >= cnt) continue;
             const std::integral_constant<int, kGroup> n{};
-            const float gate = reduced(w_g, n, m, l * 4 + hi), up = reduced(w_g, n, m, l * 4 + 2 + hi);
+            constexpr float unit = kQ4 ? kQ4Unit : 1.0f;
+            const float gate = unit * reduced(w_g, n, m, l * 4 + hi), up = unit * reduced(w_g, n, m, l * 4 + 2 + hi);
             const float a = sh ? 1.0f : r.row_alpha[row0 + c];
             const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
             __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
@@ -985,7 +991,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
             const int m = i >> 7, l = (i & 127) >> 2, v = i & 3;
             const int row = m * 16 + (l >> 2) + (v >> 1) * 8, c = (l & 3) * 2 + (v & 1);
             if (row >= ty.n || c >= cnt || *abort_flag) continue;
-            const float y = reduced(kByToken ? 0 : w_g, std::integral_constant<int, kYWarps>{}, m, i & 127);
+            const float y = (kQ4 ? kQ4Unit : 1.0f) *
+                            reduced(kByToken ? 0 : w_g, std::integral_constant<int, kYWarps>{}, m, i & 127);
             if (kByToken) {
                 const size_t at = static_cast<size_t>(c) * H + ty.row + row;
                 d.Y[at] = (d.A ? x_at<ESTREAM_BF16>(d.A, at) : d.Y[at]) + y;
