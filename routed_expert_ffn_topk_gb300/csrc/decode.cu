@@ -454,7 +454,7 @@ constexpr int kMaxStages = 6;
 // (4-bit rows are short, so a tile takes more of them)
 template <bool kQ4>
 struct Stream {
-    static constexpr int kHRows = kQ4 ? 32 : 16;  // h rows of a gate/up tile
+    static constexpr int kHRows = kQ4 ? 48 : 16;  // h rows of a gate/up tile
     static constexpr int kYRows = kQ4 ? 32 : 16;  // Y rows of a down tile
     static constexpr int kStep = kQ4 ? 4 : 1;      // granularity of a range
     static constexpr int kHTiles = kHRows / 8;     // m16 tiles (8 gate + 8 up rows)
@@ -466,7 +466,8 @@ struct Stream {
     static constexpr int kYPart = kYRows * kRowBytes;  // a unit of Y: two k-blocks
     static constexpr int kUnit = 2 * (kHPart > kYPart ? kHPart : kYPart);
     // the warps' partial sums of a tile, twice: a tile's are written while the last one's are read
-    static constexpr int kTiles = kHTiles > kYTiles ? kHTiles : kYTiles;
+    // (two m16 tiles at a time)
+    static constexpr int kTiles = 2;
     static constexpr int kRedTile = kWarps * kTiles * 128;  // floats
     static constexpr int kRed = 2 * kRedTile;
 };
@@ -852,29 +853,33 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         // the warps' partial sums, SwiGLU and the weights of the routes
         const int len = sh ? Fs : F;
         __nv_bfloat16* hp = static_cast<__nv_bfloat16*>(sh ? d.h_shared : d.h);
-#pragma unroll
-        for (int m = 0; m < S::kHTiles; ++m) gather(acc[m], m);
-        sync_group();
         copy_wait(weights_bar, 0, abort_flag, d.err);
-        // lane l's values 0, 1 are gate and 2, 3 up of columns 2 (l % 4), + 1
-        for (int i = tid_g; i < S::kHTiles * 64; i += 32 * kGroup) {
-            const int m = i >> 6, l = (i & 63) >> 1, hi = i & 1;
-            const int row = m * 8 + (l >> 2), f = t.row + row, c = (l & 3) * 2 + hi;
-            if (row >= t.n || c >= cnt) continue;
-            const std::integral_constant<int, kGroup> n{};
-            constexpr float unit = kQ4 ? kQ4Unit : 1.0f;
-            const float gate = unit * reduced(w_g, n, m, l * 4 + hi), up = unit * reduced(w_g, n, m, l * 4 + 2 + hi);
-            const float a = sh ? 1.0f : r.row_alpha[row0 + c];
-            const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
-            __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
-            const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
-            const float r1 = v - __bfloat162float(p0);
-            const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-            o[0] = p0;
-            o[len] = p1;
-            o[2 * len] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+#pragma unroll
+        for (int m0 = 0; m0 < S::kHTiles; m0 += S::kTiles) {
+            if (m0 > 0 && m0 * 8 >= t.n) continue;
+#pragma unroll
+            for (int m = 0; m < S::kTiles; ++m) gather(acc[m0 + m], m);
+            sync_group();
+            // lane l's values 0, 1 are gate and 2, 3 up of columns 2 (l % 4), + 1
+            for (int i = tid_g; i < S::kTiles * 64; i += 32 * kGroup) {
+                const int m = i >> 6, l = (i & 63) >> 1, hi = i & 1;
+                const int row = (m0 + m) * 8 + (l >> 2), f = t.row + row, c = (l & 3) * 2 + hi;
+                if (row >= t.n || c >= cnt) continue;
+                const std::integral_constant<int, kGroup> n{};
+                constexpr float unit = kQ4 ? kQ4Unit : 1.0f;
+                const float gate = unit * reduced(w_g, n, m, l * 4 + hi), up = unit * reduced(w_g, n, m, l * 4 + 2 + hi);
+                const float a = sh ? 1.0f : r.row_alpha[row0 + c];
+                const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
+                __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
+                const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
+                const float r1 = v - __bfloat162float(p0);
+                const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+                o[0] = p0;
+                o[len] = p1;
+                o[2 * len] = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+            }
+            turn ^= 1;
         }
-        turn ^= 1;
     }
     // every h row of the call is written
     turn = 0;
