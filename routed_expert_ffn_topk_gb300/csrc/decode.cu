@@ -437,12 +437,12 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
 // Measured, L2 cold, of the time that the chosen experts' bytes take at 6.7 TB/s:
 //   OLMoE shape (2048 x 1024, 8 of 64), 1 token, router included     36 us of 15
 //   DeepSeek shape (2048 x 1408, 6 of 64 and 2), 4 tokens            74-83 us of 59
-//   Mixtral shape (4096 x 14336, 2 of 8) in 4 bits, 2 tokens         115-150 us of 52
-//   OLMoE shape, 32 tokens                                           168 us of 119
+//   Mixtral shape (4096 x 14336, 2 of 8) in 4 bits, 2 tokens         115-127 us of 52
+//   OLMoE shape, 32 tokens                                           161-172 us of 119
 // At one token, latency: 8 us until the routes are known in every CTA and the first
 // weights are there, and 7 us of down projection after the grid barrier, though its
 // weights wait in shared memory by then (every SM reads the same h rows out of L2).
-// In 4 bits, issue slots: 27 instructions for 8 weights, of which 9 decode them.
+// In 4 bits, issue slots: 26 instructions for 8 weights, of which 9 decode them.
 // ---------------------------------------------------------------------------
 
 constexpr int kWarps = 16;
