@@ -431,7 +431,8 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
  * earlier call that loaded it with B*G >= E), else ESTREAM_ERR_CAPACITY.
  * The h intermediate is kept in fp32 and split exactly for the tensor cores,
  * so no activation overflows here and Y has fp32 accuracy; NaNs and infinities
- * in a token's X reach that token's Y alone. A grid barrier that gives up (1 s)
+ * in a token's X reach that token's Y alone, and those in an expert's weights the
+ * tokens that chose it. A grid barrier that gives up (1 s)
  * leaves Y as it was and is reported by estream_get_device_error. Nothing is
  * synchronised; a call can be captured into a CUDA graph, whose replays the
  * caller orders against calls that refill the arena.

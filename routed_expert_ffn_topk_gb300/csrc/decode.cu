@@ -899,6 +899,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         // without the expert (kByToken); columns past the last token repeat it and are
         // not read. l_len: 16-byte words of an h part.
         int l_a = 0, l_kb = 2 * wy;  // kByToken: expert and k-block of the next unit
+        uint32_t l_mask = 0;         // kByToken: tokens of the unit whose h values were fetched last
         size_t l_len = (sh_t ? Fs : F) / 8;
         auto h_at = [&](int q) -> const uint4* {
             if (!kByToken)
@@ -911,6 +912,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
             }
             const Act act = r.act[l_a];
             const bool sh = l_a >= n_act;
+            l_mask = act.mask;
             l_len = (sh ? Fs : F) / 8;
             const uint4* p = static_cast<const uint4*>(sh ? d.h_shared : d.h) +
                              static_cast<size_t>(act.row0 + __popc(act.mask & ((1u << g) - 1u))) * 3 * l_len + l_kb * 8 + tq;
@@ -928,6 +930,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         load_h(hp, l_len, xa);
         for (int q = wy; q < units; q += kYWarps) {
             const bool full = wait_full();
+            // A column without the expert is left out of the sum: 0 times an infinite or NaN
+            // weight is not 0. The lane's sums are of columns 2 tq and 2 tq + 1.
+            const uint32_t in = kByToken ? l_mask >> (2 * tq) : 3u;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint4 (&x)[3][2] = half ? xb : xa;
@@ -976,11 +981,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                         const float2 lo = q4_scales(as<uint32_t>(p), true), hi = q4_scales(as<uint32_t>(p + 32), true);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            acc[m][i] = fmaf(part[0][m][i], i < 2 ? lo.x : hi.x,
-                                             fmaf(part[1][m][i], i < 2 ? lo.y : hi.y, acc[m][i]));
+                            if (in >> (i & 1) & 1u)
+                                acc[m][i] = fmaf(part[0][m][i], i < 2 ? lo.x : hi.x,
+                                                 fmaf(part[1][m][i], i < 2 ? lo.y : hi.y, acc[m][i]));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[m][i] += part[0][m][i] + part[1][m][i];
+                        for (int i = 0; i < 4; ++i)
+                            if (in >> (i & 1) & 1u) acc[m][i] += part[0][m][i] + part[1][m][i];
                     }
                 }
             }

@@ -1,0 +1,40 @@
+"""The few-token layer call where its inputs leave the ordinary: non-finite weights.
+
+Tolerances are test_gpu_decode's."""
+import numpy as np
+import pytest
+import torch
+
+from tests import test_gpu_decode as D
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("w", ["bf16", "q4", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 8, 9])
+def test_non_finite_down_weight_stays_with_its_expert(T, w, value):
+    """Expert 3 has an infinite or NaN down weight. A token that takes it has a
+    non-finite value in that row of Y; the other tokens' rows are what they are
+    without it."""
+    if w == "q4" and np.isnan(value):
+        pytest.skip("4-bit codes hold no NaN")
+    wl = D._workload(T=T, H=256, E=8, k=2, F=256, w=w)
+    lg = wl.logits[0]
+    lg[:, 3] = -50.0          # nobody's
+    if T > 1:
+        lg[T - 1, 3] = 50.0   # but the last token's
+    ref = D._reference(wl, w)
+    wl.layers[0].Wd[3, 17, 40] = value
+    st = D._stack(wl, wdtype=D._dtype(w))
+    try:
+        Y = torch.zeros(T, 256, device="cuda")
+        st.decode(0, wl.X.cuda(), lg.cuda(), Y)
+        D._ok(st)
+        y = Y.cpu().numpy()
+        others = slice(0, T - 1 if T > 1 else 1)
+        D._check(y[others], ref[others], f"beside a non-finite weight {w} T = {T}")
+        if T > 1:
+            assert not np.isfinite(y[T - 1, 17])
+    finally:
+        st.close()
