@@ -473,7 +473,8 @@ estream_status estream_moe_layer_decode_from_x(estream_ctx* c, int layer, const 
  * A row of K values is padded with zeros to Kp = the next multiple of 32:
  * codes [rows][Kp / 2] (two to a byte, the first in the low half; 16-byte
  * aligned), scales [rows][Kp / 16 or Kp / 32] (one byte each). K and N are at
- * most 2^24, g is positive and finite.
+ * most 2^24, the rows of a call (R) at most 2^30, g is positive and finite;
+ * beyond: ESTREAM_ERR_INVALID_ARG.
  */
 enum { ESTREAM_MX4_E4M3X16 = 0, ESTREAM_MX4_E8M0X32 = 1 };
 /* Element types of the unquantised side. */

@@ -391,6 +391,7 @@ bool mx4_elem_ok(int e) { return e == ESTREAM_MX4_BF16 || e == ESTREAM_MX4_F16 |
 bool mx4_scale_ok(float s) { return s > 0.0f && s <= 3.402823466e38f; }
 bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 constexpr int kMaxWidth = 1 << 24;   // K and N: keeps a row's offsets in 32 bits
+constexpr int kMaxRows = 1 << 30;    // keeps a row index and what is added to it (a launch's stride) in 32 bits
 
 // ESTREAM_OK when the current device runs this library's kernels.
 estream_status on_device() {
@@ -420,7 +421,7 @@ size_t estream_mx4_weight_scale_bytes(int P, int N, int K) {
 estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n_src, int R, int K,
                                     const int32_t* rows, int swiglu, int fmt, float scale,
                                     void* codes, void* scales, void* cuda_stream) {
-    if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || n_src < 0 || K < 1 ||
+    if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > kMaxRows || n_src < 0 || K < 1 ||
         K > kMaxWidth || ld < (swiglu ? 2ll : 1ll) * K || (!rows && n_src < R))
         return ESTREAM_ERR_INVALID_ARG;
     if (R == 0) return ESTREAM_OK;
@@ -436,8 +437,8 @@ estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n
 
 estream_status estream_mx4_dequantize(const void* codes, const void* scales, int fmt, float scale, int R,
                                       int K, void* out, int elem, long long ld, void* cuda_stream) {
-    if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || K < 1 || K > kMaxWidth ||
-        ld < K)
+    if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > kMaxRows || K < 1 ||
+        K > kMaxWidth || ld < K)
         return ESTREAM_ERR_INVALID_ARG;
     if (R == 0) return ESTREAM_OK;
     if (!at(codes, 16) || !scales || !at(out, elem == ESTREAM_MX4_F32 ? 4 : 2)) return ESTREAM_ERR_INVALID_ARG;
@@ -466,7 +467,7 @@ estream_status estream_mx4_product(const void* x_codes, const void* x_scales, in
                                    const void* w_tiles, int P, int N, int K, int fmt, float scale,
                                    const int32_t* offsets, void* out, int elem, long long ld,
                                    void* cuda_stream) {
-    if (!mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > (1 << 30) || P < 1 || P > kMaxP || N < 1 ||
+    if (!mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > kMaxRows || P < 1 || P > kMaxP || N < 1 ||
         N > kMaxWidth || K < 1 || K > kMaxWidth || (!offsets && P != 1) || ld < N ||
         (elem != ESTREAM_MX4_BF16 && elem != ESTREAM_MX4_F32))
         return ESTREAM_ERR_INVALID_ARG;
