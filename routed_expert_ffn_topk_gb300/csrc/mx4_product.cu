@@ -121,7 +121,12 @@ __device__ void zero_outside(const Mx4Product& p, int worker, int workers, int t
 }
 
 // Exclusive prefix of the slots' row tiles of NT rows into base[0 .. P], by the
-// whole CTA (warps of 32 slots at a time; P <= kMaxP).
+// whole CTA (warps of 32 slots at a time; P <= kMaxP). Ascending offsets give at
+// most R / NT + P tiles. Others may count rows many times over, past 32 bits: the
+// sums stop at kMostTiles, above every valid total, and a total past the valid
+// ones leaves no tiles at all. (A thread's own slots, at most 16 of 2^30 / 64 + 1
+// tiles, and one addition to a sum that has stopped stay within 32 bits.)
+constexpr int kMostTiles = 1 << 29;
 __device__ void tile_prefix(const Mx4Product& p, int nt, int* base, int* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int per = (p.P + nw * 32 - 1) / (nw * 32);  // slots a thread
@@ -136,18 +141,18 @@ __device__ void tile_prefix(const Mx4Product& p, int nt, int* base, int* sums) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+        if (lane >= d) incl = min(incl + o, kMostTiles);
     }
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
     int run = incl - mine;
-    for (int w = 0; w < warp; ++w) run += sums[w];
+    for (int w = 0; w < warp; ++w) run = min(run + sums[w], kMostTiles);
     for (int s = s0; s < min(p.P, s0 + per); ++s) {
         int lo, hi;
         slot_rows(p, s, lo, hi);
         base[s] = run;
         run += (hi - lo + nt - 1) / nt;
-        if (s == p.P - 1) base[p.P] = run;
+        if (s == p.P - 1) base[p.P] = run > p.R / nt + p.P ? 0 : run;
     }
     __syncthreads();
 }

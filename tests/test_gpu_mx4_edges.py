@@ -1,0 +1,29 @@
+"""The microscaled 4-bit calls at the ends of their argument ranges."""
+import pytest
+import torch
+
+from tests import test_gpu_mx4 as M
+
+pytestmark = pytest.mark.gpu
+
+
+def test_offsets_that_count_rows_many_times():
+    """2048 slots that each claim every one of 671 million rows are more row tiles
+    than 32 bits hold: nothing outside the result is touched, no wait runs out, and
+    the same sizes with ascending offsets give their values."""
+    es = M._es()
+    R, P, K = 5 << 27, 4096, 32
+    x = es.Mx4(torch.full((R, 16), 0x22, dtype=torch.uint8, device="cuda"),
+               torch.full((R, 1), 127, dtype=torch.uint8, device="cuda"), K, 1)
+    w = es.mx4_weights(torch.full((P, 1, 16), 0x22, dtype=torch.uint8, device="cuda"),
+                       torch.full((P, 1, 1), 127, dtype=torch.uint8, device="cuda"), K, 1)
+    buf = torch.full((R + 128, 1), 5.0, device="cuda")
+    claims = torch.zeros(P + 1, dtype=torch.int32)
+    claims[1::2] = R
+    even = (torch.arange(P + 1, dtype=torch.int64) * (R // P)).to(torch.int32)
+    for off in (claims, even):
+        es.mx4_product(x, w, offsets=off.cuda(), out=buf[64:-64])
+        torch.cuda.synchronize()
+        assert bool((buf[:64] == 5.0).all()) and bool((buf[-64:] == 5.0).all())
+        assert es.mx4_error() == es.OK
+    assert bool((buf[64:-64] == 32.0).all())  # 32 products of 1 and 1
