@@ -433,7 +433,9 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
  * so no activation overflows here and Y has fp32 accuracy; NaNs and infinities
  * in a token's X reach that token's Y alone, and those in an expert's weights the
  * tokens that chose it. A grid barrier that gives up (1 s)
- * leaves Y as it was and is reported by estream_get_device_error. Nothing is
+ * gives up for the whole grid: Y is left as it was, and the error reported by
+ * estream_get_device_error. A weight copy that does not arrive (2 s) is reported
+ * the same way; after the last barrier it leaves parts of Y unwritten. Nothing is
  * synchronised; a call can be captured into a CUDA graph, whose replays the
  * caller orders against calls that refill the arena.
  */
@@ -659,6 +661,14 @@ estream_status estream_inject_route_timeout(estream_ctx* c);
  * ESTREAM_ERR_TIMEOUT. Y then holds no routed contribution. Later calls are
  * unaffected. No GPU fault is involved. */
 estream_status estream_inject_expert_timeout(estream_ctx* c);
+
+/* Test of the few-token call's grid barriers: in the next one, one CTA arrives
+ * at barrier 0 (after the router's logits), 1 (after h) or 2 (before the sum over
+ * routes; more than 8 tokens) only once the others' wait (1 s) ran out, or after
+ * 3 s. The barrier has then failed for all of them: Y stays as it was and
+ * estream_get_device_error reports ESTREAM_ERR_TIMEOUT. Later calls are
+ * unaffected. No GPU fault is involved. */
+estream_status estream_inject_late_arrival(estream_ctx* c, int barrier);
 
 /* Host-side fault injection for tests: the pager refuses to fill group
  * `group` of `layer` (before any copy is issued) and the call returns

@@ -45,34 +45,63 @@ __device__ __forceinline__ bool copy_wait(uint32_t bar, uint32_t parity, volatil
     return mbar_wait(bar, parity, abort_flag, err);
 }
 
-// Barrier of the whole (cooperative) grid, bounded in time: returns false
-// after recording a timeout. sync[0] counts arrivals and only grows within a
-// launch; decode_leave zeroes it for the next one.
-__device__ bool decode_barrier(int* sync, int generation, int* err, int* ok_flag, bool withhold) {
+// Barrier of the whole (cooperative) grid, bounded in time. sync[0] counts
+// arrivals and only grows within a launch; decode_leave zeroes it for the next
+// one. Its kFailed bit is the outcome of a barrier that is not met: the first CTA
+// whose wait runs out, or whose own work is incomplete (the abort flag), sets it
+// while the count is still short, so a barrier is met for every CTA or for none,
+// also for one that arrives after others gave up. (A CTA still polling an earlier,
+// met barrier may take a later one's failure for its own. It stops there, and only
+// the last barrier's outcome decides what is written to Y.)
+constexpr int kFailed = 1 << 30;
+constexpr uint64_t kLateNs = 3000000000ull;  // test: bound of a late arrival's delay
+
+__device__ __forceinline__ int sync_word(const int* sync) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(sync) : "memory");
+    return v;
+}
+// How this CTA arrives: a test lets one stay away, or come once the others gave up.
+enum Arrival { kArrive = 0, kWithhold = 1, kArriveLate = 2 };
+
+__device__ bool decode_barrier(int* sync, int generation, int* err, int* ok_flag, volatile int* abort_flag,
+                               Arrival how) {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
-        if (!withhold) atomicAdd(sync, 1);
         const int target = generation * static_cast<int>(gridDim.x);
+        bool give_up = abort_flag && *abort_flag;
+        if (how == kArriveLate && !give_up)
+            for (const uint64_t t0 = global_ns(); !(sync_word(sync) & kFailed) && global_ns() - t0 < kLateNs;) {}
+        if (how != kWithhold && !give_up) atomicAdd(sync, 1);
         uint64_t t0 = 0;
         bool ok = true;
         for (uint32_t spins = 1;; ++spins) {
-            int seen;
-            asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(sync) : "memory");
-            if (seen >= target) break;
-            if (spins % kSpins != 0) continue;  // the clock is slow to read
-            if (t0 == 0) t0 = global_ns();
-            if (global_ns() - t0 > kDecodeWaitNs) {
-                record_error(err, kDevErrTimeout);
+            const int seen = sync_word(sync);
+            if (seen & kFailed) {
                 ok = false;
                 break;
             }
+            if (seen >= target) break;
+            if (give_up) {
+                // fails only while someone else arrives, at most once a CTA
+                if (atomicCAS(sync, seen, seen | kFailed) == seen) record_error(err, kDevErrTimeout);
+                continue;
+            }
+            if (spins % kSpins != 0) continue;  // the clock is slow to read
+            if (t0 == 0) t0 = global_ns();
+            give_up = global_ns() - t0 > kDecodeWaitNs;
         }
         __threadfence();
         *ok_flag = ok ? 1 : 0;
     }
     __syncthreads();
     return *ok_flag != 0;
+}
+
+// CTA 0's arrival at barrier `at` (0 the router's, 1 h's, 2 the sum's) as a test asks for it.
+__device__ __forceinline__ Arrival arrival(const DecodeCall& d, int at) {
+    return blockIdx.x == 0 ? static_cast<Arrival>(d.arrival >> (2 * at) & 3) : kArrive;
 }
 
 // Every CTA passes here last; the one that completes the count leaves both
@@ -361,7 +390,7 @@ __global__ void __launch_bounds__(kSimpleThreads) k_layer_decode_simple(const De
                 }
             }
         }
-        ok = decode_barrier(d.sync, ++gen, d.err, &ok_flag, (d.withhold & 2) && blockIdx.x == 0);
+        ok = decode_barrier(d.sync, ++gen, d.err, &ok_flag, nullptr, arrival(d, 1));
     }
     if (ok) {
         const int n_act = *r.n_act;
@@ -583,7 +612,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
     bool ok = true;
     if (d.W_r) {
         router_rows(d);
-        ok = decode_barrier(d.sync, ++gen, d.err, &ok_flag, (d.withhold & 1) && blockIdx.x == 0);
+        ok = decode_barrier(d.sync, ++gen, d.err, &ok_flag, nullptr, arrival(d, 0));
     }
     if (!ok) {
         decode_leave(d.sync);
@@ -883,8 +912,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
     }
     // every h row of the call is written
     turn = 0;
-    const bool met = decode_barrier(d.sync, ++gen, d.err, &ok_flag,
-                                    *abort_flag || ((d.withhold & 2) && blockIdx.x == 0));
+    const bool met = decode_barrier(d.sync, ++gen, d.err, &ok_flag, abort_flag, arrival(d, 1));
     live = live && met;
     Walk<S::kYRows> ty;
     start_y(ty);
@@ -1015,7 +1043,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
         turn ^= 1;
     }
     if (!kByToken) {
-        const bool summed = met && decode_barrier(d.sync, ++gen, d.err, &ok_flag, *abort_flag != 0);
+        const bool summed = met && decode_barrier(d.sync, ++gen, d.err, &ok_flag, abort_flag, arrival(d, 2));
         // Y[t] = A[t] (or Y[t]) + the token's routes in ascending expert order + the shared experts
         const int n4 = T * (H / 4);
         for (int i = blockIdx.x * kStreamThreads + threadIdx.x; summed && i < n4; i += gridDim.x * kStreamThreads) {

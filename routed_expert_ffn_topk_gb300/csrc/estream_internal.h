@@ -230,7 +230,7 @@ struct DecodeCall {
     float *y_rows, *y_shared;  // [T k][H], [n_shared T][H]: Y's terms (T > 8)
     int* sync;             // two words, zero between launches
     int* err;
-    int withhold;          // test: bit 0 / 1, CTA 0 does not arrive at the router's / the h barrier
+    int arrival;           // test: two bits a barrier (router, h, sum), CTA 0 stays away (1) or comes late (2)
 };
 cudaError_t launch_layer_decode(const DecodeCall& d, int wdtype, int num_sms, cudaStream_t stream);
 

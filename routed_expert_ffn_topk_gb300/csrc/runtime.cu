@@ -187,6 +187,7 @@ struct estream_ctx {
     int* dec_sync = nullptr;                    // [2] grid-barrier words, zero between launches
     cudaEvent_t dec_done = nullptr;             // after the latest few-token call
     bool dec_recorded = false;
+    int dec_late_next = 0;                      // test: late arrivals in the next few-token call (DecodeCall)
 };
 
 namespace {
@@ -1489,9 +1490,10 @@ static estream_status decode_impl(estream_ctx* c, int layer, const void* X, cons
     d.y_shared = c->dec_ys;
     d.sync = c->dec_sync;
     d.err = c->dev_err;
-    // tests of the bounded barriers: one CTA does not arrive
-    d.withhold = (c->route_withhold_next && W_r ? 1 : 0) | (c->ffn_down_only_next ? 2 : 0);
+    // tests of the bounded barriers: one CTA does not arrive, or late
+    d.arrival = (c->route_withhold_next && W_r ? 1 : 0) | (c->ffn_down_only_next ? 1 << 2 : 0) | c->dec_late_next;
     c->route_withhold_next = c->ffn_down_only_next = false;
+    c->dec_late_next = 0;
     TimedScope ts(c, s, kTFfn, layer);
     if (launch_layer_decode(d, c->d.wdtype, c->num_sms, s) != cudaSuccess) return ESTREAM_ERR_CUDA;
     ts.end();
@@ -1659,6 +1661,13 @@ estream_status estream_inject_expert_timeout(estream_ctx* c) {
 estream_status estream_inject_route_timeout(estream_ctx* c) {
     if (!c) return ESTREAM_ERR_NOT_BOUND;
     c->route_withhold_next = true;
+    return ESTREAM_OK;
+}
+
+estream_status estream_inject_late_arrival(estream_ctx* c, int barrier) {
+    if (!c) return ESTREAM_ERR_NOT_BOUND;
+    if (barrier < 0 || barrier > 2) return ESTREAM_ERR_INVALID_ARG;
+    c->dec_late_next = 2 << (2 * barrier);
     return ESTREAM_OK;
 }
 

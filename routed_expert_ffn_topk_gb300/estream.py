@@ -115,6 +115,7 @@ SIGNATURES = {
     "estream_inject_pager_fault": (_I, [_P, _I, _I]),
     "estream_inject_route_timeout": (_I, [_P]),
     "estream_inject_expert_timeout": (_I, [_P]),
+    "estream_inject_late_arrival": (_I, [_P, _I]),
     "estream_pipeline_trace": (_I, [_P, _P, _I, ctypes.POINTER(_I), ctypes.POINTER(ctypes.c_double)]),
     "estream_maxplus_pipeline": (ctypes.c_double, [_P, _P, _I, _I, _I, ctypes.c_double, _P]),
     "estream_bank_bound": (_I, [_I, ctypes.c_double, ctypes.c_double, ctypes.c_double, _I]),
@@ -855,6 +856,10 @@ def inject_expert_timeout(ctx) -> None:
 
 def inject_route_timeout(ctx) -> None:
     _check(lib().estream_inject_route_timeout(ctx), "estream_inject_route_timeout")
+
+
+def inject_late_arrival(ctx, barrier: int) -> None:
+    _check(lib().estream_inject_late_arrival(ctx, barrier), "estream_inject_late_arrival")
 
 
 def inject_pager_fault(ctx, layer: int, group: int) -> None:

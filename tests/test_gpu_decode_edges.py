@@ -1,4 +1,5 @@
-"""The few-token layer call where its inputs leave the ordinary: non-finite weights.
+"""The few-token layer call where things leave the ordinary: non-finite weights, late
+arrivals at its grid barriers.
 
 Tolerances are test_gpu_decode's."""
 import numpy as np
@@ -36,5 +37,45 @@ def test_non_finite_down_weight_stays_with_its_expert(T, w, value):
         D._check(y[others], ref[others], f"beside a non-finite weight {w} T = {T}")
         if T > 1:
             assert not np.isfinite(y[T - 1, 17])
+    finally:
+        st.close()
+
+
+@pytest.mark.parametrize("w,T,barrier", [("bf16", 2, 0), ("bf16", 2, 1), ("q4", 3, 1), ("f32", 2, 1), ("bf16", 12, 0),
+                                         ("bf16", 12, 1), ("bf16", 12, 2), ("q4", 12, 2)])
+def test_late_arrival_leaves_y(w, T, barrier):
+    """A CTA that arrives at a grid barrier after the others gave up does not go on
+    alone: Y, accumulated into here, stays as it was, and the next call is normal."""
+    es = D._es()
+    wl = D._workload(T=T, H=256, E=8, k=2, F=128, w=w)
+    W_r = None
+    if w != "f32":
+        wl.X, W_r = D.W.make_router(T, 256, 8, seed=3)
+    st = D._stack(wl, wdtype=D._dtype(w))
+
+    def call(Y):
+        if W_r is None:
+            st.decode(0, X, wl.logits[0].cuda(), Y)
+        else:
+            st.decode_from_x(0, X, W_r, Y)
+
+    try:
+        X = wl.X.cuda()
+        W_r = None if W_r is None else W_r.cuda()
+        want = torch.zeros(T, 256, device="cuda")
+        call(want)
+        D._ok(st)
+        es.inject_late_arrival(st.ctx, barrier)
+        Y = torch.full((T, 256), 7.0, device="cuda")
+        call(Y)
+        torch.cuda.synchronize()
+        assert es.get_device_error(st.ctx) == es.ERR_TIMEOUT
+        assert bool((Y == 7.0).all())
+        Y = torch.zeros(T, 256, device="cuda")
+        call(Y)
+        D._ok(st)
+        assert torch.equal(Y, want)
+        with pytest.raises(es.EStreamError):
+            es.inject_late_arrival(st.ctx, 3)
     finally:
         st.close()
