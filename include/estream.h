@@ -436,8 +436,12 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
  * gives up for the whole grid: Y is left as it was, and the error reported by
  * estream_get_device_error. A weight copy that does not arrive (2 s) is reported
  * the same way; after the last barrier it leaves parts of Y unwritten. Nothing is
- * synchronised; a call can be captured into a CUDA graph, whose replays the
- * caller orders against calls that refill the arena.
+ * synchronised. Calls on one context share its workspace: few-token calls made on
+ * different streams run one after another in the order they were made, and a
+ * refill of the arena runs after them. The caller orders the rest: this call
+ * against prompt calls on another stream, and, as a call can be captured into a
+ * CUDA graph, a graph's replays against each other and against every call on the
+ * context.
  */
 estream_status estream_moe_layer_decode(estream_ctx* c, int layer, const void* X,
                                         const float* logits, int T, int k, int renorm,

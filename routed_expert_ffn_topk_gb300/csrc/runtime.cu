@@ -1448,6 +1448,14 @@ static estream_status decode_impl(estream_ctx* c, int layer, const void* X, cons
     if (T > c->d.T_max || T > kDecodeMaxT || k > c->d.k_max) return ESTREAM_ERR_CAPACITY;
     if (!layer_resident(c, layer)) return ESTREAM_ERR_CAPACITY;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    // The calls share h, Y's terms and the barrier words: one starts after the one
+    // before it, whatever their streams (on the same stream the wait costs nothing).
+    // A captured call has no place in that order: its replays are the caller's to order.
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    const bool captured = cap != cudaStreamCaptureStatusNone;
+    if (!captured && c->dec_recorded && cudaStreamWaitEvent(s, c->dec_done, 0) != cudaSuccess)
+        return ESTREAM_ERR_CUDA;
     c->trace.clear();
     c->stats.calls += 1;
     TimedScope total(c, s, kTTotal, layer);
@@ -1500,10 +1508,7 @@ static estream_status decode_impl(estream_ctx* c, int layer, const void* X, cons
     c->stats.launches += 1;
     c->stats.n_ffn += c->timing ? 1 : 0;
     c->stats.groups_hit += c->n_groups;
-    // a captured call has no place in the order of later refills: its replays are the caller's to order
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) return ESTREAM_ERR_CUDA;
-    if (cap == cudaStreamCaptureStatusNone) {
+    if (!captured) {
         if (cudaEventRecord(c->dec_done, s) != cudaSuccess) return ESTREAM_ERR_CUDA;
         c->dec_recorded = true;
     }

@@ -1,5 +1,5 @@
 """The few-token layer call where things leave the ordinary: non-finite weights, late
-arrivals at its grid barriers.
+arrivals at its grid barriers, calls on streams that nothing orders.
 
 Tolerances are test_gpu_decode's."""
 import numpy as np
@@ -77,5 +77,32 @@ def test_late_arrival_leaves_y(w, T, barrier):
         assert torch.equal(Y, want)
         with pytest.raises(es.EStreamError):
             es.inject_late_arrival(st.ctx, 3)
+    finally:
+        st.close()
+
+
+@pytest.mark.parametrize("w,T", [("f32", 4), ("bf16", 3), ("bf16", 20), ("q4", 5)])
+def test_streams_without_an_order(w, T):
+    """Calls on two streams that nothing orders, as fast as they can be made: each
+    has the result that it has alone."""
+    wl = D._workload(T=T, H=512, E=16, k=4, F=512, w=w)
+    st = D._stack(wl, wdtype=D._dtype(w))
+    try:
+        lg = wl.logits[0].cuda()
+        Xs = [wl.X.cuda(), (wl.X * 0.5).cuda(), wl.X.flip(0).contiguous().cuda()]
+        want = []
+        for X in Xs:
+            Y = torch.zeros(T, 512, device="cuda")
+            st.decode(0, X, lg, Y)
+            want.append(Y)
+        D._ok(st)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        Ys = torch.zeros(300, T, 512, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(300):
+            st.decode(0, Xs[i % 3], lg, Ys[i], stream=streams[i % 3])
+        D._ok(st)
+        for i in range(300):
+            assert torch.equal(Ys[i], want[i % 3]), i
     finally:
         st.close()
