@@ -421,7 +421,7 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
  * depend on timing).
  * X       device, [T][H] of the context's type (bf16; fp32 for ESTREAM_F32),
  *         16-byte aligned.
- * logits  device, [T][E] fp32.
+ * logits  device, [T][E] fp32; a NaN makes its token's Y NaN.
  * T, k    1 <= T <= min(T_max, ESTREAM_DECODE_MAX_T), 1 <= k <= min(k_max, E);
  *         beyond: ESTREAM_ERR_CAPACITY.
  * A       device, [T][H] in X's type, 16-byte aligned (A == X allowed): Y = A +

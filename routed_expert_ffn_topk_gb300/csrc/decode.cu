@@ -166,7 +166,10 @@ __device__ Routes routes_at(void* smem, int T, int k, int E, int n_shared) {
     return r;
 }
 
+// (A NaN is the largest key, whatever its sign, and a NaN again in key_logit, so its
+// token's weights are NaN. The smallest key, of -infinity, is above 0.)
 __device__ __forceinline__ uint32_t logit_key(float v) {
+    if (isnan(v)) return 0xffffffffu;
     const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 -> +0
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
@@ -232,9 +235,8 @@ __device__ void build_routes(const Routes& r, const DecodeCall& d, const float* 
                 for (int j = 0; j < kKeysE / 32; ++j)
                     if (static_cast<uint32_t>(lane + 32 * j) == e) key[j] = 0u;
                 if (lane == 0) {
-                    // (no key is left only where a row of NaNs has every bit set)
                     r.ids[t * k + i] = static_cast<int>(e);
-                    if (e < static_cast<uint32_t>(E)) atomicOr(&r.expert[e].mask, 1u << t);
+                    atomicOr(&r.expert[e].mask, 1u << t);
                 }
             }
         } else {

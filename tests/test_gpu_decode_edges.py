@@ -1,4 +1,4 @@
-"""The few-token layer call where things leave the ordinary: non-finite weights, late
+"""The few-token layer call where things leave the ordinary: non-finite weights and logits, late
 arrivals at its grid barriers, calls on streams that nothing orders.
 
 Tolerances are test_gpu_decode's."""
@@ -104,5 +104,30 @@ def test_streams_without_an_order(w, T):
         D._ok(st)
         for i in range(300):
             assert torch.equal(Ys[i], want[i % 3]), i
+    finally:
+        st.close()
+
+
+@pytest.mark.parametrize("w", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 9])
+@pytest.mark.parametrize("E", [8, 128, 130, 200])
+def test_nan_logits(E, T, w):
+    """A NaN among a token's logits makes its softmax, and with it its row of Y, NaN
+    in either form of the selection; the other rows are what they are without it."""
+    wl = D._workload(T=T, H=256, E=E, k=2, F=128, w=w)
+    ref = D._reference(wl, w)
+    others = [t for t in range(T) if t != 1]
+    st = D._stack(wl, wdtype=D._dtype(w))
+    try:
+        for bits in (0x7fc00000, 0xffc00000, 0xffffffff):
+            for where in (slice(None), slice(5, 6)):
+                lg = wl.logits[0].numpy().copy()
+                lg.view(np.uint32)[1, where] = bits
+                Y = torch.zeros(T, 256, device="cuda")
+                st.decode(0, wl.X.cuda(), torch.from_numpy(lg).cuda(), Y)
+                D._ok(st)
+                y = Y.cpu().numpy()
+                assert np.isnan(y[1]).all()
+                D._check(y[others], ref[others], f"beside NaN logits {w} E = {E} T = {T}")
     finally:
         st.close()
