@@ -902,8 +902,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_layer_decode(const Decode
                 const float a = sh ? 1.0f : r.row_alpha[row0 + c];
                 const float v = a * act.scale * (gate / (1.0f + expf(-gate)) * up);
                 __nv_bfloat16* o = hp + static_cast<size_t>(row0 + c) * 3 * len + f;
-                const __nv_bfloat16 p0 = __float2bfloat16_rn(v);
-                const float r1 = v - __bfloat162float(p0);
+                // (just below 2^128 rounding up would leave bf16's range; an infinity has no rest)
+                const __nv_bfloat16 p0 = fabsf(v) < 0x1.ffp127f ? __float2bfloat16_rn(v) : __float2bfloat16_rz(v);
+                const float r1 = isinf(v) ? 0.0f : v - __bfloat162float(p0);
                 const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
                 o[0] = p0;
                 o[len] = p1;

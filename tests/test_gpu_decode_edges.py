@@ -1,5 +1,5 @@
-"""The few-token layer call where things leave the ordinary: non-finite weights and logits, late
-arrivals at its grid barriers, calls on streams that nothing orders.
+"""The few-token layer call where things leave the ordinary: non-finite weights and logits,
+largest activations, late arrivals at its grid barriers, calls on streams that nothing orders.
 
 Tolerances are test_gpu_decode's."""
 import numpy as np
@@ -129,5 +129,30 @@ def test_nan_logits(E, T, w):
                 y = Y.cpu().numpy()
                 assert np.isnan(y[1]).all()
                 D._check(y[others], ref[others], f"beside NaN logits {w} E = {E} T = {T}")
+    finally:
+        st.close()
+
+
+@pytest.mark.parametrize("infinite", [False, True])
+@pytest.mark.parametrize("T", [1, 9])
+def test_h_at_the_top_of_the_range(T, infinite):
+    """h = (181 / 128)^2 2^127, which bf16 rounds to infinity: Y, a thousandth of it,
+    is exact. An infinite h gives an infinite Y."""
+    wl = D._workload(T=T, H=256, E=1, k=1, F=128)
+    lw = wl.layers[0]
+    for t in (lw.Wg, lw.Wu, lw.Wd, wl.X):
+        t.zero_()
+    wl.X[:, 0] = 2.0 ** 32
+    lw.Wg[0, 0, 0] = 181 / 128 * 2.0 ** (40 if infinite else 31)  # SiLU of so much is itself
+    lw.Wu[0, 0, 0] = 181 / 128 * 2.0 ** 32
+    lw.Wd[0, :, 0] = -(2.0 ** -10)
+    lw.Wd[0, 6, 1] = 2.0 ** 14  # times h = 0; the largest weight, which leaves h unscaled
+    st = D._stack(wl)
+    try:
+        Y = torch.zeros(T, 256, device="cuda")
+        st.decode(0, wl.X.cuda(), wl.logits[0].cuda(), Y)
+        D._ok(st)
+        want = -float("inf") if infinite else -(181 / 128) ** 2 * 2.0 ** 117
+        assert bool((Y.double() == want).all())
     finally:
         st.close()
