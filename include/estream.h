@@ -495,8 +495,9 @@ size_t estream_mx4_weight_scale_bytes(int P, int N, int K);
 /*
  * Quantise R rows.
  * x        device, rows of `elem` values, ld elements apart, aligned to their
- *          type; [n_src][K], or with swiglu [n_src][2 K]: gate then up, and the
- *          value quantised is fl(fl(gate / fl(1 + exp(-gate))) * up) in fp32.
+ *          type (n_src = 0: not read, may be NULL); [n_src][K], or with swiglu
+ *          [n_src][2 K]: gate then up, and the value quantised is
+ *          fl(fl(gate / fl(1 + exp(-gate))) * up) in fp32.
  * rows     device, [R] int32, or NULL: output row i is source row rows[i] (a
  *          route map's rec_tok gathers each record's token); an index outside
  *          [0, n_src) gives a row of NaNs. NULL needs n_src >= R.

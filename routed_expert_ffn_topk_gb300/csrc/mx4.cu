@@ -426,7 +426,8 @@ estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n
         return ESTREAM_ERR_INVALID_ARG;
     if (R == 0) return ESTREAM_OK;
     const size_t b = elem == ESTREAM_MX4_F32 ? 4 : 2;
-    if (!at(x, b) || !at(codes, 16) || !scales || (rows && !at(rows, 4))) return ESTREAM_ERR_INVALID_ARG;
+    if ((n_src > 0 && !at(x, b)) || !at(codes, 16) || !scales || (rows && !at(rows, 4)))
+        return ESTREAM_ERR_INVALID_ARG;
     const estream_status st = on_device();
     if (st != ESTREAM_OK) return st;
     const Mx4Quantize q{x, elem, ld, n_src, R, K, rows, swiglu != 0, fmt, scale,

@@ -27,3 +27,14 @@ def test_offsets_that_count_rows_many_times():
         assert bool((buf[:64] == 5.0).all()) and bool((buf[-64:] == 5.0).all())
         assert es.mx4_error() == es.OK
     assert bool((buf[64:-64] == 32.0).all())  # 32 products of 1 and 1
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_gather_from_no_rows(fmt, swiglu):
+    """Every index is out of range of a source without rows: rows of NaNs."""
+    es = M._es()
+    x = torch.empty(0, 128 if swiglu else 64, dtype=torch.bfloat16, device="cuda")
+    idx = torch.tensor([0, -1, 5], dtype=torch.int32).cuda()
+    q = es.mx4_quantize(x, fmt, rows=idx, swiglu=swiglu)
+    assert q.shape == (3, 64) and bool(torch.isnan(es.mx4_dequantize(q)).all())
