@@ -33,8 +33,10 @@
  *   - Tracing: the calling thread's work is marked with NVTX ranges in the
  *     domain "estream" ("layer", "route build", "route from X", "routed
  *     experts", "shared experts", "combine", "bank fill", "preload"; payload:
- *     the layer, or layer * 65536 + group for a bank fill). They cost nothing
- *     measurable unless a tool is attached.
+ *     the layer, or layer * 65536 + group for a bank fill; a few-token call is a
+ *     "layer" with its "routed experts"; and "4-bit quantise", "4-bit
+ *     dequantise", "4-bit weight scales", "4-bit product"; payload: the rows).
+ *     They cost nothing measurable unless a tool is attached.
  */
 #ifndef ESTREAM_H
 #define ESTREAM_H

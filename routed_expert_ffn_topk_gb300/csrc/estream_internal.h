@@ -30,6 +30,28 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Whether the library's kernels run on device `dev` (built for sm_103a alone).
 bool device_supported(int dev);
 
+// NVTX ranges (domain "estream") for timeline tools: one per layer call, route
+// build, expert launch, combine and bank fill, per standalone route build or
+// preload, and per 4-bit call. The payload carries the layer (bank fills: layer *
+// 65536 + group), -1 where there is none, or a 4-bit call's rows.
+enum NvtxName {
+    kNvRoute = 0, kNvRouted, kNvShared, kNvCombine, kNvLayer, kNvBankFill,  // as the timed kinds
+    kNvRouteFromX, kNvPreload, kNvMx4Quantize, kNvMx4Dequantize, kNvMx4Scales, kNvMx4Product, kNvNames
+};
+void nvtx_push(int name, long long payload);
+void nvtx_pop();
+struct NvtxRange {
+    bool on;
+    NvtxRange(int name, long long payload, bool on_ = true) : on(on_) {
+        if (on) nvtx_push(name, payload);
+    }
+    ~NvtxRange() {
+        if (on) nvtx_pop();
+    }
+    NvtxRange(const NvtxRange&) = delete;
+    NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
 // Layout of the route-build workspace (all offsets 256-byte aligned).
 struct RouteWorkspace {
     size_t err_off;      // int32 device error word

@@ -421,6 +421,7 @@ size_t estream_mx4_weight_scale_bytes(int P, int N, int K) {
 estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n_src, int R, int K,
                                     const int32_t* rows, int swiglu, int fmt, float scale,
                                     void* codes, void* scales, void* cuda_stream) {
+    NvtxRange range(kNvMx4Quantize, R);
     if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > kMaxRows || n_src < 0 || K < 1 ||
         K > kMaxWidth || ld < (swiglu ? 2ll : 1ll) * K || (!rows && n_src < R))
         return ESTREAM_ERR_INVALID_ARG;
@@ -438,6 +439,7 @@ estream_status estream_mx4_quantize(const void* x, int elem, long long ld, int n
 
 estream_status estream_mx4_dequantize(const void* codes, const void* scales, int fmt, float scale, int R,
                                       int K, void* out, int elem, long long ld, void* cuda_stream) {
+    NvtxRange range(kNvMx4Dequantize, R);
     if (!mx4_elem_ok(elem) || !mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > kMaxRows || K < 1 ||
         K > kMaxWidth || ld < K)
         return ESTREAM_ERR_INVALID_ARG;
@@ -453,6 +455,7 @@ estream_status estream_mx4_dequantize(const void* codes, const void* scales, int
 
 estream_status estream_mx4_weight_scales(const void* scales, int P, int N, int K, int fmt, void* tiles,
                                          void* cuda_stream) {
+    NvtxRange range(kNvMx4Scales, static_cast<long long>(P) * N);
     if (!mx4_fmt_ok(fmt) || estream_mx4_weight_scale_bytes(P, N, K) == 0 || P > kMaxP || !scales ||
         !at(tiles, 128))
         return ESTREAM_ERR_INVALID_ARG;
@@ -468,6 +471,7 @@ estream_status estream_mx4_product(const void* x_codes, const void* x_scales, in
                                    const void* w_tiles, int P, int N, int K, int fmt, float scale,
                                    const int32_t* offsets, void* out, int elem, long long ld,
                                    void* cuda_stream) {
+    NvtxRange range(kNvMx4Product, R);
     if (!mx4_fmt_ok(fmt) || !mx4_scale_ok(scale) || R < 0 || R > kMaxRows || P < 1 || P > kMaxP || N < 1 ||
         N > kMaxWidth || K < 1 || K > kMaxWidth || (!offsets && P != 1) || ld < N ||
         (elem != ESTREAM_MX4_BF16 && elem != ESTREAM_MX4_F32))

@@ -61,15 +61,12 @@ struct Bank {
 
 enum TimedKind { kTRoute = 0, kTFfn, kTShared, kTCombine, kTTotal, kTIo, kTKinds };
 
-// NVTX ranges (domain "estream") for timeline tools: one per layer call, route
-// build, expert launch, combine and bank fill, and per standalone route build
-// or preload. Names are registered once, so a range costs no formatting; the
-// payload carries the layer (bank fills: layer * 65536 + group). Without an
-// attached tool NVTX's calls are no-ops.
-enum NvtxName {
-    kNvRoute = kTRoute, kNvRouted = kTFfn, kNvShared = kTShared, kNvCombine = kTCombine,
-    kNvLayer = kTTotal, kNvBankFill = kTIo, kNvRouteFromX, kNvPreload, kNvNames
-};
+// Names are registered once, so a range costs no formatting. Without an attached
+// tool NVTX's calls are no-ops.
+static_assert(kNvRoute == static_cast<int>(kTRoute) && kNvRouted == static_cast<int>(kTFfn) &&
+                  kNvShared == static_cast<int>(kTShared) && kNvCombine == static_cast<int>(kTCombine) &&
+                  kNvLayer == static_cast<int>(kTTotal) && kNvBankFill == static_cast<int>(kTIo),
+              "a timed scope's range has its kind's number");
 struct NvtxNames {
     nvtxDomainHandle_t dom = nullptr;
     nvtxStringHandle_t name[kNvNames] = {};
@@ -78,17 +75,21 @@ const NvtxNames& nvtx_names() {
     static const NvtxNames n = [] {
         NvtxNames r;
         r.dom = nvtxDomainCreateA("estream");
-        const char* text[kNvNames] = {"route build",  "routed experts", "shared experts",
-                                      "combine",      "layer",          "bank fill",
-                                      "route from X", "preload"};
+        const char* text[kNvNames] = {"route build",      "routed experts",      "shared experts",
+                                      "combine",          "layer",               "bank fill",
+                                      "route from X",     "preload",             "4-bit quantise",
+                                      "4-bit dequantise", "4-bit weight scales", "4-bit product"};
         for (int i = 0; i < kNvNames; ++i) r.name[i] = nvtxDomainRegisterStringA(r.dom, text[i]);
         return r;
     }();
     return n;
 }
-void nvtx_push(int name, long long payload) {
+}  // namespace
+
+void es::nvtx_push(int name, long long payload) {
     static const uint32_t color[kNvNames] = {0xff2e9e44, 0xff2a6fdb, 0xff1aa3a3, 0xff8a4fd0,
-                                             0xff808080, 0xffe08a1e, 0xff2e9e44, 0xffe08a1e};
+                                             0xff808080, 0xffe08a1e, 0xff2e9e44, 0xffe08a1e,
+                                             0xffb8860b, 0xffb8860b, 0xffb8860b, 0xff2a6fdb};
     const NvtxNames& n = nvtx_names();
     nvtxEventAttributes_t at = {};
     at.version = NVTX_VERSION;
@@ -101,18 +102,9 @@ void nvtx_push(int name, long long payload) {
     at.message.registered = n.name[name];
     nvtxDomainRangePushEx(n.dom, &at);
 }
-void nvtx_pop() { nvtxDomainRangePop(nvtx_names().dom); }
-struct NvtxRange {
-    bool on;
-    NvtxRange(int name, long long payload, bool on_ = true) : on(on_) {
-        if (on) nvtx_push(name, payload);
-    }
-    ~NvtxRange() {
-        if (on) nvtx_pop();
-    }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
+void es::nvtx_pop() { nvtxDomainRangePop(nvtx_names().dom); }
+
+namespace {
 
 struct Timed {
     int kind;
