@@ -38,3 +38,18 @@ def test_gather_from_no_rows(fmt, swiglu):
     idx = torch.tensor([0, -1, 5], dtype=torch.int32).cuda()
     q = es.mx4_quantize(x, fmt, rows=idx, swiglu=swiglu)
     assert q.shape == (3, 64) and bool(torch.isnan(es.mx4_dequantize(q)).all())
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("P,rows", [(65, 192), (70, 260), (130, 200)])
+def test_pairs_of_many_slots(P, rows, fmt):
+    """More than 64 slots of 192 rows and more: the pair form with its slots' prefix
+    beside the ring."""
+    g = torch.Generator().manual_seed(P)
+    n = torch.randint(rows - 40, rows + 60, (P,), generator=g)
+    n[3], n[P - 2] = 0, 1
+    n[7] += max(0, P * rows - int(n.sum()))  # 192 rows a slot on average at least
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), n.cumsum(0)]).tolist()
+    for N, K, dtype in ((256, 512, torch.bfloat16), (130, 96, torch.float32)):
+        M.check_product(off[-1], N, K, fmt, P=P, offsets=off, dtype=dtype)
+    assert M._es().mx4_error() == M._es().OK
