@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_mx4_quantize(const Mx4Q
     // source row, or -1 past the end and for an index out of range
     auto source = [&](int row) {
         if (row >= q.R) return -1;
-        const int src = q.rows ? __ldg(q.rows + row) : row;
+        const int src = q.rows ? __ldca(q.rows + row) : row;
         return src < q.n_src ? src : -1;
     };
     auto at = [&](int src) { return static_cast<const T*>(q.x) + static_cast<size_t>(src) * q.ld + c; };
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_mx4_quantize(const Mx4Q
         for (int h = 0; h < (kSwiglu ? 2 : 1); ++h)
 #pragma unroll
             for (int j = 0; j < kRaw; ++j)
-                raw[h][j] = __ldg(reinterpret_cast<const uint4*>(at(src) + (h ? q.K : 0)) + j);
+                raw[h][j] = __ldca(reinterpret_cast<const uint4*>(at(src) + (h ? q.K : 0)) + j);
     };
     // half h (gate, up) of the row fetched last
     auto values = [&](int src, int h, float (&v)[kVals]) {
@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_mx4_quantize(const Mx4Q
 }
 
 template <int kElem, int kFmt>
-__global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const uint32_t* __restrict__ codes,
-                                                             const uint8_t* __restrict__ scales, float g,
+__global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const uint32_t* codes, const uint8_t* scales, float g,
                                                              int R, int K, Tiling tiling, void* out,
                                                              long long ld, bool wide) {
     using T = typename Elem<kElem>::T;
@@ -212,8 +211,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const uint32_t* __r
     const int row = tiling.row(), group = tiling.group(), c = group * 8;
     if (row >= R || group >= tiling.groups) return;
     const size_t i = static_cast<size_t>(row) * tiling.groups + group;
-    const uint32_t w = codes[i];
-    const uint8_t s = scales[i / kLanes];
+    const uint32_t w = __ldca(codes + i);
+    const uint8_t s = __ldca(scales + i / kLanes);
     const float d = __fmul_rn(kFmt == ESTREAM_MX4_E4M3X16 ? e4m3_value(s) : e8m0_value(s), g);
     alignas(16) T v[8];
 #pragma unroll

@@ -186,14 +186,14 @@ __device__ __forceinline__ RowScales row_scales(const uint8_t* row, int stage, i
     if (fmt == ESTREAM_MX4_E4M3X16) {
         const int b0 = stage * 16;
         if (wide && b0 + 16 <= nb) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + b0));
+            const uint4 v = __ldca(reinterpret_cast<const uint4*>(row + b0));
             r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int b = b0 + 4 * j;
-                const uint32_t lo = b < nb ? __ldg(reinterpret_cast<const uint16_t*>(row + b)) : 0u;
-                const uint32_t hi = b + 2 < nb ? __ldg(reinterpret_cast<const uint16_t*>(row + b + 2)) : 0u;
+                const uint32_t lo = b < nb ? __ldca(reinterpret_cast<const uint16_t*>(row + b)) : 0u;
+                const uint32_t hi = b + 2 < nb ? __ldca(reinterpret_cast<const uint16_t*>(row + b + 2)) : 0u;
                 r.w[j] = lo | (hi << 16);
             }
         }
@@ -201,12 +201,12 @@ __device__ __forceinline__ RowScales row_scales(const uint8_t* row, int stage, i
         const int b0 = stage * 8;
         uint32_t v[2] = {0u, 0u};
         if (wide && b0 + 8 <= nb) {
-            const uint2 t = __ldg(reinterpret_cast<const uint2*>(row + b0));
+            const uint2 t = __ldca(reinterpret_cast<const uint2*>(row + b0));
             v[0] = t.x, v[1] = t.y;
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (b0 + j < nb) v[j / 4] |= static_cast<uint32_t>(__ldg(row + b0 + j)) << (8 * (j % 4));
+                if (b0 + j < nb) v[j / 4] |= static_cast<uint32_t>(__ldca(row + b0 + j)) << (8 * (j % 4));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) r.w[j] = __byte_perm(v[j / 2], 0, j % 2 ? 0x3322 : 0x1100);

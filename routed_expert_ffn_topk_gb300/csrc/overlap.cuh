@@ -12,7 +12,10 @@ namespace es {
 
 // Every thread calls this before it touches memory that another kernel may write or
 // read. The kernel after this one may then start, and this one continues once all
-// those before it have ended and their writes are visible.
+// those before it have ended and their writes are visible. What they may have
+// written is read by ordinary loads, not by the read-only path (__ldg, or a const
+// __restrict__ parameter): that path is defined only for memory which nothing
+// writes while the kernel runs, and this one runs while they write.
 __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 }
