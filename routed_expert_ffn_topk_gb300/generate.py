@@ -50,6 +50,8 @@ class Mx4Experts:
         T = X.shape[0]
         if X.dim() != 2 or X.shape[1] != self.H or tuple(logits.shape) != (T, self.E):
             raise ValueError(f"X must be [T, {self.H}] and logits [T, {self.E}]")
+        if T == 0:
+            return torch.zeros(0, self.H, device=X.device)
         r = es.route_build(logits, k, renorm)
         offsets = r["offsets"][:self.E + 1]
         x = es.mx4_quantize(X, self.fmt, self.act_scale, rows=r["rec_tok"])
