@@ -46,9 +46,10 @@ __device__ int g_mx4_err;
 // (row r of 128: lane r % 32, byte group r / 32). The issuing thread copies
 // scales to tensor memory with tcgen05.cp ahead of the products that use them;
 // both run in its issue order, and two column sets alternate.
-// Bound by HBM (the weights) and by latency: 1 x 14336 x 4096 streams its 33 MB at
-// 6 TB/s for 5.5 us, after 2.5 us until the first stage is there (12 us a call back
-// to back, of 4.9 at HBM's rate); 64 slots of 128 rows, 2048 x 2048, take 42 us of 29,
+// Bound by HBM (the weights) and by latency: 1 x 14336 x 4096 streams its 33 MB (a
+// tile holds a 32-value block's scale twice) at 6 TB/s for 5.5 us, after 2.5 us until
+// the first stage is there (12 us a call back to back, of 4.7 for the data's own
+// bytes at HBM's rate), on 112 of the 152 SMs; 64 slots of 128 rows, 2048 x 2048, take 42 us of 29,
 // the tensor pipe 22% busy, with about 5 us of it the epilogue's small stores
 // (weights are M, so a thread holds a column of D).
 // ---------------------------------------------------------------------------
@@ -486,11 +487,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1) k_mx4_product(const __grid_con
 // into registers, 128 columns a thread (the roles' registers are split for that;
 // bf16 results are packed on the way, without which they spill: 99 against 94 us),
 // and store afterwards.
-// 4096 x 14336 x 4096: 94 us back to back, 5.1 PFLOP/s. Bound by what L2 delivers to an
-// SM: a stage's 38 KB take 750 clocks (51 bytes a clock; plain TMA loads out of L2
-// into every SM reach 40 to 47, with multicast in clusters of 2 or 4 no more), its
-// products 512. Another 1570 clocks of a tile's 13500 pass between its last commit and
-// the next tile's first product.
+// 4096 x 14336 x 4096: 94 us back to back, 5.1 PFLOP/s. A stage takes 750 clocks, its
+// products 512; the issuing thread waits for operands and scales meanwhile, which
+// come at 51 bytes a clock and SM. A kernel of nothing but TMA loads out of L2 into
+// every SM reached 40 to 47 (no more with multicast in clusters of 2 or 4), so the
+// products are fed as fast as anything measured here was; what would limit them at
+// a higher rate is not known. Another 1570 clocks of a tile's 13500 pass between its
+// last commit and the next tile's first product.
 // ---------------------------------------------------------------------------
 
 // Warpgroups: producer and MMA warps; two of epilogue warps; scale warps. At 128
@@ -979,7 +982,9 @@ cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t stream) {
     //   64       -     35   39        32                             13.4  11.0
     //   32       -     31   33
     // With several slots some hold more than the mean, and a tile of 64 rows then
-    // reads their weights twice.
+    // reads their weights twice. At both shapes every form has a tile for most SMs.
+    // With few weight rows none has (256 rows x N = 256 are one pair's tile); the
+    // choice there is this table's all the same, and is not measured.
     const long long per = p.R / p.P;
     if (per >= 192) return launch_pair(p, stream);
     if (per > (p.P == 1 ? 64 : 31)) return launch_mma<128>(p, stream);
