@@ -443,7 +443,8 @@ estream_status estream_moe_layer_prefill_from_x(estream_ctx* c, int layer, const
  * refill of the arena runs after them. The caller orders the rest: this call
  * against prompt calls on another stream, and, as a call can be captured into a
  * CUDA graph, a graph's replays against each other and against every call on the
- * context.
+ * context. (The first layer call after estream_arena_preload waits for its copies,
+ * which a capture cannot: make one before capturing.)
  */
 estream_status estream_moe_layer_decode(estream_ctx* c, int layer, const void* X,
                                         const float* logits, int T, int k, int renorm,

@@ -467,7 +467,7 @@ const char* estream_status_string(estream_status s) {
     return "unknown status";
 }
 
-int estream_version(void) { return 10300; }
+int estream_version(void) { return 10301; }
 
 size_t estream_route_workspace_bytes(int T, int E, int k, int P) {
     if (T < 0 || E < 1 || k < 1 || P < 0 || P > kMaxP) return 0;
