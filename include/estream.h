@@ -35,7 +35,8 @@
  *     experts", "shared experts", "combine", "bank fill", "preload"; payload:
  *     the layer, or layer * 65536 + group for a bank fill; a few-token call is a
  *     "layer" with its "routed experts"; and "4-bit quantise", "4-bit
- *     dequantise", "4-bit weight scales", "4-bit product"; payload: the rows).
+ *     dequantise", "4-bit weight scales", "4-bit product", "cache append",
+ *     "cache attend" and "sample"; payload: the rows).
  *     They cost nothing measurable unless a tool is attached.
  */
 #ifndef ESTREAM_H
@@ -550,6 +551,143 @@ estream_status estream_mx4_product(const void* x_codes, const void* x_scales, in
  * ESTREAM_ERR_TIMEOUT when a bounded wait inside one ran out (its output is then
  * incomplete). */
 estream_status estream_mx4_error(void* cuda_stream);
+
+/* ---------------------------------------------------------------------- */
+/* Paged key-value cache                                                   */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * Keys and values of many sequences in pages of page_size tokens: element d of
+ * head h of token j of page p is k[p * k_page + j * k_token + h * k_head + d]
+ * (v alike; strides in elements, rows of `dim` contiguous), so pages may be
+ * stored token by token or head by head. A sequence's position i is token
+ * i % page_size of page table[row][i / page_size].
+ * Elements are bf16, fp16, or E4M3 (the value is the element times k_scale or
+ * v_scale; the scales of the others are 1). dim is a multiple of 16, at most 256;
+ * k, v and the strides (in bytes) are multiples of 16; heads at most 1024,
+ * page_size and num_pages at most 2^30; scales from 2^-100 to 2^100. Rows do
+ * not overlap. Beyond: ESTREAM_ERR_INVALID_ARG.
+ */
+enum { ESTREAM_KV_BF16 = 0, ESTREAM_KV_F16 = 1, ESTREAM_KV_E4M3 = 2 };
+typedef struct {
+    void* k;
+    void* v;
+    int elem, num_pages, page_size, heads, dim;
+    float k_scale, v_scale;
+    long long k_page, k_token, k_head;
+    long long v_page, v_token, v_head;
+} estream_kv_cache;
+
+/*
+ * Store the keys and values of T new tokens, keys rotated by their position,
+ * and rotate the tokens' queries.
+ * elem     ESTREAM_KV_BF16 or ESTREAM_KV_F16: the type of k, v, q and q_out, and
+ *          the cache's unless that is E4M3.
+ * k, v     device, [T][heads][dim], tokens and heads *_token and *_head elements
+ *          apart (rows of dim contiguous, aligned to their type).
+ * positions  device, [T] int32: the token's place in its sequence. A token with
+ *          a negative one is padding: nothing of it is stored, its q_out row
+ *          stays as it was.
+ * rows     device, [T] int32, or NULL (token t belongs to row t): the row of
+ *          `table` that is its sequence's.
+ * table    device, [B][M] int32 page numbers, rows table_row >= 0 elements apart
+ *          (0: one row for all); entries that no token needs are not read.
+ *          A token whose row is outside [0, B), whose position is M * page_size or
+ *          more, or whose page is outside [0, num_pages) is not stored, and its
+ *          q_out row becomes NaNs. No two tokens have one row and position
+ *          (which of them is stored is then not specified).
+ * q, q_out  device, [T][Hq][dim]; q_out may be q. Hq = 0: none.
+ * inv_freq  device, [rot / 2] fp32; rot even, at most dim (0: no rotation). Pair i of
+ *          a row's first rot values is turned by position * inv_freq[i] radians:
+ *          (a, b) -> (a cos - b sin, b cos + a sin), where the pair is (i, i + rot / 2),
+ *          or with `interleaved` (2i, 2i + 1). The angle is reduced to one turn
+ *          in 64-bit integers, so far positions keep theirs; sums in fp32,
+ *          rounded once. E4M3 elements are x * fl(1 / scale), at most 448 in
+ *          magnitude; NaN stays NaN.
+ */
+estream_status estream_kv_append(const estream_kv_cache* cache, int elem, int T,
+                                 const void* k, long long k_token, long long k_head,
+                                 const void* v, long long v_token, long long v_head,
+                                 const int32_t* positions, const int32_t* rows,
+                                 const int32_t* table, int B, int M, long long table_row,
+                                 const void* q, long long q_token, long long q_head, int Hq,
+                                 void* q_out, long long qo_token, long long qo_head,
+                                 const float* inv_freq, int rot, int interleaved,
+                                 void* cuda_stream);
+
+/* Bytes of estream_kv_attend's workspace on the current device (0: none is
+ * needed, or invalid sizes). */
+size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, int Hq, int M);
+
+/*
+ * Attention of one new token per row over its sequence in the cache:
+ *   z_i = scale * (q . k_i), out = sum_i softmax(z)_i v_i, lse = log sum_i exp z_i
+ * over the positions i in [max(0, lens[b] - window), lens[b]) (window 0: from 0).
+ * elem     ESTREAM_KV_BF16 or ESTREAM_KV_F16: the type of q and out, and the
+ *          cache's unless that is E4M3.
+ * q, out   device, [B][Hq][dim], rows *_row and heads *_head elements apart, aligned to
+ *          their type; query head j meets key head j / (Hq / heads). out may be q.
+ * table    device, [B][M] int32, as above, rows table_row >= 0 elements apart; entries past
+ *          a sequence's end, or wholly before its window, are not read.
+ * lens     device, [B] int32: a sequence's tokens, the new one among them. 0: a
+ *          row of zeros, lse -infinity (so also where every z_i is -infinity). A
+ *          row whose length is outside [0, M * page_size], or that needs a page
+ *          outside [0, num_pages), becomes NaNs, its lse too.
+ * lse      device, [B][Hq] fp32, or NULL.
+ * workspace  device, 16-byte aligned, estream_kv_attend_workspace_bytes(cache, B, Hq, M)
+ *          bytes, used by this call alone until it ends (no initial value).
+ * Cache positions that are not attended (past the end, before the window, other
+ * pages) may hold anything; an infinite value that is attended gives NaN. Products and sums in fp32; weights are kept to 16
+ * bits for bf16 values and to 11 for the others. M * page_size < 2^31 - 4096, B *
+ * Hq at most 2^24. A call repeats bit for bit on one kind of device.
+ */
+estream_status estream_kv_attend(const estream_kv_cache* cache, int elem, int B, int Hq,
+                                 const void* q, long long q_row, long long q_head,
+                                 const int32_t* table, int M, long long table_row,
+                                 const int32_t* lens, float scale, int window,
+                                 void* out, long long out_row, long long out_head, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* ---------------------------------------------------------------------- */
+/* Sampling                                                                */
+/* ---------------------------------------------------------------------- */
+
+/* The largest vocabulary of estream_sample_tokens. */
+enum { ESTREAM_SAMPLE_MAX_V = 393216 };
+
+/*
+ * The next token of each of B rows of logits, from given random numbers:
+ *   w_i = exp((l_i - max l) / temperature);
+ *   1. the top_k largest logits are kept (equal ones: the lowest index first);
+ *      top_k < 1: all;
+ *   2. of these, by falling logit (equal ones: the lowest index first), those
+ *      before which less than top_p of their weight lies; the first always;
+ *      top_p >= 1: all;
+ *   3. of these, those with w_i >= min_p (the largest always);
+ *   ids[b] is the first i in the vocabulary's order at which the kept weight up
+ *   to and with i exceeds u[b] times the kept weight; prob[b] = w_i / that weight.
+ * Weights are held to 2^-38 of themselves or 2^-42 of the largest and summed as
+ * integers, so ids are those of exact arithmetic but where u or a border lies
+ * within about 1e-12 of the kept weight, and a call repeats bit for bit.
+ * logits   device, [B][V] of `elem` (ESTREAM_MX4_BF16, _F16 or _F32), rows ld >= 0
+ *          elements apart (0: one row for all), aligned to their type; -infinity:
+ *          never drawn.
+ * u        device, [B] fp32 in [0, 1) (others: the nearest end; NaN as 0).
+ * temperature, top_k, top_p, min_p: a number for all rows, or, where the *_rows pointer
+ *          is not NULL, device, [B], one for each (the number is then ignored). A
+ *          temperature that is not above 2^-100 takes the largest logit (the lowest
+ *          index of equal ones; prob 1), one above 2^100 counts as that.
+ *          NaN: top_p as 0, min_p as 0.
+ * ids      device, [B] int32; -1 (prob NaN) for a row without a finite largest logit:
+ *          all -infinity, or one +infinity or NaN.
+ * prob     device, [B] fp32, or NULL.
+ * V from 1 to ESTREAM_SAMPLE_MAX_V, B at most 2^20.
+ */
+estream_status estream_sample_tokens(const void* logits, int elem, long long ld, int B, int V,
+                                     const float* u, float temperature, const float* temperature_rows,
+                                     int top_k, const int32_t* top_k_rows, float top_p,
+                                     const float* top_p_rows, float min_p, const float* min_p_rows,
+                                     int32_t* ids, float* prob, void* cuda_stream);
 
 /* Timings and counters accumulated since the last estream_reset_stats. The
  * per-kernel times are CUDA-event times on the launching stream, recorded

@@ -32,11 +32,13 @@ bool device_supported(int dev);
 
 // NVTX ranges (domain "estream") for timeline tools: one per layer call, route
 // build, expert launch, combine and bank fill, per standalone route build or
-// preload, and per 4-bit call. The payload carries the layer (bank fills: layer *
-// 65536 + group), -1 where there is none, or a 4-bit call's rows.
+// preload, per 4-bit call, and per call of the key-value cache and of sampling. The
+// payload carries the layer (bank fills: layer * 65536 + group), -1 where there is none,
+// or the last three kinds' rows.
 enum NvtxName {
     kNvRoute = 0, kNvRouted, kNvShared, kNvCombine, kNvLayer, kNvBankFill,  // as the timed kinds
-    kNvRouteFromX, kNvPreload, kNvMx4Quantize, kNvMx4Dequantize, kNvMx4Scales, kNvMx4Product, kNvNames
+    kNvRouteFromX, kNvPreload, kNvMx4Quantize, kNvMx4Dequantize, kNvMx4Scales, kNvMx4Product,
+    kNvKvAppend, kNvKvAttend, kNvSample, kNvNames
 };
 void nvtx_push(int name, long long payload);
 void nvtx_pop();
@@ -297,6 +299,34 @@ struct Mx4Product {
 cudaError_t launch_mx4_product(const Mx4Product& p, cudaStream_t stream);
 // Reads and clears the current device's product error word (kDevErr*), after the stream's work.
 cudaError_t read_mx4_error(int* code, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Paged key-value cache
+// ---------------------------------------------------------------------------
+
+constexpr int kKvMaxDim = 256;
+constexpr int kKvMaxHeads = 1024;
+
+// n / d for 0 <= n < 2^31 without a division: with s = ceil(log2 d) and
+// mul = ceil(2^(31 + s) / d) < 2^32, (n * mul) >> (31 + s) is exact, as
+// mul * d - 2^(31 + s) < d <= 2^s and n < 2^31.
+struct FastDiv {
+    uint32_t mul, shift, d;
+    explicit FastDiv(uint32_t d_ = 1) : d(d_) {
+        uint32_t s = 0;
+        while ((1ull << s) < d) ++s;
+        shift = 31 + s;
+        mul = static_cast<uint32_t>(((1ull << shift) + d - 1) / d);
+    }
+    __host__ __device__ uint32_t div(uint32_t n) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> shift);
+    }
+};
+
+// Whether the description is one that include/estream.h allows.
+bool kv_cache_ok(const estream_kv_cache* c);
+// ESTREAM_OK when the current device runs this library's kernels.
+estream_status on_device();
 
 // Tensor-map helper (driver entry point resolved at run time); 128-byte swizzle or none.
 CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base,

@@ -1,0 +1,301 @@
+// New tokens' keys and values into a paged cache, keys (and the tokens' queries)
+// rotated by their position on the way.
+//
+// Pair i of a rotated row, (a, b), becomes (a cos t - b sin t, b cos t + a sin t)
+// with t = position * inv_freq[i]. Far positions make many turns, of which only the
+// last, unfinished one counts: inv_freq / 2 pi is taken to 64 fractional bits, where
+// the product with the position drops whole turns by itself, and the top 32 bits
+// that are left go to sincospi. The error is 2^-53 position inv_freq / 2 pi
+// (double's, of the quotient) + 2^-32 turns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "estream_internal.h"
+#include "overlap.cuh"
+
+namespace es {
+namespace {
+
+struct Append {
+    const void *k, *v, *q;
+    void *q_out, *kc, *vc;
+    long long k_token, k_head, v_token, v_head, q_token, q_head, qo_token, qo_head;
+    long long kc_page, kc_token, kc_head, vc_page, vc_token, vc_head;
+    const int32_t *positions, *rows, *table;
+    const float* inv_freq;
+    long long table_row;
+    float k_inv, v_inv;  // 1 / scale
+    int T, B, M, num_pages, Hq, heads, dim, rot, interleaved;
+    FastDiv page, per_head, per_v;  // page_size; units of a rotated and of a value head
+};
+
+template <bool kF16>
+__device__ __forceinline__ float2 up2(uint32_t w) {
+    if constexpr (kF16) return __half22float2(*reinterpret_cast<__half2*>(&w));
+    else return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t down2(float x, float y) {
+    if constexpr (kF16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <bool kF16>
+__device__ __forceinline__ float up1(uint16_t v) {
+    if constexpr (kF16) return __half2float(__ushort_as_half(v));
+    else return __bfloat162float(__ushort_as_bfloat16(v));
+}
+template <bool kF16>
+__device__ __forceinline__ uint16_t down1(float v) {
+    if constexpr (kF16) return __half_as_ushort(__float2half_rn(v));
+    else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Eight values that lie together.
+struct Eight {
+    float x[8];
+};
+template <bool kF16>
+__device__ __forceinline__ Eight widen(uint4 w) {
+    Eight e;
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = up2<kF16>(u[i]);
+        e.x[2 * i] = f.x;
+        e.x[2 * i + 1] = f.y;
+    }
+    return e;
+}
+template <bool kF16>
+__device__ __forceinline__ void store16(void* to, const Eight& e) {
+    *static_cast<uint4*>(to) = make_uint4(down2<kF16>(e.x[0], e.x[1]), down2<kF16>(e.x[2], e.x[3]),
+                                          down2<kF16>(e.x[4], e.x[5]), down2<kF16>(e.x[6], e.x[7]));
+}
+__device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+// To the cache, whose elements are of the input's type or E4M3.
+template <bool kF16, bool kE4m3>
+__device__ __forceinline__ void keep8(void* base, long long at, const Eight& e, float inv) {
+    if constexpr (kE4m3) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = e4m3x2(e.x[4 * i] * inv, e.x[4 * i + 1] * inv) |
+                   e4m3x2(e.x[4 * i + 2] * inv, e.x[4 * i + 3] * inv) << 16;
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) = make_uint2(w[0], w[1]);
+    } else {
+        store16<kF16>(static_cast<uint16_t*>(base) + at, e);
+    }
+}
+template <bool kF16, bool kE4m3>
+__device__ __forceinline__ void keep1(void* base, long long at, float x, float inv) {
+    if constexpr (kE4m3) static_cast<uint8_t*>(base)[at] = __nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3);
+    else static_cast<uint16_t*>(base)[at] = down1<kF16>(x);
+}
+
+// How a thread's unit of work lies in a row: one pair or value; eight pairs whose
+// halves are rot / 2 apart (or eight values that are not rotated); eight values
+// that hold four neighbouring pairs.
+enum Mode { kSingles, kHalves, kNeighbours };
+
+// A block takes a token at a time: its threads form the angles of the pairs once
+// for all heads, then go over the heads' units.
+template <Mode kMode, bool kF16, bool kE4m3>
+__global__ void __launch_bounds__(512) k_kv_append(const Append a) {
+    __shared__ float2 turn[2][kKvMaxDim / 2];  // cos, sin; of this token and the one after it
+    after_previous();
+    const int tid = threadIdx.x, pairs = a.rot / 2;
+    uint64_t per_position = 0;  // turns, 64 fractional bits
+    if (tid < pairs) {
+        double f = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189533577;
+        f -= floor(f);
+        per_position = static_cast<uint64_t>(f * 18446744073709551616.0);
+    }
+    const int rotated = (a.heads + a.Hq) * static_cast<int>(a.per_head.d), units = rotated + a.heads * static_cast<int>(a.per_v.d);
+    int now = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int pos = a.positions[t], row = a.rows ? a.rows[t] : t;
+        if (pos < 0) continue;  // padding: the whole block
+        if (tid < pairs) {
+            const int32_t top = static_cast<int32_t>((per_position * static_cast<uint64_t>(pos)) >> 32);
+            float s, c;
+            sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
+            turn[now][tid] = make_float2(c, s);
+        }
+        const int entry = static_cast<int>(a.page.div(pos)), slot = pos - entry * static_cast<int>(a.page.d);
+        int page = -1;
+        if (row >= 0 && row < a.B && entry < a.M) page = a.table[row * a.table_row + entry];
+        const bool ok = page >= 0 && page < a.num_pages;
+        const long long kat = page * a.kc_page + slot * a.kc_token, vat = page * a.vc_page + slot * a.vc_token;
+        __syncthreads();  // this buffer is next written behind the next token's barrier, past all its readers
+        for (int u = tid; u < units; u += blockDim.x) {
+            if (u >= rotated) {
+                if (!ok) break;
+                const int h = static_cast<int>(a.per_v.div(u - rotated)), j = u - rotated - h * static_cast<int>(a.per_v.d);
+                const uint16_t* from = static_cast<const uint16_t*>(a.v) + t * a.v_token + h * a.v_head;
+                if constexpr (kMode == kSingles)
+                    keep1<kF16, kE4m3>(a.vc, vat + h * a.vc_head + j, up1<kF16>(from[j]), a.v_inv);
+                else
+                    keep8<kF16, kE4m3>(a.vc, vat + h * a.vc_head + 8 * j,
+                                       widen<kF16>(*reinterpret_cast<const uint4*>(from + 8 * j)), a.v_inv);
+                continue;
+            }
+            const int h = static_cast<int>(a.per_head.div(u)), j = u - h * static_cast<int>(a.per_head.d);
+            const bool key = h < a.heads;
+            const int hq = h - a.heads;
+            if (key && !ok) continue;
+            const uint16_t* from = key ? static_cast<const uint16_t*>(a.k) + t * a.k_token + h * a.k_head
+                                       : static_cast<const uint16_t*>(a.q) + t * a.q_token + hq * a.q_head;
+            uint16_t* to = key ? nullptr : static_cast<uint16_t*>(a.q_out) + t * a.qo_token + hq * a.qo_head;
+            const long long kto = kat + h * a.kc_head;
+            const float nan = __int_as_float(0x7fc00000);
+            if constexpr (kMode == kSingles) {
+                auto put = [&](int d, float x) {
+                    if (key) keep1<kF16, kE4m3>(a.kc, kto + d, x, a.k_inv);
+                    else to[d] = down1<kF16>(ok ? x : nan);
+                };
+                if (j < pairs) {
+                    const int d0 = a.interleaved ? 2 * j : j, d1 = a.interleaved ? d0 + 1 : j + pairs;
+                    const float x = up1<kF16>(from[d0]), y = up1<kF16>(from[d1]);
+                    const float2 cs = turn[now][j];
+                    put(d0, x * cs.x - y * cs.y);
+                    put(d1, y * cs.x + x * cs.y);
+                } else {
+                    const int d = j + pairs;
+                    put(d, up1<kF16>(from[d]));
+                }
+            } else {
+                auto put = [&](int d, Eight& e) {
+                    if (key) {
+                        keep8<kF16, kE4m3>(a.kc, kto + d, e, a.k_inv);
+                        return;
+                    }
+                    if (!ok)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) e.x[i] = nan;
+                    store16<kF16>(to + d, e);
+                };
+                if constexpr (kMode == kHalves) {
+                    if (8 * j < pairs) {
+                        Eight x = widen<kF16>(*reinterpret_cast<const uint4*>(from + 8 * j));
+                        Eight y = widen<kF16>(*reinterpret_cast<const uint4*>(from + pairs + 8 * j));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 cs = turn[now][8 * j + i];
+                            const float lo = x.x[i] * cs.x - y.x[i] * cs.y;
+                            y.x[i] = y.x[i] * cs.x + x.x[i] * cs.y;
+                            x.x[i] = lo;
+                        }
+                        put(8 * j, x);
+                        put(pairs + 8 * j, y);
+                    } else {
+                        const int d = 8 * j + pairs;
+                        Eight x = widen<kF16>(*reinterpret_cast<const uint4*>(from + d));
+                        put(d, x);
+                    }
+                } else {
+                    Eight x = widen<kF16>(*reinterpret_cast<const uint4*>(from + 8 * j));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = 4 * j + i;
+                        if (p < pairs) {
+                            const float2 cs = turn[now][p];
+                            const float lo = x.x[2 * i] * cs.x - x.x[2 * i + 1] * cs.y;
+                            x.x[2 * i + 1] = x.x[2 * i + 1] * cs.x + x.x[2 * i] * cs.y;
+                            x.x[2 * i] = lo;
+                        }
+                    }
+                    put(8 * j, x);
+                }
+            }
+        }
+        now ^= 1;
+    }
+}
+
+template <Mode kMode, bool kF16>
+cudaError_t launch(const Append& a, bool e4m3, int grid, int threads, cudaStream_t stream) {
+    return e4m3 ? launch_overlapped(k_kv_append<kMode, kF16, true>, dim3(grid), threads, 0, stream, a)
+                : launch_overlapped(k_kv_append<kMode, kF16, false>, dim3(grid), threads, 0, stream, a);
+}
+template <bool kF16>
+cudaError_t launch(const Append& a, Mode mode, bool e4m3, int grid, int threads, cudaStream_t stream) {
+    switch (mode) {
+        case kSingles: return launch<kSingles, kF16>(a, e4m3, grid, threads, stream);
+        case kHalves: return launch<kHalves, kF16>(a, e4m3, grid, threads, stream);
+        default: return launch<kNeighbours, kF16>(a, e4m3, grid, threads, stream);
+    }
+}
+
+bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
+// Rows of 16-bit values at `p` that start on 16 bytes.
+bool on16(const void* p, long long token, long long head) { return at(p, 16) && token % 8 == 0 && head % 8 == 0; }
+
+}  // namespace
+
+bool kv_cache_ok(const estream_kv_cache* c) {
+    if (!c || c->elem < ESTREAM_KV_BF16 || c->elem > ESTREAM_KV_E4M3 || c->num_pages < 0 || c->num_pages > 1 << 30 ||
+        c->page_size < 1 || c->page_size > 1 << 30 || c->heads < 1 || c->heads > kKvMaxHeads || c->dim < 16 ||
+        c->dim > kKvMaxDim || c->dim % 16)
+        return false;
+    auto scale = [&](float s) { return s >= 0x1p-100f && s <= 0x1p100f && (c->elem == ESTREAM_KV_E4M3 || s == 1.0f); };
+    if (!scale(c->k_scale) || !scale(c->v_scale)) return false;
+    if (c->num_pages > 0 && (!at(c->k, 16) || !at(c->v, 16))) return false;
+    const long long unit = c->elem == ESTREAM_KV_E4M3 ? 16 : 8, most = 1ll << 40;
+    auto stride = [&](long long s, int n) { return n == 1 || (s >= c->dim && s <= most && s % unit == 0); };
+    return stride(c->k_page, c->num_pages) && stride(c->v_page, c->num_pages) && stride(c->k_token, c->page_size) &&
+           stride(c->v_token, c->page_size) && stride(c->k_head, c->heads) && stride(c->v_head, c->heads);
+}
+
+}  // namespace es
+
+using namespace es;
+
+extern "C" estream_status estream_kv_append(const estream_kv_cache* c, int elem, int T, const void* k, long long k_token,
+                                            long long k_head, const void* v, long long v_token, long long v_head,
+                                            const int32_t* positions, const int32_t* rows, const int32_t* table,
+                                            int B, int M, long long table_row, const void* q, long long q_token,
+                                            long long q_head, int Hq, void* q_out, long long qo_token,
+                                            long long qo_head, const float* inv_freq, int rot, int interleaved,
+                                            void* cuda_stream) {
+    NvtxRange range(kNvKvAppend, T);
+    if (!kv_cache_ok(c) || (elem != ESTREAM_KV_BF16 && elem != ESTREAM_KV_F16) ||
+        (c->elem != ESTREAM_KV_E4M3 && c->elem != elem) || T < 0 || T > 1 << 24 || B < 0 || M < 0 || table_row < 0 ||
+        Hq < 0 || Hq > kKvMaxHeads || rot < 0 || rot % 2 || rot > c->dim)
+        return ESTREAM_ERR_INVALID_ARG;
+    if (T == 0) return ESTREAM_OK;
+    const bool entries = B > 0 && M > 0;
+    if (!at(k, 2) || !at(v, 2) || !at(positions, 4) || (rows && !at(rows, 4)) || (entries && !at(table, 4)) ||
+        (Hq && (!at(q, 2) || !at(q_out, 2))) || (rot && !at(inv_freq, 4)))
+        return ESTREAM_ERR_INVALID_ARG;
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    const bool wide = on16(k, k_token, k_head) && on16(v, v_token, v_head) &&
+                      (!Hq || (on16(q, q_token, q_head) && on16(q_out, qo_token, qo_head)));
+    const bool neighbours = interleaved || rot == 0;
+    const Mode mode = !wide || (!neighbours && rot % 16) ? kSingles : neighbours ? kNeighbours : kHalves;
+    const int dim = c->dim;
+    const int per_head = mode == kSingles ? dim - rot / 2 : mode == kHalves ? rot / 16 + (dim - rot) / 8 : dim / 8;
+    const int per_v = mode == kSingles ? dim : dim / 8;
+    const Append a{k, v, q, q_out, c->k, c->v, k_token, k_head, v_token, v_head, q_token, q_head, qo_token, qo_head,
+                   c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head, positions, rows, table,
+                   inv_freq, table_row, 1.0f / c->k_scale, 1.0f / c->v_scale, T, entries ? B : 0, M, c->num_pages, Hq,
+                   c->heads, dim, rot, interleaved != 0, FastDiv(c->page_size), FastDiv(per_head), FastDiv(per_v)};
+    const int units = (c->heads + Hq) * per_head + c->heads * per_v;
+    const int threads = std::min(512, std::max(128, (units + 31) / 32 * 32));
+    const int grid = std::min(T, 1216);
+    const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    const bool e4m3 = c->elem == ESTREAM_KV_E4M3;
+    const cudaError_t rc = elem == ESTREAM_KV_F16 ? launch<true>(a, mode, e4m3, grid, threads, stream)
+                                                  : launch<false>(a, mode, e4m3, grid, threads, stream);
+    return rc == cudaSuccess ? ESTREAM_OK : ESTREAM_ERR_CUDA;
+}

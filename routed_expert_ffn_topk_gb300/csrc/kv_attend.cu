@@ -1,0 +1,685 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+// With z_i = scale (q . k_i): out = sum_i e^{z_i - m} v_i / l, l = sum_i e^{z_i - m}, m = max z.
+// (m, l, sum) of two sets of positions join as
+//   m = max(m1, m2), l = l1 e^{m1 - m} + l2 e^{m2 - m}, the sums alike,
+// so a sequence may be cut anywhere. Exponents are held in base 2.
+//
+// The work is all (row, key head) units' blocks of 16 positions, one unit behind
+// another; every CTA takes an equal, contiguous share of them, found from the
+// lengths on the device (so a captured graph keeps its balance as sequences grow). A
+// unit that ends inside a share is finished there; pieces of a unit that crosses
+// shares go through the workspace to a second kernel. In a share the warps take turns
+// at the blocks, each with a ring of its own filled by cp.async and with its own
+// (m, l, sum), and meet at a unit's end only.
+//
+// Every query head of a key head (16 rows of a matrix instruction) meets a key when
+// it is read. This is bound by HBM: a key and value of 128 bf16 are 512 bytes, and
+// their products 8 x 2 m16n8k16 for up to 16 query heads.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "estream_internal.h"
+#include "overlap.cuh"
+
+namespace es {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBlock = 16;  // positions a warp takes at a time
+constexpr int kRows = 16;   // query heads that meet a key together
+
+struct Attend {
+    const void* q;
+    void* out;
+    float* lse;
+    const uint8_t *k, *v;
+    const int32_t *table, *lens;
+    float *part, *ml;  // workspace: pieces' sums [2 C][16][kDim], and their (m, l) [2 C][16][2]
+    int2* split;       // [C]: unit that begins in this share and goes on past it (-1: none), and how many shares follow
+    long long q_row, q_head, out_row, out_head, table_row;
+    long long k_page, k_token, k_head, v_page, v_token, v_head;  // bytes
+    float scale, v_scale;  // scale * k_scale * log2 e
+    int B, Hq, heads, group, tiles, dim, chunks, M, max_len, num_pages, window;
+    int out_f16, q_words;  // type of q and out; q rows lie on 4 bytes
+    FastDiv page;
+};
+
+// What differs by the cache's type (ESTREAM_KV_*) and the padded width.
+template <int kElem, int kDim>
+struct Shape {
+    static constexpr bool kBytes = kElem == ESTREAM_KV_E4M3;
+    static constexpr bool kBf16 = kElem == ESTREAM_KV_BF16;  // the matrix instructions' type; else fp16
+    static constexpr int kRowBytes = kDim * (kBytes ? 1 : 2);
+    static constexpr int kStageBytes = 2 * kBlock * kRowBytes;  // keys, then values
+    static constexpr int kStages = kRowBytes == 64 ? 8 : kRowBytes == 128 ? 6 : kDim == 256 && kBytes ? 2 : 3;
+    static constexpr int kPitch = kDim + 4;  // floats; a warp's eight rows begin on different banks
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kSmem = kRing + kWarps * 8 * kPitch * 4 + kWarps * 8 * 8;
+    static constexpr int kResident = 2 * (kSmem + 1024 + 128) <= 228 * 1024 ? 2 : 1;  // 1 KB a CTA is the system's
+    // fp16 weights are 2^14 times as large as the formula's: their smallest normal
+    // value is then 2^-28 of the largest weight, not 2^-14
+    static constexpr float kBias = kBf16 ? 0.0f : 14.0f;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.0f : m; }
+
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <bool kBf16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kBf16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory, zeros when !there (then `from` is not read).
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+// Two E4M3 values (the low half) as fp16, exactly.
+__device__ __forceinline__ uint32_t from_e4m3(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    if constexpr (kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+// Where 16-byte chunk c of row r lies in a tile: eight rows' chunks of one c are on
+// different banks.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t in_tile(int r, int c) {
+    const int x = kRowBytes == 64 ? (r >> 1) & 3 : r & 7;
+    return r * kRowBytes + ((c ^ x) << 4);
+}
+
+// A row's attended positions [lo, len) and its blocks, which begin at a multiple of 16.
+struct Span {
+    int len, lo, first, blocks;
+};
+__device__ __forceinline__ Span span_of(const Attend& a, int b) {
+    Span s;
+    s.len = a.lens[b];
+    s.lo = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
+    s.first = s.lo & ~(kBlock - 1);
+    s.blocks = s.len > 0 && s.len <= a.max_len ? (s.len - s.first + kBlock - 1) / kBlock : 0;
+    return s;
+}
+
+// A unit (row, key head and tile of 16 query heads) of a CTA's share [begin, end).
+struct Unit {
+    int b, head;  // head = key head * tiles + tile
+    Span span;
+    long long start;  // its first block
+    __device__ __forceinline__ long long from(long long begin) const { return max(begin, start); }
+    __device__ __forceinline__ long long to(long long end) const { return min(end, start + span.blocks); }
+    // The next unit; there is one while start + blocks < end.
+    __device__ __forceinline__ void next(const Attend& a) {
+        start += span.blocks;
+        if (++head == a.heads * a.tiles) {
+            head = 0;
+            do span = span_of(a, ++b);
+            while (span.blocks == 0);
+        }
+    }
+};
+
+// One (m, l, sum) of a row's piece to the row's result.
+template <typename F>
+__device__ __forceinline__ void finish(const Attend& a, int b, int h, int d, float acc, float l, F&& bias_and_m) {
+    const float inv = l > 0.0f ? a.v_scale / l : l == 0.0f ? 0.0f : NAN;
+    if (d < a.dim) {
+        const float y = l == 0.0f ? 0.0f : acc * inv;
+        uint16_t* to = static_cast<uint16_t*>(a.out) + b * a.out_row + h * a.out_head + d;
+        *to = a.out_f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    }
+    if (d == 0 && a.lse)
+        a.lse[static_cast<long long>(b) * a.Hq + h] =
+            l == 0.0f ? -INFINITY : (bias_and_m() + log2f(l)) * 0.69314718055994531f;
+}
+
+template <int kElem, int kDim, bool kWhole>  // kWhole: page_size a multiple of 16, a block lies in one page
+__global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_attend(const Attend a) {
+    using S = Shape<kElem, kDim>;
+    constexpr int kSteps = kDim / 16;
+    constexpr int kChunks = S::kRowBytes / 16;         // of a padded row
+    constexpr int kPerCopy = kChunks < 32 ? 32 / kChunks : 1;  // rows that a warp's copy covers
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* sums = reinterpret_cast<float*>(smem + S::kRing);               // [kWarps][8][kPitch]
+    float2* stats = reinterpret_cast<float2*>(sums + kWarps * 8 * S::kPitch);  // [kWarps][8]
+    __shared__ long long scan[kWarps];
+    __shared__ Unit first_unit;
+    after_previous();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+    const int units = a.heads * a.tiles;  // of a row
+
+    // Rows with nothing to attend: zeros, or NaN where the length is out of range.
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const Span s = span_of(a, b);
+        if (s.blocks) continue;
+        const float fill = s.len == 0 ? 0.0f : NAN;
+        for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
+            const int h = i / a.dim, d = i - h * a.dim;
+            finish(a, b, h, d, fill, fill, [] { return 0.0f; });
+        }
+    }
+
+    // This CTA's share, and the unit it begins in.
+    const int per_thread = (a.B + kThreads - 1) / kThreads, mine = tid * per_thread, past = min(a.B, mine + per_thread);
+    long long count = 0;
+    for (int b = mine; b < past; ++b) count += span_of(a, b).blocks;
+    long long upto = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    long long total = 0, before = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) before = total;
+        total += scan[w];
+    }
+    total *= units;
+    before = (before + upto - count) * units;
+    const long long share = max(static_cast<long long>(kWarps), (total + gridDim.x - 1) / gridDim.x);
+    const long long begin = blockIdx.x * share, end = min(total, begin + share);
+    if (begin >= end) {
+        if (tid == 0) a.split[blockIdx.x] = make_int2(-1, 0);
+        return;
+    }
+    if (begin >= before && begin < before + count * units) {
+        Unit u;
+        u.b = mine;
+        u.start = before;
+        for (;; ++u.b) {
+            u.span = span_of(a, u.b);
+            const long long n = static_cast<long long>(u.span.blocks) * units;
+            if (begin < u.start + n) break;
+            u.start += n;
+        }
+        u.head = static_cast<int>((begin - u.start) / u.span.blocks);
+        u.start += static_cast<long long>(u.head) * u.span.blocks;
+        first_unit = u;
+    }
+    __syncthreads();
+
+    // The warp's loads run ahead of its products, over units' ends.
+    Unit ahead = first_unit;
+    long long next = ahead.from(begin) + warp;
+    bool more = true;
+    auto settle = [&] {  // the next block at or after `next` that is this warp's
+        while (next >= ahead.to(end)) {
+            if (ahead.start + ahead.span.blocks >= end) {
+                more = false;
+                return;
+            }
+            ahead.next(a);
+            next = ahead.start + warp;
+        }
+    };
+    // The page and the place in it of position lane % 16 of the next block; page -1:
+    // not attended; -2: out of range.
+    int page = -1, slot = 0;
+    auto look_up = [&] {
+        if (!more) return;
+        const int at = ahead.span.first + static_cast<int>(next - ahead.start) * kBlock + (lane & 15);
+        page = -1;
+        const int entry = static_cast<int>(a.page.div(at));
+        slot = at - entry * static_cast<int>(a.page.d);
+        if (at >= ahead.span.lo && at < ahead.span.len) {
+            page = a.table[ahead.b * a.table_row + entry];
+            if (page < 0 || page >= a.num_pages) page = -2;
+        }
+    };
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kStages * S::kStageBytes;
+    uint32_t bad = 0;  // by stage: a page out of range
+    auto issue = [&](int stage) {
+        if (more) {
+            const uint32_t to = ring + stage * S::kStageBytes;
+            const int h = ahead.head / a.tiles, c = lane % kChunks;
+            const uint8_t* kb = a.k + h * a.k_head + c * 16;
+            const uint8_t* vb = a.v + h * a.v_head + c * 16;
+            const bool in = c < a.chunks;
+            bad = (bad & ~(1u << stage)) | (__any_sync(~0u, page == -2) ? 1u << stage : 0u);
+            if constexpr (kWhole) {
+                const int lead = __reduce_max_sync(~0u, page);  // the block's page
+                const int slot0 = __shfl_sync(~0u, slot, 0);
+                kb += static_cast<long long>(max(lead, 0)) * a.k_page + slot0 * a.k_token;
+                vb += static_cast<long long>(max(lead, 0)) * a.v_page + slot0 * a.v_token;
+            }
+#pragma unroll
+            for (int i = 0; i < kBlock / kPerCopy; ++i) {
+                const int r = i * kPerCopy + lane / kChunks;
+                const int p = __shfl_sync(~0u, page, r);
+                const uint8_t *kf, *vf;
+                if constexpr (kWhole) {
+                    kf = kb + r * a.k_token;
+                    vf = vb + r * a.v_token;
+                } else {
+                    const int s = __shfl_sync(~0u, slot, r);
+                    kf = kb + max(p, 0) * a.k_page + s * a.k_token;
+                    vf = vb + max(p, 0) * a.v_page + s * a.v_token;
+                }
+                const bool there = p >= 0 && in;
+                copy16(to + in_tile<S::kRowBytes>(r, c), there ? kf : a.k, there);
+                copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, c), there ? vf : a.v, there);
+            }
+            next += kWarps;
+            settle();
+            look_up();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    settle();
+    look_up();
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) issue(s);
+
+    Unit u = first_unit;
+    int2 unfinished = make_int2(-1, 0);
+    int stage = 0;
+    for (;;) {
+        const long long from = u.from(begin), to = u.to(end);
+        const int kv_head = u.head / a.tiles, row0 = u.head % a.tiles * kRows;  // first query head of this tile in its group
+        const int rows = min(kRows, a.group - row0);
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float o[2 * kSteps][4];
+#pragma unroll
+        for (int n = 0; n < 2 * kSteps; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
+        bool poison = false;
+        if (from + warp < to) {
+            // Query fragments. An E4M3 key's four neighbouring values lie in one lane, so pairs
+            // (2t, 2t + 1) and (2t + 8, 2t + 9) of the product are values (4t, 4t + 1) and (4t + 2, 4t + 3).
+            uint32_t qa[kSteps][4];
+            float c[2] = {a.scale, a.scale};
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int h = g + 8 * r;
+                const uint16_t* qr = static_cast<const uint16_t*>(a.q) + u.b * a.q_row +
+                                     static_cast<long long>(kv_head * a.group + row0 + min(h, rows - 1)) * a.q_head;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int d = 16 * s + (S::kBytes ? 4 * t + 2 * i : 2 * t + 8 * i);
+                        uint32_t w = 0;
+                        if (d < a.dim && h < rows)
+                            w = a.q_words ? *reinterpret_cast<const uint32_t*>(qr + d)
+                                          : qr[d] | static_cast<uint32_t>(qr[d + 1]) << 16;
+                        qa[s][r + 2 * i] = w;
+                    }
+                if constexpr (S::kBytes) {
+                    // to fp16, by the power of two that puts the largest at 2^10 to 2^11
+                    auto wide = [&](uint32_t w) {
+                        return a.out_f16 ? __half22float2(*reinterpret_cast<__half2*>(&w))
+                                         : __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+                    };
+                    float top = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 f = wide(qa[s][r + 2 * i]);
+                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    const int e = min(126, max(-126, 137 - static_cast<int>(__float_as_uint(top) >> 23)));
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 f = wide(qa[s][r + 2 * i]);
+                            qa[s][r + 2 * i] = pack<false>(f.x * up, f.y * up);
+                        }
+                    c[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                }
+            }
+            const bool tall = rows > 8;
+            for (long long blk = from + warp; blk < to; blk += kWarps) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+                __syncwarp();  // every lane's copies are there, and every lane has read the stage that is filled next
+                issue(stage == 0 ? S::kStages - 1 : stage - 1);
+                const uint32_t kt = ring + stage * S::kStageBytes, vt = kt + kBlock * S::kRowBytes;
+                poison |= bad >> stage & 1;
+                stage = stage + 1 == S::kStages ? 0 : stage + 1;
+                float z[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[n][i] = 0.0f;
+                if constexpr (S::kBytes) {
+#pragma unroll
+                    for (int s = 0; s < kSteps; s += 2) {
+                        uint32_t r[4];
+                        ldmatrix(r, kt + in_tile<S::kRowBytes>(lane & 15, s + (lane >> 4)));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma<false>(z[i & 1], qa[s + i / 2], from_e4m3(r[i] & 0xffff), from_e4m3(r[i] >> 16));
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        uint32_t r[4];
+                        ldmatrix(r, kt + in_tile<S::kRowBytes>((lane & 7) + (lane >> 4) * 8, 2 * s + (lane >> 3 & 1)));
+                        mma<S::kBf16>(z[0], qa[s], r[0], r[1]);
+                        mma<S::kBf16>(z[1], qa[s], r[2], r[3]);
+                    }
+                }
+                const int at = u.span.first + static_cast<int>(blk - u.start) * kBlock;
+                const bool edge = at < u.span.lo || at + kBlock > u.span.len;
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x = z[n][i] * c[i / 2];
+                        if (edge) {
+                            const int p = at + 8 * n + 2 * t + (i & 1);
+                            if (p < u.span.lo || p >= u.span.len) x = -INFINITY;
+                        }
+                        z[n][i] = x;
+                        top[i / 2] = fmaxf(top[i / 2], x);
+                    }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+                }
+                if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float now = fmaxf(m[r], top[r]), shrink = exp2_fast(m[r] - finite_or_zero(now));
+                        m[r] = now;
+                        l[r] *= shrink;
+#pragma unroll
+                        for (int n = 0; n < 2 * kSteps; ++n) {
+                            o[n][2 * r] *= shrink;
+                            o[n][2 * r + 1] *= shrink;
+                        }
+                    }
+                }
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (r == 1 && !tall) {
+                        hi[1] = hi[3] = lo[1] = lo[3] = 0;
+                        break;
+                    }
+                    const float base = finite_or_zero(m[r]) - S::kBias;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float x = exp2_fast(z[n][2 * r] - base), y = exp2_fast(z[n][2 * r + 1] - base);
+                        l[r] += x + y;
+                        const uint32_t w = pack<S::kBf16>(x, y);
+                        hi[2 * n + r] = w;
+                        if constexpr (S::kBf16)  // what bf16 leaves of a weight, as a second term
+                            lo[2 * n + r] = pack<true>(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u));
+                    }
+                }
+                if constexpr (S::kBytes) {
+#pragma unroll
+                    for (int s = 0; s < kSteps; s += 2) {
+                        uint32_t r[4];
+                        ldmatrix_trans(r, vt + in_tile<S::kRowBytes>(lane & 15, s + (lane >> 4)));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // values (2g, 2g + 1) of positions 2t and 2t + 1: to pairs of positions
+                            const uint32_t p = __byte_perm(r[2 * i], 0, 0x3120), q = __byte_perm(r[2 * i + 1], 0, 0x3120);
+                            mma<false>(o[2 * (s + i)], hi, from_e4m3(p & 0xffff), from_e4m3(q & 0xffff));
+                            mma<false>(o[2 * (s + i) + 1], hi, from_e4m3(p >> 16), from_e4m3(q >> 16));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        uint32_t r[4];
+                        ldmatrix_trans(r, vt + in_tile<S::kRowBytes>(lane & 15, 2 * s + (lane >> 4)));
+                        mma<S::kBf16>(o[2 * s], hi, r[0], r[1]);
+                        mma<S::kBf16>(o[2 * s + 1], hi, r[2], r[3]);
+                        if constexpr (S::kBf16) {
+                            mma<true>(o[2 * s], lo, r[0], r[1]);
+                            mma<true>(o[2 * s + 1], lo, r[2], r[3]);
+                        }
+                    }
+                }
+            }
+        }
+        // The warps' pieces meet, eight rows at a time.
+        const bool whole = from == u.start && to == u.start + u.span.blocks;
+        const int piece = 2 * blockIdx.x + (from == u.start);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (8 * r >= rows) break;
+            l[r] += __shfl_xor_sync(~0u, l[r], 1);
+            l[r] += __shfl_xor_sync(~0u, l[r], 2);
+            float* mine_at = sums + (warp * 8 + g) * S::kPitch;
+#pragma unroll
+            for (int n = 0; n < 2 * kSteps; ++n) {
+                // the column of accumulator n's first value, and how far the second is from it
+                const int d = S::kBytes ? n / 2 * 16 + 4 * t + (n & 1) : n * 8 + 2 * t;
+                mine_at[d] = o[n][2 * r];
+                mine_at[d + (S::kBytes ? 2 : 1)] = o[n][2 * r + 1];
+            }
+            if (t == 0) stats[warp * 8 + g] = make_float2(m[r], poison ? NAN : l[r]);
+            __syncthreads();
+            for (int i = tid; i < min(8, rows - 8 * r) * kDim; i += kThreads) {
+                const int row = i / kDim, d = i % kDim;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * 8 + row].x);
+                const float base = finite_or_zero(top);
+                float acc = 0.0f, sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 s = stats[w * 8 + row];
+                    const float f = exp2_fast(s.x - base);
+                    acc += f * sums[(w * 8 + row) * S::kPitch + d];
+                    sum += f * s.y;
+                }
+                if (whole) {
+                    finish(a, u.b, kv_head * a.group + row0 + 8 * r + row, d, acc, sum, [&] { return top - S::kBias; });
+                } else {
+                    const long long at = static_cast<long long>(piece) * kRows + 8 * r + row;
+                    a.part[at * kDim + d] = acc;
+                    if (d == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, sum);
+                }
+            }
+            __syncthreads();
+        }
+        if (!whole && from == u.start)
+            unfinished = make_int2(u.b * units + u.head,
+                                   static_cast<int>((u.start + u.span.blocks - 1) / share) - static_cast<int>(blockIdx.x));
+        if (u.start + u.span.blocks >= end) break;
+        u.next(a);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (tid == 0) a.split[blockIdx.x] = unfinished;
+}
+
+// The pieces of the unit that begins in share blockIdx.x and ends in a later one:
+// the head piece of its share, then the leading pieces of those that follow. One
+// query head a block, one column a thread.
+template <int kDim>
+__global__ void __launch_bounds__(kDim) k_kv_join(const Attend a, float bias) {
+    after_previous();
+    const int2 split = a.split[blockIdx.x];
+    const int units = a.heads * a.tiles;
+    if (split.x < 0) return;
+    const int b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
+    const int row = blockIdx.y, d = threadIdx.x, lane = d % 32;
+    if (row >= min(kRows, a.group - row0)) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.ml);
+    auto at = [&](int i) {  // piece i's row
+        return static_cast<long long>(2 * (blockIdx.x + i) + (i == 0)) * kRows + row;
+    };
+    float top = -INFINITY;
+    for (int i = lane; i <= split.y; i += 32) top = fmaxf(top, ml[at(i)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float base = finite_or_zero(top);
+    float acc = 0.0f, sum = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i <= split.y; ++i) {
+        const float2 s = ml[at(i)];
+        const float f = exp2_fast(s.x - base);
+        acc += f * a.part[at(i) * kDim + d];
+        sum += f * s.y;
+    }
+    finish(a, b, head / a.tiles * a.group + row0 + row, d, acc, sum, [&] { return top - bias; });
+}
+
+int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// How a call is laid out: shares, and the workspace's parts.
+struct Layout {
+    int grid;
+    size_t ml, split, bytes;  // offsets behind the sums
+};
+Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int resident, int sms) {
+    const int group = Hq / c->heads, tiles = (group + kRows - 1) / kRows, kd = padded_dim(c->dim);
+    long long blocks = (static_cast<long long>(M) * c->page_size + kBlock - 1) / kBlock;
+    if (window > 0) blocks = std::min(blocks, window / kBlock + 2ll);
+    const long long most = (blocks * B * c->heads * tiles + kWarps - 1) / kWarps;
+    Layout l;
+    l.grid = static_cast<int>(std::max(1ll, std::min(most, static_cast<long long>(sms) * resident)));
+    l.ml = static_cast<size_t>(l.grid) * 2 * kRows * kd * 4;
+    l.split = l.ml + static_cast<size_t>(l.grid) * 2 * kRows * 8;
+    l.bytes = (l.split + static_cast<size_t>(l.grid) * 8 + 15) / 16 * 16;
+    return l;
+}
+
+template <int kElem, int kDim, bool kWhole>
+cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
+    using S = Shape<kElem, kDim>;
+    cudaError_t rc = cudaFuncSetAttribute(k_kv_attend<kElem, kDim, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (rc == cudaSuccess)
+        rc = launch_overlapped(k_kv_attend<kElem, kDim, kWhole>, dim3(grid), kThreads, S::kSmem, stream, a);
+    if (rc != cudaSuccess || grid == 1) return rc;
+    return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, kRows)), kDim, 0, stream, a, S::kBias);
+}
+template <int kElem, int kDim>
+cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
+    return whole ? launch<kElem, kDim, true>(a, grid, stream) : launch<kElem, kDim, false>(a, grid, stream);
+}
+template <int kElem>
+cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
+    switch (padded_dim(a.dim)) {
+        case 64: return launch<kElem, 64>(a, whole, grid, stream);
+        case 128: return launch<kElem, 128>(a, whole, grid, stream);
+        default: return launch<kElem, 256>(a, whole, grid, stream);
+    }
+}
+
+template <int kElem>
+int resident_of(int dim) {
+    switch (padded_dim(dim)) {
+        case 64: return Shape<kElem, 64>::kResident;
+        case 128: return Shape<kElem, 128>::kResident;
+        default: return Shape<kElem, 256>::kResident;
+    }
+}
+int resident(const estream_kv_cache* c) {
+    return c->elem == ESTREAM_KV_BF16  ? resident_of<ESTREAM_KV_BF16>(c->dim)
+           : c->elem == ESTREAM_KV_F16 ? resident_of<ESTREAM_KV_F16>(c->dim)
+                                       : resident_of<ESTREAM_KV_E4M3>(c->dim);
+}
+
+bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool sizes_ok(const estream_kv_cache* c, int B, int Hq, int M) {
+    return kv_cache_ok(c) && B >= 0 && Hq >= 1 && Hq % c->heads == 0 && Hq <= 1 << 16 && M >= 0 &&
+           static_cast<long long>(B) * Hq <= 1 << 24 && static_cast<long long>(M) * c->page_size < (1ll << 31) - 4096;
+}
+
+cudaError_t sm_count(int* sms) {
+    int dev = 0;
+    const cudaError_t rc = cudaGetDevice(&dev);
+    return rc != cudaSuccess ? rc : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+}  // namespace
+}  // namespace es
+
+using namespace es;
+
+extern "C" {
+
+size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* c, int B, int Hq, int M) {
+    int sms = 0;
+    if (!sizes_ok(c, B, Hq, M) || B == 0 || sm_count(&sms) != cudaSuccess) return 0;
+    return layout(c, B, Hq, M, 0, resident(c), sms).bytes;
+}
+
+estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int Hq, const void* q, long long q_row,
+                                 long long q_head, const int32_t* table, int M, long long table_row,
+                                 const int32_t* lens, float scale, int window, void* out, long long out_row,
+                                 long long out_head, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* cuda_stream) {
+    NvtxRange range(kNvKvAttend, B);
+    if (!sizes_ok(c, B, Hq, M) || (elem != ESTREAM_KV_BF16 && elem != ESTREAM_KV_F16) ||
+        (c->elem != ESTREAM_KV_E4M3 && c->elem != elem) || table_row < 0 || window < 0 ||
+        !(scale >= -3.402823466e38f && scale <= 3.402823466e38f))
+        return ESTREAM_ERR_INVALID_ARG;
+    if (B == 0) return ESTREAM_OK;
+    if (!at(q, 2) || !at(out, 2) || (M > 0 && !at(table, 4)) || !at(lens, 4) || (lse && !at(lse, 4)) || !at(workspace, 16))
+        return ESTREAM_ERR_INVALID_ARG;
+    const estream_status st = on_device();
+    if (st != ESTREAM_OK) return st;
+    int sms = 0;
+    if (sm_count(&sms) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    const Layout l = layout(c, B, Hq, M, window, resident(c), sms);
+    if (workspace_bytes < l.bytes) return ESTREAM_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int size = c->elem == ESTREAM_KV_E4M3 ? 1 : 2, group = Hq / c->heads;
+    const Attend a{q, out, lse, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), table, lens,
+                   reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.ml), reinterpret_cast<int2*>(ws + l.split),
+                   q_row, q_head, out_row, out_head, table_row, c->k_page * size, c->k_token * size, c->k_head * size,
+                   c->v_page * size, c->v_token * size, c->v_head * size,
+                   static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634), c->v_scale, B, Hq,
+                   c->heads, group, (group + kRows - 1) / kRows, c->dim, c->dim * size / 16, M,
+                   M * c->page_size, c->num_pages, window, elem == ESTREAM_KV_F16,
+                   at(q, 4) && q_row % 2 == 0 && q_head % 2 == 0, FastDiv(c->page_size)};
+    const bool whole = c->page_size % kBlock == 0;
+    const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t rc = c->elem == ESTREAM_KV_BF16  ? launch<ESTREAM_KV_BF16>(a, whole, l.grid, stream)
+                           : c->elem == ESTREAM_KV_F16 ? launch<ESTREAM_KV_F16>(a, whole, l.grid, stream)
+                                                       : launch<ESTREAM_KV_E4M3>(a, whole, l.grid, stream);
+    return rc == cudaSuccess ? ESTREAM_OK : ESTREAM_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -339,13 +339,6 @@ bool mx4_scale_ok(float s) { return s > 0.0f && s <= 3.402823466e38f; }
 bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 constexpr int kMaxWidth = 1 << 24;   // K and N: keeps a row's offsets in 32 bits
 constexpr int kMaxRows = 1 << 30;    // keeps a row index and what is added to it (a launch's stride) in 32 bits
-
-// ESTREAM_OK when the current device runs this library's kernels.
-estream_status on_device() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ESTREAM_ERR_CUDA;
-    return device_supported(dev) ? ESTREAM_OK : ESTREAM_ERR_UNSUPPORTED;
-}
 }  // namespace
 
 extern "C" {

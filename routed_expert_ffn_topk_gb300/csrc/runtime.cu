@@ -44,6 +44,11 @@ bool device_supported(int dev) {
         return false;
     return major == 10 && minor == 3;
 }
+estream_status on_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    return device_supported(dev) ? ESTREAM_OK : ESTREAM_ERR_UNSUPPORTED;
+}
 }  // namespace es
 
 using namespace es;
@@ -78,7 +83,8 @@ const NvtxNames& nvtx_names() {
         const char* text[kNvNames] = {"route build",      "routed experts",      "shared experts",
                                       "combine",          "layer",               "bank fill",
                                       "route from X",     "preload",             "4-bit quantise",
-                                      "4-bit dequantise", "4-bit weight scales", "4-bit product"};
+                                      "4-bit dequantise", "4-bit weight scales", "4-bit product",
+                                      "cache append",     "cache attend",        "sample"};
         for (int i = 0; i < kNvNames; ++i) r.name[i] = nvtxDomainRegisterStringA(r.dom, text[i]);
         return r;
     }();
@@ -89,7 +95,8 @@ const NvtxNames& nvtx_names() {
 void es::nvtx_push(int name, long long payload) {
     static const uint32_t color[kNvNames] = {0xff2e9e44, 0xff2a6fdb, 0xff1aa3a3, 0xff8a4fd0,
                                              0xff808080, 0xffe08a1e, 0xff2e9e44, 0xffe08a1e,
-                                             0xffb8860b, 0xffb8860b, 0xffb8860b, 0xff2a6fdb};
+                                             0xffb8860b, 0xffb8860b, 0xffb8860b, 0xff2a6fdb,
+                                             0xff1aa3a3, 0xff8a4fd0, 0xff2e9e44};
     const NvtxNames& n = nvtx_names();
     nvtxEventAttributes_t at = {};
     at.version = NVTX_VERSION;
@@ -467,7 +474,7 @@ const char* estream_status_string(estream_status s) {
     return "unknown status";
 }
 
-int estream_version(void) { return 10301; }
+int estream_version(void) { return 10400; }
 
 size_t estream_route_workspace_bytes(int T, int E, int k, int P) {
     if (T < 0 || E < 1 || k < 1 || P < 0 || P > kMaxP) return 0;

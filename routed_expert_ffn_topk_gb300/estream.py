@@ -27,6 +27,9 @@ PAIR_MIN_ROWS = 160
 DECODE_MAX_T = 32
 FP4_E4M3X16, FP4_E8M0X32 = 0, 1
 _MX4_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+KV_BF16, KV_F16, KV_E4M3 = 0, 1, 2
+_KV_ELEM = {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.float8_e4m3fn: KV_E4M3}
+SAMPLE_MAX_V = 393216
 STATE_NAMES = {0: "Available", 1: "Filling", 2: "Ready", 3: "InUse"}
 
 
@@ -64,6 +67,17 @@ class Stats(ctypes.Structure):
         ("groups_hit", ctypes.c_int),
         ("ms_io_busy", ctypes.c_double),
         ("hidden_fraction", ctypes.c_double), ("bubble_rate", ctypes.c_double),
+    ]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("elem", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("k_page", ctypes.c_longlong), ("k_token", ctypes.c_longlong), ("k_head", ctypes.c_longlong),
+        ("v_page", ctypes.c_longlong), ("v_token", ctypes.c_longlong), ("v_head", ctypes.c_longlong),
     ]
 
 
@@ -107,6 +121,11 @@ SIGNATURES = {
     "estream_mx4_weight_scales": (_I, [_P, _I, _I, _I, _I, _P, _P]),
     "estream_mx4_product": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _P, _I, _L, _P]),
     "estream_mx4_error": (_I, [_P]),
+    "estream_kv_append": (_I, [_P, _I, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _I, _I, _L, _P, _L, _L, _I, _P, _L, _L,
+                              _P, _I, _I, _P]),
+    "estream_kv_attend_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "estream_kv_attend": (_I, [_P, _I, _I, _I, _P, _L, _L, _P, _I, _L, _P, _F, _I, _P, _L, _L, _P, _P, _SZ, _P]),
+    "estream_sample_tokens": (_I, [_P, _I, _L, _I, _I, _P, _F, _P, _I, _P, _F, _P, _F, _P, _P, _P, _P]),
     "estream_set_timing": (_I, [_P, _I]),
     "estream_reset_stats": (_I, [_P]),
     "estream_last_stats": (_I, [_P, ctypes.POINTER(Stats)]),
@@ -767,6 +786,217 @@ def mx4_error(device=None, stream=None) -> int:
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(device):
         return lib().estream_mx4_error(_stream(stream, device))
+
+
+# ---------------------------------------------------------------------------
+# paged key-value cache
+# ---------------------------------------------------------------------------
+
+class PagedKV:
+    """Keys and values in pages: k, v [pages, page_size, heads, dim] (bf16, fp16 or
+    float8_e4m3fn; dim contiguous, the other strides any, so a cache stored head by
+    head is given as a transposed view). With E4M3 the value of an element is the
+    element times k_scale or v_scale. The tensors stay the caller's; they are kept
+    alive by this object."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        elem = _KV_ELEM.get(k.dtype)
+        if elem is None or v.dtype != k.dtype or not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be bf16, fp16 or float8_e4m3fn, of one type on one CUDA device")
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [pages, page_size, heads, dim]")
+        pages, page, heads, dim = k.shape
+        if page < 1 or not 1 <= heads <= 1024 or dim % 16 or not 16 <= dim <= 256 or max(pages, page) > 1 << 30:
+            raise ValueError("1 to 1024 heads, dim a multiple of 16 up to 256, and pages of at least one token")
+        unit = 16 // k.element_size()
+        for t in (k, v):
+            if t.stride(3) != 1 or t.data_ptr() % 16 or any(
+                    n > 1 and (s < dim or s % unit) for n, s in zip(t.shape[:3], t.stride()[:3])):
+                raise ValueError("rows of dim must be contiguous, start on 16 bytes and not overlap")
+        if not all(2.0 ** -100 <= s <= 2.0 ** 100 and (elem == KV_E4M3 or s == 1.0) for s in (k_scale, v_scale)):
+            raise ValueError("scales must be between 2^-100 and 2^100, and 1 for 16-bit caches")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
+        self.dtype, self.device, self.heads, self.dim, self.page_size = k.dtype, k.device, heads, dim, page
+        self._desc = KvCache(k.data_ptr(), v.data_ptr(), elem, pages, page, heads, dim, k_scale, v_scale,
+                             *k.stride()[:3], *v.stride()[:3])
+        self._ref = ctypes.byref(self._desc)
+        self._workspaces = {}
+
+    def attend_workspace_bytes(self, B: int, Hq: int, M: int) -> int:
+        """Bytes of kv_attend's workspace for B rows of Hq heads and tables of M pages."""
+        n = self._workspaces.get((B, Hq, M))
+        if n is None:
+            with torch.cuda.device(self.device):
+                n = lib().estream_kv_attend_workspace_bytes(self._ref, B, Hq, M)
+            if len(self._workspaces) < 256:
+                self._workspaces[B, Hq, M] = n
+        return n
+
+
+def _kv_heads(t: torch.Tensor, n: int, heads: int | None, cache: PagedKV, name: str, dtype=None):
+    """Checks [n, heads, dim] next to a cache; its strides of rows and heads."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != n or (heads is not None and shape[1] != heads) or shape[2] != cache.dim:
+        raise ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {cache.dim}]")
+    if (t.dtype is not dtype if dtype is not None else
+            t.dtype is not cache.dtype and (cache._desc.elem != KV_E4M3 or t.dtype not in (torch.bfloat16, torch.float16))):
+        raise ValueError(f"{name} must be of the cache's type, or bf16 or fp16 next to an E4M3 cache, like the call's other rows")
+    if st[2] != 1 or t.device != cache.device:
+        raise ValueError(f"{name} must have contiguous rows of dim, on the cache's device")
+    return st[0], st[1]
+
+
+def _kv_table(table: torch.Tensor, cache: PagedKV) -> int:
+    """Elements between a page table's rows."""
+    shape, st = table.shape, table.stride()
+    if len(shape) != 2 or table.dtype is not torch.int32 or table.device != cache.device or (shape[1] > 1 and st[1] != 1):
+        raise ValueError("table must be [B, M] int32 with contiguous rows, on the cache's device")
+    return st[0]
+
+
+def _kv_ints(t: torch.Tensor, n: int, name: str, cache: PagedKV) -> int:
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != cache.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be [{n}] int32, contiguous, on the cache's device")
+    return t.data_ptr()
+
+
+def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, table: torch.Tensor,
+              rows: torch.Tensor | None = None, q: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
+              interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Stores keys and values [T, heads, dim] of new tokens at their positions [T]
+    int32 of the sequences whose pages are table [B, M] int32 (rows [T]: the
+    tokens' table rows; without it token t has row t). With inv_freq [rot / 2]
+    fp32 the keys, and q [T, Hq, dim], are rotated by position; returns the rotated
+    queries (q_out, which may be q). A token with a negative position is skipped;
+    one without a valid page is not stored and its queries become NaNs."""
+    T = k.shape[0]
+    ks = _kv_heads(k, T, cache.heads, cache, "k")
+    vs = _kv_heads(v, T, cache.heads, cache, "v", k.dtype)
+    table_row = _kv_table(table, cache)
+    B, M = table.shape
+    if rows is None and B < T:
+        raise ValueError("table must have a row for each token, or rows must name them")
+    pp = _kv_ints(positions, T, "positions", cache)
+    rp = None if rows is None else _kv_ints(rows, T, "rows", cache)
+    qp = op = fp = None
+    qs = os_ = (0, 0)
+    Hq = rot = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _kv_heads(q, T, None, cache, "q", k.dtype)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cache.dim), dtype=q.dtype, device=q.device)
+        os_ = _kv_heads(q_out, T, Hq, cache, "q_out", k.dtype)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or rot > cache.dim \
+                or inv_freq.device != cache.device or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be [rot / 2] fp32, contiguous, with rot at most dim, on the cache's device")
+        fp = inv_freq.data_ptr()
+    with _on(k):
+        st = lib().estream_kv_append(cache._ref, _KV_ELEM[k.dtype], T, k.data_ptr(), *ks, v.data_ptr(), *vs, pp, rp,
+                                     table.data_ptr(), B, M, table_row, qp, *qs, Hq, op, *os_, fp, rot,
+                                     1 if interleaved else 0, _stream(stream, cache.device))
+    if st:
+        _check(st, "estream_kv_append")
+    return q_out
+
+
+def kv_attend(cache: PagedKV, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+              window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per row, q [B, Hq, dim], over the first lens [B]
+    int32 positions (the last `window` of them, if given) of the sequence whose
+    pages are table [B, M] int32: [B, Hq, dim], and the logarithms of the sums of
+    exponentials into lse [B, Hq] fp32. scale: 1 / sqrt(dim) unless given. Rows
+    that share a sequence (the tokens of a prompt) may share a table row
+    (table.expand). workspace: uint8, cache.attend_workspace_bytes(B, Hq, M) of
+    them, for this call alone until it ends (allocated when not given)."""
+    B = q.shape[0]
+    qs = _kv_heads(q, B, None, cache, "q")
+    Hq, dev = q.shape[1], cache.device
+    if Hq < 1 or Hq % cache.heads:
+        raise ValueError(f"q must have a multiple of {cache.heads} heads")
+    table_row = _kv_table(table, cache)
+    M = table.shape[1]
+    if table.shape[0] != B:
+        raise ValueError("table must have a row for each row of q")
+    lp = _kv_ints(lens, B, "lens", cache)
+    if out is None:
+        out = torch.empty((B, Hq, cache.dim), dtype=q.dtype, device=dev)
+    os_ = _kv_heads(out, B, Hq, cache, "out", q.dtype)
+    ep = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or tuple(lse.shape) != (B, Hq) or lse.device != dev or not lse.is_contiguous():
+            raise ValueError(f"lse must be [{B}, {Hq}] fp32, contiguous, on the cache's device")
+        ep = lse.data_ptr()
+    if window < 0:
+        raise ValueError("window must not be negative")
+    n = cache.attend_workspace_bytes(B, Hq, M)
+    if workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.dtype is not torch.uint8 or workspace.numel() < n \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must hold {n} bytes (uint8, contiguous) on the cache's device")
+    with _on(q):
+        st = lib().estream_kv_attend(cache._ref, _KV_ELEM[q.dtype], B, Hq, q.data_ptr(), *qs, table.data_ptr(), M,
+                                     table_row, lp, cache.dim ** -0.5 if scale is None else scale, window,
+                                     out.data_ptr(), *os_, ep, workspace.data_ptr(), n, _stream(stream, dev))
+    if st:
+        _check(st, "estream_kv_attend")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# sampling
+# ---------------------------------------------------------------------------
+
+def _choice(x, B: int, dtype, name: str, device):
+    """A choice of all rows, or a tensor with one for each: the number and the pointer."""
+    if not isinstance(x, torch.Tensor):
+        return x, None
+    if x.dtype is not dtype or x.dim() != 1 or x.shape[0] != B or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name} must be a number or [{B}] {dtype}, contiguous, on the logits' device")
+    return 0, x.data_ptr()
+
+
+def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                  out: torch.Tensor | None = None, prob: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The next token of each row of logits [B, V] (bf16, fp16 or fp32), [B] int32, from
+    the random numbers u [B] fp32 in [0, 1): temperature, then the top_k largest (0:
+    all), then of those the likeliest with top_p of the weight, then those with at
+    least min_p of the largest's probability (rows may be one expanded row); the token is the first in the vocabulary's
+    order whose cumulative probability exceeds u, and its probability goes to
+    prob [B] fp32. Temperature 0 takes the largest logit. Each choice is a number or a
+    tensor [B] (fp32; top_k int32). A row without a finite largest logit gives -1."""
+    elem = _MX4_ELEM.get(logits.dtype)
+    if elem is None or not logits.is_cuda:
+        raise ValueError("logits must be a bf16, fp16 or fp32 CUDA tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-d with contiguous rows")
+    B, V = logits.shape
+    ld, dev = logits.stride(0), logits.device
+    if not 1 <= V <= SAMPLE_MAX_V:
+        raise ValueError(f"a vocabulary must have 1 to {SAMPLE_MAX_V} tokens")
+    _, up = _choice(u, B, torch.float32, "u", dev)
+    if up is None:
+        raise ValueError("u must be a tensor with a random number for each row")
+    choices = (*_choice(temperature, B, torch.float32, "temperature", dev), *_choice(top_k, B, torch.int32, "top_k", dev),
+               *_choice(top_p, B, torch.float32, "top_p", dev), *_choice(min_p, B, torch.float32, "min_p", dev))
+    if out is None:
+        out = torch.empty(B, dtype=torch.int32, device=dev)
+    elif out.dtype is not torch.int32 or tuple(out.shape) != (B,) or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be [{B}] int32, contiguous, on the logits' device")
+    pp = None if prob is None else _choice(prob, B, torch.float32, "prob", dev)[1]
+    with _on(logits):
+        st = lib().estream_sample_tokens(logits.data_ptr(), elem, ld, B, V, up, *choices, out.data_ptr(), pp,
+                                         _stream(stream, dev))
+    if st:
+        _check(st, "estream_sample_tokens")
+    return out
 
 
 def set_timing(ctx, on: bool) -> None:
