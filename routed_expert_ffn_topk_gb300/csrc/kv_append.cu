@@ -4,9 +4,12 @@
 // Pair i of a rotated row, (a, b), becomes (a cos t - b sin t, b cos t + a sin t)
 // with t = position * inv_freq[i]. Far positions make many turns, of which only the
 // last, unfinished one counts: inv_freq / 2 pi is taken to 64 fractional bits, where
-// the product with the position drops whole turns by itself, and the top 32 bits
-// that are left go to sincospi. The error is 2^-53 position inv_freq / 2 pi
-// (double's, of the quotient) + 2^-32 turns.
+// the product with the position drops whole turns by itself. Of what is left the top 32
+// bits are taken: a quarter turn and a rest of at most pi / 4, whose sine and cosine
+// are Taylor series with the leading terms in two floats each, right to about 0.6 of
+// fp32's half step (sincospi of the fraction as one float is off by four times that,
+// which an 8-bit cache's rounding borders show). The angle's error is 2^-53 position
+// inv_freq / 2 pi (double's, of the quotient) + 2^-33 turns.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -102,6 +105,35 @@ __device__ __forceinline__ void keep1(void* base, long long at, float x, float i
     else static_cast<uint16_t*>(base)[at] = down1<kF16>(x);
 }
 
+// cos, sin of a fraction of a turn, 32 bits.
+__device__ __forceinline__ float2 cos_sin(uint32_t turn) {
+    const uint32_t quarter = (turn + 0x20000000u) >> 30;
+    const int rest = static_cast<int>(turn - (quarter << 30));  // of 2^32, in [-2^29, 2^29)
+    const float r = static_cast<float>(rest), r_low = static_cast<float>(rest - static_cast<int>(r));
+    constexpr float kUnit = 1.4629180e-9f;  // 2 pi / 2^32, rounded, and what that leaves
+    constexpr float kUnitLow = static_cast<float>(1.4629180792671596e-9 - static_cast<double>(kUnit));
+    const float x = r * kUnit, x_low = fmaf(r, kUnit, -x) + fmaf(r, kUnitLow, r_low * kUnit);
+    const float q = x * x, q_low = fmaf(x, x, -q) + 2.0f * x * x_low;
+    // x - x^3/6 + x^5/120 - ... : next term x^13/13! < 2^-36
+    float s = fmaf(q, -1.0f / 39916800.0f, 1.0f / 362880.0f);
+    s = fmaf(q, s, -1.0f / 5040.0f);
+    s = fmaf(q, s, 1.0f / 120.0f);
+    s = fmaf(q, s, -1.0f / 6.0f);
+    s = x + fmaf(x * q, s, x_low);
+    // 1 - x^2/2 + x^4/24 - ... : next term x^12/12! < 2^-32
+    float c = fmaf(q, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+    c = fmaf(q, c, -1.0f / 720.0f);
+    c = fmaf(q, c, 1.0f / 24.0f);
+    const float lead = fmaf(q, -0.5f, 1.0f), lead_low = fmaf(q, -0.5f, 1.0f - lead);
+    c = lead + fmaf(q * q, c, fmaf(q_low, -0.5f, lead_low));
+    if (quarter & 1) {
+        const float t = c;
+        c = -s;
+        s = t;
+    }
+    return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
+}
+
 // How a thread's unit of work lies in a row: one pair or value; eight pairs whose
 // halves are rot / 2 apart (or eight values that are not rotated); eight values
 // that hold four neighbouring pairs.
@@ -126,10 +158,8 @@ __global__ void __launch_bounds__(512) k_kv_append(const Append a) {
         const int pos = a.positions[t], row = a.rows ? a.rows[t] : t;
         if (pos < 0) continue;  // padding: the whole block
         if (tid < pairs) {
-            const int32_t top = static_cast<int32_t>((per_position * static_cast<uint64_t>(pos)) >> 32);
-            float s, c;
-            sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
-            turn[now][tid] = make_float2(c, s);
+            const uint64_t angle = per_position * static_cast<uint64_t>(pos);
+            turn[now][tid] = cos_sin(static_cast<uint32_t>((angle + 0x80000000u) >> 32));
         }
         const int entry = static_cast<int>(a.page.div(pos)), slot = pos - entry * static_cast<int>(a.page.d);
         int page = -1;

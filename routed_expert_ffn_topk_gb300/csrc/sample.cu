@@ -7,17 +7,22 @@
 // weights are integers, 2^42 for the largest, within 2^-38 of their value or one unit, and
 // their sums are exact and the same in every order.
 //
-// A cluster of CTAs holds a row's logits in its shared memory (they are read from
-// HBM once) and goes over them in passes, between which the CTAs exchange a few
-// numbers. A cut (the k-th largest logit, or the logit at which top_p of the weight
-// is reached) is found by bins: first of equal width in the logit, which spreads
-// the logits over the bins, then, inside the bin with the cut, of equal width in
-// the ordered bit pattern until a bin is a single value.
+// A cluster of CTAs holds a row's logits in its shared memory, so they are read from HBM
+// once, and goes over them in passes, between which the CTAs exchange a few numbers.
+//
+// A cut (the k-th largest logit, or the one at which top_p of the weight is reached)
+// is found by bins of equal width in the logit below the largest, counted and weighed by
+// shared-memory atomics and added up over the cluster. Where few tokens lie up to
+// the cut's bin, as after most prompts, they are gathered in one CTA, which sorts
+// them and does the rest alone. Else the bin with the cut is divided again until its tokens
+// can be sorted or are all equal, and the kept tokens are weighed and searched
+// where they are.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "estream_internal.h"
 #include "overlap.cuh"
@@ -28,9 +33,11 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kMaxCtas = 8;  // of a cluster
-constexpr int kOne = 42;     // log2 of the largest weight
+constexpr int kBins = kThreads;  // one a thread
+constexpr int kMaxCtas = 8;      // of a cluster
+constexpr int kFew = 2 * kThreads;  // tokens that one CTA sorts
+constexpr int kParts = 64;       // of a CTA's logits, weighed apart
+constexpr int kOne = 42;         // log2 of the largest weight
 
 struct Sample {
     const void* logits;
@@ -47,11 +54,15 @@ struct Sample {
 };
 
 template <int kElem>
-__device__ __forceinline__ float widen(const void* p, long long i) {
-    if constexpr (kElem == ESTREAM_MX4_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    else if constexpr (kElem == ESTREAM_MX4_F16) return __half2float(static_cast<const __half*>(p)[i]);
-    else return static_cast<const float*>(p)[i];
-}
+struct Elem {
+    static constexpr int kBytes = kElem == ESTREAM_MX4_F32 ? 4 : 2;
+    static constexpr int kPer = 16 / kBytes;  // in 16 bytes
+    static __device__ __forceinline__ float at(const void* p, int i) {
+        if constexpr (kElem == ESTREAM_MX4_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+        else if constexpr (kElem == ESTREAM_MX4_F16) return __half2float(static_cast<const __half*>(p)[i]);
+        else return static_cast<const float*>(p)[i];
+    }
+};
 
 // Bit patterns in the order of the values, -0 as 0, NaN above all.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -100,6 +111,12 @@ struct Weights {
         const uint64_t w = parts(l, s);
         return (w + (1ull << s >> 1)) >> s;
     }
+    // A kept token's probability, from its weight before that became a whole number of units.
+    __device__ __forceinline__ float share(float l, uint64_t whole) const {
+        int s;
+        const double w = static_cast<double>(parts(l, s));
+        return static_cast<float>(w / (static_cast<double>(1ull << s) * static_cast<double>(whole)));
+    }
 };
 
 template <typename T, typename F>
@@ -112,89 +129,119 @@ template <typename T>
 __device__ __forceinline__ T add(T a, T b) {
     return a + b;
 }
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 
-struct Exchange {  // a CTA's numbers that its cluster reads
-    uint64_t best;   // key of its largest logit, then the complement of its index
-    float least;     // its smallest finite logit
-    uint32_t lo, hi; // keys of a bin
-    uint64_t mass;
-    uint32_t ties;
+// The cut: kept are logits above `at`, and of those equal to it, `all` in number, the
+// first `ties` in the vocabulary's order.
+struct Cut {
+    float at;
+    uint32_t ties, all;
 };
 
-// The cut: kept are logits with key > tau, and the first `ties` in the vocabulary's
-// order of those with key == tau.
-struct Cut {
-    uint32_t tau, ties;
+// What a search found: nothing, all tokens up to the cut's bin, listed in the leading CTA, or the cut.
+enum Found { kNothing, kListed, kFound };
+
+struct Exchange {  // a CTA's numbers that its cluster reads
+    float top, least;  // its largest logit (NaN if it has one), and smallest finite one
+    int first;         // its first largest logit's index
+    uint32_t lo, hi;   // keys of a bin
+    uint64_t mass;
+    uint32_t ties;
+    Cut cut;
 };
 
 struct Shared {
     uint64_t table[256];
-    uint64_t bins[2][kBins];  // of this CTA, read by its cluster; used in turn
+    uint64_t mass[2][kBins];  // of this CTA, read by its cluster; used in turn
+    uint32_t count[2][kBins];
+    uint64_t list[kFew];      // the leading CTA's: tokens to sort
+    uint64_t part[kParts];
+    uint32_t part_ties[kParts];
     uint64_t warp[kWarps];
     uint32_t warp2[kWarps];
-    uint64_t found[2];
+    uint64_t before, chosen;
+    uint32_t bin, members, upto, listed;
     double min_below;         // temperature ln(min_p)
     float c, c_low;           // log2 e / temperature
     Exchange exchange[2];     // used in turn
 };
 
+// Ascending, n <= kFew values; those past n are free and become ~0. Pairs that are
+// 32 apart or less stay inside a warp's 64 values, so only wider steps need the CTA's barrier.
+__device__ __forceinline__ void sort(uint64_t* v, int n) {
+    const int tid = threadIdx.x;
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kThreads) v[i] = ~0ull;
+    __syncthreads();
+    for (int run = 2; run <= size; run *= 2) {
+        for (int step = run / 2; step; step /= 2) {
+            if (tid < size / 2) {
+                const int i = 2 * tid - (tid & (step - 1)), j = i + step;
+                const uint64_t x = v[i], y = v[j];
+                if ((x > y) == ((i & run) == 0)) {
+                    v[i] = y;
+                    v[j] = x;
+                }
+            }
+            if (step > 32 || (step == 1 && run >= 64)) __syncthreads();
+            else __syncwarp();
+        }
+    }
+    __syncthreads();
+}
+
 template <int kElem>
-__global__ void __launch_bounds__(kThreads) k_sample(const Sample a) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
+    using E = Elem<kElem>;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
-    float* logits = reinterpret_cast<float*>(raw + (sizeof(Shared) + 15) / 16 * 16);
+    uint8_t* logits = raw + (sizeof(Shared) + 15) / 16 * 16;
     after_previous();
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int first = rank * a.slice, n = max(0, min(a.slice, a.V - first));
+
+    // The logits come to shared memory.
+    {
+        const uint8_t* from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
+        const int vec = a.wide ? n / E::kPer : 0;
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(logits));
+        for (int i = tid; i < vec; i += kThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * i), "l"(from + 16ll * i) : "memory");
+        for (int i = vec * E::kPer + tid; i < n; i += kThreads) {
+            if constexpr (E::kBytes == 4) reinterpret_cast<uint32_t*>(logits)[i] = reinterpret_cast<const uint32_t*>(from)[i];
+            else reinterpret_cast<uint16_t*>(logits)[i] = reinterpret_cast<const uint16_t*>(from)[i];
+        }
+    }
     const float given = a.temperatures ? a.temperatures[row] : a.temperature, temperature = given > 0x1p100f ? 0x1p100f : given;
     const int top_k = a.top_ks ? a.top_ks[row] : a.top_k;
     const float top_p = a.top_ps ? a.top_ps[row] : a.top_p;
     const float min_p = a.min_ps ? a.min_ps[row] : a.min_p;
-
+    const bool greedy = !(temperature > 0x1p-100f);
+    const bool use_p = !(top_p >= 1.0f);
+    const bool use_k = top_k > 0 && top_k < a.V;
     // in 64 bits by one thread: an SM does two such operations a clock
     if (tid == kThreads - 1) {
         const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 0x1p-100f));
         sh.c = static_cast<float>(c);
         sh.c_low = static_cast<float>(c - static_cast<double>(sh.c));
         if (min_p > 0.0f && min_p < 1.0f) sh.min_below = static_cast<double>(temperature) * log(static_cast<double>(min_p));
-    }
-
-    int turn = 0;  // of the exchanges: a number is written again only after a further meeting of the cluster
-    // One value of every CTA, joined.
-    auto across = [&](auto pick, auto join) {
-        cluster.sync();
-        auto v = pick(*cluster.map_shared_rank(&sh.exchange[turn], 0));
-        for (int r = 1; r < ctas; ++r) v = join(v, pick(*cluster.map_shared_rank(&sh.exchange[turn], r)));
-        turn ^= 1;
-        return v;
-    };
-
-    // The logits, and the largest of them.
-    uint64_t best = 0;
-    float least = INFINITY;
-    {
-        const uint8_t* from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * (kElem == ESTREAM_MX4_F32 ? 4 : 2);
-        constexpr int kPer = kElem == ESTREAM_MX4_F32 ? 4 : 8;
-        auto take = [&](int i, float x) {
-            logits[i] = x;
-            best = max(best, static_cast<uint64_t>(key_of(x)) << 32 | ~static_cast<uint32_t>(first + i));
-            if (x > -INFINITY) least = fminf(least, x);
-        };
-        const int vec = a.wide ? n / kPer * kPer : 0;
-        for (int i = tid * kPer; i < vec; i += kThreads * kPer) {
-            const uint4 w = *reinterpret_cast<const uint4*>(from + static_cast<size_t>(i) * (16 / kPer));
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) take(i + j, widen<kElem>(&w, j));
-        }
-        for (int i = vec + tid; i < n; i += kThreads) take(i, widen<kElem>(from, i));
-    }
-    best = warp_reduce(best, [](uint64_t x, uint64_t y) { return max(x, y); });
-    least = warp_reduce(least, [](float x, float y) { return fminf(x, y); });
-    if (lane == 0) {
-        sh.warp[warp] = best;
-        sh.warp2[warp] = __float_as_uint(least);
+        sh.listed = 0;
     }
     if (tid < 256) {  // the table
         uint64_t v = 1ull << 63;
@@ -203,27 +250,68 @@ __global__ void __launch_bounds__(kThreads) k_sample(const Sample a) {
             if (tid >> (7 - j) & 1) v = __umul64hi(v, kRoots[j] << 1);
         sh.table[tid] = (v + (1ull << (62 - kOne))) >> (63 - kOne);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    if (tid == 0) {
-        Exchange& e = sh.exchange[turn];
-        e.best = 0;
-        e.least = INFINITY;
-        for (int w = 0; w < kWarps; ++w) {
-            e.best = max(e.best, sh.warp[w]);
-            e.least = fminf(e.least, __uint_as_float(sh.warp2[w]));
-        }
-    }
-    const int seen = turn;
-    best = across([](const Exchange& e) { return e.best; }, [](uint64_t x, uint64_t y) { return max(x, y); });
-    least = INFINITY;
-    for (int r = 0; r < ctas; ++r) least = fminf(least, cluster.map_shared_rank(&sh.exchange[seen], r)->least);
 
-    const uint32_t top_key = static_cast<uint32_t>(best >> 32);
-    const float top = value_of(top_key);
-    const bool none = !(fabsf(top) < INFINITY) || top_key == ~0u, greedy = !(temperature > 0x1p-100f);
+    auto at = [&](int i) { return E::at(logits, i); };
+    // f(x, i) for the logits i of [begin, end), by `threads` threads of which this is `t`; begin a multiple of 8
+    auto each = [&](int begin, int end, int t, int threads, auto f) {
+        for (int i = begin + t * E::kPer; i < end; i += threads * E::kPer) {
+            const uint4 w = *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
+#pragma unroll
+            for (int j = 0; j < E::kPer; ++j)
+                if (i + j < end) f(E::at(&w, j), i + j);
+        }
+    };
+
+    int turn = 0;  // of the exchanges: a number is written again only after a further meeting of the cluster
+    auto other = [&](int r) -> const Exchange& { return *cluster.map_shared_rank(&sh.exchange[turn], r); };
+
+    // The largest logit, and the range.
+    {
+        float top = -INFINITY, least = INFINITY;
+        if (use_k || use_p)
+            each(0, n, tid, kThreads, [&](float x, int) {
+                top = max_or_nan(top, x);
+                if (x > -INFINITY) least = fminf(least, x);
+            });
+        else each(0, n, tid, kThreads, [&](float x, int) { top = max_or_nan(top, x); });
+        top = warp_reduce(top, max_or_nan);
+        least = warp_reduce(least, fminf);
+        if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(__float_as_uint(top)) << 32 | __float_as_uint(least);
+        __syncthreads();
+        if (warp == 0) {
+            const uint64_t w = sh.warp[lane % kWarps];
+            top = warp_reduce(__uint_as_float(static_cast<uint32_t>(w >> 32)), max_or_nan);
+            least = warp_reduce(__uint_as_float(static_cast<uint32_t>(w)), fminf);
+            if (lane == 0) {
+                sh.exchange[turn].top = top;
+                sh.exchange[turn].least = least;
+            }
+        }
+        cluster.sync();
+    }
+    float top = -INFINITY, least = INFINITY;
+    for (int r = 0; r < ctas; ++r) {
+        top = max_or_nan(top, other(r).top);
+        least = fminf(least, other(r).least);
+    }
+    turn ^= 1;
+    const bool none = !(fabsf(top) < INFINITY);
     if (none || greedy) {
+        if (tid == 0) sh.exchange[turn].first = 0x7fffffff;
+        __syncthreads();
+        int mine = 0x7fffffff;
+        if (!none)
+            each(0, n, tid, kThreads, [&](float x, int i) {
+                if (x == top) mine = min(mine, first + i);
+            });
+        mine = __reduce_min_sync(~0u, mine);
+        if (lane == 0) atomicMin(&sh.exchange[turn].first, mine);
+        cluster.sync();
         if (rank == 0 && tid == 0) {
-            a.ids[row] = none ? -1 : static_cast<int>(~static_cast<uint32_t>(best));
+            for (int r = 0; r < ctas; ++r) mine = min(mine, other(r).first);
+            a.ids[row] = none ? -1 : mine;
             if (a.prob) a.prob[row] = none ? NAN : 1.0f;
         }
         cluster.sync();  // nobody leaves while others read its numbers
@@ -231,96 +319,207 @@ __global__ void __launch_bounds__(kThreads) k_sample(const Sample a) {
     }
 
     const Weights w{top, sh.c, sh.c_low, sh.table};
+    const float u = a.u[row];
+    // the first token whose cumulative weight exceeds this is drawn
+    auto point = [&](uint64_t whole) {
+        return u >= 1.0f ? whole - 1 : u > 0.0f ? __umul64hi(__float2ull_rz(u * 0x1p64f), whole) : 0;
+    };
+    // before < top_p whole, for integers: before < this
+    auto share = [&](uint64_t whole) -> uint64_t {
+        if (!(top_p > 0.0f)) return 0;
+        const uint64_t p = __float2ull_rz(top_p * 0x1p64f);
+        return __umul64hi(p, whole) + (p * whole != 0);
+    };
+    // w >= min_p as a smallest logit: max + temperature ln(min_p), and the largest always
+    float least_kept = -INFINITY;
+    if (min_p > 0.0f)
+        least_kept = min_p < 1.0f ? fminf(top, __double2float_ru(static_cast<double>(top) + sh.min_below)) : top;
+    auto item = [&](float x, int i) { return static_cast<uint64_t>(~key_of(x)) << 32 | static_cast<uint32_t>(first + i); };
+    auto logit_of = [&](uint64_t it) { return value_of(~static_cast<uint32_t>(it >> 32)); };
+    // Sums of two values a thread, in the threads' order: what lies before them, and all.
+    auto scan = [&](uint64_t v0, uint64_t v1, uint64_t& before, uint64_t& whole) {
+        const uint64_t upto = warp_scan(v0 + v1, lane);
+        __syncthreads();
+        if (lane == 31) sh.warp[warp] = upto;
+        __syncthreads();
+        before = upto - v0 - v1;
+        whole = 0;
+        for (int q = 0; q < kWarps; ++q) {
+            if (q < warp) before += sh.warp[q];
+            whole += sh.warp[q];
+        }
+    };
 
-    // Finds where the measure of the tokens before reaches `target` > 0: by bins over
-    // all logits of some weight and key >= floor_key, each bin's measure from `measure`.
+    // Where the measure (each token's weight, or 1) reaches a target: bins over the logits
+    // at or above `floor`, then over those of the bin with the cut. The target is formed
+    // from the whole measure; with may_list, tokens up to the first bin's end are
+    // only listed where they are few.
     int which = 0;
-    auto find = [&](auto measure, uint32_t floor_key, uint64_t target) {
+    uint64_t target = 0;
+    Cut cut{-INFINITY, 0, 0};  // everything
+    auto find = [&](auto weighs, float floor, auto aim, bool may_list) {
+        constexpr bool kWeigh = decltype(weighs)::value;
         const float span = fminf(top - least, (kOne + 2.0f) / w.c);
         const float scale = span > 0.0f ? static_cast<float>(kBins) / span : 0.0f;
-        auto linear = [&](float x) { return static_cast<int>(fminf((top - x) * scale, kBins - 1.0f)); };
-        uint32_t lo = 0, hi = top_key;  // keys of the bin that holds the cut
+        auto bin_of = [&](float x) { return fminf((top - x) * scale, static_cast<float>(kBins)); };  // kBins: as kBins - 1
+        float base = 0.0f;     // of the second division's bin
+        uint32_t lo = 0, hi = 0;  // keys that later ones divide
+        int shift = 0;
         uint64_t before = 0;
-        int shift = -1;                 // -1: bins over the logit
-        for (;;) {
-            uint64_t* bins = sh.bins[which];
-            for (int b = tid; b < kBins; b += kThreads) bins[b] = 0;
+        for (int level = 0;; ++level) {
+            uint64_t* mass = sh.mass[which];
+            uint32_t* count = sh.count[which];
+            mass[tid] = 0;
+            count[tid] = 0;
             __syncthreads();
-            for (int i = tid; i < n; i += kThreads) {
-                const float x = logits[i];
-                const uint32_t k = key_of(x);
-                if (k < lo || k > hi || k < floor_key || x == -INFINITY) continue;
-                const uint64_t m = measure(x, k);
-                if (m == 0) continue;
-                const int b = shift < 0 ? linear(x) : static_cast<int>((hi - k) >> shift);
-                atomicAdd(reinterpret_cast<unsigned long long*>(bins + b), static_cast<unsigned long long>(m));
-            }
-            cluster.sync();
-            // every CTA adds up all CTAs' bins; a thread two neighbouring ones
-            uint64_t v[2] = {0, 0};
-            for (int r = 0; r < ctas; ++r) {
-                const uint64_t* other = cluster.map_shared_rank(bins, r);
-                v[0] += other[2 * tid];
-                v[1] += other[2 * tid + 1];
-            }
-            uint64_t upto = v[0] + v[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(~0u, upto, o);
-                if (lane >= o) upto += y;
-            }
-            if (lane == 31) sh.warp[warp] = upto;
-            if (tid == 0) sh.found[0] = ~0ull;
-            __syncthreads();
-            uint64_t base = before;
-            for (int q = 0; q < warp; ++q) base += sh.warp[q];
-            uint64_t at = base + upto - v[0] - v[1];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (at < target && at + v[j] >= target) {
-                    sh.found[0] = 2 * tid + j;
-                    sh.found[1] = at;
+            auto place = [&](float x) {  // -1: not in question
+                if (level >= 2) {
+                    const uint32_t k = key_of(x);
+                    return k < lo || k > hi ? -1 : static_cast<int>((hi - k) >> shift);
                 }
-                at += v[j];
+                const int b = min(kBins - 1, static_cast<int>(bin_of(x)));
+                if (level == 0) return b;
+                return b != static_cast<int>(base) ? -1 : min(kBins - 1, static_cast<int>((bin_of(x) - base) * kBins));
+            };
+            each(0, n, tid, kThreads, [&](float x, int) {
+                if (!(x >= floor) || x == -INFINITY) return;
+                const int b = place(x);
+                if (b < 0) return;
+                if constexpr (kWeigh) {
+                    const uint64_t m = w.of(x);
+                    if (m == 0) return;
+                    atomicAdd(reinterpret_cast<unsigned long long*>(mass + b), static_cast<unsigned long long>(m));
+                }
+                atomicAdd(count + b, 1u);
+            });
+            cluster.sync();
+            uint64_t v = 0;
+            uint32_t c = 0;
+            for (int r = 0; r < ctas; ++r) {
+                c += cluster.map_shared_rank(count, r)[tid];
+                if constexpr (kWeigh) v += cluster.map_shared_rank(mass, r)[tid];
+            }
+            if constexpr (!kWeigh) v = c;
+            which ^= 1;
+            const uint64_t upto = warp_scan(v, lane);
+            const uint32_t counted = warp_scan(c, lane);
+            if (lane == 31) {
+                sh.warp[warp] = upto;
+                sh.warp2[warp] = counted;
+            }
+            if (tid == 0) sh.bin = ~0u;
+            __syncthreads();
+            uint64_t start = before, whole = 0;
+            uint32_t ahead = 0;
+            for (int q = 0; q < kWarps; ++q) {
+                if (q < warp) {
+                    start += sh.warp[q];
+                    ahead += sh.warp2[q];
+                }
+                whole += sh.warp[q];
+            }
+            if (level == 0) target = aim(whole);
+            start += upto - v;
+            if (start < target && start + v >= target) {
+                sh.bin = tid;
+                sh.before = start;
+                sh.members = c;
+                sh.upto = ahead + counted;
             }
             __syncthreads();
-            which ^= 1;
-            const uint64_t bin = sh.found[0];
-            if (bin == ~0ull) return Cut{floor_key ? floor_key - 1 : 0, 0};  // less than that in all: no cut
-            before = sh.found[1];
-            if (shift == 0) {
-                const uint32_t tau = hi - static_cast<uint32_t>(bin);
-                const uint64_t each = measure(value_of(tau), tau);
-                return Cut{tau, static_cast<uint32_t>((target - before + each - 1) / each)};
+            const int bin = static_cast<int>(sh.bin);
+            if (bin < 0) return kNothing;  // less than that in all, or a target of 0
+            before = sh.before;
+            const uint32_t members = sh.members;
+            const bool all = may_list && level == 0 && sh.upto <= kFew;
+            if (all || members <= kFew) {
+                uint64_t* list = cluster.map_shared_rank(sh.list, 0);
+                uint32_t* listed = cluster.map_shared_rank(&sh.listed, 0);
+                each(0, n, tid, kThreads, [&](float x, int i) {
+                    if (!(x >= floor) || x == -INFINITY) return;
+                    const int b = place(x);
+                    if (b != bin && !(all && b < bin && b >= 0)) return;
+                    if (kWeigh && w.of(x) == 0) return;  // not counted either
+                    list[atomicAdd(listed, 1u)] = item(x, i);
+                });
+                cluster.sync();
+                if (all) return kListed;
+                if (rank == 0) {
+                    const int m = static_cast<int>(sh.listed);
+                    sort(sh.list, m);
+                    uint64_t v2[2], lead, sum;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int p = 2 * tid + j;
+                        v2[j] = p >= m ? 0 : kWeigh ? w.of(logit_of(sh.list[p])) : 1;
+                    }
+                    scan(v2[0], v2[1], lead, sum);
+                    lead += before;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (lead < target && lead + v2[j] >= target) {
+                            const int p = 2 * tid + j;
+                            const uint64_t key = sh.list[p] >> 32;
+                            auto bound = [&](uint64_t k) {  // the first with a key at or behind k
+                                int x = 0, y = m;
+                                while (x < y) {
+                                    const int mid = (x + y) / 2;
+                                    if (sh.list[mid] >> 32 < k) x = mid + 1;
+                                    else y = mid;
+                                }
+                                return x;
+                            };
+                            const int from = bound(key), to = bound(key + 1);
+                            sh.exchange[turn].cut = Cut{logit_of(sh.list[p]), static_cast<uint32_t>(p + 1 - from),
+                                                        static_cast<uint32_t>(to - from)};
+                        }
+                        lead += v2[j];
+                    }
+                    if (tid == 0) sh.listed = 0;
+                }
+                cluster.sync();
+                cut = other(0).cut;
+                turn ^= 1;
+                return kFound;
             }
-            if (shift < 0) {
-                // the keys that the bin holds
+            if (level >= 2 && shift == 0) {  // equal logits
+                const float x = value_of(hi - static_cast<uint32_t>(bin));
+                const uint64_t m = kWeigh ? w.of(x) : 1;
+                cut = Cut{x, static_cast<uint32_t>((target - before + m - 1) / m), members};
+                return kFound;
+            }
+            if (level == 0) {
+                base = static_cast<float>(bin);
+                continue;
+            }
+            if (level == 1) {  // the keys that the bin holds
                 uint32_t small = ~0u, large = 0;
-                for (int i = tid; i < n; i += kThreads) {
-                    const float x = logits[i];
-                    if (x == -INFINITY || linear(x) != static_cast<int>(bin)) continue;
+                each(0, n, tid, kThreads, [&](float x, int) {
+                    if (!(x >= floor) || x == -INFINITY || place(x) != bin) return;
                     small = min(small, key_of(x));
                     large = max(large, key_of(x));
-                }
+                });
                 small = __reduce_min_sync(~0u, small);
                 large = __reduce_max_sync(~0u, large);
                 if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(small) << 32 | large;
                 __syncthreads();
-                if (tid == 0) {
-                    Exchange& e = sh.exchange[turn];
-                    e.lo = ~0u;
-                    e.hi = 0;
-                    for (int q = 0; q < kWarps; ++q) {
-                        e.lo = min(e.lo, static_cast<uint32_t>(sh.warp[q] >> 32));
-                        e.hi = max(e.hi, static_cast<uint32_t>(sh.warp[q]));
+                if (warp == 0) {
+                    const uint64_t both = sh.warp[lane % kWarps];
+                    small = __reduce_min_sync(~0u, static_cast<uint32_t>(both >> 32));
+                    large = __reduce_max_sync(~0u, static_cast<uint32_t>(both));
+                    if (lane == 0) {
+                        sh.exchange[turn].lo = small;
+                        sh.exchange[turn].hi = large;
                     }
                 }
-                const uint64_t both = across([](const Exchange& e) { return static_cast<uint64_t>(~e.lo) << 32 | e.hi; },
-                                             [](uint64_t x, uint64_t y) {
-                                                 return max(x >> 32, y >> 32) << 32 | max(x & 0xffffffffu, y & 0xffffffffu);
-                                             });
-                lo = ~static_cast<uint32_t>(both >> 32);
-                hi = static_cast<uint32_t>(both);
+                cluster.sync();
+                lo = ~0u;
+                hi = 0;
+                for (int r = 0; r < ctas; ++r) {
+                    lo = min(lo, other(r).lo);
+                    hi = max(hi, other(r).hi);
+                }
+                turn ^= 1;
             } else {
                 hi -= static_cast<uint32_t>(bin) << shift;
                 lo = max(lo, hi - ((1u << shift) - 1));
@@ -329,133 +528,161 @@ __global__ void __launch_bounds__(kThreads) k_sample(const Sample a) {
             while ((hi - lo) >> shift >= kBins) ++shift;
         }
     };
-    // The kept weight, by warps (each a run of the CTA's logits) and over the cluster.
-    const int run = (n + kWarps - 1) / kWarps, r0 = min(n, warp * run), r1 = min(n, r0 + run);
-    auto kept = [&](Cut cut, uint64_t& above, uint32_t& ties) {
-        above = 0;
-        ties = 0;
-        for (int i = r0 + lane; i < r1; i += 32) {
-            const float x = logits[i];
-            const uint32_t k = key_of(x);
-            if (k > cut.tau) above += w.of(x);
-            else if (k == cut.tau) ++ties;
+    // What the leading CTA does with a list of the likeliest tokens: the first `most` of them
+    // are what top-k keeps; limit: the target of top-p, or 0 to form it from their weight.
+    auto finish = [&](int most, uint64_t limit) {
+        const int m = static_cast<int>(sh.listed);
+        sort(sh.list, m);
+        most = min(most, m);
+        float x[2];
+        uint64_t v[2], lead, whole;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int p = 2 * tid + j;
+            x[j] = p < most ? logit_of(sh.list[p]) : -INFINITY;
+            v[j] = w.of(x[j]);
         }
-        above = warp_reduce(above, add<uint64_t>);
-        ties = warp_reduce(ties, add<uint32_t>);
-        __syncthreads();
-        if (lane == 0) {
-            sh.warp[warp] = above;
-            sh.warp2[warp] = ties;
+        scan(v[0], v[1], lead, whole);
+        if (use_p && limit == 0) limit = share(whole);
+        const bool keep[2] = {tid == 0 || (2 * tid < most && x[0] >= least_kept && (!use_p || lead < limit)),
+                              2 * tid + 1 < most && x[1] >= least_kept && (!use_p || lead + v[0] < limit)};
+        // kept tokens are the first ones
+        const int kept = __syncthreads_count(keep[0]) + __syncthreads_count(keep[1]);
+        uint64_t to[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint64_t it = sh.list[2 * tid + j];
+            to[j] = it << 32 | it >> 32;  // index first
         }
         __syncthreads();
-        if (tid == 0) {
-            Exchange& e = sh.exchange[turn];
-            e.mass = 0;
-            e.ties = 0;
-            for (int q = 0; q < kWarps; ++q) {
-                e.mass += sh.warp[q];
-                e.ties += sh.warp2[q];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (keep[j]) sh.list[2 * tid + j] = to[j];
+        sort(sh.list, kept);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int p = 2 * tid + j;
+            to[j] = p < kept ? sh.list[p] : 0;
+            x[j] = value_of(~static_cast<uint32_t>(to[j]));
+            v[j] = p < kept ? w.of(x[j]) : 0;
+        }
+        scan(v[0], v[1], lead, whole);
+        const uint64_t goal = point(whole);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (lead <= goal && lead + v[j] > goal) {
+                a.ids[row] = static_cast<int>(to[j] >> 32);
+                if (a.prob) a.prob[row] = w.share(x[j], whole);
             }
+            lead += v[j];
         }
     };
 
-    Cut cut{0, 0};  // everything
-    uint64_t above;
-    uint32_t ties;
-    if (top_k > 0 && top_k < a.V)
-        cut = find([](float, uint32_t) { return 1ull; }, 0u, static_cast<uint64_t>(top_k));
-    if (top_p < 1.0f || top_p != top_p) {
-        kept(cut, above, ties);
-        const int t = turn;
-        uint64_t whole = across([](const Exchange& e) { return e.mass; }, add<uint64_t>);
-        uint32_t all_ties = 0;
-        for (int r = 0; r < ctas; ++r) all_ties += cluster.map_shared_rank(&sh.exchange[t], r)->ties;
-        const uint64_t each = w.of(value_of(cut.tau));
-        if (cut.ties) whole += min(cut.ties, all_ties) * each;
-        // before < p whole, for integers: before < ceil(p whole)
-        uint64_t target = 0;
-        if (top_p > 0.0f) {
-            const uint64_t p = __float2ull_rz(top_p * 0x1p64f);
-            target = __umul64hi(p, whole) + (p * whole != 0);
-        }
-        if (target == 0) cut = Cut{top_key, 1};
-        // the target is at most what the first cut keeps: where that ends among equal
-        // logits, this one ends there or before
-        else cut = find([&](float x, uint32_t) { return w.of(x); }, cut.tau + (cut.ties == 0), target);
-    }
-    if (min_p > 0.0f) {
-        // w >= min_p, as a smallest logit: max + temperature ln(min_p)
-        if (!(min_p < 1.0f)) {
-            if (cut.tau < top_key) cut = Cut{top_key - 1, 0};
-        } else {
-            const uint32_t k = key_of(__double2float_ru(static_cast<double>(top) + sh.min_below));
-            if (k > cut.tau) cut = Cut{k - 1, 0};
+    if (use_k) {
+        const Found f = find(std::false_type{}, -INFINITY, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, true);
+        if (f == kListed) {
+            if (rank == 0) finish(top_k, 0);
+            return;
         }
     }
-    kept(cut, above, ties);
+    if (use_p) {
+        // equal logits that top-k leaves out are weighed with the others
+        const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of(cut.at) : 0;
+        const Found f = find(std::true_type{}, cut.at, [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
+        if (f == kListed) {
+            if (rank == 0) finish(kFew, target);
+            return;
+        }
+        if (f == kNothing) cut = Cut{top, 1, 1};  // top_p of 0
+    }
+    if (least_kept > cut.at) cut = Cut{-INFINITY, 0, 0};
+    // The kept weight, by parts of the CTA's logits, and over the cluster.
+    const int length = ((n + kParts - 1) / kParts + 7) / 8 * 8;
     {
-        cluster.sync();
-        const uint64_t each = cut.ties ? w.of(value_of(cut.tau)) : 0;
-        uint64_t whole = 0, my_start = 0, my_mass = 0;
-        uint32_t ties_left = cut.ties, my_ties = 0;
-        for (int r = 0; r < ctas; ++r) {
-            const Exchange& e = *cluster.map_shared_rank(&sh.exchange[turn], r);
-            const uint32_t t = min(ties_left, e.ties);
-            const uint64_t m = e.mass + t * each;
-            if (r == rank) {
-                my_start = whole;
-                my_mass = m;
-                my_ties = ties_left;
+        uint64_t mass = 0;
+        uint32_t ties = 0;
+        for (int q = warp * (kParts / kWarps); q < (warp + 1) * (kParts / kWarps); ++q) {
+            uint64_t v = 0;
+            uint32_t t = 0;
+            each(q * length, min(n, (q + 1) * length), lane, 32, [&](float x, int) {
+                if (x > cut.at) {
+                    if (x >= least_kept) v += w.of(x);
+                } else if (x == cut.at) {
+                    ++t;
+                }
+            });
+            v = warp_reduce(v, add<uint64_t>);
+            t = __reduce_add_sync(~0u, t);
+            if (lane == 0) {
+                sh.part[q] = v;
+                sh.part_ties[q] = t;
             }
-            ties_left -= t;
-            whole += m;
+            mass += v;
+            ties += t;
         }
-        const float u = a.u[row];
-        uint64_t target = 0;  // the first token whose cumulative weight exceeds this
-        if (u >= 1.0f) target = whole - 1;
-        else if (u > 0.0f) target = __umul64hi(__float2ull_rz(u * 0x1p64f), whole);
-        cluster.sync();  // the others' numbers have been read
-        if (target < my_start || target >= my_start + my_mass) return;
-        // the run with it
-        uint64_t at = my_start;
-        int q = 0;
-        for (;; ++q) {
-            const uint32_t t = min(my_ties, sh.warp2[q]);
-            const uint64_t m = sh.warp[q] + t * each;
-            if (target < at + m) break;
-            at += m;
-            my_ties -= t;
+        if (lane == 0) {
+            sh.warp[warp] = mass;
+            sh.warp2[warp] = ties;
         }
-        if (warp != q) return;
-        for (int i0 = r0;; i0 += 32) {
+        __syncthreads();
+        if (warp == 0) {
+            mass = warp_reduce(lane < kWarps ? sh.warp[lane] : 0, add<uint64_t>);
+            ties = __reduce_add_sync(~0u, lane < kWarps ? sh.warp2[lane] : 0);
+            if (lane == 0) {
+                sh.exchange[turn].mass = mass;
+                sh.exchange[turn].ties = ties;
+            }
+        }
+    }
+    cluster.sync();
+    const uint64_t tie = cut.ties ? w.of(cut.at) : 0;
+    uint64_t whole = 0, start = 0, mine = 0;
+    uint32_t left = cut.ties, my_left = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const uint32_t t = min(left, other(r).ties);
+        const uint64_t m = other(r).mass + t * tie;
+        if (r == rank) {
+            start = whole;
+            mine = m;
+            my_left = left;
+        }
+        left -= t;
+        whole += m;
+    }
+    const uint64_t goal = point(whole);
+    cluster.sync();  // the others' numbers have been read
+    if (goal < start || goal >= start + mine || warp != 0) return;
+    // The part with it: two a lane.
+    {
+        const uint32_t t0 = sh.part_ties[2 * lane], t1 = sh.part_ties[2 * lane + 1];
+        const uint32_t ties_before = warp_scan(t0 + t1, lane) - t0 - t1;
+        const uint32_t l0 = my_left - min(my_left, ties_before), l1 = l0 - min(l0, t0);
+        const uint64_t m0 = sh.part[2 * lane] + min(l0, t0) * tie, m1 = sh.part[2 * lane + 1] + min(l1, t1) * tie;
+        const uint64_t at0 = start + warp_scan(m0 + m1, lane) - m0 - m1, at1 = at0 + m0;
+        const bool in0 = goal >= at0 && goal < at1, in1 = goal >= at1 && goal < at1 + m1;
+        const int who = __ffs(__ballot_sync(~0u, in0 || in1)) - 1;
+        const int part = __shfl_sync(~0u, 2 * lane + (in1 ? 1 : 0), who);
+        start = __shfl_sync(~0u, in1 ? at1 : at0, who);
+        my_left = __shfl_sync(~0u, in1 ? l1 : l0, who);
+        const int end = min(n, (part + 1) * length);
+        for (int i0 = part * length; i0 < end; i0 += 32) {
             const int i = i0 + lane;
-            const float x = i < r1 ? logits[i] : -INFINITY;
-            const uint32_t k = key_of(x);
-            const bool tie = i < r1 && cut.ties && k == cut.tau;
-            const uint32_t tied = __ballot_sync(~0u, tie);
-            const bool keep = i < r1 && (k > cut.tau || (tie && __popc(tied & ((1u << lane) - 1)) < my_ties));
-            const uint64_t weight = keep ? w.of(x) : 0;
-            uint64_t upto = weight;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(~0u, upto, o);
-                if (lane >= o) upto += y;
-            }
-            const uint32_t over = __ballot_sync(~0u, at + upto > target);
+            const float x = i < end ? at(i) : -INFINITY;
+            const bool equal = cut.ties && x == cut.at;
+            const uint32_t tied = __ballot_sync(~0u, equal);
+            const bool keep = (x > cut.at && x >= least_kept) || (equal && __popc(tied & ((1u << lane) - 1)) < my_left);
+            my_left -= min(my_left, static_cast<uint32_t>(__popc(tied)));
+            if (!__any_sync(~0u, keep)) continue;
+            const uint64_t upto = start + warp_scan(keep ? w.of(x) : 0, lane);
+            const uint32_t over = __ballot_sync(~0u, upto > goal);
             if (over) {
                 if (lane == __ffs(over) - 1) {
                     a.ids[row] = first + i;
-                    if (a.prob) {  // from the weight before it became a whole number of units
-                        int s;
-                        const double mine = static_cast<double>(w.parts(x, s));
-                        a.prob[row] = static_cast<float>(mine / (static_cast<double>(1ull << s) * static_cast<double>(whole)));
-                    }
+                    if (a.prob) a.prob[row] = w.share(x, whole);
                 }
                 return;
             }
-            at += __shfl_sync(~0u, upto, 31);
-            my_ties -= min(my_ties, static_cast<uint32_t>(__popc(tied)));
-            if (i0 + 32 >= r1) return;
+            start = __shfl_sync(~0u, upto, 31);
         }
     }
 }
@@ -464,7 +691,7 @@ bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % 
 
 template <int kElem>
 cudaError_t launch(const Sample& s, int B, int ctas, cudaStream_t stream) {
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(s.slice) * 4;
+    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(s.slice) * Elem<kElem>::kBytes;
     cudaError_t rc = cudaFuncSetAttribute(k_sample<kElem>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
     cudaLaunchAttribute attr[2] = {overlapped(), {}};
