@@ -13,9 +13,10 @@
 // at the blocks, each with a ring of its own filled by cp.async and with its own
 // (m, l, sum), and meet at a unit's end only.
 //
-// Every query head of a key head (16 rows of a matrix instruction) meets a key when
-// it is read. This is bound by HBM: a key and value of 128 bf16 are 512 bytes, and
-// their products 8 x 2 m16n8k16 for up to 16 query heads.
+// The matrix instructions take keys and transposed values as their 16 rows and the query heads of
+// a key head as their 8 columns (a wider group of heads: two tiles of 8, and units of 16),
+// so a group of 8 heads or fewer wastes no row: with the heads as rows, it took twice the
+// instructions and registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -30,8 +31,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBlock = 16;  // positions a warp takes at a time
-constexpr int kRows = 16;   // query heads that meet a key together
+constexpr int kGroup = 16;  // positions that lie in one page together where page_size is a multiple of it
+constexpr int kRows = 16;   // query heads that meet a key together, at most
 
 struct Attend {
     const void* q;
@@ -55,9 +56,10 @@ struct Shape {
     static constexpr bool kBytes = kElem == ESTREAM_KV_E4M3;
     static constexpr bool kBf16 = kElem == ESTREAM_KV_BF16;  // the matrix instructions' type; else fp16
     static constexpr int kRowBytes = kDim * (kBytes ? 1 : 2);
+    static constexpr int kBlock = kRowBytes <= 128 ? 32 : 16;  // positions a warp takes at a time
     static constexpr int kStageBytes = 2 * kBlock * kRowBytes;  // keys, then values
-    static constexpr int kStages = kRowBytes == 64 ? 8 : kRowBytes == 128 ? 6 : kDim == 256 && kBytes ? 2 : 3;
-    static constexpr int kPitch = kDim + 4;  // floats; a warp's eight rows begin on different banks
+    static constexpr int kStages = kRowBytes == 64 ? 6 : kDim == 256 && kBytes ? 2 : 3;
+    static constexpr int kPitch = kDim + 4;  // floats; a warp's stores of sums are on different banks
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kSmem = kRing + kWarps * 8 * kPitch * 4 + kWarps * 8 * 8;
     static constexpr int kResident = 2 * (kSmem + 1024 + 128) <= 228 * 1024 ? 2 : 1;  // 1 KB a CTA is the system's
@@ -121,15 +123,22 @@ __device__ __forceinline__ uint32_t in_tile(int r, int c) {
     return r * kRowBytes + ((c ^ x) << 4);
 }
 
+__device__ __forceinline__ uint32_t transpose(uint32_t x) {  // 8 x 8 values of 16 bits
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // A row's attended positions [lo, len) and its blocks, which begin at a multiple of 16.
 struct Span {
     int len, lo, first, blocks;
 };
+template <int kBlock>
 __device__ __forceinline__ Span span_of(const Attend& a, int b) {
     Span s;
     s.len = a.lens[b];
     s.lo = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
-    s.first = s.lo & ~(kBlock - 1);
+    s.first = s.lo & ~(kGroup - 1);
     s.blocks = s.len > 0 && s.len <= a.max_len ? (s.len - s.first + kBlock - 1) / kBlock : 0;
     return s;
 }
@@ -142,11 +151,12 @@ struct Unit {
     __device__ __forceinline__ long long from(long long begin) const { return max(begin, start); }
     __device__ __forceinline__ long long to(long long end) const { return min(end, start + span.blocks); }
     // The next unit; there is one while start + blocks < end.
+    template <int kBlock>
     __device__ __forceinline__ void next(const Attend& a) {
         start += span.blocks;
         if (++head == a.heads * a.tiles) {
             head = 0;
-            do span = span_of(a, ++b);
+            do span = span_of<kBlock>(a, ++b);
             while (span.blocks == 0);
         }
     }
@@ -166,14 +176,16 @@ __device__ __forceinline__ void finish(const Attend& a, int b, int h, int d, flo
             l == 0.0f ? -INFINITY : (bias_and_m() + log2f(l)) * 0.69314718055994531f;
 }
 
-template <int kElem, int kDim, bool kWhole>  // kWhole: page_size a multiple of 16, a block lies in one page
+// kTiles: tiles of 8 query heads (2 only where a group has more than 8). kWhole: page_size is a
+// multiple of 16, so 16 positions from a multiple of 16 on lie in one page.
+template <int kElem, int kDim, int kTiles, bool kWhole>
 __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_attend(const Attend a) {
     using S = Shape<kElem, kDim>;
-    constexpr int kSteps = kDim / 16;
-    constexpr int kChunks = S::kRowBytes / 16;         // of a padded row
+    constexpr int kSteps = kDim / 16, kBlock = S::kBlock;
+    constexpr int kChunks = S::kRowBytes / 16;                 // of a padded row
     constexpr int kPerCopy = kChunks < 32 ? 32 / kChunks : 1;  // rows that a warp's copy covers
     extern __shared__ __align__(128) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + S::kRing);               // [kWarps][8][kPitch]
+    float* sums = reinterpret_cast<float*>(smem + S::kRing);                   // [kWarps][8][kPitch]
     float2* stats = reinterpret_cast<float2*>(sums + kWarps * 8 * S::kPitch);  // [kWarps][8]
     __shared__ long long scan[kWarps];
     __shared__ Unit first_unit;
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 
     // Rows with nothing to attend: zeros, or NaN where the length is out of range.
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const Span s = span_of(a, b);
+        const Span s = span_of<kBlock>(a, b);
         if (s.blocks) continue;
         const float fill = s.len == 0 ? 0.0f : NAN;
         for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
@@ -195,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     // This CTA's share, and the unit it begins in.
     const int per_thread = (a.B + kThreads - 1) / kThreads, mine = tid * per_thread, past = min(a.B, mine + per_thread);
     long long count = 0;
-    for (int b = mine; b < past; ++b) count += span_of(a, b).blocks;
+    for (int b = mine; b < past; ++b) count += span_of<kBlock>(a, b).blocks;
     long long upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         u.b = mine;
         u.start = before;
         for (;; ++u.b) {
-            u.span = span_of(a, u.b);
+            u.span = span_of<kBlock>(a, u.b);
             const long long n = static_cast<long long>(u.span.blocks) * units;
             if (begin < u.start + n) break;
             u.start += n;
@@ -243,56 +255,66 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                 more = false;
                 return;
             }
-            ahead.next(a);
+            ahead.template next<kBlock>(a);
             next = ahead.start + warp;
         }
     };
-    // The page and the place in it of position lane % 16 of the next block; page -1:
-    // not attended; -2: out of range.
+    // The page (-1: not attended, -2: out of range) and the place in it of the next block's
+    // position lane % kBlock, or where a page holds whole groups, of its group's first one.
     int page = -1, slot = 0;
     auto look_up = [&] {
         if (!more) return;
-        const int at = ahead.span.first + static_cast<int>(next - ahead.start) * kBlock + (lane & 15);
+        int at = ahead.span.first + static_cast<int>(next - ahead.start) * kBlock + lane % kBlock;
+        if constexpr (kWhole) at &= ~(kGroup - 1);
         page = -1;
         const int entry = static_cast<int>(a.page.div(at));
         slot = at - entry * static_cast<int>(a.page.d);
-        if (at >= ahead.span.lo && at < ahead.span.len) {
+        if (at < ahead.span.len && (kWhole || at >= ahead.span.lo)) {
             page = a.table[ahead.b * a.table_row + entry];
             if (page < 0 || page >= a.num_pages) page = -2;
         }
     };
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::kStages * S::kStageBytes;
+    const int my_chunk = lane % kChunks, my_row = lane / kChunks;
     uint32_t bad = 0;  // by stage: a page out of range
     auto issue = [&](int stage) {
         if (more) {
             const uint32_t to = ring + stage * S::kStageBytes;
-            const int h = ahead.head / a.tiles, c = lane % kChunks;
-            const uint8_t* kb = a.k + h * a.k_head + c * 16;
-            const uint8_t* vb = a.v + h * a.v_head + c * 16;
-            const bool in = c < a.chunks;
+            const int h = ahead.head / a.tiles;
+            const uint8_t* kb = a.k + h * a.k_head + my_chunk * 16;
+            const uint8_t* vb = a.v + h * a.v_head + my_chunk * 16;
+            const bool in = my_chunk < a.chunks;
             bad = (bad & ~(1u << stage)) | (__any_sync(~0u, page == -2) ? 1u << stage : 0u);
             if constexpr (kWhole) {
-                const int lead = __reduce_max_sync(~0u, page);  // the block's page
-                const int slot0 = __shfl_sync(~0u, slot, 0);
-                kb += static_cast<long long>(max(lead, 0)) * a.k_page + slot0 * a.k_token;
-                vb += static_cast<long long>(max(lead, 0)) * a.v_page + slot0 * a.v_token;
-            }
+                const int at = ahead.span.first + static_cast<int>(next - ahead.start) * kBlock + my_row;
+                const int lo = ahead.span.lo - at, len = ahead.span.len - at;  // relative to this lane's first row
 #pragma unroll
-            for (int i = 0; i < kBlock / kPerCopy; ++i) {
-                const int r = i * kPerCopy + lane / kChunks;
-                const int p = __shfl_sync(~0u, page, r);
-                const uint8_t *kf, *vf;
-                if constexpr (kWhole) {
-                    kf = kb + r * a.k_token;
-                    vf = vb + r * a.v_token;
-                } else {
-                    const int s = __shfl_sync(~0u, slot, r);
-                    kf = kb + max(p, 0) * a.k_page + s * a.k_token;
-                    vf = vb + max(p, 0) * a.v_page + s * a.v_token;
+                for (int j = 0; j < kBlock / kGroup; ++j) {
+                    const int p = __shfl_sync(~0u, page, j * kGroup), s = __shfl_sync(~0u, slot, j * kGroup) + my_row;
+                    const uint8_t* kf = kb + max(p, 0) * a.k_page + s * a.k_token;
+                    const uint8_t* vf = vb + max(p, 0) * a.v_page + s * a.v_token;
+                    const long long k_step = kPerCopy * a.k_token, v_step = kPerCopy * a.v_token;
+#pragma unroll
+                    for (int i = 0; i < kGroup / kPerCopy; ++i) {
+                        const int r = j * kGroup + i * kPerCopy;
+                        const bool there = in && p >= 0 && r >= lo && r < len;
+                        copy16(to + in_tile<S::kRowBytes>(r + my_row, my_chunk), there ? kf : a.k, there);
+                        copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r + my_row, my_chunk), there ? vf : a.v, there);
+                        kf += k_step;
+                        vf += v_step;
+                    }
                 }
-                const bool there = p >= 0 && in;
-                copy16(to + in_tile<S::kRowBytes>(r, c), there ? kf : a.k, there);
-                copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, c), there ? vf : a.v, there);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kBlock / kPerCopy; ++i) {
+                    const int r = i * kPerCopy + my_row;
+                    const int p = __shfl_sync(~0u, page, r), s = __shfl_sync(~0u, slot, r);
+                    const bool there = in && p >= 0;
+                    const uint8_t* kf = kb + max(p, 0) * a.k_page + s * a.k_token;
+                    const uint8_t* vf = vb + max(p, 0) * a.v_page + s * a.v_token;
+                    copy16(to + in_tile<S::kRowBytes>(r, my_chunk), there ? kf : a.k, there);
+                    copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), there ? vf : a.v, there);
+                }
             }
             next += kWarps;
             settle();
@@ -311,23 +333,29 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     int stage = 0;
     for (;;) {
         const long long from = u.from(begin), to = u.to(end);
-        const int kv_head = u.head / a.tiles, row0 = u.head % a.tiles * kRows;  // first query head of this tile in its group
+        const int kv_head = u.head / a.tiles, row0 = u.head % a.tiles * kRows;  // first query head of this unit in its group
         const int rows = min(kRows, a.group - row0);
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        float o[2 * kSteps][4];
+        // Of heads 2t and 2t + 1 of each tile: the maximum (the same in all lanes of one t), this
+        // lane's part of the sum of weights, and of the values' dims g and g + 8 of each 16 (E4M3: 2g, 2g + 1).
+        float m[kTiles][2], l[kTiles][2], o[kTiles][kSteps][4];
 #pragma unroll
-        for (int n = 0; n < 2 * kSteps; ++n)
+        for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
+            for (int i = 0; i < 2; ++i) {
+                m[j][i] = -INFINITY;
+                l[j][i] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) o[j][s][i] = o[j][s][i + 2] = 0.0f;
+            }
         bool poison = false;
         if (from + warp < to) {
             // Query fragments. An E4M3 key's four neighbouring values lie in one lane, so pairs
             // (2t, 2t + 1) and (2t + 8, 2t + 9) of the product are values (4t, 4t + 1) and (4t + 2, 4t + 3).
-            uint32_t qa[kSteps][4];
-            float c[2] = {a.scale, a.scale};
+            uint32_t qb[kTiles][kSteps][2];
+            float c[kTiles][2];  // scale of heads 2t and 2t + 1
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int h = g + 8 * r;
+            for (int j = 0; j < kTiles; ++j) {
+                const int h = 8 * j + g;
                 const uint16_t* qr = static_cast<const uint16_t*>(a.q) + u.b * a.q_row +
                                      static_cast<long long>(kv_head * a.group + row0 + min(h, rows - 1)) * a.q_head;
 #pragma unroll
@@ -339,10 +367,11 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                         if (d < a.dim && h < rows)
                             w = a.q_words ? *reinterpret_cast<const uint32_t*>(qr + d)
                                           : qr[d] | static_cast<uint32_t>(qr[d + 1]) << 16;
-                        qa[s][r + 2 * i] = w;
+                        qb[j][s][i] = w;
                     }
+                c[j][0] = c[j][1] = a.scale;
                 if constexpr (S::kBytes) {
-                    // to fp16, by the power of two that puts the largest at 2^10 to 2^11
+                    // to fp16, by the power of two that puts the head's largest at 2^10 to 2^11
                     auto wide = [&](uint32_t w) {
                         return a.out_f16 ? __half22float2(*reinterpret_cast<__half2*>(&w))
                                          : __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
@@ -352,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float2 f = wide(qa[s][r + 2 * i]);
+                            const float2 f = wide(qb[j][s][i]);
                             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                         }
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
@@ -363,13 +392,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float2 f = wide(qa[s][r + 2 * i]);
-                            qa[s][r + 2 * i] = pack<false>(f.x * up, f.y * up);
+                            const float2 f = wide(qb[j][s][i]);
+                            qb[j][s][i] = pack<false>(f.x * up, f.y * up);
                         }
-                    c[r] = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    const float down = a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // head g's
+                    c[j][0] = __shfl_sync(~0u, down, 8 * t);
+                    c[j][1] = __shfl_sync(~0u, down, 8 * t + 4);
                 }
             }
-            const bool tall = rows > 8;
             for (long long blk = from + warp; blk < to; blk += kWarps) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
                 __syncwarp();  // every lane's copies are there, and every lane has read the stage that is filled next
@@ -377,127 +407,135 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                 const uint32_t kt = ring + stage * S::kStageBytes, vt = kt + kBlock * S::kRowBytes;
                 poison |= bad >> stage & 1;
                 stage = stage + 1 == S::kStages ? 0 : stage + 1;
-                float z[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z[n][i] = 0.0f;
-                if constexpr (S::kBytes) {
-#pragma unroll
-                    for (int s = 0; s < kSteps; s += 2) {
-                        uint32_t r[4];
-                        ldmatrix(r, kt + in_tile<S::kRowBytes>(lane & 15, s + (lane >> 4)));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma<false>(z[i & 1], qa[s + i / 2], from_e4m3(r[i] & 0xffff), from_e4m3(r[i] >> 16));
-                    }
-                } else {
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        uint32_t r[4];
-                        ldmatrix(r, kt + in_tile<S::kRowBytes>((lane & 7) + (lane >> 4) * 8, 2 * s + (lane >> 3 & 1)));
-                        mma<S::kBf16>(z[0], qa[s], r[0], r[1]);
-                        mma<S::kBf16>(z[1], qa[s], r[2], r[3]);
-                    }
-                }
                 const int at = u.span.first + static_cast<int>(blk - u.start) * kBlock;
                 const bool edge = at < u.span.lo || at + kBlock > u.span.len;
-                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int half = 0; half < kBlock / 16; ++half) {
+                    // z: positions g and g + 8 of heads 2t and 2t + 1
+                    float z[kTiles][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = z[n][i] * c[i / 2];
-                        if (edge) {
-                            const int p = at + 8 * n + 2 * t + (i & 1);
-                            if (p < u.span.lo || p >= u.span.len) x = -INFINITY;
+                    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[j][i] = 0.0f;
+                    const int row = 16 * half + (lane & 15), side = lane >> 4;
+                    if constexpr (S::kBytes) {
+#pragma unroll
+                        for (int s = 0; s < kSteps; s += 2) {
+                            uint32_t r[4];
+                            ldmatrix(r, kt + in_tile<S::kRowBytes>(row, s + side));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t f[4] = {from_e4m3(r[2 * i] & 0xffff), from_e4m3(r[2 * i + 1] & 0xffff),
+                                                       from_e4m3(r[2 * i] >> 16), from_e4m3(r[2 * i + 1] >> 16)};
+#pragma unroll
+                                for (int j = 0; j < kTiles; ++j) mma<false>(z[j], f, qb[j][s + i][0], qb[j][s + i][1]);
+                            }
                         }
-                        z[n][i] = x;
-                        top[i / 2] = fmaxf(top[i / 2], x);
-                    }
+                    } else {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-                }
-                if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+                        for (int s = 0; s < kSteps; ++s) {
+                            uint32_t r[4];
+                            ldmatrix(r, kt + in_tile<S::kRowBytes>(row, 2 * s + side));
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float now = fmaxf(m[r], top[r]), shrink = exp2_fast(m[r] - finite_or_zero(now));
-                        m[r] = now;
-                        l[r] *= shrink;
-#pragma unroll
-                        for (int n = 0; n < 2 * kSteps; ++n) {
-                            o[n][2 * r] *= shrink;
-                            o[n][2 * r + 1] *= shrink;
-                        }
-                    }
-                }
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    if (r == 1 && !tall) {
-                        hi[1] = hi[3] = lo[1] = lo[3] = 0;
-                        break;
-                    }
-                    const float base = finite_or_zero(m[r]) - S::kBias;
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float x = exp2_fast(z[n][2 * r] - base), y = exp2_fast(z[n][2 * r + 1] - base);
-                        l[r] += x + y;
-                        const uint32_t w = pack<S::kBf16>(x, y);
-                        hi[2 * n + r] = w;
-                        if constexpr (S::kBf16)  // what bf16 leaves of a weight, as a second term
-                            lo[2 * n + r] = pack<true>(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u));
-                    }
-                }
-                if constexpr (S::kBytes) {
-#pragma unroll
-                    for (int s = 0; s < kSteps; s += 2) {
-                        uint32_t r[4];
-                        ldmatrix_trans(r, vt + in_tile<S::kRowBytes>(lane & 15, s + (lane >> 4)));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            // values (2g, 2g + 1) of positions 2t and 2t + 1: to pairs of positions
-                            const uint32_t p = __byte_perm(r[2 * i], 0, 0x3120), q = __byte_perm(r[2 * i + 1], 0, 0x3120);
-                            mma<false>(o[2 * (s + i)], hi, from_e4m3(p & 0xffff), from_e4m3(q & 0xffff));
-                            mma<false>(o[2 * (s + i) + 1], hi, from_e4m3(p >> 16), from_e4m3(q >> 16));
+                            for (int j = 0; j < kTiles; ++j) mma<S::kBf16>(z[j], r, qb[j][s][0], qb[j][s][1]);
                         }
                     }
-                } else {
+                    bool above = false;
 #pragma unroll
-                    for (int s = 0; s < kSteps; ++s) {
-                        uint32_t r[4];
-                        ldmatrix_trans(r, vt + in_tile<S::kRowBytes>(lane & 15, 2 * s + (lane >> 4)));
-                        mma<S::kBf16>(o[2 * s], hi, r[0], r[1]);
-                        mma<S::kBf16>(o[2 * s + 1], hi, r[2], r[3]);
-                        if constexpr (S::kBf16) {
-                            mma<true>(o[2 * s], lo, r[0], r[1]);
-                            mma<true>(o[2 * s + 1], lo, r[2], r[3]);
+                    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x = z[j][i] * c[j][i & 1];
+                            if (edge) {
+                                const int p = at + 16 * half + g + (i & 2) * 4;
+                                if (p < u.span.lo || p >= u.span.len) x = -INFINITY;
+                            }
+                            z[j][i] = x;
+                            above |= x > m[j][i & 1];
+                        }
+                    if (__any_sync(~0u, above)) {  // seldom, after the first blocks
+#pragma unroll
+                        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float top = fmaxf(z[j][i], z[j][i + 2]);
+#pragma unroll
+                                for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+                                const float now = fmaxf(m[j][i], top), shrink = exp2_fast(m[j][i] - finite_or_zero(now));
+                                m[j][i] = now;
+                                l[j][i] *= shrink;
+#pragma unroll
+                                for (int s = 0; s < kSteps; ++s) {
+                                    o[j][s][i] *= shrink;
+                                    o[j][s][i + 2] *= shrink;
+                                }
+                            }
+                    }
+                    uint32_t hi[kTiles][2], lo[kTiles][2];
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {  // positions g, then g + 8
+                            const float x = exp2_fast(z[j][2 * i] - (finite_or_zero(m[j][0]) - S::kBias));
+                            const float y = exp2_fast(z[j][2 * i + 1] - (finite_or_zero(m[j][1]) - S::kBias));
+                            l[j][0] += x;
+                            l[j][1] += y;
+                            const uint32_t w = pack<S::kBf16>(x, y);
+                            hi[j][i] = transpose(w);
+                            if constexpr (S::kBf16)  // what bf16 leaves of a weight, as a second term
+                                lo[j][i] = transpose(pack<true>(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
+                        }
+                    if constexpr (S::kBytes) {
+#pragma unroll
+                        for (int s = 0; s < kSteps; s += 2) {
+                            uint32_t r[4];
+                            ldmatrix_trans(r, vt + in_tile<S::kRowBytes>(row, s + side));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                // values (2g, 2g + 1) of positions 2t and 2t + 1: to pairs of positions
+                                const uint32_t p = __byte_perm(r[2 * i], 0, 0x3120), q = __byte_perm(r[2 * i + 1], 0, 0x3120);
+                                const uint32_t f[4] = {from_e4m3(p & 0xffff), from_e4m3(p >> 16), from_e4m3(q & 0xffff), from_e4m3(q >> 16)};
+#pragma unroll
+                                for (int j = 0; j < kTiles; ++j) mma<false>(o[j][s + i], f, hi[j][0], hi[j][1]);
+                            }
+                        }
+                    } else {
+                        const int vrow = 16 * half + (lane & 7) + (lane >> 4) * 8, vside = lane >> 3 & 1;
+#pragma unroll
+                        for (int s = 0; s < kSteps; ++s) {
+                            uint32_t r[4];
+                            ldmatrix_trans(r, vt + in_tile<S::kRowBytes>(vrow, 2 * s + vside));
+#pragma unroll
+                            for (int j = 0; j < kTiles; ++j) {
+                                mma<S::kBf16>(o[j][s], r, hi[j][0], hi[j][1]);
+                                if constexpr (S::kBf16) mma<true>(o[j][s], r, lo[j][0], lo[j][1]);
+                            }
                         }
                     }
                 }
             }
         }
-        // The warps' pieces meet, eight rows at a time.
+        // The warps' pieces meet, eight heads at a time.
         const bool whole = from == u.start && to == u.start + u.span.blocks;
         const int piece = 2 * blockIdx.x + (from == u.start);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if (8 * r >= rows) break;
-            l[r] += __shfl_xor_sync(~0u, l[r], 1);
-            l[r] += __shfl_xor_sync(~0u, l[r], 2);
-            float* mine_at = sums + (warp * 8 + g) * S::kPitch;
+        for (int j = 0; j < kTiles; ++j) {
+            if (8 * j >= rows) break;
 #pragma unroll
-            for (int n = 0; n < 2 * kSteps; ++n) {
-                // the column of accumulator n's first value, and how far the second is from it
-                const int d = S::kBytes ? n / 2 * 16 + 4 * t + (n & 1) : n * 8 + 2 * t;
-                mine_at[d] = o[n][2 * r];
-                mine_at[d + (S::kBytes ? 2 : 1)] = o[n][2 * r + 1];
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) l[j][i] += __shfl_xor_sync(~0u, l[j][i], x);
+                float* mine_at = sums + (warp * 8 + 2 * t + i) * S::kPitch;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const int d = 16 * s + (S::kBytes ? 2 * g : g);
+                    mine_at[d] = o[j][s][i];
+                    mine_at[d + (S::kBytes ? 1 : 8)] = o[j][s][i + 2];
+                }
+                if (g == 0) stats[warp * 8 + 2 * t + i] = make_float2(m[j][i], poison ? NAN : l[j][i]);
             }
-            if (t == 0) stats[warp * 8 + g] = make_float2(m[r], poison ? NAN : l[r]);
             __syncthreads();
-            for (int i = tid; i < min(8, rows - 8 * r) * kDim; i += kThreads) {
+            for (int i = tid; i < min(8, rows - 8 * j) * kDim; i += kThreads) {
                 const int row = i / kDim, d = i % kDim;
                 float top = -INFINITY;
 #pragma unroll
@@ -512,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     sum += f * s.y;
                 }
                 if (whole) {
-                    finish(a, u.b, kv_head * a.group + row0 + 8 * r + row, d, acc, sum, [&] { return top - S::kBias; });
+                    finish(a, u.b, kv_head * a.group + row0 + 8 * j + row, d, acc, sum, [&] { return top - S::kBias; });
                 } else {
-                    const long long at = static_cast<long long>(piece) * kRows + 8 * r + row;
+                    const long long at = static_cast<long long>(piece) * kRows + 8 * j + row;
                     a.part[at * kDim + d] = acc;
                     if (d == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, sum);
                 }
@@ -525,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
             unfinished = make_int2(u.b * units + u.head,
                                    static_cast<int>((u.start + u.span.blocks - 1) / share) - static_cast<int>(blockIdx.x));
         if (u.start + u.span.blocks >= end) break;
-        u.next(a);
+        u.template next<kBlock>(a);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (tid == 0) a.split[blockIdx.x] = unfinished;
@@ -533,32 +571,59 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 
 // The pieces of the unit that begins in share blockIdx.x and ends in a later one:
 // the head piece of its share, then the leading pieces of those that follow. One
-// query head a block, one column a thread.
+// query head a block, one column a thread, the pieces shared by the block's groups of kDim threads.
+constexpr int kJoin = 512;
 template <int kDim>
-__global__ void __launch_bounds__(kDim) k_kv_join(const Attend a, float bias) {
+__global__ void __launch_bounds__(kJoin) k_kv_join(const Attend a, float bias) {
+    constexpr int kGroups = kJoin / kDim;
+    __shared__ float sums[kGroups][kDim];
+    __shared__ float2 stats[kGroups];
     after_previous();
     const int2 split = a.split[blockIdx.x];
-    const int units = a.heads * a.tiles;
     if (split.x < 0) return;
-    const int b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
-    const int row = blockIdx.y, d = threadIdx.x, lane = d % 32;
+    const int units = a.heads * a.tiles, b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
+    const int row = blockIdx.y, d = threadIdx.x % kDim, group = threadIdx.x / kDim;
     if (row >= min(kRows, a.group - row0)) return;
     const float2* ml = reinterpret_cast<const float2*>(a.ml);
     auto at = [&](int i) {  // piece i's row
         return static_cast<long long>(2 * (blockIdx.x + i) + (i == 0)) * kRows + row;
     };
-    float top = -INFINITY;
-    for (int i = lane; i <= split.y; i += 32) top = fmaxf(top, ml[at(i)].x);
+    float top = -INFINITY, acc = 0.0f, sum = 0.0f;
+    constexpr int kAtOnce = 8;
+    for (int i0 = group; i0 <= split.y; i0 += kAtOnce * kGroups) {
+        float2 s[kAtOnce];
+        float x[kAtOnce];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = i0 + j * kGroups;
+            s[j] = i <= split.y ? ml[at(i)] : make_float2(-INFINITY, 0.0f);
+            x[j] = i <= split.y ? a.part[at(i) * kDim + d] : 0.0f;
+        }
+        float now = top;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) now = fmaxf(now, s[j].x);
+        const float base = finite_or_zero(now), shrink = exp2_fast(top - base);
+        acc *= shrink;
+        sum *= shrink;
+        top = now;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const float f = exp2_fast(s[j].x - base);
+            acc += f * x[j];
+            sum += f * s[j].y;
+        }
+    }
+    sums[group][d] = acc;
+    if (d == 0) stats[group] = make_float2(top, sum);
+    __syncthreads();
+    if (group) return;
+    for (int i = 1; i < kGroups; ++i) top = fmaxf(top, stats[i].x);
     const float base = finite_or_zero(top);
-    float acc = 0.0f, sum = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i <= split.y; ++i) {
-        const float2 s = ml[at(i)];
-        const float f = exp2_fast(s.x - base);
-        acc += f * a.part[at(i) * kDim + d];
-        sum += f * s.y;
+    acc = sum = 0.0f;
+    for (int i = 0; i < kGroups; ++i) {
+        const float f = exp2_fast(stats[i].x - base);
+        acc += f * sums[i][d];
+        sum += f * stats[i].y;
     }
     finish(a, b, head / a.tiles * a.group + row0 + row, d, acc, sum, [&] { return top - bias; });
 }
@@ -572,8 +637,8 @@ struct Layout {
 };
 Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int resident, int sms) {
     const int group = Hq / c->heads, tiles = (group + kRows - 1) / kRows, kd = padded_dim(c->dim);
-    long long blocks = (static_cast<long long>(M) * c->page_size + kBlock - 1) / kBlock;
-    if (window > 0) blocks = std::min(blocks, window / kBlock + 2ll);
+    long long blocks = (static_cast<long long>(M) * c->page_size + kGroup - 1) / kGroup;  // of 16: as many as of 32 or more
+    if (window > 0) blocks = std::min(blocks, window / kGroup + 2ll);
     const long long most = (blocks * B * c->heads * tiles + kWarps - 1) / kWarps;
     Layout l;
     l.grid = static_cast<int>(std::max(1ll, std::min(most, static_cast<long long>(sms) * resident)));
@@ -583,18 +648,19 @@ Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int r
     return l;
 }
 
-template <int kElem, int kDim, bool kWhole>
+template <int kElem, int kDim, int kTiles, bool kWhole>
 cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
     using S = Shape<kElem, kDim>;
-    cudaError_t rc = cudaFuncSetAttribute(k_kv_attend<kElem, kDim, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (rc == cudaSuccess)
-        rc = launch_overlapped(k_kv_attend<kElem, kDim, kWhole>, dim3(grid), kThreads, S::kSmem, stream, a);
+    const auto kernel = k_kv_attend<kElem, kDim, kTiles, kWhole>;
+    cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (rc == cudaSuccess) rc = launch_overlapped(kernel, dim3(grid), kThreads, S::kSmem, stream, a);
     if (rc != cudaSuccess || grid == 1) return rc;
-    return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, kRows)), kDim, 0, stream, a, S::kBias);
+    return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, kRows)), kJoin, 0, stream, a, S::kBias);
 }
 template <int kElem, int kDim>
 cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
-    return whole ? launch<kElem, kDim, true>(a, grid, stream) : launch<kElem, kDim, false>(a, grid, stream);
+    if (a.group > 8) return whole ? launch<kElem, kDim, 2, true>(a, grid, stream) : launch<kElem, kDim, 2, false>(a, grid, stream);
+    return whole ? launch<kElem, kDim, 1, true>(a, grid, stream) : launch<kElem, kDim, 1, false>(a, grid, stream);
 }
 template <int kElem>
 cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
@@ -674,7 +740,7 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
                    c->heads, group, (group + kRows - 1) / kRows, c->dim, c->dim * size / 16, M,
                    M * c->page_size, c->num_pages, window, elem == ESTREAM_KV_F16,
                    at(q, 4) && q_row % 2 == 0 && q_head % 2 == 0, FastDiv(c->page_size)};
-    const bool whole = c->page_size % kBlock == 0;
+    const bool whole = c->page_size % kGroup == 0;
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t rc = c->elem == ESTREAM_KV_BF16  ? launch<ESTREAM_KV_BF16>(a, whole, l.grid, stream)
                            : c->elem == ESTREAM_KV_F16 ? launch<ESTREAM_KV_F16>(a, whole, l.grid, stream)
