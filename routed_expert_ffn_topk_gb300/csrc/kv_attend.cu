@@ -5,13 +5,14 @@
 //   m = max(m1, m2), l = l1 e^{m1 - m} + l2 e^{m2 - m}, the sums alike,
 // so a sequence may be cut anywhere. Exponents are held in base 2.
 //
-// The work is all (row, key head) units' blocks of 16 positions, one unit behind
-// another; every CTA takes an equal, contiguous share of them, found from the
-// lengths on the device (so a captured graph keeps its balance as sequences grow). A
-// unit that ends inside a share is finished there; pieces of a unit that crosses
-// shares go through the workspace to a second kernel. In a share the warps take turns
-// at the blocks, each with a ring of its own filled by cp.async and with its own
-// (m, l, sum), and meet at a unit's end only.
+// The work is all (row, key head) units' blocks of 16 or 32 positions, one unit behind
+// another; every warp takes an equal, contiguous share of them, found from the
+// lengths on the device (so a captured graph keeps its balance as sequences grow), with
+// a ring of its own that cp.async fills ahead over units' ends. A unit that lies in one
+// share is finished there; the pieces of others go through the workspace to a
+// second kernel. With shares of CTAs, whose warps took turns at the blocks and met
+// at a unit's end, a batch with many short sequences waited for its slowest CTA
+// twice as long as the average one took.
 //
 // The matrix instructions take keys and transposed values as their 16 rows and the query heads of
 // a key head as their 8 columns (a wider group of heads: two tiles of 8, and units of 16),
@@ -40,8 +41,8 @@ struct Attend {
     float* lse;
     const uint8_t *k, *v;
     const int32_t *table, *lens;
-    float *part, *ml;  // workspace: pieces' sums [2 C][16][kDim], and their (m, l) [2 C][16][2]
-    int2* split;       // [C]: unit that begins in this share and goes on past it (-1: none), and how many shares follow
+    float *part, *ml;  // workspace: pieces' sums [2 warps][16][kDim], and their (m, l) [2 warps][16][2]
+    int2* split;       // [warps]: unit that begins in this share and goes on past it (-1: none), and how many shares follow
     long long q_row, q_head, out_row, out_head, table_row;
     long long k_page, k_token, k_head, v_page, v_token, v_head;  // bytes
     float scale, v_scale;  // scale * k_scale * log2 e
@@ -58,11 +59,9 @@ struct Shape {
     static constexpr int kRowBytes = kDim * (kBytes ? 1 : 2);
     static constexpr int kBlock = kRowBytes <= 128 ? 32 : 16;  // positions a warp takes at a time
     static constexpr int kStageBytes = 2 * kBlock * kRowBytes;  // keys, then values
-    static constexpr int kStages = kRowBytes == 64 ? 6 : kDim == 256 && kBytes ? 2 : 3;
-    static constexpr int kPitch = kDim + 4;  // floats; a warp's stores of sums are on different banks
-    static constexpr int kRing = kWarps * kStages * kStageBytes;
-    static constexpr int kSmem = kRing + kWarps * 8 * kPitch * 4 + kWarps * 8 * 8;
-    static constexpr int kResident = 2 * (kSmem + 1024 + 128) <= 228 * 1024 ? 2 : 1;  // 1 KB a CTA is the system's
+    static constexpr int kStages = kRowBytes == 64 ? 6 : 3;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes;
+    static constexpr int kResident = std::min(4, 228 * 1024 / (kSmem + 1024 + 128));  // 1 KB a CTA is the system's
     // fp16 weights are 2^14 times as large as the formula's: their smallest normal
     // value is then 2^-28 of the largest weight, not 2^-14
     static constexpr float kBias = kBf16 ? 0.0f : 14.0f;
@@ -162,18 +161,23 @@ struct Unit {
     }
 };
 
-// One (m, l, sum) of a row's piece to the row's result.
-template <typename F>
-__device__ __forceinline__ void finish(const Attend& a, int b, int h, int d, float acc, float l, F&& bias_and_m) {
-    const float inv = l > 0.0f ? a.v_scale / l : l == 0.0f ? 0.0f : NAN;
-    if (d < a.dim) {
-        const float y = l == 0.0f ? 0.0f : acc * inv;
-        uint16_t* to = static_cast<uint16_t*>(a.out) + b * a.out_row + h * a.out_head + d;
-        *to = a.out_f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
-    }
-    if (d == 0 && a.lse)
-        a.lse[static_cast<long long>(b) * a.Hq + h] =
-            l == 0.0f ? -INFINITY : (bias_and_m() + log2f(l)) * 0.69314718055994531f;
+// What a row's (m, l, sum) gives: the factor of its sums, and lse.
+struct Finish {
+    float by, lse;
+};
+__device__ __forceinline__ Finish finish(const Attend& a, float m, float l, float bias) {
+    if (l == 0.0f) return {0.0f, -INFINITY};
+    return {l > 0.0f ? a.v_scale / l : NAN, (m - bias + log2f(l)) * 0.69314718055994531f};
+}
+// One value of the result; sums of nothing may be anything.
+__device__ __forceinline__ void put(const Attend& a, int b, int h, int d, float sum, const Finish& f) {
+    if (d >= a.dim) return;
+    const float y = f.by == 0.0f ? 0.0f : sum * f.by;
+    static_cast<uint16_t*>(a.out)[b * a.out_row + h * a.out_head + d] =
+        a.out_f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
+__device__ __forceinline__ void put_lse(const Attend& a, int b, int h, const Finish& f) {
+    if (a.lse) a.lse[static_cast<long long>(b) * a.Hq + h] = f.lse;
 }
 
 // kTiles: tiles of 8 query heads (2 only where a group has more than 8). kWhole: page_size is a
@@ -185,10 +189,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     constexpr int kChunks = S::kRowBytes / 16;                 // of a padded row
     constexpr int kPerCopy = kChunks < 32 ? 32 / kChunks : 1;  // rows that a warp's copy covers
     extern __shared__ __align__(128) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + S::kRing);                   // [kWarps][8][kPitch]
-    float2* stats = reinterpret_cast<float2*>(sums + kWarps * 8 * S::kPitch);  // [kWarps][8]
     __shared__ long long scan[kWarps];
-    __shared__ Unit first_unit;
+    __shared__ Unit first_unit[kWarps];
     after_previous();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int units = a.heads * a.tiles;  // of a row
@@ -197,14 +199,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const Span s = span_of<kBlock>(a, b);
         if (s.blocks) continue;
-        const float fill = s.len == 0 ? 0.0f : NAN;
+        const Finish f = finish(a, 0.0f, s.len == 0 ? 0.0f : NAN, 0.0f);
         for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
             const int h = i / a.dim, d = i - h * a.dim;
-            finish(a, b, h, d, fill, fill, [] { return 0.0f; });
+            put(a, b, h, d, 1.0f, f);
+            if (d == 0) put_lse(a, b, h, f);
         }
     }
 
-    // This CTA's share, and the unit it begins in.
+    // This warp's share, and the unit it begins in.
     const int per_thread = (a.B + kThreads - 1) / kThreads, mine = tid * per_thread, past = min(a.B, mine + per_thread);
     long long count = 0;
     for (int b = mine; b < past; ++b) count += span_of<kBlock>(a, b).blocks;
@@ -223,13 +226,11 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     }
     total *= units;
     before = (before + upto - count) * units;
-    const long long share = max(static_cast<long long>(kWarps), (total + gridDim.x - 1) / gridDim.x);
-    const long long begin = blockIdx.x * share, end = min(total, begin + share);
-    if (begin >= end) {
-        if (tid == 0) a.split[blockIdx.x] = make_int2(-1, 0);
-        return;
-    }
-    if (begin >= before && begin < before + count * units) {
+    const int workers = gridDim.x * kWarps, worker = blockIdx.x * kWarps + warp;
+    const long long share = (total + workers - 1) / workers;
+    for (int w = 0; w < kWarps; ++w) {
+        const long long begin = (blockIdx.x * kWarps + w) * share;
+        if (begin < before || begin >= before + count * units) continue;
         Unit u;
         u.b = mine;
         u.start = before;
@@ -241,24 +242,19 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         }
         u.head = static_cast<int>((begin - u.start) / u.span.blocks);
         u.start += static_cast<long long>(u.head) * u.span.blocks;
-        first_unit = u;
+        first_unit[w] = u;
     }
     __syncthreads();
+    const long long begin = worker * share, end = min(total, begin + share);
+    if (begin >= end) {
+        if (lane == 0) a.split[worker] = make_int2(-1, 0);
+        return;
+    }
 
     // The warp's loads run ahead of its products, over units' ends.
-    Unit ahead = first_unit;
-    long long next = ahead.from(begin) + warp;
+    Unit ahead = first_unit[warp];
+    long long next = begin;
     bool more = true;
-    auto settle = [&] {  // the next block at or after `next` that is this warp's
-        while (next >= ahead.to(end)) {
-            if (ahead.start + ahead.span.blocks >= end) {
-                more = false;
-                return;
-            }
-            ahead.template next<kBlock>(a);
-            next = ahead.start + warp;
-        }
-    };
     // The page (-1: not attended, -2: out of range) and the place in it of the next block's
     // position lane % kBlock, or where a page holds whole groups, of its group's first one.
     int page = -1, slot = 0;
@@ -316,19 +312,18 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), there ? vf : a.v, there);
                 }
             }
-            next += kWarps;
-            settle();
+            if (++next == end) more = false;
+            else if (next == ahead.start + ahead.span.blocks) ahead.template next<kBlock>(a);
             look_up();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    settle();
     look_up();
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) issue(s);
 
-    Unit u = first_unit;
+    Unit u = first_unit[warp];
     int2 unfinished = make_int2(-1, 0);
     int stage = 0;
     for (;;) {
@@ -348,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                 for (int s = 0; s < kSteps; ++s) o[j][s][i] = o[j][s][i + 2] = 0.0f;
             }
         bool poison = false;
-        if (from + warp < to) {
+        {
             // Query fragments. An E4M3 key's four neighbouring values lie in one lane, so pairs
             // (2t, 2t + 1) and (2t + 8, 2t + 9) of the product are values (4t, 4t + 1) and (4t + 2, 4t + 3).
             uint32_t qb[kTiles][kSteps][2];
@@ -400,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     c[j][1] = __shfl_sync(~0u, down, 8 * t + 4);
                 }
             }
-            for (long long blk = from + warp; blk < to; blk += kWarps) {
+            for (long long blk = from; blk < to; ++blk) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
                 __syncwarp();  // every lane's copies are there, and every lane has read the stage that is filled next
                 issue(stage == 0 ? S::kStages - 1 : stage - 1);
@@ -515,117 +510,127 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                 }
             }
         }
-        // The warps' pieces meet, eight heads at a time.
+        // The unit's result, or this piece of it.
         const bool whole = from == u.start && to == u.start + u.span.blocks;
-        const int piece = 2 * blockIdx.x + (from == u.start);
+        const long long piece = 2ll * worker + (from == u.start);
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-            if (8 * j >= rows) break;
+        for (int j = 0; j < kTiles; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) l[j][i] += __shfl_xor_sync(~0u, l[j][i], x);
-                float* mine_at = sums + (warp * 8 + 2 * t + i) * S::kPitch;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const int d = 16 * s + (S::kBytes ? 2 * g : g);
-                    mine_at[d] = o[j][s][i];
-                    mine_at[d + (S::kBytes ? 1 : 8)] = o[j][s][i + 2];
-                }
-                if (g == 0) stats[warp * 8 + 2 * t + i] = make_float2(m[j][i], poison ? NAN : l[j][i]);
-            }
-            __syncthreads();
-            for (int i = tid; i < min(8, rows - 8 * j) * kDim; i += kThreads) {
-                const int row = i / kDim, d = i % kDim;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * 8 + row].x);
-                const float base = finite_or_zero(top);
-                float acc = 0.0f, sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 s = stats[w * 8 + row];
-                    const float f = exp2_fast(s.x - base);
-                    acc += f * sums[(w * 8 + row) * S::kPitch + d];
-                    sum += f * s.y;
-                }
+                if (poison) l[j][i] = NAN;
+                const int row = 8 * j + 2 * t + i;
+                if (row >= rows) continue;
+                const int h = kv_head * a.group + row0 + row;
                 if (whole) {
-                    finish(a, u.b, kv_head * a.group + row0 + 8 * j + row, d, acc, sum, [&] { return top - S::kBias; });
+                    const Finish f = finish(a, m[j][i], l[j][i], S::kBias);
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const int d = 16 * s + (S::kBytes ? 2 * g : g);
+                        put(a, u.b, h, d, o[j][s][i], f);
+                        put(a, u.b, h, d + (S::kBytes ? 1 : 8), o[j][s][i + 2], f);
+                    }
+                    if (g == 0) put_lse(a, u.b, h, f);
                 } else {
-                    const long long at = static_cast<long long>(piece) * kRows + 8 * j + row;
-                    a.part[at * kDim + d] = acc;
-                    if (d == 0) reinterpret_cast<float2*>(a.ml)[at] = make_float2(top, sum);
+                    float* to = a.part + (piece * kRows + row) * kDim;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const int d = 16 * s + (S::kBytes ? 2 * g : g);
+                        to[d] = o[j][s][i];
+                        to[d + (S::kBytes ? 1 : 8)] = o[j][s][i + 2];
+                    }
+                    if (g == 0) reinterpret_cast<float2*>(a.ml)[piece * kRows + row] = make_float2(m[j][i], l[j][i]);
                 }
             }
-            __syncthreads();
-        }
         if (!whole && from == u.start)
-            unfinished = make_int2(u.b * units + u.head,
-                                   static_cast<int>((u.start + u.span.blocks - 1) / share) - static_cast<int>(blockIdx.x));
+            unfinished = make_int2(u.b * units + u.head, static_cast<int>((u.start + u.span.blocks - 1) / share) - worker);
         if (u.start + u.span.blocks >= end) break;
         u.template next<kBlock>(a);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (tid == 0) a.split[blockIdx.x] = unfinished;
+    if (lane == 0) a.split[worker] = unfinished;
 }
 
-// The pieces of the unit that begins in share blockIdx.x and ends in a later one:
+// The pieces of the units that begin in a share of CTA blockIdx.x and end in a later one:
 // the head piece of its share, then the leading pieces of those that follow. One
-// query head a block, one column a thread, the pieces shared by the block's groups of kDim threads.
+// query head a block, one column a thread; a unit of many pieces takes the whole
+// block, of few a group of kDim threads.
 constexpr int kJoin = 512;
+constexpr int kAtOnce = 8;  // pieces a thread has under way
+struct Joined {
+    float m, l, sum;
+};
+template <int kDim>
+__device__ __forceinline__ Joined join(const Attend& a, int worker, int row, int d, int first, int last, int step) {
+    const float2* ml = reinterpret_cast<const float2*>(a.ml);
+    Joined r{-INFINITY, 0.0f, 0.0f};
+    for (int i0 = first; i0 <= last; i0 += kAtOnce * step) {
+        float2 s[kAtOnce];
+        float x[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = i0 + j * step;
+            s[j] = make_float2(-INFINITY, 0.0f);
+            x[j] = 0.0f;
+            if (i <= last) {
+                const long long at = (2ll * (worker + i) + (i == 0)) * kRows + row;  // piece i's row
+                s[j] = ml[at];
+                x[j] = a.part[at * kDim + d];
+            }
+        }
+        float now = r.m;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) now = fmaxf(now, s[j].x);
+        const float base = finite_or_zero(now), shrink = exp2_fast(r.m - base);
+        r.m = now;
+        r.l *= shrink;
+        r.sum *= shrink;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const float f = exp2_fast(s[j].x - base);
+            r.sum += f * x[j];
+            r.l += f * s[j].y;
+        }
+    }
+    return r;
+}
 template <int kDim>
 __global__ void __launch_bounds__(kJoin) k_kv_join(const Attend a, float bias) {
     constexpr int kGroups = kJoin / kDim;
     __shared__ float sums[kGroups][kDim];
     __shared__ float2 stats[kGroups];
     after_previous();
-    const int2 split = a.split[blockIdx.x];
-    if (split.x < 0) return;
-    const int units = a.heads * a.tiles, b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
-    const int row = blockIdx.y, d = threadIdx.x % kDim, group = threadIdx.x / kDim;
-    if (row >= min(kRows, a.group - row0)) return;
-    const float2* ml = reinterpret_cast<const float2*>(a.ml);
-    auto at = [&](int i) {  // piece i's row
-        return static_cast<long long>(2 * (blockIdx.x + i) + (i == 0)) * kRows + row;
-    };
-    float top = -INFINITY, acc = 0.0f, sum = 0.0f;
-    constexpr int kAtOnce = 8;
-    for (int i0 = group; i0 <= split.y; i0 += kAtOnce * kGroups) {
-        float2 s[kAtOnce];
-        float x[kAtOnce];
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int i = i0 + j * kGroups;
-            s[j] = i <= split.y ? ml[at(i)] : make_float2(-INFINITY, 0.0f);
-            x[j] = i <= split.y ? a.part[at(i) * kDim + d] : 0.0f;
+    const int units = a.heads * a.tiles, row = blockIdx.y, d = threadIdx.x % kDim, group = threadIdx.x / kDim;
+    for (int w = 0; w < kWarps; ++w) {
+        const int worker = blockIdx.x * kWarps + w;
+        const int2 split = a.split[worker];
+        if (split.x < 0) continue;
+        const int b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
+        if (row >= min(kRows, a.group - row0)) continue;
+        const bool few = split.y < 2 * kAtOnce;
+        if (few && w % kGroups != group) continue;
+        Joined r = join<kDim>(a, worker, row, d, few ? 0 : group, split.y, few ? 1 : kGroups);
+        if (!few) {
+            __syncthreads();  // all have read those before
+            sums[group][d] = r.sum;
+            if (d == 0) stats[group] = make_float2(r.m, r.l);
+            __syncthreads();
+            if (group) continue;
+            for (int i = 1; i < kGroups; ++i) r.m = fmaxf(r.m, stats[i].x);
+            const float base = finite_or_zero(r.m);
+            r.l = r.sum = 0.0f;
+            for (int i = 0; i < kGroups; ++i) {
+                const float f = exp2_fast(stats[i].x - base);
+                r.sum += f * sums[i][d];
+                r.l += f * stats[i].y;
+            }
         }
-        float now = top;
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) now = fmaxf(now, s[j].x);
-        const float base = finite_or_zero(now), shrink = exp2_fast(top - base);
-        acc *= shrink;
-        sum *= shrink;
-        top = now;
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const float f = exp2_fast(s[j].x - base);
-            acc += f * x[j];
-            sum += f * s[j].y;
-        }
+        const int h = head / a.tiles * a.group + row0 + row;
+        const Finish f = finish(a, r.m, r.l, bias);
+        put(a, b, h, d, r.sum, f);
+        if (d == 0) put_lse(a, b, h, f);
     }
-    sums[group][d] = acc;
-    if (d == 0) stats[group] = make_float2(top, sum);
-    __syncthreads();
-    if (group) return;
-    for (int i = 1; i < kGroups; ++i) top = fmaxf(top, stats[i].x);
-    const float base = finite_or_zero(top);
-    acc = sum = 0.0f;
-    for (int i = 0; i < kGroups; ++i) {
-        const float f = exp2_fast(stats[i].x - base);
-        acc += f * sums[i][d];
-        sum += f * stats[i].y;
-    }
-    finish(a, b, head / a.tiles * a.group + row0 + row, d, acc, sum, [&] { return top - bias; });
 }
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -642,9 +647,10 @@ Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int r
     const long long most = (blocks * B * c->heads * tiles + kWarps - 1) / kWarps;
     Layout l;
     l.grid = static_cast<int>(std::max(1ll, std::min(most, static_cast<long long>(sms) * resident)));
-    l.ml = static_cast<size_t>(l.grid) * 2 * kRows * kd * 4;
-    l.split = l.ml + static_cast<size_t>(l.grid) * 2 * kRows * 8;
-    l.bytes = (l.split + static_cast<size_t>(l.grid) * 8 + 15) / 16 * 16;
+    const size_t workers = static_cast<size_t>(l.grid) * kWarps;
+    l.ml = workers * 2 * kRows * kd * 4;
+    l.split = l.ml + workers * 2 * kRows * 8;
+    l.bytes = (l.split + workers * 8 + 15) / 16 * 16;
     return l;
 }
 
@@ -654,7 +660,7 @@ cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
     const auto kernel = k_kv_attend<kElem, kDim, kTiles, kWhole>;
     cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (rc == cudaSuccess) rc = launch_overlapped(kernel, dim3(grid), kThreads, S::kSmem, stream, a);
-    if (rc != cudaSuccess || grid == 1) return rc;
+    if (rc != cudaSuccess) return rc;
     return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, kRows)), kJoin, 0, stream, a, S::kBias);
 }
 template <int kElem, int kDim>
