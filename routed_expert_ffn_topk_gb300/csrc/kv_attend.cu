@@ -99,10 +99,10 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
-// Two E4M3 values (the low half) as fp16, exactly.
-__device__ __forceinline__ uint32_t from_e4m3(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// Four E4M3 values as fp16, exactly: the lower two, and the upper two.
+__device__ __forceinline__ void from_e4m3(uint32_t four, uint32_t& low, uint32_t& high) {
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(low), "=r"(high) : "r"(four));
 }
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack(float x, float y) {
@@ -253,14 +253,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 
     // The warp's loads run ahead of its products, over units' ends.
     Unit ahead = first_unit[warp];
-    long long next = begin;
-    bool more = true;
+    int next = static_cast<int>(begin - ahead.start);  // of the unit's blocks
+    long long left = end - begin;                      // blocks of the share that are not under way yet
     // The page (-1: not attended, -2: out of range) and the place in it of the next block's
     // position lane % kBlock, or where a page holds whole groups, of its group's first one.
     int page = -1, slot = 0;
     auto look_up = [&] {
-        if (!more) return;
-        int at = ahead.span.first + static_cast<int>(next - ahead.start) * kBlock + lane % kBlock;
+        int at = ahead.span.first + next * kBlock + lane % kBlock;
         if constexpr (kWhole) at &= ~(kGroup - 1);
         page = -1;
         const int entry = static_cast<int>(a.page.div(at));
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     const int my_chunk = lane % kChunks, my_row = lane / kChunks;
     uint32_t bad = 0;  // by stage: a page out of range
     auto issue = [&](int stage) {
-        if (more) {
+        if (left > 0) {
             const uint32_t to = ring + stage * S::kStageBytes;
             const int h = ahead.head / a.tiles;
             const uint8_t* kb = a.k + h * a.k_head + my_chunk * 16;
@@ -282,23 +281,41 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
             const bool in = my_chunk < a.chunks;
             bad = (bad & ~(1u << stage)) | (__any_sync(~0u, page == -2) ? 1u << stage : 0u);
             if constexpr (kWhole) {
-                const int at = ahead.span.first + static_cast<int>(next - ahead.start) * kBlock + my_row;
-                const int lo = ahead.span.lo - at, len = ahead.span.len - at;  // relative to this lane's first row
+                const int at = ahead.span.first + next * kBlock;
+                const uint8_t *kf[kBlock / kGroup], *vf[kBlock / kGroup];
+                bool there[kBlock / kGroup];
 #pragma unroll
                 for (int j = 0; j < kBlock / kGroup; ++j) {
                     const int p = __shfl_sync(~0u, page, j * kGroup), s = __shfl_sync(~0u, slot, j * kGroup) + my_row;
-                    const uint8_t* kf = kb + max(p, 0) * a.k_page + s * a.k_token;
-                    const uint8_t* vf = vb + max(p, 0) * a.v_page + s * a.v_token;
-                    const long long k_step = kPerCopy * a.k_token, v_step = kPerCopy * a.v_token;
+                    there[j] = in && p >= 0;
+                    kf[j] = kb + max(p, 0) * a.k_page + s * a.k_token;
+                    vf[j] = vb + max(p, 0) * a.v_page + s * a.v_token;
+                }
+                const long long k_step = kPerCopy * a.k_token, v_step = kPerCopy * a.v_token;
+                if (at >= ahead.span.lo && at + kBlock <= ahead.span.len) {  // all rows are attended
 #pragma unroll
-                    for (int i = 0; i < kGroup / kPerCopy; ++i) {
-                        const int r = j * kGroup + i * kPerCopy;
-                        const bool there = in && p >= 0 && r >= lo && r < len;
-                        copy16(to + in_tile<S::kRowBytes>(r + my_row, my_chunk), there ? kf : a.k, there);
-                        copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r + my_row, my_chunk), there ? vf : a.v, there);
-                        kf += k_step;
-                        vf += v_step;
-                    }
+                    for (int j = 0; j < kBlock / kGroup; ++j)
+#pragma unroll
+                        for (int i = 0; i < kGroup / kPerCopy; ++i) {
+                            const int r = j * kGroup + i * kPerCopy + my_row;
+                            copy16(to + in_tile<S::kRowBytes>(r, my_chunk), kf[j], there[j]);
+                            copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), vf[j], there[j]);
+                            kf[j] += k_step;
+                            vf[j] += v_step;
+                        }
+                } else {
+                    const int lo = ahead.span.lo - at, len = ahead.span.len - at;
+#pragma unroll
+                    for (int j = 0; j < kBlock / kGroup; ++j)
+#pragma unroll
+                        for (int i = 0; i < kGroup / kPerCopy; ++i) {
+                            const int r = j * kGroup + i * kPerCopy + my_row;
+                            const bool one = there[j] && r >= lo && r < len;
+                            copy16(to + in_tile<S::kRowBytes>(r, my_chunk), kf[j], one);
+                            copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), vf[j], one);
+                            kf[j] += k_step;
+                            vf[j] += v_step;
+                        }
                 }
             } else {
 #pragma unroll
@@ -308,13 +325,17 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     const bool there = in && p >= 0;
                     const uint8_t* kf = kb + max(p, 0) * a.k_page + s * a.k_token;
                     const uint8_t* vf = vb + max(p, 0) * a.v_page + s * a.v_token;
-                    copy16(to + in_tile<S::kRowBytes>(r, my_chunk), there ? kf : a.k, there);
-                    copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), there ? vf : a.v, there);
+                    copy16(to + in_tile<S::kRowBytes>(r, my_chunk), kf, there);
+                    copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), vf, there);
                 }
             }
-            if (++next == end) more = false;
-            else if (next == ahead.start + ahead.span.blocks) ahead.template next<kBlock>(a);
-            look_up();
+            if (--left > 0) {
+                if (++next == ahead.span.blocks) {
+                    ahead.template next<kBlock>(a);
+                    next = 0;
+                }
+                look_up();
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -332,12 +353,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         const int rows = min(kRows, a.group - row0);
         // Of heads 2t and 2t + 1 of each tile: the maximum (the same in all lanes of one t), this
         // lane's part of the sum of weights, and of the values' dims g and g + 8 of each 16 (E4M3: 2g, 2g + 1).
-        float m[kTiles][2], l[kTiles][2], o[kTiles][kSteps][4];
+        float m[kTiles][2], base[kTiles][2], l[kTiles][2], o[kTiles][kSteps][4];  // base: finite m, less the bias
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[j][i] = -INFINITY;
+                base[j][i] = -S::kBias;
                 l[j][i] = 0.0f;
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) o[j][s][i] = o[j][s][i + 2] = 0.0f;
@@ -395,14 +417,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     c[j][1] = __shfl_sync(~0u, down, 8 * t + 4);
                 }
             }
-            for (long long blk = from; blk < to; ++blk) {
+            int at = u.span.first + static_cast<int>(from - u.start) * kBlock;
+            for (int count = static_cast<int>(to - from); count > 0; --count, at += kBlock) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
                 __syncwarp();  // every lane's copies are there, and every lane has read the stage that is filled next
                 issue(stage == 0 ? S::kStages - 1 : stage - 1);
                 const uint32_t kt = ring + stage * S::kStageBytes, vt = kt + kBlock * S::kRowBytes;
                 poison |= bad >> stage & 1;
                 stage = stage + 1 == S::kStages ? 0 : stage + 1;
-                const int at = u.span.first + static_cast<int>(blk - u.start) * kBlock;
                 const bool edge = at < u.span.lo || at + kBlock > u.span.len;
 #pragma unroll
                 for (int half = 0; half < kBlock / 16; ++half) {
@@ -420,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                             ldmatrix(r, kt + in_tile<S::kRowBytes>(row, s + side));
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t f[4] = {from_e4m3(r[2 * i] & 0xffff), from_e4m3(r[2 * i + 1] & 0xffff),
-                                                       from_e4m3(r[2 * i] >> 16), from_e4m3(r[2 * i + 1] >> 16)};
+                                uint32_t f[4];
+                                from_e4m3(r[2 * i], f[0], f[2]);
+                                from_e4m3(r[2 * i + 1], f[1], f[3]);
 #pragma unroll
                                 for (int j = 0; j < kTiles; ++j) mma<false>(z[j], f, qb[j][s + i][0], qb[j][s + i][1]);
                             }
@@ -458,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                                 for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
                                 const float now = fmaxf(m[j][i], top), shrink = exp2_fast(m[j][i] - finite_or_zero(now));
                                 m[j][i] = now;
+                                base[j][i] = finite_or_zero(now) - S::kBias;
                                 l[j][i] *= shrink;
 #pragma unroll
                                 for (int s = 0; s < kSteps; ++s) {
@@ -471,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     for (int j = 0; j < kTiles; ++j)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {  // positions g, then g + 8
-                            const float x = exp2_fast(z[j][2 * i] - (finite_or_zero(m[j][0]) - S::kBias));
-                            const float y = exp2_fast(z[j][2 * i + 1] - (finite_or_zero(m[j][1]) - S::kBias));
+                            const float x = exp2_fast(z[j][2 * i] - base[j][0]);
+                            const float y = exp2_fast(z[j][2 * i + 1] - base[j][1]);
                             l[j][0] += x;
                             l[j][1] += y;
                             const uint32_t w = pack<S::kBf16>(x, y);
@@ -488,8 +512,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 // values (2g, 2g + 1) of positions 2t and 2t + 1: to pairs of positions
-                                const uint32_t p = __byte_perm(r[2 * i], 0, 0x3120), q = __byte_perm(r[2 * i + 1], 0, 0x3120);
-                                const uint32_t f[4] = {from_e4m3(p & 0xffff), from_e4m3(p >> 16), from_e4m3(q & 0xffff), from_e4m3(q >> 16)};
+                                uint32_t f[4];
+                                from_e4m3(__byte_perm(r[2 * i], 0, 0x3120), f[0], f[1]);
+                                from_e4m3(__byte_perm(r[2 * i + 1], 0, 0x3120), f[2], f[3]);
 #pragma unroll
                                 for (int j = 0; j < kTiles; ++j) mma<false>(o[j][s + i], f, hi[j][0], hi[j][1]);
                             }
@@ -554,8 +579,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 
 // The pieces of the units that begin in a share of CTA blockIdx.x and end in a later one:
 // the head piece of its share, then the leading pieces of those that follow. One
-// query head a block, one column a thread; a unit of many pieces takes the whole
-// block, of few a group of kDim threads.
+// column a thread; a unit of many pieces takes the whole block, of few a group of kDim threads. Where
+// units are few, and so their pieces many, each query head has a block of its own, else
+// two blocks share the heads, so that all fit on the device at once.
 constexpr int kJoin = 512;
 constexpr int kAtOnce = 8;  // pieces a thread has under way
 struct Joined {
@@ -601,35 +627,37 @@ __global__ void __launch_bounds__(kJoin) k_kv_join(const Attend a, float bias) {
     __shared__ float sums[kGroups][kDim];
     __shared__ float2 stats[kGroups];
     after_previous();
-    const int units = a.heads * a.tiles, row = blockIdx.y, d = threadIdx.x % kDim, group = threadIdx.x / kDim;
+    const int units = a.heads * a.tiles, d = threadIdx.x % kDim, group = threadIdx.x / kDim;
     for (int w = 0; w < kWarps; ++w) {
         const int worker = blockIdx.x * kWarps + w;
         const int2 split = a.split[worker];
         if (split.x < 0) continue;
         const int b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
-        if (row >= min(kRows, a.group - row0)) continue;
+        const int rows = min(kRows, a.group - row0);
         const bool few = split.y < 2 * kAtOnce;
         if (few && w % kGroups != group) continue;
-        Joined r = join<kDim>(a, worker, row, d, few ? 0 : group, split.y, few ? 1 : kGroups);
-        if (!few) {
-            __syncthreads();  // all have read those before
-            sums[group][d] = r.sum;
-            if (d == 0) stats[group] = make_float2(r.m, r.l);
-            __syncthreads();
-            if (group) continue;
-            for (int i = 1; i < kGroups; ++i) r.m = fmaxf(r.m, stats[i].x);
-            const float base = finite_or_zero(r.m);
-            r.l = r.sum = 0.0f;
-            for (int i = 0; i < kGroups; ++i) {
-                const float f = exp2_fast(stats[i].x - base);
-                r.sum += f * sums[i][d];
-                r.l += f * stats[i].y;
+        for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+            Joined r = join<kDim>(a, worker, row, d, few ? 0 : group, split.y, few ? 1 : kGroups);
+            if (!few) {
+                __syncthreads();  // all have read those before
+                sums[group][d] = r.sum;
+                if (d == 0) stats[group] = make_float2(r.m, r.l);
+                __syncthreads();
+                if (group) continue;
+                for (int i = 1; i < kGroups; ++i) r.m = fmaxf(r.m, stats[i].x);
+                const float base = finite_or_zero(r.m);
+                r.l = r.sum = 0.0f;
+                for (int i = 0; i < kGroups; ++i) {
+                    const float f = exp2_fast(stats[i].x - base);
+                    r.sum += f * sums[i][d];
+                    r.l += f * stats[i].y;
+                }
             }
+            const int h = head / a.tiles * a.group + row0 + row;
+            const Finish f = finish(a, r.m, r.l, bias);
+            put(a, b, h, d, r.sum, f);
+            if (d == 0) put_lse(a, b, h, f);
         }
-        const int h = head / a.tiles * a.group + row0 + row;
-        const Finish f = finish(a, r.m, r.l, bias);
-        put(a, b, h, d, r.sum, f);
-        if (d == 0) put_lse(a, b, h, f);
     }
 }
 
@@ -661,7 +689,8 @@ cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
     cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (rc == cudaSuccess) rc = launch_overlapped(kernel, dim3(grid), kThreads, S::kSmem, stream, a);
     if (rc != cudaSuccess) return rc;
-    return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, kRows)), kJoin, 0, stream, a, S::kBias);
+    const bool many = static_cast<long long>(a.B) * a.heads * a.tiles * 4 <= grid;  // 16 pieces a unit, when all are as long
+    return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, many ? kRows : 2)), kJoin, 0, stream, a, S::kBias);
 }
 template <int kElem, int kDim>
 cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
