@@ -34,6 +34,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;  // positions that lie in one page together where page_size is a multiple of it
 constexpr int kRows = 16;   // query heads that meet a key together, at most
+// What a unit costs a warp beside its blocks (queries, results), in blocks.
+constexpr int kOver = 1;
 
 struct Attend {
     const void* q;
@@ -41,12 +43,12 @@ struct Attend {
     float* lse;
     const uint8_t *k, *v;
     const int32_t *table, *lens;
-    float *part, *ml;  // workspace: pieces' sums [2 warps][16][kDim], and their (m, l) [2 warps][16][2]
-    int2* split;       // [warps]: unit that begins in this share and goes on past it (-1: none), and how many shares follow
+    float *part, *ml;  // workspace: pieces' sums [2 warps][rows][kDim], and their (m, l) [2 warps][rows][2]
+    int2* pieces;      // [B * heads * tiles]: the warp with a unit's first piece, and how many further pieces there are
     long long q_row, q_head, out_row, out_head, table_row;
     long long k_page, k_token, k_head, v_page, v_token, v_head;  // bytes
     float scale, v_scale;  // scale * k_scale * log2 e
-    int B, Hq, heads, group, tiles, dim, chunks, M, max_len, num_pages, window;
+    int B, Hq, heads, group, tiles, rows, dim, chunks, M, max_len, num_pages, window;
     int out_f16, q_words;  // type of q and out; q rows lie on 4 bytes
     FastDiv page;
 };
@@ -142,22 +144,31 @@ __device__ __forceinline__ Span span_of(const Attend& a, int b) {
     return s;
 }
 
-// A unit (row, key head and tile of 16 query heads) of a CTA's share [begin, end).
+// A unit: row, key head and tile of 16 query heads. Shares are cut from all units' costs,
+// one unit's kOver + blocks behind the other's.
 struct Unit {
     int b, head;  // head = key head * tiles + tile
     Span span;
-    long long start;  // its first block
-    __device__ __forceinline__ long long from(long long begin) const { return max(begin, start); }
-    __device__ __forceinline__ long long to(long long end) const { return min(end, start + span.blocks); }
-    // The next unit; there is one while start + blocks < end.
+    long long start;  // its cost's beginning
+    __device__ __forceinline__ long long cost() const { return span.blocks + kOver; }
+    // Its blocks [from, to) of a share [begin, end).
+    __device__ __forceinline__ int from(long long begin) const {
+        return static_cast<int>(max(0ll, begin - start - kOver));
+    }
+    __device__ __forceinline__ int to(long long end) const {
+        return static_cast<int>(min(static_cast<long long>(span.blocks), end - start - kOver));
+    }
+    // To the next unit with blocks in the share; false: there is none.
     template <int kBlock>
-    __device__ __forceinline__ void next(const Attend& a) {
-        start += span.blocks;
+    __device__ __forceinline__ bool next(const Attend& a, long long end) {
+        start += cost();
+        if (start + kOver >= end) return false;
         if (++head == a.heads * a.tiles) {
             head = 0;
             do span = span_of<kBlock>(a, ++b);
             while (span.blocks == 0);
         }
+        return true;
     }
 };
 
@@ -199,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const Span s = span_of<kBlock>(a, b);
         if (s.blocks) continue;
+        for (int i = tid; i < units; i += kThreads) a.pieces[static_cast<long long>(b) * units + i] = make_int2(0, 0);
         const Finish f = finish(a, 0.0f, s.len == 0 ? 0.0f : NAN, 0.0f);
         for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
             const int h = i / a.dim, d = i - h * a.dim;
@@ -209,8 +221,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 
     // This warp's share, and the unit it begins in.
     const int per_thread = (a.B + kThreads - 1) / kThreads, mine = tid * per_thread, past = min(a.B, mine + per_thread);
+    auto cost_of = [&](int b) {
+        const int n = span_of<kBlock>(a, b).blocks;
+        return n ? n + kOver : 0;
+    };
     long long count = 0;
-    for (int b = mine; b < past; ++b) count += span_of<kBlock>(a, b).blocks;
+    for (int b = mine; b < past; ++b) count += cost_of(b);
     long long upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,26 +251,25 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         u.b = mine;
         u.start = before;
         for (;; ++u.b) {
-            u.span = span_of<kBlock>(a, u.b);
-            const long long n = static_cast<long long>(u.span.blocks) * units;
+            const long long n = static_cast<long long>(cost_of(u.b)) * units;
             if (begin < u.start + n) break;
             u.start += n;
         }
-        u.head = static_cast<int>((begin - u.start) / u.span.blocks);
-        u.start += static_cast<long long>(u.head) * u.span.blocks;
+        u.span = span_of<kBlock>(a, u.b);
+        u.head = static_cast<int>((begin - u.start) / u.cost());
+        u.start += u.head * u.cost();
         first_unit[w] = u;
     }
     __syncthreads();
     const long long begin = worker * share, end = min(total, begin + share);
-    if (begin >= end) {
-        if (lane == 0) a.split[worker] = make_int2(-1, 0);
-        return;
-    }
+    if (begin >= end) return;
 
     // The warp's loads run ahead of its products, over units' ends.
-    Unit ahead = first_unit[warp];
-    int next = static_cast<int>(begin - ahead.start);  // of the unit's blocks
-    long long left = end - begin;                      // blocks of the share that are not under way yet
+    Unit u = first_unit[warp];
+    if (u.from(begin) >= u.to(end) && !u.template next<kBlock>(a, end)) return;
+    Unit ahead = u;
+    int next = ahead.from(begin), stop = ahead.to(end);  // of the unit's blocks
+    bool more = true;
     // The page (-1: not attended, -2: out of range) and the place in it of the next block's
     // position lane % kBlock, or where a page holds whole groups, of its group's first one.
     int page = -1, slot = 0;
@@ -273,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     const int my_chunk = lane % kChunks, my_row = lane / kChunks;
     uint32_t bad = 0;  // by stage: a page out of range
     auto issue = [&](int stage) {
-        if (left > 0) {
+        if (more) {
             const uint32_t to = ring + stage * S::kStageBytes;
             const int h = ahead.head / a.tiles;
             const uint8_t* kb = a.k + h * a.k_head + my_chunk * 16;
@@ -329,13 +344,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     copy16(to + kBlock * S::kRowBytes + in_tile<S::kRowBytes>(r, my_chunk), vf, there);
                 }
             }
-            if (--left > 0) {
-                if (++next == ahead.span.blocks) {
-                    ahead.template next<kBlock>(a);
-                    next = 0;
-                }
-                look_up();
+            if (++next == stop) {
+                more = ahead.template next<kBlock>(a, end);
+                next = 0;
+                stop = ahead.to(end);
             }
+            if (more) look_up();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -344,11 +358,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) issue(s);
 
-    Unit u = first_unit[warp];
-    int2 unfinished = make_int2(-1, 0);
     int stage = 0;
     for (;;) {
-        const long long from = u.from(begin), to = u.to(end);
+        const int from = u.from(begin), to = u.to(end);
         const int kv_head = u.head / a.tiles, row0 = u.head % a.tiles * kRows;  // first query head of this unit in its group
         const int rows = min(kRows, a.group - row0);
         // Of heads 2t and 2t + 1 of each tile: the maximum (the same in all lanes of one t), this
@@ -417,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     c[j][1] = __shfl_sync(~0u, down, 8 * t + 4);
                 }
             }
-            int at = u.span.first + static_cast<int>(from - u.start) * kBlock;
-            for (int count = static_cast<int>(to - from); count > 0; --count, at += kBlock) {
+            for (int at = u.span.first + from * kBlock, past = u.span.first + to * kBlock; at < past; at += kBlock) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
                 __syncwarp();  // every lane's copies are there, and every lane has read the stage that is filled next
                 issue(stage == 0 ? S::kStages - 1 : stage - 1);
@@ -536,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
             }
         }
         // The unit's result, or this piece of it.
-        const bool whole = from == u.start && to == u.start + u.span.blocks;
-        const long long piece = 2ll * worker + (from == u.start);
+        const bool whole = from == 0 && to == u.span.blocks;
+        const long long piece = 2ll * worker + (from == 0);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
 #pragma unroll
@@ -558,106 +569,136 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                     }
                     if (g == 0) put_lse(a, u.b, h, f);
                 } else {
-                    float* to = a.part + (piece * kRows + row) * kDim;
+                    float* to = a.part + (piece * a.rows + row) * kDim;
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s) {
                         const int d = 16 * s + (S::kBytes ? 2 * g : g);
                         to[d] = o[j][s][i];
                         to[d + (S::kBytes ? 1 : 8)] = o[j][s][i + 2];
                     }
-                    if (g == 0) reinterpret_cast<float2*>(a.ml)[piece * kRows + row] = make_float2(m[j][i], l[j][i]);
+                    if (g == 0) reinterpret_cast<float2*>(a.ml)[piece * a.rows + row] = make_float2(m[j][i], l[j][i]);
                 }
             }
-        if (!whole && from == u.start)
-            unfinished = make_int2(u.b * units + u.head, static_cast<int>((u.start + u.span.blocks - 1) / share) - worker);
-        if (u.start + u.span.blocks >= end) break;
-        u.template next<kBlock>(a);
+        if (from == 0 && lane == 0)
+            a.pieces[static_cast<long long>(u.b) * units + u.head] =
+                make_int2(worker, static_cast<int>((u.start + kOver + u.span.blocks - 1) / share) - worker);
+        if (!u.template next<kBlock>(a, end)) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0) a.split[worker] = unfinished;
 }
 
-// The pieces of the units that begin in a share of CTA blockIdx.x and end in a later one:
-// the head piece of its share, then the leading pieces of those that follow. One
-// column a thread; a unit of many pieces takes the whole block, of few a group of kDim threads. Where
-// units are few, and so their pieces many, each query head has a block of its own, else
-// two blocks share the heads, so that all fit on the device at once.
-constexpr int kJoin = 512;
-constexpr int kAtOnce = 8;  // pieces a thread has under way
+// The results of units in pieces: the first piece of one warp's share, then the leading pieces
+// of those that follow. An item is a unit's query head; a warp joins one of few pieces, a
+// block one of many (or, where items are few, any): 8 pieces a warp are under way at a time.
+// Neighbouring items, of one unit, go to different blocks.
+constexpr int kJoinWarps = 16;
+constexpr int kAtOnce = 8;
+template <int kDim>
 struct Joined {
-    float m, l, sum;
-};
-template <int kDim>
-__device__ __forceinline__ Joined join(const Attend& a, int worker, int row, int d, int first, int last, int step) {
-    const float2* ml = reinterpret_cast<const float2*>(a.ml);
-    Joined r{-INFINITY, 0.0f, 0.0f};
-    for (int i0 = first; i0 <= last; i0 += kAtOnce * step) {
-        float2 s[kAtOnce];
-        float x[kAtOnce];
+    static constexpr int kPer = kDim / 32;  // columns a lane, beside each other
+    float m = -INFINITY, l = 0.0f, sum[kPer] = {};
+    __device__ __forceinline__ void add(const Attend& a, int worker, int row, int lane, int first, int last, int step) {
+        const float2* ml = reinterpret_cast<const float2*>(a.ml);
+        for (int i0 = first; i0 <= last; i0 += kAtOnce * step) {
+            float2 s[kAtOnce];
+            float x[kAtOnce][kPer];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int i = i0 + j * step;
-            s[j] = make_float2(-INFINITY, 0.0f);
-            x[j] = 0.0f;
-            if (i <= last) {
-                const long long at = (2ll * (worker + i) + (i == 0)) * kRows + row;  // piece i's row
-                s[j] = ml[at];
-                x[j] = a.part[at * kDim + d];
-            }
-        }
-        float now = r.m;
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int i = i0 + j * step;
+                s[j] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) now = fmaxf(now, s[j].x);
-        const float base = finite_or_zero(now), shrink = exp2_fast(r.m - base);
-        r.m = now;
-        r.l *= shrink;
-        r.sum *= shrink;
+                for (int c = 0; c < kPer; ++c) x[j][c] = 0.0f;
+                if (i <= last) {
+                    const long long at = (2ll * (worker + i) + (i == 0)) * a.rows + row;  // piece i's row
+                    s[j] = ml[at];
+                    const float* from = a.part + at * kDim + lane * kPer;
+                    if constexpr (kPer == 2) {
+                        *reinterpret_cast<float2*>(x[j]) = *reinterpret_cast<const float2*>(from);
+                    } else {
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const float f = exp2_fast(s[j].x - base);
-            r.sum += f * x[j];
-            r.l += f * s[j].y;
-        }
-    }
-    return r;
-}
-template <int kDim>
-__global__ void __launch_bounds__(kJoin) k_kv_join(const Attend a, float bias) {
-    constexpr int kGroups = kJoin / kDim;
-    __shared__ float sums[kGroups][kDim];
-    __shared__ float2 stats[kGroups];
-    after_previous();
-    const int units = a.heads * a.tiles, d = threadIdx.x % kDim, group = threadIdx.x / kDim;
-    for (int w = 0; w < kWarps; ++w) {
-        const int worker = blockIdx.x * kWarps + w;
-        const int2 split = a.split[worker];
-        if (split.x < 0) continue;
-        const int b = split.x / units, head = split.x % units, row0 = head % a.tiles * kRows;
-        const int rows = min(kRows, a.group - row0);
-        const bool few = split.y < 2 * kAtOnce;
-        if (few && w % kGroups != group) continue;
-        for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-            Joined r = join<kDim>(a, worker, row, d, few ? 0 : group, split.y, few ? 1 : kGroups);
-            if (!few) {
-                __syncthreads();  // all have read those before
-                sums[group][d] = r.sum;
-                if (d == 0) stats[group] = make_float2(r.m, r.l);
-                __syncthreads();
-                if (group) continue;
-                for (int i = 1; i < kGroups; ++i) r.m = fmaxf(r.m, stats[i].x);
-                const float base = finite_or_zero(r.m);
-                r.l = r.sum = 0.0f;
-                for (int i = 0; i < kGroups; ++i) {
-                    const float f = exp2_fast(stats[i].x - base);
-                    r.sum += f * sums[i][d];
-                    r.l += f * stats[i].y;
+                        for (int c = 0; c < kPer; c += 4)
+                            *reinterpret_cast<float4*>(x[j] + c) = *reinterpret_cast<const float4*>(from + c);
+                    }
                 }
             }
-            const int h = head / a.tiles * a.group + row0 + row;
-            const Finish f = finish(a, r.m, r.l, bias);
-            put(a, b, h, d, r.sum, f);
-            if (d == 0) put_lse(a, b, h, f);
+            float now = m;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) now = fmaxf(now, s[j].x);
+            const float base = finite_or_zero(now), shrink = exp2_fast(m - base);
+            m = now;
+            l *= shrink;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) sum[c] *= shrink;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const float f = exp2_fast(s[j].x - base);
+                l += f * s[j].y;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) sum[c] += f * x[j][c];
+            }
         }
+    }
+};
+template <int kDim>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(const Attend a, float bias, int items, int per_block) {
+    using J = Joined<kDim>;
+    __shared__ float sums[kJoinWarps][kDim];
+    __shared__ float2 stats[kJoinWarps];
+    __shared__ bool many[kJoinWarps];
+    after_previous();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int units = a.heads * a.tiles, rows = a.rows;
+    // item i of this block: row, query head, that head's place in its unit, and the pieces; false: it has none, or one
+    auto item = [&](int i, int& b, int& h, int& row, int2& pieces) {
+        const int it = i * gridDim.x + blockIdx.x;
+        if (i >= per_block || it >= items) return false;
+        const int unit = it / rows, head = unit % units, row0 = head % a.tiles * kRows;
+        row = it % rows;
+        if (row0 + row >= a.group) return false;
+        pieces = a.pieces[unit];
+        b = unit / units;
+        h = head / a.tiles * a.group + row0 + row;
+        return pieces.y > 0;
+    };
+    int b, h, row;
+    int2 pieces = {};
+    uint32_t left = 1;  // items that the block joins
+    if (per_block > 1) {
+        const bool any = item(warp, b, h, row, pieces), few = pieces.y < 4 * kAtOnce;
+        if (any && few) {
+            J r;
+            r.add(a, pieces.x, row, lane, 0, pieces.y, 1);
+            const Finish f = finish(a, r.m, r.l, bias);
+#pragma unroll
+            for (int c = 0; c < J::kPer; ++c) put(a, b, h, lane * J::kPer + c, r.sum[c], f);
+            if (lane == 0) put_lse(a, b, h, f);
+        }
+        if (lane == 0) many[warp] = any && !few;
+        __syncthreads();
+        left = __ballot_sync(~0u, lane < kJoinWarps && many[lane]);
+    }
+    for (; left; left &= left - 1) {
+        if (!item(__ffs(left) - 1, b, h, row, pieces)) return;
+        J r;
+        r.add(a, pieces.x, row, lane, warp, pieces.y, kJoinWarps);
+        __syncthreads();  // all have read those before
+#pragma unroll
+        for (int c = 0; c < J::kPer; ++c) sums[warp][lane * J::kPer + c] = r.sum[c];
+        if (lane == 0) stats[warp] = make_float2(r.m, r.l);
+        __syncthreads();
+        const int d = threadIdx.x;
+        if (d >= kDim) continue;
+        float m = -INFINITY, l = 0.0f, sum = 0.0f;
+        for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, stats[w].x);
+        const float base = finite_or_zero(m);
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = exp2_fast(stats[w].x - base);
+            sum += f * sums[w][d];
+            l += f * stats[w].y;
+        }
+        const Finish f = finish(a, m, l, bias);
+        put(a, b, h, d, sum, f);
+        if (d == 0) put_lse(a, b, h, f);
     }
 }
 
@@ -666,7 +707,7 @@ int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 // How a call is laid out: shares, and the workspace's parts.
 struct Layout {
     int grid;
-    size_t ml, split, bytes;  // offsets behind the sums
+    size_t ml, pieces, bytes;  // offsets behind the sums
 };
 Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int resident, int sms) {
     const int group = Hq / c->heads, tiles = (group + kRows - 1) / kRows, kd = padded_dim(c->dim);
@@ -675,10 +716,10 @@ Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int r
     const long long most = (blocks * B * c->heads * tiles + kWarps - 1) / kWarps;
     Layout l;
     l.grid = static_cast<int>(std::max(1ll, std::min(most, static_cast<long long>(sms) * resident)));
-    const size_t workers = static_cast<size_t>(l.grid) * kWarps;
-    l.ml = workers * 2 * kRows * kd * 4;
-    l.split = l.ml + workers * 2 * kRows * 8;
-    l.bytes = (l.split + workers * 8 + 15) / 16 * 16;
+    const size_t workers = static_cast<size_t>(l.grid) * kWarps, rows = std::min(group, kRows);
+    l.ml = workers * 2 * rows * kd * 4;
+    l.pieces = l.ml + workers * 2 * rows * 8;
+    l.bytes = (l.pieces + static_cast<size_t>(B) * c->heads * tiles * 8 + 15) / 16 * 16;
     return l;
 }
 
@@ -689,8 +730,10 @@ cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
     cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (rc == cudaSuccess) rc = launch_overlapped(kernel, dim3(grid), kThreads, S::kSmem, stream, a);
     if (rc != cudaSuccess) return rc;
-    const bool many = static_cast<long long>(a.B) * a.heads * a.tiles * 4 <= grid;  // 16 pieces a unit, when all are as long
-    return launch_overlapped(k_kv_join<kDim>, dim3(grid, std::min(a.group, many ? kRows : 2)), kJoin, 0, stream, a, S::kBias);
+    // a block an item while all are on the device at once, else a warp
+    const int items = a.B * a.heads * a.tiles * a.rows, per_block = items <= 2 * grid ? 1 : kJoinWarps;
+    return launch_overlapped(k_kv_join<kDim>, dim3((items + per_block - 1) / per_block), 32 * kJoinWarps, 0, stream, a, S::kBias,
+                             items, per_block);
 }
 template <int kElem, int kDim>
 cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
@@ -768,11 +811,11 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int size = c->elem == ESTREAM_KV_E4M3 ? 1 : 2, group = Hq / c->heads;
     const Attend a{q, out, lse, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), table, lens,
-                   reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.ml), reinterpret_cast<int2*>(ws + l.split),
+                   reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.ml), reinterpret_cast<int2*>(ws + l.pieces),
                    q_row, q_head, out_row, out_head, table_row, c->k_page * size, c->k_token * size, c->k_head * size,
                    c->v_page * size, c->v_token * size, c->v_head * size,
                    static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634), c->v_scale, B, Hq,
-                   c->heads, group, (group + kRows - 1) / kRows, c->dim, c->dim * size / 16, M,
+                   c->heads, group, (group + kRows - 1) / kRows, std::min(group, kRows), c->dim, c->dim * size / 16, M,
                    M * c->page_size, c->num_pages, window, elem == ESTREAM_KV_F16,
                    at(q, 4) && q_row % 2 == 0 && q_head % 2 == 0, FastDiv(c->page_size)};
     const bool whole = c->page_size % kGroup == 0;
