@@ -617,7 +617,8 @@ estream_status estream_kv_append(const estream_kv_cache* cache, int elem, int T,
 
 /* Bytes of estream_kv_attend's workspace on the current device (0: none is
  * needed, or invalid sizes). */
-size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, int Hq, int M);
+size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, int Hq, int M,
+                                         int window);
 
 /*
  * Attention of one new token per row over its sequence in the cache:
@@ -634,8 +635,9 @@ size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, i
  *          row whose length is outside [0, M * page_size], or that needs a page
  *          outside [0, num_pages), becomes NaNs, its lse too.
  * lse      device, [B][Hq] fp32, or NULL.
- * workspace  device, 16-byte aligned, estream_kv_attend_workspace_bytes(cache, B, Hq, M)
- *          bytes, used by this call alone until it ends (no initial value).
+ * workspace  device, 16-byte aligned, estream_kv_attend_workspace_bytes(cache, B, Hq, M,
+ *          window) bytes, used by this call alone until it ends (no initial value);
+ *          may be NULL where that is 0.
  * Cache positions that are not attended (past the end, before the window, other
  * pages) may hold anything; an infinite value that is attended gives NaN. Products and sums in fp32; weights are kept to 16
  * bits for bf16 values and to 11 for the others. M * page_size < 2^31 - 4096, B *

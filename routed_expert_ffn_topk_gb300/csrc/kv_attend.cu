@@ -14,10 +14,15 @@
 // at a unit's end, a batch with many short sequences waited for its slowest CTA
 // twice as long as the average one took.
 //
+// Where all units fit on the device with a cluster of CTAs each and the table allows no
+// long sequence, a unit is split over its cluster's warps instead, whose pieces meet
+// through distributed shared memory: one launch, no workspace.
+//
 // The matrix instructions take keys and transposed values as their 16 rows and the query heads of
 // a key head as their 8 columns (a wider group of heads: two tiles of 8, and units of 16),
 // so a group of 8 heads or fewer wastes no row: with the heads as rows, it took twice the
 // instructions and registers.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -29,6 +34,7 @@
 
 namespace es {
 namespace {
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -49,6 +55,7 @@ struct Attend {
     long long k_page, k_token, k_head, v_page, v_token, v_head;  // bytes
     float scale, v_scale;  // scale * k_scale * log2 e
     int B, Hq, heads, group, tiles, rows, dim, chunks, M, max_len, num_pages, window;
+    int ctas;  // of the cluster that has a unit to itself; 0: shares of all units
     int out_f16, q_words;  // type of q and out; q rows lie on 4 bytes
     FastDiv page;
 };
@@ -202,74 +209,100 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scan[kWarps];
     __shared__ Unit first_unit[kWarps];
+    __shared__ float2 stats[kWarps][kRows];  // of a cluster's unit: the warps' (m, l)
     after_previous();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int units = a.heads * a.tiles;  // of a row
 
-    // Rows with nothing to attend: zeros, or NaN where the length is out of range.
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const Span s = span_of<kBlock>(a, b);
-        if (s.blocks) continue;
-        for (int i = tid; i < units; i += kThreads) a.pieces[static_cast<long long>(b) * units + i] = make_int2(0, 0);
-        const Finish f = finish(a, 0.0f, s.len == 0 ? 0.0f : NAN, 0.0f);
-        for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
-            const int h = i / a.dim, d = i - h * a.dim;
-            put(a, b, h, d, 1.0f, f);
-            if (d == 0) put_lse(a, b, h, f);
-        }
-    }
-
-    // This warp's share, and the unit it begins in.
-    const int per_thread = (a.B + kThreads - 1) / kThreads, mine = tid * per_thread, past = min(a.B, mine + per_thread);
-    auto cost_of = [&](int b) {
-        const int n = span_of<kBlock>(a, b).blocks;
-        return n ? n + kOver : 0;
-    };
-    long long count = 0;
-    for (int b = mine; b < past; ++b) count += cost_of(b);
-    long long upto = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) scan[warp] = upto;
-    __syncthreads();
-    long long total = 0, before = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) before = total;
-        total += scan[w];
-    }
-    total *= units;
-    before = (before + upto - count) * units;
-    const int workers = gridDim.x * kWarps, worker = blockIdx.x * kWarps + warp;
-    const long long share = (total + workers - 1) / workers;
-    for (int w = 0; w < kWarps; ++w) {
-        const long long begin = (blockIdx.x * kWarps + w) * share;
-        if (begin < before || begin >= before + count * units) continue;
-        Unit u;
-        u.b = mine;
-        u.start = before;
-        for (;; ++u.b) {
-            const long long n = static_cast<long long>(cost_of(u.b)) * units;
-            if (begin < u.start + n) break;
-            u.start += n;
-        }
+    const int worker = blockIdx.x * kWarps + warp;
+    Unit u;
+    long long begin, end, share = 0;
+    if (a.ctas) {
+        const int id = blockIdx.x / a.ctas;
+        u.b = id / units;
+        u.head = id % units;
+        u.start = 0;
         u.span = span_of<kBlock>(a, u.b);
-        u.head = static_cast<int>((begin - u.start) / u.cost());
-        u.start += u.head * u.cost();
-        first_unit[w] = u;
+        const int workers = a.ctas * kWarps, mine = worker % workers, each = (u.span.blocks + workers - 1) / workers;
+        begin = kOver + mine * each;
+        end = min(kOver + u.span.blocks, static_cast<int>(begin) + each);
+        if (u.span.blocks == 0) {  // nothing to attend: zeros, or NaN where the length is out of range
+            const Finish f = finish(a, 0.0f, u.span.len == 0 ? 0.0f : NAN, 0.0f);
+            const int h0 = u.head / a.tiles * a.group + u.head % a.tiles * kRows;
+            const int rows = min(kRows, a.group - u.head % a.tiles * kRows);
+            for (int i = mine / kWarps * kThreads + tid; i < rows * kDim; i += a.ctas * kThreads) {
+                put(a, u.b, h0 + i / kDim, i % kDim, 1.0f, f);
+                if (i % kDim == 0) put_lse(a, u.b, h0 + i / kDim, f);
+            }
+            return;
+        }
+    } else {
+        // Rows with nothing to attend: zeros, or NaN where the length is out of range.
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const Span s = span_of<kBlock>(a, b);
+            if (s.blocks) continue;
+            for (int i = tid; i < units; i += kThreads) a.pieces[static_cast<long long>(b) * units + i] = make_int2(0, 0);
+            const Finish f = finish(a, 0.0f, s.len == 0 ? 0.0f : NAN, 0.0f);
+            for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
+                const int h = i / a.dim, d = i - h * a.dim;
+                put(a, b, h, d, 1.0f, f);
+                if (d == 0) put_lse(a, b, h, f);
+            }
+        }
+
+        // This warp's share, and the unit it begins in.
+        const int per_thread = (a.B + kThreads - 1) / kThreads, mine = tid * per_thread, past = min(a.B, mine + per_thread);
+        auto cost_of = [&](int b) {
+            const int n = span_of<kBlock>(a, b).blocks;
+            return n ? n + kOver : 0;
+        };
+        long long count = 0;
+        for (int b = mine; b < past; ++b) count += cost_of(b);
+        long long upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        long long total = 0, before = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) before = total;
+            total += scan[w];
+        }
+        total *= units;
+        before = (before + upto - count) * units;
+        const int workers = gridDim.x * kWarps;
+        share = (total + workers - 1) / workers;
+        for (int w = 0; w < kWarps; ++w) {
+            const long long begin = (blockIdx.x * kWarps + w) * share;
+            if (begin < before || begin >= before + count * units) continue;
+            Unit u;
+            u.b = mine;
+            u.start = before;
+            for (;; ++u.b) {
+                const long long n = static_cast<long long>(cost_of(u.b)) * units;
+                if (begin < u.start + n) break;
+                u.start += n;
+            }
+            u.span = span_of<kBlock>(a, u.b);
+            u.head = static_cast<int>((begin - u.start) / u.cost());
+            u.start += u.head * u.cost();
+            first_unit[w] = u;
+        }
+        __syncthreads();
+        begin = worker * share;
+        end = min(total, begin + share);
+        if (begin >= end) return;
+        u = first_unit[warp];
+        if (u.from(begin) >= u.to(end) && !u.template next<kBlock>(a, end)) return;
     }
-    __syncthreads();
-    const long long begin = worker * share, end = min(total, begin + share);
-    if (begin >= end) return;
 
     // The warp's loads run ahead of its products, over units' ends.
-    Unit u = first_unit[warp];
-    if (u.from(begin) >= u.to(end) && !u.template next<kBlock>(a, end)) return;
     Unit ahead = u;
     int next = ahead.from(begin), stop = ahead.to(end);  // of the unit's blocks
-    bool more = true;
+    bool more = next < stop;
     // The page (-1: not attended, -2: out of range) and the place in it of the next block's
     // position lane % kBlock, or where a page holds whole groups, of its group's first one.
     int page = -1, slot = 0;
@@ -354,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    look_up();
+    if (more) look_up();
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) issue(s);
 
@@ -377,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                 for (int s = 0; s < kSteps; ++s) o[j][s][i] = o[j][s][i + 2] = 0.0f;
             }
         bool poison = false;
-        {
+        if (from < to) {
             // Query fragments. An E4M3 key's four neighbouring values lie in one lane, so pairs
             // (2t, 2t + 1) and (2t + 8, 2t + 9) of the product are values (4t, 4t + 1) and (4t + 2, 4t + 3).
             uint32_t qb[kTiles][kSteps][2];
@@ -547,6 +580,64 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
             }
         }
         // The unit's result, or this piece of it.
+        if (a.ctas) {  // the cluster's pieces meet
+            cg::cluster_group cluster = cg::this_cluster();
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            float* const mine = reinterpret_cast<float*>(smem + warp * S::kStages * S::kStageBytes);  // the warp's ring, as [kRows][kDim]
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int x = 4; x < 32; x *= 2) l[j][i] += __shfl_xor_sync(~0u, l[j][i], x);
+                    const int row = 8 * j + 2 * t + i;
+                    if (g == 0) stats[warp][row] = make_float2(m[j][i], poison ? NAN : l[j][i]);
+                    if (row >= rows) continue;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const int d = 16 * s + (S::kBytes ? 2 * g : g);
+                        mine[row * kDim + d] = o[j][s][i];
+                        mine[row * kDim + d + (S::kBytes ? 1 : 8)] = o[j][s][i + 2];
+                    }
+                }
+            cluster.sync();
+            const int rank = static_cast<int>(cluster.block_rank());
+            for (int e = rank * kThreads + tid; e < rows * kDim; e += a.ctas * kThreads) {
+                const int row = e / kDim, d = e % kDim;
+                float top = -INFINITY, sum = 0.0f, weight = 0.0f;
+                for (int r = 0; r < a.ctas; ++r) {
+                    const float2* theirs = cluster.map_shared_rank(&stats[0][0], r);
+                    const float* sums = reinterpret_cast<const float*>(cluster.map_shared_rank(smem, r)) + e;
+                    float2 s[kWarps];
+                    float x[kWarps];
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        s[w] = theirs[w * kRows + row];
+                        x[w] = sums[w * (S::kStages * S::kStageBytes / 4)];
+                    }
+                    float now = top;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) now = fmaxf(now, s[w].x);
+                    const float at = finite_or_zero(now), shrink = exp2_fast(top - at);
+                    top = now;
+                    sum *= shrink;
+                    weight *= shrink;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = exp2_fast(s[w].x - at);
+                        sum += f * x[w];
+                        weight += f * s[w].y;
+                    }
+                }
+                const Finish f = finish(a, top, weight, S::kBias);
+                const int h = kv_head * a.group + row0 + row;
+                put(a, u.b, h, d, sum, f);
+                if (d == 0) put_lse(a, u.b, h, f);
+            }
+            cluster.sync();  // nobody leaves while others read its piece
+            return;
+        }
         const bool whole = from == 0 && to == u.span.blocks;
         const long long piece = 2ll * worker + (from == 0);
 #pragma unroll
@@ -704,22 +795,56 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(const Attend a, flo
 
 int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// How a call is laid out: shares, and the workspace's parts.
+// How a call is laid out: CTAs, those of a unit's cluster (0: shares of all units), and the workspace's parts.
 struct Layout {
-    int grid;
+    int grid, ctas;
     size_t ml, pieces, bytes;  // offsets behind the sums
 };
-Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int resident, int sms) {
+template <template <int, int> class F, int kElem>
+int by_dim(int dim) {
+    switch (padded_dim(dim)) {
+        case 64: return F<kElem, 64>::value;
+        case 128: return F<kElem, 128>::value;
+        default: return F<kElem, 256>::value;
+    }
+}
+template <template <int, int> class F>
+int by_shape(const estream_kv_cache* c) {
+    return c->elem == ESTREAM_KV_BF16  ? by_dim<F, ESTREAM_KV_BF16>(c->dim)
+           : c->elem == ESTREAM_KV_F16 ? by_dim<F, ESTREAM_KV_F16>(c->dim)
+                                       : by_dim<F, ESTREAM_KV_E4M3>(c->dim);
+}
+template <int kElem, int kDim>
+struct Resident {
+    static constexpr int value = Shape<kElem, kDim>::kResident;
+};
+template <int kElem, int kDim>
+struct Block {
+    static constexpr int value = Shape<kElem, kDim>::kBlock;
+};
+
+constexpr int kMaxCtas = 8;
+constexpr int kDeep = 8;  // blocks of a cluster's warp, at most
+
+Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int sms) {
     const int group = Hq / c->heads, tiles = (group + kRows - 1) / kRows, kd = padded_dim(c->dim);
-    long long blocks = (static_cast<long long>(M) * c->page_size + kGroup - 1) / kGroup;  // of 16: as many as of 32 or more
-    if (window > 0) blocks = std::min(blocks, window / kGroup + 2ll);
-    const long long most = (blocks * B * c->heads * tiles + kWarps - 1) / kWarps;
-    Layout l;
-    l.grid = static_cast<int>(std::max(1ll, std::min(most, static_cast<long long>(sms) * resident)));
+    const int block = by_shape<Block>(c), resident = by_shape<Resident>(c);
+    long long blocks = (static_cast<long long>(M) * c->page_size + block - 1) / block;
+    if (window > 0) blocks = std::min(blocks, window / block + 2ll);
+    const long long units = static_cast<long long>(B) * c->heads * tiles, room = static_cast<long long>(sms) * resident;
+    Layout l{};
+    int ctas = 1;
+    while (ctas < kMaxCtas && ctas * kWarps < blocks) ctas *= 2;
+    if (units * ctas <= room && blocks <= ctas * kWarps * kDeep) {
+        l.ctas = ctas;
+        l.grid = static_cast<int>(units) * ctas;
+        return l;
+    }
+    l.grid = static_cast<int>(std::max(1ll, std::min((blocks * units + kWarps - 1) / kWarps, room)));
     const size_t workers = static_cast<size_t>(l.grid) * kWarps, rows = std::min(group, kRows);
     l.ml = workers * 2 * rows * kd * 4;
     l.pieces = l.ml + workers * 2 * rows * 8;
-    l.bytes = (l.pieces + static_cast<size_t>(B) * c->heads * tiles * 8 + 15) / 16 * 16;
+    l.bytes = (l.pieces + static_cast<size_t>(units) * 8 + 15) / 16 * 16;
     return l;
 }
 
@@ -728,8 +853,20 @@ cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
     using S = Shape<kElem, kDim>;
     const auto kernel = k_kv_attend<kElem, kDim, kTiles, kWhole>;
     cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (rc == cudaSuccess) rc = launch_overlapped(kernel, dim3(grid), kThreads, S::kSmem, stream, a);
     if (rc != cudaSuccess) return rc;
+    cudaLaunchAttribute attr[2] = {overlapped(), {}};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.ctas);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.ctas ? 2 : 1;
+    rc = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (rc != cudaSuccess || a.ctas) return rc;
     // a block an item while all are on the device at once, else a warp
     const int items = a.B * a.heads * a.tiles * a.rows, per_block = items <= 2 * grid ? 1 : kJoinWarps;
     return launch_overlapped(k_kv_join<kDim>, dim3((items + per_block - 1) / per_block), 32 * kJoinWarps, 0, stream, a, S::kBias,
@@ -747,20 +884,6 @@ cudaError_t launch(const Attend& a, bool whole, int grid, cudaStream_t stream) {
         case 128: return launch<kElem, 128>(a, whole, grid, stream);
         default: return launch<kElem, 256>(a, whole, grid, stream);
     }
-}
-
-template <int kElem>
-int resident_of(int dim) {
-    switch (padded_dim(dim)) {
-        case 64: return Shape<kElem, 64>::kResident;
-        case 128: return Shape<kElem, 128>::kResident;
-        default: return Shape<kElem, 256>::kResident;
-    }
-}
-int resident(const estream_kv_cache* c) {
-    return c->elem == ESTREAM_KV_BF16  ? resident_of<ESTREAM_KV_BF16>(c->dim)
-           : c->elem == ESTREAM_KV_F16 ? resident_of<ESTREAM_KV_F16>(c->dim)
-                                       : resident_of<ESTREAM_KV_E4M3>(c->dim);
 }
 
 bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -783,10 +906,10 @@ using namespace es;
 
 extern "C" {
 
-size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* c, int B, int Hq, int M) {
+size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* c, int B, int Hq, int M, int window) {
     int sms = 0;
-    if (!sizes_ok(c, B, Hq, M) || B == 0 || sm_count(&sms) != cudaSuccess) return 0;
-    return layout(c, B, Hq, M, 0, resident(c), sms).bytes;
+    if (!sizes_ok(c, B, Hq, M) || B == 0 || window < 0 || sm_count(&sms) != cudaSuccess) return 0;
+    return layout(c, B, Hq, M, window, sms).bytes;
 }
 
 estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int Hq, const void* q, long long q_row,
@@ -800,14 +923,14 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
         !(scale >= -3.402823466e38f && scale <= 3.402823466e38f))
         return ESTREAM_ERR_INVALID_ARG;
     if (B == 0) return ESTREAM_OK;
-    if (!at(q, 2) || !at(out, 2) || (M > 0 && !at(table, 4)) || !at(lens, 4) || (lse && !at(lse, 4)) || !at(workspace, 16))
+    if (!at(q, 2) || !at(out, 2) || (M > 0 && !at(table, 4)) || !at(lens, 4) || (lse && !at(lse, 4)))
         return ESTREAM_ERR_INVALID_ARG;
     const estream_status st = on_device();
     if (st != ESTREAM_OK) return st;
     int sms = 0;
     if (sm_count(&sms) != cudaSuccess) return ESTREAM_ERR_CUDA;
-    const Layout l = layout(c, B, Hq, M, window, resident(c), sms);
-    if (workspace_bytes < l.bytes) return ESTREAM_ERR_INVALID_ARG;
+    const Layout l = layout(c, B, Hq, M, window, sms);
+    if (l.bytes && (workspace_bytes < l.bytes || !at(workspace, 16))) return ESTREAM_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int size = c->elem == ESTREAM_KV_E4M3 ? 1 : 2, group = Hq / c->heads;
     const Attend a{q, out, lse, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), table, lens,
@@ -816,7 +939,7 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
                    c->v_page * size, c->v_token * size, c->v_head * size,
                    static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634), c->v_scale, B, Hq,
                    c->heads, group, (group + kRows - 1) / kRows, std::min(group, kRows), c->dim, c->dim * size / 16, M,
-                   M * c->page_size, c->num_pages, window, elem == ESTREAM_KV_F16,
+                   M * c->page_size, c->num_pages, window, l.ctas, elem == ESTREAM_KV_F16,
                    at(q, 4) && q_row % 2 == 0 && q_head % 2 == 0, FastDiv(c->page_size)};
     const bool whole = c->page_size % kGroup == 0;
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);

@@ -123,7 +123,7 @@ SIGNATURES = {
     "estream_mx4_error": (_I, [_P]),
     "estream_kv_append": (_I, [_P, _I, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _I, _I, _L, _P, _L, _L, _I, _P, _L, _L,
                               _P, _I, _I, _P]),
-    "estream_kv_attend_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "estream_kv_attend_workspace_bytes": (_SZ, [_P, _I, _I, _I, _I]),
     "estream_kv_attend": (_I, [_P, _I, _I, _I, _P, _L, _L, _P, _I, _L, _P, _F, _I, _P, _L, _L, _P, _P, _SZ, _P]),
     "estream_sample_tokens": (_I, [_P, _I, _L, _I, _I, _P, _F, _P, _I, _P, _F, _P, _F, _P, _P, _P, _P]),
     "estream_set_timing": (_I, [_P, _I]),
@@ -817,47 +817,69 @@ class PagedKV:
             raise ValueError("scales must be between 2^-100 and 2^100, and 1 for 16-bit caches")
         self.k, self.v, self.k_scale, self.v_scale = k, v, float(k_scale), float(v_scale)
         self.dtype, self.device, self.heads, self.dim, self.page_size = k.dtype, k.device, heads, dim, page
+        self._scale = dim ** -0.5
         self._desc = KvCache(k.data_ptr(), v.data_ptr(), elem, pages, page, heads, dim, k_scale, v_scale,
                              *k.stride()[:3], *v.stride()[:3])
         self._ref = ctypes.byref(self._desc)
         self._workspaces = {}
+        self._elem, self._index = elem, k.get_device()
 
-    def attend_workspace_bytes(self, B: int, Hq: int, M: int) -> int:
+    def attend_workspace_bytes(self, B: int, Hq: int, M: int, window: int = 0) -> int:
         """Bytes of kv_attend's workspace for B rows of Hq heads and tables of M pages."""
-        n = self._workspaces.get((B, Hq, M))
+        n = self._workspaces.get((B, Hq, M, window))
         if n is None:
             with torch.cuda.device(self.device):
-                n = lib().estream_kv_attend_workspace_bytes(self._ref, B, Hq, M)
+                n = lib().estream_kv_attend_workspace_bytes(self._ref, B, Hq, M, window)
             if len(self._workspaces) < 256:
-                self._workspaces[B, Hq, M] = n
+                self._workspaces[B, Hq, M, window] = n
         return n
 
 
-def _kv_heads(t: torch.Tensor, n: int, heads: int | None, cache: PagedKV, name: str, dtype=None):
-    """Checks [n, heads, dim] next to a cache; its strides of rows and heads."""
-    shape, st = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != n or (heads is not None and shape[1] != heads) or shape[2] != cache.dim:
-        raise ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {cache.dim}]")
-    if (t.dtype is not dtype if dtype is not None else
-            t.dtype is not cache.dtype and (cache._desc.elem != KV_E4M3 or t.dtype not in (torch.bfloat16, torch.float16))):
-        raise ValueError(f"{name} must be of the cache's type, or bf16 or fp16 next to an E4M3 cache, like the call's other rows")
-    if st[2] != 1 or t.device != cache.device:
-        raise ValueError(f"{name} must have contiguous rows of dim, on the cache's device")
-    return st[0], st[1]
+def _kv_bad(t: torch.Tensor, n: int, heads: int | None, cache: PagedKV, name: str, dtype):
+    """Why a tensor is not [n, heads, dim] next to the cache."""
+    if t.dim() != 3 or t.shape[0] != n or (heads is not None and t.shape[1] != heads) or t.shape[2] != cache.dim:
+        return ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {cache.dim}]")
+    if t.dtype is not dtype:
+        return ValueError(f"{name} must be {dtype}, as the call's other rows")
+    return ValueError(f"{name} must have contiguous rows of dim that do not overlap, on the cache's device")
 
 
-def _kv_table(table: torch.Tensor, cache: PagedKV) -> int:
-    """Elements between a page table's rows."""
-    shape, st = table.shape, table.stride()
-    if len(shape) != 2 or table.dtype is not torch.int32 or table.device != cache.device or (shape[1] > 1 and st[1] != 1):
-        raise ValueError("table must be [B, M] int32 with contiguous rows, on the cache's device")
-    return st[0]
+def _kv_dtype(t: torch.Tensor, cache: PagedKV, name: str) -> int:
+    """The element type of a call's rows."""
+    elem = _KV_ELEM.get(t.dtype)
+    if elem != cache._elem and (cache._elem != KV_E4M3 or elem is None):
+        raise ValueError(f"{name} must be of the cache's type, or bf16 or fp16 next to an E4M3 cache")
+    if elem == KV_E4M3:
+        raise ValueError(f"{name} must be bf16 or fp16")
+    return elem
 
 
 def _kv_ints(t: torch.Tensor, n: int, name: str, cache: PagedKV) -> int:
-    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != cache.device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != cache._index or not t.is_contiguous():
         raise ValueError(f"{name} must be [{n}] int32, contiguous, on the cache's device")
     return t.data_ptr()
+
+
+def _kv_table(t: torch.Tensor, cache: PagedKV):
+    """A page table's address, rows, columns and the elements between rows."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != cache._index:
+        raise ValueError("table must be [B, M] int32 on the cache's device")
+    (B, M), (row, one) = t.shape, t.stride()
+    if one != 1 and M > 1:
+        raise ValueError("table must have contiguous rows")
+    return t.data_ptr(), B, M, row
+
+
+def _kv_run(name: str, index: int, args) -> None:
+    """One call on the cache's device."""
+    fn = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st:
+        _check(st, name)
 
 
 def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, table: torch.Tensor,
@@ -869,39 +891,43 @@ def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch
     fp32 the keys, and q [T, Hq, dim], are rotated by position; returns the rotated
     queries (q_out, which may be q). A token with a negative position is skipped;
     one without a valid page is not stored and its queries become NaNs."""
+    elem, dt, heads, dim, index = _kv_dtype(k, cache, "k"), k.dtype, cache.heads, cache.dim, cache._index
     T = k.shape[0]
-    ks = _kv_heads(k, T, cache.heads, cache, "k")
-    vs = _kv_heads(v, T, cache.heads, cache, "v", k.dtype)
-    table_row = _kv_table(table, cache)
-    B, M = table.shape
+    k0, k1, k2 = k.stride() if k.dim() == 3 else (0, 0, 0)
+    if k2 != 1 or k.shape != (T, heads, dim) or k.get_device() != index:
+        raise _kv_bad(k, T, heads, cache, "k", dt)
+    v0, v1, v2 = v.stride() if v.dim() == 3 else (0, 0, 0)
+    if v2 != 1 or v.dtype is not dt or v.shape != (T, heads, dim) or v.get_device() != index:
+        raise _kv_bad(v, T, heads, cache, "v", dt)
+    tp, B, M, table_row = _kv_table(table, cache)
     if rows is None and B < T:
         raise ValueError("table must have a row for each token, or rows must name them")
-    pp = _kv_ints(positions, T, "positions", cache)
-    rp = None if rows is None else _kv_ints(rows, T, "rows", cache)
+    Hq = rot = q0 = q1 = o0 = o1 = 0
     qp = op = fp = None
-    qs = os_ = (0, 0)
-    Hq = rot = 0
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qs = _kv_heads(q, T, None, cache, "q", k.dtype)
+        q0, q1, q2 = q.stride() if q.dim() == 3 else (0, 0, 0)
+        Hq = q.shape[1] if q2 == 1 else 0
+        if q2 != 1 or q.dtype is not dt or q.shape != (T, Hq, dim) or q.get_device() != index:
+            raise _kv_bad(q, T, None, cache, "q", dt)
         if q_out is None:
-            q_out = torch.empty((T, Hq, cache.dim), dtype=q.dtype, device=q.device)
-        os_ = _kv_heads(q_out, T, Hq, cache, "q_out", k.dtype)
+            q_out = torch.empty((T, Hq, dim), dtype=dt, device=cache.device)
+        o0, o1, o2 = q_out.stride() if q_out.dim() == 3 else (0, 0, 0)
+        if o2 != 1 or q_out.dtype is not dt or q_out.shape != (T, Hq, dim) or q_out.get_device() != index \
+                or (T > 1 and o0 < dim) or (Hq > 1 and o1 < dim):
+            raise _kv_bad(q_out, T, Hq, cache, "q_out", dt)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or rot > cache.dim \
-                or inv_freq.device != cache.device or not inv_freq.is_contiguous():
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or rot > dim \
+                or inv_freq.get_device() != index or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be [rot / 2] fp32, contiguous, with rot at most dim, on the cache's device")
         fp = inv_freq.data_ptr()
-    with _on(k):
-        st = lib().estream_kv_append(cache._ref, _KV_ELEM[k.dtype], T, k.data_ptr(), *ks, v.data_ptr(), *vs, pp, rp,
-                                     table.data_ptr(), B, M, table_row, qp, *qs, Hq, op, *os_, fp, rot,
-                                     1 if interleaved else 0, _stream(stream, cache.device))
-    if st:
-        _check(st, "estream_kv_append")
+    _kv_run("estream_kv_append", index, (
+        cache._ref, elem, T, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _kv_ints(positions, T, "positions", cache),
+        None if rows is None else _kv_ints(rows, T, "rows", cache), tp, B, M, table_row, qp, q0, q1, Hq, op, o0, o1,
+        fp, rot, 1 if interleaved else 0, _stream(stream, cache.device)))
     return q_out
 
 
@@ -913,40 +939,43 @@ def kv_attend(cache: PagedKV, q: torch.Tensor, table: torch.Tensor, lens: torch.
     pages are table [B, M] int32: [B, Hq, dim], and the logarithms of the sums of
     exponentials into lse [B, Hq] fp32. scale: 1 / sqrt(dim) unless given. Rows
     that share a sequence (the tokens of a prompt) may share a table row
-    (table.expand). workspace: uint8, cache.attend_workspace_bytes(B, Hq, M) of
-    them, for this call alone until it ends (allocated when not given)."""
-    B = q.shape[0]
-    qs = _kv_heads(q, B, None, cache, "q")
-    Hq, dev = q.shape[1], cache.device
-    if Hq < 1 or Hq % cache.heads:
-        raise ValueError(f"q must have a multiple of {cache.heads} heads")
-    table_row = _kv_table(table, cache)
-    M = table.shape[1]
-    if table.shape[0] != B:
+    (table.expand). workspace: uint8, cache.attend_workspace_bytes(B, Hq, M,
+    window) of them, for this call alone until it ends (allocated when not given)."""
+    elem, dt, dim, index = _kv_dtype(q, cache, "q"), q.dtype, cache.dim, cache._index
+    if q.dim() != 3 or q.shape[2] != dim or q.shape[1] < 1 or q.shape[1] % cache.heads:
+        raise ValueError(f"q must be [B, Hq, {dim}] with Hq a multiple of {cache.heads}")
+    shape = B, Hq, _ = q.shape
+    q0, q1, q2 = q.stride()
+    if q2 != 1 or q.get_device() != index:
+        raise _kv_bad(q, B, None, cache, "q", dt)
+    tp, rows, M, table_row = _kv_table(table, cache)
+    if rows != B:
         raise ValueError("table must have a row for each row of q")
-    lp = _kv_ints(lens, B, "lens", cache)
-    if out is None:
-        out = torch.empty((B, Hq, cache.dim), dtype=q.dtype, device=dev)
-    os_ = _kv_heads(out, B, Hq, cache, "out", q.dtype)
-    ep = None
-    if lse is not None:
-        if lse.dtype is not torch.float32 or tuple(lse.shape) != (B, Hq) or lse.device != dev or not lse.is_contiguous():
-            raise ValueError(f"lse must be [{B}, {Hq}] fp32, contiguous, on the cache's device")
-        ep = lse.data_ptr()
     if window < 0:
         raise ValueError("window must not be negative")
-    n = cache.attend_workspace_bytes(B, Hq, M)
-    if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.dtype is not torch.uint8 or workspace.numel() < n \
-            or not workspace.is_contiguous():
-        raise ValueError(f"workspace must hold {n} bytes (uint8, contiguous) on the cache's device")
-    with _on(q):
-        st = lib().estream_kv_attend(cache._ref, _KV_ELEM[q.dtype], B, Hq, q.data_ptr(), *qs, table.data_ptr(), M,
-                                     table_row, lp, cache.dim ** -0.5 if scale is None else scale, window,
-                                     out.data_ptr(), *os_, ep, workspace.data_ptr(), n, _stream(stream, dev))
-    if st:
-        _check(st, "estream_kv_attend")
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=cache.device)
+    o0, o1, o2 = out.stride() if out.dim() == 3 else (0, 0, 0)
+    if o2 != 1 or out.dtype is not dt or out.shape != shape or out.get_device() != index \
+            or (B > 1 and o0 < dim) or (Hq > 1 and o1 < dim):
+        raise _kv_bad(out, B, Hq, cache, "out", dt)
+    ep = wp = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (B, Hq) or lse.get_device() != index or not lse.is_contiguous():
+            raise ValueError(f"lse must be [{B}, {Hq}] fp32, contiguous, on the cache's device")
+        ep = lse.data_ptr()
+    n = cache.attend_workspace_bytes(B, Hq, M, window)
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or workspace.numel() < n or workspace.get_device() != index \
+                or not workspace.is_contiguous():
+            raise ValueError(f"workspace must hold {n} bytes (uint8, contiguous) on the cache's device")
+        wp = workspace.data_ptr()
+    elif n:
+        workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        wp = workspace.data_ptr()
+    _kv_run("estream_kv_attend", index, (
+        cache._ref, elem, B, Hq, q.data_ptr(), q0, q1, tp, M, table_row, _kv_ints(lens, B, "lens", cache),
+        cache._scale if scale is None else scale, window, out.data_ptr(), o0, o1, ep, wp, n, _stream(stream, cache.device)))
     return out
 
 

@@ -245,7 +245,7 @@ def test_streams_and_graphs():
 def test_workspace():
     """A given workspace holds anything before the call; one that is too small is refused."""
     es = _es()
-    c = _kv.Case([3000, 100], 2, 64, 16, "bf16")
+    c = _kv.Case([30000, 100], 2, 64, 16, "bf16")
     q = _q(2, 8, 64, "bf16")
     want = es.kv_attend(c.cache, q, c.table, c.lens)
     n = c.cache.attend_workspace_bytes(2, 8, c.table.shape[1])

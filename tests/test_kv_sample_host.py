@@ -79,11 +79,11 @@ def test_attend_arguments(es, p):
     for kw in (dict(elem=1), dict(elem=2), dict(B=-1), dict(Hq=0), dict(Hq=3), dict(B=1 << 20, Hq=32), dict(q=None), dict(q=p + 1),
                dict(table=None), dict(table=p + 2), dict(M=-1), dict(M=1 << 28), dict(table_row=-1), dict(lens=None),
                dict(lens=p + 1), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(out=None),
-               dict(lse=p + 2), dict(ws=None), dict(ws=p + 8)):
+               dict(lse=p + 2)):
         assert call(**kw) == es.ERR_INVALID_ARG, kw
     assert call(B=0, q=None) == es.OK
-    assert L.estream_kv_attend_workspace_bytes(ctypes.byref(c), 0, 4, 1) == 0
-    assert L.estream_kv_attend_workspace_bytes(ctypes.byref(c), 2, 3, 1) == 0
+    assert L.estream_kv_attend_workspace_bytes(ctypes.byref(c), 0, 4, 1, 0) == 0
+    assert L.estream_kv_attend_workspace_bytes(ctypes.byref(c), 2, 3, 1, 0) == 0
 
 
 def test_sample_arguments(es, p):
