@@ -4,7 +4,7 @@
 //
 // Which token that is has to be what exact arithmetic says: with 10^5 tokens a
 // cumulative weight that is off by 1e-7 names another one in a row of a hundred. So
-// weights are integers, 2^42 for the largest, within 2^-38 of their value or one unit, and
+// weights are integers, 2^42 for the largest, within 2^-37 of their value or one unit, and
 // their sums are exact and the same in every order.
 //
 // A cluster of CTAs holds a row's logits in its shared memory, so they are read from HBM
@@ -36,7 +36,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;  // one a thread
 constexpr int kMaxCtas = 8;      // of a cluster
 constexpr int kFew = 2 * kThreads;  // tokens that one CTA sorts
-constexpr int kParts = 64;       // of a CTA's logits, weighed apart
 constexpr int kOne = 42;         // log2 of the largest weight
 
 struct Sample {
@@ -61,6 +60,11 @@ struct Elem {
         if constexpr (kElem == ESTREAM_MX4_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
         else if constexpr (kElem == ESTREAM_MX4_F16) return __half2float(static_cast<const __half*>(p)[i]);
         else return static_cast<const float*>(p)[i];
+    }
+    static __device__ __forceinline__ void put(void* p, int i, float x) {
+        if constexpr (kElem == ESTREAM_MX4_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+        else if constexpr (kElem == ESTREAM_MX4_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
+        else static_cast<float*>(p)[i] = x;
     }
 };
 
@@ -100,9 +104,9 @@ struct Weights {
         const float xh = r * kLn2, xl = fmaf(r, kLn2, -xh) + fmaf(r, kLn2Low, q * kLn2), x = xh + xl;
         // e^-x - 1 + xh, without its leading -xh
         const float tail = fmaf(x * x, fmaf(x, fmaf(x, 1.0f / 24.0f, -1.0f / 6.0f), 0.5f), -xl);
-        const long long change = static_cast<long long>(rintf(tail * 0x1p39f)) - static_cast<long long>(rintf(xh * 0x1p39f));
+        const int change = __float2int_rn(tail * 0x1p39f) - __float2int_rn(xh * 0x1p39f);  // above -2^31: xh < ln 2 / 256
         const uint64_t t = table[i];
-        const uint64_t w = t + static_cast<uint64_t>((static_cast<long long>(t >> 11) * change) >> 28);
+        const uint64_t w = t + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(t >> 12)) * change) >> 27);
         s = static_cast<int>(n);
         return w;
     }
@@ -143,6 +147,23 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
     return m;
 }
+// The largest of 16 bytes' logits, NaN if one is NaN; packed types as they lie.
+template <int kElem>
+__device__ __forceinline__ float largest(const uint4& w) {
+    if constexpr (kElem == ESTREAM_MX4_F32) {
+        float m;
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(w.x)), "f"(__uint_as_float(w.y)), "f"(__uint_as_float(w.z)));
+        return max_or_nan(m, __uint_as_float(w.w));
+    } else if constexpr (kElem == ESTREAM_MX4_BF16) {
+        const auto* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+        const float2 m = __bfloat1622float2(__hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
+        return max_or_nan(m.x, m.y);
+    } else {
+        const auto* h = reinterpret_cast<const __half2*>(&w);
+        const float2 m = __half22float2(__hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
+        return max_or_nan(m.x, m.y);
+    }
+}
 
 // The cut: kept are logits above `at`, and of those equal to it, `all` in number, the
 // first `ties` in the vocabulary's order.
@@ -154,12 +175,14 @@ struct Cut {
 // What a search found: nothing, all tokens up to the cut's bin, listed in the leading CTA, or the cut.
 enum Found { kNothing, kListed, kFound };
 
-struct Exchange {  // a CTA's numbers that its cluster reads
+// A CTA's numbers that its cluster needs: each CTA stores its own in all of them, so that they are local
+// when the cluster has met, and nobody has to stay for the others.
+struct Exchange {
     float top, least;  // its largest logit (NaN if it has one), and smallest finite one
     int first;         // its first largest logit's index
     uint32_t lo, hi;   // keys of a bin
-    uint64_t mass;
     uint32_t ties;
+    uint64_t mass;
     Cut cut;
 };
 
@@ -168,15 +191,14 @@ struct Shared {
     uint64_t mass[2][kBins];  // of this CTA, read by its cluster; used in turn
     uint32_t count[2][kBins];
     uint64_t list[kFew];      // the leading CTA's: tokens to sort
-    uint64_t part[kParts];
-    uint32_t part_ties[kParts];
     uint64_t warp[kWarps];
     uint32_t warp2[kWarps];
-    uint64_t before, chosen;
+    uint64_t before;
+    Cut cut;
     uint32_t bin, members, upto, listed;
     double min_below;         // temperature ln(min_p)
     float c, c_low;           // log2 e / temperature
-    Exchange exchange[2];     // used in turn
+    Exchange exchange[2][kMaxCtas];  // used in turn
 };
 
 // Ascending, n <= kFew values; those past n are free and become ~0. Pairs that are
@@ -216,18 +238,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     const int row = blockIdx.x / ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int first = rank * a.slice, n = max(0, min(a.slice, a.V - first));
 
-    // The logits come to shared memory.
-    {
-        const uint8_t* from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
-        const int vec = a.wide ? n / E::kPer : 0;
-        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(logits));
-        for (int i = tid; i < vec; i += kThreads)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * i), "l"(from + 16ll * i) : "memory");
-        for (int i = vec * E::kPer + tid; i < n; i += kThreads) {
-            if constexpr (E::kBytes == 4) reinterpret_cast<uint32_t*>(logits)[i] = reinterpret_cast<const uint32_t*>(from)[i];
-            else reinterpret_cast<uint16_t*>(logits)[i] = reinterpret_cast<const uint16_t*>(from)[i];
-        }
-    }
     const float given = a.temperatures ? a.temperatures[row] : a.temperature, temperature = given > 0x1p100f ? 0x1p100f : given;
     const int top_k = a.top_ks ? a.top_ks[row] : a.top_k;
     const float top_p = a.top_ps ? a.top_ps[row] : a.top_p;
@@ -250,71 +260,97 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             if (tid >> (7 - j) & 1) v = __umul64hi(v, kRoots[j] << 1);
         sh.table[tid] = (v + (1ull << (62 - kOne))) >> (63 - kOne);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-
     auto at = [&](int i) { return E::at(logits, i); };
-    // f(x, i) for the logits i of [begin, end), by `threads` threads of which this is `t`; begin a multiple of 8
-    auto each = [&](int begin, int end, int t, int threads, auto f) {
+    // f(x, i) for the logits i of [begin, end) from `lowest` on, by `threads` threads of which this is
+    // `t`; begin and end are multiples of 8 (past the row's end lies -infinity)
+    auto each = [&](int begin, int end, int t, int threads, float lowest, auto f) {
         for (int i = begin + t * E::kPer; i < end; i += threads * E::kPer) {
             const uint4 w = *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
+            if (!(largest<kElem>(w) >= lowest)) continue;
 #pragma unroll
-            for (int j = 0; j < E::kPer; ++j)
-                if (i + j < end) f(E::at(&w, j), i + j);
-        }
-    };
-
-    int turn = 0;  // of the exchanges: a number is written again only after a further meeting of the cluster
-    auto other = [&](int r) -> const Exchange& { return *cluster.map_shared_rank(&sh.exchange[turn], r); };
-
-    // The largest logit, and the range.
-    {
-        float top = -INFINITY, least = INFINITY;
-        if (use_k || use_p)
-            each(0, n, tid, kThreads, [&](float x, int) {
-                top = max_or_nan(top, x);
-                if (x > -INFINITY) least = fminf(least, x);
-            });
-        else each(0, n, tid, kThreads, [&](float x, int) { top = max_or_nan(top, x); });
-        top = warp_reduce(top, max_or_nan);
-        least = warp_reduce(least, fminf);
-        if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(__float_as_uint(top)) << 32 | __float_as_uint(least);
-        __syncthreads();
-        if (warp == 0) {
-            const uint64_t w = sh.warp[lane % kWarps];
-            top = warp_reduce(__uint_as_float(static_cast<uint32_t>(w >> 32)), max_or_nan);
-            least = warp_reduce(__uint_as_float(static_cast<uint32_t>(w)), fminf);
-            if (lane == 0) {
-                sh.exchange[turn].top = top;
-                sh.exchange[turn].least = least;
+            for (int j = 0; j < E::kPer; ++j) {
+                const float x = E::at(&w, j);
+                if (x >= lowest) f(x, i + j);
             }
         }
+    };
+    int turn = 0;  // of the exchanges: a number is stored again only after a further meeting of the cluster
+    // This CTA's numbers to the others: by the first warp, a CTA a lane. Then the cluster meets, and
+    // warps read a CTA a lane, and join them.
+    auto give = [&](auto set) {
+        if (warp == 0 && lane < ctas) set(cluster.map_shared_rank(&sh.exchange[turn][rank], lane));
         cluster.sync();
-    }
+        turn ^= 1;
+    };
+    auto given_by = [&](int r) -> const Exchange& { return sh.exchange[turn ^ 1][r]; };
+    // v of the first warp, joined over the CTA
+    auto in_first_warp = [&](uint64_t v) {
+        if (lane == 0) sh.warp[warp] = v;
+        __syncthreads();
+        return sh.warp[lane % kWarps];
+    };
+
+    // The logits come to shared memory, and the largest of them and the range are found on the way.
+    const int padded = (n + 7) / 8 * 8;
     float top = -INFINITY, least = INFINITY;
-    for (int r = 0; r < ctas; ++r) {
-        top = max_or_nan(top, other(r).top);
-        least = fminf(least, other(r).least);
+    {
+        const uint8_t* from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
+        const int vec = a.wide ? n / E::kPer : 0;
+        const bool ranged = use_k || use_p;
+        auto low = [&](float x) {
+            if (x > -INFINITY) least = fminf(least, x);
+        };
+        constexpr int kAtOnce = 4;
+        for (int i0 = tid; i0 < vec; i0 += kAtOnce * kThreads) {
+            uint4 v[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                if (i0 + j * kThreads < vec) v[j] = reinterpret_cast<const uint4*>(from)[i0 + j * kThreads];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                if (i0 + j * kThreads < vec) {
+                    reinterpret_cast<uint4*>(logits)[i0 + j * kThreads] = v[j];
+                    top = max_or_nan(top, largest<kElem>(v[j]));
+                    if (ranged)
+#pragma unroll
+                        for (int q = 0; q < E::kPer; ++q) low(E::at(&v[j], q));
+                }
+        }
+        for (int i = vec * E::kPer + tid; i < padded; i += kThreads) {
+            const float x = i < n ? E::at(from, i) : -INFINITY;
+            top = max_or_nan(top, x);
+            if (ranged) low(x);
+            E::put(logits, i, x);
+        }
+        top = warp_reduce(top, max_or_nan);
+        least = warp_reduce(least, fminf);
+        const uint64_t both = in_first_warp(static_cast<uint64_t>(__float_as_uint(top)) << 32 | __float_as_uint(least));
+        top = __uint_as_float(static_cast<uint32_t>(both >> 32));
+        least = __uint_as_float(static_cast<uint32_t>(both));
+        if (warp == 0) {
+            top = warp_reduce(top, max_or_nan);
+            least = warp_reduce(least, fminf);
+        }
+        give([&](Exchange* e) {
+            e->top = top;
+            e->least = least;
+        });
+        top = warp_reduce(lane < ctas ? given_by(lane).top : -INFINITY, max_or_nan);
+        least = warp_reduce(lane < ctas ? given_by(lane).least : INFINITY, fminf);
     }
-    turn ^= 1;
     const bool none = !(fabsf(top) < INFINITY);
     if (none || greedy) {
-        if (tid == 0) sh.exchange[turn].first = 0x7fffffff;
-        __syncthreads();
         int mine = 0x7fffffff;
-        if (!none)
-            each(0, n, tid, kThreads, [&](float x, int i) {
-                if (x == top) mine = min(mine, first + i);
-            });
-        mine = __reduce_min_sync(~0u, mine);
-        if (lane == 0) atomicMin(&sh.exchange[turn].first, mine);
-        cluster.sync();
+        if (!none) each(0, padded, tid, kThreads, top, [&](float, int i) { mine = min(mine, first + i); });
+        mine = __reduce_min_sync(~0u, static_cast<uint32_t>(mine));
+        mine = static_cast<int>(in_first_warp(static_cast<uint64_t>(mine)));
+        if (warp == 0) mine = __reduce_min_sync(~0u, static_cast<uint32_t>(mine));
+        give([&](Exchange* e) { e->first = mine; });
         if (rank == 0 && tid == 0) {
-            for (int r = 0; r < ctas; ++r) mine = min(mine, other(r).first);
+            for (int r = 0; r < ctas; ++r) mine = min(mine, given_by(r).first);
             a.ids[row] = none ? -1 : mine;
             if (a.prob) a.prob[row] = none ? NAN : 1.0f;
         }
-        cluster.sync();  // nobody leaves while others read its numbers
         return;
     }
 
@@ -356,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     // only listed where they are few.
     int which = 0;
     uint64_t target = 0;
+    constexpr float kLowest = -3.402823466e38f;  // what can be drawn is finite
     Cut cut{-INFINITY, 0, 0};  // everything
     auto find = [&](auto weighs, float floor, auto aim, bool may_list) {
         constexpr bool kWeigh = decltype(weighs)::value;
@@ -381,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                 if (level == 0) return b;
                 return b != static_cast<int>(base) ? -1 : min(kBins - 1, static_cast<int>((bin_of(x) - base) * kBins));
             };
-            each(0, n, tid, kThreads, [&](float x, int) {
-                if (!(x >= floor) || x == -INFINITY) return;
+            each(0, padded, tid, kThreads, floor, [&](float x, int) {
                 const int b = place(x);
                 if (b < 0) return;
                 if constexpr (kWeigh) {
@@ -435,8 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             if (all || members <= kFew) {
                 uint64_t* list = cluster.map_shared_rank(sh.list, 0);
                 uint32_t* listed = cluster.map_shared_rank(&sh.listed, 0);
-                each(0, n, tid, kThreads, [&](float x, int i) {
-                    if (!(x >= floor) || x == -INFINITY) return;
+                each(0, padded, tid, kThreads, floor, [&](float x, int i) {
                     const int b = place(x);
                     if (b != bin && !(all && b < bin && b >= 0)) return;
                     if (kWeigh && w.of(x) == 0) return;  // not counted either
@@ -470,16 +505,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                                 return x;
                             };
                             const int from = bound(key), to = bound(key + 1);
-                            sh.exchange[turn].cut = Cut{logit_of(sh.list[p]), static_cast<uint32_t>(p + 1 - from),
-                                                        static_cast<uint32_t>(to - from)};
+                            sh.cut = Cut{logit_of(sh.list[p]), static_cast<uint32_t>(p + 1 - from), static_cast<uint32_t>(to - from)};
                         }
                         lead += v2[j];
                     }
+                    __syncthreads();
+                    cut = sh.cut;
                     if (tid == 0) sh.listed = 0;
+                    if (warp == 0 && lane < ctas) cluster.map_shared_rank(&sh.exchange[turn][0], lane)->cut = cut;
                 }
                 cluster.sync();
-                cut = other(0).cut;
                 turn ^= 1;
+                cut = given_by(0).cut;
                 return kFound;
             }
             if (level >= 2 && shift == 0) {  // equal logits
@@ -494,32 +531,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             }
             if (level == 1) {  // the keys that the bin holds
                 uint32_t small = ~0u, large = 0;
-                each(0, n, tid, kThreads, [&](float x, int) {
-                    if (!(x >= floor) || x == -INFINITY || place(x) != bin) return;
+                each(0, padded, tid, kThreads, floor, [&](float x, int) {
+                    if (place(x) != bin) return;
                     small = min(small, key_of(x));
                     large = max(large, key_of(x));
                 });
                 small = __reduce_min_sync(~0u, small);
                 large = __reduce_max_sync(~0u, large);
-                if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(small) << 32 | large;
-                __syncthreads();
+                const uint64_t both = in_first_warp(static_cast<uint64_t>(small) << 32 | large);
+                small = static_cast<uint32_t>(both >> 32);
+                large = static_cast<uint32_t>(both);
                 if (warp == 0) {
-                    const uint64_t both = sh.warp[lane % kWarps];
-                    small = __reduce_min_sync(~0u, static_cast<uint32_t>(both >> 32));
-                    large = __reduce_max_sync(~0u, static_cast<uint32_t>(both));
-                    if (lane == 0) {
-                        sh.exchange[turn].lo = small;
-                        sh.exchange[turn].hi = large;
-                    }
+                    small = __reduce_min_sync(~0u, small);
+                    large = __reduce_max_sync(~0u, large);
                 }
-                cluster.sync();
-                lo = ~0u;
-                hi = 0;
-                for (int r = 0; r < ctas; ++r) {
-                    lo = min(lo, other(r).lo);
-                    hi = max(hi, other(r).hi);
-                }
-                turn ^= 1;
+                give([&](Exchange* e) {
+                    e->lo = small;
+                    e->hi = large;
+                });
+                lo = __reduce_min_sync(~0u, lane < ctas ? given_by(lane).lo : ~0u);
+                hi = __reduce_max_sync(~0u, lane < ctas ? given_by(lane).hi : 0u);
             } else {
                 hi -= static_cast<uint32_t>(bin) << shift;
                 lo = max(lo, hi - ((1u << shift) - 1));
@@ -579,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     };
 
     if (use_k) {
-        const Found f = find(std::false_type{}, -INFINITY, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, true);
+        const Found f = find(std::false_type{}, kLowest, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, true);
         if (f == kListed) {
             if (rank == 0) finish(top_k, 0);
             return;
@@ -588,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     if (use_p) {
         // equal logits that top-k leaves out are weighed with the others
         const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of(cut.at) : 0;
-        const Found f = find(std::true_type{}, cut.at, [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
+        const Found f = find(std::true_type{}, fmaxf(cut.at, kLowest), [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
         if (f == kListed) {
             if (rank == 0) finish(kFew, target);
             return;
@@ -596,94 +627,89 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         if (f == kNothing) cut = Cut{top, 1, 1};  // top_p of 0
     }
     if (least_kept > cut.at) cut = Cut{-INFINITY, 0, 0};
-    // The kept weight, by parts of the CTA's logits, and over the cluster.
-    const int length = ((n + kParts - 1) / kParts + 7) / 8 * 8;
-    {
-        uint64_t mass = 0;
-        uint32_t ties = 0;
-        for (int q = warp * (kParts / kWarps); q < (warp + 1) * (kParts / kWarps); ++q) {
-            uint64_t v = 0;
-            uint32_t t = 0;
-            each(q * length, min(n, (q + 1) * length), lane, 32, [&](float x, int) {
-                if (x > cut.at) {
-                    if (x >= least_kept) v += w.of(x);
-                } else if (x == cut.at) {
-                    ++t;
-                }
-            });
-            v = warp_reduce(v, add<uint64_t>);
-            t = __reduce_add_sync(~0u, t);
-            if (lane == 0) {
-                sh.part[q] = v;
-                sh.part_ties[q] = t;
-            }
-            mass += v;
-            ties += t;
-        }
-        if (lane == 0) {
-            sh.warp[warp] = mass;
-            sh.warp2[warp] = ties;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            mass = warp_reduce(lane < kWarps ? sh.warp[lane] : 0, add<uint64_t>);
-            ties = __reduce_add_sync(~0u, lane < kWarps ? sh.warp2[lane] : 0);
-            if (lane == 0) {
-                sh.exchange[turn].mass = mass;
-                sh.exchange[turn].ties = ties;
-            }
-        }
-    }
-    cluster.sync();
+    // The kept weight, by warps, each of which has a run of the CTA's logits, and over the cluster.
+    const float lowest = fmaxf(fmaxf(cut.at, least_kept), kLowest);
+    auto weigh = [&](int begin, int end, int t, int threads, uint64_t& mass, uint32_t& ties) {
+        mass = 0;
+        ties = 0;
+        each(begin, end, t, threads, lowest, [&](float x, int) {
+            if (cut.ties && x == cut.at) ++ties;
+            else mass += w.of(x);
+        });
+        mass = warp_reduce(mass, add<uint64_t>);
+        ties = __reduce_add_sync(~0u, ties);
+    };
+    const int length = ((padded + kWarps - 1) / kWarps + 7) / 8 * 8;
     const uint64_t tie = cut.ties ? w.of(cut.at) : 0;
-    uint64_t whole = 0, start = 0, mine = 0;
-    uint32_t left = cut.ties, my_left = 0;
-    for (int r = 0; r < ctas; ++r) {
-        const uint32_t t = min(left, other(r).ties);
-        const uint64_t m = other(r).mass + t * tie;
-        if (r == rank) {
-            start = whole;
-            mine = m;
-            my_left = left;
-        }
-        left -= t;
-        whole += m;
+    uint64_t mass;
+    uint32_t ties;
+    weigh(min(padded, warp * length), min(padded, (warp + 1) * length), lane, 32, mass, ties);
+    // What precedes, of this lane's value in its warp: (mass, ties) in the vocabulary's order, of which only the
+    // first `left` ties count.
+    struct Before {
+        uint64_t start, mass;
+        uint32_t left;
+    };
+    auto line_up = [&](uint64_t m, uint32_t n_ties, uint64_t start, uint32_t left) {
+        const uint32_t earlier = warp_scan(n_ties, lane) - n_ties;
+        Before b;
+        b.left = left - min(left, earlier);
+        b.mass = m + min(b.left, n_ties) * tie;
+        b.start = start + warp_scan(b.mass, lane) - b.mass;
+        return b;
+    };
+    // The lane whose value has the goal, and what precedes it there.
+    auto pick = [&](Before& b, uint64_t goal) {
+        const int who = __ffs(__ballot_sync(~0u, goal >= b.start && goal < b.start + b.mass)) - 1;
+        b.start = __shfl_sync(~0u, b.start, max(who, 0));
+        b.left = __shfl_sync(~0u, b.left, max(who, 0));
+        return who;
+    };
+    if (lane == 0) {
+        sh.warp[warp] = mass;
+        sh.warp2[warp] = ties;
     }
-    const uint64_t goal = point(whole);
-    cluster.sync();  // the others' numbers have been read
-    if (goal < start || goal >= start + mine || warp != 0) return;
-    // The part with it: two a lane.
-    {
-        const uint32_t t0 = sh.part_ties[2 * lane], t1 = sh.part_ties[2 * lane + 1];
-        const uint32_t ties_before = warp_scan(t0 + t1, lane) - t0 - t1;
-        const uint32_t l0 = my_left - min(my_left, ties_before), l1 = l0 - min(l0, t0);
-        const uint64_t m0 = sh.part[2 * lane] + min(l0, t0) * tie, m1 = sh.part[2 * lane + 1] + min(l1, t1) * tie;
-        const uint64_t at0 = start + warp_scan(m0 + m1, lane) - m0 - m1, at1 = at0 + m0;
-        const bool in0 = goal >= at0 && goal < at1, in1 = goal >= at1 && goal < at1 + m1;
-        const int who = __ffs(__ballot_sync(~0u, in0 || in1)) - 1;
-        const int part = __shfl_sync(~0u, 2 * lane + (in1 ? 1 : 0), who);
-        start = __shfl_sync(~0u, in1 ? at1 : at0, who);
-        my_left = __shfl_sync(~0u, in1 ? l1 : l0, who);
-        const int end = min(n, (part + 1) * length);
-        for (int i0 = part * length; i0 < end; i0 += 32) {
-            const int i = i0 + lane;
-            const float x = i < end ? at(i) : -INFINITY;
-            const bool equal = cut.ties && x == cut.at;
-            const uint32_t tied = __ballot_sync(~0u, equal);
-            const bool keep = (x > cut.at && x >= least_kept) || (equal && __popc(tied & ((1u << lane) - 1)) < my_left);
-            my_left -= min(my_left, static_cast<uint32_t>(__popc(tied)));
-            if (!__any_sync(~0u, keep)) continue;
-            const uint64_t upto = start + warp_scan(keep ? w.of(x) : 0, lane);
-            const uint32_t over = __ballot_sync(~0u, upto > goal);
-            if (over) {
-                if (lane == __ffs(over) - 1) {
-                    a.ids[row] = first + i;
-                    if (a.prob) a.prob[row] = w.share(x, whole);
-                }
-                return;
+    __syncthreads();
+    if (warp == 0) {
+        mass = warp_reduce(lane < kWarps ? sh.warp[lane] : 0, add<uint64_t>);
+        ties = __reduce_add_sync(~0u, lane < kWarps ? sh.warp2[lane] : 0);
+    }
+    give([&](Exchange* e) {
+        e->mass = mass;
+        e->ties = ties;
+    });
+    Before b = line_up(lane < ctas ? given_by(lane).mass : 0, lane < ctas ? given_by(lane).ties : 0, 0, cut.ties);
+    const uint64_t whole = __shfl_sync(~0u, b.start + b.mass, 31), goal = point(whole);
+    if (pick(b, goal) != rank) return;
+    // The run with it, its 16th part, and the token.
+    b = line_up(lane < kWarps ? sh.warp[lane] : 0, lane < kWarps ? sh.warp2[lane] : 0, b.start, b.left);
+    const int run = pick(b, goal), begin = run * length, end = min(padded, begin + length);
+    const int sub = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
+    weigh(min(end, begin + warp * sub), min(end, begin + (warp + 1) * sub), lane, 32, mass, ties);
+    __syncthreads();
+    if (lane == 0) {
+        sh.warp[warp] = mass;
+        sh.warp2[warp] = ties;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    b = line_up(lane < kWarps ? sh.warp[lane] : 0, lane < kWarps ? sh.warp2[lane] : 0, b.start, b.left);
+    const int part = pick(b, goal);
+    for (int i0 = begin + part * sub; i0 < min(end, begin + (part + 1) * sub); i0 += 32) {
+        const int i = i0 + lane;
+        const float x = i < min(end, begin + (part + 1) * sub) ? at(i) : -INFINITY;
+        const bool tied = cut.ties && x == cut.at;
+        Before c = line_up(!tied && x >= lowest ? w.of(x) : 0, tied, b.start, b.left);
+        const uint32_t over = __ballot_sync(~0u, c.start + c.mass > goal);
+        if (over) {
+            if (lane == __ffs(over) - 1) {
+                a.ids[row] = first + i;
+                if (a.prob) a.prob[row] = w.share(x, whole);
             }
-            start = __shfl_sync(~0u, upto, 31);
+            return;
         }
+        b.start = __shfl_sync(~0u, c.start + c.mass, 31);
+        b.left = __shfl_sync(~0u, c.left - min(c.left, static_cast<uint32_t>(tied)), 31);
     }
 }
 
