@@ -85,35 +85,38 @@ __constant__ uint64_t kRoots[8] = {0x5a827999fcef3242ull, 0x6ba27e656b4eb57aull,
 
 // Weights of a row: exp((l - max) / temperature) = 2^-t, t = (max - l) c, c = log2 e / temperature.
 // max - l and c are held as sums of two floats, so t is good to 2^-40; it is cut into
-// whole, 1/256ths (a table) and a rest r < 2^-8, whose 2^-r is a short series.
+// whole, 1/256ths (a table) and a rest |r| <= 2^-9, whose 2^-r is a short series. Whole
+// numbers come out of floats by adding 1.5 * 2^23, whose last bit is 1: conversions
+// go through a unit of a quarter of the rate.
 struct Weights {
     float top, c, c_low;
     const uint64_t* table;  // 2^(42 - i / 256)
     // The weight is the result times 2^-s.
     __device__ __forceinline__ uint64_t parts(float l, int& s) const {
+        constexpr float kRound = 12582912.0f;
+        constexpr int kRoundBits = 0x4b400000;
         s = 0;
         const float d = top - l;
         const float z = d - top, low = (top - (d - z)) - (l + z);  // what rounding took from d
         const float p = d * c;
         if (!(p < kOne + 2.0f)) return 0;
         const float q = fmaf(d, c, -p) + fmaf(d, c_low, low * c);
-        const float n = floorf(p), f = p - n;
-        const int i = static_cast<int>(f * 256.0f);
-        const float r = f - static_cast<float>(i) * (1.0f / 256.0f);
+        const float rounded = fmaf(p, 256.0f, kRound);
+        const int k = __float_as_int(rounded) - kRoundBits;
+        const float r = fmaf(rounded - kRound, -1.0f / 256.0f, p);
         constexpr float kLn2 = 0.693147182464599609375f, kLn2Low = -1.904654299957767e-9f;
         const float xh = r * kLn2, xl = fmaf(r, kLn2, -xh) + fmaf(r, kLn2Low, q * kLn2), x = xh + xl;
-        // e^-x - 1 + xh, without its leading -xh
-        const float tail = fmaf(x * x, fmaf(x, fmaf(x, 1.0f / 24.0f, -1.0f / 6.0f), 0.5f), -xl);
-        const int change = __float2int_rn(tail * 0x1p39f) - __float2int_rn(xh * 0x1p39f);  // above -2^31: xh < ln 2 / 256
-        const uint64_t t = table[i];
-        const uint64_t w = t + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(t >> 12)) * change) >> 27);
-        s = static_cast<int>(n);
-        return w;
+        // e^-x - 1 + xh, without its leading -xh; the next term is below 2^-42
+        const float tail = fmaf(x * x, fmaf(x, -1.0f / 6.0f, 0.5f), -xl);
+        const int change = __float_as_int(fmaf(tail, 0x1p39f, kRound)) - kRoundBits - __float2int_rn(xh * 0x1p39f);
+        const uint64_t t = table[k & 255];
+        s = k >> 8;
+        return t + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(t >> 12)) * change) >> 27);
     }
     __device__ __forceinline__ uint64_t of(float l) const {
         int s;
         const uint64_t w = parts(l, s);
-        return (w + (1ull << s >> 1)) >> s;
+        return ((w << 1 >> s) + 1) >> 1;
     }
     // A kept token's probability, from its weight before that became a whole number of units.
     __device__ __forceinline__ float share(float l, uint64_t whole) const {
@@ -186,43 +189,77 @@ struct Exchange {
     Cut cut;
 };
 
+// A bin's measure: the number of its tokens, and their weight in three parts of 15 bits,
+// which native 32-bit atomics add up (an SM has none of 64 bits on shared memory, and loops instead: bins of
+// 32000 logits took 11 us).
+constexpr int kPart = 15;
+struct Bins {
+    uint32_t count[kBins], part[3][kBins];
+};
 struct Shared {
     uint64_t table[256];
-    uint64_t mass[2][kBins];  // of this CTA, read by its cluster; used in turn
-    uint32_t count[2][kBins];
+    Bins bins[2];             // of this CTA, read by its cluster; used in turn
     uint64_t list[kFew];      // the leading CTA's: tokens to sort
     uint64_t warp[kWarps];
     uint32_t warp2[kWarps];
     uint64_t before;
     Cut cut;
     uint32_t bin, members, upto, listed;
-    double min_below;         // temperature ln(min_p)
-    float c, c_low;           // log2 e / temperature
+    float min_below, min_below_low;  // temperature ln(min_p)
+    float c, c_low;                  // log2 e / temperature
     Exchange exchange[2][kMaxCtas];  // used in turn
 };
 
-// Ascending, n <= kFew values; those past n are free and become ~0. Pairs that are
-// 32 apart or less stay inside a warp's 64 values, so only wider steps need the CTA's barrier.
+// Puts n <= kFew different values in ascending order. A few are counted: each value's
+// place is the number of smaller ones. More go through a bitonic network, two values a
+// thread; pairs that are less than 64 apart lie in one warp.
 __device__ __forceinline__ void sort(uint64_t* v, int n) {
     const int tid = threadIdx.x;
-    int size = 64;
+    if (n <= kFew / 4) {
+        int size = 16;
+        while (size < n) size *= 2;
+        const int share = kThreads / size, i = tid / share, part = tid % share;  // threads of a value
+        const uint64_t mine = i < n ? v[i] : 0;
+        int place = 0;
+        if (i < n)
+            for (int j = part; j < n; j += share) place += v[j] < mine;
+        for (int o = share / 2; o; o >>= 1) place += __shfl_xor_sync(~0u, place, o);
+        __syncthreads();
+        if (i < n && part == 0) v[place] = mine;
+        __syncthreads();
+        return;
+    }
+    int size = kFew / 2;
     while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kThreads) v[i] = ~0ull;
-    __syncthreads();
+    uint64_t x[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) x[j] = 2 * tid + j < n ? v[2 * tid + j] : ~0ull;
     for (int run = 2; run <= size; run *= 2) {
-        for (int step = run / 2; step; step /= 2) {
-            if (tid < size / 2) {
-                const int i = 2 * tid - (tid & (step - 1)), j = i + step;
-                const uint64_t x = v[i], y = v[j];
-                if ((x > y) == ((i & run) == 0)) {
-                    v[i] = y;
-                    v[j] = x;
-                }
+        const bool up = (2 * tid & run) == 0;
+        for (int step = run / 2; step >= 2; step /= 2) {
+            const bool first = (2 * tid & step) == 0;
+            if (step >= 64) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) v[2 * tid + j] = x[j];
+                __syncthreads();
             }
-            if (step > 32 || (step == 1 && run >= 64)) __syncthreads();
-            else __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint64_t y = step >= 64 ? v[(2 * tid + j) ^ step] : __shfl_xor_sync(~0u, x[j], step / 2);
+                if ((x[j] > y) == (first == up)) x[j] = y;
+            }
+        }
+        if ((x[0] > x[1]) == up) {
+            const uint64_t y = x[0];
+            x[0] = x[1];
+            x[1] = y;
         }
     }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (2 * tid + j < n) v[2 * tid + j] = x[j];
     __syncthreads();
 }
 
@@ -250,7 +287,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 0x1p-100f));
         sh.c = static_cast<float>(c);
         sh.c_low = static_cast<float>(c - static_cast<double>(sh.c));
-        if (min_p > 0.0f && min_p < 1.0f) sh.min_below = static_cast<double>(temperature) * log(static_cast<double>(min_p));
+        if (min_p > 0.0f && min_p < 1.0f) {
+            const double below = static_cast<double>(temperature) * log(static_cast<double>(min_p));
+            sh.min_below = static_cast<float>(below);
+            sh.min_below_low = static_cast<float>(below - static_cast<double>(sh.min_below));
+        }
         sh.listed = 0;
     }
     if (tid < 256) {  // the table
@@ -261,10 +302,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         sh.table[tid] = (v + (1ull << (62 - kOne))) >> (63 - kOne);
     }
     auto at = [&](int i) { return E::at(logits, i); };
-    // f(x, i) for the logits i of [begin, end) from `lowest` on, by `threads` threads of which this is
-    // `t`; begin and end are multiples of 8 (past the row's end lies -infinity)
-    auto each = [&](int begin, int end, int t, int threads, float lowest, auto f) {
-        for (int i = begin + t * E::kPer; i < end; i += threads * E::kPer) {
+    // A warp has a run of the CTA's logits. f(x, i) for those of [begin, end) from `lowest` on,
+    // by a warp; begin and end are multiples of 8 (past the row's end lies -infinity).
+    const int padded = (n + 7) / 8 * 8, length = ((padded + kWarps - 1) / kWarps + 7) / 8 * 8;
+    const int run_begin = min(padded, warp * length), run_end = min(padded, run_begin + length);
+    float run_top = -INFINITY;  // its largest
+    auto each = [&](int begin, int end, float lowest, auto f) {
+        for (int i = begin + lane * E::kPer; i < end; i += 32 * E::kPer) {
             const uint4 w = *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
             if (!(largest<kElem>(w) >= lowest)) continue;
 #pragma unroll
@@ -283,48 +327,50 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         turn ^= 1;
     };
     auto given_by = [&](int r) -> const Exchange& { return sh.exchange[turn ^ 1][r]; };
-    // v of the first warp, joined over the CTA
-    auto in_first_warp = [&](uint64_t v) {
+    auto each_of_run = [&](float lowest, auto f) {
+        if (run_top >= lowest) each(run_begin, run_end, lowest, f);
+    };
+    // the warps' v, a lane of each warp
+    auto of_warps = [&](uint64_t v) {
         if (lane == 0) sh.warp[warp] = v;
         __syncthreads();
         return sh.warp[lane % kWarps];
     };
 
     // The logits come to shared memory, and the largest of them and the range are found on the way.
-    const int padded = (n + 7) / 8 * 8;
     float top = -INFINITY, least = INFINITY;
     {
         const uint8_t* from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
-        const int vec = a.wide ? n / E::kPer : 0;
+        const int vec = a.wide ? min(n, run_end) / E::kPer : 0;  // past the run's last whole 16 bytes
         const bool ranged = use_k || use_p;
         auto low = [&](float x) {
             if (x > -INFINITY) least = fminf(least, x);
         };
-        constexpr int kAtOnce = 4;
-        for (int i0 = tid; i0 < vec; i0 += kAtOnce * kThreads) {
+        constexpr int kAtOnce = 8;
+        for (int i0 = run_begin / E::kPer + lane; i0 < vec; i0 += kAtOnce * 32) {
             uint4 v[kAtOnce];
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j)
-                if (i0 + j * kThreads < vec) v[j] = reinterpret_cast<const uint4*>(from)[i0 + j * kThreads];
+                if (i0 + j * 32 < vec) v[j] = reinterpret_cast<const uint4*>(from)[i0 + j * 32];
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j)
-                if (i0 + j * kThreads < vec) {
-                    reinterpret_cast<uint4*>(logits)[i0 + j * kThreads] = v[j];
-                    top = max_or_nan(top, largest<kElem>(v[j]));
+                if (i0 + j * 32 < vec) {
+                    reinterpret_cast<uint4*>(logits)[i0 + j * 32] = v[j];
+                    run_top = max_or_nan(run_top, largest<kElem>(v[j]));
                     if (ranged)
 #pragma unroll
                         for (int q = 0; q < E::kPer; ++q) low(E::at(&v[j], q));
                 }
         }
-        for (int i = vec * E::kPer + tid; i < padded; i += kThreads) {
+        for (int i = max(run_begin, vec * E::kPer) + lane; i < run_end; i += 32) {
             const float x = i < n ? E::at(from, i) : -INFINITY;
-            top = max_or_nan(top, x);
+            run_top = max_or_nan(run_top, x);
             if (ranged) low(x);
             E::put(logits, i, x);
         }
-        top = warp_reduce(top, max_or_nan);
+        top = run_top = warp_reduce(run_top, max_or_nan);
         least = warp_reduce(least, fminf);
-        const uint64_t both = in_first_warp(static_cast<uint64_t>(__float_as_uint(top)) << 32 | __float_as_uint(least));
+        const uint64_t both = of_warps(static_cast<uint64_t>(__float_as_uint(top)) << 32 | __float_as_uint(least));
         top = __uint_as_float(static_cast<uint32_t>(both >> 32));
         least = __uint_as_float(static_cast<uint32_t>(both));
         if (warp == 0) {
@@ -341,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     const bool none = !(fabsf(top) < INFINITY);
     if (none || greedy) {
         int mine = 0x7fffffff;
-        if (!none) each(0, padded, tid, kThreads, top, [&](float, int i) { mine = min(mine, first + i); });
+        if (!none) each_of_run(top, [&](float, int i) { mine = min(mine, first + i); });
         mine = __reduce_min_sync(~0u, static_cast<uint32_t>(mine));
-        mine = static_cast<int>(in_first_warp(static_cast<uint64_t>(mine)));
+        mine = static_cast<int>(of_warps(static_cast<uint64_t>(mine)));
         if (warp == 0) mine = __reduce_min_sync(~0u, static_cast<uint32_t>(mine));
         give([&](Exchange* e) { e->first = mine; });
         if (rank == 0 && tid == 0) {
@@ -368,8 +414,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     };
     // w >= min_p as a smallest logit: max + temperature ln(min_p), and the largest always
     float least_kept = -INFINITY;
-    if (min_p > 0.0f)
-        least_kept = min_p < 1.0f ? fminf(top, __double2float_ru(static_cast<double>(top) + sh.min_below)) : top;
+    if (min_p > 0.0f) {
+        least_kept = top;
+        if (min_p < 1.0f) {
+            const float y = sh.min_below, sum = top + y, z = sum - top;
+            const float rest = ((top - (sum - z)) + (y - z)) + sh.min_below_low;  // of the sum in full
+            const float up = rest > 0.0f ? value_of(key_of(sum) + 1) : sum;     // rounded up
+            least_kept = fminf(top, up);
+        }
+    }
     auto item = [&](float x, int i) { return static_cast<uint64_t>(~key_of(x)) << 32 | static_cast<uint32_t>(first + i); };
     auto logit_of = [&](uint64_t it) { return value_of(~static_cast<uint32_t>(it >> 32)); };
     // Sums of two values a thread, in the threads' order: what lies before them, and all.
@@ -404,10 +457,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         int shift = 0;
         uint64_t before = 0;
         for (int level = 0;; ++level) {
-            uint64_t* mass = sh.mass[which];
-            uint32_t* count = sh.count[which];
-            mass[tid] = 0;
-            count[tid] = 0;
+            Bins& bins = sh.bins[which];
+            bins.count[tid] = bins.part[0][tid] = bins.part[1][tid] = bins.part[2][tid] = 0;
             __syncthreads();
             auto place = [&](float x) {  // -1: not in question
                 if (level >= 2) {
@@ -418,22 +469,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                 if (level == 0) return b;
                 return b != static_cast<int>(base) ? -1 : min(kBins - 1, static_cast<int>((bin_of(x) - base) * kBins));
             };
-            each(0, padded, tid, kThreads, floor, [&](float x, int) {
+            each_of_run(floor, [&](float x, int) {
                 const int b = place(x);
                 if (b < 0) return;
                 if constexpr (kWeigh) {
                     const uint64_t m = w.of(x);
                     if (m == 0) return;
-                    atomicAdd(reinterpret_cast<unsigned long long*>(mass + b), static_cast<unsigned long long>(m));
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) atomicAdd(&bins.part[j][b], static_cast<uint32_t>(m >> kPart * j) & (1u << kPart) - 1);
                 }
-                atomicAdd(count + b, 1u);
+                atomicAdd(&bins.count[b], 1u);
             });
             cluster.sync();
             uint64_t v = 0;
             uint32_t c = 0;
-            for (int r = 0; r < ctas; ++r) {
-                c += cluster.map_shared_rank(count, r)[tid];
-                if constexpr (kWeigh) v += cluster.map_shared_rank(mass, r)[tid];
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) {
+                if (r >= ctas) break;
+                const Bins& theirs = *cluster.map_shared_rank(&bins, r);
+                c += theirs.count[tid];
+                if constexpr (kWeigh)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) v += static_cast<uint64_t>(theirs.part[j][tid]) << kPart * j;
             }
             if constexpr (!kWeigh) v = c;
             which ^= 1;
@@ -471,7 +528,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             if (all || members <= kFew) {
                 uint64_t* list = cluster.map_shared_rank(sh.list, 0);
                 uint32_t* listed = cluster.map_shared_rank(&sh.listed, 0);
-                each(0, padded, tid, kThreads, floor, [&](float x, int i) {
+                // nothing below the bin's end, with room for roundings, can be in it
+                float end = floor;
+                if (level == 0) end = fmaxf(floor, top - (static_cast<float>(bin + 1) / scale) * 1.00001f - fabsf(top) * 1e-6f);
+                if (level == 0 && bin == kBins - 1) end = floor;
+                each_of_run(end, [&](float x, int i) {
                     const int b = place(x);
                     if (b != bin && !(all && b < bin && b >= 0)) return;
                     if (kWeigh && w.of(x) == 0) return;  // not counted either
@@ -531,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             }
             if (level == 1) {  // the keys that the bin holds
                 uint32_t small = ~0u, large = 0;
-                each(0, padded, tid, kThreads, floor, [&](float x, int) {
+                each_of_run(floor, [&](float x, int) {
                     if (place(x) != bin) return;
                     small = min(small, key_of(x));
                     large = max(large, key_of(x));
                 });
                 small = __reduce_min_sync(~0u, small);
                 large = __reduce_max_sync(~0u, large);
-                const uint64_t both = in_first_warp(static_cast<uint64_t>(small) << 32 | large);
+                const uint64_t both = of_warps(static_cast<uint64_t>(small) << 32 | large);
                 small = static_cast<uint32_t>(both >> 32);
                 large = static_cast<uint32_t>(both);
                 if (warp == 0) {
@@ -629,21 +690,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     if (least_kept > cut.at) cut = Cut{-INFINITY, 0, 0};
     // The kept weight, by warps, each of which has a run of the CTA's logits, and over the cluster.
     const float lowest = fmaxf(fmaxf(cut.at, least_kept), kLowest);
-    auto weigh = [&](int begin, int end, int t, int threads, uint64_t& mass, uint32_t& ties) {
+    auto weigh = [&](int begin, int end, uint64_t& mass, uint32_t& ties) {
         mass = 0;
         ties = 0;
-        each(begin, end, t, threads, lowest, [&](float x, int) {
+        each(begin, end, lowest, [&](float x, int) {
             if (cut.ties && x == cut.at) ++ties;
             else mass += w.of(x);
         });
         mass = warp_reduce(mass, add<uint64_t>);
         ties = __reduce_add_sync(~0u, ties);
     };
-    const int length = ((padded + kWarps - 1) / kWarps + 7) / 8 * 8;
     const uint64_t tie = cut.ties ? w.of(cut.at) : 0;
-    uint64_t mass;
-    uint32_t ties;
-    weigh(min(padded, warp * length), min(padded, (warp + 1) * length), lane, 32, mass, ties);
+    uint64_t mass = 0;
+    uint32_t ties = 0;
+    if (run_top >= lowest) weigh(run_begin, run_end, mass, ties);
     // What precedes, of this lane's value in its warp: (mass, ties) in the vocabulary's order, of which only the
     // first `left` ties count.
     struct Before {
@@ -685,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     b = line_up(lane < kWarps ? sh.warp[lane] : 0, lane < kWarps ? sh.warp2[lane] : 0, b.start, b.left);
     const int run = pick(b, goal), begin = run * length, end = min(padded, begin + length);
     const int sub = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
-    weigh(min(end, begin + warp * sub), min(end, begin + (warp + 1) * sub), lane, 32, mass, ties);
+    weigh(min(end, begin + warp * sub), min(end, begin + (warp + 1) * sub), mass, ties);
     __syncthreads();
     if (lane == 0) {
         sh.warp[warp] = mass;
