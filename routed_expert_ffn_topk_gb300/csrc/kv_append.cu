@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "estream_internal.h"
 #include "overlap.cuh"
@@ -32,7 +33,9 @@ struct Append {
     long long table_row;
     float k_inv, v_inv;  // 1 / scale
     int T, B, M, num_pages, Hq, heads, dim, rot, interleaved;
-    FastDiv page, per_head, per_v;  // page_size; units of a rotated and of a value head
+    int per_head, per_v;  // units of a rotated and of a value head
+    int parts;            // log2 of the warps that share a token's heads
+    FastDiv page;
 };
 
 template <bool kF16>
@@ -134,135 +137,187 @@ __device__ __forceinline__ float2 cos_sin(uint32_t turn) {
     return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// How a thread's unit of work lies in a row: one pair or value; eight pairs whose
+// How a lane's unit of work lies in a row: one pair or value; eight pairs whose
 // halves are rot / 2 apart (or eight values that are not rotated); eight values
 // that hold four neighbouring pairs.
 enum Mode { kSingles, kHalves, kNeighbours };
 
-// A block takes a token at a time: its threads form the angles of the pairs once
-// for all heads, then go over the heads' units.
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Bound by HBM for many tokens and by latency for few. A warp has a token, or where tokens
+// are few a part of its heads: it forms the token's sines and cosines, one pair a lane,
+// and goes over the heads, several steps' values under way; a lane has
+// the same unit of every head it comes to, so sines, cosines and strides stay in
+// registers. Nothing waits for another warp. A block a token, with a division and sines
+// from shared memory for every unit, took 169 instructions a unit and 24 us for 4096 tokens of
+// 16 + 32 heads of 128.
 template <Mode kMode, bool kF16, bool kE4m3>
-__global__ void __launch_bounds__(512) k_kv_append(const Append a) {
-    __shared__ float2 turn[2][kKvMaxDim / 2];  // cos, sin; of this token and the one after it
+__global__ void __launch_bounds__(kThreads, kMode == kHalves ? 3 : 4) k_kv_append(const Append a) {
+    constexpr int kPairs = kMode == kSingles ? 1 : kMode == kHalves ? 8 : 4;  // of a unit
+    constexpr int kBytes = kE4m3 ? 1 : 2;                                     // of a cache element
+    constexpr int kAtOnce = kMode == kHalves ? 2 : 4;                         // heads whose values a lane has under way
+    using Raw = std::conditional_t<kMode == kSingles, uint16_t, uint4>;
+    __shared__ __align__(16) float2 turn[kWarps][kKvMaxDim / 2];  // cos, sin
     after_previous();
-    const int tid = threadIdx.x, pairs = a.rot / 2;
-    uint64_t per_position = 0;  // turns, 64 fractional bits
-    if (tid < pairs) {
-        double f = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189533577;
-        f -= floor(f);
-        per_position = static_cast<uint64_t>(f * 18446744073709551616.0);
-    }
-    const int rotated = (a.heads + a.Hq) * static_cast<int>(a.per_head.d), units = rotated + a.heads * static_cast<int>(a.per_v.d);
-    int now = 0;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const int pos = a.positions[t], row = a.rows ? a.rows[t] : t;
-        if (pos < 0) continue;  // padding: the whole block
-        if (tid < pairs) {
-            const uint64_t angle = per_position * static_cast<uint64_t>(pos);
-            turn[now][tid] = cos_sin(static_cast<uint32_t>((angle + 0x80000000u) >> 32));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int item = blockIdx.x * kWarps + warp, t = item >> a.parts, part = item & ((1 << a.parts) - 1);
+    if (t >= a.T) return;
+    const int pos = a.positions[t], row = a.rows ? a.rows[t] : t, pairs = a.rot / 2;
+    if (pos < 0) return;  // padding
+    const int entry = static_cast<int>(a.page.div(pos)), slot = pos - entry * static_cast<int>(a.page.d);
+    int page = -1;
+    if (row >= 0 && row < a.B && entry < a.M) page = a.table[row * a.table_row + entry];
+    const bool ok = page >= 0 && page < a.num_pages;
+    bool formed = false;
+    auto form_angles = [&] {  // once the first values are under way
+        if (formed) return;
+        formed = true;
+        for (int p = lane; p < pairs; p += 32) {
+            // turns a position, 64 fractional bits
+            double f = static_cast<double>(a.inv_freq[p]) * 0.15915494309189533577;
+            f -= floor(f);
+            const uint64_t angle = static_cast<uint64_t>(f * 18446744073709551616.0) * static_cast<uint64_t>(pos);
+            turn[warp][p] = cos_sin(static_cast<uint32_t>((angle + 0x80000000u) >> 32));
         }
-        const int entry = static_cast<int>(a.page.div(pos)), slot = pos - entry * static_cast<int>(a.page.d);
-        int page = -1;
-        if (row >= 0 && row < a.B && entry < a.M) page = a.table[row * a.table_row + entry];
-        const bool ok = page >= 0 && page < a.num_pages;
-        const long long kat = page * a.kc_page + slot * a.kc_token, vat = page * a.vc_page + slot * a.vc_token;
-        __syncthreads();  // this buffer is next written behind the next token's barrier, past all its readers
-        for (int u = tid; u < units; u += blockDim.x) {
-            if (u >= rotated) {
-                if (!ok) break;
-                const int h = static_cast<int>(a.per_v.div(u - rotated)), j = u - rotated - h * static_cast<int>(a.per_v.d);
-                const uint16_t* from = static_cast<const uint16_t*>(a.v) + t * a.v_token + h * a.v_head;
-                if constexpr (kMode == kSingles)
-                    keep1<kF16, kE4m3>(a.vc, vat + h * a.vc_head + j, up1<kF16>(from[j]), a.v_inv);
-                else
-                    keep8<kF16, kE4m3>(a.vc, vat + h * a.vc_head + 8 * j,
-                                       widen<kF16>(*reinterpret_cast<const uint4*>(from + 8 * j)), a.v_inv);
-                continue;
-            }
-            const int h = static_cast<int>(a.per_head.div(u)), j = u - h * static_cast<int>(a.per_head.d);
-            const bool key = h < a.heads;
-            const int hq = h - a.heads;
-            if (key && !ok) continue;
-            const uint16_t* from = key ? static_cast<const uint16_t*>(a.k) + t * a.k_token + h * a.k_head
-                                       : static_cast<const uint16_t*>(a.q) + t * a.q_token + hq * a.q_head;
-            uint16_t* to = key ? nullptr : static_cast<uint16_t*>(a.q_out) + t * a.qo_token + hq * a.qo_head;
-            const long long kto = kat + h * a.kc_head;
-            const float nan = __int_as_float(0x7fc00000);
+        __syncwarp();
+    };
+    int steps = 0;  // of the kinds of heads before; the parts of a token take turns at all of them
+    const float nan = __int_as_float(0x7fc00000);
+    // The heads of one kind: from `from` (of this token), heads from_head elements apart, to `to`,
+    // to_head bytes apart; into the cache, or as queries.
+    auto go = [&](auto rotated, auto cached, int heads, int per_head, const void* from, long long from_head, void* to,
+                  long long to_head, float inv) {
+        constexpr bool kRotated = decltype(rotated)::value, kCached = decltype(cached)::value;
+        const int together = per_head < 32 ? 32 / per_head : 1;  // heads of a step
+        const int parts = 1 << a.parts, mine = part - steps & parts - 1;  // this warp's first step
+        steps += (heads + together - 1) / together;
+        for (int j0 = 0; j0 < per_head; j0 += 32) {
+            if (mine * together >= heads) break;
+            const int sub = per_head < 32 ? lane / per_head : 0, j = per_head < 32 ? lane - sub * per_head : j0 + lane;
+            const bool active = sub < together && j < per_head;
+            const bool turns = kRotated && active && j * kPairs < pairs;
+            int d0, d1;  // where the unit's values lie
             if constexpr (kMode == kSingles) {
-                auto put = [&](int d, float x) {
-                    if (key) keep1<kF16, kE4m3>(a.kc, kto + d, x, a.k_inv);
-                    else to[d] = down1<kF16>(ok ? x : nan);
-                };
-                if (j < pairs) {
-                    const int d0 = a.interleaved ? 2 * j : j, d1 = a.interleaved ? d0 + 1 : j + pairs;
-                    const float x = up1<kF16>(from[d0]), y = up1<kF16>(from[d1]);
-                    const float2 cs = turn[now][j];
-                    put(d0, x * cs.x - y * cs.y);
-                    put(d1, y * cs.x + x * cs.y);
-                } else {
-                    const int d = j + pairs;
-                    put(d, up1<kF16>(from[d]));
-                }
+                d0 = !kRotated ? j : !turns ? j + pairs : a.interleaved ? 2 * j : j;
+                d1 = !turns ? d0 : a.interleaved ? d0 + 1 : j + pairs;
+            } else if constexpr (kMode == kHalves && kRotated) {
+                d0 = turns ? 8 * j : 8 * j + pairs;
+                d1 = turns ? 8 * j + pairs : d0;
             } else {
-                auto put = [&](int d, Eight& e) {
-                    if (key) {
-                        keep8<kF16, kE4m3>(a.kc, kto + d, e, a.k_inv);
-                        return;
+                d0 = d1 = 8 * j;
+            }
+            float2 cs[kPairs];
+            const int first = active ? mine * together + sub : heads, step = together << a.parts;
+            const uint16_t* f = static_cast<const uint16_t*>(from) + first * from_head;
+            uint8_t* o = static_cast<uint8_t*>(to) + first * to_head;
+            const long long f_step = step * from_head, o_step = step * to_head;
+            constexpr bool kTwo = kMode != kNeighbours && kRotated;
+            bool begun = false;
+            for (int h = first; h < heads || !begun; h += kAtOnce * step) {  // at least once, for the angles
+                Raw raw[kAtOnce][kTwo ? 2 : 1];
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q)
+                    if (h + q * step < heads) {
+                        raw[q][0] = *reinterpret_cast<const Raw*>(f + d0);
+                        if constexpr (kTwo) raw[q][1] = *reinterpret_cast<const Raw*>(f + d1);
+                        f += f_step;
                     }
-                    if (!ok)
+                if (!begun) {
+                    begun = true;
+                    if constexpr (kRotated) form_angles();
+                    if (turns) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) e.x[i] = nan;
-                    store16<kF16>(to + d, e);
-                };
-                if constexpr (kMode == kHalves) {
-                    if (8 * j < pairs) {
-                        Eight x = widen<kF16>(*reinterpret_cast<const uint4*>(from + 8 * j));
-                        Eight y = widen<kF16>(*reinterpret_cast<const uint4*>(from + pairs + 8 * j));
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 cs = turn[now][8 * j + i];
-                            const float lo = x.x[i] * cs.x - y.x[i] * cs.y;
-                            y.x[i] = y.x[i] * cs.x + x.x[i] * cs.y;
-                            x.x[i] = lo;
+                        for (int q = 0; q < kPairs; ++q) {
+                            cs[q] = make_float2(1.0f, 0.0f);
+                            if (j * kPairs + q < pairs) cs[q] = turn[warp][j * kPairs + q];
                         }
-                        put(8 * j, x);
-                        put(pairs + 8 * j, y);
+                    }
+                    if (kCached && !ok) return;
+                }
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    if (h + q * step >= heads) break;
+                    if constexpr (kMode == kSingles) {
+                        float x = up1<kF16>(raw[q][0]), y = 0.0f;
+                        if (turns) {
+                            y = up1<kF16>(raw[q][kTwo ? 1 : 0]);
+                            const float lo = x * cs[0].x - y * cs[0].y;
+                            y = y * cs[0].x + x * cs[0].y;
+                            x = lo;
+                        }
+                        if (!kCached && !ok) x = y = nan;
+                        if constexpr (kCached) {
+                            keep1<kF16, kE4m3>(o, d0, x, inv);
+                            if (turns) keep1<kF16, kE4m3>(o, d1, y, inv);
+                        } else {
+                            reinterpret_cast<uint16_t*>(o)[d0] = down1<kF16>(x);
+                            if (turns) reinterpret_cast<uint16_t*>(o)[d1] = down1<kF16>(y);
+                        }
+                    } else if (kRotated || (kCached && kE4m3)) {
+                        Eight x = widen<kF16>(raw[q][0]), y;
+                        if (turns) {
+                            if constexpr (kTwo) {
+                                y = widen<kF16>(raw[q][1]);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float2 c = cs[e % kPairs];
+                                    const float lo = x.x[e] * c.x - y.x[e] * c.y;
+                                    y.x[e] = y.x[e] * c.x + x.x[e] * c.y;
+                                    x.x[e] = lo;
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 c = cs[e % kPairs];
+                                    const float lo = x.x[2 * e] * c.x - x.x[2 * e + 1] * c.y;
+                                    x.x[2 * e + 1] = x.x[2 * e + 1] * c.x + x.x[2 * e] * c.y;
+                                    x.x[2 * e] = lo;
+                                }
+                            }
+                        }
+                        if (!kCached && !ok)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x.x[e] = y.x[e] = nan;
+                        if constexpr (kCached) {
+                            keep8<kF16, kE4m3>(o, d0, x, inv);
+                            if constexpr (kTwo)
+                                if (turns) keep8<kF16, kE4m3>(o, d1, y, inv);
+                        } else {
+                            store16<kF16>(o + 2 * d0, x);
+                            if constexpr (kTwo)
+                                if (turns) store16<kF16>(o + 2 * d1, y);
+                        }
                     } else {
-                        const int d = 8 * j + pairs;
-                        Eight x = widen<kF16>(*reinterpret_cast<const uint4*>(from + d));
-                        put(d, x);
+                        *reinterpret_cast<Raw*>(o + 2 * d0) = raw[q][0];  // as it is
                     }
-                } else {
-                    Eight x = widen<kF16>(*reinterpret_cast<const uint4*>(from + 8 * j));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = 4 * j + i;
-                        if (p < pairs) {
-                            const float2 cs = turn[now][p];
-                            const float lo = x.x[2 * i] * cs.x - x.x[2 * i + 1] * cs.y;
-                            x.x[2 * i + 1] = x.x[2 * i + 1] * cs.x + x.x[2 * i] * cs.y;
-                            x.x[2 * i] = lo;
-                        }
-                    }
-                    put(8 * j, x);
+                    o += o_step;
                 }
             }
         }
-        now ^= 1;
-    }
+    };
+    using yes = std::true_type;
+    using no = std::false_type;
+    if (a.Hq)
+        go(yes{}, no{}, a.Hq, a.per_head, static_cast<const uint16_t*>(a.q) + t * a.q_token, a.q_head,
+           static_cast<uint16_t*>(a.q_out) + t * a.qo_token, 2 * a.qo_head, 1.0f);
+    go(yes{}, yes{}, a.heads, a.per_head, static_cast<const uint16_t*>(a.k) + t * a.k_token, a.k_head,
+       static_cast<uint8_t*>(a.kc) + (page * a.kc_page + slot * a.kc_token) * kBytes, kBytes * a.kc_head, a.k_inv);
+    go(no{}, yes{}, a.heads, a.per_v, static_cast<const uint16_t*>(a.v) + t * a.v_token, a.v_head,
+       static_cast<uint8_t*>(a.vc) + (page * a.vc_page + slot * a.vc_token) * kBytes, kBytes * a.vc_head, a.v_inv);
 }
 
 template <Mode kMode, bool kF16>
-cudaError_t launch(const Append& a, bool e4m3, int grid, int threads, cudaStream_t stream) {
-    return e4m3 ? launch_overlapped(k_kv_append<kMode, kF16, true>, dim3(grid), threads, 0, stream, a)
-                : launch_overlapped(k_kv_append<kMode, kF16, false>, dim3(grid), threads, 0, stream, a);
+cudaError_t launch(const Append& a, bool e4m3, int grid, cudaStream_t stream) {
+    return e4m3 ? launch_overlapped(k_kv_append<kMode, kF16, true>, dim3(grid), kThreads, 0, stream, a)
+                : launch_overlapped(k_kv_append<kMode, kF16, false>, dim3(grid), kThreads, 0, stream, a);
 }
 template <bool kF16>
-cudaError_t launch(const Append& a, Mode mode, bool e4m3, int grid, int threads, cudaStream_t stream) {
+cudaError_t launch(const Append& a, Mode mode, bool e4m3, int grid, cudaStream_t stream) {
     switch (mode) {
-        case kSingles: return launch<kSingles, kF16>(a, e4m3, grid, threads, stream);
-        case kHalves: return launch<kHalves, kF16>(a, e4m3, grid, threads, stream);
-        default: return launch<kNeighbours, kF16>(a, e4m3, grid, threads, stream);
+        case kSingles: return launch<kSingles, kF16>(a, e4m3, grid, stream);
+        case kHalves: return launch<kHalves, kF16>(a, e4m3, grid, stream);
+        default: return launch<kNeighbours, kF16>(a, e4m3, grid, stream);
     }
 }
 
@@ -316,16 +371,17 @@ extern "C" estream_status estream_kv_append(const estream_kv_cache* c, int elem,
     const int dim = c->dim;
     const int per_head = mode == kSingles ? dim - rot / 2 : mode == kHalves ? rot / 16 + (dim - rot) / 8 : dim / 8;
     const int per_v = mode == kSingles ? dim : dim / 8;
+    // warps for a token: one while tokens alone fill the device (152 SMs of 32 warps), at most 32
+    int parts = 0;
+    while (parts < 5 && (static_cast<long long>(T) << parts) < 152 * 32) ++parts;
     const Append a{k, v, q, q_out, c->k, c->v, k_token, k_head, v_token, v_head, q_token, q_head, qo_token, qo_head,
                    c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head, positions, rows, table,
                    inv_freq, table_row, 1.0f / c->k_scale, 1.0f / c->v_scale, T, entries ? B : 0, M, c->num_pages, Hq,
-                   c->heads, dim, rot, interleaved != 0, FastDiv(c->page_size), FastDiv(per_head), FastDiv(per_v)};
-    const int units = (c->heads + Hq) * per_head + c->heads * per_v;
-    const int threads = std::min(512, std::max(128, (units + 31) / 32 * 32));
-    const int grid = std::min(T, 1216);
+                   c->heads, dim, rot, interleaved != 0, per_head, per_v, parts, FastDiv(c->page_size)};
+    const int grid = static_cast<int>(((static_cast<long long>(T) << parts) + kWarps - 1) / kWarps);
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     const bool e4m3 = c->elem == ESTREAM_KV_E4M3;
-    const cudaError_t rc = elem == ESTREAM_KV_F16 ? launch<true>(a, mode, e4m3, grid, threads, stream)
-                                                  : launch<false>(a, mode, e4m3, grid, threads, stream);
+    const cudaError_t rc = elem == ESTREAM_KV_F16 ? launch<true>(a, mode, e4m3, grid, stream)
+                                                  : launch<false>(a, mode, e4m3, grid, stream);
     return rc == cudaSuccess ? ESTREAM_OK : ESTREAM_ERR_CUDA;
 }
