@@ -8,8 +8,8 @@
 // bits are taken: a quarter turn and a rest of at most pi / 4, whose sine and cosine
 // are Taylor series with the leading terms in two floats each, right to about 0.6 of
 // fp32's half step (sincospi of the fraction as one float is off by four times that,
-// which an 8-bit cache's rounding borders show). The angle's error is 2^-53 position
-// inv_freq / 2 pi (double's, of the quotient) + 2^-33 turns.
+// which an 8-bit cache's rounding borders show). The angle's error is 2^-64 position
+// (2^-53 position inv_freq / 2 pi from an inv_freq of 2 on) + 2^-33 turns.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -108,6 +108,26 @@ __device__ __forceinline__ void keep1(void* base, long long at, float x, float i
     else static_cast<uint16_t*>(base)[at] = down1<kF16>(x);
 }
 
+// f / 2 pi turns, 64 fractional bits, rounded down. In integers below 2: with double's
+// operations, of which an SM does two a clock, 4096 tokens took 5 us longer.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    const uint32_t u = __float_as_uint(f), e = u >> 23 & 0xff;
+    uint64_t w;
+    if (e < 128) {
+        // f = m 2^(max(e, 1) - 150); 2^88 / 2 pi in two words
+        constexpr uint64_t kHigh = 0x28be60, kLow = 0xdb9391054a7f09d6ull;
+        const uint64_t m = (u & 0x7fffff) | (e ? 0x800000u : 0u);
+        const uint64_t low = m * kLow, high = m * kHigh + __umul64hi(m, kLow);
+        const uint32_t s = 174 - max(e, 1u);  // 47 for the largest
+        w = s < 64 ? high << (64 - s) | low >> s : s < 128 ? high >> (s - 64) : 0;
+    } else {
+        double turns = static_cast<double>(fabsf(f)) * 0.15915494309189533577;
+        turns -= floor(turns);
+        w = static_cast<uint64_t>(turns * 18446744073709551616.0);
+    }
+    return u >> 31 ? ~w + 1 : w;
+}
+
 // cos, sin of a fraction of a turn, 32 bits.
 __device__ __forceinline__ float2 cos_sin(uint32_t turn) {
     const uint32_t quarter = (turn + 0x20000000u) >> 30;
@@ -174,10 +194,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kHalves ? 3 : 4) k_kv_appen
         if (formed) return;
         formed = true;
         for (int p = lane; p < pairs; p += 32) {
-            // turns a position, 64 fractional bits
-            double f = static_cast<double>(a.inv_freq[p]) * 0.15915494309189533577;
-            f -= floor(f);
-            const uint64_t angle = static_cast<uint64_t>(f * 18446744073709551616.0) * static_cast<uint64_t>(pos);
+            const uint64_t angle = turns_of(a.inv_freq[p]) * static_cast<uint64_t>(pos);
             turn[warp][p] = cos_sin(static_cast<uint32_t>((angle + 0x80000000u) >> 32));
         }
         __syncwarp();
@@ -371,9 +388,9 @@ extern "C" estream_status estream_kv_append(const estream_kv_cache* c, int elem,
     const int dim = c->dim;
     const int per_head = mode == kSingles ? dim - rot / 2 : mode == kHalves ? rot / 16 + (dim - rot) / 8 : dim / 8;
     const int per_v = mode == kSingles ? dim : dim / 8;
-    // warps for a token: one while tokens alone fill the device (152 SMs of 32 warps), at most 32
+    // warps for a token: one while tokens alone fill the device (152 SMs of 32 warps), at most 16
     int parts = 0;
-    while (parts < 5 && (static_cast<long long>(T) << parts) < 152 * 32) ++parts;
+    while (parts < 4 && (static_cast<long long>(T) << parts) < 152 * 32) ++parts;
     const Append a{k, v, q, q_out, c->k, c->v, k_token, k_head, v_token, v_head, q_token, q_head, qo_token, qo_head,
                    c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head, positions, rows, table,
                    inv_freq, table_row, 1.0f / c->k_scale, 1.0f / c->v_scale, T, entries ? B : 0, M, c->num_pages, Hq,
