@@ -16,7 +16,8 @@
 // the cut's bin, as after most prompts, they are gathered in one CTA, which sorts
 // them and does the rest alone. Else the bin with the cut is divided again until its tokens
 // can be sorted or are all equal, and the kept tokens are weighed and searched
-// where they are.
+// where they are. With top-p alone the bins are left out where the tokens of at least 2^-9 of the
+// largest weight are few and reach the target.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -89,17 +90,17 @@ __constant__ uint64_t kRoots[8] = {0x5a827999fcef3242ull, 0x6ba27e656b4eb57aull,
 // numbers come out of floats by adding 1.5 * 2^23, whose last bit is 1: conversions
 // go through a unit of a quarter of the rate.
 struct Weights {
-    float top, c, c_low;
-    const uint64_t* table;  // 2^(42 - i / 256)
-    // The weight is the result times 2^-s.
+    float top, c, c_low, past;  // past: a distance from the top at which weights are 0
+    const uint64_t* table;      // 2^(43 - i / 256)
+    // Twice the weight is the result times 2^-s. Without branches, so that several are on their way.
     __device__ __forceinline__ uint64_t parts(float l, int& s) const {
         constexpr float kRound = 12582912.0f;
         constexpr int kRoundBits = 0x4b400000;
-        s = 0;
-        const float d = top - l;
-        const float z = d - top, low = (top - (d - z)) - (l + z);  // what rounding took from d
+        const float full = top - l;
+        const bool near = full < past;
+        const float d = near ? full : past;
+        const float z = d - top, low = near ? (top - (d - z)) - (l + z) : 0.0f;  // what rounding took from d
         const float p = d * c;
-        if (!(p < kOne + 2.0f)) return 0;
         const float q = fmaf(d, c, -p) + fmaf(d, c_low, low * c);
         const float rounded = fmaf(p, 256.0f, kRound);
         const int k = __float_as_int(rounded) - kRoundBits;
@@ -111,18 +112,18 @@ struct Weights {
         const int change = __float_as_int(fmaf(tail, 0x1p39f, kRound)) - kRoundBits - __float2int_rn(xh * 0x1p39f);
         const uint64_t t = table[k & 255];
         s = k >> 8;
-        return t + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(t >> 12)) * change) >> 27);
+        return t + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(t >> 13)) * change) >> 26);
     }
     __device__ __forceinline__ uint64_t of(float l) const {
         int s;
         const uint64_t w = parts(l, s);
-        return ((w << 1 >> s) + 1) >> 1;
+        return ((w >> s) + 1) >> 1;
     }
     // A kept token's probability, from its weight before that became a whole number of units.
     __device__ __forceinline__ float share(float l, uint64_t whole) const {
         int s;
         const double w = static_cast<double>(parts(l, s));
-        return static_cast<float>(w / (static_cast<double>(1ull << s) * static_cast<double>(whole)));
+        return static_cast<float>(w / (static_cast<double>(2ull << s) * static_cast<double>(whole)));
     }
 };
 
@@ -184,8 +185,8 @@ struct Exchange {
     float top, least;  // its largest logit (NaN if it has one), and smallest finite one
     int first;         // its first largest logit's index
     uint32_t lo, hi;   // keys of a bin
-    uint32_t ties;
-    uint64_t mass;
+    uint32_t ties, listed;
+    uint64_t mass, heavy;
     Cut cut;
 };
 
@@ -198,24 +199,37 @@ struct Bins {
 };
 struct Shared {
     uint64_t table[256];
-    Bins bins[2];             // of this CTA, read by its cluster; used in turn
+    Bins bins;                // of this CTA, read by its cluster; else room for a list
+    uint64_t sum[kBins];      // all CTAs' bins, added up
+    uint32_t sum_count[kBins];
     uint64_t list[kFew];      // the leading CTA's: tokens to sort
     uint64_t warp[kWarps];
     uint32_t warp2[kWarps];
     uint64_t before;
     Cut cut;
-    uint32_t bin, members, upto, listed;
+    uint32_t bin, members, upto, listed, collected, listed_at;
     float min_below, min_below_low;  // temperature ln(min_p)
     float c, c_low;                  // log2 e / temperature
     Exchange exchange[2][kMaxCtas];  // used in turn
 };
 
-// Puts n <= kFew different values in ascending order. A few are counted: each value's
-// place is the number of smaller ones. More go through a bitonic network, two values a
-// thread; pairs that are less than 64 apart lie in one warp.
-__device__ __forceinline__ void sort(uint64_t* v, int n) {
-    const int tid = threadIdx.x;
-    if (n <= kFew / 4) {
+__device__ __forceinline__ uint32_t cta_min(uint32_t v, uint32_t* room) {  // room: kWarps values
+    v = __reduce_min_sync(~0u, v);
+    if (threadIdx.x % 32 == 0) room[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = __reduce_min_sync(~0u, room[threadIdx.x % kWarps]);
+    __syncthreads();
+    return v;
+}
+
+// Puts the list's n <= kFew different values in ascending order. Of a few, each value's place is
+// the number of smaller ones. More are first dealt into as many bins of equal width in the
+// upper word as there are threads, so that a value is compared with those of its bin alone.
+__device__ __forceinline__ void sort(Shared& sh, int n) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    uint64_t* v = sh.list;
+    __syncthreads();
+    if (n <= kFew / 8) {
         int size = 16;
         while (size < n) size *= 2;
         const int share = kThreads / size, i = tid / share, part = tid % share;  // threads of a value
@@ -229,37 +243,52 @@ __device__ __forceinline__ void sort(uint64_t* v, int n) {
         __syncthreads();
         return;
     }
-    int size = kFew / 2;
-    while (size < n) size *= 2;
+    static_assert(sizeof(Bins) >= kFew * sizeof(uint64_t), "a list fits the bins");
+    uint64_t* dealt = reinterpret_cast<uint64_t*>(&sh.bins);
+    uint32_t* count = sh.sum_count;
     uint64_t x[2];
+    uint32_t small = ~0u, small_not = ~0u;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) x[j] = 2 * tid + j < n ? v[2 * tid + j] : ~0ull;
-    for (int run = 2; run <= size; run *= 2) {
-        const bool up = (2 * tid & run) == 0;
-        for (int step = run / 2; step >= 2; step /= 2) {
-            const bool first = (2 * tid & step) == 0;
-            if (step >= 64) {
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < 2; ++j) v[2 * tid + j] = x[j];
-                __syncthreads();
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint64_t y = step >= 64 ? v[(2 * tid + j) ^ step] : __shfl_xor_sync(~0u, x[j], step / 2);
-                if ((x[j] > y) == (first == up)) x[j] = y;
-            }
+    for (int j = 0; j < 2; ++j)
+        if (tid + j * kThreads < n) {
+            x[j] = v[tid + j * kThreads];
+            small = min(small, static_cast<uint32_t>(x[j] >> 32));
+            small_not = min(small_not, ~static_cast<uint32_t>(x[j] >> 32));
         }
-        if ((x[0] > x[1]) == up) {
-            const uint64_t y = x[0];
-            x[0] = x[1];
-            x[1] = y;
+    count[tid] = 0;
+    small = cta_min(small, sh.warp2);
+    small_not = cta_min(small_not, sh.warp2);
+    int shift = 0;
+    while ((~small_not - small) >> shift >= kThreads) ++shift;
+    uint32_t at[2], bin[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (tid + j * kThreads < n) {
+            bin[j] = (static_cast<uint32_t>(x[j] >> 32) - small) >> shift;
+            at[j] = atomicAdd(&count[bin[j]], 1u);
         }
-    }
+    __syncthreads();
+    const uint32_t mine = count[tid], upto = warp_scan(mine, lane);
+    if (lane == 31) sh.warp2[warp] = upto;
+    __syncthreads();
+    uint32_t before = upto - mine;
+    for (int q = 0; q < warp; ++q) before += sh.warp2[q];
+    uint32_t* start = reinterpret_cast<uint32_t*>(sh.sum);  // [kThreads + 1]
+    start[tid] = before;
+    if (tid == 0) start[kThreads] = n;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        if (2 * tid + j < n) v[2 * tid + j] = x[j];
+        if (tid + j * kThreads < n) dealt[start[bin[j]] + at[j]] = x[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (tid + j * kThreads < n) {
+            const uint32_t from = start[bin[j]], to = start[bin[j] + 1];
+            uint32_t place = from;
+            for (uint32_t q = from; q < to; ++q) place += dealt[q] < x[j];
+            v[place] = x[j];
+        }
     __syncthreads();
 }
 
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (tid >> (7 - j) & 1) v = __umul64hi(v, kRoots[j] << 1);
-        sh.table[tid] = (v + (1ull << (62 - kOne))) >> (63 - kOne);
+        sh.table[tid] = (v + (1ull << (61 - kOne))) >> (62 - kOne);
     }
     auto at = [&](int i) { return E::at(logits, i); };
     // A warp has a run of the CTA's logits. f(x, i) for those of [begin, end) from `lowest` on,
@@ -315,6 +344,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             for (int j = 0; j < E::kPer; ++j) {
                 const float x = E::at(&w, j);
                 if (x >= lowest) f(x, i + j);
+            }
+        }
+    };
+    // f(x, i) for four logits from i on, where one of them is at or above `lowest`
+    auto each_four = [&](int begin, int end, float lowest, auto f) {
+        for (int i = begin + lane * E::kPer; i < end; i += 32 * E::kPer) {
+            const uint4 w = *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
+            if (!(largest<kElem>(w) >= lowest)) continue;
+#pragma unroll
+            for (int j = 0; j < E::kPer; j += 4) {
+                const float x[4] = {E::at(&w, j), E::at(&w, j + 1), E::at(&w, j + 2), E::at(&w, j + 3)};
+                f(x, i + j);
             }
         }
     };
@@ -400,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         return;
     }
 
-    const Weights w{top, sh.c, sh.c_low, sh.table};
+    const Weights w{top, sh.c, sh.c_low, (kOne + 3.0f) / sh.c, sh.table};
     const float u = a.u[row];
     // the first token whose cumulative weight exceeds this is drawn
     auto point = [&](uint64_t whole) {
@@ -443,10 +484,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     // at or above `floor`, then over those of the bin with the cut. The target is formed
     // from the whole measure; with may_list, tokens up to the first bin's end are
     // only listed where they are few.
-    int which = 0;
     uint64_t target = 0;
     constexpr float kLowest = -3.402823466e38f;  // what can be drawn is finite
     Cut cut{-INFINITY, 0, 0};  // everything
+    // This CTA's tokens that are wanted go where the bins are; room for kFew. sh.collected is 0 before.
+    uint64_t* const staged = reinterpret_cast<uint64_t*>(&sh.bins);
+    auto append = [&](bool wanted, float x, int i) {  // by the lanes that come here together
+        const uint32_t here = __activemask(), mask = __ballot_sync(here, wanted);
+        if (!mask) return;
+        uint32_t to = 0;
+        if (lane == __ffs(mask) - 1) to = atomicAdd(&sh.collected, static_cast<uint32_t>(__popc(mask)));
+        to = __shfl_sync(here, to, __ffs(mask) - 1) + __popc(mask & ((1u << lane) - 1));
+        if (wanted && to < kFew) staged[to] = item(x, i);
+    };
+    auto hand_over = [&](uint32_t at) {  // to the leading CTA's list
+        uint64_t* list = cluster.map_shared_rank(sh.list, 0);
+        for (uint32_t i = tid; i < sh.collected; i += kThreads) list[at + i] = staged[i];
+    };
     auto find = [&](auto weighs, float floor, auto aim, bool may_list) {
         constexpr bool kWeigh = decltype(weighs)::value;
         const float span = fminf(top - least, (kOne + 2.0f) / w.c);
@@ -457,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         int shift = 0;
         uint64_t before = 0;
         for (int level = 0;; ++level) {
-            Bins& bins = sh.bins[which];
+            Bins& bins = sh.bins;
             bins.count[tid] = bins.part[0][tid] = bins.part[1][tid] = bins.part[2][tid] = 0;
             __syncthreads();
             auto place = [&](float x) {  // -1: not in question
@@ -469,31 +523,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                 if (level == 0) return b;
                 return b != static_cast<int>(base) ? -1 : min(kBins - 1, static_cast<int>((bin_of(x) - base) * kBins));
             };
-            each_of_run(floor, [&](float x, int) {
-                const int b = place(x);
-                if (b < 0) return;
-                if constexpr (kWeigh) {
-                    const uint64_t m = w.of(x);
-                    if (m == 0) return;
+            if (run_top >= floor)
+                each_four(run_begin, run_end, floor, [&](const float (&x)[4], int) {
+                    int b[4];
+                    uint64_t m[4];
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) atomicAdd(&bins.part[j][b], static_cast<uint32_t>(m >> kPart * j) & (1u << kPart) - 1);
-                }
-                atomicAdd(&bins.count[b], 1u);
-            });
+                    for (int q = 0; q < 4; ++q) {
+                        b[q] = x[q] >= floor ? place(x[q]) : -1;
+                        m[q] = 1;
+                        if constexpr (kWeigh) m[q] = w.of(x[q]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (b[q] < 0 || m[q] == 0) continue;
+                        if constexpr (kWeigh)
+#pragma unroll
+                            for (int j = 0; j < 3; ++j)
+                                atomicAdd(&bins.part[j][b[q]], static_cast<uint32_t>(m[q] >> kPart * j) & (1u << kPart) - 1);
+                        atomicAdd(&bins.count[b[q]], 1u);
+                    }
+                });
             cluster.sync();
+            // A CTA adds up its share of the bins, a thread a bin of one of the CTAs, and stores the sums in all.
             uint64_t v = 0;
             uint32_t c = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) {
-                if (r >= ctas) break;
+            {
+                const int r = tid & (ctas - 1), b = rank * (kBins / ctas) + tid / ctas;
                 const Bins& theirs = *cluster.map_shared_rank(&bins, r);
-                c += theirs.count[tid];
+                c = theirs.count[b];
                 if constexpr (kWeigh)
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) v += static_cast<uint64_t>(theirs.part[j][tid]) << kPart * j;
+                    for (int j = 0; j < 3; ++j) v += static_cast<uint64_t>(theirs.part[j][b]) << kPart * j;
+                for (int o = 1; o < ctas; o *= 2) {
+                    c += __shfl_xor_sync(~0u, c, o);
+                    if constexpr (kWeigh) v += __shfl_xor_sync(~0u, v, o);
+                }
+                cluster.map_shared_rank(sh.sum_count, r)[b] = c;
+                if constexpr (kWeigh) cluster.map_shared_rank(sh.sum, r)[b] = v;
             }
-            if constexpr (!kWeigh) v = c;
-            which ^= 1;
+            cluster.sync();
+            c = sh.sum_count[tid];
+            v = kWeigh ? sh.sum[tid] : c;
             const uint64_t upto = warp_scan(v, lane);
             const uint32_t counted = warp_scan(c, lane);
             if (lane == 31) {
@@ -526,23 +596,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             const uint32_t members = sh.members;
             const bool all = may_list && level == 0 && sh.upto <= kFew;
             if (all || members <= kFew) {
-                uint64_t* list = cluster.map_shared_rank(sh.list, 0);
-                uint32_t* listed = cluster.map_shared_rank(&sh.listed, 0);
-                // nothing below the bin's end, with room for roundings, can be in it
-                float end = floor;
-                if (level == 0) end = fmaxf(floor, top - (static_cast<float>(bin + 1) / scale) * 1.00001f - fabsf(top) * 1e-6f);
-                if (level == 0 && bin == kBins - 1) end = floor;
-                each_of_run(end, [&](float x, int i) {
+                // nothing outside the bin's ends, with room for roundings, can be in it
+                float from = floor, to = INFINITY;
+                if (level == 0) {
+                    const float width = 1.0f / scale, slack = width * 0.01f + fabsf(top) * 1e-6f;
+                    if (bin < kBins - 1) from = fmaxf(floor, top - static_cast<float>(bin + 1) * width - slack);
+                    if (!all) to = top - static_cast<float>(bin) * width + slack;
+                }
+                if (tid == 0) sh.collected = 0;
+                __syncthreads();  // and all have read the bins' sums
+                each_of_run(from, [&](float x, int i) {
+                    if (x > to) return;
                     const int b = place(x);
                     if (b != bin && !(all && b < bin && b >= 0)) return;
-                    if (kWeigh && w.of(x) == 0) return;  // not counted either
-                    list[atomicAdd(listed, 1u)] = item(x, i);
+                    append(!(kWeigh && w.of(x) == 0), x, i);  // as they were counted
                 });
+                __syncthreads();
+                if (tid == 0) sh.listed_at = atomicAdd(cluster.map_shared_rank(&sh.listed, 0), sh.collected);
+                __syncthreads();
+                hand_over(sh.listed_at);
                 cluster.sync();
                 if (all) return kListed;
                 if (rank == 0) {
                     const int m = static_cast<int>(sh.listed);
-                    sort(sh.list, m);
+                    sort(sh, m);
                     uint64_t v2[2], lead, sum;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -624,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     // are what top-k keeps; limit: the target of top-p, or 0 to form it from their weight.
     auto finish = [&](int most, uint64_t limit) {
         const int m = static_cast<int>(sh.listed);
-        sort(sh.list, m);
+        sort(sh, m);
         most = min(most, m);
         float x[2];
         uint64_t v[2], lead, whole;
@@ -650,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (keep[j]) sh.list[2 * tid + j] = to[j];
-        sort(sh.list, kept);
+        sort(sh, kept);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int p = 2 * tid + j;
@@ -680,6 +757,57 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     if (use_p) {
         // equal logits that top-k leaves out are weighed with the others
         const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of(cut.at) : 0;
+        if (cut.ties == 0) {
+            // Are the tokens of at least 2^-9 of the largest weight few?
+            const float heavy_from = fmaxf(top - 9.0f / w.c, kLowest);
+            uint32_t mine = 0;
+            each_of_run(heavy_from, [&](float, int) { ++mine; });
+            mine = __reduce_add_sync(~0u, mine);
+            mine = static_cast<uint32_t>(of_warps(mine));
+            if (warp == 0) mine = __reduce_add_sync(~0u, lane < kWarps ? mine : 0);
+            if (tid == 0) sh.collected = 0;
+            give([&](Exchange* e) { e->listed = mine; });
+            const uint32_t theirs = lane < ctas ? given_by(lane).listed : 0, upto = warp_scan(theirs, lane);
+            const uint32_t in_all = __shfl_sync(~0u, upto, 31);
+            if (in_all <= kFew) {
+                uint64_t mass = 0, heavy = 0;  // of all tokens, and theirs
+                if (run_top >= kLowest)
+                    each_four(run_begin, run_end, kLowest, [&](const float (&x)[4], int i) {
+                        uint64_t m[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) m[q] = w.of(x[q]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            mass += m[q];
+                            heavy += x[q] >= heavy_from ? m[q] : 0;
+                            append(x[q] >= heavy_from, x[q], i + q);
+                        }
+                    });
+                mass = warp_reduce(mass, add<uint64_t>);
+                heavy = warp_reduce(heavy, add<uint64_t>);
+                mass = of_warps(mass);
+                __syncthreads();
+                heavy = of_warps(heavy);
+                if (warp == 0) {
+                    mass = warp_reduce(lane < kWarps ? mass : 0, add<uint64_t>);
+                    heavy = warp_reduce(lane < kWarps ? heavy : 0, add<uint64_t>);
+                }
+                hand_over(__shfl_sync(~0u, upto - theirs, rank));
+                if (rank == 0 && tid == 0) sh.listed = in_all;
+                give([&](Exchange* e) {
+                    e->mass = mass;
+                    e->heavy = heavy;
+                });
+                mass = warp_reduce(lane < ctas ? given_by(lane).mass : 0, add<uint64_t>);
+                heavy = warp_reduce(lane < ctas ? given_by(lane).heavy : 0, add<uint64_t>);
+                const uint64_t goal = share(mass);
+                if (heavy >= goal && goal > 0) {
+                    if (rank == 0) finish(kFew, goal);
+                    return;
+                }
+                if (rank == 0 && tid == 0) sh.listed = 0;
+            }
+        }
         const Found f = find(std::true_type{}, fmaxf(cut.at, kLowest), [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
         if (f == kListed) {
             if (rank == 0) finish(kFew, target);
@@ -693,9 +821,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     auto weigh = [&](int begin, int end, uint64_t& mass, uint32_t& ties) {
         mass = 0;
         ties = 0;
-        each(begin, end, lowest, [&](float x, int) {
-            if (cut.ties && x == cut.at) ++ties;
-            else mass += w.of(x);
+        each_four(begin, end, lowest, [&](const float (&x)[4], int) {
+            uint64_t m[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m[q] = w.of(x[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool tied = cut.ties && x[q] == cut.at;
+                ties += tied;
+                mass += x[q] >= lowest && !tied ? m[q] : 0;
+            }
         });
         mass = warp_reduce(mass, add<uint64_t>);
         ties = __reduce_add_sync(~0u, ties);
