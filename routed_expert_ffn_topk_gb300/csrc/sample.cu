@@ -119,8 +119,10 @@ struct Weights {
         const uint64_t w = parts(l, s);
         return ((w >> s) + 1) >> 1;
     }
+    // The same for single logits: one copy of the code, which is fetched once.
+    __device__ __noinline__ uint64_t of_one(float l) const { return of(l); }
     // A kept token's probability, from its weight before that became a whole number of units.
-    __device__ __forceinline__ float share(float l, uint64_t whole) const {
+    __device__ __noinline__ float share(float l, uint64_t whole) const {
         int s;
         const double w = static_cast<double>(parts(l, s));
         return static_cast<float>(w / (static_cast<double>(2ull << s) * static_cast<double>(whole)));
@@ -225,7 +227,7 @@ __device__ __forceinline__ uint32_t cta_min(uint32_t v, uint32_t* room) {  // ro
 // Puts the list's n <= kFew different values in ascending order. Of a few, each value's place is
 // the number of smaller ones. More are first dealt into as many bins of equal width in the
 // upper word as there are threads, so that a value is compared with those of its bin alone.
-__device__ __forceinline__ void sort(Shared& sh, int n) {
+__device__ __noinline__ void sort(Shared& sh, int n) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     uint64_t* v = sh.list;
     __syncthreads();
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                     if (x > to) return;
                     const int b = place(x);
                     if (b != bin && !(all && b < bin && b >= 0)) return;
-                    append(!(kWeigh && w.of(x) == 0), x, i);  // as they were counted
+                    append(!(kWeigh && w.of_one(x) == 0), x, i);  // as they were counted
                 });
                 __syncthreads();
                 if (tid == 0) sh.listed_at = atomicAdd(cluster.map_shared_rank(&sh.listed, 0), sh.collected);
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int p = 2 * tid + j;
-                        v2[j] = p >= m ? 0 : kWeigh ? w.of(logit_of(sh.list[p])) : 1;
+                        v2[j] = p >= m ? 0 : kWeigh ? w.of_one(logit_of(sh.list[p])) : 1;
                     }
                     scan(v2[0], v2[1], lead, sum);
                     lead += before;
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             }
             if (level >= 2 && shift == 0) {  // equal logits
                 const float x = value_of(hi - static_cast<uint32_t>(bin));
-                const uint64_t m = kWeigh ? w.of(x) : 1;
+                const uint64_t m = kWeigh ? w.of_one(x) : 1;
                 cut = Cut{x, static_cast<uint32_t>((target - before + m - 1) / m), members};
                 return kFound;
             }
@@ -709,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         for (int j = 0; j < 2; ++j) {
             const int p = 2 * tid + j;
             x[j] = p < most ? logit_of(sh.list[p]) : -INFINITY;
-            v[j] = w.of(x[j]);
+            v[j] = w.of_one(x[j]);
         }
         scan(v[0], v[1], lead, whole);
         if (use_p && limit == 0) limit = share(whole);
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             const int p = 2 * tid + j;
             to[j] = p < kept ? sh.list[p] : 0;
             x[j] = value_of(~static_cast<uint32_t>(to[j]));
-            v[j] = p < kept ? w.of(x[j]) : 0;
+            v[j] = p < kept ? w.of_one(x[j]) : 0;
         }
         scan(v[0], v[1], lead, whole);
         const uint64_t goal = point(whole);
@@ -747,16 +749,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         }
     };
 
+    int most = 0;        // listed: the leading CTA's list has the cut
+    uint64_t limit = 0;  // its target, for top-p alone
     if (use_k) {
         const Found f = find(std::false_type{}, kLowest, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, true);
-        if (f == kListed) {
-            if (rank == 0) finish(top_k, 0);
-            return;
-        }
+        if (f == kListed) most = top_k;
     }
-    if (use_p) {
+    if (use_p && !most) {
         // equal logits that top-k leaves out are weighed with the others
-        const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of(cut.at) : 0;
+        const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of_one(cut.at) : 0;
         if (cut.ties == 0) {
             // Are the tokens of at least 2^-9 of the largest weight few?
             const float heavy_from = fmaxf(top - 9.0f / w.c, kLowest);
@@ -802,18 +803,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                 heavy = warp_reduce(lane < ctas ? given_by(lane).heavy : 0, add<uint64_t>);
                 const uint64_t goal = share(mass);
                 if (heavy >= goal && goal > 0) {
-                    if (rank == 0) finish(kFew, goal);
-                    return;
+                    most = kFew;
+                    limit = goal;
+                } else if (rank == 0 && tid == 0) {
+                    sh.listed = 0;
                 }
-                if (rank == 0 && tid == 0) sh.listed = 0;
             }
         }
-        const Found f = find(std::true_type{}, fmaxf(cut.at, kLowest), [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
-        if (f == kListed) {
-            if (rank == 0) finish(kFew, target);
-            return;
+        if (!most) {
+            const Found f = find(std::true_type{}, fmaxf(cut.at, kLowest), [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
+            if (f == kListed) {
+                most = kFew;
+                limit = target;
+            }
+            if (f == kNothing) cut = Cut{top, 1, 1};  // top_p of 0
         }
-        if (f == kNothing) cut = Cut{top, 1, 1};  // top_p of 0
+    }
+    if (most) {
+        if (rank == 0) finish(most, limit);
+        return;
     }
     if (least_kept > cut.at) cut = Cut{-INFINITY, 0, 0};
     // The kept weight, by warps, each of which has a run of the CTA's logits, and over the cluster.
@@ -835,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         mass = warp_reduce(mass, add<uint64_t>);
         ties = __reduce_add_sync(~0u, ties);
     };
-    const uint64_t tie = cut.ties ? w.of(cut.at) : 0;
+    const uint64_t tie = cut.ties ? w.of_one(cut.at) : 0;
     uint64_t mass = 0;
     uint32_t ties = 0;
     if (run_top >= lowest) weigh(run_begin, run_end, mass, ties);
@@ -894,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         const int i = i0 + lane;
         const float x = i < min(end, begin + (part + 1) * sub) ? at(i) : -INFINITY;
         const bool tied = cut.ties && x == cut.at;
-        Before c = line_up(!tied && x >= lowest ? w.of(x) : 0, tied, b.start, b.left);
+        Before c = line_up(!tied && x >= lowest ? w.of_one(x) : 0, tied, b.start, b.left);
         const uint32_t over = __ballot_sync(~0u, c.start + c.mass > goal);
         if (over) {
             if (lane == __ffs(over) - 1) {
