@@ -7,8 +7,8 @@
 // weights are integers, 2^42 for the largest, within 2^-37 of their value or one unit, and
 // their sums are exact and the same in every order.
 //
-// A cluster of CTAs holds a row's logits in its shared memory, so they are read from HBM
-// once, and goes over them in passes, between which the CTAs exchange a few numbers.
+// A cluster of CTAs goes over a row in passes, between which the CTAs exchange a few numbers. Where a
+// row may have a cut, it holds the row's logits in its shared memory, so they are read from HBM once.
 //
 // A cut (the k-th largest logit, or the one at which top_p of the weight is reached)
 // is found by bins of equal width in the logit below the largest, counted and weighed by
@@ -16,14 +16,21 @@
 // the cut's bin, as after most prompts, they are gathered in one CTA, which sorts
 // them and does the rest alone. Else the bin with the cut is divided again until its tokens
 // can be sorted or are all equal, and the kept tokens are weighed and searched
-// where they are. With top-p alone the bins are left out where the tokens of at least 2^-9 of the
-// largest weight are few and reach the target.
+// where they are.
+//
+// Without cuts the logits are not kept: a warp reads its run of a row again, out of L2,
+// where the run's largest allows a kept token, and more rows are under way (256 rows of 151936
+// fp32 with min-p 76 us instead of 102, without any choice 119 instead of 167).
+//
+// What bounds it: for few rows the meetings of the cluster (about 1 us each: three for a
+// list, two without cuts), for many the weights (45 instructions each).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "estream_internal.h"
 #include "overlap.cuh"
@@ -119,10 +126,8 @@ struct Weights {
         const uint64_t w = parts(l, s);
         return ((w >> s) + 1) >> 1;
     }
-    // The same for single logits: one copy of the code, which is fetched once.
-    __device__ __noinline__ uint64_t of_one(float l) const { return of(l); }
     // A kept token's probability, from its weight before that became a whole number of units.
-    __device__ __noinline__ float share(float l, uint64_t whole) const {
+    __device__ __forceinline__ float share(float l, uint64_t whole) const {
         int s;
         const double w = static_cast<double>(parts(l, s));
         return static_cast<float>(w / (static_cast<double>(2ull << s) * static_cast<double>(whole)));
@@ -187,8 +192,8 @@ struct Exchange {
     float top, least;  // its largest logit (NaN if it has one), and smallest finite one
     int first;         // its first largest logit's index
     uint32_t lo, hi;   // keys of a bin
-    uint32_t ties, listed;
-    uint64_t mass, heavy;
+    uint32_t ties;
+    uint64_t mass;
     Cut cut;
 };
 
@@ -227,7 +232,7 @@ __device__ __forceinline__ uint32_t cta_min(uint32_t v, uint32_t* room) {  // ro
 // Puts the list's n <= kFew different values in ascending order. Of a few, each value's place is
 // the number of smaller ones. More are first dealt into as many bins of equal width in the
 // upper word as there are threads, so that a value is compared with those of its bin alone.
-__device__ __noinline__ void sort(Shared& sh, int n) {
+__device__ __forceinline__ void sort(Shared& sh, int n) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     uint64_t* v = sh.list;
     __syncthreads();
@@ -294,7 +299,9 @@ __device__ __noinline__ void sort(Shared& sh, int n) {
     __syncthreads();
 }
 
-template <int kElem>
+// kCuts: some row may have a top-k or a top-p. Without, logits are read again where a run's largest
+// allows a kept token, out of L2, and a row needs no shared memory, so that more rows are under way.
+template <int kElem, bool kCuts>
 __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     using E = Elem<kElem>;
     extern __shared__ __align__(16) uint8_t raw[];
@@ -302,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     uint8_t* logits = raw + (sizeof(Shared) + 15) / 16 * 16;
     after_previous();
     cg::cluster_group cluster = cg::this_cluster();
+    auto begun = cluster.barrier_arrive();  // nobody stores in a CTA that has not begun
     const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int first = rank * a.slice, n = max(0, min(a.slice, a.V - first));
@@ -311,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     const float top_p = a.top_ps ? a.top_ps[row] : a.top_p;
     const float min_p = a.min_ps ? a.min_ps[row] : a.min_p;
     const bool greedy = !(temperature > 0x1p-100f);
-    const bool use_p = !(top_p >= 1.0f);
-    const bool use_k = top_k > 0 && top_k < a.V;
+    const bool use_p = kCuts && !(top_p >= 1.0f);
+    const bool use_k = kCuts && top_k > 0 && top_k < a.V;
     // in 64 bits by one thread: an SM does two such operations a clock
     if (tid == kThreads - 1) {
         const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 0x1p-100f));
@@ -332,7 +340,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             if (tid >> (7 - j) & 1) v = __umul64hi(v, kRoots[j] << 1);
         sh.table[tid] = (v + (1ull << (61 - kOne))) >> (62 - kOne);
     }
-    auto at = [&](int i) { return E::at(logits, i); };
+    const uint8_t* const from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
+    auto at = [&](int i) { return kCuts ? E::at(logits, i) : i < n ? E::at(from, i) : -INFINITY; };
+    auto chunk = [&](int i) {  // 16 bytes from logit i on
+        if constexpr (kCuts) return *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
+        if (a.wide && i + E::kPer <= n) return *reinterpret_cast<const uint4*>(from + static_cast<size_t>(i) * E::kBytes);
+        uint4 w;
+#pragma unroll
+        for (int j = 0; j < E::kPer; ++j) E::put(&w, j, at(i + j));
+        return w;
+    };
     // A warp has a run of the CTA's logits. f(x, i) for those of [begin, end) from `lowest` on,
     // by a warp; begin and end are multiples of 8 (past the row's end lies -infinity).
     const int padded = (n + 7) / 8 * 8, length = ((padded + kWarps - 1) / kWarps + 7) / 8 * 8;
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     float run_top = -INFINITY;  // its largest
     auto each = [&](int begin, int end, float lowest, auto f) {
         for (int i = begin + lane * E::kPer; i < end; i += 32 * E::kPer) {
-            const uint4 w = *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
+            const uint4 w = chunk(i);
             if (!(largest<kElem>(w) >= lowest)) continue;
 #pragma unroll
             for (int j = 0; j < E::kPer; ++j) {
@@ -352,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
     // f(x, i) for four logits from i on, where one of them is at or above `lowest`
     auto each_four = [&](int begin, int end, float lowest, auto f) {
         for (int i = begin + lane * E::kPer; i < end; i += 32 * E::kPer) {
-            const uint4 w = *reinterpret_cast<const uint4*>(logits + static_cast<size_t>(i) * E::kBytes);
+            const uint4 w = chunk(i);
             if (!(largest<kElem>(w) >= lowest)) continue;
 #pragma unroll
             for (int j = 0; j < E::kPer; j += 4) {
@@ -380,10 +397,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         return sh.warp[lane % kWarps];
     };
 
-    // The logits come to shared memory, and the largest of them and the range are found on the way.
+    // The largest logit and the range; with cuts the logits come to shared memory on the way.
     float top = -INFINITY, least = INFINITY;
     {
-        const uint8_t* from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
         const int vec = a.wide ? min(n, run_end) / E::kPer : 0;  // past the run's last whole 16 bytes
         const bool ranged = use_k || use_p;
         auto low = [&](float x) {
@@ -398,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j)
                 if (i0 + j * 32 < vec) {
-                    reinterpret_cast<uint4*>(logits)[i0 + j * 32] = v[j];
+                    if constexpr (kCuts) reinterpret_cast<uint4*>(logits)[i0 + j * 32] = v[j];
                     run_top = max_or_nan(run_top, largest<kElem>(v[j]));
                     if (ranged)
 #pragma unroll
@@ -409,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             const float x = i < n ? E::at(from, i) : -INFINITY;
             run_top = max_or_nan(run_top, x);
             if (ranged) low(x);
-            E::put(logits, i, x);
+            if constexpr (kCuts) E::put(logits, i, x);
         }
         top = run_top = warp_reduce(run_top, max_or_nan);
         least = warp_reduce(least, fminf);
@@ -420,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             top = warp_reduce(top, max_or_nan);
             least = warp_reduce(least, fminf);
         }
+        cluster.barrier_wait(std::move(begun));
         give([&](Exchange* e) {
             e->top = top;
             e->least = least;
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
                     if (x > to) return;
                     const int b = place(x);
                     if (b != bin && !(all && b < bin && b >= 0)) return;
-                    append(!(kWeigh && w.of_one(x) == 0), x, i);  // as they were counted
+                    append(!(kWeigh && w.of(x) == 0), x, i);  // as they were counted
                 });
                 __syncthreads();
                 if (tid == 0) sh.listed_at = atomicAdd(cluster.map_shared_rank(&sh.listed, 0), sh.collected);
@@ -626,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int p = 2 * tid + j;
-                        v2[j] = p >= m ? 0 : kWeigh ? w.of_one(logit_of(sh.list[p])) : 1;
+                        v2[j] = p >= m ? 0 : kWeigh ? w.of(logit_of(sh.list[p])) : 1;
                     }
                     scan(v2[0], v2[1], lead, sum);
                     lead += before;
@@ -661,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             }
             if (level >= 2 && shift == 0) {  // equal logits
                 const float x = value_of(hi - static_cast<uint32_t>(bin));
-                const uint64_t m = kWeigh ? w.of_one(x) : 1;
+                const uint64_t m = kWeigh ? w.of(x) : 1;
                 cut = Cut{x, static_cast<uint32_t>((target - before + m - 1) / m), members};
                 return kFound;
             }
@@ -711,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         for (int j = 0; j < 2; ++j) {
             const int p = 2 * tid + j;
             x[j] = p < most ? logit_of(sh.list[p]) : -INFINITY;
-            v[j] = w.of_one(x[j]);
+            v[j] = w.of(x[j]);
         }
         scan(v[0], v[1], lead, whole);
         if (use_p && limit == 0) limit = share(whole);
@@ -735,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             const int p = 2 * tid + j;
             to[j] = p < kept ? sh.list[p] : 0;
             x[j] = value_of(~static_cast<uint32_t>(to[j]));
-            v[j] = p < kept ? w.of_one(x[j]) : 0;
+            v[j] = p < kept ? w.of(x[j]) : 0;
         }
         scan(v[0], v[1], lead, whole);
         const uint64_t goal = point(whole);
@@ -749,68 +766,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         }
     };
 
-    int most = 0;        // listed: the leading CTA's list has the cut
-    uint64_t limit = 0;  // its target, for top-p alone
-    if (use_k) {
-        const Found f = find(std::false_type{}, kLowest, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, true);
-        if (f == kListed) most = top_k;
-    }
-    if (use_p && !most) {
-        // equal logits that top-k leaves out are weighed with the others
-        const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of_one(cut.at) : 0;
-        if (cut.ties == 0) {
-            // Are the tokens of at least 2^-9 of the largest weight few?
-            const float heavy_from = fmaxf(top - 9.0f / w.c, kLowest);
-            uint32_t mine = 0;
-            each_of_run(heavy_from, [&](float, int) { ++mine; });
-            mine = __reduce_add_sync(~0u, mine);
-            mine = static_cast<uint32_t>(of_warps(mine));
-            if (warp == 0) mine = __reduce_add_sync(~0u, lane < kWarps ? mine : 0);
-            if (tid == 0) sh.collected = 0;
-            give([&](Exchange* e) { e->listed = mine; });
-            const uint32_t theirs = lane < ctas ? given_by(lane).listed : 0, upto = warp_scan(theirs, lane);
-            const uint32_t in_all = __shfl_sync(~0u, upto, 31);
-            if (in_all <= kFew) {
-                uint64_t mass = 0, heavy = 0;  // of all tokens, and theirs
-                if (run_top >= kLowest)
-                    each_four(run_begin, run_end, kLowest, [&](const float (&x)[4], int i) {
-                        uint64_t m[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) m[q] = w.of(x[q]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            mass += m[q];
-                            heavy += x[q] >= heavy_from ? m[q] : 0;
-                            append(x[q] >= heavy_from, x[q], i + q);
-                        }
-                    });
-                mass = warp_reduce(mass, add<uint64_t>);
-                heavy = warp_reduce(heavy, add<uint64_t>);
-                mass = of_warps(mass);
-                __syncthreads();
-                heavy = of_warps(heavy);
-                if (warp == 0) {
-                    mass = warp_reduce(lane < kWarps ? mass : 0, add<uint64_t>);
-                    heavy = warp_reduce(lane < kWarps ? heavy : 0, add<uint64_t>);
-                }
-                hand_over(__shfl_sync(~0u, upto - theirs, rank));
-                if (rank == 0 && tid == 0) sh.listed = in_all;
-                give([&](Exchange* e) {
-                    e->mass = mass;
-                    e->heavy = heavy;
-                });
-                mass = warp_reduce(lane < ctas ? given_by(lane).mass : 0, add<uint64_t>);
-                heavy = warp_reduce(lane < ctas ? given_by(lane).heavy : 0, add<uint64_t>);
-                const uint64_t goal = share(mass);
-                if (heavy >= goal && goal > 0) {
-                    most = kFew;
-                    limit = goal;
-                } else if (rank == 0 && tid == 0) {
-                    sh.listed = 0;
-                }
-            }
+    if constexpr (kCuts) {
+        int most = 0;        // listed: the leading CTA's list has the cut
+        uint64_t limit = 0;  // its target, for top-p alone
+        if (use_k) {
+            const Found f = find(std::false_type{}, kLowest, [&](uint64_t) { return static_cast<uint64_t>(top_k); }, true);
+            if (f == kListed) most = top_k;
         }
-        if (!most) {
+        if (use_p && !most) {
+            // equal logits that top-k leaves out are weighed with the others
+            const uint64_t surplus = cut.ties ? (cut.all - cut.ties) * w.of(cut.at) : 0;
             const Found f = find(std::true_type{}, fmaxf(cut.at, kLowest), [&](uint64_t whole) { return share(whole - surplus); }, cut.ties == 0);
             if (f == kListed) {
                 most = kFew;
@@ -818,10 +783,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
             }
             if (f == kNothing) cut = Cut{top, 1, 1};  // top_p of 0
         }
-    }
-    if (most) {
-        if (rank == 0) finish(most, limit);
-        return;
+        if (most) {
+            if (rank == 0) finish(most, limit);
+            return;
+        }
     }
     if (least_kept > cut.at) cut = Cut{-INFINITY, 0, 0};
     // The kept weight, by warps, each of which has a run of the CTA's logits, and over the cluster.
@@ -843,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         mass = warp_reduce(mass, add<uint64_t>);
         ties = __reduce_add_sync(~0u, ties);
     };
-    const uint64_t tie = cut.ties ? w.of_one(cut.at) : 0;
+    const uint64_t tie = cut.ties ? w.of(cut.at) : 0;
     uint64_t mass = 0;
     uint32_t ties = 0;
     if (run_top >= lowest) weigh(run_begin, run_end, mass, ties);
@@ -902,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         const int i = i0 + lane;
         const float x = i < min(end, begin + (part + 1) * sub) ? at(i) : -INFINITY;
         const bool tied = cut.ties && x == cut.at;
-        Before c = line_up(!tied && x >= lowest ? w.of_one(x) : 0, tied, b.start, b.left);
+        Before c = line_up(!tied && x >= lowest ? w.of(x) : 0, tied, b.start, b.left);
         const uint32_t over = __ballot_sync(~0u, c.start + c.mass > goal);
         if (over) {
             if (lane == __ffs(over) - 1) {
@@ -918,10 +883,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
 
 bool at(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <int kElem>
+template <int kElem, bool kCuts>
 cudaError_t launch(const Sample& s, int B, int ctas, cudaStream_t stream) {
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + static_cast<size_t>(s.slice) * Elem<kElem>::kBytes;
-    cudaError_t rc = cudaFuncSetAttribute(k_sample<kElem>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (kCuts ? static_cast<size_t>(s.slice) * Elem<kElem>::kBytes : 0);
+    const auto kernel = k_sample<kElem, kCuts>;
+    cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (rc != cudaSuccess) return rc;
     cudaLaunchAttribute attr[2] = {overlapped(), {}};
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -934,7 +900,11 @@ cudaError_t launch(const Sample& s, int B, int ctas, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_sample<kElem>, s);
+    return cudaLaunchKernelEx(&cfg, kernel, s);
+}
+template <int kElem>
+cudaError_t launch(const Sample& s, bool cuts, int B, int ctas, cudaStream_t stream) {
+    return cuts ? launch<kElem, true>(s, B, ctas, stream) : launch<kElem, false>(s, B, ctas, stream);
 }
 
 }  // namespace
@@ -959,14 +929,15 @@ extern "C" estream_status estream_sample_tokens(const void* logits, int elem, lo
         return ESTREAM_ERR_INVALID_ARG;
     const estream_status st = on_device();
     if (st != ESTREAM_OK) return st;
-    // as many CTAs a row as keep the device busy, of 2048 logits at least, and as many as hold the row
+    const bool cuts = top_k_rows || top_p_rows || (top_k > 0 && top_k < V) || !(top_p >= 1.0f);
+    // as many CTAs a row as keep the device busy, of 2048 logits at least, and with cuts as many as hold the row
     int ctas = 1;
-    while (ctas < kMaxCtas && (V > ctas * 24576 || (B * ctas < 152 && V > ctas * 2048))) ctas *= 2;
+    while (ctas < kMaxCtas && ((cuts && V > ctas * 24576) || (B * ctas < (cuts ? 152 : 608) && V > ctas * 2048))) ctas *= 2;
     Sample s{logits, ld, V, ((V + ctas - 1) / ctas + 7) / 8 * 8, at(logits, 16) && ld * size % 16 == 0, u,
              temperature, top_p, min_p, top_k, temperature_rows, top_p_rows, min_p_rows, top_k_rows, ids, prob};
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-    const cudaError_t rc = elem == ESTREAM_MX4_BF16  ? launch<ESTREAM_MX4_BF16>(s, B, ctas, stream)
-                           : elem == ESTREAM_MX4_F16 ? launch<ESTREAM_MX4_F16>(s, B, ctas, stream)
-                                                     : launch<ESTREAM_MX4_F32>(s, B, ctas, stream);
+    const cudaError_t rc = elem == ESTREAM_MX4_BF16  ? launch<ESTREAM_MX4_BF16>(s, cuts, B, ctas, stream)
+                           : elem == ESTREAM_MX4_F16 ? launch<ESTREAM_MX4_F16>(s, cuts, B, ctas, stream)
+                                                     : launch<ESTREAM_MX4_F32>(s, cuts, B, ctas, stream);
     return rc == cudaSuccess ? ESTREAM_OK : ESTREAM_ERR_CUDA;
 }
