@@ -1,12 +1,15 @@
 """A prompt and the tokens after it through one MoE layer, on one GPU.
 
     python -m routed_expert_ffn_topk_gb300.generate --config c2 --batch 4 --prompt 256 --tokens 32
+    python -m routed_expert_ffn_topk_gb300.generate --attention --temperature 0.8 --top-k 50 --top-p 0.95
 
 The prompt goes through experts in microscaled 4-bit floating point (route map,
 quantised gather, grouped product, SwiGLU quantised for the down product, weighted
 sum); each generated token through the few-token layer call, one launch with the
-router's logits formed in it, and then a dense 4-bit output projection. A token's
-step is captured once and replayed. Weights, embedding and projection are seeded
+router's logits formed in it, and then a dense 4-bit output projection. With
+--attention the layer is preceded by attention over a paged key-value cache, which
+the prompt fills and every token extends. Tokens are the likeliest ones, or drawn
+from given random numbers. A token's step is captured once and replayed. Weights, embedding and projection are seeded
 and random: it shows the calls together, not a language.
 """
 from __future__ import annotations
@@ -63,50 +66,121 @@ class Mx4Experts:
         return (routes.view(T, k, self.H) * r["alpha"].view(T, k, 1)).sum(1)
 
 
+class PagedAttention:
+    """One attention layer of `batch` sequences of at most max_tokens: a 4-bit
+    projection to queries, keys and values (Wqkv [(heads + 2 kv_heads) dim, H], queries
+    first), keys and queries rotated by position, attention over the paged cache,
+    and a 4-bit projection back (Wo [H, heads dim])."""
+
+    def __init__(self, Wqkv: torch.Tensor, Wo: torch.Tensor, heads: int, kv_heads: int, batch: int, max_tokens: int,
+                 page_size: int = 16, kv_dtype=torch.bfloat16, base: float = 10000.0, fmt: int = es.FP4_E4M3X16,
+                 device="cuda"):
+        self.heads, self.kv_heads, self.fmt, self.batch = heads, kv_heads, fmt, batch
+        self.dim = Wqkv.shape[0] // (heads + 2 * kv_heads)
+        self.act_scale = ACT_SCALE if fmt == es.FP4_E4M3X16 else 1.0
+        self.qkv, self.out = mx4_weight_rows(Wqkv.to(device), fmt), mx4_weight_rows(Wo.to(device), fmt)
+        M = -(-max_tokens // page_size)
+        pages = torch.zeros(2, batch * M, page_size, kv_heads, self.dim, device=device).to(kv_dtype)
+        self.cache = es.PagedKV(pages[0], pages[1])
+        # an allocator hands pages out as sequences grow; here each has its own from the start
+        self.table = torch.arange(batch * M, dtype=torch.int32, device=device).view(batch, M)
+        self.max_tokens, self.lens = max_tokens, torch.zeros(batch, dtype=torch.int32, device=device)
+        self.inv_freq = (base ** (-torch.arange(0, self.dim, 2, dtype=torch.float64) / self.dim)).float().to(device)
+
+    def _project(self, x: torch.Tensor, w: es.Mx4Weights) -> torch.Tensor:
+        return es.mx4_product(es.mx4_quantize(x, self.fmt, self.act_scale), w)
+
+    def _attend(self, X: torch.Tensor, positions: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                rows: torch.Tensor | None) -> torch.Tensor:
+        qkv = self._project(X, self.qkv).view(X.shape[0], self.heads + 2 * self.kv_heads, self.dim)
+        q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
+        q = es.kv_append(self.cache, k, v, positions, self.table, rows=rows, q=q, inv_freq=self.inv_freq)
+        a = es.kv_attend(self.cache, q, table, lens)
+        return self._project(a.view(X.shape[0], -1), self.out)
+
+    def prefill(self, X: torch.Tensor, m: int) -> torch.Tensor:
+        """X [batch * m, H], m tokens of every sequence from its beginning: attention's output rows. Every
+        token attends to itself and those before it: a row of its own length over its sequence's pages."""
+        if not 1 <= m <= self.max_tokens or X.shape[0] != self.batch * m:
+            raise ValueError(f"X must hold 1 to {self.max_tokens} tokens of {self.batch} sequences")
+        positions = torch.arange(m, dtype=torch.int32, device=X.device).repeat(self.batch)
+        rows = torch.arange(self.batch, dtype=torch.int32, device=X.device).repeat_interleave(m)
+        y = self._attend(X, positions, positions + 1, self.table.repeat_interleave(m, 0), rows)
+        self.lens.fill_(m)
+        return y
+
+    def step(self, X: torch.Tensor) -> torch.Tensor:
+        """X [batch, H], the next token of every sequence."""
+        after = self.lens + 1
+        y = self._attend(X, self.lens, after, self.table, None)
+        self.lens.copy_(after)
+        return y
+
+
 class TokenLoop:
-    """Greedy tokens of up to DECODE_MAX_T sequences: embedding row [vocab, H], layer
-    with its residual, output projection [vocab, H], largest logit."""
+    """Tokens of up to DECODE_MAX_T sequences: embedding row [vocab, H], attention
+    where there is one, layer with its residual, output projection [vocab, H], and
+    the largest logit, or with `sampling` (sample_tokens' choices) a token drawn
+    from a given random number."""
 
     def __init__(self, stack: BoundLayerStack, W_r: torch.Tensor, embedding: torch.Tensor, head: torch.Tensor,
-                 fmt: int = es.FP4_E4M3X16):
+                 fmt: int = es.FP4_E4M3X16, attention: PagedAttention | None = None, sampling: dict | None = None):
         self.stack, self.W_r, self.embedding, self.fmt = stack, W_r, embedding, fmt
+        self.attention, self.sampling = attention, sampling
         self.head = mx4_weight_rows(head, fmt)
         self.act_scale = ACT_SCALE if fmt == es.FP4_E4M3X16 else 1.0
         self.graph = None
 
-    def project(self, Y: torch.Tensor) -> torch.Tensor:
-        """Token ids [n] of hidden rows [n, H]."""
+    def project(self, Y: torch.Tensor, u: torch.Tensor | None = None) -> torch.Tensor:
+        """Token ids [n] of hidden rows [n, H], drawn from u [n] when sampling."""
         q = es.mx4_quantize(Y, self.fmt, self.act_scale)
-        return es.mx4_product(q, self.head, out_dtype=torch.float32).argmax(1)
+        logits = es.mx4_product(q, self.head, out_dtype=torch.float32)
+        if self.sampling is None:
+            return logits.argmax(1)
+        return es.sample_tokens(logits, u, **self.sampling).long()
 
-    def step(self, ids: torch.Tensor) -> torch.Tensor:
-        X = self.embedding[ids]
+    def attend(self, X: torch.Tensor, m: int | None = None) -> torch.Tensor:
+        """X plus its attention, as rows of a prompt (m tokens a sequence) or as the next tokens."""
+        if self.attention is None:
+            return X
+        return X + (self.attention.step(X) if m is None else self.attention.prefill(X, m))
+
+    def step(self, ids: torch.Tensor, u: torch.Tensor | None = None) -> torch.Tensor:
+        X = self.attend(self.embedding[ids])
         Y = torch.empty(X.shape, dtype=torch.float32, device=X.device)
         self.stack.decode_from_x(0, X, self.W_r, Y, residual=X)
-        return self.project(Y)
+        return self.project(Y, u)
 
-    def run(self, ids: torch.Tensor, n: int) -> torch.Tensor:
-        """The n tokens after ids [b] of every sequence, [b, n]."""
+    def run(self, ids: torch.Tensor, n: int, u: torch.Tensor | None = None) -> torch.Tensor:
+        """The n tokens after ids [b] of every sequence, [b, n]; u [n, b] random numbers when sampling."""
         if self.graph is None or self.ids.shape != ids.shape:
             self.ids = ids.clone()
+            self.u = None if u is None else torch.zeros_like(u[0])
+            lens = None if self.attention is None else self.attention.lens.clone()
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
             with torch.cuda.stream(side):
-                self.step(self.ids)  # allocations and first-call work outside the capture
+                self.step(self.ids, self.u)  # allocations and first-call work outside the capture
             torch.cuda.current_stream().wait_stream(side)
+            if lens is not None:
+                self.attention.lens.copy_(lens)  # the next step stores its token in that one's place
             self.graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(self.graph):
-                self.ids.copy_(self.step(self.ids))
+                self.ids.copy_(self.step(self.ids, self.u))
         self.ids.copy_(ids)
         out = torch.empty(ids.shape[0], n, dtype=ids.dtype, device=ids.device)
         for i in range(n):
+            if u is not None:
+                self.u.copy_(u[i])
             self.graph.replay()
             out[:, i] = self.ids
         return out
 
 
-def build(config: str, batch: int, vocab: int, seed: int = 0, wdtype=None):
-    """The layer of a workload configuration with an embedding and a router."""
+def build(config: str, batch: int, vocab: int, seed: int = 0, wdtype=None, attend_tokens: int = 0,
+          sampling: dict | None = None):
+    """The layer of a workload configuration with an embedding and a router, and with attend_tokens
+    an attention layer (heads of 128, a key head for four of them) for sequences of as many tokens."""
     import dataclasses
 
     cfg = dataclasses.replace(W.CONFIGS[config], T=batch)
@@ -117,16 +191,30 @@ def build(config: str, batch: int, vocab: int, seed: int = 0, wdtype=None):
     lw = wl.layers[0]
     experts = Mx4Experts(lw.Wg, lw.Wu, lw.Wd)
     stack = BoundLayerStack(wl, mode="resident", wdtype=wdtype)
-    return cfg, experts, TokenLoop(stack, W_r, emb, head)
+    attention = None
+    if attend_tokens:
+        heads, dim = max(1, cfg.H // 128), min(cfg.H, 128)
+        kv_heads = max(1, heads // 4)
+        Wqkv = torch.randn((heads + 2 * kv_heads) * dim, cfg.H, generator=g) / math.sqrt(cfg.H)
+        Wo = torch.randn(cfg.H, heads * dim, generator=g) / math.sqrt(heads * dim)
+        attention = PagedAttention(Wqkv.to(torch.bfloat16), Wo.to(torch.bfloat16), heads, kv_heads, batch, attend_tokens)
+    return cfg, experts, TokenLoop(stack, W_r, emb, head, attention=attention, sampling=sampling)
 
 
-def generate(cfg, experts: Mx4Experts, loop: TokenLoop, prompt: torch.Tensor, n: int) -> torch.Tensor:
-    """prompt [b, m] token ids; the n tokens after it, [b, n]."""
-    X = loop.embedding[prompt.reshape(-1)]
+def generate(cfg, experts: Mx4Experts, loop: TokenLoop, prompt: torch.Tensor, n: int,
+             u: torch.Tensor | None = None) -> torch.Tensor:
+    """prompt [b, m] token ids; the n tokens after it, [b, n]; u [n, b] random numbers when sampling."""
+    if loop.attention is not None and prompt.shape[1] + n - 1 > loop.attention.max_tokens:
+        raise ValueError(f"the attention layer holds {loop.attention.max_tokens} tokens a sequence")
+    if loop.sampling is not None and (u is None or tuple(u.shape) != (n, prompt.shape[0])):
+        raise ValueError(f"sampling needs random numbers [{n}, {prompt.shape[0]}]")
+    if loop.sampling is None:
+        u = None
+    X = loop.attend(loop.embedding[prompt.reshape(-1)], prompt.shape[1])
     logits = es.router_logits(X, loop.W_r)
     Y = X.float() + experts.prefill(X, logits, cfg.k, cfg.renorm)
-    first = loop.project(Y.view(*prompt.shape, cfg.H)[:, -1])
-    rest = loop.run(first, n - 1) if n > 1 else first[:, None][:, :0]
+    first = loop.project(Y.view(*prompt.shape, cfg.H)[:, -1], None if u is None else u[0])
+    rest = loop.run(first, n - 1, None if u is None else u[1:]) if n > 1 else first[:, None][:, :0]
     return torch.cat([first[:, None], rest], 1)
 
 
@@ -137,18 +225,29 @@ def main() -> None:
     p.add_argument("--prompt", type=int, default=256)
     p.add_argument("--tokens", type=int, default=32)
     p.add_argument("--vocab", type=int, default=8192)
+    p.add_argument("--attention", action="store_true", help="attention over a paged cache before the layer")
+    p.add_argument("--temperature", type=float, default=0.0, help="0: the likeliest token")
+    p.add_argument("--top-k", type=int, default=0)
+    p.add_argument("--top-p", type=float, default=1.0)
+    p.add_argument("--min-p", type=float, default=0.0)
     a = p.parse_args()
     c = W.CONFIGS[a.config]
     if c.dtype != "bf16" or c.n_shared:
         p.error("the configuration must be bf16 and without shared experts")
     if not 1 <= a.batch <= es.DECODE_MAX_T or min(a.prompt, a.tokens, a.vocab) < 1:
         p.error(f"1 to {es.DECODE_MAX_T} sequences, and at least one token of prompt and output")
-    cfg, experts, loop = build(a.config, a.batch, a.vocab)
-    prompt = torch.randint(0, a.vocab, (a.batch, a.prompt), generator=torch.Generator().manual_seed(1)).cuda()
-    generate(cfg, experts, loop, prompt, a.tokens)  # first-call work
+    sampling = None
+    if a.temperature > 0:
+        sampling = dict(temperature=a.temperature, top_k=a.top_k, top_p=a.top_p, min_p=a.min_p)
+    cfg, experts, loop = build(a.config, a.batch, a.vocab, sampling=sampling,
+                               attend_tokens=a.prompt + a.tokens if a.attention else 0)
+    g = torch.Generator().manual_seed(1)
+    prompt = torch.randint(0, a.vocab, (a.batch, a.prompt), generator=g).cuda()
+    u = torch.rand(a.tokens, a.batch, generator=g).cuda() if sampling else None
+    generate(cfg, experts, loop, prompt, a.tokens, u)  # first-call work
     torch.cuda.synchronize()
     t0 = time.perf_counter()
-    ids = generate(cfg, experts, loop, prompt, a.tokens)
+    ids = generate(cfg, experts, loop, prompt, a.tokens, u)
     torch.cuda.synchronize()
     t = time.perf_counter() - t0
     if es.get_device_error(loop.stack.ctx) != es.OK or es.mx4_error() != es.OK:

@@ -242,3 +242,23 @@ def test_refusals():
         with pytest.raises(ValueError):
             es.kv_append(s.cache, **{**good, **kw})
     assert es.kv_append(s.cache, s.nk[:0], s.nv[:0], s.positions[:0], s.table) is None
+
+
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -140, 1e-8, 0.999, 1.0, 1.999, 2.0, 7.25, 1000.5])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_frequencies_of_any_size(size, sign):
+    """Slow, fast and negative turns; below 2 they are formed in integers, from there in 64 bits."""
+    s = _Step([0, 1, 999, 65537], [0, 1, 2, 3], 1, 2, 32, 16, "f16", "f16")
+    f = torch.full((16,), sign * size).cuda() * torch.linspace(0.5, 1.0, 16).cuda()
+    q = _es().kv_append(s.cache, s.nk, s.nv, s.positions, s.table, q=s.q, inv_freq=f)
+    s.check(f, False, q)
+
+
+@pytest.mark.parametrize("heads,Hq,dim", [(1, 0, 16), (1, 1, 256), (7, 49, 64), (64, 64, 128), (3, 300, 48)])
+@pytest.mark.parametrize("T", [1, 3, 400])
+def test_head_counts(heads, Hq, dim, T):
+    """Few and many heads, over few warps and many."""
+    s = _Step(list(range(T)), [0] * T, heads, Hq, dim, 16, "bf16")
+    f = _inv(dim)
+    q = _es().kv_append(s.cache, s.nk, s.nv, s.positions, s.table, rows=s.rows, q=s.q if Hq else None, inv_freq=f)
+    s.check(f, False, q)

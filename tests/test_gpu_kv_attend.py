@@ -279,3 +279,40 @@ def test_refusals():
     for s in (0.5, 0.0, float("nan")):
         with pytest.raises(ValueError):
             es.PagedKV(k, k, s)
+
+
+@pytest.mark.parametrize("B,heads,n", [(1, 1, 4097), (1, 8, 4096), (2, 16, 2048), (4, 16, 600), (40, 8, 100), (37, 1, 64), (300, 1, 33)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_units_and_clusters(B, heads, n, kind):
+    """On both sides of the rule by which a unit gets a cluster of its own: lengths from nothing to the table's end."""
+    g = torch.Generator().manual_seed(B + n)
+    lens = torch.randint(0, n + 1, (B,), generator=g).tolist()
+    lens[-1] = n
+    c = _kv.Case(lens, heads, 64, 16, kind, M=-(-n // 16), seed=n)
+    _check(c, _q(B, 2 * heads, 64, "bf16"))
+
+
+def test_two_graphs_at_once():
+    """Two captured graphs over one cache, replayed on two streams at once, with and without a workspace."""
+    es = _es()
+    for n in (500, 40000):
+        c = _kv.Case([n, n // 3], 2, 64, 16, "bf16")
+        q = [_q(2, 8, 64, "bf16", seed=s) for s in (1, 2)]
+        want = [es.kv_attend(c.cache, x, c.table, c.lens) for x in q]
+        outs, graphs = [torch.zeros_like(x) for x in q], []
+        for x, o in zip(q, outs):
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                for _ in range(20):
+                    es.kv_attend(c.cache, x, c.table, c.lens, out=o)
+            graphs.append(graph)
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for graph, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)

@@ -225,3 +225,29 @@ def test_refusals():
     with pytest.raises(ValueError):
         es.sample_tokens(torch.zeros(1, es.SAMPLE_MAX_V + 1, device="cuda"), u[:1])
     assert es.sample_tokens(l[:0], u[:0]).shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kw", [dict(top_k=1500, temperature=2.0), dict(top_p=0.97, temperature=3.0), dict(top_k=20000, top_p=0.9),
+                                dict(top_p=0.3, temperature=0.2), dict(top_k=1024), dict(top_k=1025), dict(temperature=50.0, top_p=0.5)])
+def test_large_sets(dtype, kw):
+    """More kept tokens than one CTA sorts, at its limit and past it; cuts in the bulk of 60000 tokens."""
+    l, u = rows(5, 60000, seed=11, std=2.5, dtype=dtype)
+    check(l, u, **kw)
+
+
+def test_many_equal_values():
+    """More equal logits at the cut than one CTA sorts, spread over the row or together."""
+    for l in ((torch.arange(40000) * 7919 % 5).float().repeat(3, 1).cuda(), (torch.arange(40000) // 9000).float().repeat(3, 1).cuda()):
+        u = torch.tensor([0.01, 0.5, 0.99], device="cuda")
+        for kw in (dict(top_k=5000), dict(top_k=12345, top_p=0.9), dict(top_p=0.5), dict(top_p=0.99, temperature=0.3)):
+            check(l, u, **kw)
+
+
+@pytest.mark.parametrize("B", [1, 3, 20, 80, 160, 700])
+def test_rows_and_ctas(B):
+    """Rows that have eight, four, two CTAs and one, with and without cuts."""
+    l, u = rows(B, 9001, seed=B)
+    check(l, u)
+    check(l, u, min_p=0.05, temperature=0.8)
+    check(l, u, top_k=30, top_p=0.9)
