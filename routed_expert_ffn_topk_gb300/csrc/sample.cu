@@ -20,7 +20,7 @@
 //
 // Without cuts the logits are not kept: a warp reads its run of a row again, out of L2,
 // where the run's largest allows a kept token, and more rows are under way (256 rows of 151936
-// fp32 with min-p 76 us instead of 102, without any choice 119 instead of 167).
+// fp32 with min-p 75 us instead of 102, without any choice 135 instead of 167).
 //
 // What bounds it: for few rows the meetings of the cluster (about 1 us each: three for a
 // list, two without cuts), for many the weights (45 instructions each).
@@ -41,6 +41,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+template <bool kCuts>
+constexpr int kThreadsOf = kCuts ? kThreads : 256;  // without cuts: four CTAs an SM instead of two
 constexpr int kBins = kThreads;  // one a thread
 constexpr int kMaxCtas = 8;      // of a cluster
 constexpr int kFew = 2 * kThreads;  // tokens that one CTA sorts
@@ -302,8 +304,9 @@ __device__ __forceinline__ void sort(Shared& sh, int n) {
 // kCuts: some row may have a top-k or a top-p. Without, logits are read again where a run's largest
 // allows a kept token, out of L2, and a row needs no shared memory, so that more rows are under way.
 template <int kElem, bool kCuts>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
+__global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k_sample(const Sample a) {
     using E = Elem<kElem>;
+    constexpr int kThreads = kThreadsOf<kCuts>, kWarps = kThreads / 32;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
     uint8_t* logits = raw + (sizeof(Shared) + 15) / 16 * 16;
@@ -333,12 +336,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const Sample a) {
         }
         sh.listed = 0;
     }
-    if (tid < 256) {  // the table
+    for (int i = tid; i < 256; i += kThreads) {  // the table
         uint64_t v = 1ull << 63;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (tid >> (7 - j) & 1) v = __umul64hi(v, kRoots[j] << 1);
-        sh.table[tid] = (v + (1ull << (61 - kOne))) >> (62 - kOne);
+            if (i >> (7 - j) & 1) v = __umul64hi(v, kRoots[j] << 1);
+        sh.table[i] = (v + (1ull << (61 - kOne))) >> (62 - kOne);
     }
     const uint8_t* const from = static_cast<const uint8_t*>(a.logits) + (row * a.ld + first) * E::kBytes;
     auto at = [&](int i) { return kCuts ? E::at(logits, i) : i < n ? E::at(from, i) : -INFINITY; };
@@ -895,7 +898,7 @@ cudaError_t launch(const Sample& s, int B, int ctas, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(B) * ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreadsOf<kCuts>);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
