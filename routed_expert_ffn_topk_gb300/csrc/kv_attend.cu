@@ -21,7 +21,10 @@
 // The matrix instructions take keys and transposed values as their 16 rows and the query heads of
 // a key head as their 8 columns (a wider group of heads: two tiles of 8, and units of 16),
 // so a group of 8 heads or fewer wastes no row: with the heads as rows, it took twice the
-// instructions and registers.
+// instructions and registers (64 ragged sequences over E4M3 243 us instead of 208).
+//
+// Bound by HBM: 131072 positions of 8 heads of 128 bf16 in 82 us (6.5 TB/s, 96% of the copy rate) and
+// 5 us of joining; 64 ragged sequences up to 16384 in E4M3 122 us (6.0 TB/s), 32 in fp16 60 us (6.2).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,7 +43,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;  // positions that lie in one page together where page_size is a multiple of it
 constexpr int kRows = 16;   // query heads that meet a key together, at most
-// What a unit costs a warp beside its blocks (queries, results), in blocks.
+// What a unit costs a warp beside its blocks (queries, results), in blocks: without it the warps with the short
+// sequences of a ragged batch end last (140 us instead of 134, 64 sequences over E4M3).
 constexpr int kOver = 1;
 
 struct Attend {
@@ -823,6 +827,9 @@ struct Block {
     static constexpr int value = Shape<kElem, kDim>::kBlock;
 };
 
+// A cluster a unit: one launch less (5.5 us instead of 8.2 for 1 x 500 in a graph, 9 instead of 17 a call with
+// its workspace, window case 8.4 instead of 9.7). Past 8 blocks a warp, and where clusters do not all fit, shares are
+// at least level: they use every SM.
 constexpr int kMaxCtas = 8;
 constexpr int kDeep = 8;  // blocks of a cluster's warp, at most
 
