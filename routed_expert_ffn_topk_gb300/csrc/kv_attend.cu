@@ -827,11 +827,13 @@ struct Block {
     static constexpr int value = Shape<kElem, kDim>::kBlock;
 };
 
-// A cluster a unit: one launch less (5.5 us instead of 8.2 for 1 x 500 in a graph, 9 instead of 17 a call with
-// its workspace, window case 8.4 instead of 9.7). Past 8 blocks a warp, and where clusters do not all fit, shares are
-// at least level: they use every SM.
+// A unit gets a cluster while all fit on the device at once and its warps have 128 positions or fewer: one launch
+// and no workspace (9 us a call instead of 17 for 1 x 500). In a graph, cluster against shares, us: 8 key heads of 500
+// positions 5.6 / 8.9, 2048 8.0 / 9.6, 4096 10.6 / 10.4, 8192 16.3 / 12.0; 32 of 4096 11.9 / 14.4, 8192
+// 24.9 / 28.1, where equal lengths fill the device either way but a cluster of a short sequence would leave it idle;
+// 8 in E4M3 of 4096 9.6 / 10.8, 8192 13.7 / 11.4.
 constexpr int kMaxCtas = 8;
-constexpr int kDeep = 8;  // blocks of a cluster's warp, at most
+constexpr int kDeep = 128;  // positions of a cluster's warp, at most
 
 Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int sms) {
     const int group = Hq / c->heads, tiles = (group + kRows - 1) / kRows, kd = padded_dim(c->dim);
@@ -842,7 +844,7 @@ Layout layout(const estream_kv_cache* c, int B, int Hq, int M, int window, int s
     Layout l{};
     int ctas = 1;
     while (ctas < kMaxCtas && ctas * kWarps < blocks) ctas *= 2;
-    if (units * ctas <= room && blocks <= ctas * kWarps * kDeep) {
+    if (units * ctas <= room && blocks * block <= ctas * kWarps * kDeep) {
         l.ctas = ctas;
         l.grid = static_cast<int>(units) * ctas;
         return l;
