@@ -252,7 +252,7 @@ __device__ __forceinline__ void sort(Shared& sh, int n) {
         __syncthreads();
         return;
     }
-    static_assert(sizeof(Bins) >= kFew * sizeof(uint64_t), "a list fits the bins");
+    static_assert(sizeof(Bins) >= kFew * sizeof(uint64_t) && kBins >= kFew / 4, "a list fits the bins, two short ones the sums");
     uint64_t* dealt = reinterpret_cast<uint64_t*>(&sh.bins);
     uint32_t* count = sh.sum_count;
     uint64_t x[2];
@@ -723,6 +723,56 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     // are what top-k keeps; limit: the target of top-p, or 0 to form it from their weight.
     auto finish = [&](int most, uint64_t limit) {
         const int m = static_cast<int>(sh.listed);
+        if (m <= kFew / 8) {
+            // Nothing is sorted: every token meets every other, by several threads a token. First what is likelier,
+            // or as likely and earlier; then what is kept and earlier.
+            uint64_t* weights = sh.sum;
+            uint64_t* kept = sh.sum + kFew / 8;
+            int size = 16;
+            while (size < m) size *= 2;
+            const int parts = kThreads / size, i = tid / parts, part = tid % parts;
+            __syncthreads();  // the list is whole
+            const uint64_t mine = i < m ? sh.list[i] : 0;
+            const float x = i < m ? logit_of(mine) : -INFINITY;
+            const uint64_t weight = w.of(x);
+            if (i < m && part == 0) weights[i] = weight;
+            __syncthreads();
+            int place = 0;
+            uint64_t lead = 0;
+            if (i < m)
+                for (int j = part; j < m; j += parts) {
+                    const bool ahead = sh.list[j] < mine;
+                    place += ahead;
+                    lead += ahead ? weights[j] : 0;
+                }
+            for (int o = parts / 2; o; o >>= 1) {
+                place += __shfl_xor_sync(~0u, place, o);
+                lead += __shfl_xor_sync(~0u, lead, o);
+            }
+            if (use_p && limit == 0) {
+                uint64_t before, whole;
+                scan(i < m && part == 0 && place < most ? weight : 0, 0, before, whole);
+                limit = share(whole);
+            }
+            const bool keep = i < m && (place == 0 || (place < most && x >= least_kept && (!use_p || lead < limit)));
+            if (i < m && part == 0) kept[i] = keep ? weight : 0;
+            __syncthreads();
+            uint64_t upto = 0, whole = 0;
+            for (int j = part; j < m; j += parts) {
+                whole += kept[j];
+                upto += static_cast<uint32_t>(sh.list[j]) <= static_cast<uint32_t>(mine) ? kept[j] : 0;
+            }
+            for (int o = parts / 2; o; o >>= 1) {
+                whole += __shfl_xor_sync(~0u, whole, o);
+                upto += __shfl_xor_sync(~0u, upto, o);
+            }
+            const uint64_t goal = point(whole);
+            if (keep && part == 0 && upto > goal && upto - weight <= goal) {
+                a.ids[row] = static_cast<int>(static_cast<uint32_t>(mine));
+                if (a.prob) a.prob[row] = w.share(x, whole);
+            }
+            return;
+        }
         sort(sh, m);
         most = min(most, m);
         float x[2];
