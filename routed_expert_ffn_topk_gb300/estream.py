@@ -867,6 +867,8 @@ def _kv_table(t: torch.Tensor, cache: PagedKV):
     (B, M), (row, one) = t.shape, t.stride()
     if one != 1 and M > 1:
         raise ValueError("table must have contiguous rows")
+    if max(B, M) > 1 << 30:
+        raise ValueError("a table has at most 2^30 rows and columns")
     return t.data_ptr(), B, M, row
 
 
@@ -893,6 +895,8 @@ def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch
     one without a valid page is not stored and its queries become NaNs."""
     elem, dt, heads, dim, index = _kv_dtype(k, cache, "k"), k.dtype, cache.heads, cache.dim, cache._index
     T = k.shape[0]
+    if T > 1 << 30:
+        raise ValueError("at most 2^30 tokens a call")
     k0, k1, k2 = k.stride() if k.dim() == 3 else (0, 0, 0)
     if k2 != 1 or k.shape != (T, heads, dim) or k.get_device() != index:
         raise _kv_bad(k, T, heads, cache, "k", dt)
@@ -951,8 +955,8 @@ def kv_attend(cache: PagedKV, q: torch.Tensor, table: torch.Tensor, lens: torch.
     tp, rows, M, table_row = _kv_table(table, cache)
     if rows != B:
         raise ValueError("table must have a row for each row of q")
-    if window < 0:
-        raise ValueError("window must not be negative")
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be between 0 and 2^31 - 1")
     if out is None:
         out = torch.empty(shape, dtype=dt, device=cache.device)
     o0, o1, o2 = out.stride() if out.dim() == 3 else (0, 0, 0)
@@ -1010,6 +1014,10 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=
     ld, dev = logits.stride(0), logits.device
     if not 1 <= V <= SAMPLE_MAX_V:
         raise ValueError(f"a vocabulary must have 1 to {SAMPLE_MAX_V} tokens")
+    if B > 1 << 30:
+        raise ValueError("at most 2^30 rows a call")
+    if not isinstance(top_k, torch.Tensor) and not -(1 << 31) <= top_k < 1 << 31:
+        raise ValueError("top_k must fit in 32 bits")
     _, up = _choice(u, B, torch.float32, "u", dev)
     if up is None:
         raise ValueError("u must be a tensor with a random number for each row")
