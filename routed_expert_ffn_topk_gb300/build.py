@@ -2,7 +2,8 @@
 
 Compiles each CUDA translation unit in parallel (one -gencode, no fast-math)
 and links them with the shared CUDA runtime into
-``routed_expert_ffn_topk_gb300/libestream.so``.
+``routed_expert_ffn_topk_gb300/libestream.so``, and the compiled part of the
+binding (plain C, Python's own headers) into ``_binding.so``.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libestream.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 SOURCES = ["route.cu", "route_static.cu", "expert_gemm.cu", "expert_f32.cu", "runtime.cu",
            "pipeline_model.cu", "router.cu", "decode.cu", "mx4.cu", "mx4_product.cu", "kv_append.cu",
            "kv_attend.cu", "sample.cu"]
@@ -61,10 +64,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("the compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         if verbose:
             sys.stderr.write(r.stdout + r.stderr)
 
+    binding = os.path.join(CSRC, "binding.c")
+    python_include = sysconfig.get_paths()["include"]
+    # without Python's headers the binding takes its interpreted way alone
+    if os.path.exists(os.path.join(python_include, "Python.h")) and (
+            force or _stale(BINDING_PATH, [binding, os.path.join(INCLUDE, "estream.h")])):
+        tmp_binding = BINDING_PATH + ".tmp%d" % os.getpid()
+        run([shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I" + INCLUDE,
+             "-I" + python_include, binding, "-o", tmp_binding])
+        os.replace(tmp_binding, BINDING_PATH)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             list(ex.map(run, jobs))

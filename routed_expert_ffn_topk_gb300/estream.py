@@ -82,6 +82,7 @@ class KvCache(ctypes.Structure):
 
 
 _lib = None
+_fast = None  # the compiled part of the binding, once the library is loaded
 
 # name -> (restype, argtypes)
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -160,7 +161,22 @@ def lib():
             fn.restype = res
             fn.argtypes = args
         _lib = L
+        _load_fast(L)
     return _lib
+
+
+def _load_fast(L) -> None:
+    """The compiled part of the binding, where it was built: the calls of a generation
+    step are shorter than an interpreted check of their arguments."""
+    global _fast
+    if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+        return
+    from . import _binding
+    address = lambda name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+    _binding.setup(address("estream_kv_append"), address("estream_kv_attend"), address("estream_kv_attend_workspace_bytes"),
+                   address("estream_sample_tokens"), torch.Tensor, torch.bfloat16, torch.float16, torch.float32, torch.int32,
+                   torch.uint8, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    _fast = _binding
 
 
 def status_string(status: int) -> str:
@@ -820,7 +836,8 @@ class PagedKV:
         self._scale = dim ** -0.5
         self._desc = KvCache(k.data_ptr(), v.data_ptr(), elem, pages, page, heads, dim, k_scale, v_scale,
                              *k.stride()[:3], *v.stride()[:3])
-        self._ref = ctypes.byref(self._desc)
+        self._ref, self._address = ctypes.byref(self._desc), ctypes.addressof(self._desc)
+        lib()
         self._workspaces = {}
         self._elem, self._index = elem, k.get_device()
 
@@ -893,6 +910,12 @@ def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch
     fp32 the keys, and q [T, Hq, dim], are rotated by position; returns the rotated
     queries (q_out, which may be q). A token with a negative position is skipped;
     one without a valid page is not stored and its queries become NaNs."""
+    if _fast is not None and stream is None and (q_out is not None or q is None):
+        st = _fast.kv_append(cache._address, cache._index, k, v, positions, table, rows, q, inv_freq, interleaved, q_out)
+        if st == 0:
+            return q_out
+        if st is not None:
+            _check(st, "estream_kv_append")
     elem, dt, heads, dim, index = _kv_dtype(k, cache, "k"), k.dtype, cache.heads, cache.dim, cache._index
     T = k.shape[0]
     if T > 1 << 30:
@@ -945,6 +968,13 @@ def kv_attend(cache: PagedKV, q: torch.Tensor, table: torch.Tensor, lens: torch.
     that share a sequence (the tokens of a prompt) may share a table row
     (table.expand). workspace: uint8, cache.attend_workspace_bytes(B, Hq, M,
     window) of them, for this call alone until it ends (allocated when not given)."""
+    if _fast is not None and stream is None and out is not None:
+        st = _fast.kv_attend(cache._address, cache._index, q, table, lens, cache._scale if scale is None else scale, window,
+                             out, lse, workspace)
+        if st == 0:
+            return out
+        if st is not None:
+            _check(st, "estream_kv_attend")
     elem, dt, dim, index = _kv_dtype(q, cache, "q"), q.dtype, cache.dim, cache._index
     if q.dim() != 3 or q.shape[2] != dim or q.shape[1] < 1 or q.shape[1] % cache.heads:
         raise ValueError(f"q must be [B, Hq, {dim}] with Hq a multiple of {cache.heads}")
@@ -1005,6 +1035,12 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=
     order whose cumulative probability exceeds u, and its probability goes to
     prob [B] fp32. Temperature 0 takes the largest logit. Each choice is a number or a
     tensor [B] (fp32; top_k int32). A row without a finite largest logit gives -1."""
+    if _fast is not None and stream is None and out is not None:
+        st = _fast.sample(logits.get_device(), logits, u, temperature, top_k, top_p, min_p, out, prob)
+        if st == 0:
+            return out
+        if st is not None:
+            _check(st, "estream_sample_tokens")
     elem = _MX4_ELEM.get(logits.dtype)
     if elem is None or not logits.is_cuda:
         raise ValueError("logits must be a bf16, fp16 or fp32 CUDA tensor")
