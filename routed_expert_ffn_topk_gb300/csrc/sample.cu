@@ -13,17 +13,21 @@
 // A cut (the k-th largest logit, or the one at which top_p of the weight is reached)
 // is found by bins of equal width in the logit below the largest, counted and weighed by
 // shared-memory atomics and added up over the cluster. Where few tokens lie up to
-// the cut's bin, as after most prompts, they are gathered in one CTA, which sorts
-// them and does the rest alone. Else the bin with the cut is divided again until its tokens
+// the cut's bin, as after most prompts, they are gathered in one CTA, which does
+// the rest alone: up to 128 by comparing each with all (sorting them took 32 rows of
+// 102400 with top-k 40 from 17 to 21 us), more by sorting. Else the bin with the cut is divided again until its tokens
 // can be sorted or are all equal, and the kept tokens are weighed and searched
 // where they are.
 //
-// Without cuts the logits are not kept: a warp reads its run of a row again, out of L2,
-// where the run's largest allows a kept token, and more rows are under way (256 rows of 151936
-// fp32 with min-p 75 us instead of 102, without any choice 135 instead of 167).
+// Without cuts the logits are not kept, so that more rows are under way: what may hold a kept
+// token is read again, out of L2. With min-p or temperature 0 that is little: each lane notes
+// the largest of every 8 reads of 16 bytes, and the warp shares out those with a hit (256 rows of
+// 151936 fp32 with min-p 50 us; reading whole runs of a warp again 69). Without any choice all is weighed
+// (112 us).
 //
 // What bounds it: for few rows the meetings of the cluster (about 1 us each: three for a
-// list, two without cuts), for many the weights (45 instructions each).
+// list, two without cuts), for many the weights. With each float operation of two logits'
+// weights in one instruction, 256 rows without a choice take 120 us instead of 135.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -93,6 +97,34 @@ __constant__ uint64_t kRoots[8] = {0x5a827999fcef3242ull, 0x6ba27e656b4eb57aull,
                                    0x7a92be8a92436616ull, 0x7d41d96db915019dull, 0x7e9f06067a4360baull,
                                    0x7f4f08ae3dc7c426ull, 0x7fa765aca88f6453ull};
 
+// Two floats that one instruction works on.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
+    __device__ __forceinline__ float2 get() const {
+        float2 f;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+        return f;
+    }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // Weights of a row: exp((l - max) / temperature) = 2^-t, t = (max - l) c, c = log2 e / temperature.
 // max - l and c are held as sums of two floats, so t is good to 2^-40; it is cut into
 // whole, 1/256ths (a table) and a rest |r| <= 2^-9, whose 2^-r is a short series. Whole
@@ -101,38 +133,60 @@ __constant__ uint64_t kRoots[8] = {0x5a827999fcef3242ull, 0x6ba27e656b4eb57aull,
 struct Weights {
     float top, c, c_low, past;  // past: a distance from the top at which weights are 0
     const uint64_t* table;      // 2^(43 - i / 256)
-    // Twice the weight is the result times 2^-s. Without branches, so that several are on their way.
-    __device__ __forceinline__ uint64_t parts(float l, int& s) const {
+    struct Two {
+        uint64_t of[2];
+        int s[2];
+    };
+    // Twice a weight is the result times 2^-s. Without branches, so that several are on their way, and for two logits
+    // at once, whose floats' steps are one instruction for both.
+    __device__ __forceinline__ Two parts(float l0, float l1) const {
         constexpr float kRound = 12582912.0f;
         constexpr int kRoundBits = 0x4b400000;
-        const float full = top - l;
-        const bool near = full < past;
-        const float d = near ? full : past;
-        const float z = d - top, low = near ? (top - (d - z)) - (l + z) : 0.0f;  // what rounding took from d
-        const float p = d * c;
-        const float q = fmaf(d, c, -p) + fmaf(d, c_low, low * c);
-        const float rounded = fmaf(p, 256.0f, kRound);
-        const int k = __float_as_int(rounded) - kRoundBits;
-        const float r = fmaf(rounded - kRound, -1.0f / 256.0f, p);
         constexpr float kLn2 = 0.693147182464599609375f, kLn2Low = -1.904654299957767e-9f;
-        const float xh = r * kLn2, xl = fmaf(r, kLn2, -xh) + fmaf(r, kLn2Low, q * kLn2), x = xh + xl;
+        const F2 l(l0, l1), t(top), minus(-1.0f);
+        const float2 full = fma(l, minus, t).get();
+        const bool near[2] = {full.x < past, full.y < past};
+        const F2 d(near[0] ? full.x : past, near[1] ? full.y : past);
+        const F2 z = d + F2(-top);
+        // what rounding took from d: (top - (d - z)) - (l + z)
+        const float2 off = fma(l + z, minus, fma(fma(z, minus, d), minus, t)).get();
+        const F2 low(near[0] ? off.x : 0.0f, near[1] ? off.y : 0.0f);
+        const F2 np = d * F2(-c);  // -t, rounded, and what that leaves of t
+        const F2 q = fma(d, F2(c), np) + fma(d, F2(c_low), low * F2(c));
+        const F2 rounded = fma(np, F2(-256.0f), F2(kRound));
+        const F2 nr = fma(rounded + F2(-kRound), F2(1.0f / 256.0f), np);  // -r
+        const F2 xh = nr * F2(-kLn2);
+        // -xl, where the exponent x is xh + xl
+        const F2 nxl = fma(nr, F2(kLn2), xh) + fma(nr, F2(kLn2Low), q * F2(-kLn2));
+        const F2 x = fma(nxl, minus, xh);
         // e^-x - 1 + xh, without its leading -xh; the next term is below 2^-42
-        const float tail = fmaf(x * x, fmaf(x, -1.0f / 6.0f, 0.5f), -xl);
-        const int change = __float_as_int(fmaf(tail, 0x1p39f, kRound)) - kRoundBits - __float2int_rn(xh * 0x1p39f);
-        const uint64_t t = table[k & 255];
-        s = k >> 8;
-        return t + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(t >> 13)) * change) >> 26);
+        const F2 tail = fma(x * x, fma(x, F2(-1.0f / 6.0f), F2(0.5f)), nxl);
+        const float2 small = fma(tail, F2(0x1p39f), F2(kRound)).get(), large = (xh * F2(0x1p39f)).get(), k2 = rounded.get();
+        Two two;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = __float_as_int(i ? k2.y : k2.x) - kRoundBits;
+            const int change = __float_as_int(i ? small.y : small.x) - kRoundBits - __float2int_rn(i ? large.y : large.x);
+            const uint64_t w = table[k & 255];
+            two.s[i] = k >> 8;
+            two.of[i] = w + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(w >> 13)) * change) >> 26);
+        }
+        return two;
+    }
+    __device__ __forceinline__ void of(float l0, float l1, uint64_t& w0, uint64_t& w1) const {
+        const Two two = parts(l0, l1);
+        w0 = ((two.of[0] >> two.s[0]) + 1) >> 1;
+        w1 = ((two.of[1] >> two.s[1]) + 1) >> 1;
     }
     __device__ __forceinline__ uint64_t of(float l) const {
-        int s;
-        const uint64_t w = parts(l, s);
-        return ((w >> s) + 1) >> 1;
+        uint64_t w, again;
+        of(l, l, w, again);
+        return w;
     }
     // A kept token's probability, from its weight before that became a whole number of units.
     __device__ __forceinline__ float share(float l, uint64_t whole) const {
-        int s;
-        const double w = static_cast<double>(parts(l, s));
-        return static_cast<float>(w / (static_cast<double>(2ull << s) * static_cast<double>(whole)));
+        const Two two = parts(l, l);
+        return static_cast<float>(static_cast<double>(two.of[0]) / (static_cast<double>(2ull << two.s[0]) * static_cast<double>(whole)));
     }
 };
 
@@ -206,12 +260,21 @@ constexpr int kPart = 15;
 struct Bins {
     uint32_t count[kBins], part[3][kBins];
 };
+constexpr int kSlots = 8;  // parts of what a lane reads, at most
 struct Shared {
     uint64_t table[256];
-    Bins bins;                // of this CTA, read by its cluster; else room for a list
-    uint64_t sum[kBins];      // all CTAs' bins, added up
-    uint32_t sum_count[kBins];
-    uint64_t list[kFew];      // the leading CTA's: tokens to sort
+    union {
+        struct {
+            Bins bins;            // of this CTA, read by its cluster; else room for a list
+            uint64_t sum[kBins];  // all CTAs' bins, added up
+            uint32_t sum_count[kBins];
+            uint64_t list[kFew];  // the leading CTA's: tokens to sort
+        };
+        struct {  // without cuts
+            float tops[kSlots][kThreadsOf<false>];  // the largest logit of each part of what a lane reads
+            uint16_t hits[kThreadsOf<false> / 32][32 * kSlots];  // a warp's parts with a kept token: part * 32 + lane
+        };
+    };
     uint64_t warp[kWarps];
     uint32_t warp2[kWarps];
     uint64_t before;
@@ -353,34 +416,14 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
         for (int j = 0; j < E::kPer; ++j) E::put(&w, j, at(i + j));
         return w;
     };
-    // A warp has a run of the CTA's logits. f(x, i) for those of [begin, end) from `lowest` on,
-    // by a warp; begin and end are multiples of 8 (past the row's end lies -infinity).
+    // A warp has a run of the CTA's logits; runs begin and end at multiples of 8 (past the row's end lies -infinity).
     const int padded = (n + 7) / 8 * 8, length = ((padded + kWarps - 1) / kWarps + 7) / 8 * 8;
     const int run_begin = min(padded, warp * length), run_end = min(padded, run_begin + length);
     float run_top = -INFINITY;  // its largest
-    auto each = [&](int begin, int end, float lowest, auto f) {
-        for (int i = begin + lane * E::kPer; i < end; i += 32 * E::kPer) {
-            const uint4 w = chunk(i);
-            if (!(largest<kElem>(w) >= lowest)) continue;
-#pragma unroll
-            for (int j = 0; j < E::kPer; ++j) {
-                const float x = E::at(&w, j);
-                if (x >= lowest) f(x, i + j);
-            }
-        }
-    };
-    // f(x, i) for four logits from i on, where one of them is at or above `lowest`
-    auto each_four = [&](int begin, int end, float lowest, auto f) {
-        for (int i = begin + lane * E::kPer; i < end; i += 32 * E::kPer) {
-            const uint4 w = chunk(i);
-            if (!(largest<kElem>(w) >= lowest)) continue;
-#pragma unroll
-            for (int j = 0; j < E::kPer; j += 4) {
-                const float x[4] = {E::at(&w, j), E::at(&w, j + 1), E::at(&w, j + 2), E::at(&w, j + 3)};
-                f(x, i + j);
-            }
-        }
-    };
+    const int vec = a.wide ? min(n, run_end) / E::kPer : 0;  // past the run's last whole 16 bytes
+    constexpr int kAtOnce = kCuts ? 8 : 8;                               // 16 bytes that a lane reads at a time
+    const int batches = (vec - run_begin / E::kPer + 32 * kAtOnce - 1) / (32 * kAtOnce);  // of a warp; none or less: none
+    const int per_slot = max(1, (batches + kSlots - 1) / kSlots);
     int turn = 0;  // of the exchanges: a number is stored again only after a further meeting of the cluster
     // This CTA's numbers to the others: by the first warp, a CTA a lane. Then the cluster meets, and
     // warps read a CTA a lane, and join them.
@@ -390,8 +433,75 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
         turn ^= 1;
     };
     auto given_by = [&](int r) -> const Exchange& { return sh.exchange[turn ^ 1][r]; };
+    constexpr float kLowest = -3.402823466e38f;  // what can be drawn is finite
+    // f(16 bytes' logits, i) where one of them may be at or above `lowest`
+    constexpr int kAhead = 4;  // reads that a lane has under way, without cuts (112 us without a choice; with one, 117)
+    auto chunks_of_run = [&](float lowest, auto f) {
+        if (!(run_top >= lowest)) return;
+        int i = run_begin;
+        if (!kCuts && lowest > kLowest) {
+            // the warp shares out what its lanes with a hit have read
+            int hits = 0;
+            for (int slot = 0; slot * per_slot < batches; ++slot) {
+                const bool hit = sh.tops[slot][tid] >= lowest;
+                const uint32_t mask = __ballot_sync(~0u, hit);
+                if (hit) sh.hits[warp][hits + __popc(mask & ((1u << lane) - 1))] = slot * 32 + lane;
+                hits += __popc(mask);
+            }
+            __syncwarp();
+            const int each = per_slot * kAtOnce;                       // reads of a part
+            const uint32_t over = 0xffffffffu / max(1, hits) + 1;  // 2^32 / hits: e * hits < 2^32, so quotients are exact
+            for (int e0 = lane; e0 < hits * each; e0 += 32 * kAhead) {
+                uint4 w[kAhead];
+                int c[kAhead];
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) {
+                    const int e = e0 + 32 * q;
+                    c[q] = vec;
+                    if (e < hits * each) {
+                        const int j = hits == 1 ? e : __umulhi(e, over), h = sh.hits[warp][e - j * hits];
+                        c[q] = run_begin / E::kPer + ((h >> 5) * each + j) * 32 + (h & 31);
+                    }
+                    if (c[q] < vec) w[q] = reinterpret_cast<const uint4*>(from)[c[q]];
+                }
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q)
+                    if (c[q] < vec) f(w[q], c[q] * E::kPer);
+            }
+            __syncwarp();
+            i = max(i, vec * E::kPer);
+        }
+        constexpr int kStep = 32 * E::kPer;
+        if (!kCuts)
+            for (; i + kAhead * kStep <= run_end; i += kAhead * kStep) {
+                uint4 w[kAhead];
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) w[q] = chunk(i + q * kStep + lane * E::kPer);
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) f(w[q], i + q * kStep + lane * E::kPer);
+            }
+        for (i += lane * E::kPer; i < run_end; i += kStep) f(chunk(i), i);
+    };
+    // f(x, i) for four logits from i on, where one of them is at or above `lowest`
+    auto fours_of_run = [&](float lowest, auto f) {
+        chunks_of_run(lowest, [&](const uint4& w, int i) {
+            if (!(largest<kElem>(w) >= lowest)) return;
+#pragma unroll
+            for (int j = 0; j < E::kPer; j += 4) {
+                const float x[4] = {E::at(&w, j), E::at(&w, j + 1), E::at(&w, j + 2), E::at(&w, j + 3)};
+                f(x);
+            }
+        });
+    };
     auto each_of_run = [&](float lowest, auto f) {
-        if (run_top >= lowest) each(run_begin, run_end, lowest, f);
+        chunks_of_run(lowest, [&](const uint4& w, int i) {
+            if (!(largest<kElem>(w) >= lowest)) return;
+#pragma unroll
+            for (int j = 0; j < E::kPer; ++j) {
+                const float x = E::at(&w, j);
+                if (x >= lowest) f(x, i + j);
+            }
+        });
     };
     // the warps' v, a lane of each warp
     auto of_warps = [&](uint64_t v) {
@@ -403,14 +513,14 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     // The largest logit and the range; with cuts the logits come to shared memory on the way.
     float top = -INFINITY, least = INFINITY;
     {
-        const int vec = a.wide ? min(n, run_end) / E::kPer : 0;  // past the run's last whole 16 bytes
         const bool ranged = use_k || use_p;
         auto low = [&](float x) {
             if (x > -INFINITY) least = fminf(least, x);
         };
-        constexpr int kAtOnce = 8;
-        for (int i0 = run_begin / E::kPer + lane; i0 < vec; i0 += kAtOnce * 32) {
+        for (int batch = 0; batch < batches; ++batch) {
+            const int i0 = run_begin / E::kPer + batch * kAtOnce * 32 + lane;
             uint4 v[kAtOnce];
+            float batch_top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j)
                 if (i0 + j * 32 < vec) v[j] = reinterpret_cast<const uint4*>(from)[i0 + j * 32];
@@ -418,11 +528,16 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
             for (int j = 0; j < kAtOnce; ++j)
                 if (i0 + j * 32 < vec) {
                     if constexpr (kCuts) reinterpret_cast<uint4*>(logits)[i0 + j * 32] = v[j];
-                    run_top = max_or_nan(run_top, largest<kElem>(v[j]));
+                    batch_top = max_or_nan(batch_top, largest<kElem>(v[j]));
                     if (ranged)
 #pragma unroll
                         for (int q = 0; q < E::kPer; ++q) low(E::at(&v[j], q));
                 }
+            run_top = max_or_nan(run_top, batch_top);
+            if constexpr (!kCuts) {
+                float& slot_top = sh.tops[batch / per_slot][tid];
+                slot_top = batch % per_slot ? max_or_nan(slot_top, batch_top) : batch_top;
+            }
         }
         for (int i = max(run_begin, vec * E::kPer) + lane; i < run_end; i += 32) {
             const float x = i < n ? E::at(from, i) : -INFINITY;
@@ -507,7 +622,6 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     // from the whole measure; with may_list, tokens up to the first bin's end are
     // only listed where they are few.
     uint64_t target = 0;
-    constexpr float kLowest = -3.402823466e38f;  // what can be drawn is finite
     Cut cut{-INFINITY, 0, 0};  // everything
     // This CTA's tokens that are wanted go where the bins are; room for kFew. sh.collected is 0 before.
     uint64_t* const staged = reinterpret_cast<uint64_t*>(&sh.bins);
@@ -545,26 +659,28 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
                 if (level == 0) return b;
                 return b != static_cast<int>(base) ? -1 : min(kBins - 1, static_cast<int>((bin_of(x) - base) * kBins));
             };
-            if (run_top >= floor)
-                each_four(run_begin, run_end, floor, [&](const float (&x)[4], int) {
-                    int b[4];
-                    uint64_t m[4];
+            fours_of_run(floor, [&](const float (&x)[4]) {
+                int b[4];
+                uint64_t m[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        b[q] = x[q] >= floor ? place(x[q]) : -1;
-                        m[q] = 1;
-                        if constexpr (kWeigh) m[q] = w.of(x[q]);
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    b[q] = x[q] >= floor ? place(x[q]) : -1;
+                    m[q] = 1;
+                }
+                if constexpr (kWeigh) {
+                    w.of(x[0], x[1], m[0], m[1]);
+                    w.of(x[2], x[3], m[2], m[3]);
+                }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (b[q] < 0 || m[q] == 0) continue;
-                        if constexpr (kWeigh)
+                for (int q = 0; q < 4; ++q) {
+                    if (b[q] < 0 || m[q] == 0) continue;
+                    if constexpr (kWeigh)
 #pragma unroll
-                            for (int j = 0; j < 3; ++j)
-                                atomicAdd(&bins.part[j][b[q]], static_cast<uint32_t>(m[q] >> kPart * j) & (1u << kPart) - 1);
-                        atomicAdd(&bins.count[b[q]], 1u);
-                    }
-                });
+                        for (int j = 0; j < 3; ++j)
+                            atomicAdd(&bins.part[j][b[q]], static_cast<uint32_t>(m[q] >> kPart * j) & (1u << kPart) - 1);
+                    atomicAdd(&bins.count[b[q]], 1u);
+                }
+            });
             cluster.sync();
             // A CTA adds up its share of the bins, a thread a bin of one of the CTAs, and stores the sums in all.
             uint64_t v = 0;
@@ -844,27 +960,28 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     if (least_kept > cut.at) cut = Cut{-INFINITY, 0, 0};
     // The kept weight, by warps, each of which has a run of the CTA's logits, and over the cluster.
     const float lowest = fmaxf(fmaxf(cut.at, least_kept), kLowest);
-    auto weigh = [&](int begin, int end, uint64_t& mass, uint32_t& ties) {
-        mass = 0;
-        ties = 0;
-        each_four(begin, end, lowest, [&](const float (&x)[4], int) {
-            uint64_t m[4];
+    auto weigh_chunk = [&](const uint4& v, uint64_t& mass, uint32_t& ties) {
+        if (!(largest<kElem>(v) >= lowest)) return;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) m[q] = w.of(x[q]);
+        for (int j = 0; j < E::kPer; j += 4) {
+            const float x[4] = {E::at(&v, j), E::at(&v, j + 1), E::at(&v, j + 2), E::at(&v, j + 3)};
+            uint64_t m[4];
+            w.of(x[0], x[1], m[0], m[1]);
+            w.of(x[2], x[3], m[2], m[3]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const bool tied = cut.ties && x[q] == cut.at;
                 ties += tied;
                 mass += x[q] >= lowest && !tied ? m[q] : 0;
             }
-        });
-        mass = warp_reduce(mass, add<uint64_t>);
-        ties = __reduce_add_sync(~0u, ties);
+        }
     };
     const uint64_t tie = cut.ties ? w.of(cut.at) : 0;
     uint64_t mass = 0;
     uint32_t ties = 0;
-    if (run_top >= lowest) weigh(run_begin, run_end, mass, ties);
+    chunks_of_run(lowest, [&](const uint4& v, int) { weigh_chunk(v, mass, ties); });
+    mass = warp_reduce(mass, add<uint64_t>);
+    ties = __reduce_add_sync(~0u, ties);
     // What precedes, of this lane's value in its warp: (mass, ties) in the vocabulary's order, of which only the
     // first `left` ties count.
     struct Before {
@@ -902,23 +1019,28 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     Before b = line_up(lane < ctas ? given_by(lane).mass : 0, lane < ctas ? given_by(lane).ties : 0, 0, cut.ties);
     const uint64_t whole = __shfl_sync(~0u, b.start + b.mass, 31), goal = point(whole);
     if (pick(b, goal) != rank) return;
-    // The run with it, its 16th part, and the token.
+    // The run with it, a thread's share of that run, and the token.
     b = line_up(lane < kWarps ? sh.warp[lane] : 0, lane < kWarps ? sh.warp2[lane] : 0, b.start, b.left);
     const int run = pick(b, goal), begin = run * length, end = min(padded, begin + length);
-    const int sub = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
-    weigh(min(end, begin + warp * sub), min(end, begin + (warp + 1) * sub), mass, ties);
+    const int part = ((end - begin + kThreads - 1) / kThreads + 7) / 8 * 8, mine = begin + tid * part;
+    uint64_t of_part = 0;
+    uint32_t ties_of_part = 0;
+    for (int i = mine; i < min(end, mine + part); i += E::kPer) weigh_chunk(chunk(i), of_part, ties_of_part);
+    mass = warp_reduce(of_part, add<uint64_t>);
+    ties = __reduce_add_sync(~0u, ties_of_part);
     __syncthreads();
     if (lane == 0) {
         sh.warp[warp] = mass;
         sh.warp2[warp] = ties;
     }
     __syncthreads();
-    if (warp != 0) return;
     b = line_up(lane < kWarps ? sh.warp[lane] : 0, lane < kWarps ? sh.warp2[lane] : 0, b.start, b.left);
-    const int part = pick(b, goal);
-    for (int i0 = begin + part * sub; i0 < min(end, begin + (part + 1) * sub); i0 += 32) {
+    if (pick(b, goal) != warp) return;
+    b = line_up(of_part, ties_of_part, b.start, b.left);
+    const int from_here = begin + (warp * 32 + pick(b, goal)) * part, to_here = min(end, from_here + part);
+    for (int i0 = from_here; i0 < to_here; i0 += 32) {
         const int i = i0 + lane;
-        const float x = i < min(end, begin + (part + 1) * sub) ? at(i) : -INFINITY;
+        const float x = i < to_here ? at(i) : -INFINITY;
         const bool tied = cut.ties && x == cut.at;
         Before c = line_up(!tied && x >= lowest ? w.of(x) : 0, tied, b.start, b.left);
         const uint32_t over = __ballot_sync(~0u, c.start + c.mass > goal);
