@@ -211,6 +211,13 @@ def _stream(stream=None, device=None):
     return stream
 
 
+def _current(stream, device: torch.device):
+    """`stream` as the current one: what is allocated meanwhile belongs to it, so that its
+    memory is not another stream's still, and not reused before the stream is done."""
+    handle = _stream(stream, device)
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device))
+
+
 _SAME_DEVICE = contextlib.nullcontext()
 
 
@@ -910,7 +917,10 @@ def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch
     fp32 the keys, and q [T, Hq, dim], are rotated by position; returns the rotated
     queries (q_out, which may be q). A token with a negative position is skipped;
     one without a valid page is not stored and its queries become NaNs."""
-    if _fast is not None and stream is None and (q_out is not None or q is None):
+    if stream is not None:
+        with _current(stream, cache.device):
+            return kv_append(cache, k, v, positions, table, rows, q, inv_freq, interleaved, q_out)
+    if _fast is not None and (q_out is not None or q is None):
         st = _fast.kv_append(cache._address, cache._index, k, v, positions, table, rows, q, inv_freq, interleaved, q_out)
         if st == 0:
             return q_out
@@ -954,7 +964,7 @@ def kv_append(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, positions: torch
     _kv_run("estream_kv_append", index, (
         cache._ref, elem, T, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _kv_ints(positions, T, "positions", cache),
         None if rows is None else _kv_ints(rows, T, "rows", cache), tp, B, M, table_row, qp, q0, q1, Hq, op, o0, o1,
-        fp, rot, 1 if interleaved else 0, _stream(stream, cache.device)))
+        fp, rot, 1 if interleaved else 0, _stream(None, cache.device)))
     return q_out
 
 
@@ -968,7 +978,10 @@ def kv_attend(cache: PagedKV, q: torch.Tensor, table: torch.Tensor, lens: torch.
     that share a sequence (the tokens of a prompt) may share a table row
     (table.expand). workspace: uint8, cache.attend_workspace_bytes(B, Hq, M,
     window) of them, for this call alone until it ends (allocated when not given)."""
-    if _fast is not None and stream is None and out is not None:
+    if stream is not None:
+        with _current(stream, cache.device):
+            return kv_attend(cache, q, table, lens, scale, window, out, lse, workspace)
+    if _fast is not None and out is not None:
         st = _fast.kv_attend(cache._address, cache._index, q, table, lens, cache._scale if scale is None else scale, window,
                              out, lse, workspace)
         if st == 0:
@@ -1009,7 +1022,7 @@ def kv_attend(cache: PagedKV, q: torch.Tensor, table: torch.Tensor, lens: torch.
         wp = workspace.data_ptr()
     _kv_run("estream_kv_attend", index, (
         cache._ref, elem, B, Hq, q.data_ptr(), q0, q1, tp, M, table_row, _kv_ints(lens, B, "lens", cache),
-        cache._scale if scale is None else scale, window, out.data_ptr(), o0, o1, ep, wp, n, _stream(stream, cache.device)))
+        cache._scale if scale is None else scale, window, out.data_ptr(), o0, o1, ep, wp, n, _stream(None, cache.device)))
     return out
 
 
@@ -1035,7 +1048,10 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=
     order whose cumulative probability exceeds u, and its probability goes to
     prob [B] fp32. Temperature 0 takes the largest logit. Each choice is a number or a
     tensor [B] (fp32; top_k int32). A row without a finite largest logit gives -1."""
-    if _fast is not None and stream is None and out is not None:
+    if stream is not None and logits.is_cuda:
+        with _current(stream, logits.device):
+            return sample_tokens(logits, u, temperature, top_k, top_p, min_p, out, prob)
+    if _fast is not None and out is not None:
         st = _fast.sample(logits.get_device(), logits, u, temperature, top_k, top_p, min_p, out, prob)
         if st == 0:
             return out
@@ -1066,7 +1082,7 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=
     pp = None if prob is None else _choice(prob, B, torch.float32, "prob", dev)[1]
     with _on(logits):
         st = lib().estream_sample_tokens(logits.data_ptr(), elem, ld, B, V, up, *choices, out.data_ptr(), pp,
-                                         _stream(stream, dev))
+                                         _stream(None, dev))
     if st:
         _check(st, "estream_sample_tokens")
     return out
