@@ -363,7 +363,7 @@ __device__ __forceinline__ void sort(Shared& sh, int n) {
     __syncthreads();
 }
 
-// kCuts: some row may have a top-k or a top-p. Without, logits are read again where a run's largest
+// kCuts: some row may have a top-k or a top-p. Without, logits are read again where a part's largest
 // allows a kept token, out of L2, and a row needs no shared memory, so that more rows are under way.
 template <int kElem, bool kCuts>
 __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k_sample(const Sample a) {
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     float run_top = -INFINITY;  // its largest
     // the run's whole 16 bytes are [vec_begin, vec)
     const int vec_begin = run_begin / E::kPer + (run_begin < skew), vec = kCuts && past16 ? 0 : min(n, run_end) / E::kPer;
-    constexpr int kAtOnce = kCuts ? 8 : 8;                               // 16 bytes that a lane reads at a time
+    constexpr int kAtOnce = 8;  // 16 bytes that a lane reads at a time
     const int batches = (vec - vec_begin + 32 * kAtOnce - 1) / (32 * kAtOnce);  // of a warp; none or less: none
     const int per_slot = max(1, (batches + kSlots - 1) / kSlots);
     int turn = 0;  // of the exchanges: a number is stored again only after a further meeting of the cluster
