@@ -245,10 +245,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kHalves ? 3 : 4) k_kv_appen
                     if constexpr (kRotated) form_angles();
                     if (turns) {
 #pragma unroll
-                        for (int q = 0; q < kPairs; ++q) {
-                            cs[q] = make_float2(1.0f, 0.0f);
-                            if (j * kPairs + q < pairs) cs[q] = turn[warp][j * kPairs + q];
-                        }
+                        for (int q = 0; q < kPairs; ++q) cs[q] = turn[warp][j * kPairs + q];  // past the last pair: not used
                     }
                     if (kCached && !ok) return;
                 }
@@ -286,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, kMode == kHalves ? 3 : 4) k_kv_appen
                             } else {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
+                                    // pairs behind the rotated ones stay as they are: by (1, 0), an infinity's neighbour would be NaN
+                                    if (j * kPairs + e >= pairs) continue;
                                     const float2 c = cs[e % kPairs];
                                     const float lo = x.x[2 * e] * c.x - x.x[2 * e + 1] * c.y;
                                     x.x[2 * e + 1] = x.x[2 * e + 1] * c.x + x.x[2 * e] * c.y;
