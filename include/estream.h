@@ -602,7 +602,7 @@ typedef struct {
  *          (a, b) -> (a cos - b sin, b cos + a sin), where the pair is (i, i + rot / 2),
  *          or with `interleaved` (2i, 2i + 1). The angle is reduced to one turn
  *          in 64-bit integers, so far positions keep theirs; sums in fp32,
- *          rounded once. E4M3 elements are x * fl(1 / scale), at most 448 in
+ *          rounded once. An infinite or NaN inv_freq makes its pair NaN. E4M3 elements are x * fl(1 / scale), at most 448 in
  *          magnitude; NaN stays NaN.
  */
 estream_status estream_kv_append(const estream_kv_cache* cache, int elem, int T,

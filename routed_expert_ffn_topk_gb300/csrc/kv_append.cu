@@ -108,7 +108,7 @@ __device__ __forceinline__ void keep1(void* base, long long at, float x, float i
     else static_cast<uint16_t*>(base)[at] = down1<kF16>(x);
 }
 
-// f / 2 pi turns, 64 fractional bits, rounded down. In integers below 2: with double's
+// f / 2 pi turns, 64 fractional bits, rounded down, of a finite f (of others: any). In integers below 2: with double's
 // operations, of which an SM does two a clock, 4096 tokens took 5 us longer.
 __device__ __forceinline__ uint64_t turns_of(float f) {
     const uint32_t u = __float_as_uint(f), e = u >> 23 & 0xff;
@@ -121,7 +121,7 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
         const uint32_t s = 174 - max(e, 1u);  // 47 for the largest
         w = s < 64 ? high << (64 - s) | low >> s : s < 128 ? high >> (s - 64) : 0;
     } else {
-        double turns = static_cast<double>(fabsf(f)) * 0.15915494309189533577;
+        double turns = static_cast<double>(fminf(fabsf(f), 3.402823466e38f)) * 0.15915494309189533577;
         turns -= floor(turns);
         w = static_cast<uint64_t>(turns * 18446744073709551616.0);
     }
@@ -189,18 +189,19 @@ __global__ void __launch_bounds__(kThreads, kMode == kHalves ? 3 : 4) k_kv_appen
     int page = -1;
     if (row >= 0 && row < a.B && entry < a.M) page = a.table[row * a.table_row + entry];
     const bool ok = page >= 0 && page < a.num_pages;
+    const float nan = __int_as_float(0x7fc00000);
     bool formed = false;
     auto form_angles = [&] {  // once the first values are under way
         if (formed) return;
         formed = true;
         for (int p = lane; p < pairs; p += 32) {
-            const uint64_t angle = turns_of(a.inv_freq[p]) * static_cast<uint64_t>(pos);
-            turn[warp][p] = cos_sin(static_cast<uint32_t>((angle + 0x80000000u) >> 32));
+            const float f = a.inv_freq[p];
+            const uint64_t angle = turns_of(f) * static_cast<uint64_t>(pos);
+            turn[warp][p] = fabsf(f) < INFINITY ? cos_sin(static_cast<uint32_t>((angle + 0x80000000u) >> 32)) : make_float2(nan, nan);
         }
         __syncwarp();
     };
     int steps = 0;  // of the kinds of heads before; the parts of a token take turns at all of them
-    const float nan = __int_as_float(0x7fc00000);
     // The heads of one kind: from `from` (of this token), heads from_head elements apart, to `to`,
     // to_head bytes apart; into the cache, or as queries.
     auto go = [&](auto rotated, auto cached, int heads, int per_head, const void* from, long long from_head, void* to,

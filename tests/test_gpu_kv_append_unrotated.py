@@ -1,4 +1,5 @@
-"""What the rotation leaves as it is: values behind the rotated part, whatever stands beside them."""
+"""What the rotation leaves as it is: values behind the rotated part, whatever stands beside them; and pairs
+whose frequency is no number."""
 import pytest
 import torch
 
@@ -48,3 +49,20 @@ def test_unrotated_values(interleaved, kind, dim, rot, off):
         want = want.float().clamp(-448.0, 448.0)
     assert _same(k[..., rot:], want) and _same(v[..., rot:], want)
     assert bool(q[..., :rot].isfinite().all()) and bool(k[..., :rot].float().isfinite().all())
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot", [(64, 64), (64, 20), (128, 64)])
+def test_frequencies_that_are_no_numbers(interleaved, dim, rot):
+    """An infinite or NaN frequency makes its pair NaN, as sine and cosine of it are, and leaves the others."""
+    x = torch.randn(4, 2, dim, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    f = torch.full((rot // 2,), 0.3, device="cuda")
+    k0, _, q0 = (t.clone() for t in _append(x, dim, rot, "bf16", interleaved, f))
+    for j, bad in ((0, float("inf")), (rot // 2 - 1, float("nan")), (3, -float("inf"))):
+        f[j] = bad
+    k, _, q = _append(x, dim, rot, "bf16", interleaved, f)
+    hit = torch.zeros(dim, dtype=torch.bool, device="cuda")
+    for j in (0, 3, rot // 2 - 1):
+        hit[[2 * j, 2 * j + 1] if interleaved else [j, j + rot // 2]] = True
+    for got, plain in ((k, k0), (q, q0)):
+        assert bool(got[..., hit].isnan().all()) and torch.equal(got[..., ~hit], plain[..., ~hit])
