@@ -665,7 +665,7 @@ enum { ESTREAM_SAMPLE_MAX_V = 393216 };
  *   2. of these, by falling logit (equal ones: the lowest index first), those
  *      before which less than top_p of their weight lies; the first always;
  *      top_p >= 1: all;
- *   3. of these, those with w_i >= min_p (the largest always);
+ *   3. of these, those with w_i >= min_p (the first of 2. always);
  *   ids[b] is the first i in the vocabulary's order at which the kept weight up
  *   to and with i exceeds u[b] times the kept weight; prob[b] = w_i / that weight.
  * Weights are held to 2^-37 of themselves or 2^-42 of the largest and summed as

@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     const int top_k = a.top_ks ? a.top_ks[row] : a.top_k;
     const float top_p = a.top_ps ? a.top_ps[row] : a.top_p;
     const float min_p = a.min_ps ? a.min_ps[row] : a.min_p;
-    const bool greedy = !(temperature > 0x1p-100f);
+    // a min-p above 1 leaves the first largest logit, too
+    const bool greedy = !(temperature > 0x1p-100f) || min_p > 1.0f;
     const bool use_p = kCuts && !(top_p >= 1.0f);
     const bool use_k = kCuts && top_k > 0 && top_k < a.V;
     // in 64 bits by one thread: an SM does two such operations a clock
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
         const uint64_t p = __float2ull_rz(top_p * 0x1p64f);
         return __umul64hi(p, whole) + (p * whole != 0);
     };
-    // w >= min_p as a smallest logit: max + temperature ln(min_p), and the largest always
+    // w >= min_p as a smallest logit: max + temperature ln(min_p)
     float least_kept = -INFINITY;
     if (min_p > 0.0f) {
         least_kept = top;
