@@ -668,9 +668,10 @@ enum { ESTREAM_SAMPLE_MAX_V = 393216 };
  *   3. of these, those with w_i >= min_p (the first of 2. always);
  *   ids[b] is the first i in the vocabulary's order at which the kept weight up
  *   to and with i exceeds u[b] times the kept weight; prob[b] = w_i / that weight.
- * Weights are held to 2^-37 of themselves or 2^-42 of the largest and summed as
- * integers, so ids are those of exact arithmetic but where u or a border lies
- * within about 1e-12 of the kept weight, and a call repeats bit for bit.
+ * Weights are held to 2^-37 of themselves, rounded to units of 2^-45 of the largest
+ * (less than half a unit: 0) and summed as integers. So ids are those of exact
+ * arithmetic but where u, or top_p, lies within 2^-36 + V * 2^-46 (at most 5.6e-9) of
+ * the share of the weight at which the answer changes; and a call repeats bit for bit.
  * logits   device, [B][V] of `elem` (ESTREAM_MX4_BF16, _F16 or _F32), rows ld >= 0
  *          elements apart (0: one row for all), aligned to their type; -infinity:
  *          never drawn.

@@ -4,8 +4,10 @@
 //
 // Which token that is has to be what exact arithmetic says: with 10^5 tokens a
 // cumulative weight that is off by 1e-7 names another one in a row of a hundred. So
-// weights are integers, 2^42 for the largest, within 2^-37 of their value or one unit, and
-// their sums are exact and the same in every order.
+// weights are integers, 2^45 for the largest, within 2^-37 of their value and half a unit, and
+// their sums are exact and the same in every order. 2^45 is the most that 2^18.6 tokens
+// leave 64 bits: half units add up to V 2^-46 of the largest weight where tokens far
+// below it share one logit, at most 5.6e-9 (with 2^42, 4.5e-8 and a wrong token where u lay that near).
 //
 // A cluster of CTAs goes over a row in passes, between which the CTAs exchange a few numbers. Where a
 // row may have a cut, it holds the row's logits in its shared memory, so they are read from HBM once.
@@ -50,7 +52,8 @@ constexpr int kThreadsOf = kCuts ? kThreads : 256;  // without cuts: four CTAs a
 constexpr int kBins = kThreads;  // one a thread
 constexpr int kMaxCtas = 8;      // of a cluster
 constexpr int kFew = 2 * kThreads;  // tokens that one CTA sorts
-constexpr int kOne = 42;         // log2 of the largest weight
+constexpr int kOne = 45;         // log2 of the largest weight
+static_assert(ESTREAM_SAMPLE_MAX_V <= ~0ull >> kOne, "sums stay below 2^64");
 
 struct Sample {
     const void* logits;
@@ -131,7 +134,7 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 // go through a unit of a quarter of the rate.
 struct Weights {
     float top, c, c_low, past;  // past: a distance from the top at which weights are 0
-    const uint64_t* table;      // 2^(43 - i / 256)
+    const uint64_t* table;      // 2^(kOne + 1 - i / 256)
     struct Two {
         uint64_t of[2];
         int s[2];
@@ -168,7 +171,7 @@ struct Weights {
             const int change = __float_as_int(i ? small.y : small.x) - kRoundBits - __float2int_rn(i ? large.y : large.x);
             const uint64_t w = table[k & 255];
             two.s[i] = k >> 8;
-            two.of[i] = w + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(w >> 13)) * change) >> 26);
+            two.of[i] = w + static_cast<uint64_t>((static_cast<long long>(static_cast<int>(w >> (kOne - 29))) * change) >> (68 - kOne));
         }
         return two;
     }
@@ -252,10 +255,11 @@ struct Exchange {
     Cut cut;
 };
 
-// A bin's measure: the number of its tokens, and their weight in three parts of 15 bits,
-// which native 32-bit atomics add up (an SM has none of 64 bits on shared memory, and loops instead: bins of
+// A bin's measure: the number of its tokens, and their weight in three parts of 16 bits (a CTA has fewer than 2^16
+// logits, so a part's sum stays in 32 bits), which native 32-bit atomics add up (an SM has none of 64 bits on shared memory, and loops instead: bins of
 // 32000 logits took 11 us).
-constexpr int kPart = 15;
+constexpr int kPart = 16;
+static_assert(3 * kPart > kOne, "the largest weight fits its parts");
 struct Bins {
     uint32_t count[kBins], part[3][kBins];
 };
