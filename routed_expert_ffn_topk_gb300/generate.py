@@ -151,11 +151,28 @@ class TokenLoop:
         self.stack.decode_from_x(0, X, self.W_r, Y, residual=X)
         return self.project(Y, u)
 
+    def numbers(self, u: torch.Tensor | None, n: int, b: int) -> torch.Tensor | None:
+        """The random numbers of n tokens of b sequences: u [n, b] when sampling, else none."""
+        if self.sampling is None:
+            return None
+        if not isinstance(u, torch.Tensor) or tuple(u.shape) != (n, b):
+            raise ValueError(f"sampling needs random numbers [{n}, {b}]")
+        return u
+
+    def _as_captured(self, ids: torch.Tensor) -> bool:
+        """Whether the captured step is for as many sequences and the present choices."""
+        if self.graph is None or self.ids.shape != ids.shape or (self.choices is None) != (self.sampling is None):
+            return False
+        same = lambda x, y: x is y or not (torch.is_tensor(x) or torch.is_tensor(y)) and x == y
+        return self.choices is None or (self.choices.keys() == self.sampling.keys()
+                                        and all(same(x, self.sampling[k]) for k, x in self.choices.items()))
+
     def run(self, ids: torch.Tensor, n: int, u: torch.Tensor | None = None) -> torch.Tensor:
         """The n tokens after ids [b] of every sequence, [b, n]; u [n, b] random numbers when sampling."""
-        if self.graph is None or self.ids.shape != ids.shape:
-            self.ids = ids.clone()
-            self.u = None if u is None else torch.zeros_like(u[0])
+        u = self.numbers(u, n, ids.shape[0])
+        if not self._as_captured(ids):
+            self.ids, self.choices = ids.clone(), None if self.sampling is None else dict(self.sampling)
+            self.u = None if u is None else torch.zeros(ids.shape, dtype=torch.float32, device=ids.device)
             lens = None if self.attention is None else self.attention.lens.clone()
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
@@ -206,10 +223,7 @@ def generate(cfg, experts: Mx4Experts, loop: TokenLoop, prompt: torch.Tensor, n:
     """prompt [b, m] token ids; the n tokens after it, [b, n]; u [n, b] random numbers when sampling."""
     if loop.attention is not None and prompt.shape[1] + n - 1 > loop.attention.max_tokens:
         raise ValueError(f"the attention layer holds {loop.attention.max_tokens} tokens a sequence")
-    if loop.sampling is not None and (u is None or tuple(u.shape) != (n, prompt.shape[0])):
-        raise ValueError(f"sampling needs random numbers [{n}, {prompt.shape[0]}]")
-    if loop.sampling is None:
-        u = None
+    u = loop.numbers(u, n, prompt.shape[0])
     X = loop.attend(loop.embedding[prompt.reshape(-1)], prompt.shape[1])
     logits = es.router_logits(X, loop.W_r)
     Y = X.float() + experts.prefill(X, logits, cfg.k, cfg.renorm)
