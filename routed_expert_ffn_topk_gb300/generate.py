@@ -84,8 +84,24 @@ class PagedAttention:
         self.cache = es.PagedKV(pages[0], pages[1])
         # an allocator hands pages out as sequences grow; here each has its own from the start
         self.table = torch.arange(batch * M, dtype=torch.int32, device=device).view(batch, M)
-        self.max_tokens, self.lens = max_tokens, torch.zeros(batch, dtype=torch.int32, device=device)
+        self.max_tokens, self._lens = max_tokens, torch.zeros(batch, dtype=torch.int32, device=device)
+        self._held = 0  # the longest sequence's tokens, as far as the host knows; None: ask the device
         self.inv_freq = (base ** (-torch.arange(0, self.dim, 2, dtype=torch.float64) / self.dim)).float().to(device)
+
+    @property
+    def lens(self) -> torch.Tensor:
+        """The sequences' tokens, [batch] int32. A caller may set them (back, to give up tokens)."""
+        self._held = None
+        return self._lens
+
+    def reserve(self, n: int) -> int:
+        """Refuses n more tokens than every sequence has room for; the longest one's tokens. The device is asked
+        only where a caller may have changed the lengths, or before a refusal."""
+        if self._held is None or self._held + n > self.max_tokens:
+            self._held = int(self._lens.max())
+        if self._held + n > self.max_tokens:
+            raise ValueError(f"the attention layer holds {self.max_tokens} tokens a sequence: no room for {n} behind {self._held}")
+        return self._held
 
     def _project(self, x: torch.Tensor, w: es.Mx4Weights) -> torch.Tensor:
         return es.mx4_product(es.mx4_quantize(x, self.fmt, self.act_scale), w)
@@ -106,14 +122,18 @@ class PagedAttention:
         positions = torch.arange(m, dtype=torch.int32, device=X.device).repeat(self.batch)
         rows = torch.arange(self.batch, dtype=torch.int32, device=X.device).repeat_interleave(m)
         y = self._attend(X, positions, positions + 1, self.table.repeat_interleave(m, 0), rows)
-        self.lens.fill_(m)
+        self._lens.fill_(m)
+        self._held = m
         return y
 
     def step(self, X: torch.Tensor) -> torch.Tensor:
-        """X [batch, H], the next token of every sequence."""
-        after = self.lens + 1
-        y = self._attend(X, self.lens, after, self.table, None)
-        self.lens.copy_(after)
+        """X [batch, H], the next token of every sequence. Where it is captured, whoever replays it reserves the tokens."""
+        held = None if torch.cuda.is_current_stream_capturing() else self.reserve(1)
+        after = self._lens + 1
+        y = self._attend(X, self._lens, after, self.table, None)
+        self._lens.copy_(after)
+        if held is not None:
+            self._held = held + 1
         return y
 
 
@@ -170,20 +190,25 @@ class TokenLoop:
     def run(self, ids: torch.Tensor, n: int, u: torch.Tensor | None = None) -> torch.Tensor:
         """The n tokens after ids [b] of every sequence, [b, n]; u [n, b] random numbers when sampling."""
         u = self.numbers(u, n, ids.shape[0])
+        held = None if self.attention is None else self.attention.reserve(n)
+        if n == 0:
+            return ids[:, None][:, :0]
         if not self._as_captured(ids):
             self.ids, self.choices = ids.clone(), None if self.sampling is None else dict(self.sampling)
             self.u = None if u is None else torch.zeros(ids.shape, dtype=torch.float32, device=ids.device)
-            lens = None if self.attention is None else self.attention.lens.clone()
+            lens = None if self.attention is None else self.attention._lens.clone()
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
             with torch.cuda.stream(side):
                 self.step(self.ids, self.u)  # allocations and first-call work outside the capture
             torch.cuda.current_stream().wait_stream(side)
             if lens is not None:
-                self.attention.lens.copy_(lens)  # the next step stores its token in that one's place
+                self.attention._lens.copy_(lens)  # the next step stores its token in that one's place
             self.graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(self.graph):
                 self.ids.copy_(self.step(self.ids, self.u))
+        if held is not None:
+            self.attention._held = None  # until all n are held
         self.ids.copy_(ids)
         out = torch.empty(ids.shape[0], n, dtype=ids.dtype, device=ids.device)
         for i in range(n):
@@ -191,6 +216,8 @@ class TokenLoop:
                 self.u.copy_(u[i])
             self.graph.replay()
             out[:, i] = self.ids
+        if held is not None:
+            self.attention._held = held + n
         return out
 
 

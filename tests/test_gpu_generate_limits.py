@@ -1,5 +1,5 @@
 """What the token loop refuses and follows: random numbers that are missing or of another shape, and choices that
-change."""
+change; and its attention's end."""
 import pytest
 import torch
 
@@ -46,5 +46,39 @@ def test_other_choices_than_captured():
         loop.sampling = None
         assert torch.equal(G.generate(cfg, experts, loop, prompt, 7), likeliest)
         assert torch.equal(G.generate(cfg, experts, loop, prompt, 7, u), likeliest)  # no use for u
+    finally:
+        loop.stack.close()
+
+
+def test_tokens_past_the_end():
+    from routed_expert_ffn_topk_gb300 import generate as G
+    cfg, experts, loop = _build(tokens=20)
+    try:
+        a = loop.attention
+        prompt = torch.randint(0, 500, (3, 10), generator=torch.Generator().manual_seed(7)).cuda()
+        ids = G.generate(cfg, experts, loop, prompt, 6)  # holds 15
+        with pytest.raises(ValueError):
+            loop.run(ids[:, -1], 6)
+        assert a.lens.tolist() == [15] * 3
+        more = loop.run(ids[:, -1], 5)
+        assert int(more.min()) >= 0 and a.lens.tolist() == [20] * 3
+        X = torch.zeros(3, cfg.H, dtype=torch.bfloat16, device="cuda")
+        for call in (lambda: loop.run(more[:, -1], 1), lambda: loop.step(more[:, -1]), lambda: a.step(X)):
+            with pytest.raises(ValueError):
+                call()
+        assert a.lens.tolist() == [20] * 3
+        # a caller that sets the lengths back has the room again, by whichever reference
+        lens = a.lens
+        lens.fill_(19)
+        a.step(X)
+        with pytest.raises(ValueError):
+            a.step(X)
+        lens.fill_(18)
+        a.step(X)
+        # one long sequence is enough for a refusal
+        a.lens.copy_(torch.tensor([3, 20, 4], dtype=torch.int32))
+        with pytest.raises(ValueError):
+            a.step(X)
+        assert torch.equal(G.generate(cfg, experts, loop, prompt, 6), ids)
     finally:
         loop.stack.close()
