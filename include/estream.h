@@ -639,7 +639,10 @@ size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, i
  *          window) bytes, used by this call alone until it ends (no initial value);
  *          may be NULL where that is 0.
  * Cache positions that are not attended (past the end, before the window, other
- * pages) may hold anything; an infinite value that is attended gives NaN. Products and sums in fp32; weights are kept to 16
+ * pages) may hold anything. A score of +infinity or NaN makes its head's row and lse NaN; an
+ * infinite element of v that is attended makes its column of the heads that meet it
+ * infinite or NaN (a weight's second term may be 0 or negative), and nothing else.
+ * Products and sums in fp32; weights are kept to 16
  * bits for bf16 values and to 11 for the others. M * page_size < 2^31 - 4096, B *
  * Hq at most 2^24. A call repeats bit for bit on one kind of device.
  */
