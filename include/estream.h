@@ -42,6 +42,9 @@
 #ifndef ESTREAM_H
 #define ESTREAM_H
 
+/* What estream_version returns: major * 10000 + minor * 100 + patch. */
+#define ESTREAM_VERSION 10401
+
 #include <stddef.h>
 #include <stdint.h>
 

@@ -3,7 +3,8 @@
 Compiles each CUDA translation unit in parallel (one -gencode, no fast-math)
 and links them with the shared CUDA runtime into
 ``routed_expert_ffn_topk_gb300/libestream.so``, and the compiled part of the
-binding (plain C, Python's own headers) into ``_binding.so``.
+binding (plain C, Python's own headers) into ``_binding`` with this interpreter's
+suffix.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libestream.so")
-BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_PATH = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["route.cu", "route_static.cu", "expert_gemm.cu", "expert_f32.cu", "runtime.cu",
            "pipeline_model.cu", "router.cu", "decode.cu", "mx4.cu", "mx4_product.cu", "kv_append.cu",
            "kv_attend.cu", "sample.cu"]
@@ -45,6 +46,36 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _compile(cmd, verbose: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+
+
+def build_binding(path: str = BINDING_PATH, python_include: str | None = None, force: bool = False,
+                  verbose: bool = False) -> None:
+    """The compiled part of the binding; without Python's headers there is none, and the binding takes its
+    interpreted way alone. What an import would find in its stead (a file without this interpreter's tag, or of an
+    older source) is removed."""
+    python_include = sysconfig.get_paths()["include"] if python_include is None else python_include
+    source = os.path.join(CSRC, "binding.c")
+    untagged = os.path.join(os.path.dirname(path), "_binding.so")
+    if untagged != path and os.path.exists(untagged):
+        os.remove(untagged)
+    if not force and not _stale(path, [source, os.path.join(INCLUDE, "estream.h")]):
+        return
+    if not os.path.exists(os.path.join(python_include, "Python.h")):
+        if os.path.exists(path):
+            os.remove(path)
+        return
+    tmp = path + ".tmp%d" % os.getpid()
+    _compile([shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I" + INCLUDE,
+              "-I" + python_include, source, "-o", tmp], verbose)
+    os.replace(tmp, path)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -61,30 +92,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append(common + ["-c", s, "-o", o])
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("the compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-        if verbose:
-            sys.stderr.write(r.stdout + r.stderr)
-
-    binding = os.path.join(CSRC, "binding.c")
-    python_include = sysconfig.get_paths()["include"]
-    # without Python's headers the binding takes its interpreted way alone
-    if os.path.exists(os.path.join(python_include, "Python.h")) and (
-            force or _stale(BINDING_PATH, [binding, os.path.join(INCLUDE, "estream.h")])):
-        tmp_binding = BINDING_PATH + ".tmp%d" % os.getpid()
-        run([shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I" + INCLUDE,
-             "-I" + python_include, binding, "-o", tmp_binding])
-        os.replace(tmp_binding, BINDING_PATH)
+    build_binding(force=force, verbose=verbose)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            list(ex.map(run, jobs))
+            list(ex.map(lambda cmd: _compile(cmd, verbose), jobs))
     if force or jobs or _stale(LIB_PATH, objs):
         libdir = _cuda_lib_dir(nvcc)
         tmp = LIB_PATH + ".tmp%d" % os.getpid()
-        run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
-             "-Xlinker", "-rpath=" + libdir, "-L" + libdir])
+        _compile([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
+                  "-Xlinker", "-rpath=" + libdir, "-L" + libdir], verbose)
         os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -3,7 +3,9 @@
  * each. A function returns the status, or None for whatever it does not take as it is
  * (a wrong type or size, another device, a stream of its own, a workspace to be
  * allocated): Python then does the call, or says what is wrong with it. Tensors are
- * asked through their public methods, so nothing here depends on a version of torch. */
+ * asked through their public methods; the current device and stream come from the
+ * functions that setup is given. The file's name has the interpreter's tag and the
+ * module the header's version, so that another interpreter or library leaves it alone. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -275,4 +277,11 @@ static PyMethodDef methods[] = {
 };
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "The short calls' way into libestream.", -1, methods,
                                     NULL, NULL, NULL, NULL};
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddIntConstant(m, "version", ESTREAM_VERSION)) {
+        Py_DECREF(m);
+        return NULL;
+    }
+    return m;
+}

@@ -166,16 +166,21 @@ def lib():
 
 
 def _load_fast(L) -> None:
-    """The compiled part of the binding, where it was built: the calls of a generation
-    step are shorter than an interpreted check of their arguments."""
+    """The compiled part of the binding, where it was built for this interpreter and this
+    library: the calls of a generation step are shorter than an interpreted check of
+    their arguments. Else all calls take the interpreted way."""
     global _fast
-    if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+    _fast = None
+    try:
+        from . import _binding
+        if _binding.version != L.estream_version():
+            return
+        address = lambda name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+        _binding.setup(address("estream_kv_append"), address("estream_kv_attend"), address("estream_kv_attend_workspace_bytes"),
+                       address("estream_sample_tokens"), torch.Tensor, torch.bfloat16, torch.float16, torch.float32, torch.int32,
+                       torch.uint8, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    except (ImportError, AttributeError):
         return
-    from . import _binding
-    address = lambda name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value
-    _binding.setup(address("estream_kv_append"), address("estream_kv_attend"), address("estream_kv_attend_workspace_bytes"),
-                   address("estream_sample_tokens"), torch.Tensor, torch.bfloat16, torch.float16, torch.float32, torch.int32,
-                   torch.uint8, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     _fast = _binding
 
 
