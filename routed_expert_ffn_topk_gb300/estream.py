@@ -226,6 +226,11 @@ def _current(stream, device: torch.device):
 _SAME_DEVICE = contextlib.nullcontext()
 
 
+def _allocating(stream, device: torch.device):
+    """Where a call that launches on `stream` allocates what it returns or works in."""
+    return _SAME_DEVICE if stream is None or device.type != "cuda" else _current(stream, device)
+
+
 def _on(t: torch.Tensor):
     """Makes the tensors' device current for the duration of one library call
     (the library launches on the current device, with these pointers); costs
@@ -267,6 +272,16 @@ def _check_route_args(logits: torch.Tensor, k: int, phi, P: int, o: dict) -> Non
     _need(o["rec_route"], R, torch.int32, "rec_route", dev)
 
 
+def _route_outputs(o: dict, R: int, P: int, stream, dev) -> None:
+    """What a route build writes and the caller did not give."""
+    with _allocating(stream, dev):
+        o.setdefault("topk_ids", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
+        o.setdefault("alpha", torch.empty(max(R, 1), dtype=torch.float32, device=dev))
+        o.setdefault("offsets", torch.empty(P + 2, dtype=torch.int32, device=dev))
+        o.setdefault("rec_tok", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
+        o.setdefault("rec_route", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
+
+
 def route_build(logits: torch.Tensor, k: int, renorm: bool, phi: torch.Tensor | None = None,
                 P: int | None = None, out: dict | None = None, workspace: torch.Tensor | None = None,
                 stream=None) -> dict:
@@ -277,15 +292,12 @@ def route_build(logits: torch.Tensor, k: int, renorm: bool, phi: torch.Tensor | 
     dev = logits.device
     R = T * k
     o = dict(out or {})
-    o.setdefault("topk_ids", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
-    o.setdefault("alpha", torch.empty(max(R, 1), dtype=torch.float32, device=dev))
-    o.setdefault("offsets", torch.empty(P + 2, dtype=torch.int32, device=dev))
-    o.setdefault("rec_tok", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
-    o.setdefault("rec_route", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
+    _route_outputs(o, R, P, stream, dev)
     _check_route_args(logits, k, phi, P, o)
     nbytes = route_workspace_bytes(T, E, k, P)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        with _allocating(stream, dev):
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     if workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}")
     with _on(logits):
@@ -312,11 +324,12 @@ def router_logits(X: torch.Tensor, W_r: torch.Tensor, logits: torch.Tensor | Non
         raise ValueError("X and W_r must be on one CUDA device")
     T, H = X.shape
     E = W_r.shape[0]
-    if logits is None:
-        logits = torch.empty(T, E, dtype=torch.float32, device=X.device)
-    if workspace is None:
-        workspace = torch.empty(max(router_workspace_bytes(T, H, E), 256), dtype=torch.uint8,
-                                device=X.device)
+    with _allocating(stream, X.device):
+        if logits is None:
+            logits = torch.empty(T, E, dtype=torch.float32, device=X.device)
+        if workspace is None:
+            workspace = torch.empty(max(router_workspace_bytes(T, H, E), 256), dtype=torch.uint8,
+                                    device=X.device)
     if tuple(logits.shape) != (T, E) or logits.dtype != torch.float32 or logits.device != X.device:
         raise ValueError(f"logits must be [{T}, {E}] fp32 on X's device")
     if workspace.device != X.device:
@@ -345,19 +358,17 @@ def route_build_from_x(X: torch.Tensor, W_r: torch.Tensor, k: int, renorm: bool,
     dev = X.device
     R = T * k
     o = dict(out or {})
-    o.setdefault("logits", torch.empty(T, E, dtype=torch.float32, device=dev))
-    o.setdefault("topk_ids", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
-    o.setdefault("alpha", torch.empty(max(R, 1), dtype=torch.float32, device=dev))
-    o.setdefault("offsets", torch.empty(P + 2, dtype=torch.int32, device=dev))
-    o.setdefault("rec_tok", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
-    o.setdefault("rec_route", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
+    with _allocating(stream, dev):
+        o.setdefault("logits", torch.empty(T, E, dtype=torch.float32, device=dev))
+    _route_outputs(o, R, P, stream, dev)
     if tuple(o["logits"].shape) != (T, E) or o["logits"].dtype != torch.float32 \
             or o["logits"].device != dev:
         raise ValueError(f"logits must be [{T}, {E}] fp32 on X's device")
     _check_route_args(o["logits"], k, phi, P, o)
     nbytes = route_workspace_bytes(T, E, k, P)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        with _allocating(stream, dev):
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     if workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}")
     with _on(X):
@@ -386,11 +397,7 @@ def route_build_noalloc(logits: torch.Tensor, k: int, renorm: bool, phi: torch.T
     dev = logits.device
     R = T * k
     o = dict(out or {})
-    o.setdefault("topk_ids", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
-    o.setdefault("alpha", torch.empty(max(R, 1), dtype=torch.float32, device=dev))
-    o.setdefault("offsets", torch.empty(P + 2, dtype=torch.int32, device=dev))
-    o.setdefault("rec_tok", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
-    o.setdefault("rec_route", torch.empty(max(R, 1), dtype=torch.int32, device=dev))
+    _route_outputs(o, R, P, stream, dev)
     _check_route_args(logits, k, phi, P, o)
     with _on(logits):
         st = lib().estream_route_build_noalloc(
@@ -717,7 +724,8 @@ def mx4_quantize(x: torch.Tensor, fmt: int, scale: float = 1.0, rows: torch.Tens
             raise ValueError("rows must be a 1-d int32 tensor on x's device")
         R, rp = rows.numel(), _dptr(rows)
     if out is None:
-        out = Mx4._empty(R, K, mx4_padded(K), b, fmt, scale, dev)
+        with _allocating(stream, dev):
+            out = Mx4._empty(R, K, mx4_padded(K), b, fmt, scale, dev)
     elif out.shape != (R, K) or out.fmt != fmt or out.device != dev:
         raise ValueError(f"out must hold {R} rows of {K} in this format on x's device")
     else:
@@ -735,7 +743,8 @@ def mx4_dequantize(q: Mx4, dtype=torch.float32, out: torch.Tensor | None = None,
     """The values [R, K] that quantised rows stand for (bf16, fp16 or fp32)."""
     R, K, dev = q._R, q.K, q.device
     if out is None:
-        out, ld = torch.empty((R, K), dtype=dtype, device=dev), K
+        with _allocating(stream, dev):
+            out, ld = torch.empty((R, K), dtype=dtype, device=dev), K
     else:
         if tuple(out.shape) != (R, K) or out.device != dev:
             raise ValueError(f"out must be [{R}, {K}] on the codes' device")
@@ -766,7 +775,8 @@ def mx4_weights(codes: torch.Tensor, scales: torch.Tensor, K: int, fmt: int, sca
         raise ValueError(f"codes must be [P, N, {Kp // 2}] and scales [P, N, {Kp // b}] for K = {K}")
     if not codes.is_cuda or scales.device != codes.device:
         raise ValueError("codes and scales must be on one CUDA device")
-    tiles = torch.empty(lib().estream_mx4_weight_scale_bytes(P, N, K), dtype=torch.uint8, device=codes.device)
+    with _allocating(stream, codes.device):
+        tiles = torch.empty(lib().estream_mx4_weight_scale_bytes(P, N, K), dtype=torch.uint8, device=codes.device)
     with _on(codes):
         _check(lib().estream_mx4_weight_scales(_dptr(scales), P, N, K, fmt, _dptr(tiles),
                                                _stream(stream, codes.device)), "estream_mx4_weight_scales")
@@ -791,7 +801,8 @@ def mx4_product(x: Mx4, w: Mx4Weights, offsets: torch.Tensor | None = None, out:
     elif P != 1:
         raise ValueError("weights of several slots need offsets")
     if out is None:
-        out, ld = torch.empty((R, N), dtype=out_dtype, device=dev), N
+        with _allocating(stream, dev):
+            out, ld = torch.empty((R, N), dtype=out_dtype, device=dev), N
     else:
         if tuple(out.shape) != (R, N) or out.device != dev:
             raise ValueError(f"out must be [{R}, {N}] on x's device")

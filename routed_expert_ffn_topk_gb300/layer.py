@@ -101,8 +101,9 @@ class BoundLayerStack:
         buf = getattr(self, "_router_buf", None)
         if buf is None or buf[0].shape[0] < T * E or buf[1].device != X.device:
             ws_bytes = max(es.router_workspace_bytes(self.T_max, X.shape[1], E), 256)
-            buf = (torch.empty(self.T_max * E, dtype=torch.float32, device=X.device),
-                   torch.empty(ws_bytes, dtype=torch.uint8, device=X.device))
+            with es._allocating(stream, X.device):
+                buf = (torch.empty(self.T_max * E, dtype=torch.float32, device=X.device),
+                       torch.empty(ws_bytes, dtype=torch.uint8, device=X.device))
             self._router_buf = buf
         logits = buf[0][:T * E].view(T, E)
         es.router_logits(X, W_r, logits=logits, workspace=buf[1], stream=stream)
