@@ -220,7 +220,10 @@ def _current(stream, device: torch.device):
     """`stream` as the current one: what is allocated meanwhile belongs to it, so that its
     memory is not another stream's still, and not reused before the stream is done."""
     handle = _stream(stream, device)
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device))
+    if not hasattr(stream, "cuda_stream"):
+        # the legacy default stream's two handles are no external streams to torch, which would make a new one
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
+    return torch.cuda.stream(stream)
 
 
 _SAME_DEVICE = contextlib.nullcontext()
