@@ -327,6 +327,8 @@ struct FastDiv {
 bool kv_cache_ok(const estream_kv_cache* c);
 // ESTREAM_OK when the current device runs this library's kernels.
 estream_status on_device();
+// The current device's SMs.
+cudaError_t sm_count(int* sms);
 
 // Tensor-map helper (driver entry point resolved at run time); 128-byte swizzle or none.
 CUresult encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base,

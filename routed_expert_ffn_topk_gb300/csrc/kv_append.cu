@@ -388,10 +388,11 @@ extern "C" estream_status estream_kv_append(const estream_kv_cache* c, int elem,
     const int dim = c->dim;
     const int per_head = mode == kSingles ? dim - rot / 2 : mode == kHalves ? rot / 16 + (dim - rot) / 8 : dim / 8;
     const int per_v = mode == kSingles ? dim : dim / 8;
-    // warps for a token: one while tokens alone fill the device (152 SMs of 32 warps), at most 16 (32 tokens 3.8 us;
+    // warps for a token: one while tokens alone fill the device with 32 warps an SM, at most 16 (32 tokens 3.8 us;
     // with 32 warps 4.2, and 1 token 3.0 with either)
-    int parts = 0;
-    while (parts < 4 && (static_cast<long long>(T) << parts) < 152 * 32) ++parts;
+    int parts = 0, sms = 0;
+    if (sm_count(&sms) != cudaSuccess) return ESTREAM_ERR_CUDA;
+    while (parts < 4 && (static_cast<long long>(T) << parts) < sms * 32) ++parts;
     const Append a{k, v, q, q_out, c->k, c->v, k_token, k_head, v_token, v_head, q_token, q_head, qo_token, qo_head,
                    c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head, positions, rows, table,
                    inv_freq, table_row, 1.0f / c->k_scale, 1.0f / c->v_scale, T, entries ? B : 0, M, c->num_pages, Hq,

@@ -902,12 +902,6 @@ bool sizes_ok(const estream_kv_cache* c, int B, int Hq, int M) {
            static_cast<long long>(B) * Hq <= 1 << 24 && static_cast<long long>(M) * c->page_size < (1ll << 31) - 4096;
 }
 
-cudaError_t sm_count(int* sms) {
-    int dev = 0;
-    const cudaError_t rc = cudaGetDevice(&dev);
-    return rc != cudaSuccess ? rc : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-}
-
 }  // namespace
 }  // namespace es
 

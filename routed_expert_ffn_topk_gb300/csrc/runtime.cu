@@ -49,6 +49,11 @@ estream_status on_device() {
     if (cudaGetDevice(&dev) != cudaSuccess) return ESTREAM_ERR_CUDA;
     return device_supported(dev) ? ESTREAM_OK : ESTREAM_ERR_UNSUPPORTED;
 }
+cudaError_t sm_count(int* sms) {
+    int dev = 0;
+    const cudaError_t rc = cudaGetDevice(&dev);
+    return rc != cudaSuccess ? rc : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
 }  // namespace es
 
 using namespace es;

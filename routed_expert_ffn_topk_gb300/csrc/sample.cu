@@ -1124,9 +1124,10 @@ extern "C" estream_status estream_sample_tokens(const void* logits, int elem, lo
     const bool cuts = top_k_rows || top_p_rows || (top_k > 0 && top_k < V) || !(top_p >= 1.0f);
     // as many CTAs a row as keep the device busy, of 2048 logits at least, and with cuts as many as hold the row in 96 KB
     // each (256 rows of 151936 bf16, top-p 0.9: 4 CTAs a row 294 us, 8 366)
-    int ctas = 1;
+    int ctas = 1, sms = 0;
+    if (sm_count(&sms) != cudaSuccess) return ESTREAM_ERR_CUDA;
     while (ctas < kMaxCtas && ((cuts && V * static_cast<long long>(size) > ctas * 98304ll) ||
-                               (B * ctas < (cuts ? 152 : 608) && V > ctas * 2048)))
+                               (B * ctas < (cuts ? sms : 4 * sms) && V > ctas * 2048)))
         ctas *= 2;
     const Sample s{logits, ld, V, ((V + ctas - 1) / ctas + 7) / 8 * 8, u, temperature, top_p, min_p, top_k,
                    temperature_rows, top_p_rows, min_p_rows, top_k_rows, ids, prob};
