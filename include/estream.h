@@ -646,7 +646,7 @@ size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, i
  * infinite element of v that is attended makes its column of the heads that meet it
  * infinite or NaN (a weight's second term may be 0 or negative), and nothing else.
  * Products and sums in fp32; weights are kept to 16
- * bits for bf16 values, 22 for fp16 and 11 for E4M3. M * page_size < 2^31 - 4096, B *
+ * bits for bf16 values and to 22 for the others. M * page_size < 2^31 - 4096, B *
  * Hq at most 2^24. A call repeats bit for bit on one kind of device.
  */
 estream_status estream_kv_attend(const estream_kv_cache* cache, int elem, int B, int Hq,

@@ -3,7 +3,9 @@
 // With z_i = scale (q . k_i): out = sum_i e^{z_i - m} v_i / l, l = sum_i e^{z_i - m}, m = max z.
 // (m, l, sum) of two sets of positions join as
 //   m = max(m1, m2), l = l1 e^{m1 - m} + l2 e^{m2 - m}, the sums alike,
-// so a sequence may be cut anywhere. Exponents are held in base 2.
+// so a sequence may be cut anywhere. Exponents are held in base 2, and m is the next whole number from the
+// largest on: it loses nothing when it is subtracted from a score, when sums by two of them are joined, or when lse is
+// formed, and a unit's sums are rescaled by powers of two.
 //
 // The work is all (row, key head) units' blocks of 16 or 32 positions, one unit behind
 // another; every warp takes an equal, contiguous share of them, found from the
@@ -31,6 +33,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "estream_internal.h"
 #include "overlap.cuh"
@@ -58,6 +61,7 @@ struct Attend {
     long long q_row, q_head, out_row, out_head, table_row;
     long long k_page, k_token, k_head, v_page, v_token, v_head;  // bytes
     float scale, v_scale;  // scale * k_scale * log2 e
+    float back, back_low;  // what a score in base 2 is worth: (scale * k_scale) / Attend::scale in two floats, which undoes its rounding
     int B, Hq, heads, group, tiles, rows, dim, chunks, M, max_len, num_pages, window;
     int ctas;  // of the cluster that has a unit to itself; 0: shares of all units
     int out_f16, q_words;  // type of q and out; q rows lie on 4 bytes
@@ -69,10 +73,6 @@ template <int kElem, int kDim>
 struct Shape {
     static constexpr bool kBytes = kElem == ESTREAM_KV_E4M3;
     static constexpr bool kBf16 = kElem == ESTREAM_KV_BF16;  // the matrix instructions' type; else fp16
-    // A weight enters the products as two terms, what the type holds of it and what that leaves: 16 bits for bf16,
-    // 22 for fp16. One fp16 term made a ragged batch's results 6% less exact for 1% of the time. Next to 8-bit values, of
-    // 4 bits, one term of 11 bits is enough: a second one took 1 to 4% longer and changed bf16 results' error by a thousandth.
-    static constexpr bool kTwoTerms = !kBytes;
     static constexpr int kRowBytes = kDim * (kBytes ? 1 : 2);
     static constexpr int kBlock = kRowBytes <= 128 ? 32 : 16;  // positions a warp takes at a time
     static constexpr int kStageBytes = 2 * kBlock * kRowBytes;  // keys, then values
@@ -82,6 +82,7 @@ struct Shape {
     // fp16 weights are 2^14 times as large as the formula's: their smallest normal
     // value is then 2^-28 of the largest weight, not 2^-14
     static constexpr float kBias = kBf16 ? 0.0f : 14.0f;
+    static constexpr float kUnit = kBf16 ? 1.0f : 0x1p-14f;  // 2^-kBias
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -192,13 +193,13 @@ struct Unit {
     }
 };
 
-// What a row's (m, l, sum) gives: the factor of its sums, and lse.
+// What a row's (m, l, sum) gives: the factor of its sums, and lse; unit: what a weight of 1 is worth.
 struct Finish {
     float by, lse;
 };
-__device__ __forceinline__ Finish finish(const Attend& a, float m, float l, float bias) {
+__device__ __forceinline__ Finish finish(const Attend& a, float m, float l, float unit) {
     if (l == 0.0f) return {0.0f, -INFINITY};
-    return {l > 0.0f ? a.v_scale / l : NAN, (m - bias + log2f(l)) * 0.69314718055994531f};
+    return {l > 0.0f ? a.v_scale / l : NAN, fmaf(m, a.back, fmaf(m, a.back_low, log2f(l * unit) * 0.69314718055994531f))};
 }
 // One value of the result; sums of nothing may be anything.
 __device__ __forceinline__ void put(const Attend& a, int b, int h, int d, float sum, const Finish& f) {
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         begin = kOver + mine * each;
         end = min(kOver + u.span.blocks, static_cast<int>(begin) + each);
         if (u.span.blocks == 0) {  // nothing to attend: zeros, or NaN where the length is out of range
-            const Finish f = finish(a, 0.0f, u.span.len == 0 ? 0.0f : NAN, 0.0f);
+            const Finish f = finish(a, 0.0f, u.span.len == 0 ? 0.0f : NAN, 1.0f);
             const int h0 = u.head / a.tiles * a.group + u.head % a.tiles * kRows;
             const int rows = min(kRows, a.group - u.head % a.tiles * kRows);
             for (int i = mine / kWarps * kThreads + tid; i < rows * kDim; i += a.ctas * kThreads) {
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
             const Span s = span_of<kBlock>(a, b);
             if (s.blocks) continue;
             for (int i = tid; i < units; i += kThreads) a.pieces[static_cast<long long>(b) * units + i] = make_int2(0, 0);
-            const Finish f = finish(a, 0.0f, s.len == 0 ? 0.0f : NAN, 0.0f);
+            const Finish f = finish(a, 0.0f, s.len == 0 ? 0.0f : NAN, 1.0f);
             for (int i = tid; i < a.Hq * a.dim; i += kThreads) {
                 const int h = i / a.dim, d = i - h * a.dim;
                 put(a, b, h, d, 1.0f, f);
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
         const int from = u.from(begin), to = u.to(end);
         const int kv_head = u.head / a.tiles, row0 = u.head % a.tiles * kRows;  // first query head of this unit in its group
         const int rows = min(kRows, a.group - row0);
-        // Of heads 2t and 2t + 1 of each tile: the maximum (the same in all lanes of one t), this
+        // Of heads 2t and 2t + 1 of each tile: the maximum, rounded up (the same in all lanes of one t), this
         // lane's part of the sum of weights, and of the values' dims g and g + 8 of each 16 (E4M3: 2g, 2g + 1).
         float m[kTiles][2], base[kTiles][2], l[kTiles][2], o[kTiles][kSteps][4];  // base: finite m, less the bias
 #pragma unroll
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                                 float top = fmaxf(z[j][i], z[j][i + 2]);
 #pragma unroll
                                 for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-                                const float now = fmaxf(m[j][i], top), shrink = exp2_fast(m[j][i] - finite_or_zero(now));
+                                const float now = fmaxf(m[j][i], ceilf(top)), shrink = exp2_fast(m[j][i] - finite_or_zero(now));
                                 m[j][i] = now;
                                 base[j][i] = finite_or_zero(now) - S::kBias;
                                 l[j][i] *= shrink;
@@ -547,6 +548,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                                 }
                             }
                     }
+                    // A weight enters the products as two terms, what the type holds of it and what that leaves: 16 bits for
+                    // bf16, 22 for fp16. With one fp16 term results were 2 to 6% less exact (2.20e-4 of the norm instead of
+                    // 2.07e-4, fp16 pages) for at most 1% of the time, next to 8-bit pages for 1 to 4%.
                     uint32_t hi[kTiles][2], lo[kTiles][2];
 #pragma unroll
                     for (int j = 0; j < kTiles; ++j)
@@ -558,10 +562,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                             l[j][1] += y;
                             const uint32_t w = pack<S::kBf16>(x, y);
                             hi[j][i] = transpose(w);
-                            if constexpr (S::kTwoTerms) {  // what the type leaves of a weight, as a second term
-                                const float2 first = unpack<S::kBf16>(w);
-                                lo[j][i] = transpose(pack<S::kBf16>(x - first.x, y - first.y));
-                            }
+                            const float2 first = unpack<S::kBf16>(w);
+                            lo[j][i] = transpose(pack<S::kBf16>(x - first.x, y - first.y));
                         }
                     if constexpr (S::kBytes) {
 #pragma unroll
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 #pragma unroll
                                 for (int j = 0; j < kTiles; ++j) {
                                     mma<false>(o[j][s + i], f, hi[j][0], hi[j][1]);
-                                    if constexpr (S::kTwoTerms) mma<false>(o[j][s + i], f, lo[j][0], lo[j][1]);
+                                    mma<false>(o[j][s + i], f, lo[j][0], lo[j][1]);
                                 }
                             }
                         }
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
 #pragma unroll
                             for (int j = 0; j < kTiles; ++j) {
                                 mma<S::kBf16>(o[j][s], r, hi[j][0], hi[j][1]);
-                                if constexpr (S::kTwoTerms) mma<S::kBf16>(o[j][s], r, lo[j][0], lo[j][1]);
+                                mma<S::kBf16>(o[j][s], r, lo[j][0], lo[j][1]);
                             }
                         }
                     }
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                         weight += f * s[w].y;
                     }
                 }
-                const Finish f = finish(a, top, weight, S::kBias);
+                const Finish f = finish(a, top, weight, S::kUnit);
                 const int h = kv_head * a.group + row0 + row;
                 put(a, u.b, h, d, sum, f);
                 if (d == 0) put_lse(a, u.b, h, f);
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kElem, kDim>::kResident) k_kv_
                 if (row >= rows) continue;
                 const int h = kv_head * a.group + row0 + row;
                 if (whole) {
-                    const Finish f = finish(a, m[j][i], l[j][i], S::kBias);
+                    const Finish f = finish(a, m[j][i], l[j][i], S::kUnit);
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s) {
                         const int d = 16 * s + (S::kBytes ? 2 * g : g);
@@ -749,7 +751,7 @@ struct Joined {
     }
 };
 template <int kDim>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(const Attend a, float bias, int items, int per_block) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(const Attend a, float unit, int items, int per_block) {
     using J = Joined<kDim>;
     __shared__ float sums[kJoinWarps][kDim];
     __shared__ float2 stats[kJoinWarps];
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(const Attend a, flo
         if (any && few) {
             J r;
             r.add(a, pieces.x, row, lane, 0, pieces.y, 1);
-            const Finish f = finish(a, r.m, r.l, bias);
+            const Finish f = finish(a, r.m, r.l, unit);
 #pragma unroll
             for (int c = 0; c < J::kPer; ++c) put(a, b, h, lane * J::kPer + c, r.sum[c], f);
             if (lane == 0) put_lse(a, b, h, f);
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(const Attend a, flo
             sum += f * sums[w][d];
             l += f * stats[w].y;
         }
-        const Finish f = finish(a, m, l, bias);
+        const Finish f = finish(a, m, l, unit);
         put(a, b, h, d, sum, f);
         if (d == 0) put_lse(a, b, h, f);
     }
@@ -892,7 +894,7 @@ cudaError_t launch(const Attend& a, int grid, cudaStream_t stream) {
     if (rc != cudaSuccess || a.ctas) return rc;
     // a block an item while all are on the device at once, else a warp
     const int items = a.B * a.heads * a.tiles * a.rows, per_block = items <= 2 * grid ? 1 : kJoinWarps;
-    return launch_overlapped(k_kv_join<kDim>, dim3((items + per_block - 1) / per_block), 32 * kJoinWarps, 0, stream, a, S::kBias,
+    return launch_overlapped(k_kv_join<kDim>, dim3((items + per_block - 1) / per_block), 32 * kJoinWarps, 0, stream, a, S::kUnit,
                              items, per_block);
 }
 template <int kElem, int kDim>
@@ -950,12 +952,15 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
     if (l.bytes && (workspace_bytes < l.bytes || !at(workspace, 16))) return ESTREAM_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int size = c->elem == ESTREAM_KV_E4M3 ? 1 : 2, group = Hq / c->heads;
+    const double natural = static_cast<double>(scale) * c->k_scale;
+    const float base2 = static_cast<float>(natural * 1.4426950408889634);
+    const double back = base2 == 0.0f || std::isinf(base2) ? 0.69314718055994531 : natural / base2;
     const Attend a{q, out, lse, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), table, lens,
                    reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.ml), reinterpret_cast<int2*>(ws + l.pieces),
                    q_row, q_head, out_row, out_head, table_row, c->k_page * size, c->k_token * size, c->k_head * size,
                    c->v_page * size, c->v_token * size, c->v_head * size,
-                   static_cast<float>(static_cast<double>(scale) * c->k_scale * 1.4426950408889634), c->v_scale, B, Hq,
-                   c->heads, group, (group + kRows - 1) / kRows, std::min(group, kRows), c->dim, c->dim * size / 16, M,
+                   base2, c->v_scale, static_cast<float>(back),
+                   static_cast<float>(back - static_cast<double>(static_cast<float>(back))), B, Hq, c->heads, group, (group + kRows - 1) / kRows, std::min(group, kRows), c->dim, c->dim * size / 16, M,
                    M * c->page_size, c->num_pages, window, l.ctas, elem == ESTREAM_KV_F16,
                    at(q, 4) && q_row % 2 == 0 && q_head % 2 == 0, FastDiv(c->page_size)};
     const bool whole = c->page_size % kGroup == 0;
