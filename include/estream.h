@@ -637,6 +637,7 @@ size_t estream_kv_attend_workspace_bytes(const estream_kv_cache* cache, int B, i
  *          row of zeros, lse -infinity (so also where every z_i is -infinity). A
  *          row whose length is outside [0, M * page_size], or that needs a page
  *          outside [0, num_pages), becomes NaNs, its lse too.
+ * scale    scale * k_scale * log2(e) within fp32's range (else ESTREAM_ERR_INVALID_ARG).
  * lse      device, [B][Hq] fp32, or NULL.
  * workspace  device, 16-byte aligned, estream_kv_attend_workspace_bytes(cache, B, Hq, M,
  *          window) bytes, used by this call alone until it ends (no initial value);

@@ -938,9 +938,10 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
                                  void* cuda_stream) {
     NvtxRange range(kNvKvAttend, B);
     if (!sizes_ok(c, B, Hq, M) || (elem != ESTREAM_KV_BF16 && elem != ESTREAM_KV_F16) ||
-        (c->elem != ESTREAM_KV_E4M3 && c->elem != elem) || table_row < 0 || window < 0 ||
-        !(scale >= -3.402823466e38f && scale <= 3.402823466e38f))
+        (c->elem != ESTREAM_KV_E4M3 && c->elem != elem) || table_row < 0 || window < 0)
         return ESTREAM_ERR_INVALID_ARG;
+    const double natural = static_cast<double>(scale) * c->k_scale;  // base 2's factor is to be finite
+    if (!(std::fabs(natural) * 1.4426950408889634 <= 3.4028234e38)) return ESTREAM_ERR_INVALID_ARG;
     if (B == 0) return ESTREAM_OK;
     if (!at(q, 2) || !at(out, 2) || (M > 0 && !at(table, 4)) || !at(lens, 4) || (lse && !at(lse, 4)))
         return ESTREAM_ERR_INVALID_ARG;
@@ -952,9 +953,8 @@ estream_status estream_kv_attend(const estream_kv_cache* c, int elem, int B, int
     if (l.bytes && (workspace_bytes < l.bytes || !at(workspace, 16))) return ESTREAM_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int size = c->elem == ESTREAM_KV_E4M3 ? 1 : 2, group = Hq / c->heads;
-    const double natural = static_cast<double>(scale) * c->k_scale;
     const float base2 = static_cast<float>(natural * 1.4426950408889634);
-    const double back = base2 == 0.0f || std::isinf(base2) ? 0.69314718055994531 : natural / base2;
+    const double back = base2 == 0.0f ? 0.69314718055994531 : natural / base2;
     const Attend a{q, out, lse, static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), table, lens,
                    reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.ml), reinterpret_cast<int2*>(ws + l.pieces),
                    q_row, q_head, out_row, out_head, table_row, c->k_page * size, c->k_token * size, c->k_head * size,
