@@ -26,7 +26,7 @@
 // instructions and registers (64 ragged sequences over E4M3 243 us instead of 208).
 //
 // Bound by HBM: 131072 positions of 8 heads of 128 bf16 in 82 us (6.5 TB/s, 96% of the copy rate) and
-// 5 us of joining; 64 ragged sequences up to 16384 in E4M3 122 us (6.0 TB/s), 32 in fp16 60 us (6.2).
+// 5 us of joining; 64 ragged sequences up to 16384 in E4M3 124 us (5.9 TB/s), 32 in fp16 60 us (6.2).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -1,6 +1,6 @@
-// Programmatic dependent launch of the 4-bit calls' kernels: a kernel's start (block
-// launch, barriers, tensor memory) overlaps the end of the one before it in the
-// stream. Between two small products, launched plainly, the device idles for
+// Programmatic dependent launch of the kernels of the 4-bit calls, the key-value cache and
+// sampling: a kernel's start (block launch, barriers, tensor memory) overlaps the
+// end of the one before it in the stream. Between two small products, launched plainly, the device idles for
 // about 4 us, which is as long as one of them runs.
 #pragma once
 

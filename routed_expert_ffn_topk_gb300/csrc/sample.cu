@@ -23,13 +23,13 @@
 //
 // Without cuts the logits are not kept, so that more rows are under way: what may hold a kept
 // token is read again, out of L2. With min-p or temperature 0 that is little: each lane notes
-// the largest of each part (8 or more reads of 16 bytes), and the warp shares out those with a hit (256 rows of
-// 151936 fp32 with min-p 50 us; reading whole runs of a warp again 69). Without any choice all is weighed
-// (112 us).
+// the largest of each part (8 or more reads of 16 bytes), and the warp shares out those with a hit (reading whole runs
+// of a warp again took 256 rows of 151936 fp32 with min-p 1.4 times as long). Without any choice all is weighed. Such rows
+// take 30 us with temperature 0, 42 with min-p 0.02 and 111 without a choice.
 //
 // What bounds it: for few rows the meetings of the cluster (about 1 us each: three for a
 // list, two without cuts), for many the weights. With each float operation of two logits'
-// weights in one instruction, 256 rows without a choice take 120 us instead of 135.
+// weights in one instruction, 256 rows without a choice take a tenth less.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     // Without cuts the CTA's logits are counted from the 16-byte boundary before them: `skew` of what lies from there
-    // on is not the row's and never read. So rows of any alignment are read 16 bytes at a time (with single reads,
-    // 256 rows of 151937 fp32 with min-p took 53 us, now 38). With cuts a row that is not on 16 bytes is read singly: it
+    // on is not the row's and never read. So rows of any alignment are read 16 bytes at a time (256 rows of
+    // 151937 fp32 with min-p take as long as of 151936, with single reads 1.4 times as long). With cuts a row that is not on 16 bytes is read singly: it
     // costs 5 to 15% where it happens, and the counting 3% everywhere.
     const uint8_t* const start = static_cast<const uint8_t*>(a.logits) + (row * a.ld + rank * a.slice) * E::kBytes;
     const int past16 = static_cast<int>(reinterpret_cast<uintptr_t>(start) % 16 / E::kBytes), skew = kCuts ? 0 : past16;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreadsOf<kCuts>, 1024 / kThreadsOf<kCuts>) k
     auto given_by = [&](int r) -> const Exchange& { return sh.exchange[turn ^ 1][r]; };
     constexpr float kLowest = -3.402823466e38f;  // what can be drawn is finite
     // f(16 bytes' logits, i) where one of them may be at or above `lowest`
-    constexpr int kAhead = 4;  // reads that a lane has under way, without cuts (112 us without a choice; with one, 117)
+    constexpr int kAhead = 4;  // reads that a lane has under way, without cuts (one alone: 4% longer without a choice)
     auto chunks_of_run = [&](float lowest, auto f) {
         if (!(run_top >= lowest)) return;
         int i = run_begin;
@@ -1123,7 +1123,8 @@ extern "C" estream_status estream_sample_tokens(const void* logits, int elem, lo
     if (st != ESTREAM_OK) return st;
     const bool cuts = top_k_rows || top_p_rows || (top_k > 0 && top_k < V) || !(top_p >= 1.0f);
     // as many CTAs a row as keep the device busy, of 2048 logits at least, and with cuts as many as hold the row in 96 KB
-    // each (256 rows of 151936 bf16, top-p 0.9: 4 CTAs a row 294 us, 8 366)
+    // each (256 rows of 151936: bf16 with top-p 0.9, 4 CTAs a row 294 us, 8 366; fp32 with min-p, in two waves of which one
+    // reads while the other meets, 4 CTAs 42 us, 2 53, 8 51)
     int ctas = 1, sms = 0;
     if (sm_count(&sms) != cudaSuccess) return ESTREAM_ERR_CUDA;
     while (ctas < kMaxCtas && ((cuts && V * static_cast<long long>(size) > ctas * 98304ll) ||
