@@ -90,7 +90,7 @@ class PagedAttention:
 
     @property
     def lens(self) -> torch.Tensor:
-        """The sequences' tokens, [batch] int32. A caller may set them (back, to give up tokens)."""
+        """The sequences' tokens, [batch] int32. A caller may set them (back, to give up tokens), asking for them here each time."""
         self._held = None
         return self._lens
 
